@@ -80,7 +80,7 @@ extern "C" {
 
 struct CUstream_st; /* cudaStream_t == struct CUstream_st* */
 
-#define KAMERA_ABI_VERSION 9
+#define KAMERA_ABI_VERSION 10
 
 /* Limits of this library. */
 #define KAMERA_MAX_RANK 128          /* largest patch rank m */
@@ -626,6 +626,230 @@ int kamera_prefill_attend_reused(const KameraAttnKV* kv, const KameraPrefillQuer
 int kamera_attend_reused_static(const KameraAttnKV* kv, const KameraAttnQuery* query, const KameraRope* rope,
                                 const KameraChunk* d_chunks, const int32_t* d_seq_start, int32_t n_chunks,
                                 int32_t max_len, int32_t max_rank, int32_t* d_err, struct CUstream_st* stream);
+
+/*
+ * ---- Decode steps over the paged pool --------------------------------------
+ *
+ * The entry points above move reused chunks into the pool's slots; the ones
+ * below are what a decode step does with the pool then: append the new token's
+ * row, attend over the pages (a prefix that several sequences share is read
+ * once for all of them), or attend only over the pages that a cheap bound
+ * selects.  The pages have no counterpart: they leave the pool's readers to
+ * the serving engine.
+ *
+ * Pages: page g of page_size P is slots g*P .. g*P + P-1 (whole pages only:
+ * floor(num_slots / P) of them).  A page table row lists a sequence's pages in
+ * order, int32; token t sits in slot pages[t / P] * P + t % P.  Entries past
+ * ceil(len / P) are never read.  A page outside the pool: its tokens are left
+ * out (as if masked) and KAMERA_DEVERR_SLOT raised.
+ */
+
+/*
+ * New rows for one layer of the pool, n_tokens of them.
+ *   GQA/MHA: k, v bf16 [n_tokens][num_kv_heads][head_dim], heads packed, tokens
+ *            k_stride / v_stride elements apart; q (or NULL) bf16
+ *            [n_tokens][num_q_heads][head_dim], element (t, h, i) at
+ *            q[t*q_stride + h*q_head_stride + i]; q_out as q with its own
+ *            strides, written (NULL iff q is; it may equal q with the same
+ *            strides, else it overlaps none of the inputs and its rows not
+ *            each other)
+ *   MLA:     k is the new k_rope rows [n_tokens][rope_dim], v the c_KV rows
+ *            [n_tokens][kv_lora_rank], q the rope part of the queries
+ *            [n_tokens][num_q_heads][rope_dim]
+ * Pointers 16-byte aligned, strides in elements, multiples of 8 (a head stride
+ * is not used where there is one head).
+ *   positions  device int64 [n_tokens], |position| <= KAMERA_MAX_ABS_DELTA (else
+ *              KAMERA_DEVERR_DESCRIPTOR, the token skipped); NULL when the rope
+ *              has axes: then rope->d_axis_delta is int64 [n_tokens][n_axes],
+ *              each token's position along each axis
+ *   slots      device int64 [n_tokens]: the token's pool slot.  -1: a padding
+ *              row, skipped whole without an error (its q_out row stays as it
+ *              is).  Any other slot outside the pool: KAMERA_DEVERR_SLOT, the
+ *              token skipped.  Slots other than -1 are distinct within a call
+ *   layer      the pool layer written, 0 <= layer < num_layers
+ */
+typedef struct KameraAppendRows {
+    const void* k;
+    const void* v;
+    const void* q;
+    void* q_out;
+    int64_t k_stride, v_stride;
+    int64_t q_stride, q_head_stride;
+    int64_t q_out_stride, q_out_head_stride;
+    const int64_t* positions;
+    const int64_t* slots;
+    int32_t n_tokens, num_q_heads, layer;
+    int32_t reserved;   /* 0 */
+} KameraAppendRows;
+
+/*
+ * Appending to the pool with the rotation applied on the way: for every token t
+ *   K[layer][slot_t][h] = bf16( R(p_t) k_t[h] ),  V[layer][slot_t][h] = v_t[h]
+ *   q_out_t[h] = bf16( R(p_t) q_t[h] )            (when q is given)
+ * R(p): RoPE at position p (KameraRope's layout), components outside the
+ * rotary range copied.  The phase is exact to about 2^-34 of a turn over the
+ * whole position range, the rotation fp32, one rounding to bf16; values are
+ * bit copies.  n_tokens == 0 is a successful no-op.
+ */
+int kamera_append_kv(const KameraGqaPool* pool, const KameraAppendRows* rows, const KameraRope* rope, int32_t* d_err,
+                     struct CUstream_st* stream);
+
+/* MLA: row = c_KV (bit copy) | R(p) k_rope; rope->rot_offset / rot_dim relative
+ * to k_rope (and to each q row).  Otherwise as kamera_append_kv. */
+int kamera_mla_append_kv(const KameraMlaPool* pool, const KameraAppendRows* rows, const KameraRope* rope,
+                         int32_t* d_err, struct CUstream_st* stream);
+
+/* One layer of the paged pool as attention reads it: k, v bf16 [num_slots]
+ * [num_kv_heads][head_dim], slots slot_stride elements apart (16-byte aligned,
+ * slot_stride a multiple of 8), page_size tokens to a page (a multiple of 16). */
+typedef struct KameraPagedKV {
+    const void* k;
+    const void* v;
+    int64_t num_slots;
+    int64_t slot_stride;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t reserved;   /* 0 */
+} KameraPagedKV;
+
+/* q bf16 [n_seqs][num_q_heads][head_dim] (RoPE already applied, 16-byte
+ * aligned), out bf16 of the same shape (written, 16-byte aligned), lse float
+ * [n_seqs][num_q_heads] (written: natural log of sum_j exp(scale q . K_j)) or
+ * NULL.  Query head h reads KV head h / (num_q_heads / num_kv_heads). */
+typedef struct KameraPagedQuery {
+    const void* q;
+    void* out;
+    float* lse;
+    int32_t n_seqs;
+    int32_t num_q_heads;
+    float scale;
+    int32_t reserved;   /* 0 */
+} KameraPagedQuery;
+
+/* Each sequence's own tokens: device int32 pages [n_seqs][max_pages], lens
+ * [n_seqs]; 0 <= len <= max_len (else KAMERA_DEVERR_LEN, the sequence read as
+ * empty), max_len <= max_pages * page_size. */
+typedef struct KameraPageTable {
+    const int32_t* pages;
+    const int32_t* lens;
+    int32_t max_pages;
+    int32_t max_len;
+} KameraPageTable;
+
+/* Groups of sequences that share a prefix: group g is sequences group_start[g]
+ * .. group_start[g+1]-1 (device int32 [n_groups + 1], non-decreasing from 0 to
+ * n_seqs, at most max_group sequences each; a malformed entry raises
+ * KAMERA_DEVERR_DESCRIPTOR and its sequences' results are unspecified), its
+ * prefix tokens 0 .. lens[g]-1 of page table row g (pages [n_groups]
+ * [max_pages]; len outside 0..max_len: KAMERA_DEVERR_LEN, the prefix left out). */
+typedef struct KameraPrefixGroups {
+    const int32_t* group_start;
+    const int32_t* pages;
+    const int32_t* lens;
+    int32_t n_groups;
+    int32_t max_pages;
+    int32_t max_len;
+    int32_t max_group;
+} KameraPrefixGroups;
+
+/*
+ * Decode attention over the pool for a batch that shares prefixes: every
+ * sequence's query token attends, in one softmax, over its group's prefix and
+ * then its own tokens,
+ *     out = softmax(scale q [K_prefix | K_own]^T) [V_prefix | V_own]
+ * The prefix rows are read once per group and KV head: the query heads of all
+ * the group's sequences are the rows of one tensor-core tile.  Own tokens are
+ * read once per sequence and KV head.  fp32 accumulation, softmax weights as
+ * bf16 hi + lo pairs, one bf16 rounding of the output; a sequence with no token
+ * gets zeros and lse = -infinity.
+ *   prefix  NULL (or n_groups 0): no shared prefix
+ *   own     the sequences' own tokens (max_len 0: none; pages, lens then unread)
+ *   d_workspace, workspace_bytes  device scratch of at least
+ *           kamera_attend_shared_workspace_bytes(...) bytes (0: may be NULL),
+ *           16-byte aligned, disjoint from the call's arrays, owned by the
+ *           caller, overwritten by the call; calls that overlap on the GPU must
+ *           not share one
+ * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..16, page_size a
+ * multiple of 16, num_slots <= 2^31 - 1.  Device errors: SLOT, LEN, DESCRIPTOR
+ * as above; TIMEOUT if a pipeline wait runs past its bound (outputs of the
+ * call then undefined).
+ */
+int kamera_attend_shared(const KameraPagedKV* kv, const KameraPagedQuery* query, const KameraPrefixGroups* prefix,
+                         const KameraPageTable* own, void* d_workspace, size_t workspace_bytes, int32_t* d_err,
+                         struct CUstream_st* stream);
+
+/* Workspace bytes kamera_attend_shared needs for these arguments on the
+ * current device; 0 also when it refuses them. */
+size_t kamera_attend_shared_workspace_bytes(const KameraPagedKV* kv, const KameraPagedQuery* query,
+                                            const KameraPrefixGroups* prefix, const KameraPageTable* own);
+
+/*
+ * Page summaries, the boxes that hold a page's keys: for i < n, with page g =
+ * page_ids[i] and its first c = page_tokens[i] tokens (1 <= c <= page_size; 0:
+ * nothing is written),
+ *     summary[g][h][0] = min_t K[g*P + t][h],  summary[g][h][1] = max_t K[g*P + t][h]
+ * per channel (t < c; exact, a NaN key makes both NaN).  summary: bf16
+ * [num_slots / P][num_kv_heads][2][head_dim], 16-byte aligned, other pages'
+ * entries stay as they are.  Device errors, the entry skipped: SLOT (page
+ * outside the pool), LEN (c outside 0..page_size).  The same page twice in a
+ * call: one of the two results.  head_dim a multiple of 8; kv->v is not read
+ * and may be NULL.
+ */
+int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, const int32_t* d_page_tokens, int32_t n,
+                           void* summary, int32_t* d_err, struct CUstream_st* stream);
+
+/*
+ * The pages a sequence's query needs most, per KV head: page j of the sequence
+ * scores the sum over the KV head's query heads of the largest q . k that any
+ * key inside the page's box can reach,
+ *     score_j = sum_g sum_i max(q_gi min_ji, q_gi max_ji)
+ * and the n_select highest scores are taken; the first n_first and the last
+ * n_last pages are always taken (their summaries are not read), equal scores
+ * go to the lower page, a score that is not finite ranks with +infinity.  Scores
+ * are held to about 2^-40 of the sum of their terms, so the choice is that of the
+ * exact scores unless two differ by less.
+ *   q         bf16 [n_seqs][num_q_heads][head_dim] (16-byte aligned)
+ *   summary   bf16 [num_pages][num_kv_heads][2][head_dim] (16-byte aligned)
+ *   selected  int32 [n_seqs][num_kv_heads][n_select] (written): indices into the
+ *             sequence's page table row, ascending, then -1 where the sequence
+ *             has fewer pages
+ *   table     the sequences' page tables and lengths, as for attention
+ *   d_workspace  at least kamera_select_pages_workspace_bytes(...) bytes, rules
+ *             as for kamera_attend_shared
+ * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..16, n_first,
+ * n_last >= 0 with n_first + n_last <= n_select.  Device errors: LEN (the
+ * sequence read as empty: all -1), SLOT (a page outside num_pages ranks last).
+ */
+typedef struct KameraPageSelect {
+    const void* q;
+    const void* summary;
+    int32_t* selected;
+    int64_t num_pages;
+    int32_t n_seqs, num_q_heads, num_kv_heads, head_dim;
+    int32_t page_size, n_select, n_first, n_last;
+} KameraPageSelect;
+
+int kamera_select_pages(const KameraPageSelect* select, const KameraPageTable* table, void* d_workspace,
+                        size_t workspace_bytes, int32_t* d_err, struct CUstream_st* stream);
+
+/* 8 bytes per (sequence, KV head, page of max_len); 0 when the call would refuse. */
+size_t kamera_select_pages_workspace_bytes(const KameraPageSelect* select, const KameraPageTable* table);
+
+/*
+ * Decode attention over selected pages: as kamera_attend_shared without a
+ * prefix, each (sequence, KV head) attending over the tokens of its selected
+ * pages only (tokens past the sequence's length masked).
+ *   selected  device int32 [n_seqs][num_kv_heads][n_select]: distinct indices into
+ *             the sequence's page table row; negative entries are skipped, one at
+ *             or past ceil(len / page_size): KAMERA_DEVERR_SLOT, skipped
+ */
+int kamera_attend_selected(const KameraPagedKV* kv, const KameraPagedQuery* query, const KameraPageTable* table,
+                           const int32_t* d_selected, int32_t n_select, void* d_workspace, size_t workspace_bytes,
+                           int32_t* d_err, struct CUstream_st* stream);
+
+size_t kamera_attend_selected_workspace_bytes(const KameraPagedKV* kv, const KameraPagedQuery* query,
+                                              const KameraPageTable* table, int32_t n_select);
 
 /* KAMERA_ABI_VERSION of the loaded library. */
 int kamera_abi_version(void);

@@ -26,6 +26,8 @@ __all__ = [
     "kamera_relocate_patch", "kamera_slide_inplace", "kamera_mla_relocate_patch",
     "kamera_ingest_canonical", "kamera_mla_ingest_canonical", "kamera_form_patch", "kamera_attend_reused",
     "kamera_prefill_attend_reused",
+    "kamera_append_kv", "kamera_mla_append_kv", "kamera_attend_shared", "kamera_summarize_pages",
+    "kamera_select_pages", "kamera_attend_selected",
     "kamera_validate_chunks", "kamera_status_string", "kamera_abi_version",
     "ROTATE_HALF", "INTERLEAVED", "DEVERR",
 ]
@@ -121,6 +123,41 @@ class _MlaStore(C.Structure):
                 ("row_stride", C.c_int64)]
 
 
+class _AppendRows(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("q", C.c_void_p), ("q_out", C.c_void_p),
+                ("k_stride", C.c_int64), ("v_stride", C.c_int64), ("q_stride", C.c_int64),
+                ("q_head_stride", C.c_int64), ("q_out_stride", C.c_int64), ("q_out_head_stride", C.c_int64),
+                ("positions", C.c_void_p), ("slots", C.c_void_p), ("n_tokens", C.c_int32),
+                ("num_q_heads", C.c_int32), ("layer", C.c_int32), ("reserved", C.c_int32)]
+
+
+class _PagedKV(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("num_slots", C.c_int64), ("slot_stride", C.c_int64),
+                ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("page_size", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class _PagedQuery(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("out", C.c_void_p), ("lse", C.c_void_p), ("n_seqs", C.c_int32),
+                ("num_q_heads", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32)]
+
+
+class _PageTable(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("lens", C.c_void_p), ("max_pages", C.c_int32), ("max_len", C.c_int32)]
+
+
+class _PrefixGroups(C.Structure):
+    _fields_ = [("group_start", C.c_void_p), ("pages", C.c_void_p), ("lens", C.c_void_p), ("n_groups", C.c_int32),
+                ("max_pages", C.c_int32), ("max_len", C.c_int32), ("max_group", C.c_int32)]
+
+
+class _PageSelect(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("summary", C.c_void_p), ("selected", C.c_void_p), ("num_pages", C.c_int64),
+                ("n_seqs", C.c_int32), ("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("page_size", C.c_int32), ("n_select", C.c_int32), ("n_first", C.c_int32),
+                ("n_last", C.c_int32)]
+
+
 assert C.sizeof(_Chunk) == 64
 
 _LIB: Optional[C.CDLL] = None
@@ -174,6 +211,27 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = True) -> C
     lib.kamera_attend_workspace_bytes.argtypes = [C.c_int32, C.c_int32, C.c_int32]
     lib.kamera_mla_attend_workspace_bytes.restype = C.c_size_t
     lib.kamera_mla_attend_workspace_bytes.argtypes = [C.c_int32, C.c_int32]
+    lib.kamera_append_kv.restype = C.c_int
+    lib.kamera_append_kv.argtypes = [P(_GqaPool), P(_AppendRows), P(_Rope), C.c_void_p, C.c_void_p]
+    lib.kamera_mla_append_kv.restype = C.c_int
+    lib.kamera_mla_append_kv.argtypes = [P(_MlaPool), P(_AppendRows), P(_Rope), C.c_void_p, C.c_void_p]
+    lib.kamera_attend_shared.restype = C.c_int
+    lib.kamera_attend_shared.argtypes = [P(_PagedKV), P(_PagedQuery), P(_PrefixGroups), P(_PageTable), C.c_void_p,
+                                         C.c_size_t, C.c_void_p, C.c_void_p]
+    lib.kamera_attend_shared_workspace_bytes.restype = C.c_size_t
+    lib.kamera_attend_shared_workspace_bytes.argtypes = [P(_PagedKV), P(_PagedQuery), P(_PrefixGroups), P(_PageTable)]
+    lib.kamera_summarize_pages.restype = C.c_int
+    lib.kamera_summarize_pages.argtypes = [P(_PagedKV), C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p, C.c_void_p,
+                                           C.c_void_p]
+    lib.kamera_select_pages.restype = C.c_int
+    lib.kamera_select_pages.argtypes = [P(_PageSelect), P(_PageTable), C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]
+    lib.kamera_select_pages_workspace_bytes.restype = C.c_size_t
+    lib.kamera_select_pages_workspace_bytes.argtypes = [P(_PageSelect), P(_PageTable)]
+    lib.kamera_attend_selected.restype = C.c_int
+    lib.kamera_attend_selected.argtypes = [P(_PagedKV), P(_PagedQuery), P(_PageTable), C.c_void_p, C.c_int32,
+                                           C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]
+    lib.kamera_attend_selected_workspace_bytes.restype = C.c_size_t
+    lib.kamera_attend_selected_workspace_bytes.argtypes = [P(_PagedKV), P(_PagedQuery), P(_PageTable), C.c_int32]
     lib.kamera_validate_chunks.restype = C.c_int
     lib.kamera_validate_chunks.argtypes = [P(_Chunk), C.c_int32, C.c_int64, C.c_int64, C.c_int32,
                                            C.c_int32, P(C.c_int32), P(C.c_int32)]
@@ -193,7 +251,7 @@ def kamera_status_string(status: int) -> str:
     return load_library().kamera_status_string(int(status)).decode()
 
 
-ABI_VERSION = 9   # the KAMERA_ABI_VERSION these bindings marshal for
+ABI_VERSION = 10   # the KAMERA_ABI_VERSION these bindings marshal for
 
 
 def kamera_abi_version() -> int:
@@ -736,3 +794,352 @@ def kamera_mla_attend_reused(store: torch.Tensor, kv_lora: int, q: torch.Tensor,
     del keep
     _check(rc, "kamera_mla_attend_reused")
     return out
+
+
+# ------------------------------------------------ decode steps over the pool --
+class _On:
+    """Where a call runs: the tensors' device (made current for the call) and its
+    stream.  Every tensor must live on that device.  ``empty`` gives memory that
+    is safe on that stream: with another stream than the current one it comes
+    from that stream's pool (a block of the current stream's could still be in
+    use there) and is marked as used on the current one, where the caller reads
+    it; so no buffer is kept between calls, and a captured graph owns its own."""
+
+    __slots__ = ("device", "guard", "stream", "handle", "side")
+
+    def __init__(self, where: str, ref: torch.Tensor, stream, **tensors):
+        self.device, self.guard, self.side = ref.device, None, None
+        cuda = torch.cuda.is_available()
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if cuda and not t.is_cuda:
+                raise ValueError(f"{where}: {name} must be a CUDA tensor")
+            if t.device != self.device:
+                raise ValueError(f"{where}: {name} is on {t.device}, not on {self.device}")
+        self.stream = stream
+        self.handle = 0
+
+    def __enter__(self):
+        if self.device.type == "cuda":
+            if self.device.index != torch.cuda.current_device():
+                self.guard = torch.cuda.device(self.device)
+                self.guard.__enter__()
+            current = int(torch.cuda.current_stream().cuda_stream)
+            self.handle = current if self.stream is None else _stream_handle(self.stream)
+            if self.handle != current:
+                self.side = (self.stream if isinstance(self.stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(self.handle, device=self.device))
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        if self.side is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        here = torch.cuda.current_stream()
+        with torch.cuda.stream(self.side):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(here)
+        return t
+
+    def workspace(self, workspace, need: int):
+        """(tensor to keep until the launch, address, bytes): the caller's, or one of `need` bytes."""
+        if workspace is not None:
+            if not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+            return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        if need == 0:
+            return None, None, 0
+        t = self.empty(need, torch.uint8)
+        return t, t.data_ptr(), need
+
+
+def _ints(t: torch.Tensor, name: str, shape, dtype=torch.int32):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _append(where, call, pool, rope, rows_k, rows_v, q, q_out, positions, slots, layer, T, err, stream, tensors):
+    """The arguments both append entry points share, and the call."""
+    _ints(slots, "slots", (T,), torch.int64)
+    if rope.axis_delta is not None:
+        if positions is not None:
+            raise ValueError("with rope.axis_delta the positions are its rows; positions must be None")
+        if rope.axis_delta.dim() != 2 or rope.axis_delta.shape[0] != T or not rope.axis_delta.is_contiguous():
+            raise ValueError("rope.axis_delta must be a contiguous [T, n_axes] tensor of positions")
+    elif positions is None:
+        raise ValueError("positions are needed")
+    else:
+        _ints(positions, "positions", (T,), torch.int64)
+    hq, qs, qh, os, oh = 0, 0, 0, 0, 0
+    if q_out is not None and q is None:
+        raise ValueError("q_out without q")
+    if err is not None and (err.dtype != torch.int32 or err.numel() < 1):
+        raise ValueError("err must be an int32 tensor")
+    with _On(where, rows_k, stream, **tensors, q=q, q_out=q_out, positions=positions, slots=slots, err=err,
+             axis_delta=rope.axis_delta) as on:
+        if q is not None:
+            _bf16(q, "q")
+            if q_out is None:
+                q_out = on.empty(q.shape, torch.bfloat16)
+            _bf16(q_out, "q_out")
+            if q_out.shape != q.shape or (q.shape[2] > 0 and (q.stride(2) != 1 or q_out.stride(2) != 1)):
+                raise ValueError("q and q_out must be [T, H_q, width] with packed rows")
+            hq, qs, qh, os, oh = q.shape[1], q.stride(0), q.stride(1), q_out.stride(0), q_out.stride(1)
+        rows = _AppendRows(_addr(rows_k), _addr(rows_v), _addr(q), _addr(q_out), rows_k.stride(0), rows_v.stride(0),
+                           qs, qh, os, oh, _addr(positions), _addr(slots), T, hq, int(layer), 0)
+        r, keep = rope._c(T)
+        rc = call(C.byref(pool), C.byref(rows), C.byref(r), _addr(err), on.handle)
+    del keep
+    _check(rc, where)
+    return q_out
+
+
+def kamera_append_kv(pool_k: torch.Tensor, pool_v: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: Rope,
+                     positions: Optional[torch.Tensor], slots: torch.Tensor, layer: int = 0,
+                     q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                     err: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """New tokens' keys (turned by R(position)) and values into one layer of the
+    paged pool, and the queries turned on the way (``kamera_append_kv`` in
+    kamera.h).
+
+    pool_*: bf16 ``[L, S, H, d]`` (packed heads); k, v: bf16 ``[T, H, d]`` with
+    packed heads, any token stride (views of a fused projection); q: None or
+    bf16 ``[T, H_q, d]``, any token and head strides; q_out: like q (allocated
+    when None; may be q itself); positions, slots: int64 ``[T]``, slot -1 a
+    padding row.  Multi-axis RoPE: positions None, ``rope.axis_delta`` int64
+    ``[T, n_axes]``.  Returns ``q_out`` (None without q)."""
+    for t, nm in ((pool_k, "pool_k"), (pool_v, "pool_v"), (k, "k"), (v, "v")):
+        _bf16(t, nm)
+    if pool_k.dim() != 4 or pool_k.stride(3) != 1 or pool_k.stride(2) != pool_k.shape[3]:
+        raise ValueError("pool_k must be [L, S, H, d] with packed heads")
+    if pool_v.stride() != pool_k.stride() or pool_v.shape != pool_k.shape:
+        raise ValueError("pool_k and pool_v must share shape and strides")
+    L, S, H, d = pool_k.shape
+    for t, nm in ((k, "k"), (v, "v")):
+        if t.dim() != 3 or t.shape[1] != H or t.shape[2] != d or t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+            raise ValueError(f"{nm} must be [T, {H}, {d}] with packed heads")
+    T = k.shape[0]
+    if v.shape[0] != T or (q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != d)):
+        raise ValueError("k, v and q must hold the same tokens and head width")
+    pool = _GqaPool(L, H, d, 0, _addr(pool_k), _addr(pool_v), S, pool_k.stride(0), pool_k.stride(1))
+    return _append("kamera_append_kv", load_library().kamera_append_kv, pool, rope, k, v, q, q_out, positions, slots,
+                   layer, T, err, stream, dict(pool_k=pool_k, pool_v=pool_v, k=k, v=v))
+
+
+def kamera_mla_append_kv(pool: torch.Tensor, kv_lora: int, c: torch.Tensor, k_rope: torch.Tensor, rope: Rope,
+                         positions: Optional[torch.Tensor], slots: torch.Tensor, layer: int = 0,
+                         q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                         err: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """New tokens' latent rows into one layer of an MLA pool: c_KV copied, k_rope
+    turned by R(position) (``kamera_mla_append_kv`` in kamera.h).
+
+    pool: bf16 ``[L, S, kv_lora + rope_dim]``; c: bf16 ``[T, kv_lora]``; k_rope: bf16
+    ``[T, rope_dim]`` (packed rows, any token stride); q: None or the rope part of
+    the queries, bf16 ``[T, H_q, rope_dim]`` (any token and head strides, e.g. a
+    view of the full query heads); q_out likewise, e.g. the rope columns of the
+    absorbed queries; the rest as for ``kamera_append_kv``."""
+    for t, nm in ((pool, "pool"), (c, "c"), (k_rope, "k_rope")):
+        _bf16(t, nm)
+    if pool.dim() != 3 or pool.stride(2) != 1:
+        raise ValueError("pool must be [L, S, kv_lora + rope_dim] with packed rows")
+    L, S, W = pool.shape
+    lora, rd = int(kv_lora), W - int(kv_lora)
+    for t, nm, w in ((c, "c", lora), (k_rope, "k_rope", rd)):
+        if t.dim() != 2 or t.shape[1] != w or (w > 1 and t.stride(1) != 1):
+            raise ValueError(f"{nm} must be [T, {w}] with packed rows")
+    T = c.shape[0]
+    if k_rope.shape[0] != T or (q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != rd)):
+        raise ValueError("c, k_rope and q must hold the same tokens and rope width")
+    p = _MlaPool(L, lora, rd, 0, _addr(pool), S, pool.stride(0), pool.stride(1))
+    return _append("kamera_mla_append_kv", load_library().kamera_mla_append_kv, p, rope, k_rope, c, q, q_out, positions,
+                   slots, layer, T, err, stream, dict(pool=pool, c=c, k_rope=k_rope))
+
+
+def _paged_kv(pool_k, pool_v, page_size):
+    for t, nm in ((pool_k, "pool_k"), (pool_v, "pool_v")):
+        if t is None:
+            continue
+        _bf16(t, nm)
+        if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+            raise ValueError(f"{nm} must be [S, H, d] (one layer) with packed heads")
+    if pool_v is not None and (pool_v.shape != pool_k.shape or pool_v.stride() != pool_k.stride()):
+        raise ValueError("pool_k and pool_v must share shape and strides")
+    S, H, d = pool_k.shape
+    return _PagedKV(_addr(pool_k), _addr(pool_v), S, pool_k.stride(0), H, d, int(page_size), 0)
+
+
+def _paged_outputs(on, q, out, lse):
+    n, hq, _ = q.shape
+    if out is None:
+        out = on.empty(q.shape, torch.bfloat16)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 tensor shaped like q")
+    if lse is None:
+        lse = on.empty((n, hq), torch.float32)
+    elif lse is False:
+        lse = None
+    elif tuple(lse.shape) != (n, hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 [S, H_q] tensor")
+    return out, lse
+
+
+def _paged_q(q, d):
+    _bf16(q, "q")
+    if q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
+        raise ValueError("q must be a contiguous [S, H_q, d] tensor")
+
+
+def _table(pages, lens, n, max_len):
+    if pages is None and lens is None and int(max_len) == 0:
+        return _PageTable(None, None, 0, 0)
+    if pages is None or lens is None or pages.dim() != 2:
+        raise ValueError("pages must be [S, max_pages] and lens [S]")
+    _ints(pages, "pages", (n, pages.shape[1]))
+    _ints(lens, "lens", (n,))
+    return _PageTable(_addr(pages), _addr(lens), pages.shape[1], int(max_len))
+
+
+def kamera_attend_shared(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.Tensor, page_size: int,
+                         group_start: Optional[torch.Tensor], prefix_pages: Optional[torch.Tensor],
+                         prefix_len: Optional[torch.Tensor], pages: Optional[torch.Tensor],
+                         lens: Optional[torch.Tensor], max_group: int, max_prefix: int, max_len: int,
+                         scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse=None,
+                         err: Optional[torch.Tensor] = None, stream=None, workspace: Optional[torch.Tensor] = None):
+    """Decode attention over the paged pool for a batch whose sequences share
+    prefixes by groups, each prefix read once (``kamera_attend_shared`` in
+    kamera.h).
+
+    pool_*: bf16 ``[S_slots, H, d]`` (one layer); q: bf16 ``[S, H_q, d]`` contiguous;
+    group_start int32 ``[n_groups + 1]``, prefix_pages int32 ``[n_groups, width]``,
+    prefix_len int32 ``[n_groups]`` (all three None: no shared prefix); pages int32
+    ``[S, width]``, lens int32 ``[S]``: the sequences' own tokens (None with max_len
+    0); max_group, max_prefix, max_len: bounds of the group sizes and lengths;
+    lse: None (allocated), False (not computed) or fp32 ``[S, H_q]``; workspace:
+    None (allocated for the call) or a tensor of at least
+    ``kamera_attend_shared_workspace_bytes`` bytes.  Returns ``(out, lse)``."""
+    kv = _paged_kv(pool_k, pool_v, page_size)
+    _paged_q(q, kv.head_dim)
+    n, hq, d = q.shape
+    own = _table(pages, lens, n, max_len)
+    pre = None
+    if group_start is not None:
+        if prefix_pages is None or prefix_len is None or prefix_pages.dim() != 2:
+            raise ValueError("group_start, prefix_pages and prefix_len go together")
+        groups = prefix_pages.shape[0]
+        _ints(group_start, "group_start", (groups + 1,))
+        _ints(prefix_pages, "prefix_pages", (groups, prefix_pages.shape[1]))
+        _ints(prefix_len, "prefix_len", (groups,))
+        pre = _PrefixGroups(_addr(group_start), _addr(prefix_pages), _addr(prefix_len), groups, prefix_pages.shape[1],
+                            int(max_prefix), int(max_group))
+    elif prefix_pages is not None or prefix_len is not None:
+        raise ValueError("group_start, prefix_pages and prefix_len go together")
+    lib = load_library()
+    with _On("kamera_attend_shared", q, stream, pool_k=pool_k, pool_v=pool_v, q=q, group_start=group_start,
+             prefix_pages=prefix_pages, prefix_len=prefix_len, pages=pages, lens=lens, out=out, err=err,
+             lse=lse if isinstance(lse, torch.Tensor) else None, workspace=workspace) as on:
+        out, lse = _paged_outputs(on, q, out, lse)
+        qq = _PagedQuery(_addr(q), _addr(out), _addr(lse), n, hq, float(d ** -0.5 if scale is None else scale), 0)
+        pp = C.byref(pre) if pre is not None else None
+        need = (lib.kamera_attend_shared_workspace_bytes(C.byref(kv), C.byref(qq), pp, C.byref(own))
+                if workspace is None else 0)
+        keep, ws, ws_bytes = on.workspace(workspace, need)
+        rc = lib.kamera_attend_shared(C.byref(kv), C.byref(qq), pp, C.byref(own), ws, ws_bytes, _addr(err), on.handle)
+    del keep
+    _check(rc, "kamera_attend_shared")
+    return out, lse
+
+
+def kamera_summarize_pages(pool_k: torch.Tensor, page_size: int, page_ids: torch.Tensor, page_tokens: torch.Tensor,
+                           summary: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Per-channel minimum and maximum of the pages' keys (``kamera_summarize_pages``
+    in kamera.h).  pool_k: bf16 ``[S_slots, H, d]`` (one layer); page_ids,
+    page_tokens: int32 ``[n]``, the pages and how many of their first tokens
+    count; summary: bf16 ``[S_slots // page_size, H, 2, d]``, those pages' entries
+    written.  Returns ``summary``."""
+    kv = _paged_kv(pool_k, None, page_size)
+    S, H, d = pool_k.shape
+    _bf16(summary, "summary")
+    if int(page_size) < 1 or tuple(summary.shape) != (S // int(page_size), H, 2, d) or not summary.is_contiguous():
+        raise ValueError("summary must be a contiguous [S_slots // page_size, H, 2, d] tensor")
+    n = page_ids.shape[0] if page_ids.dim() == 1 else -1
+    _ints(page_ids, "page_ids", (n,))
+    _ints(page_tokens, "page_tokens", (n,))
+    with _On("kamera_summarize_pages", pool_k, stream, pool_k=pool_k, page_ids=page_ids, page_tokens=page_tokens,
+             summary=summary, err=err) as on:
+        rc = load_library().kamera_summarize_pages(C.byref(kv), _addr(page_ids), _addr(page_tokens), n, _addr(summary),
+                                                   _addr(err), on.handle)
+    _check(rc, "kamera_summarize_pages")
+    return summary
+
+
+def kamera_select_pages(q: torch.Tensor, summary: torch.Tensor, page_size: int, pages: torch.Tensor,
+                        lens: torch.Tensor, max_len: int, n_select: int, n_first: int = 1, n_last: int = 1,
+                        selected: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None, stream=None,
+                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The n_select pages of each sequence and KV head whose boxes reach the
+    largest q . k (``kamera_select_pages`` in kamera.h), the first n_first and last
+    n_last always among them.
+
+    q: bf16 ``[S, H_q, d]`` contiguous; summary: bf16 ``[n_pages, H, 2, d]``
+    (``kamera_summarize_pages``); pages int32 ``[S, width]``, lens int32 ``[S]``.
+    Returns ``selected``: int32 ``[S, H, n_select]``, ascending indices into the
+    sequence's page table row, then -1."""
+    _bf16(summary, "summary")
+    if summary.dim() != 4 or summary.shape[2] != 2 or not summary.is_contiguous():
+        raise ValueError("summary must be a contiguous [n_pages, H, 2, d] tensor")
+    N, H, _, d = summary.shape
+    _paged_q(q, d)
+    n, hq, _ = q.shape
+    k = int(n_select)
+    table = _table(pages, lens, n, max_len)
+    lib = load_library()
+    with _On("kamera_select_pages", q, stream, q=q, summary=summary, pages=pages, lens=lens, selected=selected,
+             err=err, workspace=workspace) as on:
+        if selected is None:
+            selected = on.empty((n, H, max(k, 0)), torch.int32)
+        _ints(selected, "selected", (n, H, k))
+        x = _PageSelect(_addr(q), _addr(summary), _addr(selected), N, n, hq, H, d, int(page_size), k, int(n_first),
+                        int(n_last))
+        need = (lib.kamera_select_pages_workspace_bytes(C.byref(x), C.byref(table)) if workspace is None else 0)
+        keep, ws, ws_bytes = on.workspace(workspace, need)
+        rc = lib.kamera_select_pages(C.byref(x), C.byref(table), ws, ws_bytes, _addr(err), on.handle)
+    del keep
+    _check(rc, "kamera_select_pages")
+    return selected
+
+
+def kamera_attend_selected(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.Tensor, page_size: int,
+                           pages: torch.Tensor, lens: torch.Tensor, selected: torch.Tensor, max_len: int,
+                           scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse=None,
+                           err: Optional[torch.Tensor] = None, stream=None,
+                           workspace: Optional[torch.Tensor] = None):
+    """Decode attention of each sequence and KV head over its selected pages only
+    (``kamera_attend_selected`` in kamera.h).  selected: int32 ``[S, H, k]`` as
+    ``kamera_select_pages`` returns it (distinct; negative entries skipped); the
+    rest as for ``kamera_attend_shared``.  Returns ``(out, lse)``."""
+    kv = _paged_kv(pool_k, pool_v, page_size)
+    _paged_q(q, kv.head_dim)
+    n, hq, d = q.shape
+    table = _table(pages, lens, n, max_len)
+    if selected.dim() != 3:
+        raise ValueError("selected must be [S, H, k]")
+    k = selected.shape[2]
+    _ints(selected, "selected", (n, kv.num_kv_heads, k))
+    lib = load_library()
+    with _On("kamera_attend_selected", q, stream, pool_k=pool_k, pool_v=pool_v, q=q, pages=pages, lens=lens,
+             selected=selected, out=out, err=err, lse=lse if isinstance(lse, torch.Tensor) else None,
+             workspace=workspace) as on:
+        out, lse = _paged_outputs(on, q, out, lse)
+        qq = _PagedQuery(_addr(q), _addr(out), _addr(lse), n, hq, float(d ** -0.5 if scale is None else scale), 0)
+        need = (lib.kamera_attend_selected_workspace_bytes(C.byref(kv), C.byref(qq), C.byref(table), k)
+                if workspace is None else 0)
+        keep, ws, ws_bytes = on.workspace(workspace, need)
+        rc = lib.kamera_attend_selected(C.byref(kv), C.byref(qq), C.byref(table), _addr(selected), k, ws, ws_bytes,
+                                        _addr(err), on.handle)
+    del keep
+    _check(rc, "kamera_attend_selected")
+    return out, lse

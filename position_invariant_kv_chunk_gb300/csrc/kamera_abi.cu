@@ -15,6 +15,7 @@
 
 #include "kamera.h"
 #include "kamera_common.cuh"
+#include "kamera_hostcheck.h"
 #include "kamera_internal.h"
 
 using namespace kamera;
@@ -77,28 +78,6 @@ int cluster_fit(const void* kernel, int block_threads, int smem_bytes, int cl)
     return fit;
 }
 
-}  // namespace kamera
-
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Byte range [lo, hi) spanned by a strided [L][rows][width] bf16 array.
-std::pair<uintptr_t, uintptr_t> span(const void* base, int64_t L, int64_t ls, int64_t rows, int64_t rs,
-                                     int64_t width)
-{
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(base);
-    if (L <= 0 || rows <= 0)
-        return {lo, lo};
-    const int64_t last = (L - 1) * ls + (rows - 1) * rs + width;
-    return {lo, lo + static_cast<uintptr_t>(last) * 2u};
-}
-
-bool overlap(std::pair<uintptr_t, uintptr_t> a, std::pair<uintptr_t, uintptr_t> b)
-{
-    return a.first < b.second && b.first < a.second;
-}
-
 // RoPE: theta_i = base^(-2i/rot_dim) (standard rotary frequencies) or the
 // caller's table.  `width` is the extent the rotary range must fit in.
 int fill_rope(const KameraRope* r, int width, RopeParams* out)
@@ -154,6 +133,10 @@ int fill_rope(const KameraRope* r, int width, RopeParams* out)
     return KAMERA_OK;
 }
 
+}  // namespace kamera
+
+namespace {
+
 int check_call(const KameraChunk* d_chunks, int32_t n_chunks, int32_t max_len, int32_t max_rank,
                bool* noop)
 {
@@ -170,20 +153,6 @@ int check_call(const KameraChunk* d_chunks, int32_t n_chunks, int32_t max_len, i
         return KAMERA_ERR_INVALID_ARGUMENT;
     if (reinterpret_cast<uintptr_t>(d_chunks) & 7u)
         return KAMERA_ERR_MISALIGNED;
-    return KAMERA_OK;
-}
-
-int check_strided(const void* base, int64_t L, int64_t ls, int64_t rows, int64_t rs, int64_t width,
-                  bool need_rows)
-{
-    if (!base)
-        return KAMERA_ERR_INVALID_ARGUMENT;
-    if (!aligned16(base) || (ls & 7) || (rs & 7))
-        return KAMERA_ERR_MISALIGNED;
-    if (rows < 0 || (need_rows && rows < 1) || rs < width || ls < 0)
-        return KAMERA_ERR_INVALID_ARGUMENT;
-    if (L > 1 && ls < rows * rs)
-        return KAMERA_ERR_INVALID_ARGUMENT;
     return KAMERA_OK;
 }
 

@@ -55,11 +55,14 @@
 #include "kamera_common.cuh"
 #include "kamera_internal.h"
 #include "kamera_ptx.cuh"
+#include "kamera_tc.cuh"
 #include "kamera_warpmma.cuh"
 
 namespace kamera {
 
 namespace {
+
+using namespace tc;
 
 constexpr int kPfRows = 128;          // query rows per CTA = MMA M = TMEM lanes
 constexpr int kPfTok = 64;            // tokens per tile
@@ -116,45 +119,6 @@ struct PrefillLaunch {
     int32_t withhold;                  // test hook: the producer starts no tile copy
 };
 
-__device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(ta)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t ta, const uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(ta),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st4(uint32_t ta, const uint32_t (&r)[4])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ta), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// 16-byte piece c of row r of a 128B-swizzled tile of 128-byte rows (the TMA
-// and MMA layout): piece c ^ (r & 7).
-__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ int32_t prefill_check(const KameraChunk& ch, int c, const PrefillParams& p)
@@ -186,16 +150,6 @@ __device__ __forceinline__ void seq_chunks(const PrefillParams& p, int seq, int&
     c1 = p.seq_start[seq + 1];
     if (c0 < 0 || c1 < c0 || c1 > p.n_chunks)
         c0 = c1 = 0;
-}
-
-// Waits for a phase whatever the abort flag says, up to `limit` ns: the drain
-// of copies and MMAs a role started before it leaves.
-__device__ __forceinline__ void pf_drain_wait(uint32_t bar, uint32_t parity, uint64_t limit)
-{
-    const uint64_t t0 = ptx::globaltimer();
-    while (!ptx::mbar_try_wait(bar, parity))
-        if (ptx::globaltimer() - t0 > limit)
-            return;
 }
 
 // Rows [0, ntok) of the tile's U and U' blocks (m-wide factor rows, `uk` and
@@ -338,55 +292,6 @@ __device__ void pf_producer(const PrefillLaunch& P, uint32_t sbase, PfBars& b, i
         for (uint32_t k = n > (uint32_t)L::NS ? n - L::NS : 0u; k < n; ++k)
             pf_drain_wait(ptx::smem_addr(&b.full[k % L::NS]), (k / L::NS) & 1u, P.wait_ns);
     __syncwarp();
-}
-
-// Shared-memory matrix descriptors as (low word, high word): the low word holds
-// the start address (bytes >> 4) and the leading byte offset, so a step inside
-// an operand is one 32-bit add.  High word: stride byte offset 1024 (8-row
-// groups), descriptor version 1, 128-byte swizzle.  A K-major operand (the key
-// and U rows) ignores the leading offset; for an MN-major one (the value and U'
-// rows: the rows of a TMA box are K, the N dimension is contiguous) it is the
-// distance between 64-element atoms along N.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint64_t pf_desc(uint32_t lo)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
-    return d;
-}
-
-// D[tmem] (+)= A[tmem] * B[smem]^T (kind::f16: bf16 in, fp32 accumulate), the
-// accumulate flag a compile-time constant.  A's row r sits in TMEM lane r,
-// elements 2c and 2c + 1 in the low and high half of column c.
-template <bool ACC>
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc)
-{
-    if constexpr (ACC)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 1, 1;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "r"(a_tmem), "l"(pf_desc(b_lo)), "r"(idesc)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 1, 1;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "r"(a_tmem), "l"(pf_desc(b_lo)), "r"(idesc)
-                     : "memory");
-}
-
-// D[tmem] (+)= A[smem] * B[smem]^T (kind::f16), accumulate flag constant.
-template <bool ACC>
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
-{
-    if constexpr (ACC)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 1, 1;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "l"(pf_desc(a_lo)), "l"(pf_desc(b_lo)), "r"(idesc)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 1, 1;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "l"(pf_desc(a_lo)), "l"(pf_desc(b_lo)), "r"(idesc)
-                     : "memory");
 }
 
 // The MMA lane.  Per tile n: S(n) = [Q'hi | Q'lo | Xhi | Xlo] [k | k | u | u]^T
@@ -613,15 +518,6 @@ __device__ __forceinline__ void pf_split_w(uint32_t lane_base)
     tmem_st32(lane_base + L::kTmOu, hi);
     tmem_st32(lane_base + L::kTmOu + 32, lo);
     tmem_wait_st();
-}
-
-// 2^x (the MUFU approximation: relative error near 2^-22, subnormal results
-// flushed to zero).
-__device__ __forceinline__ float pf_ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // The largest (`neg`: smallest) of the row's first ntok raw scores.
