@@ -11,6 +11,7 @@ without the compiled library (or without a GPU) every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -797,104 +798,125 @@ def kamera_mla_attend_reused(store: torch.Tensor, kv_lora: int, q: torch.Tensor,
 
 
 # ------------------------------------------------ decode steps over the pool --
-class _On:
-    """Where a call runs: the tensors' device (made current for the call) and its
-    stream.  Every tensor must live on that device.  ``empty`` gives memory that
-    is safe on that stream: with another stream than the current one it comes
-    from that stream's pool (a block of the current stream's could still be in
-    use there) and is marked as used on the current one, where the caller reads
-    it; so no buffer is kept between calls, and a captured graph owns its own."""
-
-    __slots__ = ("device", "guard", "stream", "handle", "side")
-
-    def __init__(self, where: str, ref: torch.Tensor, stream, **tensors):
-        self.device, self.guard, self.side = ref.device, None, None
-        cuda = torch.cuda.is_available()
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if cuda and not t.is_cuda:
-                raise ValueError(f"{where}: {name} must be a CUDA tensor")
-            if t.device != self.device:
-                raise ValueError(f"{where}: {name} is on {t.device}, not on {self.device}")
-        self.stream = stream
-        self.handle = 0
-
-    def __enter__(self):
-        if self.device.type == "cuda":
-            if self.device.index != torch.cuda.current_device():
-                self.guard = torch.cuda.device(self.device)
-                self.guard.__enter__()
-            current = int(torch.cuda.current_stream().cuda_stream)
-            self.handle = current if self.stream is None else _stream_handle(self.stream)
-            if self.handle != current:
-                self.side = (self.stream if isinstance(self.stream, torch.cuda.Stream)
-                             else torch.cuda.ExternalStream(self.handle, device=self.device))
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def empty(self, shape, dtype):
-        if self.side is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        here = torch.cuda.current_stream()
-        with torch.cuda.stream(self.side):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
-        t.record_stream(here)
-        return t
-
-    def workspace(self, workspace, need: int):
-        """(tensor to keep until the launch, address, bytes): the caller's, or one of `need` bytes."""
-        if workspace is not None:
-            if not workspace.is_contiguous():
-                raise ValueError("workspace must be contiguous")
-            return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        if need == 0:
-            return None, None, 0
-        t = self.empty(need, torch.uint8)
-        return t, t.data_ptr(), need
+# A decode step's kernels take a few microseconds, so what these wrappers do per
+# call is kept short: device indices instead of device objects, no call that
+# only repeats a check, and one allocation per array.
+_BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+_NOTHING = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _ints(t: torch.Tensor, name: str, shape, dtype=torch.int32):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _wrong_place(where, names, tensors):
+    dev = tensors[0].device
+    for name, t in zip(names.split(), tensors):
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} must be a CUDA tensor")
+        if t.device != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, not on {dev}")
+
+
+def _place(where: str, names: str, *tensors) -> int:
+    """The device index that every tensor lives on (-1: host memory, where no CUDA
+    is present; ``_on_device`` says why)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _wrong_place(where, names, tensors)
+    if dev < 0 and torch.cuda.is_available():
+        _wrong_place(where, names, tensors)
+    return dev
+
+
+def _current(dev: int):
+    """A context in which device ``dev`` is the current one."""
+    return _NOTHING if dev < 0 or dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _on_stream(dev: int, stream):
+    """(handle of the call's stream, that stream where it is not the current one)."""
+    if dev < 0:
+        return 0, None
+    here = _raw_stream(dev) if _raw_stream is not None else int(torch.cuda.current_stream().cuda_stream)
+    if stream is None:
+        return here, None
+    handle = _stream_handle(stream)
+    if handle == here:
+        return handle, None
+    return handle, (stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle))
+
+
+def _new(ref: torch.Tensor, shape, dtype, side):
+    """Memory on ref's device that is safe on the call's stream: with another stream
+    than the current one (``side``) it comes from that stream's pool -- a block of
+    the current stream's could still be in use there -- and is marked as used on
+    the current one, where the caller reads it.  Nothing is kept between calls,
+    so a captured graph owns its workspace."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=ref.device)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=ref.device)
+    t.record_stream(here)
+    return t
+
+
+def _scratch(ref, workspace, need: int, side):
+    """(tensor to keep until the launch, address, bytes): the caller's, or one of `need` bytes."""
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, None, 0
+    t = _new(ref, need, torch.uint8, side)
+    return t, t.data_ptr(), need
+
+
+def _ints(t: torch.Tensor, name: str, shape, dtype=_I32):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
-def _append(where, call, pool, rope, rows_k, rows_v, q, q_out, positions, slots, layer, T, err, stream, tensors):
+def _append(where, call, pool, rope, rows_k, rows_v, q, q_out, positions, slots, layer, T, err, stream, names, *pools):
     """The arguments both append entry points share, and the call."""
-    _ints(slots, "slots", (T,), torch.int64)
-    if rope.axis_delta is not None:
+    _ints(slots, "slots", (T,), _I64)
+    axes = rope.axis_delta
+    if axes is not None:
         if positions is not None:
             raise ValueError("with rope.axis_delta the positions are its rows; positions must be None")
-        if rope.axis_delta.dim() != 2 or rope.axis_delta.shape[0] != T or not rope.axis_delta.is_contiguous():
+        if axes.dim() != 2 or axes.shape[0] != T or not axes.is_contiguous():
             raise ValueError("rope.axis_delta must be a contiguous [T, n_axes] tensor of positions")
     elif positions is None:
         raise ValueError("positions are needed")
     else:
-        _ints(positions, "positions", (T,), torch.int64)
-    hq, qs, qh, os, oh = 0, 0, 0, 0, 0
+        _ints(positions, "positions", (T,), _I64)
     if q_out is not None and q is None:
         raise ValueError("q_out without q")
-    if err is not None and (err.dtype != torch.int32 or err.numel() < 1):
+    if err is not None and (err.dtype != _I32 or err.numel() < 1):
         raise ValueError("err must be an int32 tensor")
-    with _On(where, rows_k, stream, **tensors, q=q, q_out=q_out, positions=positions, slots=slots, err=err,
-             axis_delta=rope.axis_delta) as on:
+    dev = _place(where, "k v q q_out positions slots err axis_delta " + names, rows_k, rows_v, q, q_out, positions,
+                 slots, err, axes, *pools)
+    with _current(dev):
+        handle, side = _on_stream(dev, stream)
+        hq, qs, qh, os, oh = 0, 0, 0, 0, 0
         if q is not None:
-            _bf16(q, "q")
             if q_out is None:
-                q_out = on.empty(q.shape, torch.bfloat16)
-            _bf16(q_out, "q_out")
-            if q_out.shape != q.shape or (q.shape[2] > 0 and (q.stride(2) != 1 or q_out.stride(2) != 1)):
-                raise ValueError("q and q_out must be [T, H_q, width] with packed rows")
-            hq, qs, qh, os, oh = q.shape[1], q.stride(0), q.stride(1), q_out.stride(0), q_out.stride(1)
-        rows = _AppendRows(_addr(rows_k), _addr(rows_v), _addr(q), _addr(q_out), rows_k.stride(0), rows_v.stride(0),
-                           qs, qh, os, oh, _addr(positions), _addr(slots), T, hq, int(layer), 0)
+                q_out = _new(q, q.shape, _BF16, side)
+            if (q.dtype != _BF16 or q_out.dtype != _BF16 or q_out.shape != q.shape
+                    or (q.shape[2] > 0 and (q.stride(2) != 1 or q_out.stride(2) != 1))):
+                raise ValueError("q and q_out must be bf16 [T, H_q, width] with packed rows")
+            hq = q.shape[1]
+            qs, qh, _ = q.stride()
+            os, oh, _ = q_out.stride()
+        rows = _AppendRows(rows_k.data_ptr(), rows_v.data_ptr(), _addr(q), _addr(q_out), rows_k.stride(0),
+                           rows_v.stride(0), qs, qh, os, oh, _addr(positions), slots.data_ptr(), T, hq, int(layer), 0)
         r, keep = rope._c(T)
-        rc = call(C.byref(pool), C.byref(rows), C.byref(r), _addr(err), on.handle)
+        rc = call(C.byref(pool), C.byref(rows), C.byref(r), _addr(err), handle)
     del keep
-    _check(rc, where)
+    if rc:
+        raise KameraError(rc, where)
     return q_out
 
 
@@ -913,21 +935,24 @@ def kamera_append_kv(pool_k: torch.Tensor, pool_v: torch.Tensor, k: torch.Tensor
     padding row.  Multi-axis RoPE: positions None, ``rope.axis_delta`` int64
     ``[T, n_axes]``.  Returns ``q_out`` (None without q)."""
     for t, nm in ((pool_k, "pool_k"), (pool_v, "pool_v"), (k, "k"), (v, "v")):
-        _bf16(t, nm)
-    if pool_k.dim() != 4 or pool_k.stride(3) != 1 or pool_k.stride(2) != pool_k.shape[3]:
+        if t.dtype != _BF16:
+            _bf16(t, nm)
+    if pool_k.dim() != 4:
         raise ValueError("pool_k must be [L, S, H, d] with packed heads")
-    if pool_v.stride() != pool_k.stride() or pool_v.shape != pool_k.shape:
+    (L, S, H, d), strides = pool_k.shape, pool_k.stride()
+    if strides[3] != 1 or strides[2] != d:
+        raise ValueError("pool_k must be [L, S, H, d] with packed heads")
+    if pool_v.stride() != strides or pool_v.shape != pool_k.shape:
         raise ValueError("pool_k and pool_v must share shape and strides")
-    L, S, H, d = pool_k.shape
-    for t, nm in ((k, "k"), (v, "v")):
-        if t.dim() != 3 or t.shape[1] != H or t.shape[2] != d or t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
-            raise ValueError(f"{nm} must be [T, {H}, {d}] with packed heads")
     T = k.shape[0]
-    if v.shape[0] != T or (q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != d)):
+    for t, nm in ((k, "k"), (v, "v")):
+        if t.shape != (T, H, d) or t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+            raise ValueError(f"{nm} must be [T, {H}, {d}] with packed heads")
+    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != d):
         raise ValueError("k, v and q must hold the same tokens and head width")
-    pool = _GqaPool(L, H, d, 0, _addr(pool_k), _addr(pool_v), S, pool_k.stride(0), pool_k.stride(1))
+    pool = _GqaPool(L, H, d, 0, pool_k.data_ptr(), pool_v.data_ptr(), S, strides[0], strides[1])
     return _append("kamera_append_kv", load_library().kamera_append_kv, pool, rope, k, v, q, q_out, positions, slots,
-                   layer, T, err, stream, dict(pool_k=pool_k, pool_v=pool_v, k=k, v=v))
+                   layer, T, err, stream, "pool_k pool_v", pool_k, pool_v)
 
 
 def kamera_mla_append_kv(pool: torch.Tensor, kv_lora: int, c: torch.Tensor, k_rope: torch.Tensor, rope: Rope,
@@ -943,54 +968,55 @@ def kamera_mla_append_kv(pool: torch.Tensor, kv_lora: int, c: torch.Tensor, k_ro
     view of the full query heads); q_out likewise, e.g. the rope columns of the
     absorbed queries; the rest as for ``kamera_append_kv``."""
     for t, nm in ((pool, "pool"), (c, "c"), (k_rope, "k_rope")):
-        _bf16(t, nm)
+        if t.dtype != _BF16:
+            _bf16(t, nm)
     if pool.dim() != 3 or pool.stride(2) != 1:
         raise ValueError("pool must be [L, S, kv_lora + rope_dim] with packed rows")
     L, S, W = pool.shape
-    lora, rd = int(kv_lora), W - int(kv_lora)
+    lora, rd, T = int(kv_lora), W - int(kv_lora), c.shape[0]
     for t, nm, w in ((c, "c", lora), (k_rope, "k_rope", rd)):
-        if t.dim() != 2 or t.shape[1] != w or (w > 1 and t.stride(1) != 1):
+        if t.shape != (T, w) or (w > 1 and t.stride(1) != 1):
             raise ValueError(f"{nm} must be [T, {w}] with packed rows")
-    T = c.shape[0]
-    if k_rope.shape[0] != T or (q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != rd)):
+    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != rd):
         raise ValueError("c, k_rope and q must hold the same tokens and rope width")
-    p = _MlaPool(L, lora, rd, 0, _addr(pool), S, pool.stride(0), pool.stride(1))
+    p = _MlaPool(L, lora, rd, 0, pool.data_ptr(), S, pool.stride(0), pool.stride(1))
     return _append("kamera_mla_append_kv", load_library().kamera_mla_append_kv, p, rope, k_rope, c, q, q_out, positions,
-                   slots, layer, T, err, stream, dict(pool=pool, c=c, k_rope=k_rope))
+                   slots, layer, T, err, stream, "pool", pool)
 
 
 def _paged_kv(pool_k, pool_v, page_size):
-    for t, nm in ((pool_k, "pool_k"), (pool_v, "pool_v")):
-        if t is None:
-            continue
-        _bf16(t, nm)
-        if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
-            raise ValueError(f"{nm} must be [S, H, d] (one layer) with packed heads")
-    if pool_v is not None and (pool_v.shape != pool_k.shape or pool_v.stride() != pool_k.stride()):
-        raise ValueError("pool_k and pool_v must share shape and strides")
-    S, H, d = pool_k.shape
-    return _PagedKV(_addr(pool_k), _addr(pool_v), S, pool_k.stride(0), H, d, int(page_size), 0)
+    if pool_k.dtype != _BF16 or pool_k.dim() != 3:
+        raise ValueError("pool_k must be bf16 [S, H, d] (one layer) with packed heads")
+    (S, H, d), strides = pool_k.shape, pool_k.stride()
+    if strides[2] != 1 or strides[1] != d:
+        raise ValueError("pool_k must be bf16 [S, H, d] (one layer) with packed heads")
+    if pool_v is None:
+        return _PagedKV(pool_k.data_ptr(), None, S, strides[0], H, d, int(page_size), 0), H, d
+    if pool_v.dtype != _BF16 or pool_v.shape != pool_k.shape or pool_v.stride() != strides:
+        raise ValueError("pool_k and pool_v must share type, shape and strides")
+    return _PagedKV(pool_k.data_ptr(), pool_v.data_ptr(), S, strides[0], H, d, int(page_size), 0), H, d
 
 
-def _paged_outputs(on, q, out, lse):
+def _paged_query(q, d, scale, out, lse, side):
+    """The outputs and the query struct; out and lse allocated where they are None."""
     n, hq, _ = q.shape
     if out is None:
-        out = on.empty(q.shape, torch.bfloat16)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        out = _new(q, q.shape, _BF16, side)
+    elif out.shape != q.shape or out.dtype != _BF16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if lse is None:
-        lse = on.empty((n, hq), torch.float32)
+        lse = _new(q, (n, hq), _F32, side)
     elif lse is False:
         lse = None
-    elif tuple(lse.shape) != (n, hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    elif lse.shape != (n, hq) or lse.dtype != _F32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 [S, H_q] tensor")
-    return out, lse
+    return out, lse, _PagedQuery(q.data_ptr(), out.data_ptr(), _addr(lse), n, hq,
+                                 d ** -0.5 if scale is None else float(scale), 0)
 
 
 def _paged_q(q, d):
-    _bf16(q, "q")
-    if q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
-        raise ValueError("q must be a contiguous [S, H_q, d] tensor")
+    if q.dtype != _BF16 or q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 [S, H_q, d] tensor")
 
 
 def _table(pages, lens, n, max_len):
@@ -998,9 +1024,10 @@ def _table(pages, lens, n, max_len):
         return _PageTable(None, None, 0, 0)
     if pages is None or lens is None or pages.dim() != 2:
         raise ValueError("pages must be [S, max_pages] and lens [S]")
-    _ints(pages, "pages", (n, pages.shape[1]))
+    width = pages.shape[1]
+    _ints(pages, "pages", (n, width))
     _ints(lens, "lens", (n,))
-    return _PageTable(_addr(pages), _addr(lens), pages.shape[1], int(max_len))
+    return _PageTable(pages.data_ptr(), lens.data_ptr(), width, int(max_len))
 
 
 def kamera_attend_shared(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.Tensor, page_size: int,
@@ -1021,35 +1048,35 @@ def kamera_attend_shared(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.Te
     lse: None (allocated), False (not computed) or fp32 ``[S, H_q]``; workspace:
     None (allocated for the call) or a tensor of at least
     ``kamera_attend_shared_workspace_bytes`` bytes.  Returns ``(out, lse)``."""
-    kv = _paged_kv(pool_k, pool_v, page_size)
-    _paged_q(q, kv.head_dim)
-    n, hq, d = q.shape
-    own = _table(pages, lens, n, max_len)
+    kv, _, d = _paged_kv(pool_k, pool_v, page_size)
+    _paged_q(q, d)
+    own = C.byref(_table(pages, lens, q.shape[0], max_len))
     pre = None
     if group_start is not None:
         if prefix_pages is None or prefix_len is None or prefix_pages.dim() != 2:
             raise ValueError("group_start, prefix_pages and prefix_len go together")
-        groups = prefix_pages.shape[0]
+        groups, width = prefix_pages.shape
         _ints(group_start, "group_start", (groups + 1,))
-        _ints(prefix_pages, "prefix_pages", (groups, prefix_pages.shape[1]))
+        _ints(prefix_pages, "prefix_pages", (groups, width))
         _ints(prefix_len, "prefix_len", (groups,))
-        pre = _PrefixGroups(_addr(group_start), _addr(prefix_pages), _addr(prefix_len), groups, prefix_pages.shape[1],
-                            int(max_prefix), int(max_group))
+        pre = C.byref(_PrefixGroups(group_start.data_ptr(), prefix_pages.data_ptr(), prefix_len.data_ptr(), groups,
+                                    width, int(max_prefix), int(max_group)))
     elif prefix_pages is not None or prefix_len is not None:
         raise ValueError("group_start, prefix_pages and prefix_len go together")
+    dev = _place("kamera_attend_shared", "q pool_k pool_v group_start prefix_pages prefix_len pages lens out err "
+                 "workspace lse", q, pool_k, pool_v, group_start, prefix_pages, prefix_len, pages, lens, out, err,
+                 workspace, lse if isinstance(lse, torch.Tensor) else None)
     lib = load_library()
-    with _On("kamera_attend_shared", q, stream, pool_k=pool_k, pool_v=pool_v, q=q, group_start=group_start,
-             prefix_pages=prefix_pages, prefix_len=prefix_len, pages=pages, lens=lens, out=out, err=err,
-             lse=lse if isinstance(lse, torch.Tensor) else None, workspace=workspace) as on:
-        out, lse = _paged_outputs(on, q, out, lse)
-        qq = _PagedQuery(_addr(q), _addr(out), _addr(lse), n, hq, float(d ** -0.5 if scale is None else scale), 0)
-        pp = C.byref(pre) if pre is not None else None
-        need = (lib.kamera_attend_shared_workspace_bytes(C.byref(kv), C.byref(qq), pp, C.byref(own))
-                if workspace is None else 0)
-        keep, ws, ws_bytes = on.workspace(workspace, need)
-        rc = lib.kamera_attend_shared(C.byref(kv), C.byref(qq), pp, C.byref(own), ws, ws_bytes, _addr(err), on.handle)
+    with _current(dev):
+        handle, side = _on_stream(dev, stream)
+        out, lse, qq = _paged_query(q, d, scale, out, lse, side)
+        kv, qq = C.byref(kv), C.byref(qq)
+        need = lib.kamera_attend_shared_workspace_bytes(kv, qq, pre, own) if workspace is None else 0
+        keep, ws, ws_bytes = _scratch(q, workspace, need, side)
+        rc = lib.kamera_attend_shared(kv, qq, pre, own, ws, ws_bytes, _addr(err), handle)
     del keep
-    _check(rc, "kamera_attend_shared")
+    if rc:
+        raise KameraError(rc, "kamera_attend_shared")
     return out, lse
 
 
@@ -1060,19 +1087,20 @@ def kamera_summarize_pages(pool_k: torch.Tensor, page_size: int, page_ids: torch
     page_tokens: int32 ``[n]``, the pages and how many of their first tokens
     count; summary: bf16 ``[S_slots // page_size, H, 2, d]``, those pages' entries
     written.  Returns ``summary``."""
-    kv = _paged_kv(pool_k, None, page_size)
-    S, H, d = pool_k.shape
-    _bf16(summary, "summary")
-    if int(page_size) < 1 or tuple(summary.shape) != (S // int(page_size), H, 2, d) or not summary.is_contiguous():
-        raise ValueError("summary must be a contiguous [S_slots // page_size, H, 2, d] tensor")
-    n = page_ids.shape[0] if page_ids.dim() == 1 else -1
+    kv, H, d = _paged_kv(pool_k, None, page_size)
+    if (summary.dtype != _BF16 or int(page_size) < 1 or not summary.is_contiguous()
+            or summary.shape != (pool_k.shape[0] // int(page_size), H, 2, d)):
+        raise ValueError("summary must be a contiguous bf16 [S_slots // page_size, H, 2, d] tensor")
+    n = page_ids.numel()
     _ints(page_ids, "page_ids", (n,))
     _ints(page_tokens, "page_tokens", (n,))
-    with _On("kamera_summarize_pages", pool_k, stream, pool_k=pool_k, page_ids=page_ids, page_tokens=page_tokens,
-             summary=summary, err=err) as on:
-        rc = load_library().kamera_summarize_pages(C.byref(kv), _addr(page_ids), _addr(page_tokens), n, _addr(summary),
-                                                   _addr(err), on.handle)
-    _check(rc, "kamera_summarize_pages")
+    dev = _place("kamera_summarize_pages", "pool_k page_ids page_tokens summary err", pool_k, page_ids, page_tokens,
+                 summary, err)
+    with _current(dev):
+        rc = load_library().kamera_summarize_pages(C.byref(kv), page_ids.data_ptr(), page_tokens.data_ptr(), n,
+                                                   summary.data_ptr(), _addr(err), _on_stream(dev, stream)[0])
+    if rc:
+        raise KameraError(rc, "kamera_summarize_pages")
     return summary
 
 
@@ -1088,27 +1116,30 @@ def kamera_select_pages(q: torch.Tensor, summary: torch.Tensor, page_size: int, 
     (``kamera_summarize_pages``); pages int32 ``[S, width]``, lens int32 ``[S]``.
     Returns ``selected``: int32 ``[S, H, n_select]``, ascending indices into the
     sequence's page table row, then -1."""
-    _bf16(summary, "summary")
-    if summary.dim() != 4 or summary.shape[2] != 2 or not summary.is_contiguous():
-        raise ValueError("summary must be a contiguous [n_pages, H, 2, d] tensor")
+    if summary.dtype != _BF16 or summary.dim() != 4 or summary.shape[2] != 2 or not summary.is_contiguous():
+        raise ValueError("summary must be a contiguous bf16 [n_pages, H, 2, d] tensor")
     N, H, _, d = summary.shape
     _paged_q(q, d)
     n, hq, _ = q.shape
     k = int(n_select)
-    table = _table(pages, lens, n, max_len)
+    table = C.byref(_table(pages, lens, n, max_len))
+    dev = _place("kamera_select_pages", "q summary pages lens selected err workspace", q, summary, pages, lens,
+                 selected, err, workspace)
     lib = load_library()
-    with _On("kamera_select_pages", q, stream, q=q, summary=summary, pages=pages, lens=lens, selected=selected,
-             err=err, workspace=workspace) as on:
+    with _current(dev):
+        handle, side = _on_stream(dev, stream)
         if selected is None:
-            selected = on.empty((n, H, max(k, 0)), torch.int32)
-        _ints(selected, "selected", (n, H, k))
-        x = _PageSelect(_addr(q), _addr(summary), _addr(selected), N, n, hq, H, d, int(page_size), k, int(n_first),
-                        int(n_last))
-        need = (lib.kamera_select_pages_workspace_bytes(C.byref(x), C.byref(table)) if workspace is None else 0)
-        keep, ws, ws_bytes = on.workspace(workspace, need)
-        rc = lib.kamera_select_pages(C.byref(x), C.byref(table), ws, ws_bytes, _addr(err), on.handle)
+            selected = _new(q, (n, H, max(k, 0)), _I32, side)
+        else:
+            _ints(selected, "selected", (n, H, k))
+        x = C.byref(_PageSelect(q.data_ptr(), summary.data_ptr(), selected.data_ptr(), N, n, hq, H, d, int(page_size),
+                                k, int(n_first), int(n_last)))
+        need = lib.kamera_select_pages_workspace_bytes(x, table) if workspace is None else 0
+        keep, ws, ws_bytes = _scratch(q, workspace, need, side)
+        rc = lib.kamera_select_pages(x, table, ws, ws_bytes, _addr(err), handle)
     del keep
-    _check(rc, "kamera_select_pages")
+    if rc:
+        raise KameraError(rc, "kamera_select_pages")
     return selected
 
 
@@ -1121,25 +1152,25 @@ def kamera_attend_selected(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.
     (``kamera_attend_selected`` in kamera.h).  selected: int32 ``[S, H, k]`` as
     ``kamera_select_pages`` returns it (distinct; negative entries skipped); the
     rest as for ``kamera_attend_shared``.  Returns ``(out, lse)``."""
-    kv = _paged_kv(pool_k, pool_v, page_size)
-    _paged_q(q, kv.head_dim)
-    n, hq, d = q.shape
-    table = _table(pages, lens, n, max_len)
+    kv, H, d = _paged_kv(pool_k, pool_v, page_size)
+    _paged_q(q, d)
+    n = q.shape[0]
+    table = C.byref(_table(pages, lens, n, max_len))
     if selected.dim() != 3:
         raise ValueError("selected must be [S, H, k]")
     k = selected.shape[2]
-    _ints(selected, "selected", (n, kv.num_kv_heads, k))
+    _ints(selected, "selected", (n, H, k))
+    dev = _place("kamera_attend_selected", "q pool_k pool_v pages lens selected out err workspace lse", q, pool_k,
+                 pool_v, pages, lens, selected, out, err, workspace, lse if isinstance(lse, torch.Tensor) else None)
     lib = load_library()
-    with _On("kamera_attend_selected", q, stream, pool_k=pool_k, pool_v=pool_v, q=q, pages=pages, lens=lens,
-             selected=selected, out=out, err=err, lse=lse if isinstance(lse, torch.Tensor) else None,
-             workspace=workspace) as on:
-        out, lse = _paged_outputs(on, q, out, lse)
-        qq = _PagedQuery(_addr(q), _addr(out), _addr(lse), n, hq, float(d ** -0.5 if scale is None else scale), 0)
-        need = (lib.kamera_attend_selected_workspace_bytes(C.byref(kv), C.byref(qq), C.byref(table), k)
-                if workspace is None else 0)
-        keep, ws, ws_bytes = on.workspace(workspace, need)
-        rc = lib.kamera_attend_selected(C.byref(kv), C.byref(qq), C.byref(table), _addr(selected), k, ws, ws_bytes,
-                                        _addr(err), on.handle)
+    with _current(dev):
+        handle, side = _on_stream(dev, stream)
+        out, lse, qq = _paged_query(q, d, scale, out, lse, side)
+        kv, qq = C.byref(kv), C.byref(qq)
+        need = lib.kamera_attend_selected_workspace_bytes(kv, qq, table, k) if workspace is None else 0
+        keep, ws, ws_bytes = _scratch(q, workspace, need, side)
+        rc = lib.kamera_attend_selected(kv, qq, table, selected.data_ptr(), k, ws, ws_bytes, _addr(err), handle)
     del keep
-    _check(rc, "kamera_attend_selected")
+    if rc:
+        raise KameraError(rc, "kamera_attend_selected")
     return out, lse

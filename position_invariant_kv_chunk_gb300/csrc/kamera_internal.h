@@ -75,12 +75,38 @@ cudaError_t launch_attend_merge(const float* ws, int64_t units, int64_t ctas, in
 bool prefill_supported(int head_dim, int max_rank);
 cudaError_t launch_prefill(const PrefillParams& p, cudaStream_t stream);
 
+// Launch of `kernel`; `dependent`: it may start before the stream's previous
+// kernel has completed (its device code orders itself with grid_wait).
+template <typename... K, typename... A>
+inline cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int block, size_t smem, cudaStream_t stream,
+                                bool dependent, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
+}
+
 // 2-D tensor map (a CUtensorMap, 64-byte aligned, at `map`) over a bf16 array
 // of `rows` rows of `width` elements, row_stride elements apart: boxes of
 // box_cols x box_rows, 128-byte swizzle, rows past the end read as zero.
 // False if the driver has no encoder or refuses the shape.
 bool make_rows_map(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int box_cols,
                    int box_rows);
+
+// The same array in groups of eight rows (64 columns, row in its group, column
+// block of 64, group): one box holds `blocks` column blocks of `groups` groups,
+// as [group][block][8 rows][128 bytes] in shared memory.  Rows past the last
+// whole group are left out.
+bool make_groups_map(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int blocks,
+                     int groups);
 
 // Tensor-core path (tcgen05 MMA for the rank-m patch; relocation with rank > 0).
 bool umma_supported(const RowsParams& p, int family);

@@ -48,7 +48,7 @@ struct PgLayout {
     static constexpr int NB = D / 64;
     static constexpr uint32_t kBox = kPgTok * 128;
     static constexpr uint32_t kPiece = 2 * NB * kBox;          // keys, then values
-    static constexpr int NS = D == 128 ? 3 : 6;
+    static constexpr int NS = D == 128 ? 2 : 4;
     static constexpr uint32_t kWarp = NS * kPiece;
     static constexpr uint32_t kRing = kPgWarps * kWarp;
     static constexpr uint32_t kOut = kPgWarps * 8 * NT * (D + 4) * 4;   // warps' outputs (rows padded)
@@ -88,12 +88,39 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
     const int seq = blockIdx.y / p.H, h = blockIdx.y - seq * p.H, split = blockIdx.x;
     const int HQ = p.H * p.G, ppp = p.P / kPgTok;   // pieces per page
+    ptx::grid_launch_next();
 
+    // The warp's pieces are i0 + warp, i0 + warp + 4, ...; lane l looks up the
+    // (32 r + l)-th of them: its page (read ahead of the sequence's length, which
+    // says later whether it counts), its first token's place in the sequence.
+    const int32_t* table = p.pages + (int64_t)seq * p.max_pages;
+    const int32_t* sel = p.selected ? p.selected + ((int64_t)seq * p.H + h) * p.n_select : nullptr;
+    const int i0 = split * p.own_split;
+    const int most = sel ? p.n_select * ppp : (p.max_len + kPgTok - 1) / kPgTok;   // pieces at most
+    auto look_up = [&](int k, int& page, int& token) {
+        const int i = i0 + warp + kPgWarps * k;
+        page = -1;
+        token = -1;
+        if (k >= (p.own_split + kPgWarps - 1) / kPgWarps || i >= most)
+            return;
+        int slot = i / ppp;                      // place in the page table row
+        const int off = (i - slot * ppp) * kPgTok;
+        if (sel)
+            slot = sel[slot];
+        if (slot < 0)
+            return;                              // not selected
+        token = (int)min((int64_t)slot * p.P + off, (int64_t)0x7FFFFFFF);
+        if (slot < p.max_pages)
+            page = table[slot];
+    };
+    int page_c, token_c, page_n, token_n;        // this round's 32 pieces and the next round's
+    look_up(lane, page_c, token_c);
+    look_up(32 + lane, page_n, token_n);
     const int len = own_len(p, seq);
     if (threadIdx.x == 0 && split == 0 && h == 0 && p.max_len > 0 && (p.lens[seq] < 0 || p.lens[seq] > p.max_len))
         raise_err(p.err, KAMERA_DEVERR_LEN);
     const int n_pieces = p.selected ? p.n_select * ppp : (len + kPgTok - 1) / kPgTok;
-    const int i0 = split * p.own_split, i1 = min(n_pieces, i0 + p.own_split);
+    const int i1 = min(n_pieces, i0 + p.own_split);
     if (i0 >= i1 && (p.slots > 1 || split > 0))
         return;   // the merge knows that this slot is empty
     if (threadIdx.x < kPgWarps * NS)
@@ -134,43 +161,30 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     const float sl2 = p.scale * kLog2e;
     const uint32_t ring = ptx::smem_addr(base) + warp * Y::kWarp;
     const uint32_t bar = ptx::smem_addr(full + warp * NS);
-    const int32_t* table = p.pages + (int64_t)seq * p.max_pages;
-    const int32_t* sel = p.selected ? p.selected + ((int64_t)seq * p.H + h) * p.n_select : nullptr;
-
-    // The warp's pieces are i0 + warp, i0 + warp + 4, ...; lane l looks up the
-    // (32 r + l)-th of them: its first pool row and its tokens (0: skipped).
     const int count = i1 > i0 + warp ? (i1 - i0 - warp + kPgWarps - 1) / kPgWarps : 0;
-    auto look_up = [&](int k, int& row, int& tok) {
+    // The pool row and the tokens (0: left out) of a piece that was looked up.
+    auto settle = [&](int k, int page, int token, int& row, int& tok) {
         row = 0;
         tok = 0;
-        if (k >= count)
+        if (k >= count || token < 0)
             return;
-        const int i = i0 + warp + kPgWarps * k;
-        int slot = i / ppp;                      // place in the page table row
-        const int off = (i - slot * ppp) * kPgTok;
-        if (sel) {
-            slot = sel[slot];
-            if (slot < 0)
-                return;
-            if (slot > (len - 1) / p.P || len == 0) {
-                raise_err(p.err, KAMERA_DEVERR_SLOT);
-                return;
-            }
+        if (sel && token >= (len + p.P - 1) / p.P * (int64_t)p.P) {   // past the sequence's last page
+            raise_err(p.err, KAMERA_DEVERR_SLOT);
+            return;
         }
-        const int left = len - slot * p.P - off;
-        if (left <= 0)
+        if (token >= len)
             return;
-        const int page = table[slot];
         if (page < 0 || page >= p.num_pages) {
             raise_err(p.err, KAMERA_DEVERR_SLOT);
             return;
         }
-        row = page * p.P + off;                  // < num_slots < 2^31
-        tok = min(left, kPgTok);
+        row = page * p.P + token % p.P;          // < num_slots < 2^31
+        tok = min(len - token, kPgTok);
     };
-    int row_c, tok_c, row_n, tok_n;              // this round's 32 pieces and the next round's
-    look_up(lane, row_c, tok_c);
-    look_up(32 + lane, row_n, tok_n);
+    int row_c, tok_c, row_n, tok_n;
+    settle(lane, page_c, token_c, row_c, tok_c);
+    settle(32 + lane, page_n, token_n, row_n, tok_n);
+    look_up(64 + lane, page_n, token_n);         // two rounds ahead
     int base_k = 0;                              // piece of lane 0 of row_c
     auto piece = [&](int k, int& row, int& tok) {   // k in [base_k, base_k + 64)
         const int at = k - base_k;
@@ -221,7 +235,8 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
             base_k += 32;
             row_c = row_n;
             tok_c = tok_n;
-            look_up(base_k + 32 + lane, row_n, tok_n);
+            settle(base_k + 32 + lane, page_n, token_n, row_n, tok_n);
+            look_up(base_k + 64 + lane, page_n, token_n);
         }
         load(k + NS - 1);
         mark(k + NS - 1);
@@ -394,49 +409,45 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
 }
 
 // ----------------------------------------------------------------- merge --
-// One warp per row: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the
-// row's partial states, in slot order.  The row's sequence and lengths say which
-// slots were written.
+// One CTA per row: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the
+// row's partial states.  The row's sequence and lengths say which slots were
+// written.  All latency: every warp works out the weights of 32 states at a
+// time in its lanes, then takes every fourth state's output, its loads
+// independent of one another; the four warps' sums join in warp order.
+constexpr int kMergeWarps = 4;
+
 template <int D>
-__global__ void __launch_bounds__(128) merge_kernel(const PagedParams p)
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedParams p)
 {
     constexpr int V = D / 32;   // floats of a lane
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    __shared__ float part[kMergeWarps][D];
+    __shared__ float sum;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x;
     const int HQ = p.H * p.G;
-    if (row >= (int64_t)p.n_seqs * HQ)
-        return;
     const int s = (int)(row / HQ);
-    int n_prefix = 0, n_own = 0;
-    if (p.n_groups > 0) {
-        int lo = 0, hi = p.n_groups - 1;   // the last group that starts at or before s
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.group_start[mid] <= s)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        int s0, s1, len;
-        if (group_range(p, lo, s0, s1, len) && s >= s0 && s < s1) {
-            const int tiles = (len - 1) / 128 + (len > 0);
-            n_prefix = (tiles + p.prefix_split - 1) / p.prefix_split * (p.two_tile ? 1 : 2);
-        } else if (lane == 0 && row % HQ == 0) {
-            raise_err(p.err, KAMERA_DEVERR_DESCRIPTOR);   // no group holds this sequence
-        }
-    }
-    if (p.own_slots > 0) {
-        const int len = own_len(p, s);
-        const int pieces = p.selected ? p.n_select * (p.P / kPgTok) : (len + kPgTok - 1) / kPgTok;
-        n_own = (pieces + p.own_split - 1) / p.own_split;
-    }
-    const int n = n_prefix + n_own;
     const float2* ml = p.ml + row * p.slots;
-    const float* o = p.o + row * p.slots * D;
-    // every lane's share of the slots' maxima
+    const float* o = p.o + row * p.slots * D + V * lane;
+    // what the call was given, while the kernels before may still run
+    const int own = p.own_slots > 0 ? own_len(p, s) : 0;
+    int tiles = -1;   // of the prefix of the (last) group that holds the sequence; -1: none
+    for (int g0 = 0; g0 < p.n_groups; g0 += 32) {
+        int s0, s1, len;
+        const bool mine = g0 + lane < p.n_groups && group_range(p, g0 + lane, s0, s1, len) && s >= s0 && s < s1;
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine);
+        if (who)
+            tiles = __shfl_sync(0xFFFFFFFFu, len > 0 ? (len - 1) / 128 + 1 : 0, 31 - __clz((int)who));
+    }
+    if (p.n_groups > 0 && tiles < 0 && threadIdx.x == 0 && row % HQ == 0)
+        raise_err(p.err, KAMERA_DEVERR_DESCRIPTOR);
+    const int n_prefix = tiles > 0 ? (tiles + p.prefix_split - 1) / p.prefix_split * (p.two_tile ? 1 : 2) : 0;
+    const int pieces = p.selected ? p.n_select * (p.P / kPgTok) : (own + kPgTok - 1) / kPgTok;
+    const int n_own = p.own_slots > 0 ? (pieces + p.own_split - 1) / p.own_split : 0;
+    const int n = n_prefix + n_own, gap = p.prefix_slots - n_prefix;   // unused prefix slots between
+    ptx::grid_wait();
     float m = -INFINITY;
     for (int i = lane; i < n; i += 32)
-        m = fmaxf(m, ml[i < n_prefix ? i : p.prefix_slots + i - n_prefix].x);
+        m = fmaxf(m, ml[i < n_prefix ? i : i + gap].x);
 #pragma unroll
     for (int d = 16; d >= 1; d /= 2)
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
@@ -444,38 +455,61 @@ __global__ void __launch_bounds__(128) merge_kernel(const PagedParams p)
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const int at = i < n_prefix ? i : p.prefix_slots + i - n_prefix;
-        const float2 x = ml[at];
-        if (x.y == 0.f)
-            continue;   // no weight: its output was not written or is zero
-        const float f = ex2(x.x - m);
-        l = fmaf(x.y, f, l);
-        const float* src = o + (int64_t)at * D + V * lane;
-        if constexpr (V == 4) {
-            const float4 w = *reinterpret_cast<const float4*>(src);
-            acc[0] = fmaf(w.x, f, acc[0]);
-            acc[1] = fmaf(w.y, f, acc[1]);
-            acc[2] = fmaf(w.z, f, acc[2]);
-            acc[3] = fmaf(w.w, f, acc[3]);
-        } else {
-            const float2 w = *reinterpret_cast<const float2*>(src);
-            acc[0] = fmaf(w.x, f, acc[0]);
-            acc[1] = fmaf(w.y, f, acc[1]);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        float f = 0.f;   // a state without weight adds nothing: its output was not written or is zero
+        if (i < n) {
+            const float2 x = ml[i < n_prefix ? i : i + gap];
+            if (x.y != 0.f) {
+                f = ex2(x.x - m);
+                if (warp == 0)
+                    l = fmaf(x.y, f, l);
+            }
+        }
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, f != 0.f);
+#pragma unroll
+        for (int k = 0; k < 32 / kMergeWarps; ++k) {
+            const int j = kMergeWarps * k + warp;
+            const float w = __shfl_sync(0xFFFFFFFFu, f, j);
+            if ((live >> j) & 1u) {
+                const int at = i0 + j < n_prefix ? i0 + j : i0 + j + gap;
+                if constexpr (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(o + (int64_t)at * D);
+                    acc[0] = fmaf(x.x, w, acc[0]);
+                    acc[1] = fmaf(x.y, w, acc[1]);
+                    acc[2] = fmaf(x.z, w, acc[2]);
+                    acc[3] = fmaf(x.w, w, acc[3]);
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(o + (int64_t)at * D);
+                    acc[0] = fmaf(x.x, w, acc[0]);
+                    acc[1] = fmaf(x.y, w, acc[1]);
+                }
+            }
         }
     }
-    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    __nv_bfloat16* dst = p.out + row * D + V * lane;
-    if constexpr (V == 4) {
-        uint2 w;
-        w.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        w.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-        *reinterpret_cast<uint2*>(dst) = w;
-    } else {
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (warp == 0) {
+#pragma unroll
+        for (int d = 16; d >= 1; d /= 2)
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        if (lane == 0)
+            sum = l;
     }
-    if (lane == 0 && p.lse)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        part[warp][V * lane + v] = acc[v];
+    __syncthreads();
+    l = sum;
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    for (int i = 2 * threadIdx.x; i < D; i += 64 * kMergeWarps) {
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+            x += part[w][i];
+            y += part[w][i + 1];
+        }
+        *reinterpret_cast<uint32_t*>(p.out + row * D + i) = pack_bf16x2(x * inv, y * inv);
+    }
+    if (threadIdx.x == 0 && p.lse)
         p.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
 }
 
@@ -689,6 +723,8 @@ int attend(PagedParams& p, const KameraPagedKV* kv, const KameraPagedQuery* q, c
     p.lse = q->lse;
     p.pages = own->pages;
     p.lens = own->lens;
+    if (p.own_slots == 0)
+        p.n_select = 0;   // nothing to select from
     p.selected = p.n_select > 0 ? selected : nullptr;
     if (p.n_groups > 0) {
         p.group_start = pre->group_start;
@@ -706,19 +742,11 @@ int attend(PagedParams& p, const KameraPagedKV* kv, const KameraPagedQuery* q, c
     const int64_t map_rows = kv->num_slots > 0 ? kv->num_slots : 1;
     PagedLaunch L;
     std::memset(&L, 0, sizeof(L));
-    if (p.n_groups > 0) {
-        const int r = box_rows(p.P, 128);
-        L.p = p;
-        L.v = static_cast<const __nv_bfloat16*>(kv->v);
-        L.slot_stride = kv->slot_stride;
-        L.box_rows = r;
-        if (!make_rows_map(&L.map_k, kv->k, map_rows, W, kv->slot_stride, 64, r) ||
-            !make_rows_map(&L.map_v, kv->v, map_rows, W, kv->slot_stride, 64, r) ||
-            launch_prefix(L, stream) != cudaSuccess)
-            return KAMERA_ERR_CUDA;
-    }
-    // without any token to read the one CTA of a unit writes the empty output
-    if (p.own_slots > 0 || p.slots == 0) {
+    // The own pages' kernel first; the prefix kernel needs nothing of it and starts
+    // on the SMs that it leaves free; the merge's CTAs read the call's inputs and
+    // wait for both.
+    const bool own_runs = p.own_slots > 0 || p.slots == 0;
+    if (own_runs) {   // without any token to read the one CTA of a unit writes the empty output
         if (p.slots == 0)
             p.slots = 1;
         L.p = p;
@@ -733,13 +761,23 @@ int attend(PagedParams& p, const KameraPagedKV* kv, const KameraPagedQuery* q, c
         if (e != cudaSuccess)
             return KAMERA_ERR_CUDA;
     }
+    if (p.n_groups > 0) {
+        const int r = box_rows(p.P, 128);
+        L.p = p;
+        L.v = static_cast<const __nv_bfloat16*>(kv->v);
+        L.slot_stride = kv->slot_stride;
+        L.box_rows = r;
+        const int64_t groups = std::max<int64_t>(map_rows, 8);   // a pool without a whole page has none to read
+        if (!make_groups_map(&L.map_k, kv->k, groups, W, kv->slot_stride, p.d / 64, r / 8) ||
+            !make_groups_map(&L.map_v, kv->v, groups, W, kv->slot_stride, p.d / 64, r / 8) ||
+            launch_prefix(L, own_runs, stream) != cudaSuccess)
+            return KAMERA_ERR_CUDA;
+    }
     if (need > 0) {
-        const unsigned ctas = (unsigned)((rows + 3) / 4);
-        if (p.d == 128)
-            merge_kernel<128><<<ctas, 128, 0, stream>>>(p);
-        else
-            merge_kernel<64><<<ctas, 128, 0, stream>>>(p);
-        if (cudaGetLastError() != cudaSuccess)
+        const cudaError_t e =
+            p.d == 128 ? launch_after(merge_kernel<128>, dim3((unsigned)rows), 32 * kMergeWarps, 0, stream, true, p)
+                       : launch_after(merge_kernel<64>, dim3((unsigned)rows), 32 * kMergeWarps, 0, stream, true, p);
+        if (e != cudaSuccess)
             return KAMERA_ERR_CUDA;
     }
     return KAMERA_OK;

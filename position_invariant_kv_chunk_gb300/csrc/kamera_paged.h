@@ -53,7 +53,8 @@ struct PagedParams {
 
 struct PagedLaunch {
     PagedParams p;
-    CUtensorMap map_k, map_v;       // [num_slots][H * d], boxes of 64 columns x box_rows
+    CUtensorMap map_k, map_v;       // prefix: groups of eight rows, boxes of box_rows rows of a head; own pages:
+                                    // rows, boxes of 64 columns x 16 rows
     const __nv_bfloat16* v;         // the value rows themselves, slot_stride elements apart
     int64_t slot_stride;
     int32_t box_rows;
@@ -79,6 +80,6 @@ __device__ __forceinline__ bool group_range(const PagedParams& p, int g, int& s0
     return s0 >= 0 && s1 >= s0 && s1 <= p.n_seqs && s1 - s0 <= p.max_group;
 }
 
-cudaError_t launch_prefix(const PagedLaunch& L, cudaStream_t stream);
+cudaError_t launch_prefix(const PagedLaunch& L, bool dependent, cudaStream_t stream);
 
 }  // namespace kamera

@@ -27,18 +27,20 @@
 //   warps 0-3, 4-7  softmax of side A, B: thread = row = TMEM lane; running
 //                   maximum with lazy rescaling (only when it grows by more than
 //                   2^8), at the end the partial state into the workspace
-//   warp 8          producer: key and value tiles as 128B-swizzled TMA boxes of
-//                   as many rows as a page holds in one piece, one box a lane,
-//                   into a ring of five buffers (a tile of keys or of values
-//                   each).  A value tile that the prefix ends in, or with a page
-//                   outside the pool, comes by async copies, zero where no token
-//                   is: a zero weight times what lies there must add nothing.
-//   warp 9          MMA: one lane; the warp owns TMEM
+//   warps 8, 9      producers of keys and of values: 128B-swizzled TMA boxes of
+//                   whole rows, as many as a page holds in one piece, one box a
+//                   lane, into a ring of five buffers (a tile of keys or of
+//                   values each).  A value tile that the prefix ends in, or with
+//                   a page outside the pool, comes by async copies, zero where no
+//                   token is: a zero weight times what lies there must add nothing.
+//   warp 10         MMA; the warp owns TMEM (warp 11 idles: registers are moved
+//                   between whole warpgroups)
 // Every wait is bounded in time: on expiry KAMERA_DEVERR_TIMEOUT is raised, the
-// roles leave their loops, the producer drains the copies it started and the
+// roles leave their loops, the producers drain the copies they started and the
 // MMA lane what it issued, and TMEM is freed.
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "kamera_common.cuh"
 #include "kamera_internal.h"
@@ -55,17 +57,22 @@ using namespace tc;
 
 constexpr int kPxRows = 128;           // rows of a side = MMA M = TMEM lanes
 constexpr int kPxTok = 128;            // tokens of a tile = MMA N of the scores
-constexpr int kPxThreads = 320;
-constexpr int kPxProd = 8, kPxMma = 9;
+constexpr int kPxThreads = 384;
+constexpr int kPxProdK = 8, kPxProdV = 9, kPxMma = 10;
 constexpr int kPxBuf = 5;              // ring buffers
 constexpr int kPxMasks = 8;            // tiles whose masks are kept (the ring holds at most three)
 constexpr float kPxLazy = 8.0f;        // log2 growth of the running maximum that forces a rescale
-constexpr uint32_t kAtom = 16384;      // 128 rows x 128 bytes: 64 columns of a tile
+constexpr uint32_t kAtom = 1024;       // 8 rows x 128 bytes, 128B-swizzled
 
 template <int D>
 struct PxLayout {
     static constexpr int NB = D / 64;
-    static constexpr uint32_t kTile = NB * kAtom;
+    // A tile (of Q, K or V): [16 groups of 8 rows][NB blocks of 64 columns][8][128 bytes]
+    static constexpr uint32_t kGroup = NB * kAtom;
+    static constexpr uint32_t kTile = 16 * kGroup;
+    // descriptor high word: groups kGroup apart, version 1, 128-byte swizzle
+    static constexpr uint32_t kHi = (kGroup >> 4) | (1u << 14) | (2u << 29);
+    static constexpr uint32_t kOutRow = D * 4 + 16;           // a staged output row (padded)
     static constexpr uint32_t kQ = 0;                         // [2 sides][NB atoms]
     static constexpr uint32_t kRing = 2 * kTile;
     static constexpr uint32_t kBar = kRing + kPxBuf * kTile;
@@ -75,11 +82,18 @@ struct PxLayout {
     static constexpr uint32_t kTmCols = 512;
     static_assert(kTmO + 2 * D <= kTmCols, "TMEM columns");
     static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(2 * kPxRows * kOutRow <= kRing + kPxBuf * kTile, "staged outputs");
+    // 16-byte piece c (of D / 8) of row r of a tile
+    static __device__ __forceinline__ uint32_t at(int r, int c)
+    {
+        return (uint32_t)(r >> 3) * kGroup + (uint32_t)(c >> 3) * kAtom + sw128(r & 7, c & 7);
+    }
 };
 
 struct PxBars {
     uint64_t full[kPxBuf], empty[kPxBuf];
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t q_full;           // the query rows are in shared memory
+    uint64_t s_full[2], p_full[2][2], pv_done[2];   // p_full: tokens 0-63, 64-127 of the tile
     uint64_t drained;
     uint32_t mask[kPxMasks];   // tile t (mod kPxMasks): 16-token pieces with tokens that count
     uint32_t tmem;
@@ -93,8 +107,10 @@ struct PxWork {
     int s0, rows;            // the group's first sequence, its rows (sequences x G)
     int len;                 // prefix tokens
     int t0, tiles;           // the split's tiles
-    int n_side[2];           // tiles of side A, B (0: the side is idle)
-    int row0[2];             // first row of side A, B
+    int tiles_a, tiles_b;    // tiles of side A, B (0: the side is idle)
+    int row_a, row_b;        // first row of side A, B
+    __device__ __forceinline__ int n_side(int a) const { return a ? tiles_b : tiles_a; }
+    __device__ __forceinline__ int row0(int a) const { return a ? row_b : row_a; }
 };
 
 __device__ __forceinline__ void px_work(const PagedParams& p, PxWork& w)
@@ -112,15 +128,14 @@ __device__ __forceinline__ void px_work(const PagedParams& p, PxWork& w)
     const int all = w.len > 0 ? (w.len - 1) / kPxTok + 1 : 0;
     w.t0 = w.split * p.prefix_split;
     w.tiles = max(0, min(p.prefix_split, all - w.t0));
+    w.row_a = p.two_tile ? w.blk * 2 * kPxRows : 0;
+    w.row_b = p.two_tile ? w.row_a + kPxRows : 0;
     if (p.two_tile) {
-        w.row0[0] = w.blk * 2 * kPxRows;
-        w.row0[1] = w.row0[0] + kPxRows;
-        w.n_side[0] = w.row0[0] < w.rows ? w.tiles : 0;
-        w.n_side[1] = w.row0[1] < w.rows ? w.tiles : 0;
+        w.tiles_a = w.row_a < w.rows ? w.tiles : 0;
+        w.tiles_b = w.row_b < w.rows ? w.tiles : 0;
     } else {
-        w.row0[0] = w.row0[1] = 0;
-        w.n_side[0] = w.rows > 0 ? (w.tiles + 1) / 2 : 0;
-        w.n_side[1] = w.rows > 0 ? w.tiles / 2 : 0;
+        w.tiles_a = w.rows > 0 ? (w.tiles + 1) / 2 : 0;
+        w.tiles_b = w.rows > 0 ? w.tiles / 2 : 0;
     }
 }
 
@@ -133,102 +148,107 @@ __device__ __forceinline__ uint32_t px_v_at(bool two, int t, int tiles)
     return two ? 2u * t + 1 : (t == tiles - 1 ? 2u * tiles - 1 : 2u * t + 2);
 }
 
-// One tile of keys (V = false) or values into buffer `dst`.
-template <int D>
-__device__ void px_load(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_t dst, uint32_t full, int t, bool values,
-                        int lane)
-{
-    using Y = PxLayout<D>;
-    const PagedParams& p = L.p;
-    const int tok0 = (w.t0 + t) * kPxTok, ntok = min(kPxTok, w.len - tok0);
-    const int32_t* table = p.prefix_pages + (int64_t)w.group * p.max_prefix_pages;
-    // the pieces that hold tokens of pages inside the pool
-    bool good = false;
-    if (lane < kPxTok / 16 && 16 * lane < ntok) {
-        const int page = __ldg(table + (tok0 + 16 * lane) / p.P);
-        good = page >= 0 && page < p.num_pages;
-        if (!good)
-            raise_err(p.err, KAMERA_DEVERR_SLOT);
-    }
-    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
-    const bool plain = ntok == kPxTok && mask == 0xFFu;
-    if (values && !plain) {
-        for (int e = lane; e < kPxTok * 8 * Y::NB; e += 32) {
-            const int r = e / (8 * Y::NB), c = e % (8 * Y::NB);
-            const uint32_t at = dst + (c >> 3) * kAtom + sw128(r, c & 7);
-            if (r < ntok && ((mask >> (r >> 4)) & 1u)) {
-                const int page = __ldg(table + (tok0 + r) / p.P);
-                const int64_t row = (int64_t)page * p.P + (tok0 + r) % p.P;
-                ptx::cp_async16(at, L.v + row * L.slot_stride + (int64_t)w.h * D + 8 * c);
-            } else {
-                ptx::st_shared_zero16(at);
-            }
-        }
-        ptx::cp_async_commit();
-        ptx::cp_async_wait<0>();
-        ptx::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0 && !p.withhold)
-            ptx::mbar_arrive(full);
-        return;
-    }
-    const int R = L.box_rows, boxes = (kPxTok / R) * Y::NB;
-    // lane e's box: rows rp R .. of column block x (a box lies in one page)
-    uint32_t bytes = 0;
-    int row = 0;
-    const int rp = lane / Y::NB, x = lane - rp * Y::NB;
-    if (lane < boxes && rp * R < ntok && ((mask >> (rp * R / 16)) & 1u)) {
-        const int tok = tok0 + rp * R;
-        row = __ldg(table + tok / p.P) * p.P + tok % p.P;
-        bytes = (uint32_t)R * 128u;
-    }
-    const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);
-    if (lane == 0) {
-        if (!values)
-            b.mask[t % kPxMasks] = mask;
-        if (!p.withhold) {
-            if (total > 0)
-                ptx::mbar_arrive_expect_tx(full, total);
-            else
-                ptx::mbar_arrive(full);
-        }
-    }
-    __syncwarp();
-    if (bytes && !p.withhold)
-        ptx::tma_load_2d(dst + x * kAtom + rp * R * 128, values ? &L.map_v : &L.map_k, w.h * D + 64 * x, row, full);
-}
-
-template <int D>
+// The producer of the keys (VALUES false) or the values: every tile of the split,
+// in order, into its places in the ring.  A page lies in one box of `box_rows`
+// rows or in several; lane l looks up and issues box l.  The next tile's pages
+// are looked up before the wait for a free buffer, and the two producers work
+// side by side: a fill is all latency (table, barrier, issue), and one warp
+// doing both had the tensor pipe wait for it.
+template <int D, bool VALUES>
 __device__ void px_producer(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_t ring, int lane)
 {
     using Y = PxLayout<D>;
     const PagedParams& p = L.p;
     const bool two = p.two_tile != 0;
-    const int n = 2 * w.tiles;
-    int kt = 0, vt = 0;   // next tile of keys, of values
-    int i = 0;
-    for (; i < n; ++i) {
-        const int buf = i % kPxBuf;
-        if (i >= kPxBuf) {
+    const int32_t* table = p.prefix_pages + (int64_t)w.group * p.max_prefix_pages;
+    const int R = L.box_rows, boxes = kPxTok / R;
+    auto page_at = [&](int t, int off) {   // the page of the tile's token `off`; -1 past the prefix
+        const int tok = (w.t0 + t) * kPxTok + off;
+        return t < w.tiles && tok < w.len ? __ldg(table + tok / p.P) : -1;
+    };
+    // lanes 0..7: the pages of the tile's eight 16-token pieces
+    int next = lane < kPxTok / 16 ? page_at(0, 16 * lane) : -1;
+    int t = 0;
+    bool ok = true;
+    for (; t < w.tiles; ++t) {
+        const int tok0 = (w.t0 + t) * kPxTok, ntok = min(kPxTok, w.len - tok0), page = next;
+        next = lane < kPxTok / 16 ? page_at(t + 1, 16 * lane) : -1;
+        const bool in = lane < kPxTok / 16 && 16 * lane < ntok, good = in && page >= 0 && page < p.num_pages;
+        if (in && !good)
+            raise_err(p.err, KAMERA_DEVERR_SLOT);
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
+        const uint32_t at = VALUES ? px_v_at(two, t, w.tiles) : px_k_at(two, t), buf = at % kPxBuf, lap = at / kPxBuf;
+        const uint32_t dst = ring + buf * Y::kTile, full = ptx::smem_addr(&b.full[buf]);
+        if (lap > 0) {
             bool got = true;
             if (lane == 0)
-                got = wmma16::tile_wait(ptx::smem_addr(&b.empty[buf]), ((uint32_t)(i / kPxBuf) & 1u) ^ 1u, &b.abort,
-                                        p.err, p.wait_ns);
-            if (!__shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0))
+                got = wmma16::tile_wait(ptx::smem_addr(&b.empty[buf]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns);
+            ok = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+            if (!ok)
                 break;
         }
-        const bool values = !(kt < w.tiles && px_k_at(two, kt) == (uint32_t)i);
-        px_load<D>(L, w, b, ring + buf * Y::kTile, ptx::smem_addr(&b.full[buf]), values ? vt++ : kt++, values, lane);
+        if (VALUES && (ntok < kPxTok || mask != 0xFFu)) {
+            // the prefix ends in this tile, or a page is missing: zero where no token is
+            for (int e = lane; e < kPxTok * 8 * Y::NB; e += 32) {
+                const int r = e / (8 * Y::NB), c = e % (8 * Y::NB);
+                if (r < ntok && ((mask >> (r >> 4)) & 1u)) {
+                    const int64_t row = (int64_t)__ldg(table + (tok0 + r) / p.P) * p.P + (tok0 + r) % p.P;
+                    ptx::cp_async16(dst + Y::at(r, c), L.v + row * L.slot_stride + (int64_t)w.h * D + 8 * c);
+                } else {
+                    ptx::st_shared_zero16(dst + Y::at(r, c));
+                }
+            }
+            ptx::cp_async_commit();
+            ptx::cp_async_wait<0>();
+            ptx::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0 && !p.withhold)
+                ptx::mbar_arrive(full);
+            continue;
+        }
+        // box l covers rows l R .. l R + R - 1, whose page piece l R / 16 looked up
+        const int off = lane * R, from = __shfl_sync(0xFFFFFFFFu, page, (off / 16) & 31);
+        const bool mine = lane < boxes && off < ntok && ((mask >> (off / 16)) & 1u);
+        const uint32_t total = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * (uint32_t)(R / 8) * Y::kGroup;
+        if (lane == 0) {
+            if (!VALUES)
+                b.mask[t % kPxMasks] = mask;
+            if (!p.withhold) {
+                if (total > 0)
+                    ptx::mbar_arrive_expect_tx(full, total);
+                else
+                    ptx::mbar_arrive(full);
+            }
+        }
+        __syncwarp();
+        if (mine && !p.withhold)
+            ptx::tma_load_4d(dst + (uint32_t)(off / 8) * Y::kGroup, VALUES ? &L.map_v : &L.map_k, 0, 0, w.h * Y::NB,
+                             (from * p.P + (tok0 + off) % p.P) >> 3, full);
     }
-    // the copies this warp started land before the CTA leaves
-    if (lane == 0 && !p.withhold)
-        for (int k = i > kPxBuf ? i - kPxBuf : 0; k < i; ++k)
-            pf_drain_wait(ptx::smem_addr(&b.full[k % kPxBuf]), (uint32_t)(k / kPxBuf) & 1u, p.wait_ns);
+    // Without a timeout the MMA lane has waited for every fill.  After one, the
+    // copies this warp started land before the CTA leaves.
+    if (lane == 0 && !p.withhold && *static_cast<volatile int32_t*>(&b.abort))
+        for (int k = max(0, t - kPxBuf); k < t; ++k) {
+            const uint32_t at = VALUES ? px_v_at(two, k, w.tiles) : px_k_at(two, k);
+            pf_drain_wait(ptx::smem_addr(&b.full[at % kPxBuf]), (at / kPxBuf) & 1u, p.wait_ns);
+        }
     __syncwarp();
 }
 
+// One lane of the (converged) warp: the compiler knows that a branch on it holds
+// a single thread, and hands the MMA its operands without a loop over the lanes
+// that might differ (which cost 35 of 100 cycles an MMA in a branch on lane 0).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+// The MMA lane.  TMEM addresses are offsets: the CTA holds all 512 columns, so
+// its allocation starts at address 0.
 template <int D>
-__device__ void px_mma(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_t sbase, uint32_t tm)
+__device__ void px_mma(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_t sbase)
 {
     using Y = PxLayout<D>;
     const PagedParams& p = L.p;
@@ -241,70 +261,112 @@ __device__ void px_mma(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_
         return wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
     // scores of side a's tile n; the tile's keys are free after its last side
-    auto scores = [&](int a, int n) -> bool {
+    auto scores = [&](auto side, int n) -> bool {
+        constexpr int a = decltype(side)::value;
         const int t = two ? n : 2 * n + a;
         const uint32_t at = px_k_at(two, t), buf = at % kPxBuf;
         if (!wait(&b.full[buf], at / kPxBuf))
             return false;
         ptx::tc_fence_after();
-        const uint32_t dS = tm + Y::kTmS + a * kPxTok;
+        constexpr uint32_t dS = Y::kTmS + a * kPxTok;
         const uint32_t aq = q_lo + (two ? a : 0) * (Y::kTile >> 4), bk = (r_lo + buf * (Y::kTile >> 4)) | (1u << 16);
-        mma_ss<false>(dS, aq, bk, idS);
+        mma_ss<false, Y::kHi>(dS, aq, bk, idS);
 #pragma unroll
         for (int ks = 1; ks < D / 16; ++ks)
-            mma_ss<true>(dS, aq + (ks >> 2) * (kAtom >> 4) + 2 * (ks & 3), bk + (ks >> 2) * (kAtom >> 4) + 2 * (ks & 3),
-                         idS);
+            mma_ss<true, Y::kHi>(dS, aq + (ks >> 2) * (kAtom >> 4) + 2 * (ks & 3),
+                                    bk + (ks >> 2) * (kAtom >> 4) + 2 * (ks & 3), idS);
         ptx::umma_commit(ptx::smem_addr(&b.s_full[a]));
-        if (!two || a == 1 || w.n_side[1] == 0)
+        if (!two || a == 1 || w.tiles_b == 0)
             ptx::umma_commit(ptx::smem_addr(&b.empty[buf]));
         return true;
     };
-    auto weigh = [&](int a, int n) -> bool {
+    auto weigh = [&](auto side, int n) -> bool {
+        constexpr int a = decltype(side)::value;
         const int t = two ? n : 2 * n + a;
         const uint32_t at = px_v_at(two, t, w.tiles), buf = at % kPxBuf;
-        if (!wait(&b.p_full[a], n) || !wait(&b.full[buf], at / kPxBuf))
+        if (!wait(&b.full[buf], at / kPxBuf))
             return false;
-        ptx::tc_fence_after();
-        const uint32_t dO = tm + Y::kTmO + a * D, aP = tm + Y::kTmS + a * kPxTok;
+        constexpr uint32_t dO = Y::kTmO + a * D, aP = Y::kTmS + a * kPxTok;
         const uint32_t bv = (r_lo + buf * (Y::kTile >> 4)) | ((kAtom >> 4) << 16);
-        if (n == 0)
-            mma_ts<false>(dO, aP, bv, idV);
-        else
-            mma_ts<true>(dO, aP, bv, idV);
 #pragma unroll
-        for (int ks = 1; ks < kPxTok / 16; ++ks)
-            mma_ts<true>(dO, aP + 8 * ks, bv + (2048 >> 4) * ks, idV);
+        for (int half = 0; half < 2; ++half) {   // the first 64 tokens while the others' weights are computed
+            if (!wait(&b.p_full[a][half], n))
+                return false;
+            ptx::tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < kPxTok / 16; ++ks)
-            mma_ts<true>(dO, aP + kPxTok / 2 + 8 * ks, bv + (2048 >> 4) * ks, idV);
+            for (int k = 0; k < 4; ++k) {
+                const int ks = 4 * half + k;
+                const uint32_t v = bv + (2 * Y::kGroup >> 4) * ks;
+                if (ks == 0 && n == 0)
+                    mma_ts<false, Y::kHi>(dO, aP, v, idV);
+                else
+                    mma_ts<true, Y::kHi>(dO, aP + 8 * ks, v, idV);
+                mma_ts<true, Y::kHi>(dO, aP + kPxTok / 2 + 8 * ks, v, idV);
+            }
+        }
         ptx::umma_commit(ptx::smem_addr(&b.pv_done[a]));
-        if (!two || a == 1 || w.n_side[1] == 0)
+        if (!two || a == 1 || w.tiles_b == 0)
             ptx::umma_commit(ptx::smem_addr(&b.empty[buf]));
         return true;
     };
-    bool ok = true;
-    for (int a = 0; a < 2 && ok; ++a)
-        if (w.n_side[a] > 0)
-            ok = scores(a, 0);
-    for (int n = 0; n < w.n_side[0] && ok; ++n)
-        for (int a = 0; a < 2 && ok; ++a)
-            if (n < w.n_side[a]) {
-                ok = weigh(a, n);
-                if (ok && n + 1 < w.n_side[a])
-                    ok = scores(a, n + 1);
-            }
+    constexpr auto A = std::integral_constant<int, 0>{};
+    constexpr auto B = std::integral_constant<int, 1>{};
+    bool ok = wait(&b.q_full, 0) && scores(A, 0) && (w.tiles_b == 0 || scores(B, 0));
+    for (int n = 0; n < w.tiles_a && ok; ++n) {
+        ok = weigh(A, n) && (n + 1 >= w.tiles_a || scores(A, n + 1));
+        if (ok && n < w.tiles_b)
+            ok = weigh(B, n) && (n + 1 >= w.tiles_b || scores(B, n + 1));
+    }
     // every MMA issued here completes before TMEM is freed
     ptx::umma_commit(ptx::smem_addr(&b.drained));
     pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
 }
 
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return d;
+}
+__device__ __forceinline__ float min3(float a, uint32_t b, uint32_t c)
+{
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return d;
+}
+
+// The query rows of side a into shared memory (K-major, zero past the group's
+// rows) by the side's 128 threads, a row's pieces on neighbouring lanes; all of
+// a thread's loads are in flight before the first store.
+template <int D>
+__device__ __forceinline__ void px_stage_q(const PagedParams& p, const PxWork& w, PxBars& b, uint32_t sbase, int a, int r)
+{
+    using Y = PxLayout<D>;
+    constexpr int PC = D / 8, RS = kPxRows / PC, N = kPxRows / RS;   // pieces of a row, rows a step, steps
+    uint4 x[N];
+    const int c = r % PC;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int row = w.row0(a) + i * RS + r / PC;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < w.rows)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(
+                p.q + (((int64_t)(w.s0 + row / p.G) * p.H + w.h) * p.G + row % p.G) * D + 8 * c));
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        ptx::sts128(sbase + Y::kQ + a * Y::kTile + Y::at(i * RS + r / PC, c), x[i].x, x[i].y, x[i].z, x[i].w);
+    ptx::fence_proxy_async();
+    ptx::mbar_arrive(ptx::smem_addr(&b.q_full));
+}
+
 // Side a's softmax, thread r = row r of the side = TMEM lane r.
 template <int D>
-__device__ void px_softmax(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_t tm, int a, int r)
+__device__ void px_softmax(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_t sbase, uint32_t tm, int a, int r)
 {
     using Y = PxLayout<D>;
     const PagedParams& p = L.p;
-    const int nt = w.n_side[a], row = w.row0[a] + r;
+    const int nt = w.n_side(a), row = w.row0(a) + r;
     const bool valid = row < w.rows;
     const bool idle = !__any_sync(0xFFFFFFFFu, valid);   // no row of this warp counts
     const uint32_t lanes = tm + ((uint32_t)(r & ~31) << 16);
@@ -343,26 +405,33 @@ __device__ void px_softmax(const PagedLaunch& L, const PxWork& w, PxBars& b, uin
                             s[c][j] = out;
                     }
             }
-            float e0 = neg ? INFINITY : -INFINITY, e1 = e0, e2 = e0, e3 = e0;
+            // the row's extreme score: three inputs an instruction, eight chains
+            float e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t* v = &s[k >> 1][16 * (k & 1)];
+                e[k] = neg ? fminf(__uint_as_float(v[0]), __uint_as_float(v[1]))
+                           : fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+            }
             if (neg) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    e0 = fminf(e0, __uint_as_float(s[0][j]));
-                    e1 = fminf(e1, __uint_as_float(s[1][j]));
-                    e2 = fminf(e2, __uint_as_float(s[2][j]));
-                    e3 = fminf(e3, __uint_as_float(s[3][j]));
-                }
-                e0 = fminf(fminf(e0, e1), fminf(e2, e3));
+                for (int j = 2; j < 16; j += 2)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        e[k] = min3(e[k], s[k >> 1][16 * (k & 1) + j], s[k >> 1][16 * (k & 1) + j + 1]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    e0 = fmaxf(e0, __uint_as_float(s[0][j]));
-                    e1 = fmaxf(e1, __uint_as_float(s[1][j]));
-                    e2 = fmaxf(e2, __uint_as_float(s[2][j]));
-                    e3 = fmaxf(e3, __uint_as_float(s[3][j]));
-                }
-                e0 = fmaxf(fmaxf(e0, e1), fmaxf(e2, e3));
+                for (int j = 2; j < 16; j += 2)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        e[k] = max3(e[k], s[k >> 1][16 * (k & 1) + j], s[k >> 1][16 * (k & 1) + j + 1]);
             }
+#pragma unroll
+            for (int d = 4; d >= 1; d /= 2)
+#pragma unroll
+                for (int k = 0; k < d; ++k)
+                    e[k] = neg ? fminf(e[k], e[k + d]) : fmaxf(e[k], e[k + d]);
+            const float e0 = e[0];
             const float m_new = fmaxf(m_run, sl2 * e0);
             if (n == 0) {
                 m_run = m_new;   // O is still empty
@@ -391,61 +460,81 @@ __device__ void px_softmax(const PagedLaunch& L, const PxWork& w, PxBars& b, uin
             const uint64_t neg1 = ptx::f2_make(0xBF800000u, 0xBF800000u);
             uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t ph[32], pl[32];
+            for (int c = 0; c < 4; ++c) {   // 32 tokens: 16 columns of hi, 16 of lo
+                uint32_t ph[16], pl[16];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint32_t* src = s[2 * half + (j >> 4)];
-                    const int jj = 2 * (j & 15);
+                for (int j = 0; j < 16; ++j) {
                     uint32_t a0, a1;
                     asm("mov.b64 {%0, %1}, %2;"
                         : "=r"(a0), "=r"(a1)
-                        : "l"(ptx::f2_fma(ptx::f2_make(src[jj], src[jj + 1]), sl2x2, nmx2)));
+                        : "l"(ptx::f2_fma(ptx::f2_make(s[c][2 * j], s[c][2 * j + 1]), sl2x2, nmx2)));
                     const float p0 = pf_ex2(__uint_as_float(a0)), p1 = pf_ex2(__uint_as_float(a1));
                     const uint64_t pp = ptx::f2_make(__float_as_uint(p0), __float_as_uint(p1));
                     sum2[j & 1] = ptx::f2_add(sum2[j & 1], pp);
                     ph[j] = pack_bf16x2(p0, p1);
                     pl[j] = ptx::f2_to_bf16x2(ptx::f2_fma(ptx::f2_from_bf16x2(ph[j]), neg1, pp));
                 }
-                tmem_st32(tS + 32 * half, ph);
-                tmem_st32(tS + kPxTok / 2 + 32 * half, pl);
+                tmem_st16(tS + 16 * c, ph);
+                tmem_st16(tS + kPxTok / 2 + 16 * c, pl);
+                if (c == 1) {
+                    tmem_wait_st();
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(ptx::smem_addr(&b.p_full[a][0]));
+                }
             }
             uint32_t x0, x1;
             asm("mov.b64 {%0, %1}, %2;" : "=r"(x0), "=r"(x1) : "l"(ptx::f2_add(sum2[0], sum2[1])));
             l_run += __uint_as_float(x0) + __uint_as_float(x1);
             tmem_wait_st();
+        } else {
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ptx::smem_addr(&b.p_full[a][0]));
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_addr(&b.p_full[a]));
+        ptx::mbar_arrive(ptx::smem_addr(&b.p_full[a][1]));
     }
-    // ---- the partial state
+    // ---- the partial state: rows through shared memory, so that a warp writes whole
+    // 128-byte lines (Q and the ring are free once both sides are done)
     if (nt > 0 && ok) {
         if (!wmma16::tile_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(nt - 1) & 1u, &b.abort, p.err, p.wait_ns))
             ok = false;
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
     }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
     if (idle)
         return;
-    const int seq = w.s0 + row / p.G;
-    const int64_t slot = ((int64_t)seq * p.H * p.G + w.h * p.G + row % p.G) * p.slots +
-                         (p.two_tile ? w.split : 2 * w.split + a);
-    if (nt > 0 && ok) {
+    const int HQ = p.H * p.G, per_row = p.two_tile ? w.split : 2 * w.split + a;
+    auto slot_of = [&](int rr) {
+        return ((int64_t)(w.s0 + rr / p.G) * HQ + w.h * p.G + rr % p.G) * p.slots + per_row;
+    };
+    if (valid)   // a side without tiles leaves the empty state
+        p.ml[slot_of(row)] = nt > 0 && ok ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
+    if (nt == 0 || !ok)
+        return;
+    const uint32_t mine = sbase + (uint32_t)(a * kPxRows + r) * Y::kOutRow;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * c, o);
-            if (valid) {
-                float* dst = p.o + slot * D + 32 * c;
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * c, o);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(dst + 4 * j) =
-                        make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-            }
+        for (int j = 0; j < 8; ++j)
+            ptx::sts128(mine + 128 * c + 16 * j, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    }
+    __syncwarp();
+    const int lane = r & 31, r0 = r & ~31, n = min(32, w.rows - w.row0(a) - r0);
+    constexpr int LR = D / 4, PR = 32 / LR;   // lanes of a row, rows a warp writes at once
+    const int64_t first = lane < n ? slot_of(w.row0(a) + r0 + lane) : 0;
+#pragma unroll 4
+    for (int i = 0; i < n; i += PR) {
+        const int rr = i + lane / LR;
+        const int64_t slot = __shfl_sync(0xFFFFFFFFu, first, rr & 31);
+        if (rr < n) {
+            uint32_t v[4];
+            ptx::lds128(sbase + (uint32_t)(a * kPxRows + r0 + rr) * Y::kOutRow + 16 * (lane % LR), v);
+            *reinterpret_cast<uint4*>(p.o + slot * D + 4 * (lane % LR)) = make_uint4(v[0], v[1], v[2], v[3]);
         }
     }
-    if (valid)   // a side without tiles leaves the empty state
-        p.ml[slot] = nt > 0 && ok ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
 }
 
 template <int D>
@@ -457,6 +546,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     const uint32_t at = ptx::smem_addr(raw), pad = (1024u - (at & 1023u)) & 1023u, sbase = at + pad;
     PxBars& b = *reinterpret_cast<PxBars*>(raw + pad + Y::kBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::grid_launch_next();
     PxWork w;
     px_work(p, w);
     if (threadIdx.x == 0 && w.h == 0 && w.split == 0 && w.blk == 0) {
@@ -466,8 +556,10 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         if (p.prefix_lens[w.group] != len)
             raise_err(p.err, KAMERA_DEVERR_LEN);
     }
-    if (w.n_side[0] == 0)   // no rows, or no tokens: nothing for either side
+    if (w.tiles_a == 0) {   // no rows, or no tokens: nothing for either side
+        ptx::grid_wait();   // (as below)
         return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPxBuf; ++i) {
             ptx::mbar_init(ptx::smem_addr(&b.full[i]), 1);
@@ -475,14 +567,16 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(ptx::smem_addr(&b.s_full[a]), 1);
-            ptx::mbar_init(ptx::smem_addr(&b.p_full[a]), kPxRows);
+            ptx::mbar_init(ptx::smem_addr(&b.p_full[a][0]), kPxRows);
+            ptx::mbar_init(ptx::smem_addr(&b.p_full[a][1]), kPxRows);
             ptx::mbar_init(ptx::smem_addr(&b.pv_done[a]), 1);
         }
+        ptx::mbar_init(ptx::smem_addr(&b.q_full), (p.two_tile ? 2 : 1) * kPxRows);
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
         ptx::fence_barrier_init();
     }
-    if (warp == kPxProd && lane == 0) {
+    if (warp == kPxProdK && lane == 0) {
         ptx::prefetch_tmap(&L.map_k);
         ptx::prefetch_tmap(&L.map_v);
     }
@@ -490,28 +584,31 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         ptx::tmem_alloc(ptx::smem_addr(&b.tmem), Y::kTmCols);
         ptx::tmem_relinquish();
     }
-    // the query rows, K-major and 128B-swizzled; zero past the group's rows
-    const int sides = p.two_tile ? 2 : 1;
-    for (int e = threadIdx.x; e < sides * kPxRows * (D / 8); e += kPxThreads) {
-        const int c = e % (D / 8), rr = e / (D / 8), a = rr >> 7, r = rr & (kPxRows - 1), row = w.row0[a] + r;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (row < w.rows)
-            x = __ldg(reinterpret_cast<const uint4*>(
-                p.q + (((int64_t)(w.s0 + row / p.G) * p.H + w.h) * p.G + row % p.G) * D + 8 * c));
-        ptx::sts128(sbase + Y::kQ + a * Y::kTile + (c >> 3) * kAtom + sw128(r, c & 7), x.x, x.y, x.z, x.w);
-    }
-    ptx::fence_proxy_async();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tm = b.tmem;
 
-    if (warp < 8)
-        px_softmax<D>(L, w, b, tm, warp >> 2, threadIdx.x & (kPxRows - 1));
-    else if (warp == kPxProd)
-        px_producer<D>(L, w, b, sbase + Y::kRing, lane);
-    else if (lane == 0)
-        px_mma<D>(L, w, b, sbase, tm);
+    // Registers: the softmax warps hold a row of 128 scores, the others next to
+    // nothing (256 x 208 + 128 x 56 of the launch's 384 x 168).
+    if (warp < 8) {
+        ptx::setmaxnreg_inc<208>();
+        const int a = warp >> 2, r = threadIdx.x & (kPxRows - 1);
+        if (p.two_tile || a == 0)
+            px_stage_q<D>(p, w, b, sbase, a, r);
+        px_softmax<D>(L, w, b, sbase, tm, a, r);
+    } else {
+        ptx::setmaxnreg_dec<56>();
+        if (warp == kPxProdK)
+            px_producer<D, false>(L, w, b, sbase + Y::kRing, lane);
+        else if (warp == kPxProdV)
+            px_producer<D, true>(L, w, b, sbase + Y::kRing, lane);
+        else if (warp == kPxMma && elect_one())
+            px_mma<D>(L, w, b, sbase);
+        else if (warp > kPxMma)
+            ptx::grid_wait();   // the own pages' kernel may still run beside this one; the merge that
+                                // follows waits for this grid alone, so this grid ends after that one
+    }
 
     ptx::tc_fence_before();
     __syncthreads();
@@ -522,7 +619,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
 }
 
 template <int D>
-cudaError_t launch_prefix_d(const PagedLaunch& L, cudaStream_t stream)
+cudaError_t launch_prefix_d(const PagedLaunch& L, bool dependent, cudaStream_t stream)
 {
     using Y = PxLayout<D>;
     // set at every launch: the attribute belongs to the current device's context
@@ -531,15 +628,14 @@ cudaError_t launch_prefix_d(const PagedLaunch& L, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     const unsigned ctas = (unsigned)L.p.n_groups * L.p.H * L.p.row_blocks * L.p.prefix_splits;
-    prefix_kernel<D><<<ctas, kPxThreads, Y::kBytes, stream>>>(L);
-    return cudaGetLastError();
+    return launch_after(prefix_kernel<D>, dim3(ctas), kPxThreads, Y::kBytes, stream, dependent, L);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix(const PagedLaunch& L, cudaStream_t stream)
+cudaError_t launch_prefix(const PagedLaunch& L, bool dependent, cudaStream_t stream)
 {
-    return L.p.d == 128 ? launch_prefix_d<128>(L, stream) : launch_prefix_d<64>(L, stream);
+    return L.p.d == 128 ? launch_prefix_d<128>(L, dependent, stream) : launch_prefix_d<64>(L, dependent, stream);
 }
 
 }  // namespace kamera

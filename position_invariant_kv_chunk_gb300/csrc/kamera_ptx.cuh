@@ -146,6 +146,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
         : "memory");
 }
 
+// tiled tensor load (TMA) global -> shared, 4-D coordinates, completion on `bar`
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
 // tiled tensor load (TMA) global -> shared, 2-D coordinates, completion on `bar`
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar)
 {
@@ -173,6 +182,13 @@ __device__ __forceinline__ void stg128(void* p, const uint32_t (&v)[4])
     asm volatile("st.global.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
                  : "memory");
 }
+
+// ------------------------------------- programmatic dependent launch --
+// The stream's next kernel, launched as a programmatic dependent, may start
+// once every CTA of this grid has said so (or ended); it waits for this grid's
+// completion, and sees its writes, with grid_wait.
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------ packed fp32 pairs (f32x2) --
 // Two IEEE fp32 lanes in one 64-bit register; each lane rounds exactly like

@@ -63,6 +63,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t ta, const uint32_t (&r)[32])
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t ta, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(ta),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st4(uint32_t ta, const uint32_t (&r)[4])
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ta), "r"(r[0]), "r"(r[1]),
@@ -94,44 +103,45 @@ __device__ __forceinline__ void pf_drain_wait(uint32_t bar, uint32_t parity, uin
 // rows: the rows of a TMA box are K, the N dimension is contiguous) it is the
 // distance between 64-element atoms along N.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <uint32_t HI = kDescHi>
 __device__ __forceinline__ uint64_t pf_desc(uint32_t lo)
 {
     uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(HI));
     return d;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T (kind::f16: bf16 in, fp32 accumulate), the
 // accumulate flag a compile-time constant.  A's row r sits in TMEM lane r,
 // elements 2c and 2c + 1 in the low and high half of column c.
-template <bool ACC>
+template <bool ACC, uint32_t HI = kDescHi>
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc)
 {
     if constexpr (ACC)
         asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 1, 1;\n\t"
                      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "r"(a_tmem), "l"(pf_desc(b_lo)), "r"(idesc)
+                     "r"(a_tmem), "l"(pf_desc<HI>(b_lo)), "r"(idesc)
                      : "memory");
     else
         asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 1, 1;\n\t"
                      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "r"(a_tmem), "l"(pf_desc(b_lo)), "r"(idesc)
+                     "r"(a_tmem), "l"(pf_desc<HI>(b_lo)), "r"(idesc)
                      : "memory");
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T (kind::f16), accumulate flag constant.
-template <bool ACC>
+template <bool ACC, uint32_t HI = kDescHi>
 __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
 {
     if constexpr (ACC)
         asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 1, 1;\n\t"
                      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "l"(pf_desc(a_lo)), "l"(pf_desc(b_lo)), "r"(idesc)
+                     "l"(pf_desc<HI>(a_lo)), "l"(pf_desc<HI>(b_lo)), "r"(idesc)
                      : "memory");
     else
         asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 1, 1;\n\t"
                      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                     "l"(pf_desc(a_lo)), "l"(pf_desc(b_lo)), "r"(idesc)
+                     "l"(pf_desc<HI>(a_lo)), "l"(pf_desc<HI>(b_lo)), "r"(idesc)
                      : "memory");
 }
 

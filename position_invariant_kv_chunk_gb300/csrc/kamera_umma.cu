@@ -1049,6 +1049,24 @@ bool make_rows_map(void* map, const void* base, int64_t rows, int64_t width, int
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4-D tensor map of the same array as groups of eight rows: (64 columns, row in
+// its group, column block, group), 128-byte swizzle, boxes of `blocks` column
+// blocks of `groups` groups.  A box lands as [group][block][8 rows][128 bytes],
+// one copy for whole rows of several swizzle atoms.
+bool make_groups_map(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int blocks, int groups)
+{
+    auto fn = encode_fn();
+    if (!fn || rows < 8 || width < 64 || width % 64)
+        return false;
+    cuuint64_t dims[4] = {64u, 8u, (cuuint64_t)(width / 64), (cuuint64_t)(rows / 8)};
+    cuuint64_t strides[3] = {(cuuint64_t)row_stride * 2u, 128u, (cuuint64_t)row_stride * 16u};
+    cuuint32_t box[4] = {64u, 8u, (cuuint32_t)blocks, (cuuint32_t)groups};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_umma(const RowsParams& rp, int family, const KameraChunk* h_chunks, cudaStream_t stream)
 {
     UmmaParams p;
