@@ -818,8 +818,9 @@ int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, c
  *   d_workspace  at least kamera_select_pages_workspace_bytes(...) bytes, rules
  *             as for kamera_attend_shared
  * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..16, n_first,
- * n_last >= 0 with n_first + n_last <= n_select.  Device errors: LEN (the
- * sequence read as empty: all -1), SLOT (a page outside num_pages ranks last).
+ * n_last >= 0 with n_first + n_last <= n_select, at most 49152 pages in max_len
+ * (UNSUPPORTED beyond).  Device errors: LEN (the sequence read as empty: all -1),
+ * SLOT (a page outside num_pages ranks last).
  */
 typedef struct KameraPageSelect {
     const void* q;

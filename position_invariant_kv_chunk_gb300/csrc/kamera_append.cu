@@ -54,6 +54,7 @@ struct AppendParams {
     const int64_t* slots;
     const int64_t* axis_pos;                  // [n_tokens][n_axes], or null
     int32_t n_axes, n_freq;
+    int32_t unit_log;                         // frequencies of a unit: 2^3 (halves) or 2^2 (pairs)
     int32_t* err;
     uint64_t turn[KAMERA_MAX_ROT_DIM / 2];    // theta / 2 pi, in 2^-64 turns
     uint8_t axis[KAMERA_MAX_ROT_DIM / 2];
@@ -84,9 +85,9 @@ __device__ __forceinline__ uint4 ldg_row(const __nv_bfloat16* p)
     return v;
 }
 
-// One 16-byte unit of one token, from `src` to `dst`.  q may be rotated in
-// place: a unit is read and written by this thread alone, before any other
-// access to it, so the loads need no order beyond the data's.
+// q may be rotated in place: a unit is read and written by one thread alone, its
+// loads before its stores, so the loads need no order beyond the data's (but not
+// the read-only path).
 template <bool INPLACE>
 __device__ __forceinline__ uint4 unit_load(const __nv_bfloat16* p)
 {
@@ -96,13 +97,111 @@ __device__ __forceinline__ uint4 unit_load(const __nv_bfloat16* p)
         return ldg_row(p);
 }
 
-template <int TT, bool INPLACE>
+// A thread's unit: pass, source of the CTA's first token and destination of slot
+// (or token) 0.
+struct Unit {
+    const __nv_bfloat16* src;
+    __nv_bfloat16* dst;
+    int64_t src_ts, dst_ts;
+    int32_t kind, half, to_pool, unit;   // unit: its place among the head's rotated ones
+};
+
+__device__ __forceinline__ Unit find_unit(const AppendParams& p, int it, int t0)
+{
+    int k = 0, u = it;
+    while (u >= p.pass[k].heads * p.pass[k].units) {
+        u -= p.pass[k].heads * p.pass[k].units;
+        ++k;
+    }
+    const AppendPass& ps = p.pass[k];
+    const int head = u / ps.units, unit = u - head * ps.units;
+    Unit x;
+    x.src = ps.src + (int64_t)t0 * ps.src_ts + (int64_t)head * ps.src_hs + ps.off + 8 * unit;
+    x.dst = ps.dst + (int64_t)head * ps.dst_hs + ps.off + 8 * unit;
+    x.src_ts = ps.src_ts;
+    x.dst_ts = ps.dst_ts;
+    x.kind = ps.kind;
+    x.half = ps.half;
+    x.to_pool = ps.to_pool;
+    x.unit = unit;
+    return x;
+}
+
+// HALVES: some pass rotates halves (else b is not used).
+template <int TT, bool INPLACE, bool HALVES>
+__device__ __forceinline__ void load_unit(const Unit& u, int nt, uint4 (&a)[TT], uint4 (&b)[TT])
+{
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+        if (t < nt) {   // a padding row is read too: its rows exist
+            a[t] = unit_load<INPLACE>(u.src + t * u.src_ts);
+            if (HALVES && u.kind == UNIT_HALF)
+                b[t] = unit_load<INPLACE>(u.src + t * u.src_ts + u.half);
+        }
+}
+
+template <int TT, bool HALVES>
+__device__ __forceinline__ void store_unit(const AppendParams& p, const Unit& u, int t0, const float2* cs,
+                                           const int64_t* slot_s, uint4 (&a)[TT], uint4 (&b)[TT])
+{
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const int64_t slot = slot_s[t];
+        if (slot < 0)
+            continue;
+        __nv_bfloat16* o = u.dst + (u.to_pool ? slot : (int64_t)(t0 + t)) * u.dst_ts;
+        // pairs of frequencies: pair j of unit u at j * units + u, so that neighbouring units' reads
+        // fall into neighbouring banks
+        const float4* c4 = reinterpret_cast<const float4*>(cs + t * p.n_freq) + u.unit;
+        if (HALVES && u.kind == UNIT_HALF) {
+            float x[8], y[8];
+            unpack8(a[t], x);
+            unpack8(b[t], y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {   // (cos, sin) of two frequencies
+                const float4 w = c4[j * (p.n_freq >> 3)];
+                const float x0 = x[2 * j], x1 = x[2 * j + 1];
+                x[2 * j] = fmaf(x0, w.x, -(y[2 * j] * w.y));
+                y[2 * j] = fmaf(y[2 * j], w.x, x0 * w.y);
+                x[2 * j + 1] = fmaf(x1, w.z, -(y[2 * j + 1] * w.w));
+                y[2 * j + 1] = fmaf(y[2 * j + 1], w.z, x1 * w.w);
+            }
+            a[t] = pack8(x);
+            *reinterpret_cast<uint4*>(o + u.half) = pack8(y);
+        } else if (!HALVES && u.kind == UNIT_IL) {   // pairs (2i, 2i + 1) inside the vector
+            float x[8];
+            unpack8(a[t], x);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float4 w = c4[j * (p.n_freq >> 2)];
+                const float a0 = x[4 * j], b0 = x[4 * j + 1], a1 = x[4 * j + 2], b1 = x[4 * j + 3];
+                x[4 * j] = fmaf(a0, w.x, -(b0 * w.y));
+                x[4 * j + 1] = fmaf(b0, w.x, a0 * w.y);
+                x[4 * j + 2] = fmaf(a1, w.z, -(b1 * w.w));
+                x[4 * j + 3] = fmaf(b1, w.z, a1 * w.w);
+            }
+            a[t] = pack8(x);
+        }
+        *reinterpret_cast<uint4*>(o) = a[t];
+    }
+}
+
+// The rows of a thread's first unit are loaded before anything else: their
+// latency covers the slots', the positions' and the angles'.
+template <int TT, bool INPLACE, bool HALVES>
 __global__ void __launch_bounds__(512) append_kernel(const __grid_constant__ AppendParams p)
 {
     extern __shared__ __align__(16) float2 cs[];   // [TT][n_freq] cos, sin
-    __shared__ int64_t slot_s[TT];            // -1: this token is not written
+    __shared__ int64_t slot_s[TT];                 // -1: this token is not written
     const int t0 = blockIdx.x * TT;
     const int nt = min(TT, p.n_tokens - t0);
+    uint4 a[TT], b[TT];
+    Unit u;
+    const bool has = (int)threadIdx.x < p.items;
+    if (has) {
+        u = find_unit(p, threadIdx.x, t0);
+        load_unit<TT, INPLACE, HALVES>(u, nt, a, b);
+    }
     if (threadIdx.x < TT) {
         int64_t slot = -1;
         if ((int)threadIdx.x < nt) {
@@ -117,8 +216,8 @@ __global__ void __launch_bounds__(512) append_kernel(const __grid_constant__ App
                     if (x > KAMERA_MAX_ABS_DELTA || x < -KAMERA_MAX_ABS_DELTA)
                         bits |= KAMERA_DEVERR_DESCRIPTOR;
                 }
-                for (int a = 0; a < p.n_axes; ++a) {
-                    const int64_t x = p.axis_pos[(int64_t)t * p.n_axes + a];
+                for (int c = 0; c < p.n_axes; ++c) {
+                    const int64_t x = p.axis_pos[(int64_t)t * p.n_axes + c];
                     if (x > KAMERA_MAX_ABS_DELTA || x < -KAMERA_MAX_ABS_DELTA)
                         bits |= KAMERA_DEVERR_DESCRIPTOR;
                 }
@@ -138,76 +237,16 @@ __global__ void __launch_bounds__(512) append_kernel(const __grid_constant__ App
         const int64_t ph = (int64_t)((uint64_t)pos * p.turn[f]);
         float s, c;
         sincospif((float)ph * 1.08420217248550443e-19f, &s, &c);   // 2^-63
-        cs[t * p.n_freq + f] = make_float2(c, s);
+        const int unit = f >> p.unit_log, pair = (f & ((1 << p.unit_log) - 1)) >> 1;
+        cs[t * p.n_freq + 2 * (pair * (p.n_freq >> p.unit_log) + unit) + (f & 1)] = make_float2(c, s);
     }
     __syncthreads();
-
-    for (int it = threadIdx.x; it < p.items; it += blockDim.x) {
-        int k = 0, u = it;
-        while (u >= p.pass[k].heads * p.pass[k].units) {
-            u -= p.pass[k].heads * p.pass[k].units;
-            ++k;
-        }
-        const AppendPass& ps = p.pass[k];
-        const int head = u / ps.units, unit = u - head * ps.units;
-        const __nv_bfloat16* src = ps.src + (int64_t)t0 * ps.src_ts + (int64_t)head * ps.src_hs + ps.off + 8 * unit;
-        __nv_bfloat16* dst = ps.dst + (int64_t)head * ps.dst_hs + ps.off + 8 * unit;
-        // S tokens in flight a round: 32 or 64 bytes of loads a thread, few enough
-        // registers that three or four CTAs share an SM
-        constexpr int S = TT < 2 ? 1 : 2;
-#pragma unroll 1
-        for (int tb = 0; tb < nt; tb += S, src += S * ps.src_ts) {
-            __nv_bfloat16* o[S];   // null: the token is not written
-            uint4 a[S], b[S];
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                const int64_t slot = slot_s[tb + i];
-                o[i] = slot < 0 ? nullptr : dst + (ps.to_pool ? slot : (int64_t)(t0 + tb + i)) * ps.dst_ts;
-                if (o[i]) {
-                    a[i] = unit_load<INPLACE>(src + i * ps.src_ts);
-                    if (ps.kind == UNIT_HALF)
-                        b[i] = unit_load<INPLACE>(src + i * ps.src_ts + ps.half);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                if (!o[i])
-                    continue;
-                const float2* row = cs + (tb + i) * p.n_freq;
-                if (ps.kind == UNIT_HALF) {
-                    const float4* c4 = reinterpret_cast<const float4*>(row + 8 * unit);
-                    float x[8], y[8];
-                    unpack8(a[i], x);
-                    unpack8(b[i], y);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {   // (cos, sin) of frequencies 8 unit + 2j, + 2j + 1
-                        const float4 w = c4[j];
-                        const float x0 = x[2 * j], x1 = x[2 * j + 1];
-                        x[2 * j] = fmaf(x0, w.x, -(y[2 * j] * w.y));
-                        y[2 * j] = fmaf(y[2 * j], w.x, x0 * w.y);
-                        x[2 * j + 1] = fmaf(x1, w.z, -(y[2 * j + 1] * w.w));
-                        y[2 * j + 1] = fmaf(y[2 * j + 1], w.z, x1 * w.w);
-                    }
-                    a[i] = pack8(x);
-                    *reinterpret_cast<uint4*>(o[i] + ps.half) = pack8(y);
-                } else if (ps.kind == UNIT_IL) {   // pairs (2i, 2i + 1) inside the vector, frequencies 4 unit + 0..3
-                    const float4* c4 = reinterpret_cast<const float4*>(row + 4 * unit);
-                    float x[8];
-                    unpack8(a[i], x);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float4 w = c4[j];
-                        const float a0 = x[4 * j], b0 = x[4 * j + 1], a1 = x[4 * j + 2], b1 = x[4 * j + 3];
-                        x[4 * j] = fmaf(a0, w.x, -(b0 * w.y));
-                        x[4 * j + 1] = fmaf(b0, w.x, a0 * w.y);
-                        x[4 * j + 2] = fmaf(a1, w.z, -(b1 * w.w));
-                        x[4 * j + 3] = fmaf(b1, w.z, a1 * w.w);
-                    }
-                    a[i] = pack8(x);
-                }
-                *reinterpret_cast<uint4*>(o[i]) = a[i];
-            }
-        }
+    if (has)
+        store_unit<TT, HALVES>(p, u, t0, cs, slot_s, a, b);
+    for (int it = threadIdx.x + blockDim.x; it < p.items; it += blockDim.x) {   // rows of more than 512 units
+        u = find_unit(p, it, t0);
+        load_unit<TT, INPLACE, HALVES>(u, nt, a, b);
+        store_unit<TT, HALVES>(p, u, t0, cs, slot_s, a, b);
     }
 }
 
@@ -218,10 +257,17 @@ cudaError_t launch_append_t(const AppendParams& p, bool inplace, cudaStream_t st
     const int threads = ((p.items + rounds - 1) / rounds + 31) / 32 * 32;
     const unsigned grid = (unsigned)((p.n_tokens + TT - 1) / TT);
     const size_t smem = sizeof(float2) * (size_t)TT * (size_t)p.n_freq;   // at most 8 KB
-    if (inplace)
-        append_kernel<TT, true><<<grid, threads, smem, stream>>>(p);
-    else
-        append_kernel<TT, false><<<grid, threads, smem, stream>>>(p);
+    if (p.unit_log == 3) {
+        if (inplace)
+            append_kernel<TT, true, true><<<grid, threads, smem, stream>>>(p);
+        else
+            append_kernel<TT, false, true><<<grid, threads, smem, stream>>>(p);
+    } else {
+        if (inplace)
+            append_kernel<TT, true, false><<<grid, threads, smem, stream>>>(p);
+        else
+            append_kernel<TT, false, false><<<grid, threads, smem, stream>>>(p);
+    }
     return cudaGetLastError();
 }
 
@@ -264,19 +310,20 @@ void add_passes(AppendParams& p, const RopeParams* r, const void* src, void* dst
 cudaError_t launch_append(AppendParams& p, const RopeParams& r, bool inplace, cudaStream_t stream)
 {
     p.n_freq = r.n_freq;
+    p.unit_log = r.pairing == KAMERA_ROPE_ROTATE_HALF ? 3 : 2;
     p.n_axes = r.n_axes;
     p.axis_pos = r.axis_delta;
     for (int f = 0; f < r.n_freq; ++f) {
         p.turn[f] = turn_fraction(r.inv_freq[f]);
         p.axis[f] = r.axis[f];
     }
-    // One token a CTA while that leaves SMs idle or barely filled (a decode step
-    // is latency), eight once every SM has a few such CTAs.
-    const int t = p.n_tokens;
-    if (t >= 152 * 16)
-        return launch_append_t<8>(p, inplace, stream);
-    if (t >= 152 * 4)
-        return launch_append_t<2>(p, inplace, stream);
+    // One token a CTA while that leaves SMs idle or barely filled (a decode step is
+    // latency); four once the SMs have two CTAs each, so that the set-up (slots,
+    // angles) is shared and 64 bytes a thread are in flight: 10368 tokens of 28 + 4
+    // heads of 128 take 47.7 us with one, 34.9 with two, 33.8 with four and 42.3
+    // with eight (too few CTAs fit).
+    if (p.n_tokens >= 152 * 8)
+        return launch_append_t<4>(p, inplace, stream);
     return launch_append_t<1>(p, inplace, stream);
 }
 

@@ -534,24 +534,28 @@ int device_sms()
     return sms;
 }
 
-// Splits of the own tokens: `pieces` 16-token pieces of each of `units`.  Up to
-// one CTA a slot (two CTAs share an SM) while that leaves each at least 64
-// tokens; long batches are cut finer, about six rounds of CTAs of at least 512
-// tokens, so ragged lengths even out.
+// Splits of the own tokens: `pieces` 16-token pieces of each of `units`; three
+// CTAs share an SM.  While a slot's share is at most 1536 tokens, as many splits
+// as fill one round of CTAs (a second, partly filled round would double the
+// time), each of at least 64 tokens; beyond, about six rounds of CTAs of at
+// least 512 tokens, so that ragged lengths even out.
 void split_own(PagedParams& p, int64_t pieces, int sms)
 {
-    const int64_t units = (int64_t)p.n_seqs * p.H, slots = 2ll * sms;
+    const int64_t units = (int64_t)p.n_seqs * p.H, slots = 3ll * sms;
     if (pieces <= 0) {
         p.own_split = 1;
         p.own_slots = 0;
         return;
     }
-    int64_t per = (units * pieces + slots - 1) / slots;
-    if (per > 32)
-        per = std::max<int64_t>(32, (units * pieces) / (6 * slots));
-    per = (std::max<int64_t>(per, 4) + 3) / 4 * 4;
-    per = std::max<int64_t>(per, (pieces + 255) / 256);
-    p.own_split = (int32_t)std::min<int64_t>(per, pieces);
+    int64_t n;
+    if (units * pieces <= 96 * slots)
+        n = std::min(std::max<int64_t>(1, slots / units), (pieces + 3) / 4);
+    else
+        n = pieces / std::min(pieces, std::max<int64_t>(32, units * pieces / (6 * slots)));
+    n = std::min<int64_t>(n, 256);
+    int64_t per = (pieces + n - 1) / n;
+    per = (per + 3) / 4 * 4;   // whole rounds of the four warps
+    p.own_split = (int32_t)std::min(per, pieces);
     p.own_slots = (int32_t)((pieces + p.own_split - 1) / p.own_split);
 }
 

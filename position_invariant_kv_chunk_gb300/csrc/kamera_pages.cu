@@ -9,15 +9,23 @@
 // so a page costs 4 d bytes read and 2 d multiplies per KV head, whatever G is.
 //
 // The choice of pages is a whole-number result, and fp32 sums of 2 d terms in
-// one order or another would flip it where two scores lie close.  The scores
-// are therefore held as pairs of floats: q+ and q- are split into a 16-bit part,
-// whose products with the bf16 box are exact in fp32, and a remainder; the
-// exact products are added with the error of every addition kept (the two-sum
-// of Knuth, The Art of Computer Programming vol. 2, 4.2.2), which leaves about
-// 2^-40 of the sum of the terms' magnitudes.  Two channels go through each
-// packed fp32 instruction, and the sums of eight pages are reduced across the
-// warp together (each step halves the pages a lane holds), so the arithmetic
-// stays below the time the boxes take to arrive.
+// one order or another would flip it where two scores lie close.  So it is made
+// in two steps:
+//   - every page's score in fp32 on the tensor cores (m16n8k16: 16 pages by the
+//     weights), read-bound.  The box is bf16 and exact; the weights q+, q- enter
+//     as three bf16 parts in three columns of the B operand, and a fourth
+//     column holds their magnitudes: against the magnitudes of the box it gives
+//     the sum of the terms' magnitudes, and with it a bound of the score's error.
+//   - the n-th largest of these scores, t, and the largest error bound, E, split
+//     the pages into those surely in (above t + 2 E), surely out (below t - 2 E)
+//     and a few between, which are scored again, exactly to about 2^-40 of their
+//     terms: the weights as a 16-bit part, whose products with the box are exact
+//     in fp32, and a remainder, the products added with the error of every
+//     addition kept (the two-sum of Knuth, The Art of Computer Programming
+//     vol. 2, 4.2.2).
+// Scoring every page the second way took 127 us where the boxes (32 sequences x 4
+// heads x 7300 pages, 0.47 GB) take 70 us to read: two-sums cost 100 instructions
+// a page and head.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -26,6 +34,7 @@
 #include "kamera_hostcheck.h"
 #include "kamera_internal.h"
 #include "kamera_ptx.cuh"
+#include "kamera_warpmma.cuh"
 
 namespace kamera {
 
@@ -53,65 +62,53 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
     return a;
 }
 
-// Four lanes share a 16-byte vector of a page's rows, each taking every fourth
-// token (lanes 8 apart, so eight neighbouring vectors of a token are read
-// together), and join by shuffles.  Read-bound: each key once, min and max
-// exact in bf16.
-__global__ void __launch_bounds__(256) summary_kernel(const SummaryParams p)
+// A thread takes one 16-byte vector of a page's rows, 16 tokens in flight at a
+// time (a warp reads 512 contiguous bytes of each).  Read-bound: each key once,
+// min and max exact in bf16, no exchange between threads.
+__global__ void __launch_bounds__(128) summary_kernel(const SummaryParams p)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = lane >> 3;
-    const int64_t item = ((int64_t)blockIdx.x * 8 + warp) * 8 + (lane & 7);
+    const int64_t item = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    if (item >= p.items)
+        return;
+    const int64_t e = item / p.vecs;
+    const int vec = (int)(item - e * p.vecs);
+    const int64_t page = p.ids[e];
+    const int c = p.tokens[e];
+    int32_t bits = 0;
+    if (page < 0 || page >= p.num_pages)
+        bits |= KAMERA_DEVERR_SLOT;
+    if (c < 0 || c > p.P)
+        bits |= KAMERA_DEVERR_LEN;
+    if (bits && vec == 0)
+        raise_err(p.err, bits);
+    if (bits || c == 0)
+        return;
+    const __nv_bfloat16* src = p.k + page * p.P * p.slot_stride + 8 * vec;
     uint32_t lo[4], hi[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         lo[i] = 0x7F807F80u;   // +infinity
         hi[i] = 0xFF80FF80u;   // -infinity
     }
-    bool write = false;
-    int64_t page = 0;
-    int vec = 0;
-    if (item < p.items) {
-        const int64_t e = item / p.vecs;
-        vec = (int)(item - e * p.vecs);
-        page = p.ids[e];
-        const int c = p.tokens[e];
-        int32_t bits = 0;
-        if (page < 0 || page >= p.num_pages)
-            bits |= KAMERA_DEVERR_SLOT;
-        if (c < 0 || c > p.P)
-            bits |= KAMERA_DEVERR_LEN;
-        if (bits && vec == 0 && part == 0)
-            raise_err(p.err, bits);
-        if (!bits && c > 0) {
-            write = true;
-            const __nv_bfloat16* src = p.k + page * p.P * p.slot_stride + 8 * vec;
-#pragma unroll 4
-            for (int t = part; t < c; t += 4) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + (int64_t)t * p.slot_stride));
-                lo[0] = min_bf16x2(lo[0], v.x);
-                lo[1] = min_bf16x2(lo[1], v.y);
-                lo[2] = min_bf16x2(lo[2], v.z);
-                lo[3] = min_bf16x2(lo[3], v.w);
-                hi[0] = max_bf16x2(hi[0], v.x);
-                hi[1] = max_bf16x2(hi[1], v.y);
-                hi[2] = max_bf16x2(hi[2], v.z);
-                hi[3] = max_bf16x2(hi[3], v.w);
+    for (int t0 = 0; t0 < c; t0 += 16, src += 16 * p.slot_stride) {
+        uint4 v[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t)   // past the count: the first token again
+            v[t] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + t < c ? t : 0) * p.slot_stride));
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            const uint32_t w[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = min_bf16x2(lo[i], w[i]);
+                hi[i] = max_bf16x2(hi[i], w[i]);
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int s = 8; s <= 16; s *= 2) {
-            lo[i] = min_bf16x2(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], s));
-            hi[i] = max_bf16x2(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], s));
-        }
-    if (write && part < 2) {   // lanes of part 0 write the minima, of part 1 the maxima
-        const int vh = p.d / 8, h = vec / vh;
-        __nv_bfloat16* o = p.out + ((page * p.H + h) * 2 + part) * p.d + 8 * (vec - h * vh);
-        *reinterpret_cast<uint4*>(o) =
-            part == 0 ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    }
+    const int vh = p.d / 8, h = vec / vh;
+    __nv_bfloat16* o = p.out + (page * p.H + h) * 2 * p.d + 8 * (vec - h * vh);
+    *reinterpret_cast<uint4*>(o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(o + p.d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
 }
 
 // ------------------------------------------------------------------- scores --
@@ -121,7 +118,7 @@ struct SelectParams {
     const int32_t* pages;
     const int32_t* lens;
     int32_t* selected;
-    uint64_t* keys;              // [n_seqs * H][width]
+    uint64_t* keys;              // [n_seqs * H][width]: (score, error bound) as float2, then refined keys
     int64_t num_pages;
     int32_t n_seqs, H, G, P;
     int32_t max_pages, max_len, width;
@@ -163,141 +160,213 @@ __device__ __forceinline__ uint32_t ordered(float x)
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-constexpr int kScoreWarps = 8;
-constexpr int kBatch = 8;        // loads a lane keeps in flight: kBatch * (32 / LP) pages a warp
+// q- (i < D) or q+ of channel i mod D as a pair of floats.
+template <int D>
+__device__ __forceinline__ void signed_sum(const SelectParams& p, int s, int h, int i, float& a, float& e)
+{
+    const int ch = i < D ? i : i - D;
+    const __nv_bfloat16* q = p.q + ((int64_t)s * p.H * p.G + h * p.G) * D + ch;
+    a = e = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < p.G; ++g) {
+        const float x = __bfloat162float(q[(int64_t)g * D]);
+        pair_add(a, e, i < D ? fminf(x, 0.f) : fmaxf(x, 0.f), 0.f);
+        if (x != x)
+            a = x;   // fminf and fmaxf drop a NaN
+    }
+}
+
+constexpr int kScoreWarps = 4;
+constexpr int kScoreStages = 2;  // batches in a warp's ring (three CTAs an SM)
+constexpr int kScorePages = 16;  // pages of a warp's MMA
+// A score's error: 2 d / 16 MMAs, each a sum of 17 terms no better than truncated
+// fp32, is at most 2 d / 16 x 17 x 2^-23 < 2^-14.9 of the sum of the terms'
+// magnitudes (d = 128).
+constexpr float kScoreErr = 3.4e-5f;
+
+// Scores and error bounds of the pages of one (sequence, KV head).  Each warp
+// keeps a ring of batches of 16 boxes, filled by 16-byte async copies (a box of d =
+// 128 is 512 bytes, one copy of a warp), so copies stay in flight while it
+// multiplies; a bulk copy a box was slower (86 us where these take SCORE_US: the
+// copy engine takes about 28 cycles for each).  The sum
+// over channels may run in any order, so a lane feeds the A operand with whole
+// 16-byte pieces: lane (page gq, t4) reads pieces t4 + 4 j of its page's box, and
+// the B operand holds the weights of the same pieces.  Column gq of B: 0-2 the
+// weights' bf16 parts.  (m16n8k16 takes about 32 cycles of a sub-partition here:
+// 16 of them a batch leave room for the copies, 32 would not.)
+template <int D>
+struct ScoreLayout {
+    static constexpr int NC = 2 * D / 32;                     // 16-byte pieces of a box that a lane reads
+    static constexpr uint32_t kBox = 4 * D;                   // bytes
+    static constexpr uint32_t kStage = kScorePages * kBox;    // piece c of row r at c ^ 4 (r & 1): no bank conflicts
+    static constexpr uint32_t kBytes = kScoreWarps * kScoreStages * kStage;
+};
 
 template <int D>
 __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectParams p)
 {
-    constexpr int LP = D / 4;                    // lanes of a page: 16 bytes of [min | max] each
-    constexpr int PL = 32 / LP;                  // pages a warp loads at once
-    constexpr int PB = kBatch * PL;              // pages of a warp's batch
-    __shared__ __align__(16) float qa[2 * D], qb[2 * D];   // q- | q+ : the 16-bit part and the rest
+    using Y = ScoreLayout<D>;
+    constexpr int NC = Y::NC, NS = kScoreStages;
+    extern __shared__ __align__(16) unsigned char ring_raw[];
+    __shared__ __align__(16) __nv_bfloat16 wt[3][2 * D];
+    __shared__ float norm_s[kScoreWarps];
+    ptx::grid_launch_next();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t4 = lane & 3;
     const int s = blockIdx.y / p.H, h = blockIdx.y - s * p.H;
     int lo, hi;
     page_range(p, s, lo, hi);
-    const int chunk = kScoreWarps * PB * p.sweeps;
-    const int c0 = lo + (int)blockIdx.x * chunk;
+    constexpr int step = kScoreWarps * kScorePages;
+    const int chunk = step * p.sweeps, c0 = lo + (int)blockIdx.x * chunk, c1 = min(c0 + chunk, hi);
     if (c0 >= hi)
         return;
-    for (int i = threadIdx.x; i < 2 * D; i += 32 * kScoreWarps) {
-        const int ch = i < D ? i : i - D;
-        float a = 0.f, e = 0.f;
-        for (int g = 0; g < p.G; ++g) {
-            const float x = __bfloat162float(p.q[((int64_t)s * p.H * p.G + h * p.G + g) * D + ch]);
-            pair_add(a, e, i < D ? fminf(x, 0.f) : fmaxf(x, 0.f), 0.f);
-            if (x != x)
-                a = x;   // fminf and fmaxf drop a NaN
-        }
-        const float top = __uint_as_float(__float_as_uint(a) & 0xFFFFFF00u);   // 16 significant bits
-        qa[i] = top;
-        qb[i] = __fadd_rn(__fadd_rn(a, -top), e);
-    }
-    __syncthreads();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & (LP - 1), which = lane / LP;
-    uint64_t wa[4], wb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        wa[i] = *reinterpret_cast<const uint64_t*>(&qa[8 * sub + 2 * i]);
-        wb[i] = *reinterpret_cast<const uint64_t*>(&qb[8 * sub + 2 * i]);
-    }
-    const uint64_t neg1 = ptx::f2_make(0xBF800000u, 0xBF800000u);
+    // the warp's batches: pages first + step k .. + 15
     const int32_t* table = p.pages + (int64_t)s * p.max_pages;
-    uint64_t* keys = p.keys + (int64_t)blockIdx.y * p.width;
-    const int c1 = min(c0 + chunk, hi);
-    for (int j0 = c0 + warp * PB; j0 < c1; j0 += kScoreWarps * PB) {
-        // the batch's pages, one to a lane (-1: past the range or outside the pool)
-        int mine = -1;
-        if (lane < PB && j0 + lane < c1) {
-            mine = table[j0 + lane];
-            if (mine < 0 || mine >= p.num_pages) {
-                mine = -1;
-                if (h == 0)
-                    raise_err(p.err, KAMERA_DEVERR_SLOT);
+    const int first = c0 + warp * kScorePages;
+    const int count = first < c1 ? (c1 - first + step - 1) / step : 0;
+    const uint32_t ring = ptx::smem_addr(ring_raw) + warp * NS * Y::kStage;
+    auto entry = [&](int k) {   // this lane's page of batch k as the table has it; -1 past the range
+        const int j = first + k * step + lane;
+        return k < count && lane < kScorePages && j < c1 ? table[j] : -1;
+    };
+    uint32_t known_of[NS];   // the pages of a stage inside the pool
+#pragma unroll
+    for (int b = 0; b < NS; ++b)
+        known_of[b] = 0;
+    constexpr int LB = Y::kBox / 16, PI = 32 / LB;   // lanes of a box, boxes of one copy of the warp
+    const __nv_bfloat16* src = p.summary + (int64_t)h * (2 * D) + 8 * (lane % LB);
+    const uint32_t row_bytes = (uint32_t)p.H * Y::kBox;
+    // A row without a page repeats one of the batch's boxes, which changes nothing.
+    auto load = [&](int k, int page, uint32_t& known_b) {   // one group of copies a batch, empty past the last
+        const bool in = k < count && lane < kScorePages && first + k * step + lane < c1;
+        const bool good = in && page >= 0 && page < p.num_pages;
+        if (in && !good && h == 0)
+            raise_err(p.err, KAMERA_DEVERR_SLOT);
+        known_b = __ballot_sync(0xFFFFFFFFu, good);
+        if (known_b) {
+            const int some = __shfl_sync(0xFFFFFFFFu, page, __ffs((int)known_b) - 1);
+            const uint32_t safe = (uint32_t)(good ? page : some);
+            // rows alternate in parity (one box a copy) or share it by halves of the warp (two)
+            const uint32_t dst = ring + (k % NS) * Y::kStage + (lane / LB) * Y::kBox;
+            const uint32_t even = dst + 16 * ((lane % LB) ^ (PI == 2 ? (lane / LB) << 2 : 0));
+            const uint32_t odd = dst + 16 * ((lane % LB) ^ 4);
+#pragma unroll
+            for (int i = 0; i < kScorePages / PI; ++i) {
+                const uint32_t from = __shfl_sync(0xFFFFFFFFu, safe, i * PI + lane / LB);
+                ptx::cp_async16((PI == 1 && (i & 1) ? odd : even) + i * PI * Y::kBox,
+                                reinterpret_cast<const unsigned char*>(src) + (uint64_t)from * row_bytes);
             }
         }
-        uint4 v[kBatch];
+        ptx::cp_async_commit();
+    };
+    int ahead = entry(NS - 1);
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int page = __shfl_sync(0xFFFFFFFFu, mine, b * PL + which);
-            v[b] = make_uint4(0u, 0u, 0u, 0u);
-            if (page >= 0)
-                v[b] = __ldg(reinterpret_cast<const uint4*>(p.summary + ((int64_t)page * p.H + h) * (2 * D)) + sub);
-        }
-        float S[kBatch], E[kBatch];
+    for (int k = 0; k < NS - 1; ++k)
+        load(k, entry(k), known_of[k]);
+
+    float norm = 0.f;   // the sum of the weights' magnitudes, rounded up
+    for (int i = threadIdx.x; i < 2 * D; i += 32 * kScoreWarps) {
+        float a, e;
+        signed_sum<D>(p, s, h, i, a, e);
+        a = __fadd_rn(a, e);
+        norm = __fadd_ru(norm, fabsf(a));
+        wt[0][i] = __float2bfloat16_rn(a);
+        a = __fadd_rn(a, -__bfloat162float(wt[0][i]));
+        wt[1][i] = __float2bfloat16_rn(a);
+        a = __fadd_rn(a, -__bfloat162float(wt[1][i]));
+        wt[2][i] = __float2bfloat16_rn(a);
+    }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
-            uint64_t x = ptx::f2_from_bf16x2(w[0]);
-            uint64_t sum = ptx::f2_mul(wa[0], x), err = ptx::f2_mul(wb[0], x);
+    for (int o = 16; o >= 1; o /= 2)
+        norm = __fadd_ru(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
+    if (lane == 0)
+        norm_s[warp] = norm;
+    __syncthreads();
+    norm = 0.f;
 #pragma unroll
-            for (int i = 1; i < 4; ++i) {
-                x = ptx::f2_from_bf16x2(w[i]);
-                const uint64_t pr = ptx::f2_mul(wa[i], x);           // exact
-                const uint64_t t = ptx::f2_add(sum, pr);
-                const uint64_t z = ptx::f2_fma(sum, neg1, t);        // t - sum
-                const uint64_t tz = ptx::f2_fma(z, neg1, t);         // t - z
-                const uint64_t r = ptx::f2_add(ptx::f2_fma(tz, neg1, sum), ptx::f2_fma(z, neg1, pr));
-                err = ptx::f2_add(ptx::f2_fma(wb[i], x, err), r);
-                sum = t;
+    for (int i = 0; i < kScoreWarps; ++i)
+        norm = __fadd_ru(norm, norm_s[i]);
+    uint4 w[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+        w[j] = gq < 3 ? *reinterpret_cast<const uint4*>(&wt[gq < 3 ? gq : 0][8 * (t4 + 4 * j)])
+                      : make_uint4(0u, 0u, 0u, 0u);
+    float2* keys = reinterpret_cast<float2*>(p.keys + ((int64_t)s * p.H + h) * p.width);
+    for (int k0 = 0; k0 < count; k0 += NS) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {   // batch k in stage u
+            const int k = k0 + u;
+            if (k >= count)
+                break;
+            const int page = ahead;
+            ahead = entry(k + NS);
+            load(k + NS - 1, page, known_of[(u + NS - 1) % NS]);
+            ptx::cp_async_wait<NS - 1>();   // batch k has landed, for this lane's copies and
+            __syncwarp();                   // then for every lane's
+            const uint32_t ra = ring + u * Y::kStage + gq * Y::kBox + 16 * t4, rb = ra + 8 * Y::kBox;
+            const uint32_t odd = (uint32_t)(gq & 1) << 6;
+            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};   // two chains
+            // the least and the largest entry of the batch's boxes: among the minima (the
+            // first half of a box), among the maxima (every other entry lies between)
+            uint32_t least = 0u, most = 0u;
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                uint32_t a[4], b[4];
+                ptx::lds128(ra + ((64 * j) ^ odd), a);
+                ptx::lds128(rb + ((64 * j) ^ odd), b);
+                const uint32_t f0[4] = {a[0], b[0], a[1], b[1]}, f1[4] = {a[2], b[2], a[3], b[3]};
+                wmma16::mma_bf16(sc[0], f0, w[j].x, w[j].y);
+                wmma16::mma_bf16(sc[1], f1, w[j].z, w[j].w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (j < NC / 2)
+                        least = min_bf16x2(least, min_bf16x2(a[i], b[i]));
+                    else
+                        most = max_bf16x2(most, max_bf16x2(a[i], b[i]));
             }
-            uint32_t s0, s1, e0, e1;
-            asm("mov.b64 {%0, %1}, %2;" : "=r"(s0), "=r"(s1) : "l"(sum));
-            asm("mov.b64 {%0, %1}, %2;" : "=r"(e0), "=r"(e1) : "l"(err));
-            S[b] = __uint_as_float(s0);
-            E[b] = __uint_as_float(e0);
-            pair_add(S[b], E[b], __uint_as_float(s1), __uint_as_float(e1));
-        }
-        // reduce over a page's LP lanes: each of three steps halves the batch a lane holds
+            most = max_bf16x2(most, least ^ 0x80008000u);
 #pragma unroll
-        for (int step = 0; step < 3; ++step) {
-            const int dist = LP >> (step + 1), keep = kBatch >> (step + 1);
-            const bool up = (sub & dist) != 0;
+            for (int o = 16; o >= 1; o /= 2)
+                most = max_bf16x2(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+            const float e = __fmul_ru(kScoreErr, __fmul_ru(norm, fmaxf(bf16lo(most), bf16hi(most))));
+            // columns 0, 1 of pages gq, gq + 8 sit in lanes t4 = 0, column 2 in t4 = 1
+            const float la = __shfl_down_sync(0xFFFFFFFFu, sc[0][0] + sc[1][0], 1);
+            const float lb = __shfl_down_sync(0xFFFFFFFFu, sc[0][2] + sc[1][2], 1);
+            if (t4 == 0) {
 #pragma unroll
-            for (int i = 0; i < keep; ++i) {
-                const float ss = up ? S[i] : S[i + keep], ee = up ? E[i] : E[i + keep];
-                float ks = up ? S[i + keep] : S[i], ke = up ? E[i + keep] : E[i];
-                pair_add(ks, ke, __shfl_xor_sync(0xFFFFFFFFu, ss, dist), __shfl_xor_sync(0xFFFFFFFFu, ee, dist));
-                S[i] = ks;
-                E[i] = ke;
-            }
-        }
-#pragma unroll
-        for (int dist = LP / 16; dist >= 1; dist /= 2)
-            pair_add(S[0], E[0], __shfl_xor_sync(0xFFFFFFFFu, S[0], dist), __shfl_xor_sync(0xFFFFFFFFu, E[0], dist));
-        // lane `sub` holds batch entry sub / (LP / 8)
-        const int at = (sub / (LP / 8)) * PL + which;
-        const bool known = __shfl_sync(0xFFFFFFFFu, mine, at) >= 0;
-        if ((sub & (LP / 8 - 1)) == 0 && j0 + at < c1) {
-            float t, r;
-            two_sum(S[0], E[0], t, r);   // t + r, t the sum rounded: (t, r) orders as the sum does
-            uint64_t key = 0;
-            if (known) {
-                if (!(fabsf(t) <= 3.402823466e38f && r == r)) {   // not finite: ranks first
-                    t = INFINITY;
-                    r = 0.f;
+                for (int r = 0; r < 2; ++r) {
+                    const int j = first + k * step + gq + 8 * r;
+                    if (j < c1) {
+                        const float v = (sc[0][2 * r] + sc[1][2 * r]) + ((sc[0][2 * r + 1] + sc[1][2 * r + 1]) + (r == 0 ? la : lb));
+                        const bool finite = fabsf(v) <= 3.402823466e38f;   // else it ranks first
+                        keys[j] = (known_of[u] >> (gq + 8 * r)) & 1u ? make_float2(finite ? v : INFINITY, e)
+                                                                     : make_float2(0.f, -1.f);
+                    }
                 }
-                key = ((uint64_t)ordered(t) << 32) | ordered(r);
             }
-            keys[j0 + at] = key;
+            __syncwarp();   // the stage's rows are read before it is filled again
         }
     }
+    ptx::cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------- choice --
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;              // digits of 11 bits
-constexpr int kGather = 1024;            // keys of one digit that are ranked by comparison
-constexpr int kMaxWidth = 1 << 17;       // pages of a sequence
-constexpr int kStage = 12288;            // keys kept in shared memory (96 KB)
+constexpr int kGather = 1024;            // keys that are ranked by comparison
+constexpr int kMaxWidth = 49152;         // pages of a sequence: their 32-bit keys stay in shared memory
 
+template <int D>
 struct SelSmem {
     uint32_t hist[kBins];
     uint64_t cand[kGather];
     int32_t cand_j[kGather];
-    uint32_t warp_sum[kSelThreads / 32];
-    uint64_t warp_min[kSelThreads / 32], warp_max[kSelThreads / 32];
+    float qa[2 * D], qb[2 * D];          // q- | q+: the 16-bit part and the rest
+    uint32_t warp_sum[kSelWarps];
+    uint64_t warp_min[kSelWarps], warp_max[kSelWarps];
+    float warp_err[kSelWarps];
     int32_t bin, above, n_cand;
+    uint64_t found;
 };
 
 // Exclusive sum over the block of one value a thread; `total` for everybody.
@@ -318,7 +387,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
     uint32_t before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) {
+    for (int w = 0; w < kSelWarps; ++w) {
         if (w < warp)
             before += warp_sum[w];
         total += warp_sum[w];
@@ -326,179 +395,371 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
     return before + x - v;
 }
 
-// One CTA per (sequence, KV head): the k-th largest key by radix steps of 11
-// bits from the first bit in which the keys differ, then the pages above it in
-// order from a bitmap.  A step ends the search when a digit's keys are all
-// taken, all equal (the lowest pages win), or few enough to rank by comparison,
-// which random scores reach after one or two steps.  Latency-bound: a handful of
-// passes over the keys, which stay in shared memory up to 12288 pages.
-template <bool STAGE>
+// The `need`-th largest key of a set (1 <= need <= its size), by radix steps of 11
+// bits from the first bit in which the keys differ (kmin .. kmax over the set):
+// on return the keys whose (>> shift) exceeds `prefix` are more than it, and
+// `need` is what is left to take of those whose (>> shift) equals it; shift is 0,
+// or `count` of them are at most kGather, or all of them are to be taken.
+// each(f) calls f(key) for the thread's share of the set.
+template <typename SM, typename Each>
+__device__ __forceinline__ void radix_find(SM& sm, uint64_t kmin, uint64_t kmax, Each each, int& need, int& shift,
+                                           uint64_t& prefix, int& count)
+{
+    const int tid = threadIdx.x;
+    constexpr int PT = kBins / kSelThreads;
+    const int top = 63 - __clzll((long long)(kmin ^ kmax));   // the highest bit that differs
+    shift = max(0, top - 10);
+    uint64_t fixed = top == 63 ? 0ull : kmin >> (top + 1);    // bits above the digit, shared so far
+    int width = top + 1 - shift;                              // bits of the digit
+    for (;;) {
+        __syncthreads();
+        for (int b = tid; b < kBins; b += kSelThreads)
+            sm.hist[b] = 0u;
+        __syncthreads();
+        const int up = shift + width;                         // 64: no bits above
+        each([&](uint64_t key) {
+            if ((up >= 64 ? 0ull : key >> up) == fixed)
+                atomicAdd(&sm.hist[(key >> shift) & ((1u << width) - 1u)], 1u);
+        });
+        __syncthreads();
+        // thread t's bins, from the top: kBins - 1 - PT t downwards
+        uint32_t c[PT], mine = 0, total;
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
+            c[i] = sm.hist[kBins - 1 - PT * tid - i];
+            mine += c[i];
+        }
+        uint32_t above = block_scan(mine, sm.warp_sum, total);
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
+            if ((int)above < need && need <= (int)(above + c[i])) {
+                sm.bin = kBins - 1 - PT * tid - i;
+                sm.above = (int)above;
+            }
+            above += c[i];
+        }
+        __syncthreads();
+        count = (int)sm.hist[sm.bin];
+        need -= sm.above;
+        prefix = (fixed << width) | (uint64_t)sm.bin;         // width <= 11 < 64
+        if (shift == 0 || count <= kGather || count == need)
+            return;
+        fixed = prefix;
+        width = min(11, shift);
+        shift -= width;
+    }
+}
+
+// The exact score of a page (16 bytes of its box to a lane), as an ordered key.
+template <int D>
+__device__ __forceinline__ uint64_t exact_key(const SelectParams& p, int page, int h, const uint64_t (&wa)[4],
+                                              const uint64_t (&wb)[4], int lane)
+{
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (lane < D / 4)
+        v = __ldg(reinterpret_cast<const uint4*>(p.summary + ((int64_t)page * p.H + h) * (2 * D)) + lane);
+    const uint64_t neg1 = ptx::f2_make(0xBF800000u, 0xBF800000u);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint64_t x = ptx::f2_from_bf16x2(w[0]);
+    uint64_t sum = ptx::f2_mul(wa[0], x), err = ptx::f2_mul(wb[0], x);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        x = ptx::f2_from_bf16x2(w[i]);
+        const uint64_t pr = ptx::f2_mul(wa[i], x);           // exact
+        const uint64_t t = ptx::f2_add(sum, pr);
+        const uint64_t z = ptx::f2_fma(sum, neg1, t);        // t - sum
+        const uint64_t tz = ptx::f2_fma(z, neg1, t);         // t - z
+        const uint64_t r = ptx::f2_add(ptx::f2_fma(tz, neg1, sum), ptx::f2_fma(z, neg1, pr));
+        err = ptx::f2_add(ptx::f2_fma(wb[i], x, err), r);
+        sum = t;
+    }
+    uint32_t s0, s1, e0, e1;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(s0), "=r"(s1) : "l"(sum));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(e0), "=r"(e1) : "l"(err));
+    float S = __uint_as_float(s0), E = __uint_as_float(e0);
+    pair_add(S, E, __uint_as_float(s1), __uint_as_float(e1));
+#pragma unroll
+    for (int dist = 16; dist >= 1; dist /= 2)
+        pair_add(S, E, __shfl_xor_sync(0xFFFFFFFFu, S, dist), __shfl_xor_sync(0xFFFFFFFFu, E, dist));
+    float t, r;
+    two_sum(S, E, t, r);   // t + r, t the sum rounded: (t, r) orders as the sum does
+    if (!(fabsf(t) <= 3.402823466e38f && r == r)) {
+        t = INFINITY;
+        r = 0.f;
+    }
+    return ((uint64_t)ordered(t) << 32) | ordered(r);
+}
+
+// One CTA per (sequence, KV head): the pages surely in by their fp32 scores, the
+// exact order of those near the border, and the pages in order from a bitmap.
+// Latency-bound: a handful of passes over 32-bit keys in shared memory.
+template <int D>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p)
 {
     extern __shared__ __align__(16) unsigned char sel_raw[];
-    __shared__ SelSmem sm;
+    __shared__ SelSmem<D> sm;
     const int words = (p.width + 31) >> 5;
     uint32_t* bm = reinterpret_cast<uint32_t*>(sel_raw);        // pages taken
-    uint32_t* beq = bm + words;                                 // pages whose key equals the last one taken
-    uint64_t* stage = reinterpret_cast<uint64_t*>(sel_raw + ((size_t)words * 8 + 15) / 16 * 16);
-    const int s = blockIdx.x / p.H, h = blockIdx.x - s * p.H, tid = threadIdx.x, lane = tid & 31;
+    uint32_t* band = bm + words;                                // pages near the border
+    uint32_t* key32 = band + words;
+    const int s = blockIdx.x / p.H, h = blockIdx.x - s * p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int lo, hi;
     const int n = page_range(p, s, lo, hi);
     int32_t* out = p.selected + (int64_t)blockIdx.x * p.k;
     if (h == 0 && tid == 0 && (p.lens[s] < 0 || p.lens[s] > p.max_len))
         raise_err(p.err, KAMERA_DEVERR_LEN);
     if (n <= p.k) {   // every page
+        ptx::grid_wait();
         for (int i = tid; i < p.k; i += kSelThreads)
             out[i] = i < n ? i : -1;
         return;
     }
-    const uint64_t* keys = p.keys + (int64_t)blockIdx.x * p.width;
-    int need = p.k - p.n_first - p.n_last;
-    uint64_t kmin = ~0ull, kmax = 0ull;
-    if (need > 0) {
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
-            const uint64_t key = keys[j];
-            if (STAGE)
-                stage[j] = key;
-            kmin = min(kmin, key);
-            kmax = max(kmax, key);
-        }
-#pragma unroll
-        for (int o = 16; o >= 1; o /= 2) {
-            kmin = min(kmin, __shfl_xor_sync(0xFFFFFFFFu, kmin, o));
-            kmax = max(kmax, __shfl_xor_sync(0xFFFFFFFFu, kmax, o));
-        }
-        if (lane == 0) {
-            sm.warp_min[tid >> 5] = kmin;
-            sm.warp_max[tid >> 5] = kmax;
-        }
+    for (int i = tid; i < 2 * D; i += kSelThreads) {
+        float a, e;
+        signed_sum<D>(p, s, h, i, a, e);
+        const float top = __uint_as_float(__float_as_uint(a) & 0xFFFFFF00u);   // 16 significant bits
+        sm.qa[i] = top;
+        sm.qb[i] = __fadd_rn(__fadd_rn(a, -top), e);
     }
-    for (int w = tid; w < words; w += kSelThreads)
-        bm[w] = beq[w] = 0u;
     if (tid == 0)
         sm.n_cand = 0;
-    __syncthreads();
-    const uint64_t* src = STAGE ? stage : keys;
-    // taken: keys whose top bits (>> shift) exceed `prefix`, and of those that
-    // equal it: all (mode 0), the listed ones (mode 1) or the lowest `need` pages (mode 2)
-    int mode = 0, shift = 0;
-    uint64_t prefix = ~0ull;
+    ptx::grid_wait();   // the scores
+    uint64_t* keys64 = p.keys + (int64_t)blockIdx.x * p.width;
+    const float2* scores = reinterpret_cast<const float2*>(keys64);
+    int need = p.k - p.n_first - p.n_last;
+    uint32_t in_above = 0xFFFFFFFFu, band_from = 1u;   // keys above the first are in, from the second on near; none yet
+    bool ties = false;                                 // the near ones are equal
     if (need > 0) {
-        for (int w = 0; w < kSelThreads / 32; ++w) {
-            kmin = min(kmin, sm.warp_min[w]);
-            kmax = max(kmax, sm.warp_max[w]);
+        uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
+        float err = 0.f;
+#pragma unroll 4
+        for (int j = lo + tid; j < hi; j += kSelThreads) {
+            const float2 x = scores[j];
+            const uint32_t key = x.y < 0.f ? 0u : x.x == INFINITY ? 0xFFFFFFFFu : ordered(x.x);
+            key32[j] = key;
+            kmin = min(kmin, key);
+            kmax = max(kmax, key);
+            err = fmaxf(err, x.y == x.y ? x.y : INFINITY);   // a batch with a NaN or an infinity: everything is near
         }
-        if (kmin == kmax) {
-            prefix = kmin;
-            mode = 2;
-        } else {
-            const int top = 63 - __clzll((long long)(kmin ^ kmax));   // the highest bit that differs
-            shift = max(0, top - 10);
-            uint64_t fixed = top == 63 ? 0ull : kmin >> (top + 1);    // bits above the digit, shared so far
-            int width = top + 1 - shift;                              // bits of the digit
-            for (;;) {
-                for (int b = tid; b < kBins; b += kSelThreads)
-                    sm.hist[b] = 0u;
-                __syncthreads();
-                const int up = shift + width;                         // 64: no bits above
-                for (int j = lo + tid; j < hi; j += kSelThreads) {
-                    const uint64_t key = src[j];
-                    if ((up >= 64 ? 0ull : key >> up) == fixed)
-                        atomicAdd(&sm.hist[(key >> shift) & ((1u << width) - 1u)], 1u);
-                }
-                __syncthreads();
-                // thread t's bins, from the top: kBins - 1 - 4 t downwards
-                uint32_t c[kBins / kSelThreads], mine = 0;
+        kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
+        kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
 #pragma unroll
-                for (int i = 0; i < kBins / kSelThreads; ++i) {
-                    c[i] = sm.hist[kBins - 1 - (kBins / kSelThreads) * tid - i];
-                    mine += c[i];
-                }
-                uint32_t total;
-                uint32_t above = block_scan(mine, sm.warp_sum, total);
-#pragma unroll
-                for (int i = 0; i < kBins / kSelThreads; ++i) {
-                    if ((int)above < need && need <= (int)(above + c[i])) {
-                        sm.bin = kBins - 1 - (kBins / kSelThreads) * tid - i;
-                        sm.above = (int)above;
+        for (int o = 16; o >= 1; o /= 2)
+            err = fmaxf(err, __shfl_xor_sync(0xFFFFFFFFu, err, o));
+        if (lane == 0) {
+            sm.warp_min[warp] = kmin;
+            sm.warp_max[warp] = kmax;
+            sm.warp_err[warp] = err;
+        }
+        __syncthreads();
+        for (int w = 0; w < kSelWarps; ++w) {
+            kmin = min(kmin, (uint32_t)sm.warp_min[w]);
+            kmax = max(kmax, (uint32_t)sm.warp_max[w]);
+            err = fmaxf(err, sm.warp_err[w]);
+        }
+        uint32_t T = kmin;
+        if (kmin != kmax) {
+            int left = need, shift, count;
+            uint64_t prefix;
+            radix_find(sm, (uint64_t)kmin, (uint64_t)kmax,
+                       [&](auto f) {
+                           for (int j = lo + tid; j < hi; j += kSelThreads)
+                               f((uint64_t)key32[j]);
+                       },
+                       left, shift, prefix, count);
+            if (shift == 0) {
+                T = (uint32_t)prefix;
+            } else {   // the left-th largest of the keys of one digit
+                const bool few = count <= kGather;
+                uint32_t least = 0xFFFFFFFFu;
+                for (int j = lo + tid; j < hi; j += kSelThreads)
+                    if (((uint64_t)key32[j] >> shift) == prefix) {
+                        if (few)
+                            sm.cand[atomicAdd(&sm.n_cand, 1)] = key32[j];
+                        else   // all of them are taken: the least
+                            least = min(least, key32[j]);
                     }
-                    above += c[i];
+                if (few) {
+                    __syncthreads();
+                    for (int i = tid; i < count; i += kSelThreads) {
+                        const uint64_t key = sm.cand[i];
+                        int more = 0, same = 0;
+                        for (int o = 0; o < count; ++o) {
+                            more += sm.cand[o] > key;
+                            same += sm.cand[o] == key;
+                        }
+                        if (more < left && left <= more + same)
+                            sm.found = key;
+                    }
+                } else {
+                    least = __reduce_min_sync(0xFFFFFFFFu, least);
+                    if (lane == 0)
+                        sm.warp_min[warp] = least;
+                    __syncthreads();
+                    if (tid == 0) {
+                        for (int w = 0; w < kSelWarps; ++w)
+                            least = min(least, (uint32_t)sm.warp_min[w]);
+                        sm.found = least;
+                    }
                 }
                 __syncthreads();
-                const int bin = sm.bin, count = (int)sm.hist[bin];
-                need -= sm.above;
-                prefix = (fixed << width) | (uint64_t)bin;            // width <= 11 < 64
-                if (count == need) {
-                    mode = 0;
-                    break;
-                }
-                if (shift == 0) {
-                    mode = 2;
-                    break;
-                }
-                if (count <= kGather) {
-                    mode = 1;
-                    break;
-                }
-                fixed = prefix;
-                width = min(11, shift);
-                shift -= width;
-                __syncthreads();   // the histogram is cleared next
+                T = (uint32_t)sm.found;
             }
+        }
+        if (T == 0u || T == 0xFFFFFFFFu) {   // unknown pages, or scores that are not finite: equal among themselves
+            in_above = T;
+            band_from = T;
+            ties = true;
+        } else {
+            const float t = __uint_as_float(T ^ ((uint32_t)((int32_t)~T >> 31) | 0x80000000u));   // ordered() undone
+            in_above = ordered(__fadd_ru(t, __fmul_ru(2.f, err)));
+            band_from = max(ordered(__fadd_rd(t, -__fmul_ru(2.f, err))), 1u);
+            in_above = min(in_above, 0xFFFFFFFEu);
         }
     }
     // the bitmaps: whole words, so every thread of a warp takes part
+    uint32_t n_in = 0, n_band = 0, total_in, total_band;
     for (int j = tid; j < words * 32; j += kSelThreads) {
-        bool take = j < n && (j < p.n_first || j >= n - p.n_last), eq = false;
-        uint64_t key = 0;
+        bool take = j < n && (j < p.n_first || j >= n - p.n_last), near = false;
         if (need > 0 && j >= lo && j < hi) {
-            key = src[j];
-            const uint64_t t = key >> shift;
-            take = t > prefix || (mode == 0 && t == prefix);
-            eq = mode != 0 && t == prefix;
+            const uint32_t key = key32[j];
+            take = key > in_above;
+            near = !take && key >= band_from;
+            n_in += take;
+            n_band += near;
         }
-        if (mode == 1 && eq) {
-            const int i = atomicAdd(&sm.n_cand, 1);
-            sm.cand[i] = key;
-            sm.cand_j[i] = j;
-        }
-        const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), b = __ballot_sync(0xFFFFFFFFu, eq);
+        const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), b = __ballot_sync(0xFFFFFFFFu, near);
         if (lane == 0) {
             bm[j >> 5] = a;
-            beq[j >> 5] = b;
+            band[j >> 5] = b;
         }
     }
-    __syncthreads();
-    if (mode == 1) {
-        const int m = sm.n_cand;
-        for (int i = tid; i < m; i += kSelThreads) {
-            const uint64_t key = sm.cand[i];
-            const int j = sm.cand_j[i];
-            int rank = 0;
-            for (int o = 0; o < m; ++o)
-                rank += sm.cand[o] > key || (sm.cand[o] == key && sm.cand_j[o] < j);
-            if (rank < need)
-                atomicOr(&bm[j >> 5], 1u << (j & 31));
+    (void)block_scan(n_in | n_band << 16, sm.warp_sum, total_in);   // each at most width < 2^16
+    total_band = total_in >> 16;
+    total_in &= 0xFFFFu;
+    int left = need - (int)total_in;   // of the near ones
+    bool lowest = ties;                // take the lowest pages of the (remaining) band
+    if (left > 0 && !ties && left < (int)total_band) {
+        uint64_t wa[4], wb[4];
+        const bool on = lane < D / 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            wa[i] = on ? *reinterpret_cast<const uint64_t*>(&sm.qa[8 * lane + 2 * i]) : 0ull;
+            wb[i] = on ? *reinterpret_cast<const uint64_t*>(&sm.qb[8 * lane + 2 * i]) : 0ull;
         }
-    } else if (mode == 2) {   // the lowest `need` of the equal ones
+        const int32_t* table = p.pages + (int64_t)s * p.max_pages;
+        const bool few = total_band <= (uint32_t)kGather;
+        if (few) {   // list the band
+            if (tid == 0)
+                sm.n_cand = 0;
+            __syncthreads();
+            for (int w = tid; w < words; w += kSelThreads)
+                for (uint32_t e = band[w]; e; e &= e - 1u)
+                    sm.cand_j[atomicAdd(&sm.n_cand, 1)] = 32 * w + __ffs((int)e) - 1;
+            __syncthreads();
+            for (int i = warp; i < (int)total_band; i += kSelWarps) {
+                const uint64_t key = exact_key<D>(p, table[sm.cand_j[i]], h, wa, wb, lane);
+                if (lane == 0)
+                    sm.cand[i] = key;
+            }
+            __syncthreads();
+            for (int i = tid; i < (int)total_band; i += kSelThreads) {
+                const uint64_t key = sm.cand[i];
+                const int j = sm.cand_j[i];
+                int rank = 0;
+                for (int o = 0; o < (int)total_band; ++o)
+                    rank += sm.cand[o] > key || (sm.cand[o] == key && sm.cand_j[o] < j);
+                if (rank < left)
+                    atomicOr(&bm[j >> 5], 1u << (j & 31));
+            }
+            left = 0;
+        } else {   // many equal or nearly equal scores: exact keys over the scores, then the same search
+            uint64_t kmin = ~0ull, kmax = 0ull;
+            for (int w = warp; w < words; w += kSelWarps)
+                for (uint32_t e = band[w]; e; e &= e - 1u) {
+                    const int j = 32 * w + __ffs((int)e) - 1;
+                    const uint64_t key = exact_key<D>(p, table[j], h, wa, wb, lane);
+                    if (lane == 0)
+                        keys64[j] = key;
+                    kmin = min(kmin, key);
+                    kmax = max(kmax, key);
+                }
+            if (lane == 0) {
+                sm.warp_min[warp] = kmin;
+                sm.warp_max[warp] = kmax;
+            }
+            __syncthreads();
+            for (int w = 0; w < kSelWarps; ++w) {
+                kmin = min(kmin, sm.warp_min[w]);
+                kmax = max(kmax, sm.warp_max[w]);
+            }
+            uint64_t prefix = kmin;
+            int shift = 0, count = 0;
+            auto each = [&](auto f) {
+                for (int j = tid; j < words * 32; j += kSelThreads)
+                    if ((band[j >> 5] >> (j & 31)) & 1u)
+                        f(keys64[j]);
+            };
+            if (kmin != kmax)
+                radix_find(sm, kmin, kmax, each, left, shift, prefix, count);
+            // what is above the digit is in; what shares it is the new band
+            __syncthreads();
+            if (tid == 0)
+                sm.n_cand = 0;
+            __syncthreads();
+            const bool rank_them = kmin != kmax && shift > 0 && count != left;
+            for (int j = tid; j < words * 32; j += kSelThreads) {
+                bool take = false, near = false;
+                if ((band[j >> 5] >> (j & 31)) & 1u) {
+                    const uint64_t key = keys64[j];
+                    take = (key >> shift) > prefix;
+                    near = (key >> shift) == prefix;
+                    if (near && rank_them) {
+                        const int i = atomicAdd(&sm.n_cand, 1);
+                        sm.cand[i] = key;
+                        sm.cand_j[i] = j;
+                    }
+                }
+                const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), b = __ballot_sync(0xFFFFFFFFu, near);
+                if (lane == 0) {
+                    bm[j >> 5] |= a;
+                    band[j >> 5] = b;
+                }
+            }
+            __syncthreads();
+            if (rank_them) {
+                for (int i = tid; i < count; i += kSelThreads) {
+                    const uint64_t key = sm.cand[i];
+                    const int j = sm.cand_j[i];
+                    int rank = 0;
+                    for (int o = 0; o < count; ++o)
+                        rank += sm.cand[o] > key || (sm.cand[o] == key && sm.cand_j[o] < j);
+                    if (rank < left)
+                        atomicOr(&bm[j >> 5], 1u << (j & 31));
+                }
+                left = 0;
+            } else {
+                lowest = true;
+            }
+        }
+    } else if (left > 0) {
+        lowest = true;   // all of them, or equal ones
+    }
+    __syncthreads();
+    if (left > 0 && lowest) {   // the lowest `left` pages of the band
         uint32_t run = 0;
         for (int w0 = 0; w0 < words; w0 += kSelThreads) {
             const int w = w0 + tid;
-            uint32_t e = w < words ? beq[w] : 0u, total;
-            const uint32_t before = run + block_scan((uint32_t)__popc(e), sm.warp_sum, total);
-            int left = need - (int)before;
-            uint32_t take = 0;
-            while (left > 0 && e) {
+            uint32_t e = w < words ? band[w] : 0u, total, take = 0;
+            int room = left - (int)(run + block_scan((uint32_t)__popc(e), sm.warp_sum, total));
+            for (; room > 0 && e; --room, e &= e - 1u)
                 take |= e & (0u - e);
-                e &= e - 1u;
-                --left;
-            }
             if (take)
                 bm[w] |= take;
             run += total;
         }
+        __syncthreads();
     }
-    __syncthreads();
     uint32_t run = 0;
     for (int w0 = 0; w0 < words; w0 += kSelThreads) {
         const int w = w0 + tid;
@@ -515,37 +776,41 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 }
 
 template <int D>
+cudaError_t launch_score(SelectParams& p, int scored, cudaStream_t stream)
+{
+    // about four CTAs a slot (three CTAs share an SM), so that ragged lengths even out,
+    // before a warp takes more batches
+    const int64_t units = (int64_t)p.n_seqs * p.H, step = kScoreWarps * kScorePages;
+    const int64_t batches = (scored + step - 1) / step;
+    p.sweeps = (int)std::max<int64_t>(1, std::min<int64_t>(16, units * batches / (456 * 4)));
+    const int64_t gx = (batches + p.sweeps - 1) / p.sweeps;
+    const cudaError_t a = cudaFuncSetAttribute(score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)ScoreLayout<D>::kBytes);
+    if (a != cudaSuccess)
+        return a;
+    score_kernel<D><<<dim3((unsigned)gx, (unsigned)units), 32 * kScoreWarps, ScoreLayout<D>::kBytes, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D>
 cudaError_t launch_select(SelectParams& p, cudaStream_t stream)
 {
-    constexpr int PB = kBatch * (32 / (D / 4));
     const int64_t units = (int64_t)p.n_seqs * p.H;
     const int scored = p.width - p.n_first - p.n_last;   // at most, of one sequence
+    bool after = false;
     if (p.width > p.k && scored > 0 && p.k > p.n_first + p.n_last) {
-        // enough CTAs for every SM's slots several times over before a warp takes
-        // a second batch
-        const int64_t batches = (scored + kScoreWarps * PB - 1) / (kScoreWarps * PB);
-        p.sweeps = (int)std::max<int64_t>(1, std::min<int64_t>(8, units * batches / (152 * 16)));
-        const int64_t gx = (batches + p.sweeps - 1) / p.sweeps;
-        score_kernel<D><<<dim3((unsigned)gx, (unsigned)units), 32 * kScoreWarps, 0, stream>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_score<D>(p, scored, stream);
         if (e != cudaSuccess)
             return e;
+        after = true;
     }
-    const size_t bits = ((size_t)((p.width + 31) / 32) * 8 + 15) / 16 * 16;
-    const bool stage = p.width <= kStage;
-    const size_t smem = bits + (stage ? (size_t)p.width * 8 : 0);
+    const size_t smem = (size_t)((p.width + 31) / 32) * 8 + (size_t)p.width * 4;
     // set at every launch: the attribute belongs to the current device's context
-    const cudaError_t e = stage ? cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (int)smem)
-                                : cudaFuncSetAttribute(select_kernel<false>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e =
+        cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    if (stage)
-        select_kernel<true><<<(unsigned)units, kSelThreads, smem, stream>>>(p);
-    else
-        select_kernel<false><<<(unsigned)units, kSelThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(select_kernel<D>, dim3((unsigned)units), kSelThreads, smem, stream, after, p);
 }
 
 int check_select(const KameraPageSelect* x, const KameraPageTable* t)
@@ -613,10 +878,10 @@ int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, c
     p.vecs = (int32_t)(W / 8);
     p.items = (int64_t)n * p.vecs;
     p.err = d_err;
-    const int64_t ctas = (p.items + 63) / 64;
+    const int64_t ctas = (p.items + 127) / 128;
     if (ctas > 0x7FFFFFFF)
         return KAMERA_ERR_UNSUPPORTED;
-    summary_kernel<<<(unsigned)ctas, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    summary_kernel<<<(unsigned)ctas, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
     return cudaGetLastError() == cudaSuccess ? KAMERA_OK : KAMERA_ERR_CUDA;
 }
 
