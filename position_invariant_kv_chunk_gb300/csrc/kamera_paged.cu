@@ -121,6 +121,10 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
         raise_err(p.err, KAMERA_DEVERR_LEN);
     const int n_pieces = p.selected ? p.n_select * ppp : (len + kPgTok - 1) / kPgTok;
     const int i1 = min(n_pieces, i0 + p.own_split);
+    // The prefix kernel may still run beside this one, and the merge that follows
+    // waits for this grid alone: its last CTA stays until the prefix is done.
+    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+        ptx::grid_wait();
     if (i0 >= i1 && (p.slots > 1 || split > 0))
         return;   // the merge knows that this slot is empty
     if (threadIdx.x < kPgWarps * NS)
@@ -652,7 +656,7 @@ int plan(const KameraPagedKV* kv, const KameraPagedQuery* q, const KameraPrefixG
 }
 
 template <int D, int NT>
-cudaError_t launch_own(const PagedLaunch& L, cudaStream_t stream)
+cudaError_t launch_own(const PagedLaunch& L, bool dependent, cudaStream_t stream)
 {
     using Y = PgLayout<D, NT>;
     static_assert(Y::kBytes <= 227 * 1024, "shared memory");
@@ -662,8 +666,7 @@ cudaError_t launch_own(const PagedLaunch& L, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     const dim3 grid((unsigned)std::max(L.p.own_slots, 1), (unsigned)(L.p.n_seqs * L.p.H));
-    paged_kernel<D, NT><<<grid, kPgThreads, Y::kBytes, stream>>>(L);
-    return cudaGetLastError();
+    return launch_after(paged_kernel<D, NT>, grid, kPgThreads, Y::kBytes, stream, dependent, L);
 }
 
 // The pointers both entry points share, then the launches.
@@ -746,25 +749,9 @@ int attend(PagedParams& p, const KameraPagedKV* kv, const KameraPagedQuery* q, c
     const int64_t map_rows = kv->num_slots > 0 ? kv->num_slots : 1;
     PagedLaunch L;
     std::memset(&L, 0, sizeof(L));
-    // The own pages' kernel first; the prefix kernel needs nothing of it and starts
-    // on the SMs that it leaves free; the merge's CTAs read the call's inputs and
-    // wait for both.
-    const bool own_runs = p.own_slots > 0 || p.slots == 0;
-    if (own_runs) {   // without any token to read the one CTA of a unit writes the empty output
-        if (p.slots == 0)
-            p.slots = 1;
-        L.p = p;
-        cudaError_t e = cudaErrorInvalidValue;
-        if (make_rows_map(&L.map_k, kv->k, map_rows, W, kv->slot_stride, 64, kPgTok) &&
-            make_rows_map(&L.map_v, kv->v, map_rows, W, kv->slot_stride, 64, kPgTok)) {
-            if (p.d == 128)
-                e = p.G <= 8 ? launch_own<128, 1>(L, stream) : launch_own<128, 2>(L, stream);
-            else
-                e = p.G <= 8 ? launch_own<64, 1>(L, stream) : launch_own<64, 2>(L, stream);
-        }
-        if (e != cudaSuccess)
-            return KAMERA_ERR_CUDA;
-    }
+    // The prefix kernel first, a CTA to an SM; the own pages' kernel needs nothing
+    // of it and starts at once, on the SMs that it leaves free and as they fall
+    // free; the merge's CTAs read the call's inputs and wait for both.
     if (p.n_groups > 0) {
         const int r = box_rows(p.P, 128);
         L.p = p;
@@ -774,7 +761,23 @@ int attend(PagedParams& p, const KameraPagedKV* kv, const KameraPagedQuery* q, c
         const int64_t groups = std::max<int64_t>(map_rows, 8);   // a pool without a whole page has none to read
         if (!make_groups_map(&L.map_k, kv->k, groups, W, kv->slot_stride, p.d / 64, r / 8) ||
             !make_groups_map(&L.map_v, kv->v, groups, W, kv->slot_stride, p.d / 64, r / 8) ||
-            launch_prefix(L, own_runs, stream) != cudaSuccess)
+            launch_prefix(L, stream) != cudaSuccess)
+            return KAMERA_ERR_CUDA;
+    }
+    if (p.own_slots > 0 || p.slots == 0) {   // without any token to read the one CTA of a unit writes the empty output
+        if (p.slots == 0)
+            p.slots = 1;
+        L.p = p;
+        const bool after = p.n_groups > 0;
+        cudaError_t e = cudaErrorInvalidValue;
+        if (make_rows_map(&L.map_k, kv->k, map_rows, W, kv->slot_stride, 64, kPgTok) &&
+            make_rows_map(&L.map_v, kv->v, map_rows, W, kv->slot_stride, 64, kPgTok)) {
+            if (p.d == 128)
+                e = p.G <= 8 ? launch_own<128, 1>(L, after, stream) : launch_own<128, 2>(L, after, stream);
+            else
+                e = p.G <= 8 ? launch_own<64, 1>(L, after, stream) : launch_own<64, 2>(L, after, stream);
+        }
+        if (e != cudaSuccess)
             return KAMERA_ERR_CUDA;
     }
     if (need > 0) {

@@ -80,6 +80,6 @@ __device__ __forceinline__ bool group_range(const PagedParams& p, int g, int& s0
     return s0 >= 0 && s1 >= s0 && s1 <= p.n_seqs && s1 - s0 <= p.max_group;
 }
 
-cudaError_t launch_prefix(const PagedLaunch& L, bool dependent, cudaStream_t stream);
+cudaError_t launch_prefix(const PagedLaunch& L, cudaStream_t stream);
 
 }  // namespace kamera

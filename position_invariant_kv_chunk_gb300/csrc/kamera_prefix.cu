@@ -556,10 +556,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         if (p.prefix_lens[w.group] != len)
             raise_err(p.err, KAMERA_DEVERR_LEN);
     }
-    if (w.tiles_a == 0) {   // no rows, or no tokens: nothing for either side
-        ptx::grid_wait();   // (as below)
+    if (w.tiles_a == 0)   // no rows, or no tokens: nothing for either side
         return;
-    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kPxBuf; ++i) {
             ptx::mbar_init(ptx::smem_addr(&b.full[i]), 1);
@@ -605,9 +603,6 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             px_producer<D, true>(L, w, b, sbase + Y::kRing, lane);
         else if (warp == kPxMma && elect_one())
             px_mma<D>(L, w, b, sbase);
-        else if (warp > kPxMma)
-            ptx::grid_wait();   // the own pages' kernel may still run beside this one; the merge that
-                                // follows waits for this grid alone, so this grid ends after that one
     }
 
     ptx::tc_fence_before();
@@ -619,7 +614,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
 }
 
 template <int D>
-cudaError_t launch_prefix_d(const PagedLaunch& L, bool dependent, cudaStream_t stream)
+cudaError_t launch_prefix_d(const PagedLaunch& L, cudaStream_t stream)
 {
     using Y = PxLayout<D>;
     // set at every launch: the attribute belongs to the current device's context
@@ -628,14 +623,15 @@ cudaError_t launch_prefix_d(const PagedLaunch& L, bool dependent, cudaStream_t s
     if (e != cudaSuccess)
         return e;
     const unsigned ctas = (unsigned)L.p.n_groups * L.p.H * L.p.row_blocks * L.p.prefix_splits;
-    return launch_after(prefix_kernel<D>, dim3(ctas), kPxThreads, Y::kBytes, stream, dependent, L);
+    prefix_kernel<D><<<ctas, kPxThreads, Y::kBytes, stream>>>(L);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_prefix(const PagedLaunch& L, bool dependent, cudaStream_t stream)
+cudaError_t launch_prefix(const PagedLaunch& L, cudaStream_t stream)
 {
-    return L.p.d == 128 ? launch_prefix_d<128>(L, dependent, stream) : launch_prefix_d<64>(L, dependent, stream);
+    return L.p.d == 128 ? launch_prefix_d<128>(L, stream) : launch_prefix_d<64>(L, stream);
 }
 
 }  // namespace kamera
