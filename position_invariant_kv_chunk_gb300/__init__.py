@@ -11,8 +11,8 @@ without the compiled library (or without a GPU) every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
+import importlib.util
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -798,126 +798,26 @@ def kamera_mla_attend_reused(store: torch.Tensor, kv_lora: int, q: torch.Tensor,
 
 
 # ------------------------------------------------ decode steps over the pool --
-# A decode step's kernels take a few microseconds, so what these wrappers do per
-# call is kept short: device indices instead of device objects, no call that
-# only repeats a check, and one allocation per array.
-_BF16, _I32, _I64, _F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
-_NOTHING = contextlib.nullcontext()
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# These go through csrc/kamera_binding.cpp, which checks the tensors, allocates
+# outputs and workspaces on the call's stream and calls the C entry points: a
+# decode step's kernels take a few microseconds, less than ctypes marshalling.
+_FAST = None
 
 
-def _wrong_place(where, names, tensors):
-    dev = tensors[0].device
-    for name, t in zip(names.split(), tensors):
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{where}: {name} must be a CUDA tensor")
-        if t.device != dev:
-            raise ValueError(f"{where}: {name} is on {t.device}, not on {dev}")
-
-
-def _place(where: str, names: str, *tensors) -> int:
-    """The device index that every tensor lives on (-1: host memory, where no CUDA
-    is present; ``_on_device`` says why)."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            _wrong_place(where, names, tensors)
-    if dev < 0 and torch.cuda.is_available():
-        _wrong_place(where, names, tensors)
-    return dev
-
-
-def _current(dev: int):
-    """A context in which device ``dev`` is the current one."""
-    return _NOTHING if dev < 0 or dev == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _on_stream(dev: int, stream):
-    """(handle of the call's stream, that stream where it is not the current one)."""
-    if dev < 0:
-        return 0, None
-    here = _raw_stream(dev) if _raw_stream is not None else int(torch.cuda.current_stream().cuda_stream)
-    if stream is None:
-        return here, None
-    handle = _stream_handle(stream)
-    if handle == here:
-        return handle, None
-    return handle, (stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle))
-
-
-def _new(ref: torch.Tensor, shape, dtype, side):
-    """Memory on ref's device that is safe on the call's stream: with another stream
-    than the current one (``side``) it comes from that stream's pool -- a block of
-    the current stream's could still be in use there -- and is marked as used on
-    the current one, where the caller reads it.  Nothing is kept between calls,
-    so a captured graph owns its workspace."""
-    if side is None:
-        return torch.empty(shape, dtype=dtype, device=ref.device)
-    here = torch.cuda.current_stream()
-    with torch.cuda.stream(side):
-        t = torch.empty(shape, dtype=dtype, device=ref.device)
-    t.record_stream(here)
-    return t
-
-
-def _scratch(ref, workspace, need: int, side):
-    """(tensor to keep until the launch, address, bytes): the caller's, or one of `need` bytes."""
-    if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if need == 0:
-        return None, None, 0
-    t = _new(ref, need, torch.uint8, side)
-    return t, t.data_ptr(), need
-
-
-def _ints(t: torch.Tensor, name: str, shape, dtype=_I32):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-
-
-def _append(where, call, pool, rope, rows_k, rows_v, q, q_out, positions, slots, layer, T, err, stream, names, *pools):
-    """The arguments both append entry points share, and the call."""
-    _ints(slots, "slots", (T,), _I64)
-    axes = rope.axis_delta
-    if axes is not None:
-        if positions is not None:
-            raise ValueError("with rope.axis_delta the positions are its rows; positions must be None")
-        if axes.dim() != 2 or axes.shape[0] != T or not axes.is_contiguous():
-            raise ValueError("rope.axis_delta must be a contiguous [T, n_axes] tensor of positions")
-    elif positions is None:
-        raise ValueError("positions are needed")
-    else:
-        _ints(positions, "positions", (T,), _I64)
-    if q_out is not None and q is None:
-        raise ValueError("q_out without q")
-    if err is not None and (err.dtype != _I32 or err.numel() < 1):
-        raise ValueError("err must be an int32 tensor")
-    dev = _place(where, "k v q q_out positions slots err axis_delta " + names, rows_k, rows_v, q, q_out, positions,
-                 slots, err, axes, *pools)
-    with _current(dev):
-        handle, side = _on_stream(dev, stream)
-        hq, qs, qh, os, oh = 0, 0, 0, 0, 0
-        if q is not None:
-            if q_out is None:
-                q_out = _new(q, q.shape, _BF16, side)
-            if (q.dtype != _BF16 or q_out.dtype != _BF16 or q_out.shape != q.shape
-                    or (q.shape[2] > 0 and (q.stride(2) != 1 or q_out.stride(2) != 1))):
-                raise ValueError("q and q_out must be bf16 [T, H_q, width] with packed rows")
-            hq = q.shape[1]
-            qs, qh, _ = q.stride()
-            os, oh, _ = q_out.stride()
-        rows = _AppendRows(rows_k.data_ptr(), rows_v.data_ptr(), _addr(q), _addr(q_out), rows_k.stride(0),
-                           rows_v.stride(0), qs, qh, os, oh, _addr(positions), slots.data_ptr(), T, hq, int(layer), 0)
-        r, keep = rope._c(T)
-        rc = call(C.byref(pool), C.byref(rows), C.byref(r), _addr(err), handle)
-    del keep
-    if rc:
-        raise KameraError(rc, where)
-    return q_out
+def _fast():
+    global _FAST
+    if _FAST is None:
+        load_library()
+        spec = importlib.util.spec_from_file_location("_kamera_binding", _build.BINDING_PATH)
+        if spec is None or not os.path.exists(_build.BINDING_PATH):
+            raise RuntimeError(f"Kamera binding not found at {_build.BINDING_PATH}; run build()")
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        if mod.abi_version() != ABI_VERSION:
+            raise RuntimeError(f"{_build.BINDING_PATH} implements Kamera ABI {mod.abi_version()}, these bindings "
+                               f"expect {ABI_VERSION}; rebuild it with build()")
+        _FAST = mod
+    return _FAST
 
 
 def kamera_append_kv(pool_k: torch.Tensor, pool_v: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rope: Rope,
@@ -934,25 +834,7 @@ def kamera_append_kv(pool_k: torch.Tensor, pool_v: torch.Tensor, k: torch.Tensor
     when None; may be q itself); positions, slots: int64 ``[T]``, slot -1 a
     padding row.  Multi-axis RoPE: positions None, ``rope.axis_delta`` int64
     ``[T, n_axes]``.  Returns ``q_out`` (None without q)."""
-    for t, nm in ((pool_k, "pool_k"), (pool_v, "pool_v"), (k, "k"), (v, "v")):
-        if t.dtype != _BF16:
-            _bf16(t, nm)
-    if pool_k.dim() != 4:
-        raise ValueError("pool_k must be [L, S, H, d] with packed heads")
-    (L, S, H, d), strides = pool_k.shape, pool_k.stride()
-    if strides[3] != 1 or strides[2] != d:
-        raise ValueError("pool_k must be [L, S, H, d] with packed heads")
-    if pool_v.stride() != strides or pool_v.shape != pool_k.shape:
-        raise ValueError("pool_k and pool_v must share shape and strides")
-    T = k.shape[0]
-    for t, nm in ((k, "k"), (v, "v")):
-        if t.shape != (T, H, d) or t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
-            raise ValueError(f"{nm} must be [T, {H}, {d}] with packed heads")
-    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != d):
-        raise ValueError("k, v and q must hold the same tokens and head width")
-    pool = _GqaPool(L, H, d, 0, pool_k.data_ptr(), pool_v.data_ptr(), S, strides[0], strides[1])
-    return _append("kamera_append_kv", load_library().kamera_append_kv, pool, rope, k, v, q, q_out, positions, slots,
-                   layer, T, err, stream, "pool_k pool_v", pool_k, pool_v)
+    return (_FAST or _fast()).append_kv(pool_k, pool_v, k, v, rope, positions, slots, layer, q, q_out, err, stream)
 
 
 def kamera_mla_append_kv(pool: torch.Tensor, kv_lora: int, c: torch.Tensor, k_rope: torch.Tensor, rope: Rope,
@@ -967,67 +849,8 @@ def kamera_mla_append_kv(pool: torch.Tensor, kv_lora: int, c: torch.Tensor, k_ro
     the queries, bf16 ``[T, H_q, rope_dim]`` (any token and head strides, e.g. a
     view of the full query heads); q_out likewise, e.g. the rope columns of the
     absorbed queries; the rest as for ``kamera_append_kv``."""
-    for t, nm in ((pool, "pool"), (c, "c"), (k_rope, "k_rope")):
-        if t.dtype != _BF16:
-            _bf16(t, nm)
-    if pool.dim() != 3 or pool.stride(2) != 1:
-        raise ValueError("pool must be [L, S, kv_lora + rope_dim] with packed rows")
-    L, S, W = pool.shape
-    lora, rd, T = int(kv_lora), W - int(kv_lora), c.shape[0]
-    for t, nm, w in ((c, "c", lora), (k_rope, "k_rope", rd)):
-        if t.shape != (T, w) or (w > 1 and t.stride(1) != 1):
-            raise ValueError(f"{nm} must be [T, {w}] with packed rows")
-    if q is not None and (q.dim() != 3 or q.shape[0] != T or q.shape[2] != rd):
-        raise ValueError("c, k_rope and q must hold the same tokens and rope width")
-    p = _MlaPool(L, lora, rd, 0, pool.data_ptr(), S, pool.stride(0), pool.stride(1))
-    return _append("kamera_mla_append_kv", load_library().kamera_mla_append_kv, p, rope, k_rope, c, q, q_out, positions,
-                   slots, layer, T, err, stream, "pool", pool)
-
-
-def _paged_kv(pool_k, pool_v, page_size):
-    if pool_k.dtype != _BF16 or pool_k.dim() != 3:
-        raise ValueError("pool_k must be bf16 [S, H, d] (one layer) with packed heads")
-    (S, H, d), strides = pool_k.shape, pool_k.stride()
-    if strides[2] != 1 or strides[1] != d:
-        raise ValueError("pool_k must be bf16 [S, H, d] (one layer) with packed heads")
-    if pool_v is None:
-        return _PagedKV(pool_k.data_ptr(), None, S, strides[0], H, d, int(page_size), 0), H, d
-    if pool_v.dtype != _BF16 or pool_v.shape != pool_k.shape or pool_v.stride() != strides:
-        raise ValueError("pool_k and pool_v must share type, shape and strides")
-    return _PagedKV(pool_k.data_ptr(), pool_v.data_ptr(), S, strides[0], H, d, int(page_size), 0), H, d
-
-
-def _paged_query(q, d, scale, out, lse, side):
-    """The outputs and the query struct; out and lse allocated where they are None."""
-    n, hq, _ = q.shape
-    if out is None:
-        out = _new(q, q.shape, _BF16, side)
-    elif out.shape != q.shape or out.dtype != _BF16 or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bf16 tensor shaped like q")
-    if lse is None:
-        lse = _new(q, (n, hq), _F32, side)
-    elif lse is False:
-        lse = None
-    elif lse.shape != (n, hq) or lse.dtype != _F32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous fp32 [S, H_q] tensor")
-    return out, lse, _PagedQuery(q.data_ptr(), out.data_ptr(), _addr(lse), n, hq,
-                                 d ** -0.5 if scale is None else float(scale), 0)
-
-
-def _paged_q(q, d):
-    if q.dtype != _BF16 or q.dim() != 3 or q.shape[2] != d or not q.is_contiguous():
-        raise ValueError("q must be a contiguous bf16 [S, H_q, d] tensor")
-
-
-def _table(pages, lens, n, max_len):
-    if pages is None and lens is None and int(max_len) == 0:
-        return _PageTable(None, None, 0, 0)
-    if pages is None or lens is None or pages.dim() != 2:
-        raise ValueError("pages must be [S, max_pages] and lens [S]")
-    width = pages.shape[1]
-    _ints(pages, "pages", (n, width))
-    _ints(lens, "lens", (n,))
-    return _PageTable(pages.data_ptr(), lens.data_ptr(), width, int(max_len))
+    return (_FAST or _fast()).mla_append_kv(pool, kv_lora, c, k_rope, rope, positions, slots, layer, q, q_out, err,
+                                            stream)
 
 
 def kamera_attend_shared(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.Tensor, page_size: int,
@@ -1045,39 +868,12 @@ def kamera_attend_shared(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.Te
     prefix_len int32 ``[n_groups]`` (all three None: no shared prefix); pages int32
     ``[S, width]``, lens int32 ``[S]``: the sequences' own tokens (None with max_len
     0); max_group, max_prefix, max_len: bounds of the group sizes and lengths;
-    lse: None (allocated), False (not computed) or fp32 ``[S, H_q]``; workspace:
-    None (allocated for the call) or a tensor of at least
+    scale: default 1/sqrt(d); lse: None (allocated), False (not computed) or fp32
+    ``[S, H_q]``; workspace: None (allocated for the call) or a tensor of at least
     ``kamera_attend_shared_workspace_bytes`` bytes.  Returns ``(out, lse)``."""
-    kv, _, d = _paged_kv(pool_k, pool_v, page_size)
-    _paged_q(q, d)
-    own = C.byref(_table(pages, lens, q.shape[0], max_len))
-    pre = None
-    if group_start is not None:
-        if prefix_pages is None or prefix_len is None or prefix_pages.dim() != 2:
-            raise ValueError("group_start, prefix_pages and prefix_len go together")
-        groups, width = prefix_pages.shape
-        _ints(group_start, "group_start", (groups + 1,))
-        _ints(prefix_pages, "prefix_pages", (groups, width))
-        _ints(prefix_len, "prefix_len", (groups,))
-        pre = C.byref(_PrefixGroups(group_start.data_ptr(), prefix_pages.data_ptr(), prefix_len.data_ptr(), groups,
-                                    width, int(max_prefix), int(max_group)))
-    elif prefix_pages is not None or prefix_len is not None:
-        raise ValueError("group_start, prefix_pages and prefix_len go together")
-    dev = _place("kamera_attend_shared", "q pool_k pool_v group_start prefix_pages prefix_len pages lens out err "
-                 "workspace lse", q, pool_k, pool_v, group_start, prefix_pages, prefix_len, pages, lens, out, err,
-                 workspace, lse if isinstance(lse, torch.Tensor) else None)
-    lib = load_library()
-    with _current(dev):
-        handle, side = _on_stream(dev, stream)
-        out, lse, qq = _paged_query(q, d, scale, out, lse, side)
-        kv, qq = C.byref(kv), C.byref(qq)
-        need = lib.kamera_attend_shared_workspace_bytes(kv, qq, pre, own) if workspace is None else 0
-        keep, ws, ws_bytes = _scratch(q, workspace, need, side)
-        rc = lib.kamera_attend_shared(kv, qq, pre, own, ws, ws_bytes, _addr(err), handle)
-    del keep
-    if rc:
-        raise KameraError(rc, "kamera_attend_shared")
-    return out, lse
+    return (_FAST or _fast()).attend_shared(pool_k, pool_v, q, page_size, group_start, prefix_pages, prefix_len, pages,
+                                            lens, max_group, max_prefix, max_len, scale, out, lse, err, stream,
+                                            workspace)
 
 
 def kamera_summarize_pages(pool_k: torch.Tensor, page_size: int, page_ids: torch.Tensor, page_tokens: torch.Tensor,
@@ -1087,21 +883,7 @@ def kamera_summarize_pages(pool_k: torch.Tensor, page_size: int, page_ids: torch
     page_tokens: int32 ``[n]``, the pages and how many of their first tokens
     count; summary: bf16 ``[S_slots // page_size, H, 2, d]``, those pages' entries
     written.  Returns ``summary``."""
-    kv, H, d = _paged_kv(pool_k, None, page_size)
-    if (summary.dtype != _BF16 or int(page_size) < 1 or not summary.is_contiguous()
-            or summary.shape != (pool_k.shape[0] // int(page_size), H, 2, d)):
-        raise ValueError("summary must be a contiguous bf16 [S_slots // page_size, H, 2, d] tensor")
-    n = page_ids.numel()
-    _ints(page_ids, "page_ids", (n,))
-    _ints(page_tokens, "page_tokens", (n,))
-    dev = _place("kamera_summarize_pages", "pool_k page_ids page_tokens summary err", pool_k, page_ids, page_tokens,
-                 summary, err)
-    with _current(dev):
-        rc = load_library().kamera_summarize_pages(C.byref(kv), page_ids.data_ptr(), page_tokens.data_ptr(), n,
-                                                   summary.data_ptr(), _addr(err), _on_stream(dev, stream)[0])
-    if rc:
-        raise KameraError(rc, "kamera_summarize_pages")
-    return summary
+    return (_FAST or _fast()).summarize_pages(pool_k, page_size, page_ids, page_tokens, summary, err, stream)
 
 
 def kamera_select_pages(q: torch.Tensor, summary: torch.Tensor, page_size: int, pages: torch.Tensor,
@@ -1116,31 +898,8 @@ def kamera_select_pages(q: torch.Tensor, summary: torch.Tensor, page_size: int, 
     (``kamera_summarize_pages``); pages int32 ``[S, width]``, lens int32 ``[S]``.
     Returns ``selected``: int32 ``[S, H, n_select]``, ascending indices into the
     sequence's page table row, then -1."""
-    if summary.dtype != _BF16 or summary.dim() != 4 or summary.shape[2] != 2 or not summary.is_contiguous():
-        raise ValueError("summary must be a contiguous bf16 [n_pages, H, 2, d] tensor")
-    N, H, _, d = summary.shape
-    _paged_q(q, d)
-    n, hq, _ = q.shape
-    k = int(n_select)
-    table = C.byref(_table(pages, lens, n, max_len))
-    dev = _place("kamera_select_pages", "q summary pages lens selected err workspace", q, summary, pages, lens,
-                 selected, err, workspace)
-    lib = load_library()
-    with _current(dev):
-        handle, side = _on_stream(dev, stream)
-        if selected is None:
-            selected = _new(q, (n, H, max(k, 0)), _I32, side)
-        else:
-            _ints(selected, "selected", (n, H, k))
-        x = C.byref(_PageSelect(q.data_ptr(), summary.data_ptr(), selected.data_ptr(), N, n, hq, H, d, int(page_size),
-                                k, int(n_first), int(n_last)))
-        need = lib.kamera_select_pages_workspace_bytes(x, table) if workspace is None else 0
-        keep, ws, ws_bytes = _scratch(q, workspace, need, side)
-        rc = lib.kamera_select_pages(x, table, ws, ws_bytes, _addr(err), handle)
-    del keep
-    if rc:
-        raise KameraError(rc, "kamera_select_pages")
-    return selected
+    return (_FAST or _fast()).select_pages(q, summary, page_size, pages, lens, max_len, n_select, n_first, n_last,
+                                           selected, err, stream, workspace)
 
 
 def kamera_attend_selected(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.Tensor, page_size: int,
@@ -1152,25 +911,5 @@ def kamera_attend_selected(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.
     (``kamera_attend_selected`` in kamera.h).  selected: int32 ``[S, H, k]`` as
     ``kamera_select_pages`` returns it (distinct; negative entries skipped); the
     rest as for ``kamera_attend_shared``.  Returns ``(out, lse)``."""
-    kv, H, d = _paged_kv(pool_k, pool_v, page_size)
-    _paged_q(q, d)
-    n = q.shape[0]
-    table = C.byref(_table(pages, lens, n, max_len))
-    if selected.dim() != 3:
-        raise ValueError("selected must be [S, H, k]")
-    k = selected.shape[2]
-    _ints(selected, "selected", (n, H, k))
-    dev = _place("kamera_attend_selected", "q pool_k pool_v pages lens selected out err workspace lse", q, pool_k,
-                 pool_v, pages, lens, selected, out, err, workspace, lse if isinstance(lse, torch.Tensor) else None)
-    lib = load_library()
-    with _current(dev):
-        handle, side = _on_stream(dev, stream)
-        out, lse, qq = _paged_query(q, d, scale, out, lse, side)
-        kv, qq = C.byref(kv), C.byref(qq)
-        need = lib.kamera_attend_selected_workspace_bytes(kv, qq, table, k) if workspace is None else 0
-        keep, ws, ws_bytes = _scratch(q, workspace, need, side)
-        rc = lib.kamera_attend_selected(kv, qq, table, selected.data_ptr(), k, ws, ws_bytes, _addr(err), handle)
-    del keep
-    if rc:
-        raise KameraError(rc, "kamera_attend_selected")
-    return out, lse
+    return (_FAST or _fast()).attend_selected(pool_k, pool_v, q, page_size, pages, lens, selected, max_len, scale, out,
+                                              lse, err, stream, workspace)

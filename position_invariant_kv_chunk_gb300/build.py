@@ -2,8 +2,10 @@
 
 ``build()`` compiles every ``csrc/*.cu`` translation unit in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and links them into
-``_build/libkamera.so``.  Rebuilds only when a source or header is newer than
-the library.
+``_build/libkamera.so``, and, against the installed torch's headers, the Python
+binding of the decode-step entry points (``csrc/kamera_binding.cpp`` ->
+``_build/_kamera_binding.so``).  Rebuilds only when a source or header is newer
+than its library.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libkamera.so")
+BINDING_SRC = os.path.join(CSRC, "kamera_binding.cpp")
+BINDING_PATH = os.path.join(BUILD_DIR, "_kamera_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -45,10 +50,68 @@ def _stale(out: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_version() -> str:
+    import torch
+    return torch.__version__
+
+
+def _binding_stale() -> bool:
+    """Older than its source or the header, or built against another torch."""
+    stamp = BINDING_PATH + ".torch"
+    if not os.path.exists(BINDING_PATH) or not os.path.exists(stamp):
+        return True
+    t = os.path.getmtime(BINDING_PATH)
+    if any(os.path.getmtime(d) > t for d in (BINDING_SRC, os.path.join(INCLUDE, "kamera.h"), os.path.abspath(__file__))):
+        return True
+    with open(stamp) as f:
+        return f.read() != _torch_version()
+
+
+def _compile_binding() -> str:
+    """The binding's object file (needs nothing of libkamera.so but the header)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD_DIR, "kamera_binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"), "-isystem",
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), "-isystem", cuda, "-isystem",
+           sysconfig.get_paths()["include"], "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(BINDING_SRC)}:\n{r.stderr[-4000:]}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_PATH + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", BUILD_DIR, "-lkamera", "-L", libs,
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stderr[-4000:]}")
+    os.replace(tmp, BINDING_PATH)
+    with open(BINDING_PATH + ".torch", "w") as f:
+        f.write(_torch_version())
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and not _stale(LIB_PATH):
+    lib, binding = force or _stale(LIB_PATH), force or _binding_stale()
+    if not lib and not binding:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:   # the binding compiles beside the library
+        obj = ex.submit(_compile_binding) if binding else None
+        if lib:
+            _build_library(verbose, extra_flags)
+        if obj is not None:
+            _link_binding(obj.result())
+    return LIB_PATH
+
+
+def _build_library(verbose: bool, extra_flags) -> str:
     cc = nvcc()
 
     def compile_one(src):
