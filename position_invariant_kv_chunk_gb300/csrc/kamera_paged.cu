@@ -16,9 +16,12 @@
 //     fragments to the B operand through 8 x 8 transposes in registers.
 //   - Softmax weights are not bf16 values: they enter as hi + lo pairs (about 16
 //     significant bits), which costs MMAs the tensor pipe has spare.
-//   - Few rows: the tokens of a (sequence, KV head) are split over CTAs, each
-//     leaving a partial state; the merge joins them with the shared prefix's.
+//   - Few rows: the tokens of a (sequence, KV head) are split over CTAs.  Without a
+//     shared prefix up to eight of them form a cluster and join their states in
+//     shared memory; else each leaves a partial state in the workspace, and the
+//     merge joins them with the prefix's.
 #include <algorithm>
+#include <cooperative_groups.h>
 #include <cstdint>
 #include <cstring>
 
@@ -53,7 +56,7 @@ struct PgLayout {
     static constexpr uint32_t kRing = kPgWarps * kWarp;
     static constexpr uint32_t kOut = kPgWarps * 8 * NT * (D + 4) * 4;   // warps' outputs (rows padded)
     static constexpr uint32_t kState = kRing > kOut ? kRing : kOut;
-    static constexpr uint32_t kBytes = kState + 2 * kPgWarps * 8 * NT * 4 + kPgWarps * NS * 8 + 64 + 1024;
+    static constexpr uint32_t kBytes = kState + 2 * (kPgWarps + 1) * 8 * NT * 4 + kPgWarps * NS * 8 + 64 + 1024;
 };
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
@@ -83,7 +86,9 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     float* outs = reinterpret_cast<float*>(base);                              // [warp][head][D + 4] at the end
     float* wm = reinterpret_cast<float*>(base + Y::kState);                    // [warp][8 NT]
     float* wl = wm + kPgWarps * 8 * NT;
-    uint64_t* full = reinterpret_cast<uint64_t*>(wl + kPgWarps * 8 * NT);      // [warp][NS]
+    float* cm = wl + kPgWarps * 8 * NT;                                        // [8 NT]: the CTA's state
+    float* cl = cm + 8 * NT;
+    uint64_t* full = reinterpret_cast<uint64_t*>(cl + 8 * NT);                 // [warp][NS]
     volatile int32_t* abort = reinterpret_cast<volatile int32_t*>(full + kPgWarps * NS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
     const int seq = blockIdx.y / p.H, h = blockIdx.y - seq * p.H, split = blockIdx.x;
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     // waits for this grid alone: its last CTA stays until the prefix is done.
     if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
         ptx::grid_wait();
-    if (i0 >= i1 && (p.slots > 1 || split > 0))
+    if (i0 >= i1 && p.o)
         return;   // the merge knows that this slot is empty
     if (threadIdx.x < kPgWarps * NS)
         ptx::mbar_init(ptx::smem_addr(full + threadIdx.x), 1);
@@ -373,7 +378,6 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
             }
         }
     __syncthreads();
-    const bool whole = p.slots == 1;
     const int row0 = seq * HQ + h * p.G;
     for (int e = threadIdx.x; e < p.G * (D / 4); e += kPgThreads) {
         const int g = e / (D / 4), i = 4 * (e - g * (D / 4));
@@ -394,22 +398,56 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
             acc.z = fmaf(v.z, f, acc.z);
             acc.w = fmaf(v.w, f, acc.w);
         }
-        const int64_t r = row0 + g;
-        if (whole) {
-            const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-            uint2 w;
-            w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-            w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(p.out + r * D + i) = w;
-            if (i == 0 && p.lse)
-                p.lse[r] = l > 0.f ? (m + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
-        } else {
-            const int64_t at = r * p.slots + p.prefix_slots + split;
+        if (p.o) {
+            const int64_t at = (int64_t)(row0 + g) * p.slots + p.prefix_slots + split;
             *reinterpret_cast<float4*>(p.o + at * D + i) = acc;
             if (i == 0)
                 p.ml[at] = make_float2(m, l);
+        } else {   // over warp 0's output: this thread alone reads and writes it
+            *reinterpret_cast<float4*>(outs + g * (D + 4) + i) = acc;
+            if (i == 0) {
+                cm[g] = m;
+                cl[g] = l;
+            }
         }
     }
+    if (p.o)
+        return;
+    // ---- no workspace: the splits of these rows are this cluster's CTAs; each
+    // joins its share of the outputs through distributed shared memory
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const int n = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    for (int e = threadIdx.x + rank * kPgThreads; e < p.G * (D / 4); e += n * kPgThreads) {
+        const int g = e / (D / 4), i = 4 * (e - g * (D / 4));
+        float m = -INFINITY;
+        for (int r = 0; r < n; ++r)
+            m = fmaxf(m, *cluster.map_shared_rank(cm + g, r));
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < n; ++r) {
+            const float lr = *cluster.map_shared_rank(cl + g, r);
+            if (lr == 0.f)
+                continue;
+            const float f = ex2(*cluster.map_shared_rank(cm + g, r) - m);
+            const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(outs + g * (D + 4) + i, r));
+            l = fmaf(lr, f, l);
+            acc.x = fmaf(v.x, f, acc.x);
+            acc.y = fmaf(v.y, f, acc.y);
+            acc.z = fmaf(v.z, f, acc.z);
+            acc.w = fmaf(v.w, f, acc.w);
+        }
+        const int64_t r = row0 + g;
+        const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+        uint2 w;
+        w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
+        w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(p.out + r * D + i) = w;
+        if (i == 0 && p.lse)
+            p.lse[r] = l > 0.f ? (m + log2f(l)) * kLn2 : (l == l ? -INFINITY : l);
+    }
+    cluster.sync();   // peers stay until their shares are read
 }
 
 // ----------------------------------------------------------------- merge --
@@ -542,7 +580,9 @@ int device_sms()
 // CTAs share an SM.  While a slot's share is at most 1536 tokens, as many splits
 // as fill one round of CTAs (a second, partly filled round would double the
 // time), each of at least 64 tokens; beyond, about six rounds of CTAs of at
-// least 512 tokens, so that ragged lengths even out.
+// least 512 tokens, so that ragged lengths even out.  Without a prefix up to
+// eight splits are a cluster, whose CTAs join their states in shared memory: no
+// workspace and no merge launch, so 9 to 16 splits become eight.
 void split_own(PagedParams& p, int64_t pieces, int sms)
 {
     const int64_t units = (int64_t)p.n_seqs * p.H, slots = 3ll * sms;
@@ -557,6 +597,8 @@ void split_own(PagedParams& p, int64_t pieces, int sms)
     else
         n = pieces / std::min(pieces, std::max<int64_t>(32, units * pieces / (6 * slots)));
     n = std::min<int64_t>(n, 256);
+    if (p.n_groups == 0 && n > 8 && n <= 16)
+        n = 8;
     int64_t per = (pieces + n - 1) / n;
     per = (per + 3) / 4 * 4;   // whole rounds of the four warps
     p.own_split = (int32_t)std::min(per, pieces);
@@ -593,8 +635,8 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t state_bytes(const PagedParams& p)
 {
-    if (p.slots <= 1 && p.prefix_slots == 0)
-        return 0;
+    if (p.prefix_slots == 0 && p.own_slots <= 8)
+        return 0;   // a cluster
     const size_t n = (size_t)p.n_seqs * p.H * p.G * p.slots;
     return align256(n * p.d * 4) + align256(n * 8);
 }
@@ -637,7 +679,6 @@ int plan(const KameraPagedKV* kv, const KameraPagedQuery* q, const KameraPrefixG
     const int64_t ppp = kv->page_size / 16;
     if (selected && n_select * ppp > 0x7FFFFFF)
         return KAMERA_ERR_UNSUPPORTED;
-    split_own(*p, selected ? (own->max_len > 0 ? n_select * ppp : 0) : ((int64_t)own->max_len + 15) / 16, s);
     if (pre && pre->n_groups > 0 && pre->max_len > 0 && pre->max_group > 0) {
         if ((int64_t)pre->max_pages * kv->page_size < pre->max_len)
             return KAMERA_ERR_INVALID_ARGUMENT;
@@ -651,6 +692,7 @@ int plan(const KameraPagedKV* kv, const KameraPagedQuery* q, const KameraPrefixG
         if ((int64_t)p->n_groups * p->H * p->row_blocks > 65535)
             return KAMERA_ERR_UNSUPPORTED;
     }
+    split_own(*p, selected ? (own->max_len > 0 ? n_select * ppp : 0) : ((int64_t)own->max_len + 15) / 16, s);
     p->slots = p->prefix_slots + p->own_slots;
     return KAMERA_OK;
 }
@@ -666,7 +708,21 @@ cudaError_t launch_own(const PagedLaunch& L, bool dependent, cudaStream_t stream
     if (e != cudaSuccess)
         return e;
     const dim3 grid((unsigned)std::max(L.p.own_slots, 1), (unsigned)(L.p.n_seqs * L.p.H));
-    return launch_after(paged_kernel<D, NT>, grid, kPgThreads, Y::kBytes, stream, dependent, L);
+    if (L.p.o || grid.x == 1)
+        return launch_after(paged_kernel<D, NT>, grid, kPgThreads, Y::kBytes, stream, dependent, L);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kPgThreads);
+    cfg.dynamicSmemBytes = Y::kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = grid.x;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_kernel<D, NT>, L);
 }
 
 // The pointers both entry points share, then the launches.

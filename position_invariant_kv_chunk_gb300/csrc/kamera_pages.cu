@@ -350,26 +350,27 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
 }
 
 // ------------------------------------------------------------------- choice --
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;              // digits of 11 bits
 constexpr int kGather = 1024;            // keys that are ranked by comparison
 constexpr int kMaxWidth = 49152;         // pages of a sequence: their 32-bit keys stay in shared memory
 
-template <int D>
+// NTH: threads of the CTA.
+template <int D, int NTH>
 struct SelSmem {
+    static constexpr int kWarps = NTH / 32;
     uint32_t hist[kBins];
     uint64_t cand[kGather];
     int32_t cand_j[kGather];
     float qa[2 * D], qb[2 * D];          // q- | q+: the 16-bit part and the rest
-    uint32_t warp_sum[kSelWarps];
-    uint64_t warp_min[kSelWarps], warp_max[kSelWarps];
-    float warp_err[kSelWarps];
+    uint32_t warp_sum[kWarps];
+    uint64_t warp_min[kWarps], warp_max[kWarps];
+    float warp_err[kWarps];
     int32_t bin, above, n_cand;
     uint64_t found;
 };
 
 // Exclusive sum over the block of one value a thread; `total` for everybody.
+template <int NTH>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, uint32_t& total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -387,7 +388,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
     uint32_t before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
+    for (int w = 0; w < NTH / 32; ++w) {
         if (w < warp)
             before += warp_sum[w];
         total += warp_sum[w];
@@ -401,19 +402,19 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
 // `need` is what is left to take of those whose (>> shift) equals it; shift is 0,
 // or `count` of them are at most kGather, or all of them are to be taken.
 // each(f) calls f(key) for the thread's share of the set.
-template <typename SM, typename Each>
+template <int NTH, typename SM, typename Each>
 __device__ __forceinline__ void radix_find(SM& sm, uint64_t kmin, uint64_t kmax, Each each, int& need, int& shift,
                                            uint64_t& prefix, int& count)
 {
     const int tid = threadIdx.x;
-    constexpr int PT = kBins / kSelThreads;
+    constexpr int PT = kBins / NTH;
     const int top = 63 - __clzll((long long)(kmin ^ kmax));   // the highest bit that differs
     shift = max(0, top - 10);
     uint64_t fixed = top == 63 ? 0ull : kmin >> (top + 1);    // bits above the digit, shared so far
     int width = top + 1 - shift;                              // bits of the digit
     for (;;) {
         __syncthreads();
-        for (int b = tid; b < kBins; b += kSelThreads)
+        for (int b = tid; b < kBins; b += NTH)
             sm.hist[b] = 0u;
         __syncthreads();
         const int up = shift + width;                         // 64: no bits above
@@ -429,7 +430,7 @@ __device__ __forceinline__ void radix_find(SM& sm, uint64_t kmin, uint64_t kmax,
             c[i] = sm.hist[kBins - 1 - PT * tid - i];
             mine += c[i];
         }
-        uint32_t above = block_scan(mine, sm.warp_sum, total);
+        uint32_t above = block_scan<NTH>(mine, sm.warp_sum, total);
 #pragma unroll
         for (int i = 0; i < PT; ++i) {
             if ((int)above < need && need <= (int)(above + c[i])) {
@@ -493,11 +494,12 @@ __device__ __forceinline__ uint64_t exact_key(const SelectParams& p, int page, i
 // One CTA per (sequence, KV head): the pages surely in by their fp32 scores, the
 // exact order of those near the border, and the pages in order from a bitmap.
 // Latency-bound: a handful of passes over 32-bit keys in shared memory.
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p)
+template <int D, int NTH>
+__global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
 {
+    constexpr int NW = NTH / 32;
     extern __shared__ __align__(16) unsigned char sel_raw[];
-    __shared__ SelSmem<D> sm;
+    __shared__ SelSmem<D, NTH> sm;
     const int words = (p.width + 31) >> 5;
     uint32_t* bm = reinterpret_cast<uint32_t*>(sel_raw);        // pages taken
     uint32_t* band = bm + words;                                // pages near the border
@@ -510,11 +512,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         raise_err(p.err, KAMERA_DEVERR_LEN);
     if (n <= p.k) {   // every page
         ptx::grid_wait();
-        for (int i = tid; i < p.k; i += kSelThreads)
+        for (int i = tid; i < p.k; i += NTH)
             out[i] = i < n ? i : -1;
         return;
     }
-    for (int i = tid; i < 2 * D; i += kSelThreads) {
+    for (int i = tid; i < 2 * D; i += NTH) {
         float a, e;
         signed_sum<D>(p, s, h, i, a, e);
         const float top = __uint_as_float(__float_as_uint(a) & 0xFFFFFF00u);   // 16 significant bits
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
         float err = 0.f;
 #pragma unroll 4
-        for (int j = lo + tid; j < hi; j += kSelThreads) {
+        for (int j = lo + tid; j < hi; j += NTH) {
             const float2 x = scores[j];
             const uint32_t key = x.y < 0.f ? 0u : x.x == INFINITY ? 0xFFFFFFFFu : ordered(x.x);
             key32[j] = key;
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             sm.warp_err[warp] = err;
         }
         __syncthreads();
-        for (int w = 0; w < kSelWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
             kmin = min(kmin, (uint32_t)sm.warp_min[w]);
             kmax = max(kmax, (uint32_t)sm.warp_max[w]);
             err = fmaxf(err, sm.warp_err[w]);
@@ -561,9 +563,9 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         if (kmin != kmax) {
             int left = need, shift, count;
             uint64_t prefix;
-            radix_find(sm, (uint64_t)kmin, (uint64_t)kmax,
+            radix_find<NTH>(sm, (uint64_t)kmin, (uint64_t)kmax,
                        [&](auto f) {
-                           for (int j = lo + tid; j < hi; j += kSelThreads)
+                           for (int j = lo + tid; j < hi; j += NTH)
                                f((uint64_t)key32[j]);
                        },
                        left, shift, prefix, count);
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             } else {   // the left-th largest of the keys of one digit
                 const bool few = count <= kGather;
                 uint32_t least = 0xFFFFFFFFu;
-                for (int j = lo + tid; j < hi; j += kSelThreads)
+                for (int j = lo + tid; j < hi; j += NTH)
                     if (((uint64_t)key32[j] >> shift) == prefix) {
                         if (few)
                             sm.cand[atomicAdd(&sm.n_cand, 1)] = key32[j];
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                     }
                 if (few) {
                     __syncthreads();
-                    for (int i = tid; i < count; i += kSelThreads) {
+                    for (int i = tid; i < count; i += NTH) {
                         const uint64_t key = sm.cand[i];
                         int more = 0, same = 0;
                         for (int o = 0; o < count; ++o) {
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                         sm.warp_min[warp] = least;
                     __syncthreads();
                     if (tid == 0) {
-                        for (int w = 0; w < kSelWarps; ++w)
+                        for (int w = 0; w < NW; ++w)
                             least = min(least, (uint32_t)sm.warp_min[w]);
                         sm.found = least;
                     }
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
     // the bitmaps: whole words, so every thread of a warp takes part
     uint32_t n_in = 0, n_band = 0, total_in, total_band;
-    for (int j = tid; j < words * 32; j += kSelThreads) {
+    for (int j = tid; j < words * 32; j += NTH) {
         bool take = j < n && (j < p.n_first || j >= n - p.n_last), near = false;
         if (need > 0 && j >= lo && j < hi) {
             const uint32_t key = key32[j];
@@ -634,7 +636,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             band[j >> 5] = b;
         }
     }
-    (void)block_scan(n_in | n_band << 16, sm.warp_sum, total_in);   // each at most width < 2^16
+    (void)block_scan<NTH>(n_in | n_band << 16, sm.warp_sum, total_in);   // each at most width < 2^16
     total_band = total_in >> 16;
     total_in &= 0xFFFFu;
     int left = need - (int)total_in;   // of the near ones
@@ -653,17 +655,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             if (tid == 0)
                 sm.n_cand = 0;
             __syncthreads();
-            for (int w = tid; w < words; w += kSelThreads)
+            for (int w = tid; w < words; w += NTH)
                 for (uint32_t e = band[w]; e; e &= e - 1u)
                     sm.cand_j[atomicAdd(&sm.n_cand, 1)] = 32 * w + __ffs((int)e) - 1;
             __syncthreads();
-            for (int i = warp; i < (int)total_band; i += kSelWarps) {
+            for (int i = warp; i < (int)total_band; i += NW) {
                 const uint64_t key = exact_key<D>(p, table[sm.cand_j[i]], h, wa, wb, lane);
                 if (lane == 0)
                     sm.cand[i] = key;
             }
             __syncthreads();
-            for (int i = tid; i < (int)total_band; i += kSelThreads) {
+            for (int i = tid; i < (int)total_band; i += NTH) {
                 const uint64_t key = sm.cand[i];
                 const int j = sm.cand_j[i];
                 int rank = 0;
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             left = 0;
         } else {   // many equal or nearly equal scores: exact keys over the scores, then the same search
             uint64_t kmin = ~0ull, kmax = 0ull;
-            for (int w = warp; w < words; w += kSelWarps)
+            for (int w = warp; w < words; w += NW)
                 for (uint32_t e = band[w]; e; e &= e - 1u) {
                     const int j = 32 * w + __ffs((int)e) - 1;
                     const uint64_t key = exact_key<D>(p, table[j], h, wa, wb, lane);
@@ -689,26 +691,26 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 sm.warp_max[warp] = kmax;
             }
             __syncthreads();
-            for (int w = 0; w < kSelWarps; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 kmin = min(kmin, sm.warp_min[w]);
                 kmax = max(kmax, sm.warp_max[w]);
             }
             uint64_t prefix = kmin;
             int shift = 0, count = 0;
             auto each = [&](auto f) {
-                for (int j = tid; j < words * 32; j += kSelThreads)
+                for (int j = tid; j < words * 32; j += NTH)
                     if ((band[j >> 5] >> (j & 31)) & 1u)
                         f(keys64[j]);
             };
             if (kmin != kmax)
-                radix_find(sm, kmin, kmax, each, left, shift, prefix, count);
+                radix_find<NTH>(sm, kmin, kmax, each, left, shift, prefix, count);
             // what is above the digit is in; what shares it is the new band
             __syncthreads();
             if (tid == 0)
                 sm.n_cand = 0;
             __syncthreads();
             const bool rank_them = kmin != kmax && shift > 0 && count != left;
-            for (int j = tid; j < words * 32; j += kSelThreads) {
+            for (int j = tid; j < words * 32; j += NTH) {
                 bool take = false, near = false;
                 if ((band[j >> 5] >> (j & 31)) & 1u) {
                     const uint64_t key = keys64[j];
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             }
             __syncthreads();
             if (rank_them) {
-                for (int i = tid; i < count; i += kSelThreads) {
+                for (int i = tid; i < count; i += NTH) {
                     const uint64_t key = sm.cand[i];
                     const int j = sm.cand_j[i];
                     int rank = 0;
@@ -748,10 +750,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     __syncthreads();
     if (left > 0 && lowest) {   // the lowest `left` pages of the band
         uint32_t run = 0;
-        for (int w0 = 0; w0 < words; w0 += kSelThreads) {
+        for (int w0 = 0; w0 < words; w0 += NTH) {
             const int w = w0 + tid;
             uint32_t e = w < words ? band[w] : 0u, total, take = 0;
-            int room = left - (int)(run + block_scan((uint32_t)__popc(e), sm.warp_sum, total));
+            int room = left - (int)(run + block_scan<NTH>((uint32_t)__popc(e), sm.warp_sum, total));
             for (; room > 0 && e; --room, e &= e - 1u)
                 take |= e & (0u - e);
             if (take)
@@ -761,10 +763,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         __syncthreads();
     }
     uint32_t run = 0;
-    for (int w0 = 0; w0 < words; w0 += kSelThreads) {
+    for (int w0 = 0; w0 < words; w0 += NTH) {
         const int w = w0 + tid;
         uint32_t e = w < words ? bm[w] : 0u, total;
-        uint32_t at = run + block_scan((uint32_t)__popc(e), sm.warp_sum, total);
+        uint32_t at = run + block_scan<NTH>((uint32_t)__popc(e), sm.warp_sum, total);
         while (e) {
             if (at < (uint32_t)p.k)
                 out[at] = 32 * w + __ffs((int)e) - 1;
@@ -806,11 +808,12 @@ cudaError_t launch_select(SelectParams& p, cudaStream_t stream)
     }
     const size_t smem = (size_t)((p.width + 31) / 32) * 8 + (size_t)p.width * 4;
     // set at every launch: the attribute belongs to the current device's context
-    const cudaError_t e =
-        cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess)
-        return e;
-    return launch_after(select_kernel<D>, dim3((unsigned)units), kSelThreads, smem, stream, after, p);
+    // few pages: few threads, whose barriers are cheaper
+    auto launch = [&](auto kernel, int threads) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        return e != cudaSuccess ? e : launch_after(kernel, dim3((unsigned)units), threads, smem, stream, after, p);
+    };
+    return p.width <= 2048 ? launch(select_kernel<D, 256>, 256) : launch(select_kernel<D, 1024>, 1024);
 }
 
 int check_select(const KameraPageSelect* x, const KameraPageTable* t)
