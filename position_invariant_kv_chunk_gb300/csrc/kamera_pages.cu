@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
 // ------------------------------------------------------------------- choice --
 constexpr int kBins = 2048;              // digits of 11 bits
 constexpr int kGather = 1024;            // keys that are ranked by comparison
-constexpr int kMaxWidth = 49152;         // pages of a sequence: their 32-bit keys stay in shared memory
+constexpr int kMaxWidth = 49152;         // pages of a sequence: 48 scores a thread, in registers
 
 // NTH: threads of the CTA.
 template <int D, int NTH>
@@ -364,9 +364,8 @@ struct SelSmem {
     float qa[2 * D], qb[2 * D];          // q- | q+: the 16-bit part and the rest
     uint32_t warp_sum[kWarps];
     uint64_t warp_min[kWarps], warp_max[kWarps];
-    float warp_err[kWarps];
-    int32_t bin, above, n_cand;
-    uint64_t found;
+    float lo[kWarps], hi[kWarps], err[kWarps];
+    int32_t bin, above, n_cand, n_inf, n_fin, n_in, n_band;
 };
 
 // Exclusive sum over the block of one value a thread; `total` for everybody.
@@ -493,8 +492,11 @@ __device__ __forceinline__ uint64_t exact_key(const SelectParams& p, int page, i
 
 // One CTA per (sequence, KV head): the pages surely in by their fp32 scores, the
 // exact order of those near the border, and the pages in order from a bitmap.
-// Latency-bound: a handful of passes over 32-bit keys in shared memory.
-template <int D, int NTH>
+// All latency (a chain of barriers and dependent loads), so each thread keeps
+// its NK scores in registers, and one histogram of them is enough: the border
+// lies in the bin that holds the n-th largest score, and whatever is within the
+// errors of that bin counts as near it.
+template <int D, int NTH, int NK>
 __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
 {
     constexpr int NW = NTH / 32;
@@ -503,7 +505,6 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
     const int words = (p.width + 31) >> 5;
     uint32_t* bm = reinterpret_cast<uint32_t*>(sel_raw);        // pages taken
     uint32_t* band = bm + words;                                // pages near the border
-    uint32_t* key32 = band + words;
     const int s = blockIdx.x / p.H, h = blockIdx.x - s * p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int lo, hi;
     const int n = page_range(p, s, lo, hi);
@@ -523,125 +524,167 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
         sm.qa[i] = top;
         sm.qb[i] = __fadd_rn(__fadd_rn(a, -top), e);
     }
+    for (int i = tid; i < kBins; i += NTH)
+        sm.hist[i] = 0u;
     if (tid == 0)
-        sm.n_cand = 0;
+        sm.n_cand = sm.n_inf = sm.n_fin = sm.n_in = sm.n_band = 0;
+    __syncthreads();
     ptx::grid_wait();   // the scores
     uint64_t* keys64 = p.keys + (int64_t)blockIdx.x * p.width;
     const float2* scores = reinterpret_cast<const float2*>(keys64);
     int need = p.k - p.n_first - p.n_last;
-    uint32_t in_above = 0xFFFFFFFFu, band_from = 1u;   // keys above the first are in, from the second on near; none yet
-    bool ties = false;                                 // the near ones are equal
+    // ---- the scores: finite, +infinity (not finite: first), NaN (no such page: last)
+    float v[NK], smin = INFINITY, smax = -INFINITY, err = 0.f;
+    int n_inf = 0, n_fin = 0;
     if (need > 0) {
-        uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
-        float err = 0.f;
-#pragma unroll 4
-        for (int j = lo + tid; j < hi; j += NTH) {
-            const float2 x = scores[j];
-            const uint32_t key = x.y < 0.f ? 0u : x.x == INFINITY ? 0xFFFFFFFFu : ordered(x.x);
-            key32[j] = key;
-            kmin = min(kmin, key);
-            kmax = max(kmax, key);
-            err = fmaxf(err, x.y == x.y ? x.y : INFINITY);   // a batch with a NaN or an infinity: everything is near
-        }
-        kmin = __reduce_min_sync(0xFFFFFFFFu, kmin);
-        kmax = __reduce_max_sync(0xFFFFFFFFu, kmax);
+        float2 x[NK];
 #pragma unroll
-        for (int o = 16; o >= 1; o /= 2)
+        for (int i = 0; i < NK; ++i) {
+            const int j = lo + i * NTH + tid;
+            x[i] = make_float2(0.f, -2.f);
+            if (j < hi)
+                x[i] = scores[j];
+        }
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const bool known = x[i].y >= 0.f || x[i].y != x[i].y;   // (a NaN bound comes of a NaN box)
+            const bool fin = known && fabsf(x[i].x) <= 3.402823466e38f;
+            v[i] = fin ? x[i].x : known ? INFINITY : __int_as_float(0x7FC00000);
+            if (known)
+                err = fmaxf(err, x[i].y == x[i].y ? x[i].y : INFINITY);
+            if (fin) {
+                smin = fminf(smin, v[i]);
+                smax = fmaxf(smax, v[i]);
+            }
+            n_fin += fin;
+            n_inf += known && !fin;
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o /= 2) {
+            smin = fminf(smin, __shfl_xor_sync(0xFFFFFFFFu, smin, o));
+            smax = fmaxf(smax, __shfl_xor_sync(0xFFFFFFFFu, smax, o));
             err = fmaxf(err, __shfl_xor_sync(0xFFFFFFFFu, err, o));
+        }
+        n_fin = __reduce_add_sync(0xFFFFFFFFu, n_fin);
+        n_inf = __reduce_add_sync(0xFFFFFFFFu, n_inf);
         if (lane == 0) {
-            sm.warp_min[warp] = kmin;
-            sm.warp_max[warp] = kmax;
-            sm.warp_err[warp] = err;
+            sm.lo[warp] = smin;
+            sm.hi[warp] = smax;
+            sm.err[warp] = err;
+            atomicAdd(&sm.n_fin, n_fin);
+            if (n_inf)
+                atomicAdd(&sm.n_inf, n_inf);
         }
         __syncthreads();
-        for (int w = 0; w < NW; ++w) {
-            kmin = min(kmin, (uint32_t)sm.warp_min[w]);
-            kmax = max(kmax, (uint32_t)sm.warp_max[w]);
-            err = fmaxf(err, sm.warp_err[w]);
+        smin = lane < NW ? sm.lo[lane] : INFINITY;
+        smax = lane < NW ? sm.hi[lane] : -INFINITY;
+        err = lane < NW ? sm.err[lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o >= 1; o /= 2) {
+            smin = fminf(smin, __shfl_xor_sync(0xFFFFFFFFu, smin, o));
+            smax = fmaxf(smax, __shfl_xor_sync(0xFFFFFFFFu, smax, o));
+            err = fmaxf(err, __shfl_xor_sync(0xFFFFFFFFu, err, o));
         }
-        uint32_t T = kmin;
-        if (kmin != kmax) {
-            int left = need, shift, count;
-            uint64_t prefix;
-            radix_find<NTH>(sm, (uint64_t)kmin, (uint64_t)kmax,
-                       [&](auto f) {
-                           for (int j = lo + tid; j < hi; j += NTH)
-                               f((uint64_t)key32[j]);
-                       },
-                       left, shift, prefix, count);
-            if (shift == 0) {
-                T = (uint32_t)prefix;
-            } else {   // the left-th largest of the keys of one digit
-                const bool few = count <= kGather;
-                uint32_t least = 0xFFFFFFFFu;
-                for (int j = lo + tid; j < hi; j += NTH)
-                    if (((uint64_t)key32[j] >> shift) == prefix) {
-                        if (few)
-                            sm.cand[atomicAdd(&sm.n_cand, 1)] = key32[j];
-                        else   // all of them are taken: the least
-                            least = min(least, key32[j]);
-                    }
-                if (few) {
-                    __syncthreads();
-                    for (int i = tid; i < count; i += NTH) {
-                        const uint64_t key = sm.cand[i];
-                        int more = 0, same = 0;
-                        for (int o = 0; o < count; ++o) {
-                            more += sm.cand[o] > key;
-                            same += sm.cand[o] == key;
-                        }
-                        if (more < left && left <= more + same)
-                            sm.found = key;
-                    }
-                } else {
-                    least = __reduce_min_sync(0xFFFFFFFFu, least);
-                    if (lane == 0)
-                        sm.warp_min[warp] = least;
-                    __syncthreads();
-                    if (tid == 0) {
-                        for (int w = 0; w < NW; ++w)
-                            least = min(least, (uint32_t)sm.warp_min[w]);
-                        sm.found = least;
-                    }
+        n_fin = sm.n_fin;
+        n_inf = sm.n_inf;
+    }
+    // ---- in: above `in_above`; near: from `near_from` on; ties: the near ones are equal
+    enum { kInf, kFinite, kUnknown } border = kFinite;
+    float in_above = INFINITY, near_from = INFINITY;
+    if (need > 0) {
+        if (need <= n_inf) {
+            border = kInf;
+        } else if (need - n_inf > n_fin) {
+            border = kUnknown;
+        } else {
+            // bins of equal width between the least and the largest score; bin(x) grows with
+            // x, and the bin's edges are taken a bin wide of it, which covers its rounding
+            const float range = __fadd_ru(smax, -smin);
+            float inv = (float)kBins / range;
+            if (!(inv <= 3.402823466e38f))
+                inv = 0.f;   // one value, or as good as one: a single bin
+#pragma unroll
+            for (int i = 0; i < NK; ++i)
+                if (fabsf(v[i]) <= 3.402823466e38f)
+                    atomicAdd(&sm.hist[min(kBins - 1, (int)((v[i] - smin) * inv))], 1u);
+            __syncthreads();
+            // thread t's bins, from the top: kBins - 1 - PT t downwards
+            constexpr int PT = kBins / NTH;
+            const int want = need - n_inf;
+            uint32_t c[PT], mine = 0, total;
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                c[i] = sm.hist[kBins - 1 - PT * tid - i];
+                mine += c[i];
+            }
+            uint32_t above = block_scan<NTH>(mine, sm.warp_sum, total);
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                if ((int)above < want && want <= (int)(above + c[i]))
+                    sm.bin = kBins - 1 - PT * tid - i;
+                above += c[i];
+            }
+            __syncthreads();
+            const float b = (float)sm.bin, e2 = __fmul_ru(2.f, err);
+            const float w_lo = inv > 0.f ? __fdiv_rd(1.f, inv) : 0.f, w_hi = inv > 0.f ? __fdiv_ru(1.f, inv) : 0.f;
+            const float edge_hi = inv > 0.f ? __fadd_ru(smin, __fmul_ru(b + 2.f, w_hi)) : smax;
+            const float edge_lo = inv > 0.f ? __fadd_rd(smin, b >= 1.f ? __fmul_rd(b - 1.f, w_lo) : -w_hi) : smin;
+            in_above = __fadd_ru(edge_hi, e2);
+            near_from = __fadd_rd(edge_lo, -e2);
+        }
+    }
+    // ---- the bitmaps: whole words, so every thread of a warp takes part
+    for (int w = tid; w < words; w += NTH)
+        bm[w] = band[w] = 0u;
+    __syncthreads();
+    auto forced = [&](int j) { return j < n && (j < p.n_first || j >= n - p.n_last); };
+    int n_in = 0, n_near = 0;
+    if (need > 0) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int j = lo + i * NTH + tid;
+            bool take = false, near = false;
+            if (j < hi) {
+                const bool inf = v[i] == INFINITY, unknown = v[i] != v[i];
+                if (border == kInf) {
+                    near = inf;
+                } else if (border == kUnknown) {
+                    take = !unknown;
+                    near = unknown;
+                } else if (!unknown) {
+                    take = inf || v[i] > in_above;
+                    near = !take && v[i] >= near_from;
                 }
-                __syncthreads();
-                T = (uint32_t)sm.found;
+            }
+            // pages lo + i NTH + 32 warp .. + 31: two words of the bitmap
+            const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), c = __ballot_sync(0xFFFFFFFFu, near);
+            n_in += __popc(a);
+            n_near += __popc(c);
+            if (lane < 2 && (a | c)) {
+                const int first = lo + i * NTH + 32 * warp, off = first & 31, word = (first >> 5) + lane;
+                const uint32_t wa = lane == 0 ? a << off : off ? a >> (32 - off) : 0u;
+                const uint32_t wc = lane == 0 ? c << off : off ? c >> (32 - off) : 0u;
+                if (wa)
+                    atomicOr(&bm[word], wa);
+                if (wc)
+                    atomicOr(&band[word], wc);
             }
         }
-        if (T == 0u || T == 0xFFFFFFFFu) {   // unknown pages, or scores that are not finite: equal among themselves
-            in_above = T;
-            band_from = T;
-            ties = true;
-        } else {
-            const float t = __uint_as_float(T ^ ((uint32_t)((int32_t)~T >> 31) | 0x80000000u));   // ordered() undone
-            in_above = ordered(__fadd_ru(t, __fmul_ru(2.f, err)));
-            band_from = max(ordered(__fadd_rd(t, -__fmul_ru(2.f, err))), 1u);
-            in_above = min(in_above, 0xFFFFFFFEu);
-        }
-    }
-    // the bitmaps: whole words, so every thread of a warp takes part
-    uint32_t n_in = 0, n_band = 0, total_in, total_band;
-    for (int j = tid; j < words * 32; j += NTH) {
-        bool take = j < n && (j < p.n_first || j >= n - p.n_last), near = false;
-        if (need > 0 && j >= lo && j < hi) {
-            const uint32_t key = key32[j];
-            take = key > in_above;
-            near = !take && key >= band_from;
-            n_in += take;
-            n_band += near;
-        }
-        const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), b = __ballot_sync(0xFFFFFFFFu, near);
         if (lane == 0) {
-            bm[j >> 5] = a;
-            band[j >> 5] = b;
+            atomicAdd(&sm.n_in, n_in);
+            atomicAdd(&sm.n_band, n_near);
         }
     }
-    (void)block_scan<NTH>(n_in | n_band << 16, sm.warp_sum, total_in);   // each at most width < 2^16
-    total_band = total_in >> 16;
-    total_in &= 0xFFFFu;
-    int left = need - (int)total_in;   // of the near ones
-    bool lowest = ties;                // take the lowest pages of the (remaining) band
-    if (left > 0 && !ties && left < (int)total_band) {
+    for (int j = tid; j < p.n_first; j += NTH)
+        if (forced(j))
+            atomicOr(&bm[j >> 5], 1u << (j & 31));
+    for (int j = max(0, n - p.n_last) + tid; j < n; j += NTH)
+        atomicOr(&bm[j >> 5], 1u << (j & 31));
+    __syncthreads();
+    const uint32_t total_band = (uint32_t)sm.n_band;
+    int left = need - sm.n_in;                  // of the near ones
+    bool lowest = border != kFinite;            // take the lowest pages of the (remaining) band
+    if (left > 0 && !lowest && left < (int)total_band) {
         uint64_t wa[4], wb[4];
         const bool on = lane < D / 4;
 #pragma unroll
@@ -650,11 +693,7 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
             wb[i] = on ? *reinterpret_cast<const uint64_t*>(&sm.qb[8 * lane + 2 * i]) : 0ull;
         }
         const int32_t* table = p.pages + (int64_t)s * p.max_pages;
-        const bool few = total_band <= (uint32_t)kGather;
-        if (few) {   // list the band
-            if (tid == 0)
-                sm.n_cand = 0;
-            __syncthreads();
+        if (total_band <= (uint32_t)kGather) {   // list the band
             for (int w = tid; w < words; w += NTH)
                 for (uint32_t e = band[w]; e; e &= e - 1u)
                     sm.cand_j[atomicAdd(&sm.n_cand, 1)] = 32 * w + __ffs((int)e) - 1;
@@ -675,7 +714,7 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
                     atomicOr(&bm[j >> 5], 1u << (j & 31));
             }
             left = 0;
-        } else {   // many equal or nearly equal scores: exact keys over the scores, then the same search
+        } else {   // many equal or nearly equal scores: exact keys over the scores, then a search by digits
             uint64_t kmin = ~0ull, kmax = 0ull;
             for (int w = warp; w < words; w += NW)
                 for (uint32_t e = band[w]; e; e &= e - 1u) {
@@ -706,9 +745,6 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
                 radix_find<NTH>(sm, kmin, kmax, each, left, shift, prefix, count);
             // what is above the digit is in; what shares it is the new band
             __syncthreads();
-            if (tid == 0)
-                sm.n_cand = 0;
-            __syncthreads();
             const bool rank_them = kmin != kmax && shift > 0 && count != left;
             for (int j = tid; j < words * 32; j += NTH) {
                 bool take = false, near = false;
@@ -722,10 +758,10 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
                         sm.cand_j[i] = j;
                     }
                 }
-                const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), b = __ballot_sync(0xFFFFFFFFu, near);
+                const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), c = __ballot_sync(0xFFFFFFFFu, near);
                 if (lane == 0) {
                     bm[j >> 5] |= a;
-                    band[j >> 5] = b;
+                    band[j >> 5] = c;
                 }
             }
             __syncthreads();
@@ -806,14 +842,16 @@ cudaError_t launch_select(SelectParams& p, cudaStream_t stream)
             return e;
         after = true;
     }
-    const size_t smem = (size_t)((p.width + 31) / 32) * 8 + (size_t)p.width * 4;
+    const size_t smem = (size_t)((p.width + 31) / 32) * 8;
     // set at every launch: the attribute belongs to the current device's context
     // few pages: few threads, whose barriers are cheaper
     auto launch = [&](auto kernel, int threads) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return e != cudaSuccess ? e : launch_after(kernel, dim3((unsigned)units), threads, smem, stream, after, p);
     };
-    return p.width <= 2048 ? launch(select_kernel<D, 256>, 256) : launch(select_kernel<D, 1024>, 1024);
+    return p.width <= 2048   ? launch(select_kernel<D, 256, 8>, 256)
+           : p.width <= 8192 ? launch(select_kernel<D, 1024, 8>, 1024)
+                             : launch(select_kernel<D, 1024, 48>, 1024);
 }
 
 int check_select(const KameraPageSelect* x, const KameraPageTable* t)
