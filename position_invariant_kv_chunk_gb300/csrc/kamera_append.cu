@@ -26,6 +26,7 @@
 #include "kamera_common.cuh"
 #include "kamera_hostcheck.h"
 #include "kamera_internal.h"
+#include "kamera_ptx.cuh"
 
 namespace kamera {
 
@@ -195,6 +196,8 @@ __global__ void __launch_bounds__(512) append_kernel(const __grid_constant__ App
     __shared__ int64_t slot_s[TT];                 // -1: this token is not written
     const int t0 = blockIdx.x * TT;
     const int nt = min(TT, p.n_tokens - t0);
+    ptx::grid_wait();
+    ptx::grid_launch_next();
     uint4 a[TT], b[TT];
     Unit u;
     const bool has = (int)threadIdx.x < p.items;
@@ -257,18 +260,9 @@ cudaError_t launch_append_t(const AppendParams& p, bool inplace, cudaStream_t st
     const int threads = ((p.items + rounds - 1) / rounds + 31) / 32 * 32;
     const unsigned grid = (unsigned)((p.n_tokens + TT - 1) / TT);
     const size_t smem = sizeof(float2) * (size_t)TT * (size_t)p.n_freq;   // at most 8 KB
-    if (p.unit_log == 3) {
-        if (inplace)
-            append_kernel<TT, true, true><<<grid, threads, smem, stream>>>(p);
-        else
-            append_kernel<TT, false, true><<<grid, threads, smem, stream>>>(p);
-    } else {
-        if (inplace)
-            append_kernel<TT, true, false><<<grid, threads, smem, stream>>>(p);
-        else
-            append_kernel<TT, false, false><<<grid, threads, smem, stream>>>(p);
-    }
-    return cudaGetLastError();
+    const auto kernel = p.unit_log == 3 ? (inplace ? append_kernel<TT, true, true> : append_kernel<TT, false, true>)
+                                        : (inplace ? append_kernel<TT, true, false> : append_kernel<TT, false, false>);
+    return launch_after(kernel, dim3(grid), threads, smem, stream, true, p);
 }
 
 // The passes of one source row kind: the rotary range [ro, ro + rr) rotated

@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
     const int seq = blockIdx.y / p.H, h = blockIdx.y - seq * p.H, split = blockIdx.x;
     const int HQ = p.H * p.G, ppp = p.P / kPgTok;   // pieces per page
+    if (p.n_groups == 0)   // the call's first kernel
+        ptx::grid_wait();
     ptx::grid_launch_next();
 
     // The warp's pieces are i0 + warp, i0 + warp + 4, ...; lane l looks up the
@@ -487,6 +489,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedPara
     const int n_own = p.own_slots > 0 ? (pieces + p.own_split - 1) / p.own_split : 0;
     const int n = n_prefix + n_own, gap = p.prefix_slots - n_prefix;   // unused prefix slots between
     ptx::grid_wait();
+    ptx::grid_launch_next();
     float m = -INFINITY;
     for (int i = lane; i < n; i += 32)
         m = fmaxf(m, ml[i < n_prefix ? i : i + gap].x);
@@ -698,7 +701,7 @@ int plan(const KameraPagedKV* kv, const KameraPagedQuery* q, const KameraPrefixG
 }
 
 template <int D, int NT>
-cudaError_t launch_own(const PagedLaunch& L, bool dependent, cudaStream_t stream)
+cudaError_t launch_own(const PagedLaunch& L, cudaStream_t stream)
 {
     using Y = PgLayout<D, NT>;
     static_assert(Y::kBytes <= 227 * 1024, "shared memory");
@@ -709,19 +712,21 @@ cudaError_t launch_own(const PagedLaunch& L, bool dependent, cudaStream_t stream
         return e;
     const dim3 grid((unsigned)std::max(L.p.own_slots, 1), (unsigned)(L.p.n_seqs * L.p.H));
     if (L.p.o || grid.x == 1)
-        return launch_after(paged_kernel<D, NT>, grid, kPgThreads, Y::kBytes, stream, dependent, L);
+        return launch_after(paged_kernel<D, NT>, grid, kPgThreads, Y::kBytes, stream, true, L);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kPgThreads);
     cfg.dynamicSmemBytes = Y::kBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = grid.x;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, paged_kernel<D, NT>, L);
 }
 
@@ -824,14 +829,13 @@ int attend(PagedParams& p, const KameraPagedKV* kv, const KameraPagedQuery* q, c
         if (p.slots == 0)
             p.slots = 1;
         L.p = p;
-        const bool after = p.n_groups > 0;
         cudaError_t e = cudaErrorInvalidValue;
         if (make_rows_map(&L.map_k, kv->k, map_rows, W, kv->slot_stride, 64, kPgTok) &&
             make_rows_map(&L.map_v, kv->v, map_rows, W, kv->slot_stride, 64, kPgTok)) {
             if (p.d == 128)
-                e = p.G <= 8 ? launch_own<128, 1>(L, after, stream) : launch_own<128, 2>(L, after, stream);
+                e = p.G <= 8 ? launch_own<128, 1>(L, stream) : launch_own<128, 2>(L, stream);
             else
-                e = p.G <= 8 ? launch_own<64, 1>(L, after, stream) : launch_own<64, 2>(L, after, stream);
+                e = p.G <= 8 ? launch_own<64, 1>(L, stream) : launch_own<64, 2>(L, stream);
         }
         if (e != cudaSuccess)
             return KAMERA_ERR_CUDA;

@@ -68,6 +68,8 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
 __global__ void __launch_bounds__(128) summary_kernel(const SummaryParams p)
 {
     const int64_t item = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    ptx::grid_wait();
+    ptx::grid_launch_next();
     if (item >= p.items)
         return;
     const int64_t e = item / p.vecs;
@@ -124,6 +126,7 @@ struct SelectParams {
     int32_t max_pages, max_len, width;
     int32_t k, n_first, n_last;
     int32_t sweeps;              // score kernel: batches of a warp
+    int32_t scored;              // the score kernel runs before the choice
     int32_t* err;
 };
 
@@ -210,6 +213,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
     extern __shared__ __align__(16) unsigned char ring_raw[];
     __shared__ __align__(16) __nv_bfloat16 wt[3][2 * D];
     __shared__ float norm_s[kScoreWarps];
+    ptx::grid_wait();
     ptx::grid_launch_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t4 = lane & 3;
     const int s = blockIdx.y / p.H, h = blockIdx.y - s * p.H;
@@ -506,6 +510,9 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
     uint32_t* bm = reinterpret_cast<uint32_t*>(sel_raw);        // pages taken
     uint32_t* band = bm + words;                                // pages near the border
     const int s = blockIdx.x / p.H, h = blockIdx.x - s * p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (!p.scored)   // the call's first kernel
+        ptx::grid_wait();
+    ptx::grid_launch_next();
     int lo, hi;
     const int n = page_range(p, s, lo, hi);
     int32_t* out = p.selected + (int64_t)blockIdx.x * p.k;
@@ -826,8 +833,8 @@ cudaError_t launch_score(SelectParams& p, int scored, cudaStream_t stream)
                                                (int)ScoreLayout<D>::kBytes);
     if (a != cudaSuccess)
         return a;
-    score_kernel<D><<<dim3((unsigned)gx, (unsigned)units), 32 * kScoreWarps, ScoreLayout<D>::kBytes, stream>>>(p);
-    return cudaGetLastError();
+    return launch_after(score_kernel<D>, dim3((unsigned)gx, (unsigned)units), 32 * kScoreWarps, ScoreLayout<D>::kBytes,
+                        stream, true, p);
 }
 
 template <int D>
@@ -835,19 +842,18 @@ cudaError_t launch_select(SelectParams& p, cudaStream_t stream)
 {
     const int64_t units = (int64_t)p.n_seqs * p.H;
     const int scored = p.width - p.n_first - p.n_last;   // at most, of one sequence
-    bool after = false;
     if (p.width > p.k && scored > 0 && p.k > p.n_first + p.n_last) {
         const cudaError_t e = launch_score<D>(p, scored, stream);
         if (e != cudaSuccess)
             return e;
-        after = true;
+        p.scored = 1;
     }
     const size_t smem = (size_t)((p.width + 31) / 32) * 8;
     // set at every launch: the attribute belongs to the current device's context
     // few pages: few threads, whose barriers are cheaper
     auto launch = [&](auto kernel, int threads) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        return e != cudaSuccess ? e : launch_after(kernel, dim3((unsigned)units), threads, smem, stream, after, p);
+        return e != cudaSuccess ? e : launch_after(kernel, dim3((unsigned)units), threads, smem, stream, true, p);
     };
     return p.width <= 2048   ? launch(select_kernel<D, 256, 8>, 256)
            : p.width <= 8192 ? launch(select_kernel<D, 1024, 8>, 1024)
@@ -922,8 +928,10 @@ int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, c
     const int64_t ctas = (p.items + 127) / 128;
     if (ctas > 0x7FFFFFFF)
         return KAMERA_ERR_UNSUPPORTED;
-    summary_kernel<<<(unsigned)ctas, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? KAMERA_OK : KAMERA_ERR_CUDA;
+    return launch_after(summary_kernel, dim3((unsigned)ctas), 128, 0, reinterpret_cast<cudaStream_t>(stream), true, p) ==
+                   cudaSuccess
+               ? KAMERA_OK
+               : KAMERA_ERR_CUDA;
 }
 
 size_t kamera_select_pages_workspace_bytes(const KameraPageSelect* select, const KameraPageTable* table)

@@ -546,6 +546,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     const uint32_t at = ptx::smem_addr(raw), pad = (1024u - (at & 1023u)) & 1023u, sbase = at + pad;
     PxBars& b = *reinterpret_cast<PxBars*>(raw + pad + Y::kBar);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    ptx::grid_wait();
     ptx::grid_launch_next();
     PxWork w;
     px_work(p, w);
@@ -623,8 +624,7 @@ cudaError_t launch_prefix_d(const PagedLaunch& L, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     const unsigned ctas = (unsigned)L.p.n_groups * L.p.H * L.p.row_blocks * L.p.prefix_splits;
-    prefix_kernel<D><<<ctas, kPxThreads, Y::kBytes, stream>>>(L);
-    return cudaGetLastError();
+    return launch_after(prefix_kernel<D>, dim3(ctas), kPxThreads, Y::kBytes, stream, true, L);
 }
 
 }  // namespace

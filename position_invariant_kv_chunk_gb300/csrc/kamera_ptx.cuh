@@ -186,7 +186,11 @@ __device__ __forceinline__ void stg128(void* p, const uint32_t (&v)[4])
 // ------------------------------------- programmatic dependent launch --
 // The stream's next kernel, launched as a programmatic dependent, may start
 // once every CTA of this grid has said so (or ended); it waits for this grid's
-// completion, and sees its writes, with grid_wait.
+// completion, and sees its writes, with grid_wait.  A call's first kernel waits
+// for whatever ran before it and only then lets the next one start, so the
+// call's later kernels may read the call's inputs at once; and a grid ends only
+// after the one before it has (some CTA of it waits), so that the next call's
+// wait covers them all.
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
