@@ -656,8 +656,8 @@ int kamera_attend_reused_static(const KameraAttnKV* kv, const KameraAttnQuery* q
  *   MLA:     k is the new k_rope rows [n_tokens][rope_dim], v the c_KV rows
  *            [n_tokens][kv_lora_rank], q the rope part of the queries
  *            [n_tokens][num_q_heads][rope_dim]
- * Pointers 16-byte aligned, strides in elements, multiples of 8 (a head stride
- * is not used where there is one head).
+ * Pointers 16-byte aligned, strides in elements, multiples of 8 (a token stride
+ * is not used where there is one token, a head stride where there is one head).
  *   positions  device int64 [n_tokens], |position| <= KAMERA_MAX_ABS_DELTA (else
  *              KAMERA_DEVERR_DESCRIPTOR, the token skipped); NULL when the rope
  *              has axes: then rope->d_axis_delta is int64 [n_tokens][n_axes],
@@ -739,10 +739,11 @@ typedef struct KameraPageTable {
 
 /* Groups of sequences that share a prefix: group g is sequences group_start[g]
  * .. group_start[g+1]-1 (device int32 [n_groups + 1], non-decreasing from 0 to
- * n_seqs, at most max_group sequences each; a malformed entry raises
- * KAMERA_DEVERR_DESCRIPTOR and its sequences' results are unspecified), its
- * prefix tokens 0 .. lens[g]-1 of page table row g (pages [n_groups]
- * [max_pages]; len outside 0..max_len: KAMERA_DEVERR_LEN, the prefix left out). */
+ * n_seqs, at most max_group sequences each, 1 <= max_group <= n_seqs; a malformed
+ * entry raises KAMERA_DEVERR_DESCRIPTOR and its sequences' results are
+ * unspecified), its prefix tokens 0 .. lens[g]-1 of page table row g (pages
+ * [n_groups][max_pages]; len outside 0..max_len: KAMERA_DEVERR_LEN, the prefix
+ * left out). */
 typedef struct KameraPrefixGroups {
     const int32_t* group_start;
     const int32_t* pages;
@@ -771,8 +772,9 @@ typedef struct KameraPrefixGroups {
  *           caller, overwritten by the call; calls that overlap on the GPU must
  *           not share one
  * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..16, page_size a
- * multiple of 16, num_slots <= 2^31 - 1.  Device errors: SLOT, LEN, DESCRIPTOR
- * as above; TIMEOUT if a pipeline wait runs past its bound (outputs of the
+ * multiple of 16, num_slots <= 2^31 - 1, n_seqs * num_kv_heads <= 65535 (and as many
+ * groups times KV heads times blocks of 256 query rows).  Device errors: SLOT, LEN,
+ * DESCRIPTOR as above; TIMEOUT if a pipeline wait runs past its bound (outputs of the
  * call then undefined).
  */
 int kamera_attend_shared(const KameraPagedKV* kv, const KameraPagedQuery* query, const KameraPrefixGroups* prefix,
@@ -793,7 +795,7 @@ size_t kamera_attend_shared_workspace_bytes(const KameraPagedKV* kv, const Kamer
  * [num_slots / P][num_kv_heads][2][head_dim], 16-byte aligned, other pages'
  * entries stay as they are.  Device errors, the entry skipped: SLOT (page
  * outside the pool), LEN (c outside 0..page_size).  The same page twice in a
- * call: one of the two results.  head_dim a multiple of 8; kv->v is not read
+ * call: each 16-byte piece of its summary is that of either entry.  head_dim a multiple of 8; kv->v is not read
  * and may be NULL.
  */
 int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, const int32_t* d_page_tokens, int32_t n,
@@ -818,8 +820,8 @@ int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, c
  *   d_workspace  at least kamera_select_pages_workspace_bytes(...) bytes, rules
  *             as for kamera_attend_shared
  * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..16, n_first,
- * n_last >= 0 with n_first + n_last <= n_select, at most 49152 pages in max_len
- * (UNSUPPORTED beyond).  Device errors: LEN (the sequence read as empty: all -1),
+ * n_last >= 0 with n_first + n_last <= n_select, page_size a multiple of 16,
+ * n_seqs * num_kv_heads <= 65535, at most 49152 pages in max_len.  Device errors: LEN (the sequence read as empty: all -1),
  * SLOT (a page outside num_pages ranks last).
  */
 typedef struct KameraPageSelect {

@@ -347,30 +347,30 @@ int check_rows(const KameraAppendRows* x, const KameraRope* rope, int64_t wk, in
         return KAMERA_ERR_INVALID_ARGUMENT;
     if ((reinterpret_cast<uintptr_t>(x->slots) & 7) || (reinterpret_cast<uintptr_t>(x->positions) & 7))
         return KAMERA_ERR_MISALIGNED;
-    const int64_t n = x->n_tokens;
+    const int64_t n = x->n_tokens, heads = x->num_q_heads > 1 ? x->num_q_heads - 1 : 0;
     struct Rows {
         const void* p;
         int64_t stride, width;
     };
     const Rows in[3] = {{wk > 0 ? x->k : nullptr, x->k_stride, wk},
                         {wv > 0 ? x->v : nullptr, x->v_stride, wv},
-                        {x->q, x->q_stride, (x->num_q_heads - 1) * x->q_head_stride + wq}};
+                        {x->q, x->q_stride, heads * x->q_head_stride + wq}};
     for (const Rows& r : in) {
         if (!r.p)
             continue;
-        if (!aligned16(r.p) || (r.stride & 7))
+        if (!aligned16(r.p) || (n > 1 && (r.stride & 7)))
             return KAMERA_ERR_MISALIGNED;
-        if (r.stride < 0 || (n > 1 && r.stride < r.width))
+        if (n > 1 && r.stride < r.width)
             return KAMERA_ERR_INVALID_ARGUMENT;
     }
     if (x->q) {
-        const int64_t wo = (x->num_q_heads - 1) * x->q_out_head_stride + wq;
-        if (!aligned16(x->q_out) || (x->q_out_stride & 7) ||
+        const int64_t wo = heads * x->q_out_head_stride + wq;
+        if (!aligned16(x->q_out) || (n > 1 && (x->q_out_stride & 7)) ||
             (x->num_q_heads > 1 && ((x->q_head_stride | x->q_out_head_stride) & 7)))
             return KAMERA_ERR_MISALIGNED;
         if (x->num_q_heads > 1 && (x->q_head_stride < wq || x->q_out_head_stride < wq))
             return KAMERA_ERR_INVALID_ARGUMENT;
-        if (x->q_out_stride < 0 || (n > 1 && x->q_out_stride < wo))
+        if (n > 1 && x->q_out_stride < wo)
             return KAMERA_ERR_INVALID_ARGUMENT;
         const bool same = x->q == x->q_out && (n == 1 || x->q_stride == x->q_out_stride) &&
                           (x->num_q_heads == 1 || x->q_head_stride == x->q_out_head_stride);

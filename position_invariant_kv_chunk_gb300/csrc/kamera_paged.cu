@@ -682,11 +682,11 @@ int plan(const KameraPagedKV* kv, const KameraPagedQuery* q, const KameraPrefixG
     const int64_t ppp = kv->page_size / 16;
     if (selected && n_select * ppp > 0x7FFFFFF)
         return KAMERA_ERR_UNSUPPORTED;
-    if (pre && pre->n_groups > 0 && pre->max_len > 0 && pre->max_group > 0) {
-        if ((int64_t)pre->max_pages * kv->page_size < pre->max_len)
+    if (pre && pre->n_groups > 0 && pre->max_len > 0) {
+        if ((int64_t)pre->max_pages * kv->page_size < pre->max_len || pre->max_group < 1 || pre->max_group > q->n_seqs)
             return KAMERA_ERR_INVALID_ARGUMENT;
-        if (pre->max_len > 0x7FFFFF00 || pre->max_group > q->n_seqs)
-            return pre->max_group > q->n_seqs ? KAMERA_ERR_INVALID_ARGUMENT : KAMERA_ERR_UNSUPPORTED;
+        if (pre->max_len > 0x7FFFFF00)
+            return KAMERA_ERR_UNSUPPORTED;
         p->n_groups = pre->n_groups;
         p->max_prefix_pages = pre->max_pages;
         p->max_prefix = pre->max_len;
@@ -792,7 +792,7 @@ int attend(PagedParams& p, const KameraPagedKV* kv, const KameraPagedQuery* q, c
     p.pages = own->pages;
     p.lens = own->lens;
     if (p.own_slots == 0)
-        p.n_select = 0;   // nothing to select from
+        p.n_select = p.max_len = 0;   // nothing to read: no length and no selection is looked at
     p.selected = p.n_select > 0 ? selected : nullptr;
     if (p.n_groups > 0) {
         p.group_start = pre->group_start;

@@ -169,6 +169,24 @@ def test_append_in_place_queries_of_a_fused_row():
     assert torch.equal(again[:, Hq * d:], fused[:, Hq * d:])
 
 
+def test_append_one_token_with_any_token_stride():
+    """One token's rows from a matrix of odd width: its token stride, which no row uses, is no multiple of 8."""
+    H, Hq, d = 2, 4, 64
+    g = torch.Generator(device=DEV).manual_seed(9)
+    wide = normal(g, 3, (Hq + 2 * H) * d + 3)[:1]
+    view = lambda o, heads: wide.as_strided((1, heads, d), (wide.stride(0), d, 1), o * d)
+    q, k, v = view(0, Hq), view(Hq, H), view(Hq + H, H)
+    assert k.stride(0) % 8
+    pk, pv = normal(g, 1, 8, H, d), normal(g, 1, 8, H, d)
+    pos, slots = torch.tensor([77], device=DEV), torch.tensor([5], device=DEV)
+    out = K.kamera_append_kv(pk, pv, k, v, K.Rope(1e4, d), pos, slots, q=q)
+    torch.cuda.synchronize()
+    inv = 1e4 ** (-2.0 * np.arange(d // 2) / d)
+    for got, x in ((pk[0, slots], R.f64(k)), (out, R.f64(q))):
+        near(got, R.turned(x, pos.cpu().numpy(), inv, 0, False), R.turn_scale(x, d // 2, 0, False), "one token")
+    assert torch.equal(pv[0, slots], v)
+
+
 def test_append_skips_and_reports_bad_rows():
     T, H, d = 6, 2, 64
     g = torch.Generator(device=DEV).manual_seed(6)

@@ -223,13 +223,14 @@ def test_shared_reports_bad_pages_and_lengths():
     assert not bool(out.any()) and bool((lse == -float("inf")).all())
 
 
-def test_shared_reports_malformed_groups():
+@pytest.mark.parametrize("G", [4, 16])
+def test_shared_reports_malformed_groups(G):
     """Group starts out of order or past the batch, and a sequence in no group: the
     call reports them, reads nothing out of range and serves the other sequences."""
     pool = Pool(21, 40, 16, 1, 64)
     pre, own = pool.table([100, 90, 80]), pool.table([20, 20, 20])
     pool.poison()
-    q = normal(pool.g, 3, 4, 64)
+    q = normal(pool.g, 3, G, 64)
     good, _ = K.kamera_attend_shared(pool.k, pool.v, q, 16, i32([0, 1, 2, 3]), pre, i32([100, 90, 80]), own,
                                      i32([20, 20, 20]), 1, 100, 20)
     for starts, served in (([0, 1, 1, 2], [0]), ([0, 1, 9, 3], [0]), ([0, 1, -7, 3], [0]), ([-1, 1, 2, 3], [1, 2])):
@@ -547,6 +548,97 @@ def test_selected_attention_matches_definition(H, G, d, P):
     K.kamera_attend_selected(pool.k, pool.v, q, P, pages, i32(lens), sel, max(lens), err=err)
     torch.cuda.synchronize()
     assert int(err.item()) == SLOT
+
+
+def test_selected_nothing_and_given_buffers():
+    """No page selected (an empty selection, or -1 throughout): zeros and -infinity; the
+    caller's out, lse and workspace are used, and lse False leaves it out."""
+    H, G, d, P = 2, 4, 64, 16
+    lens = [100, 37]
+    pool = Pool(42, 30, P, H, d)
+    pages = pool.table(lens)
+    pool.poison()
+    q = normal(pool.g, 2, H * G, d)
+    for k in (0, 3):
+        sel = torch.full((2, H, k), -1, dtype=torch.int32, device=DEV)
+        out, lse = K.kamera_attend_selected(pool.k, pool.v, q, P, pages, i32(lens), sel, 100)
+        torch.cuda.synchronize()
+        assert not bool(out.any()) and bool((lse == -float("inf")).all()), k
+    args = (pool.k, pool.v, q, P, i32([0, 2]), pages[:1].contiguous(), i32([90]), pages, i32(lens), 2, 90, 100)
+    out, lse = K.kamera_attend_shared(*args)
+    mine = torch.empty_like(out), torch.empty_like(lse)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device=DEV)
+    got = K.kamera_attend_shared(*args, out=mine[0], lse=mine[1], workspace=ws)
+    none = K.kamera_attend_shared(*args, lse=False)
+    torch.cuda.synchronize()
+    assert got[0] is mine[0] and got[1] is mine[1] and none[1] is None
+    assert torch.equal(out, mine[0]) and torch.equal(lse, mine[1]) and torch.equal(out, none[0])
+    with pytest.raises(K.KameraError):
+        K.kamera_attend_shared(*args, workspace=ws[:64])
+
+
+@pytest.mark.parametrize("lens", [[4000], [1500, 1, 0], [700] * 5])
+def test_own_pages_by_cluster_and_by_merge(lens):
+    """Sequences without a prefix whose splits join in a cluster, and the same beside a
+    prefix of no token, where they join through the workspace."""
+    H, G, d, P = 2, 7, 128, 16
+    n = len(lens)
+    pool = Pool(43, sum(-(-x // P) for x in lens) + 4, P, H, d)
+    table = pool.table(lens)
+    pool.poison()
+    q = normal(pool.g, n, H * G, d)
+    a = K.kamera_attend_shared(pool.k, pool.v, q, P, None, None, None, table, i32(lens), 0, 0, max(lens))
+    b = K.kamera_attend_shared(pool.k, pool.v, q, P, i32([0, n]), table[:1].contiguous(), i32([0]), table, i32(lens), n,
+                               16, max(lens))
+    torch.cuda.synchronize()
+    refs = rows_ref(q, pool, [R.slots_of(table[s].tolist(), P, x, pool.n_pages) for s, x in enumerate(lens)], d ** -0.5)
+    near(*a, refs, "cluster")
+    near(*b, refs, "merge")
+
+
+def test_calls_in_a_row_see_each_others_writes():
+    """Append, attend, append, summarise, select, attend without a wait between: each
+    call starts while the one before ends, and must still see what it wrote."""
+    H, G, d, P, n = 4, 7, 128, 16, 6
+    pool = Pool(44, 500, P, H, d)
+    lens0 = [700, 33, 1200, 16, 5, 900]
+    table = pool.table([x + 40 for x in lens0])
+    k4, v4 = pool.k.unsqueeze(0), pool.v.unsqueeze(0)
+    summary = torch.zeros(500, H, 2, d, dtype=torch.bfloat16, device=DEV)
+    q = normal(pool.g, n, H * G, d)
+    rows = [(normal(pool.g, n, H, d), normal(pool.g, n, H, d)) for _ in range(24)]
+    rope = K.Rope(1e4, d)
+    slots = [torch.tensor([int(table[s, (lens0[s] + t) // P]) * P + (lens0[s] + t) % P for s in range(n)], device=DEV)
+             for t in range(24)]
+    pos = [torch.tensor([lens0[s] + t for s in range(n)], device=DEV) for t in range(24)]
+    lens = [i32([x + t + 1 for x in lens0]) for t in range(24)]
+    ids = i32([int(table[s, j]) for s in range(n) for j in range(-(-(lens0[s] + 24) // P))])
+    full = torch.full_like(ids, P)
+    start, before = torch.clone(pool.k), torch.clone(pool.v)
+
+    def steps(wait):
+        pool.k.copy_(start)
+        pool.v.copy_(before)
+        got = []
+        for t in range(24):
+            turned = K.kamera_append_kv(k4, v4, *rows[t], rope, pos[t], slots[t], q=q)
+            wait()
+            got += K.kamera_attend_shared(pool.k, pool.v, turned, P, i32([0, 3, n]), table[:2].contiguous(),
+                                          i32([600, 20]), table, lens[t], 3, 600, 1240)
+            wait()
+            K.kamera_summarize_pages(pool.k, P, ids, full, summary)
+            wait()
+            sel = K.kamera_select_pages(turned, summary, P, table, lens[t], 1240, 9)
+            wait()
+            got += [sel, *K.kamera_attend_selected(pool.k, pool.v, turned, P, table, lens[t], sel, 1240)]
+            wait()
+        return got
+
+    alone = steps(torch.cuda.synchronize)
+    for _ in range(5):
+        together = steps(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone, together))
 
 
 def test_selecting_every_page_is_dense_attention():

@@ -65,7 +65,8 @@ APPEND_REFUSED = [
     (dict(q_out=BASE + 128 * MB), INVALID),                            # over k
     (dict(q_out=BASE + 64 * MB), INVALID), (dict(k=BASE + 16), INVALID),   # the pool itself
     (dict(q_out=BASE + 130 * MB, q_out_stride=520), INVALID),          # in place with other strides
-    (dict(base=0.0), INVALID),
+    (dict(base=0.0), INVALID), (dict(n_tokens=1, q_head_stride=68), MISALIGNED),
+    (dict(n_tokens=1, k=BASE + 128 * MB + 8), MISALIGNED),
 ]
 
 
@@ -114,7 +115,7 @@ SHARED_REFUSED = [
     (dict(out=BASE + 128 * MB), INVALID), (dict(out=BASE + 64 * MB), INVALID), (dict(lse=BASE + 129 * MB), INVALID),
     (dict(pages=0), INVALID), (dict(group_start=0), INVALID), (dict(prefix_lens=0), INVALID), (dict(q=0), INVALID),
     (dict(n_seqs=40000), UNSUPPORTED), (dict(max_pages=-1), INVALID), (dict(n_groups=-1), INVALID),
-    (dict(k=0), INVALID), (dict(out=BASE + 133 * MB), INVALID),
+    (dict(k=0), INVALID), (dict(out=BASE + 133 * MB), INVALID), (dict(max_group=0), INVALID),
 ]
 
 
