@@ -366,14 +366,29 @@ struct SelSmem {
     uint64_t cand[kGather];
     int32_t cand_j[kGather];
     float qa[2 * D], qb[2 * D];          // q- | q+: the 16-bit part and the rest
-    uint32_t warp_sum[kWarps];
+    uint32_t warp_sum[kWarps], bin_sum[kWarps], counts[kWarps];
     uint64_t warp_min[kWarps], warp_max[kWarps];
     float lo[kWarps], hi[kWarps], err[kWarps];
-    int32_t bin, above, n_cand, n_inf, n_fin, n_in, n_band;
+    int32_t bin, above, n_cand, n_in, n_band;
 };
 
+// Least and largest of a warp's floats (no NaN among them).
+__device__ __forceinline__ float warp_min(float x)
+{
+    float y;
+    asm("redux.sync.min.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_max(float x)
+{
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Exclusive sum over the block of one value a thread; `total` for everybody.
-template <int NTH>
+// FRESH: nothing has used `warp_sum` before.
+template <int NTH, bool FRESH = false>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, uint32_t& total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -384,19 +399,14 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sum, u
         if (lane >= o)
             x += y;
     }
-    __syncthreads();
+    if (!FRESH)
+        __syncthreads();
     if (lane == 31)
         warp_sum[warp] = x;
     __syncthreads();
-    uint32_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < NTH / 32; ++w) {
-        if (w < warp)
-            before += warp_sum[w];
-        total += warp_sum[w];
-    }
-    return before + x - v;
+    const uint32_t sum = lane < NTH / 32 ? warp_sum[lane] : 0u;
+    total = __reduce_add_sync(0xFFFFFFFFu, sum);
+    return __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0u) + x - v;
 }
 
 // The `need`-th largest key of a set (1 <= need <= its size), by radix steps of 11
@@ -534,66 +544,59 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
     for (int i = tid; i < kBins; i += NTH)
         sm.hist[i] = 0u;
     if (tid == 0)
-        sm.n_cand = sm.n_inf = sm.n_fin = sm.n_in = sm.n_band = 0;
+        sm.n_cand = sm.n_in = sm.n_band = 0;
     __syncthreads();
     ptx::grid_wait();   // the scores
     uint64_t* keys64 = p.keys + (int64_t)blockIdx.x * p.width;
     const float2* scores = reinterpret_cast<const float2*>(keys64);
     int need = p.k - p.n_first - p.n_last;
-    // ---- the scores: finite, +infinity (not finite: first), NaN (no such page: last)
+    // ---- the scores, page i NTH + tid a thread: finite, +infinity (not finite: first),
+    // NaN (no such page: last)
     float v[NK], smin = INFINITY, smax = -INFINITY, err = 0.f;
     int n_inf = 0, n_fin = 0;
     if (need > 0) {
-        float2 x[NK];
+        uint32_t count = 0;   // finite ones, and 2^16 times the others: a row has at most kMaxWidth < 2^16
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            const int j = lo + i * NTH + tid;
-            x[i] = make_float2(0.f, -2.f);
-            if (j < hi)
-                x[i] = scores[j];
-        }
+        for (int i0 = 0; i0 < NK; i0 += 8) {
+            float2 x[8];
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            const bool known = x[i].y >= 0.f || x[i].y != x[i].y;   // (a NaN bound comes of a NaN box)
-            const bool fin = known && fabsf(x[i].x) <= 3.402823466e38f;
-            v[i] = fin ? x[i].x : known ? INFINITY : __int_as_float(0x7FC00000);
-            if (known)
-                err = fmaxf(err, x[i].y == x[i].y ? x[i].y : INFINITY);
-            if (fin) {
-                smin = fminf(smin, v[i]);
-                smax = fmaxf(smax, v[i]);
+            for (int i = 0; i < 8; ++i) {
+                const int j = (i0 + i) * NTH + tid;
+                x[i] = make_float2(0.f, -2.f);
+                if (j >= lo && j < hi)
+                    x[i] = scores[j];
             }
-            n_fin += fin;
-            n_inf += known && !fin;
-        }
 #pragma unroll
-        for (int o = 16; o >= 1; o /= 2) {
-            smin = fminf(smin, __shfl_xor_sync(0xFFFFFFFFu, smin, o));
-            smax = fmaxf(smax, __shfl_xor_sync(0xFFFFFFFFu, smax, o));
-            err = fmaxf(err, __shfl_xor_sync(0xFFFFFFFFu, err, o));
+            for (int i = 0; i < 8; ++i) {
+                const bool known = x[i].y >= 0.f || x[i].y != x[i].y;   // (a NaN bound comes of a NaN box)
+                const bool fin = known && fabsf(x[i].x) <= 3.402823466e38f;
+                v[i0 + i] = fin ? x[i].x : known ? INFINITY : __int_as_float(0x7FC00000);
+                if (known)
+                    err = fmaxf(err, x[i].y == x[i].y ? x[i].y : INFINITY);
+                if (fin) {
+                    smin = fminf(smin, x[i].x);
+                    smax = fmaxf(smax, x[i].x);
+                }
+                count += fin ? 1u : known ? 0x10000u : 0u;
+            }
         }
-        n_fin = __reduce_add_sync(0xFFFFFFFFu, n_fin);
-        n_inf = __reduce_add_sync(0xFFFFFFFFu, n_inf);
+        smin = warp_min(smin);
+        smax = warp_max(smax);
+        err = warp_max(err);
+        count = __reduce_add_sync(0xFFFFFFFFu, count);
         if (lane == 0) {
             sm.lo[warp] = smin;
             sm.hi[warp] = smax;
             sm.err[warp] = err;
-            atomicAdd(&sm.n_fin, n_fin);
-            if (n_inf)
-                atomicAdd(&sm.n_inf, n_inf);
+            sm.counts[warp] = count;
         }
         __syncthreads();
-        smin = lane < NW ? sm.lo[lane] : INFINITY;
-        smax = lane < NW ? sm.hi[lane] : -INFINITY;
-        err = lane < NW ? sm.err[lane] : 0.f;
-#pragma unroll
-        for (int o = 16; o >= 1; o /= 2) {
-            smin = fminf(smin, __shfl_xor_sync(0xFFFFFFFFu, smin, o));
-            smax = fmaxf(smax, __shfl_xor_sync(0xFFFFFFFFu, smax, o));
-            err = fmaxf(err, __shfl_xor_sync(0xFFFFFFFFu, err, o));
-        }
-        n_fin = sm.n_fin;
-        n_inf = sm.n_inf;
+        smin = warp_min(lane < NW ? sm.lo[lane] : INFINITY);
+        smax = warp_max(lane < NW ? sm.hi[lane] : -INFINITY);
+        err = warp_max(lane < NW ? sm.err[lane] : 0.f);
+        count = __reduce_add_sync(0xFFFFFFFFu, lane < NW ? sm.counts[lane] : 0u);
+        n_fin = (int)(count & 0xFFFFu);
+        n_inf = (int)(count >> 16);
     }
     // ---- in: above `in_above`; near: from `near_from` on; ties: the near ones are equal
     enum { kInf, kFinite, kUnknown } border = kFinite;
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
                 c[i] = sm.hist[kBins - 1 - PT * tid - i];
                 mine += c[i];
             }
-            uint32_t above = block_scan<NTH>(mine, sm.warp_sum, total);
+            uint32_t above = block_scan<NTH, true>(mine, sm.bin_sum, total);
 #pragma unroll
             for (int i = 0; i < PT; ++i) {
                 if ((int)above < want && want <= (int)(above + c[i]))
@@ -640,53 +643,46 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
             near_from = __fadd_rd(edge_lo, -e2);
         }
     }
-    // ---- the bitmaps: whole words, so every thread of a warp takes part
-    for (int w = tid; w < words; w += NTH)
-        bm[w] = band[w] = 0u;
-    __syncthreads();
-    auto forced = [&](int j) { return j < n && (j < p.n_first || j >= n - p.n_last); };
-    int n_in = 0, n_near = 0;
-    if (need > 0) {
+    // ---- the bitmaps, a word a warp: pages taken whatever their scores, pages surely in,
+    // pages near the border, which are listed too (the first kGather of them)
+    int n_in = 0;
+    uint64_t near_of = 0;
+    static_assert(NK <= 64, "a bit a page of the thread");
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            const int j = lo + i * NTH + tid;
-            bool take = false, near = false;
-            if (j < hi) {
-                const bool inf = v[i] == INFINITY, unknown = v[i] != v[i];
-                if (border == kInf) {
-                    near = inf;
-                } else if (border == kUnknown) {
-                    take = !unknown;
-                    near = unknown;
-                } else if (!unknown) {
-                    take = inf || v[i] > in_above;
-                    near = !take && v[i] >= near_from;
-                }
-            }
-            // pages lo + i NTH + 32 warp .. + 31: two words of the bitmap
-            const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), c = __ballot_sync(0xFFFFFFFFu, near);
-            n_in += __popc(a);
-            n_near += __popc(c);
-            if (lane < 2 && (a | c)) {
-                const int first = lo + i * NTH + 32 * warp, off = first & 31, word = (first >> 5) + lane;
-                const uint32_t wa = lane == 0 ? a << off : off ? a >> (32 - off) : 0u;
-                const uint32_t wc = lane == 0 ? c << off : off ? c >> (32 - off) : 0u;
-                if (wa)
-                    atomicOr(&bm[word], wa);
-                if (wc)
-                    atomicOr(&band[word], wc);
+    for (int i = 0; i < NK; ++i) {
+        const int word = i * NW + warp, j = 32 * word + lane;
+        if (word >= words)
+            break;
+        const bool inside = j >= lo && j < hi;
+        bool take = false, near = false;
+        if (need > 0 && inside) {
+            const bool inf = v[i] == INFINITY, unknown = v[i] != v[i];
+            if (border == kInf) {
+                near = inf;
+            } else if (border == kUnknown) {
+                take = !unknown;
+                near = unknown;
+            } else if (!unknown) {
+                take = inf || v[i] > in_above;
+                near = !take && v[i] >= near_from;
             }
         }
+        const uint32_t a = __ballot_sync(0xFFFFFFFFu, take), c = __ballot_sync(0xFFFFFFFFu, near);
+        const uint32_t always = __ballot_sync(0xFFFFFFFFu, j < n && !inside);
+        n_in += __popc(a);
         if (lane == 0) {
-            atomicAdd(&sm.n_in, n_in);
-            atomicAdd(&sm.n_band, n_near);
+            bm[word] = a | always;
+            band[word] = c;
         }
+        near_of |= (uint64_t)near << i;
     }
-    for (int j = tid; j < p.n_first; j += NTH)
-        if (forced(j))
-            atomicOr(&bm[j >> 5], 1u << (j & 31));
-    for (int j = max(0, n - p.n_last) + tid; j < n; j += NTH)
-        atomicOr(&bm[j >> 5], 1u << (j & 31));
+    for (; near_of; near_of &= near_of - 1ull) {   // outside the unrolled loop: one copy of the code to fetch
+        const int at = atomicAdd(&sm.n_band, 1);
+        if (at < kGather)
+            sm.cand_j[at] = (__ffsll((long long)near_of) - 1) * NTH + tid;
+    }
+    if (lane == 0 && n_in)
+        atomicAdd(&sm.n_in, n_in);
     __syncthreads();
     const uint32_t total_band = (uint32_t)sm.n_band;
     int left = need - sm.n_in;                  // of the near ones
@@ -700,11 +696,7 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
             wb[i] = on ? *reinterpret_cast<const uint64_t*>(&sm.qb[8 * lane + 2 * i]) : 0ull;
         }
         const int32_t* table = p.pages + (int64_t)s * p.max_pages;
-        if (total_band <= (uint32_t)kGather) {   // list the band
-            for (int w = tid; w < words; w += NTH)
-                for (uint32_t e = band[w]; e; e &= e - 1u)
-                    sm.cand_j[atomicAdd(&sm.n_cand, 1)] = 32 * w + __ffs((int)e) - 1;
-            __syncthreads();
+        if (total_band <= (uint32_t)kGather) {
             for (int i = warp; i < (int)total_band; i += NW) {
                 const uint64_t key = exact_key<D>(p, table[sm.cand_j[i]], h, wa, wb, lane);
                 if (lane == 0)
