@@ -129,11 +129,15 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     const int n_pieces = p.selected ? p.n_select * ppp : (len + kPgTok - 1) / kPgTok;
     const int i1 = min(n_pieces, i0 + p.own_split);
     // The prefix kernel may still run beside this one, and the merge that follows
-    // waits for this grid alone: its last CTA stays until the prefix is done.
-    if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
-        ptx::grid_wait();
-    if (i0 >= i1 && p.o)
-        return;   // the merge knows that this slot is empty
+    // waits for this grid alone: its last CTA leaves when the prefix is done.
+    auto leave = [&]() {
+        if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+            ptx::grid_wait();
+    };
+    if (i0 >= i1 && p.o) {   // the merge knows that this slot is empty
+        leave();
+        return;
+    }
     if (threadIdx.x < kPgWarps * NS)
         ptx::mbar_init(ptx::smem_addr(full + threadIdx.x), 1);
     if (threadIdx.x == 0)
@@ -413,8 +417,10 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
             }
         }
     }
-    if (p.o)
+    if (p.o) {
+        leave();
         return;
+    }
     // ---- no workspace: the splits of these rows are this cluster's CTAs; each
     // joins its share of the outputs through distributed shared memory
     namespace cg = cooperative_groups;
@@ -600,6 +606,12 @@ void split_own(PagedParams& p, int64_t pieces, int sms)
     else
         n = pieces / std::min(pieces, std::max<int64_t>(32, units * pieces / (6 * slots)));
     n = std::min<int64_t>(n, 256);
+    const int64_t beside = 3 * (sms - (int64_t)p.n_groups * p.H * p.row_blocks * p.prefix_splits);
+    if (p.n_groups > 0 && beside >= units) {
+        const int64_t few = std::min(beside / units, (pieces + 3) / 4), rounds = (pieces + 4 * few - 1) / (4 * few);
+        if (few < n && 3.4 + 0.8 * (double)rounds <= 6.0 + (p.two_tile ? 2.3 : 1.3) * p.prefix_split)
+            n = few;
+    }
     if (p.n_groups == 0 && n > 8 && n <= 16)
         n = 8;
     int64_t per = (pieces + n - 1) / n;
@@ -615,6 +627,7 @@ void split_prefix(PagedParams& p, int sms)
     const int64_t rows = (int64_t)p.max_group * p.G;
     p.two_tile = rows > 128 ? 1 : 0;
     p.row_blocks = (int32_t)((rows + 255) / 256);
+    p.block_rows = (int32_t)(((rows + p.row_blocks - 1) / p.row_blocks + 31) / 32 * 32);   // whole warps
     const int64_t units = (int64_t)p.n_groups * p.H * p.row_blocks;
     const int64_t tiles = ((int64_t)p.max_prefix + 127) / 128;
     int64_t best = 1;

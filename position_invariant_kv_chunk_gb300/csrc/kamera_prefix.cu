@@ -104,7 +104,7 @@ static_assert(sizeof(PxBars) <= 512, "barrier block");
 // What a CTA does, worked out alike by every role.
 struct PxWork {
     int group, h, split, blk;
-    int s0, rows;            // the group's first sequence, its rows (sequences x G)
+    int s0, rows;            // the group's first sequence; where the CTA's rows (sequences x G) end
     int len;                 // prefix tokens
     int t0, tiles;           // the split's tiles
     int tiles_a, tiles_b;    // tiles of side A, B (0: the side is idle)
@@ -128,7 +128,8 @@ __device__ __forceinline__ void px_work(const PagedParams& p, PxWork& w)
     const int all = w.len > 0 ? (w.len - 1) / kPxTok + 1 : 0;
     w.t0 = w.split * p.prefix_split;
     w.tiles = max(0, min(p.prefix_split, all - w.t0));
-    w.row_a = p.two_tile ? w.blk * 2 * kPxRows : 0;
+    w.row_a = w.blk * p.block_rows;   // one tile of rows: a single block
+    w.rows = min(w.rows, w.row_a + p.block_rows);
     w.row_b = p.two_tile ? w.row_a + kPxRows : 0;
     if (p.two_tile) {
         w.tiles_a = w.row_a < w.rows ? w.tiles : 0;
@@ -148,6 +149,15 @@ __device__ __forceinline__ uint32_t px_v_at(bool two, int t, int tiles)
     return two ? 2u * t + 1 : (t == tiles - 1 ? 2u * tiles - 1 : 2u * t + 2);
 }
 
+// The page of tile t's 16-token piece `lane` (0..7); -1 past the prefix.
+__device__ __forceinline__ int px_page(const PagedParams& p, const PxWork& w, int t, int lane)
+{
+    const int tok = (w.t0 + t) * kPxTok + 16 * lane;
+    return lane < kPxTok / 16 && t < w.tiles && tok < w.len
+               ? __ldg(p.prefix_pages + (int64_t)w.group * p.max_prefix_pages + tok / p.P)
+               : -1;
+}
+
 // The producer of the keys (VALUES false) or the values: every tile of the split,
 // in order, into its places in the ring.  A page lies in one box of `box_rows`
 // rows or in several; lane l looks up and issues box l.  The next tile's pages
@@ -155,24 +165,19 @@ __device__ __forceinline__ uint32_t px_v_at(bool two, int t, int tiles)
 // side by side: a fill is all latency (table, barrier, issue), and one warp
 // doing both had the tensor pipe wait for it.
 template <int D, bool VALUES>
-__device__ void px_producer(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_t ring, int lane)
+__device__ void px_producer(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_t ring, int lane, int first_page)
 {
     using Y = PxLayout<D>;
     const PagedParams& p = L.p;
     const bool two = p.two_tile != 0;
     const int32_t* table = p.prefix_pages + (int64_t)w.group * p.max_prefix_pages;
     const int R = L.box_rows, boxes = kPxTok / R;
-    auto page_at = [&](int t, int off) {   // the page of the tile's token `off`; -1 past the prefix
-        const int tok = (w.t0 + t) * kPxTok + off;
-        return t < w.tiles && tok < w.len ? __ldg(table + tok / p.P) : -1;
-    };
-    // lanes 0..7: the pages of the tile's eight 16-token pieces
-    int next = lane < kPxTok / 16 ? page_at(0, 16 * lane) : -1;
+    int next = first_page;
     int t = 0;
     bool ok = true;
     for (; t < w.tiles; ++t) {
         const int tok0 = (w.t0 + t) * kPxTok, ntok = min(kPxTok, w.len - tok0), page = next;
-        next = lane < kPxTok / 16 ? page_at(t + 1, 16 * lane) : -1;
+        next = px_page(p, w, t + 1, lane);
         const bool in = lane < kPxTok / 16 && 16 * lane < ntok, good = in && page >= 0 && page < p.num_pages;
         if (in && !good)
             raise_err(p.err, KAMERA_DEVERR_SLOT);
@@ -335,6 +340,23 @@ __device__ __forceinline__ float min3(float a, uint32_t b, uint32_t c)
     return d;
 }
 
+// Row `row` of a group counted over the batch, n_seqs x H x G rows: sequence row / G
+// of the group, head h G + row mod G.  The quotient by one multiplication (a group
+// has fewer than 2^24 rows: its blocks of 256 are at most 65535).
+struct RowOf {
+    int64_t first, step;
+    uint32_t inv;   // 2^32 / G, rounded up; 0: G is 1
+    __device__ __forceinline__ RowOf(const PagedParams& p, const PxWork& w)
+        : first(((int64_t)w.s0 * p.H + w.h) * p.G), step((int64_t)(p.H - 1) * p.G),
+          inv(p.G > 1 ? 0xFFFFFFFFu / (uint32_t)p.G + 1u : 0u)
+    {
+    }
+    __device__ __forceinline__ int64_t operator()(int row) const
+    {
+        return first + row + (int64_t)(inv ? __umulhi((uint32_t)row, inv) : (uint32_t)row) * step;
+    }
+};
+
 // The query rows of side a into shared memory (K-major, zero past the group's
 // rows) by the side's 128 threads, a row's pieces on neighbouring lanes; all of
 // a thread's loads are in flight before the first store.
@@ -345,13 +367,13 @@ __device__ __forceinline__ void px_stage_q(const PagedParams& p, const PxWork& w
     constexpr int PC = D / 8, RS = kPxRows / PC, N = kPxRows / RS;   // pieces of a row, rows a step, steps
     uint4 x[N];
     const int c = r % PC;
+    const RowOf row_of(p, w);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int row = w.row0(a) + i * RS + r / PC;
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row < w.rows)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(
-                p.q + (((int64_t)(w.s0 + row / p.G) * p.H + w.h) * p.G + row % p.G) * D + 8 * c));
+            x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + row_of(row) * D + 8 * c));
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -493,8 +515,8 @@ __device__ void px_softmax(const PagedLaunch& L, const PxWork& w, PxBars& b, uin
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_addr(&b.p_full[a][1]));
     }
-    // ---- the partial state: rows through shared memory, so that a warp writes whole
-    // 128-byte lines (Q and the ring are free once both sides are done)
+    // ---- the partial state: a row through shared memory (Q and the ring are free once
+    // both sides are done), copied out in one piece
     if (nt > 0 && ok) {
         if (!wmma16::tile_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(nt - 1) & 1u, &b.abort, p.err, p.wait_ns))
             ok = false;
@@ -504,37 +526,28 @@ __device__ void px_softmax(const PagedLaunch& L, const PxWork& w, PxBars& b, uin
     asm volatile("bar.sync 1, 256;" ::: "memory");
     if (idle)
         return;
-    const int HQ = p.H * p.G, per_row = p.two_tile ? w.split : 2 * w.split + a;
-    auto slot_of = [&](int rr) {
-        return ((int64_t)(w.s0 + rr / p.G) * HQ + w.h * p.G + rr % p.G) * p.slots + per_row;
-    };
-    if (valid)   // a side without tiles leaves the empty state
-        p.ml[slot_of(row)] = nt > 0 && ok ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
-    if (nt == 0 || !ok)
-        return;
     const uint32_t mine = sbase + (uint32_t)(a * kPxRows + r) * Y::kOutRow;
+    if (nt > 0 && ok) {
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tO + 32 * c, o);
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            ptx::sts128(mine + 128 * c + 16 * j, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-    }
-    __syncwarp();
-    const int lane = r & 31, r0 = r & ~31, n = min(32, w.rows - w.row0(a) - r0);
-    constexpr int LR = D / 4, PR = 32 / LR;   // lanes of a row, rows a warp writes at once
-    const int64_t first = lane < n ? slot_of(w.row0(a) + r0 + lane) : 0;
-#pragma unroll 4
-    for (int i = 0; i < n; i += PR) {
-        const int rr = i + lane / LR;
-        const int64_t slot = __shfl_sync(0xFFFFFFFFu, first, rr & 31);
-        if (rr < n) {
-            uint32_t v[4];
-            ptx::lds128(sbase + (uint32_t)(a * kPxRows + r0 + rr) * Y::kOutRow + 16 * (lane % LR), v);
-            *reinterpret_cast<uint4*>(p.o + slot * D + 4 * (lane % LR)) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int j = 0; j < 8; ++j)
+                ptx::sts128(mine + 128 * c + 16 * j, o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
         }
     }
+    if (!valid)
+        return;
+    const int64_t slot = RowOf(p, w)(row) * p.slots + (p.two_tile ? w.split : 2 * w.split + a);
+    const bool some = nt > 0 && ok;   // a side without tiles leaves the empty state
+    p.ml[slot] = some ? make_float2(m_run, l_run) : make_float2(-INFINITY, 0.f);
+    if (!some)
+        return;
+    ptx::fence_proxy_async();
+    ptx::bulk_s2g(p.o + slot * D, mine, D * 4);
+    ptx::bulk_commit();
+    ptx::bulk_wait_all();
 }
 
 template <int D>
@@ -579,6 +592,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         ptx::prefetch_tmap(&L.map_k);
         ptx::prefetch_tmap(&L.map_v);
     }
+    int first_page = -1;   // the producers' first look-up, in flight over the barrier below
+    if (warp == kPxProdK || warp == kPxProdV)
+        first_page = px_page(p, w, 0, lane);
     if (warp == kPxMma) {
         ptx::tmem_alloc(ptx::smem_addr(&b.tmem), Y::kTmCols);
         ptx::tmem_relinquish();
@@ -599,9 +615,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     } else {
         ptx::setmaxnreg_dec<56>();
         if (warp == kPxProdK)
-            px_producer<D, false>(L, w, b, sbase + Y::kRing, lane);
+            px_producer<D, false>(L, w, b, sbase + Y::kRing, lane, first_page);
         else if (warp == kPxProdV)
-            px_producer<D, true>(L, w, b, sbase + Y::kRing, lane);
+            px_producer<D, true>(L, w, b, sbase + Y::kRing, lane, first_page);
         else if (warp == kPxMma && elect_one())
             px_mma<D>(L, w, b, sbase);
     }
