@@ -606,12 +606,6 @@ void split_own(PagedParams& p, int64_t pieces, int sms)
     else
         n = pieces / std::min(pieces, std::max<int64_t>(32, units * pieces / (6 * slots)));
     n = std::min<int64_t>(n, 256);
-    const int64_t beside = 3 * (sms - (int64_t)p.n_groups * p.H * p.row_blocks * p.prefix_splits);
-    if (p.n_groups > 0 && beside >= units) {
-        const int64_t few = std::min(beside / units, (pieces + 3) / 4), rounds = (pieces + 4 * few - 1) / (4 * few);
-        if (few < n && 3.4 + 0.8 * (double)rounds <= 6.0 + (p.two_tile ? 2.3 : 1.3) * p.prefix_split)
-            n = few;
-    }
     if (p.n_groups == 0 && n > 8 && n <= 16)
         n = 8;
     int64_t per = (pieces + n - 1) / n;
