@@ -216,11 +216,11 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
     ptx::grid_wait();
     ptx::grid_launch_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t4 = lane & 3;
-    const int s = blockIdx.y / p.H, h = blockIdx.y - s * p.H;
+    const int s = blockIdx.y, part = blockIdx.x / p.H, h = blockIdx.x - part * p.H;   // a page's heads side by side
     int lo, hi;
     page_range(p, s, lo, hi);
     constexpr int step = kScoreWarps * kScorePages;
-    const int chunk = step * p.sweeps, c0 = lo + (int)blockIdx.x * chunk, c1 = min(c0 + chunk, hi);
+    const int chunk = step * p.sweeps, c0 = lo + part * chunk, c1 = min(c0 + chunk, hi);
     if (c0 >= hi)
         return;
     // the warp's batches: pages first + step k .. + 15
@@ -825,7 +825,7 @@ cudaError_t launch_score(SelectParams& p, int scored, cudaStream_t stream)
                                                (int)ScoreLayout<D>::kBytes);
     if (a != cudaSuccess)
         return a;
-    return launch_after(score_kernel<D>, dim3((unsigned)gx, (unsigned)units), 32 * kScoreWarps, ScoreLayout<D>::kBytes,
+    return launch_after(score_kernel<D>, dim3((unsigned)(gx * p.H), (unsigned)p.n_seqs), 32 * kScoreWarps, ScoreLayout<D>::kBytes,
                         stream, true, p);
 }
 
