@@ -94,6 +94,18 @@ inline cudaError_t launch_after(void (*kernel)(K...), dim3 grid, int block, size
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
 }
 
+// SMs of the current device (152, a GB300's, where it cannot be asked).
+inline int device_sms()
+{
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) {
+        (void)cudaGetLastError();
+        return 152;
+    }
+    return sms;
+}
+
 // 2-D tensor map (a CUtensorMap, 64-byte aligned, at `map`) over a bf16 array
 // of `rows` rows of `width` elements, row_stride elements apart: boxes of
 // box_cols x box_rows, 128-byte swizzle, rows past the end read as zero.

@@ -573,18 +573,6 @@ int box_rows(int P, int most)   // the largest power of two that divides a page,
     return r;
 }
 
-// SMs of the current device (0 when it cannot be asked: the entry point fails).
-int device_sms()
-{
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return 0;
-    }
-    return sms;
-}
-
 // Splits of the own tokens: `pieces` 16-token pieces of each of `units`; three
 // CTAs share an SM.  While a slot's share is at most 1536 tokens, as many splits
 // as fill one round of CTAs (a second, partly filled round would double the
@@ -684,8 +672,7 @@ int plan(const KameraPagedKV* kv, const KameraPagedQuery* q, const KameraPrefixG
     p->n_select = selected ? n_select : 0;
     if (q->n_seqs == 0)
         return KAMERA_OK;
-    const int sms = device_sms();
-    const int s = sms > 0 ? sms : 152;
+    const int s = device_sms();
     const int64_t ppp = kv->page_size / 16;
     if (selected && n_select * ppp > 0x7FFFFFF)
         return KAMERA_ERR_UNSUPPORTED;

@@ -163,16 +163,15 @@ __device__ __forceinline__ uint32_t ordered(float x)
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
-// q- (i < D) or q+ of channel i mod D as a pair of floats.
+// q- (i < D) or q+ of channel i mod D as a pair of floats; q: the G query rows.
 template <int D>
-__device__ __forceinline__ void signed_sum(const SelectParams& p, int s, int h, int i, float& a, float& e)
+__device__ __forceinline__ void signed_sum(const __nv_bfloat16* q, int G, int i, float& a, float& e)
 {
     const int ch = i < D ? i : i - D;
-    const __nv_bfloat16* q = p.q + ((int64_t)s * p.H * p.G + h * p.G) * D + ch;
     a = e = 0.f;
 #pragma unroll 4
-    for (int g = 0; g < p.G; ++g) {
-        const float x = __bfloat162float(q[(int64_t)g * D]);
+    for (int g = 0; g < G; ++g) {
+        const float x = __bfloat162float(q[g * D + ch]);
         pair_add(a, e, i < D ? fminf(x, 0.f) : fmaxf(x, 0.f), 0.f);
         if (x != x)
             a = x;   // fminf and fmaxf drop a NaN
@@ -212,26 +211,45 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
     constexpr int NC = Y::NC, NS = kScoreStages;
     extern __shared__ __align__(16) unsigned char ring_raw[];
     __shared__ __align__(16) __nv_bfloat16 wt[3][2 * D];
+    __shared__ __align__(16) __nv_bfloat16 qs[16 * D];
     __shared__ float norm_s[kScoreWarps];
     ptx::grid_wait();
     ptx::grid_launch_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t4 = lane & 3;
     const int s = blockIdx.y, part = blockIdx.x / p.H, h = blockIdx.x - part * p.H;   // a page's heads side by side
+    // The queries, the first entries of the page table and the sequence's length at
+    // once: one after another they took longer than a batch.
+    const __nv_bfloat16* q = p.q + ((int64_t)s * p.H + h) * p.G * D;
+    for (int i = threadIdx.x; i < p.G * (D / 8); i += 32 * kScoreWarps)
+        ptx::cp_async16(ptx::smem_addr(qs + 8 * i), q + 8 * i);
+    ptx::cp_async_commit();
+    constexpr int step = kScoreWarps * kScorePages;
+    // the warp's batches: pages first + step k .. + 15
+    const int chunk = step * p.sweeps, c0 = p.n_first + part * chunk, first = c0 + warp * kScorePages;
+    const int32_t* table = p.pages + (int64_t)s * p.max_pages;
+    int start[NS];
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+        const int j = first + k * step + lane;
+        start[k] = lane < kScorePages && j < p.max_pages ? table[j] : -1;
+    }
     int lo, hi;
     page_range(p, s, lo, hi);
-    constexpr int step = kScoreWarps * kScorePages;
-    const int chunk = step * p.sweeps, c0 = lo + part * chunk, c1 = min(c0 + chunk, hi);
-    if (c0 >= hi)
+    const int c1 = min(c0 + chunk, hi);
+    if (c0 >= hi) {
+        ptx::cp_async_wait<0>();
         return;
-    // the warp's batches: pages first + step k .. + 15
-    const int32_t* table = p.pages + (int64_t)s * p.max_pages;
-    const int first = c0 + warp * kScorePages;
+    }
     const int count = first < c1 ? (c1 - first + step - 1) / step : 0;
     const uint32_t ring = ptx::smem_addr(ring_raw) + warp * NS * Y::kStage;
     auto entry = [&](int k) {   // this lane's page of batch k as the table has it; -1 past the range
         const int j = first + k * step + lane;
         return k < count && lane < kScorePages && j < c1 ? table[j] : -1;
     };
+#pragma unroll
+    for (int k = 0; k < NS; ++k)
+        if (first + k * step + lane >= c1)
+            start[k] = -1;
     uint32_t known_of[NS];   // the pages of a stage inside the pool
 #pragma unroll
     for (int b = 0; b < NS; ++b)
@@ -262,15 +280,17 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
         }
         ptx::cp_async_commit();
     };
-    int ahead = entry(NS - 1);
+    int ahead = start[NS - 1];
 #pragma unroll
     for (int k = 0; k < NS - 1; ++k)
-        load(k, entry(k), known_of[k]);
+        load(k, start[k], known_of[k]);
+    ptx::cp_async_wait<NS - 1>();   // the queries
+    __syncthreads();
 
     float norm = 0.f;   // the sum of the weights' magnitudes, rounded up
     for (int i = threadIdx.x; i < 2 * D; i += 32 * kScoreWarps) {
         float a, e;
-        signed_sum<D>(p, s, h, i, a, e);
+        signed_sum<D>(qs, p.G, i, a, e);
         a = __fadd_rn(a, e);
         norm = __fadd_ru(norm, fabsf(a));
         wt[0][i] = __float2bfloat16_rn(a);
@@ -536,7 +556,7 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
     }
     for (int i = tid; i < 2 * D; i += NTH) {
         float a, e;
-        signed_sum<D>(p, s, h, i, a, e);
+        signed_sum<D>(p.q + ((int64_t)s * p.H + h) * p.G * D, p.G, i, a, e);
         const float top = __uint_as_float(__float_as_uint(a) & 0xFFFFFF00u);   // 16 significant bits
         sm.qa[i] = top;
         sm.qb[i] = __fadd_rn(__fadd_rn(a, -top), e);
@@ -815,11 +835,14 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
 template <int D>
 cudaError_t launch_score(SelectParams& p, int scored, cudaStream_t stream)
 {
-    // about four CTAs a slot (three CTAs share an SM), so that ragged lengths even out,
-    // before a warp takes more batches
+    // CTAs that run at once: three an SM (six for boxes half the size).  Where a warp has
+    // at most four batches that way, one round of CTAs (32 sequences of 512 pages: 42.0
+    // us with the attention, 46.4 in three rounds); else three, so that ragged lengths
+    // even out (32 x 8192 pages: 119.5 us, 125.7 in one round)
     const int64_t units = (int64_t)p.n_seqs * p.H, step = kScoreWarps * kScorePages;
-    const int64_t batches = (scored + step - 1) / step;
-    p.sweeps = (int)std::max<int64_t>(1, std::min<int64_t>(16, units * batches / (456 * 4)));
+    const int64_t batches = (scored + step - 1) / step, slots = device_sms() * (D == 128 ? 3ll : 6ll);
+    const int64_t each = (units * batches + slots - 1) / slots;
+    p.sweeps = (int)std::max<int64_t>(1, std::min<int64_t>(64, each <= 4 ? each : (each + 2) / 3));
     const int64_t gx = (batches + p.sweeps - 1) / p.sweeps;
     const cudaError_t a = cudaFuncSetAttribute(score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)ScoreLayout<D>::kBytes);
