@@ -41,6 +41,7 @@ using namespace wmma16;
 constexpr int kPgWarps = 4;
 constexpr int kPgThreads = 32 * kPgWarps;
 constexpr int kPgTok = 16;             // tokens of a piece
+constexpr int kMaxCluster = 8;         // splits that a cluster joins
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -93,9 +94,31 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t4 = lane & 3;
     const int seq = blockIdx.y / p.H, h = blockIdx.y - seq * p.H, split = blockIdx.x;
     const int HQ = p.H * p.G, ppp = p.P / kPgTok;   // pieces per page
+    if (threadIdx.x < kPgWarps * NS)
+        ptx::mbar_init(ptx::smem_addr(full + threadIdx.x), 1);
+    if (threadIdx.x == 0) {
+        *abort = 0;
+        ptx::prefetch_tmap(&L.map_k);
+        ptx::prefetch_tmap(&L.map_v);
+    }
+    ptx::fence_barrier_init();
     if (p.n_groups == 0)   // the call's first kernel
         ptx::grid_wait();
     ptx::grid_launch_next();
+
+    // the queries as the B operand: heads 8 nt + gq, channels 16 ks + 2 t4 (+ 8)
+    uint32_t qb[NT][MT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int g = 8 * nt + gq;
+        const uint32_t* qp =
+            reinterpret_cast<const uint32_t*>(p.q + ((int64_t)seq * HQ + h * p.G + min(g, p.G - 1)) * D);
+#pragma unroll
+        for (int ks = 0; ks < MT; ++ks) {
+            qb[nt][ks][0] = g < p.G ? __ldg(qp + 8 * ks + t4) : 0u;
+            qb[nt][ks][1] = g < p.G ? __ldg(qp + 8 * ks + t4 + 4) : 0u;
+        }
+    }
 
     // The warp's pieces are i0 + warp, i0 + warp + 4, ...; lane l looks up the
     // (32 r + l)-th of them: its page (read ahead of the sequence's length, which
@@ -137,29 +160,6 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     if (i0 >= i1 && p.o) {   // the merge knows that this slot is empty
         leave();
         return;
-    }
-    if (threadIdx.x < kPgWarps * NS)
-        ptx::mbar_init(ptx::smem_addr(full + threadIdx.x), 1);
-    if (threadIdx.x == 0)
-        *abort = 0;
-    ptx::fence_barrier_init();
-    if (threadIdx.x == 0) {
-        ptx::prefetch_tmap(&L.map_k);
-        ptx::prefetch_tmap(&L.map_v);
-    }
-
-    // the queries as the B operand: heads 8 nt + gq, channels 16 ks + 2 t4 (+ 8)
-    uint32_t qb[NT][MT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int g = 8 * nt + gq;
-        const uint32_t* qp =
-            reinterpret_cast<const uint32_t*>(p.q + ((int64_t)seq * HQ + h * p.G + min(g, p.G - 1)) * D);
-#pragma unroll
-        for (int ks = 0; ks < MT; ++ks) {
-            qb[nt][ks][0] = g < p.G ? __ldg(qp + 8 * ks + t4) : 0u;
-            qb[nt][ks][1] = g < p.G ? __ldg(qp + 8 * ks + t4 + 4) : 0u;
-        }
     }
     __syncthreads();
 
@@ -429,18 +429,24 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     const int n = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     for (int e = threadIdx.x + rank * kPgThreads; e < p.G * (D / 4); e += n * kPgThreads) {
         const int g = e / (D / 4), i = 4 * (e - g * (D / 4));
-        float m = -INFINITY;
-        for (int r = 0; r < n; ++r)
-            m = fmaxf(m, *cluster.map_shared_rank(cm + g, r));
+        float ms[kMaxCluster], ls[kMaxCluster], m = -INFINITY;   // of every CTA before the first is used
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            ms[r] = r < n ? *cluster.map_shared_rank(cm + g, r) : -INFINITY;
+            ls[r] = r < n ? *cluster.map_shared_rank(cl + g, r) : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            m = fmaxf(m, ms[r]);
         float l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int r = 0; r < n; ++r) {
-            const float lr = *cluster.map_shared_rank(cl + g, r);
-            if (lr == 0.f)
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            if (ls[r] == 0.f)
                 continue;
-            const float f = ex2(*cluster.map_shared_rank(cm + g, r) - m);
+            const float f = ex2(ms[r] - m);
             const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(outs + g * (D + 4) + i, r));
-            l = fmaf(lr, f, l);
+            l = fmaf(ls[r], f, l);
             acc.x = fmaf(v.x, f, acc.x);
             acc.y = fmaf(v.y, f, acc.y);
             acc.z = fmaf(v.z, f, acc.z);
@@ -594,8 +600,8 @@ void split_own(PagedParams& p, int64_t pieces, int sms)
     else
         n = pieces / std::min(pieces, std::max<int64_t>(32, units * pieces / (6 * slots)));
     n = std::min<int64_t>(n, 256);
-    if (p.n_groups == 0 && n > 8 && n <= 16)
-        n = 8;
+    if (p.n_groups == 0 && n > kMaxCluster && n <= 2 * kMaxCluster)
+        n = kMaxCluster;
     int64_t per = (pieces + n - 1) / n;
     per = (per + 3) / 4 * 4;   // whole rounds of the four warps
     p.own_split = (int32_t)std::min(per, pieces);
@@ -633,7 +639,7 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t state_bytes(const PagedParams& p)
 {
-    if (p.prefix_slots == 0 && p.own_slots <= 8)
+    if (p.prefix_slots == 0 && p.own_slots <= kMaxCluster)
         return 0;   // a cluster
     const size_t n = (size_t)p.n_seqs * p.H * p.G * p.slots;
     return align256(n * p.d * 4) + align256(n * 8);
