@@ -13,9 +13,9 @@
 // in two steps:
 //   - every page's score in fp32 on the tensor cores (m16n8k16: 16 pages by the
 //     weights), read-bound.  The box is bf16 and exact; the weights q+, q- enter
-//     as three bf16 parts in three columns of the B operand, and a fourth
-//     column holds their magnitudes: against the magnitudes of the box it gives
-//     the sum of the terms' magnitudes, and with it a bound of the score's error.
+//     as three bf16 parts in three columns of the B operand.  The sum of the
+//     weights' magnitudes times the largest entry of the boxes bounds the sum of
+//     the terms' magnitudes, and with it the score's error.
 //   - the n-th largest of these scores, t, and the largest error bound, E, split
 //     the pages into those surely in (above t + 2 E), surely out (below t - 2 E)
 //     and a few between, which are scored again, exactly to about 2^-40 of their
@@ -24,8 +24,8 @@
 //     addition kept (the two-sum of Knuth, The Art of Computer Programming
 //     vol. 2, 4.2.2).
 // Scoring every page the second way took 127 us where the boxes (32 sequences x 4
-// heads x 7300 pages, 0.47 GB) take 70 us to read: two-sums cost 100 instructions
-// a page and head.
+// heads of up to 8192 pages, 0.47 GB) take 67 us to read: two-sums cost 100
+// instructions a page and head.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -178,8 +178,11 @@ __device__ __forceinline__ void signed_sum(const __nv_bfloat16* q, int G, int i,
     }
 }
 
-constexpr int kScoreWarps = 4;
-constexpr int kScoreStages = 2;  // batches in a warp's ring (three CTAs an SM)
+// Six warps with two batches each: two CTAs an SM, whose start (weights, table) the
+// other covers.  Of 32 x 4 x 8192 pages, with the attention: 114.4 us; three CTAs of
+// four warps 117.2; one of thirteen 115.9; two of four warps with three batches 119.0.
+constexpr int kScoreWarps = 6;
+constexpr int kScoreStages = 2;  // batches in a warp's ring
 constexpr int kScorePages = 16;  // pages of a warp's MMA
 // A score's error: 2 d / 16 MMAs, each a sum of 17 terms no better than truncated
 // fp32, is at most 2 d / 16 x 17 x 2^-23 < 2^-14.9 of the sum of the terms'
@@ -189,9 +192,9 @@ constexpr float kScoreErr = 3.4e-5f;
 // Scores and error bounds of the pages of one (sequence, KV head).  Each warp
 // keeps a ring of batches of 16 boxes, filled by 16-byte async copies (a box of d =
 // 128 is 512 bytes, one copy of a warp), so copies stay in flight while it
-// multiplies; a bulk copy a box was slower (86 us where these take SCORE_US: the
-// copy engine takes about 28 cycles for each).  The sum
-// over channels may run in any order, so a lane feeds the A operand with whole
+// multiplies.  75 us, 6.3 TB/s, for 32 sequences x 4 heads of up to 8192 pages (0.47
+// GB); with a bulk copy a box it took 86 us, as the copy engine takes about 28
+// cycles for each.  The sum over channels may run in any order, so a lane feeds the A operand with whole
 // 16-byte pieces: lane (page gq, t4) reads pieces t4 + 4 j of its page's box, and
 // the B operand holds the weights of the same pieces.  Column gq of B: 0-2 the
 // weights' bf16 parts.  (m16n8k16 takes about 32 cycles of a sub-partition here:
@@ -835,14 +838,15 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
 template <int D>
 cudaError_t launch_score(SelectParams& p, int scored, cudaStream_t stream)
 {
-    // CTAs that run at once: three an SM (six for boxes half the size).  Where a warp has
-    // at most four batches that way, one round of CTAs (32 sequences of 512 pages: 42.0
-    // us with the attention, 46.4 in three rounds); else three, so that ragged lengths
-    // even out (32 x 8192 pages: 119.5 us, 125.7 in one round)
+    // CTAs that run at once: two an SM (four for boxes half the size).  Where a warp has
+    // at most four batches that way, one round of CTAs (32 sequences of 512 pages with
+    // the attention: 42.0 us, 46.4 in three rounds); else three, so that ragged lengths
+    // even out (32 x 8192 pages: 114.4 us, 115.1 in two rounds, 115.5 in four; 125.7 against
+    // 119.5 in one, both with CTAs of four warps)
     const int64_t units = (int64_t)p.n_seqs * p.H, step = kScoreWarps * kScorePages;
-    const int64_t batches = (scored + step - 1) / step, slots = device_sms() * (D == 128 ? 3ll : 6ll);
+    const int64_t batches = (scored + step - 1) / step, slots = device_sms() * (D == 128 ? 2ll : 4ll);
     const int64_t each = (units * batches + slots - 1) / slots;
-    p.sweeps = (int)std::max<int64_t>(1, std::min<int64_t>(64, each <= 4 ? each : (each + 2) / 3));
+    p.sweeps = (int)std::max<int64_t>(1, each <= 4 ? each : (each + 2) / 3);
     const int64_t gx = (batches + p.sweeps - 1) / p.sweeps;
     const cudaError_t a = cudaFuncSetAttribute(score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)ScoreLayout<D>::kBytes);
