@@ -88,7 +88,7 @@ def _link_binding(obj: str) -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING_PATH + ".tmp"
     cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", BUILD_DIR, "-lkamera", "-L", libs,
-           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stderr[-4000:]}")

@@ -21,7 +21,9 @@
 #include <string>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -174,19 +176,28 @@ public:
         side_ = c10::cuda::getStreamFromExternal(handle_, device_.index());
     }
 
-    at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, bool output)
+    at::Tensor empty(at::IntArrayRef shape, at::ScalarType type)
     {
-        const auto options = at::TensorOptions().dtype(type).device(device_);
+        if (!device_.is_cuda())
+            return at::empty(shape, at::TensorOptions().dtype(type).device(device_));
+        // torch's allocation itself: on the way through its dispatcher it takes twice as long
+        auto make = [&] { return at::Tensor(at::detail::empty_cuda(shape, type, device_, std::nullopt)); };
         if (!side_)
-            return at::empty(shape, options);
+            return make();
         at::Tensor t;
         {
             c10::cuda::CUDAStreamGuard g(*side_);
-            t = at::empty(shape, options);
+            t = make();
         }
-        if (output)
-            t.record_stream(current_->unwrap());
+        t.record_stream(current_->unwrap());
         return t;
+    }
+
+    // Bytes of the call's stream, back in its pool when the call returns: what the
+    // stream runs later comes after the kernels that use them.
+    void* borrow(size_t bytes)
+    {
+        return device_.is_cuda() ? c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, handle_) : nullptr;
     }
 
     struct CUstream_st* stream() const { return reinterpret_cast<struct CUstream_st*>(handle_); }
@@ -209,11 +220,8 @@ private:
 };
 
 // A workspace for the call: the caller's tensor, or `need` bytes of the call's stream.
-struct Scratch {
-    at::Tensor own;
-    void* p = nullptr;
-    size_t bytes = 0;
-
+class Scratch {
+public:
     Scratch(Place& on, const at::Tensor* given, size_t need)
     {
         if (given) {
@@ -222,11 +230,22 @@ struct Scratch {
             p = given->data_ptr();
             bytes = given->nbytes();
         } else if (need > 0) {
-            own = on.empty({(int64_t)need}, at::kByte, false);
-            p = own.data_ptr();
-            bytes = need;
+            p = own_ = on.borrow(need);
+            bytes = p ? need : 0;
         }
     }
+    ~Scratch()
+    {
+        if (own_)
+            c10::cuda::CUDACachingAllocator::raw_delete(own_);
+    }
+    Scratch(const Scratch&) = delete;
+    Scratch& operator=(const Scratch&) = delete;
+    void* p = nullptr;
+    size_t bytes = 0;
+
+private:
+    void* own_ = nullptr;
 };
 
 void status(int rc, const char* where)
@@ -360,7 +379,7 @@ PyObject* append(const char* where, Place& on, const at::Tensor& k, const at::Te
     at::Tensor made;
     if (q) {
         if (!q_out) {
-            made = on.empty(q->sizes(), at::kBFloat16, true);
+            made = on.empty(q->sizes(), at::kBFloat16);
             q_out = &made;
         }
         if (q->scalar_type() != at::kBFloat16 || q_out->scalar_type() != at::kBFloat16 || q_out->sizes() != q->sizes() ||
@@ -551,11 +570,11 @@ struct QueryArg {
     void allocate(Place& on, const at::Tensor& q)
     {
         if (!out) {
-            made_out = on.empty(q.sizes(), at::kBFloat16, true);
+            made_out = on.empty(q.sizes(), at::kBFloat16);
             out = &made_out;
         }
         if (want_lse && !lse) {
-            made_lse = on.empty(q.sizes().slice(0, 2), at::kFloat, true);
+            made_lse = on.empty(q.sizes().slice(0, 2), at::kFloat);
             lse = &made_lse;
         }
         c.out = out->data_ptr();
@@ -731,7 +750,7 @@ PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         on.enter(a[11]);
         at::Tensor made;
         if (!given)
-            made = on.empty({q.size(0), H, (int64_t)x.n_select}, at::kInt, true);
+            made = on.empty({q.size(0), H, (int64_t)x.n_select}, at::kInt);
         x.q = q.data_ptr();
         x.summary = summary.data_ptr();
         x.selected = (given ? *given : made).data_ptr<int32_t>();
