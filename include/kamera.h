@@ -795,8 +795,8 @@ size_t kamera_attend_shared_workspace_bytes(const KameraPagedKV* kv, const Kamer
  * [num_slots / P][num_kv_heads][2][head_dim], 16-byte aligned, other pages'
  * entries stay as they are.  Device errors, the entry skipped: SLOT (page
  * outside the pool), LEN (c outside 0..page_size).  The same page twice in a
- * call: each 16-byte piece of its summary is that of either entry.  head_dim a multiple of 8; kv->v is not read
- * and may be NULL.
+ * call: each 16-byte piece of its summary is that of either entry.  head_dim a
+ * multiple of 8; kv->v is not read and may be NULL.
  */
 int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, const int32_t* d_page_tokens, int32_t n,
                            void* summary, int32_t* d_err, struct CUstream_st* stream);
@@ -821,8 +821,9 @@ int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, c
  *             as for kamera_attend_shared
  * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..16, n_first,
  * n_last >= 0 with n_first + n_last <= n_select, page_size a multiple of 16,
- * n_seqs * num_kv_heads <= 65535, at most 49152 pages in max_len.  Device errors: LEN (the sequence read as empty: all -1),
- * SLOT (a page outside num_pages ranks last).
+ * n_seqs * num_kv_heads <= 65535, at most 49152 pages in max_len.  Device errors:
+ * LEN (the sequence read as empty: all -1), SLOT (a page outside num_pages ranks
+ * last).
  */
 typedef struct KameraPageSelect {
     const void* q;

@@ -82,15 +82,14 @@ uint64_t turn_fraction(double theta)
 __device__ __forceinline__ uint4 ldg_row(const __nv_bfloat16* p)
 {
     uint4 v;   // read once: keep it out of L1
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
 }
 
 // q may be rotated in place: a unit is read and written by one thread alone, its
-// loads before its stores, so the loads need no order beyond the data's (but not
-// the read-only path).
+// loads before its stores, so the loads need no order beyond the data's.
 template <bool INPLACE>
 __device__ __forceinline__ uint4 unit_load(const __nv_bfloat16* p)
 {

@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
             reinterpret_cast<const uint32_t*>(p.q + ((int64_t)seq * HQ + h * p.G + min(g, p.G - 1)) * D);
 #pragma unroll
         for (int ks = 0; ks < MT; ++ks) {
-            qb[nt][ks][0] = g < p.G ? __ldg(qp + 8 * ks + t4) : 0u;
-            qb[nt][ks][1] = g < p.G ? __ldg(qp + 8 * ks + t4 + 4) : 0u;
+            qb[nt][ks][0] = g < p.G ? qp[8 * ks + t4] : 0u;
+            qb[nt][ks][1] = g < p.G ? qp[8 * ks + t4 + 4] : 0u;
         }
     }
 

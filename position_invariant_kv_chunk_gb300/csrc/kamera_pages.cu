@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(128) summary_kernel(const SummaryParams p)
         uint4 v[16];
 #pragma unroll
         for (int t = 0; t < 16; ++t)   // past the count: the first token again
-            v[t] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + t < c ? t : 0) * p.slot_stride));
+            v[t] = *reinterpret_cast<const uint4*>(src + (t0 + t < c ? t : 0) * p.slot_stride);
 #pragma unroll
         for (int t = 0; t < 16; ++t) {
             const uint32_t w[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
@@ -496,7 +496,7 @@ __device__ __forceinline__ uint64_t exact_key(const SelectParams& p, int page, i
 {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (lane < D / 4)
-        v = __ldg(reinterpret_cast<const uint4*>(p.summary + ((int64_t)page * p.H + h) * (2 * D)) + lane);
+        v = reinterpret_cast<const uint4*>(p.summary + ((int64_t)page * p.H + h) * (2 * D))[lane];
     const uint64_t neg1 = ptx::f2_make(0xBF800000u, 0xBF800000u);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint64_t x = ptx::f2_from_bf16x2(w[0]);

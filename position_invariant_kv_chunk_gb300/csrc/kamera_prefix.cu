@@ -161,7 +161,7 @@ __device__ __forceinline__ int px_page(const PagedParams& p, const PxWork& w, in
 {
     const int tok = (w.t0 + t) * kPxTok + 16 * lane;
     return lane < kPxTok / 16 && t < w.tiles && tok < w.len
-               ? __ldg(p.prefix_pages + (int64_t)w.group * p.max_prefix_pages + tok / p.P)
+               ? p.prefix_pages[(int64_t)w.group * p.max_prefix_pages + tok / p.P]
                : -1;
 }
 
@@ -204,7 +204,7 @@ __device__ void px_producer(const PagedLaunch& L, const PxWork& w, PxBars& b, ui
             for (int e = lane; e < kPxTok * 8 * Y::NB; e += 32) {
                 const int r = e / (8 * Y::NB), c = e % (8 * Y::NB);
                 if (r < ntok && ((mask >> (r >> 4)) & 1u)) {
-                    const int64_t row = (int64_t)__ldg(table + (tok0 + r) / p.P) * p.P + (tok0 + r) % p.P;
+                    const int64_t row = (int64_t)table[(tok0 + r) / p.P] * p.P + (tok0 + r) % p.P;
                     ptx::cp_async16(dst + Y::at(r, c), L.v + row * L.slot_stride + (int64_t)w.h * D + 8 * c);
                 } else {
                     ptx::st_shared_zero16(dst + Y::at(r, c));
@@ -380,7 +380,7 @@ __device__ __forceinline__ void px_stage_q(const PagedParams& p, const PxWork& w
         const int row = w.row0(a) + i * RS + r / PC;
         x[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row < w.rows)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + row_of(row) * D + 8 * c));
+            x[i] = *reinterpret_cast<const uint4*>(p.q + row_of(row) * D + 8 * c);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)

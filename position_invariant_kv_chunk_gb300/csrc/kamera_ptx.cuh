@@ -188,7 +188,9 @@ __device__ __forceinline__ void stg128(void* p, const uint32_t (&v)[4])
 // once every CTA of this grid has said so (or ended); it waits for this grid's
 // completion, and sees its writes, with grid_wait.  A call's first kernel waits
 // for whatever ran before it and only then lets the next one start, so the
-// call's later kernels may read the call's inputs at once; and a grid ends only
+// call's later kernels may read the call's inputs at once (by plain loads: the
+// read-only path is for data that no one writes from the kernel's start on, and a
+// kernel that waits has started); and a grid ends only
 // after the one before it has (some CTA of it waits), so that the next call's
 // wait covers them all.
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
