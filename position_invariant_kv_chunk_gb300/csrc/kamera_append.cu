@@ -18,9 +18,9 @@
 // and its partner half a range on, so both are read and written by one
 // thread).  A CTA owns TT tokens; a thread keeps its unit (pass, head, place)
 // and walks the tokens, so the unit is decoded once and the tokens' loads
-// overlap.  10368 tokens of 28 + 4 heads of 128 (191 MB): 33 us, 5.8 TB/s; 16381
+// overlap.  10368 tokens of 28 + 4 heads of 128 (191 MB): 30.6 us, 6.2 TB/s; 16381
 // latent rows with 16 rope queries (105 MB): 17 us, 6.2 TB/s; a step of 64 tokens
-// 2.5 us, its launch and two dependent loads.
+// 2.4 us, its launch and two dependent loads.
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -189,9 +189,11 @@ __device__ __forceinline__ void store_unit(const AppendParams& p, const Unit& u,
 }
 
 // The rows of a thread's first unit are loaded before anything else: their
-// latency covers the slots', the positions' and the angles'.
+// latency covers the slots', the positions' and the angles'.  Four tokens and two
+// vectors of each are 32 registers of loads: held to 64 in all three CTAs fit an SM
+// instead of two (10368 tokens of 28 + 4 heads of 128: 30.6 us, 33.1 with 87).
 template <int TT, bool INPLACE, bool HALVES>
-__global__ void __launch_bounds__(512) append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(512, HALVES && TT > 1 ? 2 : 0) append_kernel(const __grid_constant__ AppendParams p)
 {
     extern __shared__ __align__(16) float2 cs[];   // [TT][n_freq] cos, sin
     __shared__ int64_t slot_s[TT];                 // -1: this token is not written
@@ -315,8 +317,8 @@ cudaError_t launch_append(AppendParams& p, const RopeParams& r, bool inplace, cu
     // One token a CTA while that leaves SMs idle or barely filled (a decode step is
     // latency); four once the SMs have two CTAs each, so that the set-up (slots,
     // angles) is shared and 64 bytes a thread are in flight: 10368 tokens of 28 + 4
-    // heads of 128 take 47.7 us with one, 34.9 with two, 33.8 with four and 42.3
-    // with eight (too few CTAs fit).
+    // heads of 128 take 30.6 us with four and 34.0 with two (before the registers were
+    // held down 47.7 with one, 34.9 with two, 33.8 with four, 42.3 with eight).
     if (p.n_tokens >= 152 * 8)
         return launch_append_t<4>(p, inplace, stream);
     return launch_append_t<1>(p, inplace, stream);
