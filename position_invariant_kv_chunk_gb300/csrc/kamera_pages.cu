@@ -27,6 +27,7 @@
 // heads of up to 8192 pages, 0.47 GB) take 67 us to read: two-sums cost 100
 // instructions a page and head.
 #include <algorithm>
+#include <cooperative_groups.h>
 #include <cstdint>
 #include <cstring>
 
@@ -191,7 +192,7 @@ constexpr int kScorePages = 16;  // pages of a warp's MMA
 // magnitudes (d = 128).
 constexpr float kScoreErr = 3.4e-5f;
 
-// Scores and error bounds of the pages of one (sequence, KV head).  Each warp
+// Scores and error bounds of the pages of (sequence, KV head) rows.  Each warp
 // keeps a ring of batches of 16 boxes, filled by 16-byte async copies (a box of d =
 // 128 is 512 bytes, one copy of a warp), so copies stay in flight while it
 // multiplies.  75 us, 6.3 TB/s, for 32 sequences x 4 heads of up to 8192 pages (0.47
@@ -201,34 +202,38 @@ constexpr float kScoreErr = 3.4e-5f;
 // the B operand holds the weights of the same pieces.  Column gq of B: 0-2 the
 // weights' bf16 parts.  (m16n8k16 takes about 32 cycles of a sub-partition here:
 // 16 of them a batch leave room for the copies, 32 would not.)
-template <int D>
+template <int D, int WARPS>
 struct ScoreLayout {
     static constexpr int NC = 2 * D / 32;                     // 16-byte pieces of a box that a lane reads
     static constexpr uint32_t kBox = 4 * D;                   // bytes
     static constexpr uint32_t kStage = kScorePages * kBox;    // piece c of row r at c ^ 4 (r & 1): no bank conflicts
-    static constexpr uint32_t kBytes = kScoreWarps * kScoreStages * kStage;
+    static constexpr uint32_t kBytes = WARPS * kScoreStages * kStage;
 };
 
-template <int D>
-__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectParams p)
+template <int D, int WARPS>
+struct ScoreSmem {
+    alignas(16) __nv_bfloat16 wt[3][2 * D];
+    alignas(16) __nv_bfloat16 qs[16 * D];
+    float norm[WARPS];
+};
+
+// The CTA's share (`part`) of the pages of one (sequence, KV head): put(j, score and
+// error bound) for page j of the sequence, weight(i, a, e) for each of the weights
+// q- | q+ (the sum a + e), by one thread each; ready() before the first put.
+template <int D, int WARPS, typename Put, typename Weight, typename Ready>
+__device__ __forceinline__ void score_pages(const SelectParams& p, int s, int h, int part, unsigned char* ring_raw,
+                                            ScoreSmem<D, WARPS>& sm, Put put, Weight weight, Ready ready)
 {
-    using Y = ScoreLayout<D>;
+    using Y = ScoreLayout<D, WARPS>;
     constexpr int NC = Y::NC, NS = kScoreStages;
-    extern __shared__ __align__(16) unsigned char ring_raw[];
-    __shared__ __align__(16) __nv_bfloat16 wt[3][2 * D];
-    __shared__ __align__(16) __nv_bfloat16 qs[16 * D];
-    __shared__ float norm_s[kScoreWarps];
-    ptx::grid_wait();
-    ptx::grid_launch_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, t4 = lane & 3;
-    const int s = blockIdx.y, part = blockIdx.x / p.H, h = blockIdx.x - part * p.H;   // a page's heads side by side
     // The queries, the first entries of the page table and the sequence's length at
     // once: one after another they took longer than a batch.
     const __nv_bfloat16* q = p.q + ((int64_t)s * p.H + h) * p.G * D;
-    for (int i = threadIdx.x; i < p.G * (D / 8); i += 32 * kScoreWarps)
-        ptx::cp_async16(ptx::smem_addr(qs + 8 * i), q + 8 * i);
+    for (int i = threadIdx.x; i < p.G * (D / 8); i += 32 * WARPS)
+        ptx::cp_async16(ptx::smem_addr(sm.qs + 8 * i), q + 8 * i);
     ptx::cp_async_commit();
-    constexpr int step = kScoreWarps * kScorePages;
+    constexpr int step = WARPS * kScorePages;
     // the warp's batches: pages first + step k .. + 15
     const int chunk = step * p.sweeps, c0 = p.n_first + part * chunk, first = c0 + warp * kScorePages;
     const int32_t* table = p.pages + (int64_t)s * p.max_pages;
@@ -293,33 +298,34 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
     __syncthreads();
 
     float norm = 0.f;   // the sum of the weights' magnitudes, rounded up
-    for (int i = threadIdx.x; i < 2 * D; i += 32 * kScoreWarps) {
+    for (int i = threadIdx.x; i < 2 * D; i += 32 * WARPS) {
         float a, e;
-        signed_sum<D>(qs, p.G, i, a, e);
+        signed_sum<D>(sm.qs, p.G, i, a, e);
+        weight(i, a, e);
         a = __fadd_rn(a, e);
         norm = __fadd_ru(norm, fabsf(a));
-        wt[0][i] = __float2bfloat16_rn(a);
-        a = __fadd_rn(a, -__bfloat162float(wt[0][i]));
-        wt[1][i] = __float2bfloat16_rn(a);
-        a = __fadd_rn(a, -__bfloat162float(wt[1][i]));
-        wt[2][i] = __float2bfloat16_rn(a);
+        sm.wt[0][i] = __float2bfloat16_rn(a);
+        a = __fadd_rn(a, -__bfloat162float(sm.wt[0][i]));
+        sm.wt[1][i] = __float2bfloat16_rn(a);
+        a = __fadd_rn(a, -__bfloat162float(sm.wt[1][i]));
+        sm.wt[2][i] = __float2bfloat16_rn(a);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o /= 2)
         norm = __fadd_ru(norm, __shfl_xor_sync(0xFFFFFFFFu, norm, o));
     if (lane == 0)
-        norm_s[warp] = norm;
+        sm.norm[warp] = norm;
     __syncthreads();
     norm = 0.f;
 #pragma unroll
-    for (int i = 0; i < kScoreWarps; ++i)
-        norm = __fadd_ru(norm, norm_s[i]);
+    for (int i = 0; i < WARPS; ++i)
+        norm = __fadd_ru(norm, sm.norm[i]);
     uint4 w[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j)
-        w[j] = gq < 3 ? *reinterpret_cast<const uint4*>(&wt[gq < 3 ? gq : 0][8 * (t4 + 4 * j)])
+        w[j] = gq < 3 ? *reinterpret_cast<const uint4*>(&sm.wt[gq < 3 ? gq : 0][8 * (t4 + 4 * j)])
                       : make_uint4(0u, 0u, 0u, 0u);
-    float2* keys = reinterpret_cast<float2*>(p.keys + ((int64_t)s * p.H + h) * p.width);
+    ready();
     for (int k0 = 0; k0 < count; k0 += NS) {
 #pragma unroll
         for (int u = 0; u < NS; ++u) {   // batch k in stage u
@@ -367,8 +373,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
                     if (j < c1) {
                         const float v = (sc[0][2 * r] + sc[1][2 * r]) + ((sc[0][2 * r + 1] + sc[1][2 * r + 1]) + (r == 0 ? la : lb));
                         const bool finite = fabsf(v) <= 3.402823466e38f;   // else it ranks first
-                        keys[j] = (known_of[u] >> (gq + 8 * r)) & 1u ? make_float2(finite ? v : INFINITY, e)
-                                                                     : make_float2(0.f, -1.f);
+                        put(j, (known_of[u] >> (gq + 8 * r)) & 1u ? make_float2(finite ? v : INFINITY, e)
+                                                                  : make_float2(0.f, -1.f));
                     }
                 }
             }
@@ -376,6 +382,19 @@ __global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectPar
         }
     }
     ptx::cp_async_wait<0>();
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const SelectParams p)
+{
+    extern __shared__ __align__(16) unsigned char ring_raw[];
+    __shared__ ScoreSmem<D, kScoreWarps> sm;
+    ptx::grid_wait();
+    ptx::grid_launch_next();
+    const int s = blockIdx.y, part = blockIdx.x / p.H, h = blockIdx.x - part * p.H;   // a page's heads side by side
+    float2* keys = reinterpret_cast<float2*>(p.keys + ((int64_t)s * p.H + h) * p.width);
+    score_pages<D, kScoreWarps>(
+        p, s, h, part, ring_raw, sm, [&](int j, float2 x) { keys[j] = x; }, [](int, float, float) {}, [] {});
 }
 
 // ------------------------------------------------------------------- choice --
@@ -529,51 +548,50 @@ __device__ __forceinline__ uint64_t exact_key(const SelectParams& p, int page, i
     return ((uint64_t)ordered(t) << 32) | ordered(r);
 }
 
-// One CTA per (sequence, KV head): the pages surely in by their fp32 scores, the
-// exact order of those near the border, and the pages in order from a bitmap.
-// All latency (a chain of barriers and dependent loads, and fetching code that a
-// CTA runs once): 5 us for 2048 pages, 10 us for 8192.  So each thread keeps its NK
-// scores in registers, and one histogram of them is enough: the border lies in the
-// bin that holds the n-th largest score, and whatever is within the errors of that
-// bin counts as near it.
+// What every thread does before the scores are needed: an empty histogram.
+template <int D, int NTH>
+__device__ __forceinline__ void clear_choice(SelSmem<D, NTH>& sm)
+{
+    for (int i = threadIdx.x; i < kBins; i += NTH)
+        sm.hist[i] = 0u;
+    if (threadIdx.x == 0)
+        sm.n_cand = sm.n_in = sm.n_band = 0;
+}
+
+// The exact weights: a 16-bit part and the rest.
+template <int D, int NTH>
+__device__ __forceinline__ void keep_weight(SelSmem<D, NTH>& sm, int i, float a, float e)
+{
+    const float top = __uint_as_float(__float_as_uint(a) & 0xFFFFFF00u);
+    sm.qa[i] = top;
+    sm.qb[i] = __fadd_rn(__fadd_rn(a, -top), e);
+}
+
+// A sequence that has no more pages than are selected: all of them.
+template <int NTH>
+__device__ __forceinline__ void take_all(const SelectParams& p, int s, int h, int n)
+{
+    int32_t* out = p.selected + ((int64_t)s * p.H + h) * p.k;
+    for (int i = threadIdx.x; i < p.k; i += NTH)
+        out[i] = i < n ? i : -1;
+}
+
+// The choice for one (sequence, KV head) by one CTA: the pages surely in by their
+// fp32 scores, the exact order of those near the border, and the pages in order from
+// a bitmap.  All latency (a chain of barriers and dependent loads, and fetching code
+// that a CTA runs once): 5 us for 2048 pages, 10 us for 8192.  So each thread keeps
+// its NK scores in registers, and one histogram of them is enough: the border lies in
+// the bin that holds the n-th largest score, and whatever is within the errors of that
+// bin counts as near it.  keys64: the scores, overwritten; maps: two bitmaps.
 template <int D, int NTH, int NK>
-__global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
+__device__ __forceinline__ void choose(const SelectParams& p, int s, int h, int n, int lo, int hi, uint64_t* keys64,
+                                       uint32_t* maps, SelSmem<D, NTH>& sm)
 {
     constexpr int NW = NTH / 32;
-    extern __shared__ __align__(16) unsigned char sel_raw[];
-    __shared__ SelSmem<D, NTH> sm;
-    const int words = (p.width + 31) >> 5;
-    uint32_t* bm = reinterpret_cast<uint32_t*>(sel_raw);        // pages taken
-    uint32_t* band = bm + words;                                // pages near the border
-    const int s = blockIdx.x / p.H, h = blockIdx.x - s * p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (!p.scored)   // the call's first kernel
-        ptx::grid_wait();
-    ptx::grid_launch_next();
-    int lo, hi;
-    const int n = page_range(p, s, lo, hi);
-    int32_t* out = p.selected + (int64_t)blockIdx.x * p.k;
-    if (h == 0 && tid == 0 && (p.lens[s] < 0 || p.lens[s] > p.max_len))
-        raise_err(p.err, KAMERA_DEVERR_LEN);
-    if (n <= p.k) {   // every page
-        ptx::grid_wait();
-        for (int i = tid; i < p.k; i += NTH)
-            out[i] = i < n ? i : -1;
-        return;
-    }
-    for (int i = tid; i < 2 * D; i += NTH) {
-        float a, e;
-        signed_sum<D>(p.q + ((int64_t)s * p.H + h) * p.G * D, p.G, i, a, e);
-        const float top = __uint_as_float(__float_as_uint(a) & 0xFFFFFF00u);   // 16 significant bits
-        sm.qa[i] = top;
-        sm.qb[i] = __fadd_rn(__fadd_rn(a, -top), e);
-    }
-    for (int i = tid; i < kBins; i += NTH)
-        sm.hist[i] = 0u;
-    if (tid == 0)
-        sm.n_cand = sm.n_in = sm.n_band = 0;
-    __syncthreads();
-    ptx::grid_wait();   // the scores
-    uint64_t* keys64 = p.keys + (int64_t)blockIdx.x * p.width;
+    const int words = (p.width + 31) >> 5, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t* bm = maps;              // pages taken
+    uint32_t* band = maps + words;    // pages near the border
+    int32_t* out = p.selected + ((int64_t)s * p.H + h) * p.k;
     const float2* scores = reinterpret_cast<const float2*>(keys64);
     int need = p.k - p.n_first - p.n_last;
     // ---- the scores, page i NTH + tid a thread: finite, +infinity (not finite: first),
@@ -838,6 +856,111 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
     }
 }
 
+template <int D, int NTH, int NK>
+__global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
+{
+    extern __shared__ __align__(16) unsigned char sel_raw[];
+    __shared__ SelSmem<D, NTH> sm;
+    const int s = blockIdx.x / p.H, h = blockIdx.x - s * p.H;
+    if (!p.scored)   // the call's first kernel
+        ptx::grid_wait();
+    ptx::grid_launch_next();
+    int lo, hi;
+    const int n = page_range(p, s, lo, hi);
+    if (h == 0 && threadIdx.x == 0 && (p.lens[s] < 0 || p.lens[s] > p.max_len))
+        raise_err(p.err, KAMERA_DEVERR_LEN);
+    if (n <= p.k) {
+        ptx::grid_wait();
+        take_all<NTH>(p, s, h, n);
+        return;
+    }
+    for (int i = threadIdx.x; i < 2 * D; i += NTH) {
+        float a, e;
+        signed_sum<D>(p.q + ((int64_t)s * p.H + h) * p.G * D, p.G, i, a, e);
+        keep_weight(sm, i, a, e);
+    }
+    clear_choice(sm);
+    __syncthreads();
+    ptx::grid_wait();   // the scores
+    choose<D, NTH, NK>(p, s, h, n, lo, hi, p.keys + (int64_t)blockIdx.x * p.width, reinterpret_cast<uint32_t*>(sel_raw),
+                       sm);
+}
+
+// Scores and choice in one launch, for rows of at most 2048 pages that leave every
+// row an SM: the CTAs of a cluster score a row's pages into the first one's shared
+// memory, which chooses.  With the attention, against two launches: 32 rows x 4 heads
+// of 2048 pages 43.4 us for 49.0, 8 x 4 19.0 for 20.7, 48 x 2 of 334 pages of 64-wide
+// heads 15.8 for 16.6; one x 4 15.0 for 14.2 (eight CTAs a row where the other form has
+// 22), but 3 us less of host time.
+constexpr int kFusedThreads = 256;
+constexpr int kFusedWidth = 8 * kFusedThreads;
+
+template <int D>
+__global__ void __launch_bounds__(kFusedThreads) score_select_kernel(const SelectParams p)
+{
+    constexpr int WARPS = kFusedThreads / 32;
+    using Y = ScoreLayout<D, WARPS>;
+    extern __shared__ __align__(16) unsigned char ring_raw[];
+    __shared__ ScoreSmem<D, WARPS> score;
+    __shared__ SelSmem<D, kFusedThreads> sm;
+    __shared__ uint64_t keys[kFusedWidth];
+    __shared__ uint32_t maps[2 * kFusedWidth / 32];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int s = blockIdx.y / p.H, h = blockIdx.y - s * p.H, rank = blockIdx.x;
+    cluster.barrier_arrive();
+    clear_choice(sm);
+    ptx::grid_wait();
+    ptx::grid_launch_next();
+    bool peers = false;   // known: every CTA of the cluster runs, and its shared memory may be written
+    float2* at = reinterpret_cast<float2*>(cluster.map_shared_rank(keys, 0));
+    score_pages<D, WARPS>(
+        p, s, h, rank, ring_raw, score, [&](int j, float2 x) { at[j] = x; },
+        [&](int i, float a, float e) {
+            if (rank == 0)
+                keep_weight(sm, i, a, e);
+        },
+        [&] {
+            cluster.barrier_wait();
+            peers = true;
+        });
+    if (!peers)   // a share without pages
+        cluster.barrier_wait();
+    int lo, hi;
+    const int n = page_range(p, s, lo, hi);
+    if (h == 0 && rank == 0 && threadIdx.x == 0 && (p.lens[s] < 0 || p.lens[s] > p.max_len))
+        raise_err(p.err, KAMERA_DEVERR_LEN);
+    if (n <= p.k) {   // (the whole cluster)
+        if (rank == 0)
+            take_all<kFusedThreads>(p, s, h, n);
+        return;
+    }
+    cluster.sync();
+    if (rank == 0)
+        choose<D, kFusedThreads, 8>(p, s, h, n, lo, hi, keys, maps, sm);
+}
+
+// Clusters of the grid's x extent.
+template <typename K, typename... A>
+cudaError_t launch_cluster(K kernel, dim3 grid, int block, size_t smem, cudaStream_t stream, const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = grid.x;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int D>
 cudaError_t launch_score(SelectParams& p, int scored, cudaStream_t stream)
 {
@@ -852,10 +975,10 @@ cudaError_t launch_score(SelectParams& p, int scored, cudaStream_t stream)
     p.sweeps = (int)std::max<int64_t>(1, each <= 4 ? each : (each + 2) / 3);
     const int64_t gx = (batches + p.sweeps - 1) / p.sweeps;
     const cudaError_t a = cudaFuncSetAttribute(score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)ScoreLayout<D>::kBytes);
+                                               (int)ScoreLayout<D, kScoreWarps>::kBytes);
     if (a != cudaSuccess)
         return a;
-    return launch_after(score_kernel<D>, dim3((unsigned)(gx * p.H), (unsigned)p.n_seqs), 32 * kScoreWarps, ScoreLayout<D>::kBytes,
+    return launch_after(score_kernel<D>, dim3((unsigned)(gx * p.H), (unsigned)p.n_seqs), 32 * kScoreWarps, ScoreLayout<D, kScoreWarps>::kBytes,
                         stream, true, p);
 }
 
@@ -864,7 +987,22 @@ cudaError_t launch_select(SelectParams& p, cudaStream_t stream)
 {
     const int64_t units = (int64_t)p.n_seqs * p.H;
     const int scored = p.width - p.n_first - p.n_last;   // at most, of one sequence
-    if (p.width > p.k && scored > 0 && p.k > p.n_first + p.n_last) {
+    const bool score = p.width > p.k && scored > 0 && p.k > p.n_first + p.n_last;
+    const int64_t each = units > 0 ? std::min<int64_t>(8, device_sms() / units) : 0;   // CTAs of a row
+    if (score && p.width <= kFusedWidth && each > 0) {
+        constexpr int WARPS = kFusedThreads / 32;
+        using Y = ScoreLayout<D, WARPS>;
+        const int64_t batches = (scored + WARPS * kScorePages - 1) / (WARPS * kScorePages);
+        const int64_t ctas = std::min(each, batches);
+        p.sweeps = (int)((batches + ctas - 1) / ctas);
+        const cudaError_t e = cudaFuncSetAttribute(score_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)Y::kBytes);
+        if (e != cudaSuccess)
+            return e;
+        return launch_cluster(score_select_kernel<D>, dim3((unsigned)ctas, (unsigned)units), kFusedThreads, Y::kBytes,
+                              stream, p);
+    }
+    if (score) {
         const cudaError_t e = launch_score<D>(p, scored, stream);
         if (e != cudaSuccess)
             return e;

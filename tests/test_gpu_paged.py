@@ -438,6 +438,42 @@ def test_selection_is_the_exact_one(H, G, d, P, k, nf, nl):
     assert np.array_equal(got.cpu().numpy(), select_ref(q, summary, pages, lens, P, k, nf, nl))
 
 
+@pytest.mark.parametrize("n,pages_of_one", [(1, 2048), (1, 2049), (3, 700), (10, 200), (38, 97), (39, 97), (50, 130)])
+def test_selection_of_few_and_many_rows(n, pages_of_one):
+    """Rows that share a launch with their scores, by one to eight CTAs each, and rows
+    that are too many or too long for it; ragged, some with every page taken."""
+    H, G, d, P, k = 4, 3, 64, 16, 9
+    g = torch.Generator(device=DEV).manual_seed(n)
+    lens = [(pages_of_one if s == n - 1 else (s * 37) % pages_of_one) * P - (s % 5 if s else 0) for s in range(n)]
+    lens = [max(x, 0) for x in lens]
+    N = pages_of_one + 5
+    summary = boxes(g, N, H, d)
+    pages = torch.stack([torch.randperm(N, generator=g, device=DEV)[:pages_of_one] for _ in lens]).to(torch.int32)
+    q = normal(g, n, H * G, d)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ref = select_ref(q, summary, pages, lens, P, k, 1, 1)
+    for _ in range(3):
+        got = K.kamera_select_pages(q, summary, P, pages, i32(lens), pages_of_one * P, k, 1, 1, err=err)
+        assert np.array_equal(got.cpu().numpy(), ref)
+    assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("N", [2000, 5000])
+def test_selection_among_many_nearly_equal_pages(N):
+    """More pages near the border than are ranked at once: boxes that differ in one
+    channel by the least bf16 steps there are, and equal ones among them."""
+    H, G, d, P, k = 1, 2, 128, 16, 700
+    g = torch.Generator(device=DEV).manual_seed(N)
+    one = normal(g, 1, H, 1, d).expand(N, H, 2, d).contiguous()
+    steps = torch.randint(0, 500, (N,), generator=g, device=DEV)
+    one[:, 0, :, 3] = (steps.float() * 2.0 ** -30)[:, None].to(torch.bfloat16)
+    pages = torch.randperm(N, generator=g, device=DEV).to(torch.int32)[None]
+    q = normal(g, 1, H * G, d)
+    q[:, :, 3] = 1.0
+    got = K.kamera_select_pages(q, one, P, pages, i32([N * P]), N * P, k, 1, 1)
+    assert np.array_equal(got.cpu().numpy(), select_ref(q, one, pages, [N * P], P, k, 1, 1))
+
+
 def test_selection_ties_go_to_the_lower_page():
     """Few distinct boxes over many pages, and boxes all alike: equal scores by the
     hundred, more than are ranked by comparison, at every level of the search."""
