@@ -651,12 +651,13 @@ __device__ __forceinline__ void choose(const SelectParams& p, int s, int h, int 
         } else if (need - n_inf > n_fin) {
             border = kUnknown;
         } else {
-            // bins of equal width between the least and the largest score; bin(x) grows with
-            // x, and the bin's edges are taken a bin wide of it, which covers its rounding
+            // bins of equal width between the least and the largest score.  The quotient is
+            // good to 2^-20, so a score's bin is off by less than 2^-8 of a bin: the edges are
+            // taken a whole bin wide of it
             const float range = __fadd_ru(smax, -smin);
-            float inv = (float)kBins / range;
+            float inv = __fdividef((float)kBins, range);
             if (!(inv <= 3.402823466e38f))
-                inv = 0.f;   // one value, or as good as one: a single bin
+                inv = 0.f;   // one value, or as good as one (or a range past 2^126): a single bin
 #pragma unroll
             for (int i = 0; i < NK; ++i)
                 if (fabsf(v[i]) <= 3.402823466e38f)
@@ -680,9 +681,9 @@ __device__ __forceinline__ void choose(const SelectParams& p, int s, int h, int 
             }
             __syncthreads();
             const float b = (float)sm.bin, e2 = __fmul_ru(2.f, err);
-            const float w_lo = inv > 0.f ? __fdiv_rd(1.f, inv) : 0.f, w_hi = inv > 0.f ? __fdiv_ru(1.f, inv) : 0.f;
-            const float edge_hi = inv > 0.f ? __fadd_ru(smin, __fmul_ru(b + 2.f, w_hi)) : smax;
-            const float edge_lo = inv > 0.f ? __fadd_rd(smin, b >= 1.f ? __fmul_rd(b - 1.f, w_lo) : -w_hi) : smin;
+            const float w = range * (1.f / (float)kBins);
+            const float edge_hi = inv > 0.f ? __fadd_ru(smin, __fmul_ru(b + 2.f, w)) : smax;
+            const float edge_lo = inv > 0.f ? __fadd_rd(smin, __fmul_rd(b - 1.f, w)) : smin;
             in_above = __fadd_ru(edge_hi, e2);
             near_from = __fadd_rd(edge_lo, -e2);
         }
