@@ -889,10 +889,10 @@ __global__ void __launch_bounds__(NTH) select_kernel(const SelectParams p)
 
 // Scores and choice in one launch, for rows of at most 2048 pages that leave every
 // row an SM: the CTAs of a cluster score a row's pages into the first one's shared
-// memory, which chooses.  With the attention, against two launches: 32 rows x 4 heads
-// of 2048 pages 43.4 us for 49.0, 8 x 4 19.0 for 20.7, 48 x 2 of 334 pages of 64-wide
-// heads 15.8 for 16.6; one x 4 15.0 for 14.2 (eight CTAs a row where the other form has
-// 22), but 3 us less of host time.
+// memory, which chooses.  With the attention, against two launches: 32 sequences x 4
+// heads of 2048 pages 43.4 us for 49.0, 8 x 4 19.0 for 20.7, 48 x 2 of 334 pages of
+// 64-wide heads 15.8 for 16.6; 1 x 4 15.0 for 14.2 (eight CTAs a row where the other
+// form has 22), but 3 us less of host time.
 constexpr int kFusedThreads = 256;
 constexpr int kFusedWidth = 8 * kFusedThreads;
 
