@@ -687,9 +687,10 @@ typedef struct KameraAppendRows {
  *   K[layer][slot_t][h] = bf16( R(p_t) k_t[h] ),  V[layer][slot_t][h] = v_t[h]
  *   q_out_t[h] = bf16( R(p_t) q_t[h] )            (when q is given)
  * R(p): RoPE at position p (KameraRope's layout), components outside the
- * rotary range copied.  The phase is exact to about 2^-34 of a turn over the
- * whole position range, the rotation fp32, one rounding to bf16; values are
- * bit copies.  n_tokens == 0 is a successful no-op.
+ * rotary range copied.  The phase p theta of the fp64 frequency is reduced to one
+ * turn with an error below 2^-34 of a turn over the whole position range and for
+ * frequencies of either sign, then rounded to fp32 (2^-26 of a turn at most); the
+ * rotation is fp32, with one rounding to bf16; values are bit copies.  n_tokens == 0 is a successful no-op.
  */
 int kamera_append_kv(const KameraGqaPool* pool, const KameraAppendRows* rows, const KameraRope* rope, int32_t* d_err,
                      struct CUstream_st* stream);

@@ -10,7 +10,8 @@
 // double-double) times the position modulo 2^64, which reduces the angle to
 // one turn exactly by dropping the carries: three integer multiply-adds in
 // place of fp64, whose rate here is 1/64 of fp32's.  The error, 2^-65 |p| turns
-// from the fraction's last bit, is below 2^-34 turns for every int32 position.
+// from the fraction's last bit, is below 2^-34 turns for every int32 position; the
+// reduced phase then goes to sine and cosine as fp32, rounded by up to 2^-26 turns.
 // Each (token, frequency) is formed once per CTA, into shared memory, and
 // serves every head of K and q.
 //
@@ -21,7 +22,6 @@
 // overlap.  10368 tokens of 28 + 4 heads of 128 (191 MB): 30.6 us, 6.2 TB/s; 16381
 // latent rows with 16 rope queries (105 MB): 17 us, 6.2 TB/s; a step of 64 tokens
 // 2.4 us, its launch and two dependent loads.
-#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -62,22 +62,6 @@ struct AppendParams {
     uint64_t turn[KAMERA_MAX_ROT_DIM / 2];    // theta / 2 pi, in 2^-64 turns
     uint8_t axis[KAMERA_MAX_ROT_DIM / 2];
 };
-
-// theta / (2 pi) modulo 1, in units of 2^-64 (theta finite): the quotient as a
-// double-double, whose integer part drops out of a phase.
-uint64_t turn_fraction(double theta)
-{
-    const double inv_hi = 0.15915494309189535, inv_lo = -9.839338337591243e-18;   // 1 / (2 pi)
-    const double hi = theta * inv_hi;
-    const double lo = std::fma(theta, inv_hi, -hi) + theta * inv_lo;
-    const double f = (hi - std::floor(hi)) * 18446744073709551616.0;   // in [0, 2^64): exact
-    if (!(f >= 0.0) || !(f < 18446744073709551616.0))
-        return 0;   // |theta| so large that no fraction is left
-    const double whole = std::floor(f);
-    const double rest = (f - whole) + lo * 18446744073709551616.0;
-    const uint64_t r = std::fabs(rest) < 4.0e18 ? (uint64_t)(int64_t)std::llrint(rest) : 0;
-    return (uint64_t)whole + r;
-}
 
 __device__ __forceinline__ uint4 ldg_row(const __nv_bfloat16* p)
 {

@@ -1,6 +1,7 @@
 // kamera_hostcheck.h -- argument checks shared by the C entry points (host side).
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 #include <utility>
 
@@ -40,6 +41,24 @@ inline int check_strided(const void* base, int64_t L, int64_t ls, int64_t rows, 
     if (L > 1 && ls < rows * rs)
         return KAMERA_ERR_INVALID_ARGUMENT;
     return KAMERA_OK;
+}
+
+// theta / (2 pi) modulo 1, in units of 2^-64 (theta finite): the quotient as a
+// double-double, whose integer part drops out of a phase.  The fraction is taken
+// of |theta|, where it is exact (x - floor(x) is not for x in (-1, 0)), and negated
+// modulo a turn.
+inline uint64_t turn_fraction(double theta)
+{
+    const double inv_hi = 0.15915494309189535, inv_lo = -9.839338337591243e-18;   // 1 / (2 pi)
+    const double t = std::fabs(theta), hi = t * inv_hi;
+    const double lo = std::fma(t, inv_hi, -hi) + t * inv_lo;
+    const double f = (hi - std::floor(hi)) * 18446744073709551616.0;   // in [0, 2^64): exact
+    const double whole = std::floor(f);
+    const double rest = (f - whole) + lo * 18446744073709551616.0;
+    // (a quotient past 2^51 has no fraction worth the name)
+    const uint64_t r = std::fabs(rest) < 4.0e18 ? (uint64_t)(int64_t)std::llrint(rest) : 0;
+    const uint64_t x = (uint64_t)whole + r;
+    return theta < 0.0 ? 0ull - x : x;
 }
 
 // KameraRope -> RopeParams (defined with the relocation entry points): the
