@@ -62,6 +62,17 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
     asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
     return a;
 }
+// The same of the numbers alone: a NaN gives way to the other operand.
+__device__ __forceinline__ uint32_t min_num_bf16x2(uint32_t a, uint32_t b)
+{
+    asm("min.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return a;
+}
+__device__ __forceinline__ uint32_t max_num_bf16x2(uint32_t a, uint32_t b)
+{
+    asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+    return a;
+}
 
 // A thread takes one 16-byte vector of a page's rows, 16 tokens in flight at a
 // time (a warp reads 512 contiguous bytes of each).  Read-bound: each key once,
@@ -341,7 +352,8 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, int s, int h,
             const uint32_t odd = (uint32_t)(gq & 1) << 6;
             float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};   // two chains
             // the least and the largest entry of the batch's boxes: among the minima (the
-            // first half of a box), among the maxima (every other entry lies between)
+            // first half of a box), among the maxima (every other entry lies between).  A NaN
+            // makes its own page's score NaN, and does not bound the others'
             uint32_t least = 0u, most = 0u;
 #pragma unroll
             for (int j = 0; j < NC; ++j) {
@@ -354,14 +366,14 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, int s, int h,
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (j < NC / 2)
-                        least = min_bf16x2(least, min_bf16x2(a[i], b[i]));
+                        least = min_num_bf16x2(least, min_num_bf16x2(a[i], b[i]));
                     else
-                        most = max_bf16x2(most, max_bf16x2(a[i], b[i]));
+                        most = max_num_bf16x2(most, max_num_bf16x2(a[i], b[i]));
             }
-            most = max_bf16x2(most, least ^ 0x80008000u);
+            most = max_num_bf16x2(most, least ^ 0x80008000u);
 #pragma unroll
             for (int o = 16; o >= 1; o /= 2)
-                most = max_bf16x2(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+                most = max_num_bf16x2(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
             const float e = __fmul_ru(kScoreErr, __fmul_ru(norm, fmaxf(bf16lo(most), bf16hi(most))));
             // columns 0, 1 of pages gq, gq + 8 sit in lanes t4 = 0, column 2 in t4 = 1
             const float la = __shfl_down_sync(0xFFFFFFFFu, sc[0][0] + sc[1][0], 1);
@@ -612,7 +624,7 @@ __device__ __forceinline__ void choose(const SelectParams& p, int s, int h, int 
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool known = x[i].y >= 0.f || x[i].y != x[i].y;   // (a NaN bound comes of a NaN box)
+                const bool known = x[i].y >= 0.f || x[i].y != x[i].y;   // (a NaN bound comes of a NaN query)
                 const bool fin = known && fabsf(x[i].x) <= 3.402823466e38f;
                 v[i0 + i] = fin ? x[i].x : known ? INFINITY : __int_as_float(0x7FC00000);
                 if (known)

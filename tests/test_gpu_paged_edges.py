@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import position_invariant_kv_chunk_gb300 as K
-from tests.test_gpu_paged import DEV, normal
+from tests.test_gpu_paged import DEV, i32, normal, select_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +31,30 @@ def test_append_of_negative_frequencies_is_the_mirror_image(interleaved):
         got.append(pk)
     torch.cuda.synchronize()
     assert torch.equal(got[0], got[1])
+
+
+# ---------------------------------------------------------------- selection --
+def cancelling_boxes(gen, n, d):
+    """Boxes of one point whose large even channels cancel in pairs against a query of
+    ones: what is left of a score is its channel 7, a whole number below 256 times 2^-12,
+    which fp32 sums lose beside terms of up to 2^20."""
+    x = torch.zeros(n, d, dtype=torch.bfloat16, device=DEV)
+    big = normal(gen, n, d // 4).float() * 2.0 ** torch.randint(0, 20, (n, d // 4), generator=gen, device=DEV)
+    x[:, 0::4], x[:, 2::4] = big.to(torch.bfloat16), -big.to(torch.bfloat16)
+    x[:, 7] = ((torch.randperm(n, generator=gen, device=DEV) % 251).float() * 2.0 ** -12).to(torch.bfloat16)
+    return torch.stack([x, x], dim=1)[:, None].contiguous()
+
+
+@pytest.mark.parametrize("d,width", [(128, 400), (64, 400), (128, 2600)])
+def test_selection_beside_a_nan_box(d, width):
+    """A box with a NaN in one even channel, in every sixteen pages: it comes first, and
+    the order of the pages beside it, whose scores fp32 cannot tell apart, stays exact."""
+    P, k = 16, 30 + width // 16
+    g = torch.Generator(device=DEV).manual_seed(71)
+    summary = cancelling_boxes(g, width, d)
+    summary[6::16, 0, :, 4] = float("nan")
+    q = torch.ones(1, 1, d, dtype=torch.bfloat16, device=DEV)
+    pages = torch.arange(width, device=DEV, dtype=torch.int32)[None]
+    got = K.kamera_select_pages(q, summary, P, pages, i32([width * P]), width * P, k)
+    torch.cuda.synchronize()
+    assert np.array_equal(got.cpu().numpy(), select_ref(q, summary, pages, [width * P], P, k, 1, 1))
