@@ -809,9 +809,11 @@ int kamera_summarize_pages(const KameraPagedKV* kv, const int32_t* d_page_ids, c
  *     score_j = sum_g sum_i max(q_gi min_ji, q_gi max_ji)
  * and the n_select highest scores are taken; the first n_first and the last
  * n_last pages are always taken (their summaries are not read), equal scores
- * go to the lower page, a score that is not finite ranks with +infinity.  Scores
- * are held to about 2^-40 of the sum of their terms, so the choice is that of the
- * exact scores unless two differ by less.
+ * go to the lower page, a score that is not finite ranks with +infinity (an
+ * infinite bound on the side that no query of the channel asks for, and zero times
+ * an infinite bound, count as 0; a NaN anywhere makes the score NaN).  Scores
+ * are held to about 2^-40 of the sum of their terms where the terms lie in fp32's
+ * normal range, so the choice is that of the exact scores unless two differ by less.
  *   q         bf16 [n_seqs][num_q_heads][head_dim] (16-byte aligned)
  *   summary   bf16 [num_pages][num_kv_heads][2][head_dim] (16-byte aligned)
  *   selected  int32 [n_seqs][num_kv_heads][n_select] (written): indices into the

@@ -228,6 +228,47 @@ struct ScoreSmem {
     float norm[WARPS];
 };
 
+// A batch with an infinite bound among its boxes, which spoils the tensor cores' sums
+// where its weight is zero (the bound on the side that no query asks for): each page
+// by fp32 sums that leave such entries out, with the sum of its own terms' magnitudes
+// for the error.  Lane r: page r's score and error bound; a score that is not finite
+// has none, as it ranks first whatever its error.  A call, so that the loop around
+// it keeps its registers.
+template <int D, int WARPS>
+__device__ __noinline__ float2 score_infinite(uint32_t stage, const ScoreSmem<D, WARPS>& sm)
+{
+    using Y = ScoreLayout<D, WARPS>;
+    const int lane = threadIdx.x & 31;
+    float2 mine = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int r = 0; r < kScorePages; ++r) {
+        float v = 0.f, mag = 0.f;
+        if (lane < D / 4) {   // a lane, a 16-byte piece
+            uint32_t x[4];
+            ptx::lds128(stage + r * Y::kBox + 16 * (lane ^ ((r & 1) << 2)), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int ch = 8 * lane + i;
+                const float w = __bfloat162float(sm.wt[0][ch]) +
+                                (__bfloat162float(sm.wt[1][ch]) + __bfloat162float(sm.wt[2][ch]));
+                const float y = i & 1 ? bf16hi(x[i >> 1]) : bf16lo(x[i >> 1]);
+                if (!(w == 0.f && fabsf(y) == INFINITY)) {
+                    v = fmaf(w, y, v);
+                    mag = fmaf(fabsf(w), fabsf(y), mag);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o /= 2) {
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            mag += __shfl_xor_sync(0xFFFFFFFFu, mag, o);
+        }
+        if (lane == r)
+            mine = fabsf(v) <= 3.402823466e38f ? make_float2(v, __fmul_ru(kScoreErr, mag)) : make_float2(INFINITY, 0.f);
+    }
+    return mine;
+}
+
 // The CTA's share (`part`) of the pages of one (sequence, KV head): put(j, score and
 // error bound) for page j of the sequence, weight(i, a, e) for each of the weights
 // q- | q+ (the sum a + e), by one thread each; ready() before the first put.
@@ -374,7 +415,16 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, int s, int h,
 #pragma unroll
             for (int o = 16; o >= 1; o /= 2)
                 most = max_num_bf16x2(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-            const float e = __fmul_ru(kScoreErr, __fmul_ru(norm, fmaxf(bf16lo(most), bf16hi(most))));
+            const float top = fmaxf(bf16lo(most), bf16hi(most));
+            if (top == INFINITY) {   // (the warp) an infinite bound: the batch page by page
+                const float2 x = score_infinite<D, WARPS>(ring + u * Y::kStage, sm);
+                const int j = first + k * step + lane;
+                if (lane < kScorePages && j < c1)
+                    put(j, (known_of[u] >> lane) & 1u ? x : make_float2(0.f, -1.f));
+                __syncwarp();
+                continue;
+            }
+            const float e = __fmul_ru(kScoreErr, __fmul_ru(norm, top));
             // columns 0, 1 of pages gq, gq + 8 sit in lanes t4 = 0, column 2 in t4 = 1
             const float la = __shfl_down_sync(0xFFFFFFFFu, sc[0][0] + sc[1][0], 1);
             const float lb = __shfl_down_sync(0xFFFFFFFFu, sc[0][2] + sc[1][2], 1);
@@ -520,27 +570,49 @@ __device__ __forceinline__ void radix_find(SM& sm, uint64_t kmin, uint64_t kmax,
     }
 }
 
-// The exact score of a page (16 bytes of its box to a lane), as an ordered key.
+// A lane's weights for the exact scores: 8 entries' 16-bit parts and remainders, and
+// 0xFFFF for those that are zero.
 template <int D>
-__device__ __forceinline__ uint64_t exact_key(const SelectParams& p, int page, int h, const uint64_t (&wa)[4],
-                                              const uint64_t (&wb)[4], int lane)
+struct ExactWeights {
+    uint64_t a[4], b[4];
+    uint32_t zero[4];
+    __device__ __forceinline__ ExactWeights(const float* qa, const float* qb, int lane)
+    {
+        const bool on = lane < D / 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = on ? *reinterpret_cast<const uint64_t*>(qa + 8 * lane + 2 * i) : 0ull;
+            b[i] = on ? *reinterpret_cast<const uint64_t*>(qb + 8 * lane + 2 * i) : 0ull;
+            const uint64_t any = (a[i] | b[i]) & 0x7FFFFFFF7FFFFFFFull;
+            zero[i] = ((uint32_t)any ? 0u : 0xFFFFu) | ((uint32_t)(any >> 32) ? 0u : 0xFFFF0000u);
+        }
+    }
+};
+
+// The exact score of a page (16 bytes of its box to a lane), as an ordered key.
+// Infinite entries of zero weight count as 0.
+template <int D>
+__device__ __forceinline__ uint64_t exact_key(const SelectParams& p, int page, int h, const ExactWeights<D>& q, int lane)
 {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (lane < D / 4)
         v = reinterpret_cast<const uint4*>(p.summary + ((int64_t)page * p.H + h) * (2 * D))[lane];
     const uint64_t neg1 = ptx::f2_make(0xBF800000u, 0xBF800000u);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] &= ~(__vcmpeq2(w[i] & 0x7FFF7FFFu, 0x7F807F80u) & q.zero[i]);
     uint64_t x = ptx::f2_from_bf16x2(w[0]);
-    uint64_t sum = ptx::f2_mul(wa[0], x), err = ptx::f2_mul(wb[0], x);
+    uint64_t sum = ptx::f2_mul(q.a[0], x), err = ptx::f2_mul(q.b[0], x);
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
         x = ptx::f2_from_bf16x2(w[i]);
-        const uint64_t pr = ptx::f2_mul(wa[i], x);           // exact
+        const uint64_t pr = ptx::f2_mul(q.a[i], x);          // exact
         const uint64_t t = ptx::f2_add(sum, pr);
         const uint64_t z = ptx::f2_fma(sum, neg1, t);        // t - sum
         const uint64_t tz = ptx::f2_fma(z, neg1, t);         // t - z
         const uint64_t r = ptx::f2_add(ptx::f2_fma(tz, neg1, sum), ptx::f2_fma(z, neg1, pr));
-        err = ptx::f2_add(ptx::f2_fma(wb[i], x, err), r);
+        err = ptx::f2_add(ptx::f2_fma(q.b[i], x, err), r);
         sum = t;
     }
     uint32_t s0, s1, e0, e1;
@@ -745,17 +817,11 @@ __device__ __forceinline__ void choose(const SelectParams& p, int s, int h, int 
     int left = need - sm.n_in;                  // of the near ones
     bool lowest = border != kFinite;            // take the lowest pages of the (remaining) band
     if (left > 0 && !lowest && left < (int)total_band) {
-        uint64_t wa[4], wb[4];
-        const bool on = lane < D / 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            wa[i] = on ? *reinterpret_cast<const uint64_t*>(&sm.qa[8 * lane + 2 * i]) : 0ull;
-            wb[i] = on ? *reinterpret_cast<const uint64_t*>(&sm.qb[8 * lane + 2 * i]) : 0ull;
-        }
+        const ExactWeights<D> weights(sm.qa, sm.qb, lane);
         const int32_t* table = p.pages + (int64_t)s * p.max_pages;
         if (total_band <= (uint32_t)kGather) {
             for (int i = warp; i < (int)total_band; i += NW) {
-                const uint64_t key = exact_key<D>(p, table[sm.cand_j[i]], h, wa, wb, lane);
+                const uint64_t key = exact_key<D>(p, table[sm.cand_j[i]], h, weights, lane);
                 if (lane == 0)
                     sm.cand[i] = key;
             }
@@ -775,7 +841,7 @@ __device__ __forceinline__ void choose(const SelectParams& p, int s, int h, int 
             for (int w = warp; w < words; w += NW)
                 for (uint32_t e = band[w]; e; e &= e - 1u) {
                     const int j = 32 * w + __ffs((int)e) - 1;
-                    const uint64_t key = exact_key<D>(p, table[j], h, wa, wb, lane);
+                    const uint64_t key = exact_key<D>(p, table[j], h, weights, lane);
                     if (lane == 0)
                         keys64[j] = key;
                     kmin = min(kmin, key);

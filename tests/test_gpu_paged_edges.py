@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import position_invariant_kv_chunk_gb300 as K
-from tests.test_gpu_paged import DEV, i32, normal, select_ref
+from tests.test_gpu_paged import DEV, boxes, i32, normal, select_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -55,6 +55,44 @@ def test_selection_beside_a_nan_box(d, width):
     summary[6::16, 0, :, 4] = float("nan")
     q = torch.ones(1, 1, d, dtype=torch.bfloat16, device=DEV)
     pages = torch.arange(width, device=DEV, dtype=torch.int32)[None]
+    got = K.kamera_select_pages(q, summary, P, pages, i32([width * P]), width * P, k)
+    torch.cuda.synchronize()
+    assert np.array_equal(got.cpu().numpy(), select_ref(q, summary, pages, [width * P], P, k, 1, 1))
+
+
+@pytest.mark.parametrize("d,width", [(128, 400), (64, 400), (128, 2600), (64, 2600)])
+def test_selection_with_infinite_bounds_that_no_query_asks_for(d, width):
+    """A minimum of -infinity where every query is positive, a maximum of infinity where
+    every query is negative: the score is finite, and the page takes its place by it.
+    Infinities on the side that counts still come first."""
+    H, G, P, n = 2, 3, 16, 2
+    g = torch.Generator(device=DEV).manual_seed(72)
+    summary = boxes(g, width, H, d)
+    sign = torch.where(torch.arange(d, device=DEV) % 3 == 0, -1.0, 1.0)
+    q = ((normal(g, n, H * G, d).abs() + 0.25) * sign).to(torch.bfloat16)
+    summary[2::5, :, 0, 10] = -float("inf")
+    summary[3::7, 1, 1, 9] = float("inf")
+    summary[4::11, 0, 0, 1] = -float("inf")
+    summary[101, 0, 1, 10] = float("inf")
+    lens = [width * P, (width - 70) * P]
+    pages = torch.stack([torch.randperm(width, generator=g, device=DEV) for _ in lens]).to(torch.int32)
+    for k in (5, width // 3):
+        got = K.kamera_select_pages(q, summary, P, pages, i32(lens), max(lens), k)
+        torch.cuda.synchronize()
+        ref = select_ref(q, summary, pages, lens, P, k, 1, 1)
+        assert np.array_equal(got.cpu().numpy(), ref), k
+
+
+@pytest.mark.parametrize("d,width", [(128, 400), (64, 400), (128, 2600)])
+def test_selection_beside_infinite_bounds(d, width):
+    """Pages that fp32 cannot tell apart, with a bound of -infinity that counts for
+    nothing among every sixteen of them."""
+    P, k = 16, 30 + width // 16
+    g = torch.Generator(device=DEV).manual_seed(73)
+    summary = cancelling_boxes(g, width, d)
+    summary[9::16, 0, 0, 4] = -float("inf")
+    q = torch.ones(1, 1, d, dtype=torch.bfloat16, device=DEV)
+    pages = torch.randperm(width, generator=g, device=DEV)[None].to(torch.int32)
     got = K.kamera_select_pages(q, summary, P, pages, i32([width * P]), width * P, k)
     torch.cuda.synchronize()
     assert np.array_equal(got.cpu().numpy(), select_ref(q, summary, pages, [width * P], P, k, 1, 1))
