@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
         tok = 0;
         if (k >= count || token < 0)
             return;
-        if (sel && token >= (len + p.P - 1) / p.P * (int64_t)p.P) {   // past the sequence's last page
+        if (sel && token >= ((int64_t)len + p.P - 1) / p.P * p.P) {   // past the sequence's last page
             raise_err(p.err, KAMERA_DEVERR_SLOT);
             return;
         }

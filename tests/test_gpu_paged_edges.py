@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import position_invariant_kv_chunk_gb300 as K
-from tests.test_gpu_paged import DEV, boxes, i32, normal, select_ref
+from tests import paged_ref as R
+from tests.test_gpu_paged import DEV, Pool, boxes, i32, near, normal, select_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,29 @@ def test_selection_beside_infinite_bounds(d, width):
     got = K.kamera_select_pages(q, summary, P, pages, i32([width * P]), width * P, k)
     torch.cuda.synchronize()
     assert np.array_equal(got.cpu().numpy(), select_ref(q, summary, pages, [width * P], P, k, 1, 1))
+
+
+# ---------------------------------------------------------------- attention --
+@pytest.mark.parametrize("P,cut", [(1024, 0), (1024, 1000), (16, 5)])
+def test_selected_attention_of_lengths_near_2_31(P, cut):
+    """A sequence of nearly 2^31 tokens over a few pages: its last pages are inside it."""
+    H, G, d, n = 1, 4, 64, 0x7FFFFF00 - cut
+    if P == 16:
+        n = 1 << 27                                   # (the table of shorter pages)
+    pool = Pool(81, 6, P, H, d)
+    width = -(-n // P)
+    table = (torch.arange(width, device=DEV) % 6).to(torch.int32)[None]
+    q = normal(pool.g, 1, H * G, d)
+    chosen = [0, 7, width - 2, width - 1]
+    sel = i32([[chosen]])
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = K.kamera_attend_selected(pool.k, pool.v, q, P, table, i32([n]), sel, n, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    slots = np.concatenate([np.arange(j % 6 * P, j % 6 * P + min(P, n - j * P)) for j in chosen])
+    idx = torch.from_numpy(slots).to(DEV)
+    o, l, m, x = R.attention(R.f64(q)[0], R.f64(pool.k[idx])[:, 0], R.f64(pool.v[idx])[:, 0], d ** -0.5)
+    near(out, lse, [(o[g], l[g], m[g], x[g], len(slots)) for g in range(G)], "long")
+    K.kamera_attend_selected(pool.k, pool.v, q, P, table, i32([n - P]), sel, n, err=err)   # the last page is past it
+    torch.cuda.synchronize()
+    assert int(err.item()) == 1
