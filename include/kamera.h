@@ -764,7 +764,9 @@ typedef struct KameraPrefixGroups {
  * the group's sequences are the rows of one tensor-core tile.  Own tokens are
  * read once per sequence and KV head.  fp32 accumulation, softmax weights as
  * bf16 hi + lo pairs, one bf16 rounding of the output; a sequence with no token
- * gets zeros and lse = -infinity.
+ * gets zeros and lse = -infinity.  An infinite value makes its channel of the output
+ * that infinity, or NaN where both signs meet or its weight is below about 2^-100 of
+ * the row's largest (fp32 has nothing left of it); a NaN value makes it NaN.
  *   prefix  NULL (or n_groups 0): no shared prefix
  *   own     the sequences' own tokens (max_len 0: none; pages, lens then unread)
  *   d_workspace, workspace_bytes  device scratch of at least

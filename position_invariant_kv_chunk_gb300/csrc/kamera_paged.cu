@@ -15,7 +15,7 @@
 //     d / 8 registers a thread per eight heads.  P^T passes from the score
 //     fragments to the B operand through 8 x 8 transposes in registers.
 //   - Softmax weights are not bf16 values: they enter as hi + lo pairs (about 16
-//     significant bits), which costs MMAs the tensor pipe has spare.
+//     significant bits, both parts positive), which costs MMAs the tensor pipe has spare.
 //   - Two buffers a warp and three CTAs an SM: with three buffers and two CTAs 32
 //     sequences of 2048 selected tokens take 48.5 us with the selection, so 40.1.
 //     Their 134 MB take 20 us of HBM; the kernel's 25 add the start (three dependent
@@ -331,8 +331,9 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                uint32_t hi, lo;
-                split_hl(x[2 * i], x[2 * i + 1], hi, lo);
+                const uint32_t hi = weight_hi(x[2 * i], x[2 * i + 1]);
+                const uint32_t lo =
+                    pack_bf16x2(fmaf(bf16lo(hi), kLessHi, x[2 * i]), fmaf(bf16hi(hi), kLessHi, x[2 * i + 1]));
                 pb[nt][0][i] = transpose8x8(hi);
                 pb[nt][1][i] = transpose8x8(lo);
             }
@@ -544,15 +545,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const PagedPara
         if (i0 > 0)
             load(i0);
         float f = 0.f;   // a state without weight adds nothing: its output was not written or is zero
+        bool some = false;
         if (i < n) {
             const float2 y = ml[i < n_prefix ? i : i + gap];
-            if (y.y != 0.f) {
+            some = y.y != 0.f;
+            if (some) {
                 f = ex2(y.x - m);
                 if (warp == 0)
                     l = fmaf(y.y, f, l);
             }
         }
-        const uint32_t live = __ballot_sync(0xFFFFFFFFu, f != 0.f);
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, some);
 #pragma unroll
         for (int k = 0; k < PW; ++k) {
             const int j = kMergeWarps * k + warp;

@@ -81,6 +81,19 @@ __device__ __forceinline__ bool group_range(const PagedParams& p, int g, int& s0
     return s0 >= 0 && s1 >= s0 && s1 <= p.n_seqs && s1 - s0 <= p.max_group;
 }
 
+// Softmax weights as the tensor cores take them: hi + lo, two bf16 parts, about 16
+// significant bits (lo is rounded by at most 2^-16 of the weight).  hi is the weight
+// rounded towards zero, its upper half word; lo what is left and 2^-24 of hi.  Both are
+// positive, so that an infinite value reaches the sum as it is; with hi rounded to
+// nearest, lo has half the error but either sign or is zero, and an infinite value
+// became NaN.
+constexpr float kLessHi = -0.99999994f;   // -(1 - 2^-24): lo = weight + kLessHi hi
+
+__device__ __forceinline__ uint32_t weight_hi(float a, float b)
+{
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
 cudaError_t launch_prefix(const PagedLaunch& L, cudaStream_t stream);
 
 }  // namespace kamera

@@ -486,7 +486,7 @@ __device__ void px_softmax(const PagedLaunch& L, const PxWork& w, PxBars& b, uin
             const float ref = m_run == -INFINITY ? 0.f : m_run;
             const uint64_t sl2x2 = ptx::f2_make(__float_as_uint(sl2), __float_as_uint(sl2));
             const uint64_t nmx2 = ptx::f2_make(__float_as_uint(-ref), __float_as_uint(-ref));
-            const uint64_t neg1 = ptx::f2_make(0xBF800000u, 0xBF800000u);
+            const uint64_t less = ptx::f2_make(__float_as_uint(kLessHi), __float_as_uint(kLessHi));
             uint64_t sum2[2] = {0ull, 0ull};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {   // 32 tokens: 16 columns of hi, 16 of lo
@@ -500,8 +500,8 @@ __device__ void px_softmax(const PagedLaunch& L, const PxWork& w, PxBars& b, uin
                     const float p0 = pf_ex2(__uint_as_float(a0)), p1 = pf_ex2(__uint_as_float(a1));
                     const uint64_t pp = ptx::f2_make(__float_as_uint(p0), __float_as_uint(p1));
                     sum2[j & 1] = ptx::f2_add(sum2[j & 1], pp);
-                    ph[j] = pack_bf16x2(p0, p1);
-                    pl[j] = ptx::f2_to_bf16x2(ptx::f2_fma(ptx::f2_from_bf16x2(ph[j]), neg1, pp));
+                    ph[j] = weight_hi(p0, p1);
+                    pl[j] = ptx::f2_to_bf16x2(ptx::f2_fma(ptx::f2_from_bf16x2(ph[j]), less, pp));
                 }
                 tmem_st16(tS + 16 * c, ph);
                 tmem_st16(tS + kPxTok / 2 + 16 * c, pl);

@@ -1,5 +1,7 @@
 """Decode steps over the paged pool at their edges.  Tolerances are those of
-test_gpu_append and test_gpu_paged."""
+test_gpu_append and test_gpu_paged.  (There a weight's split counts 2^-17 in numerator and
+denominator; hi rounded towards zero and lo to nearest are off by 2^-16, in the
+numerator alone: the same sum.)"""
 import numpy as np
 import pytest
 import torch
@@ -123,3 +125,108 @@ def test_selected_attention_of_lengths_near_2_31(P, cut):
     K.kamera_attend_selected(pool.k, pool.v, q, P, table, i32([n - P]), sel, n, err=err)   # the last page is past it
     torch.cuda.synchronize()
     assert int(err.item()) == 1
+
+
+def special(pool, rows, values):
+    """Sets pool.v[row, head, channel] to the values; rows, values: ((row, head, channel), value) pairs."""
+    for (r, h, c), x in zip(rows, values):
+        pool.v[r, h, c] = x
+
+
+def near_with_infinities(out, lse, q, pool, slot_lists, scale, what):
+    """Each channel with an infinite value of one sign is that infinity, with both signs
+    or a NaN it is NaN, and every other one is within the tolerance; an infinite value
+    whose weight fp32 rounds to nothing (zero times infinity) may leave NaN.  slot_lists[s][h]."""
+    n, hq, d = q.shape
+    G = hq // pool.H
+    got, qh, refs = out.clone().view(n, pool.H, G, d), R.f64(q), []
+    for s in range(n):
+        for h in range(pool.H):
+            idx = torch.from_numpy(slot_lists[s][h]).to(DEV)
+            kk, vv = R.f64(pool.k[idx])[:, h], R.f64(pool.v[idx])[:, h]
+            up, down, nan = np.isposinf(vv).any(0), np.isneginf(vv).any(0), np.isnan(vv).any(0)
+            nan |= up & down
+            mine = R.f64(got[s, h])
+            assert np.isnan(mine[:, nan]).all(), what
+            if len(idx):                            # weights relative to each row's largest, in powers of two
+                z = scale * 1.4426950408889634 * (qh[s, h * G:h * G + G] @ kk.T)
+                some = (z - z.max(1, keepdims=True) > -100)[:, :, None] | ~np.isinf(vv)
+                full = some.all(1)                  # [G, d]: every infinite value has weight
+                assert not np.isfinite(mine[:, up | down]).any(), what
+                assert np.isposinf(mine[full & (up & ~nan)]).all(), what
+                assert np.isneginf(mine[full & (down & ~nan)]).all(), what
+            off = torch.from_numpy(up | down | nan).to(DEV)
+            got[s, h, :, off] = 0
+            vv[:, up | down | nan] = 0
+            o, l, m, x = R.attention(qh[s, h * G:h * G + G], kk, vv, scale)
+            refs += [(o[g], l[g], m[g], x[g], len(idx)) for g in range(G)]
+    near(got.view(n, hq, d), lse, refs, what)
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("H,G,d,P,prefix,lens", [
+    (2, 7, 128, 16, 700, [50, 333, 0]),        # prefix and own pages, one side of the prefix kernel
+    (32, 2, 128, 16, 1300, [50, 33]),          # tiles in turn on the two sides
+    (3, 16, 64, 32, 2000, [5, 70, 1, 40] * 6),  # two tiles of rows
+    (1, 3, 64, 16, 0, [700, 1, 33]),           # own pages, joined in a cluster
+    (2, 9, 128, 16, 0, [20, 4000]),            # in a cluster of several CTAs
+    (2, 4, 64, 16, 0, [30000, 17]),            # through the workspace
+])
+def test_shared_infinite_values(H, G, d, P, prefix, lens):
+    n = len(lens)
+    pool = Pool(91 + H + G, -(-prefix // P) + sum(-(-x // P) for x in lens) + 3, P, H, d)
+    pre, own = pool.table([prefix]), pool.table(lens)
+    pool.poison()
+    q = normal(pool.g, n, H * G, d)
+    q[:, :, 0] = 4.0
+    a = R.slots_of(pre[0].tolist(), P, prefix, pool.n_pages)
+    b = [R.slots_of(own[s].tolist(), P, x, pool.n_pages) for s, x in enumerate(lens)]
+    long = int(np.argmax(lens))
+    first = b[long]
+    pool.k[int(first[1]), :, 0] = -60.0            # a weight that fp32 rounds to nothing
+    special(pool, [(int(first[1]), 0, 2), (int(first[0]), H - 1, 3), (int(first[-1]), 0, 5), (int(first[2]), 0, 5),
+                   (int(first[3]), 0, d - 1), (int(first[4]), H - 1, 9), (int(first[16]), 0, 40)],
+            [INF, -INF, INF, -INF, -INF, NAN, INF])
+    if prefix:
+        pool.k[int(a[290]), :, 0] = -60.0
+        special(pool, [(int(a[0]), 0, 17), (int(a[prefix - 1]), H - 1, 20), (int(a[290]), 0, d - 3),
+                       (int(a[150]), 0, 33), (int(a[160]), 0, 33), (int(first[0]), 0, 17)],
+                [INF, -INF, -INF, INF, -INF, -INF])
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    if prefix:
+        out, lse = K.kamera_attend_shared(pool.k, pool.v, q, P, i32([0, n]), pre, i32([prefix]), own, i32(lens), n,
+                                          prefix, max(lens), err=err)
+    else:
+        out, lse = K.kamera_attend_shared(pool.k, pool.v, q, P, None, None, None, own, i32(lens), 0, 0, max(lens),
+                                          err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    near_with_infinities(out, lse, q, pool, [[np.concatenate([a, b[s]])] * H for s in range(n)], d ** -0.5, (H, G, d))
+
+
+@pytest.mark.parametrize("k,G", [(6, 3), (300, 8)])
+def test_selected_infinite_values(k, G):
+    """Infinite values in selected pages count, those in other pages do not."""
+    H, d, P, lens = 2, 128, 16, [9000, 100]
+    pool = Pool(95, sum(-(-x // P) for x in lens) + 2, P, H, d)
+    pages = pool.table(lens)
+    pool.poison()
+    q = normal(pool.g, 2, H * G, d)
+    rng = np.random.default_rng(7)
+    sel = torch.full((2, H, k), -1, dtype=torch.int32, device=DEV)
+    for s in range(2):
+        count = -(-lens[s] // P)
+        for h in range(H):
+            take = np.sort(rng.permutation(count)[:k])
+            sel[s, h, :len(take)] = torch.from_numpy(take).to(DEV)
+    slots = [R.slots_of(pages[s].tolist(), P, x, pool.n_pages) for s, x in enumerate(lens)]
+    for s in range(2):
+        for j in range(0, lens[s], 37):
+            pool.v[int(slots[s][j]), j % H, j % d] = INF if j % 2 else -INF
+    out, lse = K.kamera_attend_selected(pool.k, pool.v, q, P, pages, i32(lens), sel, max(lens))
+    torch.cuda.synchronize()
+    lists = [[np.concatenate([slots[s][j * P:j * P + P] for j in sel[s, h].tolist() if j >= 0]) for h in range(H)]
+             for s in range(2)]
+    near_with_infinities(out, lse, q, pool, lists, d ** -0.5, k)
