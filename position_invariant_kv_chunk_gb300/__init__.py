@@ -808,9 +808,9 @@ def _fast():
     global _FAST
     if _FAST is None:
         load_library()
+        if not os.path.exists(_build.BINDING_PATH):
+            _build.build_binding()   # raises what keeps it from being built
         spec = importlib.util.spec_from_file_location("_kamera_binding", _build.BINDING_PATH)
-        if spec is None or not os.path.exists(_build.BINDING_PATH):
-            raise RuntimeError(f"Kamera binding not found at {_build.BINDING_PATH}; run build()")
         mod = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(mod)
         if mod.abi_version() != ABI_VERSION:

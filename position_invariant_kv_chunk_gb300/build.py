@@ -5,7 +5,9 @@
 ``_build/libkamera.so``, and, against the installed torch's headers, the Python
 binding of the decode-step entry points (``csrc/kamera_binding.cpp`` ->
 ``_build/_kamera_binding.so``).  Rebuilds only when a source or header is newer
-than its library.
+than its library.  The library needs none of what the binding does (g++, Python's
+and torch's headers): without it ``build()`` warns, the entry points that go through
+ctypes work, and those of the binding raise its build error.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -97,17 +100,35 @@ def _link_binding(obj: str) -> None:
         f.write(_torch_version())
 
 
+def build_binding(force: bool = False) -> str:
+    """Builds the Python binding where it is missing or stale (the library is there); raises where it cannot be."""
+    if force or _binding_stale():
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        _link_binding(_compile_binding())
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    lib, binding = force or _stale(LIB_PATH), force or _binding_stale()
-    if not lib and not binding:
-        return LIB_PATH
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=1) as ex:   # the binding compiles beside the library
-        obj = ex.submit(_compile_binding) if binding else None
-        if lib:
-            _build_library(verbose, extra_flags)
-        if obj is not None:
-            _link_binding(obj.result())
+    lib = force or _stale(LIB_PATH)
+    try:
+        binding, why = force or _binding_stale(), None
+    except ImportError as e:   # no torch: nothing to build it against
+        binding, why = False, e
+    if lib or binding:
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        with ThreadPoolExecutor(max_workers=1) as ex:   # the binding compiles beside the library
+            obj = ex.submit(_compile_binding) if binding else None
+            if lib:
+                _build_library(verbose, extra_flags)
+            if obj is not None:
+                try:
+                    _link_binding(obj.result())
+                except (ImportError, OSError, RuntimeError) as e:
+                    why = e
+                    if os.path.exists(BINDING_PATH):   # built from older sources
+                        os.remove(BINDING_PATH)
+    if why is not None:
+        warnings.warn(f"the Kamera library is built, the Python binding of its decode-step entry points is not: {why}")
     return LIB_PATH
 
 

@@ -6,6 +6,7 @@ from fractions import Fraction
 import numpy as np
 import pytest
 
+import position_invariant_kv_chunk_gb300 as K
 from position_invariant_kv_chunk_gb300 import build as B
 
 # pi to 100 decimals
@@ -44,3 +45,58 @@ def test_turn_fraction_is_the_nearest_one(turn_fraction, sign):
 def test_turn_fraction_of_the_negative_is_the_negative(turn_fraction):
     for t in list(1e6 ** (-2.0 * np.arange(64) / 128)) + [7.5, 2.5e3, 1e-18]:
         assert (turn_fraction(float(t)) + turn_fraction(-float(t))) % 2 ** 64 == 0
+
+
+# -------------------------------------------------------------------- build --
+@pytest.fixture
+def elsewhere(tmp_path, monkeypatch):
+    """The build's outputs in an empty folder, the library's compilation left out."""
+    monkeypatch.setattr(B, "BUILD_DIR", str(tmp_path))
+    monkeypatch.setattr(B, "LIB_PATH", str(tmp_path / "libkamera.so"))
+    monkeypatch.setattr(B, "BINDING_PATH", str(tmp_path / "_kamera_binding.so"))
+    monkeypatch.setattr(B, "_build_library", lambda *a: (tmp_path / "libkamera.so").write_text("library"))
+    return tmp_path
+
+
+@pytest.mark.parametrize("where", ["_compile_binding", "_link_binding", "_torch_version"])
+def test_library_is_built_where_the_binding_cannot_be(elsewhere, monkeypatch, where):
+    """No g++ or headers, no libraries to link, no torch: the library is there all the
+    same, ctypes callers go on, and a call through the binding says what is wrong."""
+    def fails(*a):
+        raise (ImportError if where == "_torch_version" else RuntimeError)("no such thing here")
+    if where == "_link_binding":
+        monkeypatch.setattr(B, "_compile_binding", lambda: "x.o")
+    if where == "_torch_version":   # an older binding lies there, for a torch that is gone
+        (elsewhere / "_kamera_binding.so").write_text("older")
+        (elsewhere / "_kamera_binding.so.torch").write_text("older")
+    monkeypatch.setattr(B, where, fails)
+    with pytest.warns(UserWarning, match="no such thing here"):
+        assert B.build() == B.LIB_PATH
+    assert (elsewhere / "libkamera.so").read_text() == "library"
+    with pytest.raises((RuntimeError, ImportError), match="no such thing here"):
+        B.build_binding()
+    if where != "_torch_version":
+        monkeypatch.setattr(K, "_FAST", None)
+        monkeypatch.setattr(K, "load_library", lambda: None)
+        with pytest.raises(RuntimeError, match="no such thing here"):
+            K.kamera_summarize_pages(None, 16, None, None, None)
+
+
+def test_binding_of_older_sources_is_not_kept(elsewhere, monkeypatch):
+    (elsewhere / "_kamera_binding.so").write_text("older")
+
+    def fails():
+        raise RuntimeError("no compiler")
+    monkeypatch.setattr(B, "_compile_binding", fails)
+    with pytest.warns(UserWarning, match="no compiler"):
+        B.build()
+    assert not (elsewhere / "_kamera_binding.so").exists()
+
+
+def test_failing_library_still_raises(elsewhere, monkeypatch):
+    def fails(*a):
+        raise RuntimeError("nvcc failed")
+    monkeypatch.setattr(B, "_build_library", fails)
+    monkeypatch.setattr(B, "_compile_binding", lambda: "x.o")
+    with pytest.raises(RuntimeError, match="nvcc failed"):
+        B.build()
