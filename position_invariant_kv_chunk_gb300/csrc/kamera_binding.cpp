@@ -132,6 +132,27 @@ void exact(const at::Tensor& t, const char* name, at::ScalarType type, at::IntAr
                     shape_text(shape));
 }
 
+// A dimension's stride; 0 where it has one element and none is taken.
+int64_t step(const at::Tensor& t, int64_t dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+
+// Rows [..., H, d] whose heads lie behind one another.
+bool packed(const at::Tensor& t)
+{
+    const int64_t n = t.dim();
+    return t.stride(n - 1) == 1 && (t.size(n - 2) <= 1 || t.stride(n - 2) == t.size(n - 1));
+}
+
+// The same shape, and every element at the same offset.
+bool same_layout(const at::Tensor& a, const at::Tensor& b)
+{
+    if (a.sizes() != b.sizes())
+        return false;
+    for (int64_t i = 0; i < a.dim(); ++i)
+        if (step(a, i) != step(b, i))
+            return false;
+    return true;
+}
+
 // Where a call runs: the device every tensor must live on, its stream.
 class Place {
 public:
@@ -418,14 +439,13 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n)
         bf16(pv, "pool_v");
         bf16(k, "k");
         bf16(v, "v");
-        if (pk.dim() != 4 || pk.stride(3) != 1 || pk.stride(2) != pk.size(3))
+        if (pk.dim() != 4 || !packed(pk))
             value_error("pool_k must be [L, S, H, d] with packed heads");
-        if (pv.strides() != pk.strides() || pv.sizes() != pk.sizes())
+        if (!same_layout(pk, pv))
             value_error("pool_k and pool_v must share shape and strides");
         const int64_t H = pk.size(2), d = pk.size(3), T = k.dim() == 3 ? k.size(0) : -1;
         auto rows = [&](const at::Tensor& t, const char* name) {
-            if (t.dim() != 3 || t.size(0) != T || t.size(1) != H || t.size(2) != d || t.stride(2) != 1 ||
-                (H > 1 && t.stride(1) != d))
+            if (t.dim() != 3 || t.size(0) != T || t.size(1) != H || t.size(2) != d || !packed(t))
                 value_error(std::string(name) + " must be [T, H, d] with packed heads, the same T for k and v");
         };
         rows(k, "k");
@@ -443,7 +463,7 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n)
         pool.k = pk.data_ptr();
         pool.v = pv.data_ptr();
         pool.num_slots = pk.size(1);
-        pool.layer_stride = pk.stride(0);
+        pool.layer_stride = step(pk, 0);
         pool.slot_stride = pk.stride(1);
         return append("kamera_append_kv", on, k, v, a[4], a + 5, T, d,
                       [&](const KameraAppendRows* r, const KameraRope* rope, int32_t* e, struct CUstream_st* s) {
@@ -482,7 +502,7 @@ PyObject* mla_append_kv(PyObject*, PyObject* const* a, Py_ssize_t n)
         pool.rope_dim = size32(rd, "pool");
         pool.kv = p.data_ptr();
         pool.num_slots = p.size(1);
-        pool.layer_stride = p.stride(0);
+        pool.layer_stride = step(p, 0);
         pool.slot_stride = p.stride(1);
         return append("kamera_mla_append_kv", on, kr, c, a[4], a + 5, T, rd,
                       [&](const KameraAppendRows* r, const KameraRope* rope, int32_t* e, struct CUstream_st* s) {
@@ -495,9 +515,9 @@ PyObject* mla_append_kv(PyObject*, PyObject* const* a, Py_ssize_t n)
 KameraPagedKV paged_kv(const at::Tensor& k, const at::Tensor* v, PyObject* page_size)
 {
     bf16(k, "pool_k");
-    if (k.dim() != 3 || k.stride(2) != 1 || k.stride(1) != k.size(2))
+    if (k.dim() != 3 || !packed(k))
         value_error("pool_k must be [S, H, d] (one layer) with packed heads");
-    if (v && (v->scalar_type() != at::kBFloat16 || v->sizes() != k.sizes() || v->strides() != k.strides()))
+    if (v && (v->scalar_type() != at::kBFloat16 || !same_layout(k, *v)))
         value_error("pool_k and pool_v must share type, shape and strides");
     KameraPagedKV kv;
     std::memset(&kv, 0, sizeof(kv));

@@ -230,3 +230,22 @@ def test_selected_infinite_values(k, G):
     lists = [[np.concatenate([slots[s][j * P:j * P + P] for j in sel[s, h].tolist() if j >= 0]) for h in range(H)]
              for s in range(2)]
     near_with_infinities(out, lse, q, pool, lists, d ** -0.5, k)
+
+
+def test_one_head_of_any_head_stride():
+    """A pool of one KV head whose head stride is no row's: appended to and attended over."""
+    S, d, P, T, Hq = 64, 64, 16, 20, 3
+    g = torch.Generator(device=DEV).manual_seed(97)
+    view = lambda x: x.as_strided((1, S, 1, d), (5, d, 40, 1))
+    pk, pv = view(normal(g, S * d)), view(normal(g, S * d))
+    k, v, q = normal(g, T, 1, d), normal(g, T, 1, d), normal(g, 1, Hq, d)
+    slots = torch.randperm(S, generator=g, device=DEV)[:T].contiguous()
+    pk2, pv2 = pk.clone(memory_format=torch.contiguous_format), pv.clone(memory_format=torch.contiguous_format)
+    table, lens = i32([[2, 0, 3]]), i32([41])
+    got = []
+    for a, b in ((pk, pv), (pk2, pv2)):
+        K.kamera_append_kv(a, b, k, v, K.Rope(1e4, d), torch.arange(T, device=DEV), slots)
+        got.append(K.kamera_attend_shared(a[0], b[0], q, P, None, None, None, table, lens, 0, 0, 41))
+    torch.cuda.synchronize()
+    assert torch.equal(pk, pk2) and torch.equal(pv, pv2)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])

@@ -5,6 +5,7 @@ from fractions import Fraction
 
 import numpy as np
 import pytest
+import torch
 
 import position_invariant_kv_chunk_gb300 as K
 from position_invariant_kv_chunk_gb300 import build as B
@@ -100,3 +101,40 @@ def test_failing_library_still_raises(elsewhere, monkeypatch):
     monkeypatch.setattr(B, "_compile_binding", lambda: "x.o")
     with pytest.raises(RuntimeError, match="nvcc failed"):
         B.build()
+
+
+# -------------------------------------------------------------- the binding --
+def one_head(*lead, d=64):
+    """bf16 [*lead, 1, d] whose single head has a stride of its own, which no element takes."""
+    n = int(np.prod(lead))
+    rows = [int(np.prod(lead[i + 1:])) * d for i in range(len(lead))]
+    return torch.zeros(n * d, dtype=torch.bfloat16).as_strided((*lead, 1, d), (*rows, 40, 1))
+
+
+def test_binding_looks_at_no_stride_that_is_not_taken(monkeypatch):
+    """Pools of one head, or of one layer, whose size-1 dimensions have strides of any
+    kind: calls without tokens, which end behind the checks of the pool."""
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: False)
+    bf, i32 = torch.bfloat16, lambda *s: torch.zeros(*s, dtype=torch.int32)
+    none = torch.zeros(0, dtype=torch.int64)
+    rope = K.Rope(1e4, 64)
+    for pk in (one_head(2, 32), torch.zeros(32 * 64, dtype=bf).as_strided((1, 32, 1, 64), (3, 64, 7, 1))):
+        pv = torch.zeros(pk.shape, dtype=bf)
+        rows = torch.zeros(0, 1, 64, dtype=bf)
+        assert K.kamera_append_kv(pk, pv, rows, rows, rope, none, none) is None
+        assert K.kamera_append_kv(pv, pk, rows, rows, rope, none, none) is None
+    pool = torch.zeros(32 * 576, dtype=bf).as_strided((1, 32, 576), (5, 576, 1))
+    assert K.kamera_mla_append_kv(pool, 512, torch.zeros(0, 512, dtype=bf), torch.zeros(0, 64, dtype=bf),
+                                  K.Rope(1e4, 64, 0, K.INTERLEAVED), none, none) is None
+    pk, q = one_head(64), torch.zeros(0, 4, 64, dtype=bf)
+    pv = torch.zeros(pk.shape, dtype=bf)
+    out, lse = K.kamera_attend_shared(pk, pv, q, 16, None, None, None, i32(0, 2), i32(0), 0, 0, 20)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    K.kamera_attend_selected(pk, pv, q, 16, i32(0, 2), i32(0), i32(0, 1, 2), 20)
+    K.kamera_summarize_pages(pk, 16, i32(0), i32(0), torch.zeros(4, 1, 2, 64, dtype=bf))
+    wide = torch.zeros(64, 2, 80, dtype=bf)[:, :, :64]           # two heads that are not packed: refused as before
+    with pytest.raises(ValueError, match="packed heads"):
+        K.kamera_summarize_pages(wide, 16, i32(0), i32(0), torch.zeros(4, 2, 2, 64, dtype=bf))
+    with pytest.raises(ValueError, match="share"):
+        K.kamera_attend_shared(pk, torch.zeros(64, 1, 72, dtype=bf)[:, :, :64], q, 16, None, None, None, i32(0, 2),
+                               i32(0), 0, 0, 20)
