@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import importlib.util
+import operator
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -28,7 +29,8 @@ __all__ = [
     "kamera_ingest_canonical", "kamera_mla_ingest_canonical", "kamera_form_patch", "kamera_attend_reused",
     "kamera_prefill_attend_reused",
     "kamera_append_kv", "kamera_mla_append_kv", "kamera_attend_shared", "kamera_summarize_pages",
-    "kamera_select_pages", "kamera_attend_selected",
+    "kamera_select_pages", "kamera_attend_selected", "kamera_attend_shared_workspace_bytes",
+    "kamera_select_pages_workspace_bytes", "kamera_attend_selected_workspace_bytes",
     "kamera_validate_chunks", "kamera_status_string", "kamera_abi_version",
     "ROTATE_HALF", "INTERLEAVED", "DEVERR",
 ]
@@ -913,3 +915,69 @@ def kamera_attend_selected(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.
     rest as for ``kamera_attend_shared``.  Returns ``(out, lse)``."""
     return (_FAST or _fast()).attend_selected(pool_k, pool_v, q, page_size, pages, lens, selected, max_len, scale, out,
                                               lse, err, stream, workspace)
+
+
+def _int32(x, name: str) -> int:
+    x = operator.index(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} is out of range")
+    return x
+
+
+def _paged_structs(pool_k: torch.Tensor, q: torch.Tensor, page_size: int, max_len: int):
+    """The shapes of a paged attention call, without its arrays."""
+    if pool_k.dim() != 3 or q.dim() != 3 or q.shape[2] != pool_k.shape[2]:
+        raise ValueError("pool_k must be [S_slots, H, d] and q [S, H_q, d]")
+    P = _int32(page_size, "page_size")
+    if P < 1:
+        raise ValueError("page_size must be positive")
+    kv = _PagedKV(None, None, pool_k.shape[0], pool_k.stride(0), pool_k.shape[1], pool_k.shape[2], P, 0)
+    return kv, _PagedQuery(None, None, None, q.shape[0], q.shape[1], 1.0, 0), _page_bounds(P, max_len)
+
+
+def _page_bounds(page_size: int, max_len: int) -> _PageTable:
+    n = _int32(max_len, "max_len")
+    return _PageTable(None, None, -(-n // page_size), n)
+
+
+def _bytes_on(t: torch.Tensor, size, *structs) -> int:
+    """A workspace size by the plan for t's device (its number of SMs)."""
+    args = [C.byref(s) if isinstance(s, C.Structure) else s for s in structs]
+    if not t.is_cuda:
+        return int(size(*args))
+    with torch.cuda.device(t.device):
+        return int(size(*args))
+
+
+def kamera_attend_shared_workspace_bytes(pool_k: torch.Tensor, q: torch.Tensor, page_size: int, n_groups: int,
+                                         max_group: int, max_prefix: int, max_len: int) -> int:
+    """Bytes of the ``workspace`` that ``kamera_attend_shared`` needs on q's device for
+    these bounds (n_groups 0: no shared prefix); 0 where it needs none, and where it
+    would refuse the call."""
+    kv, query, own = _paged_structs(pool_k, q, page_size, max_len)
+    table = _page_bounds(kv.page_size, max_prefix)
+    pre = _PrefixGroups(None, None, None, _int32(n_groups, "n_groups"), table.max_pages, table.max_len,
+                        _int32(max_group, "max_group"))
+    return _bytes_on(q, load_library().kamera_attend_shared_workspace_bytes, kv, query, pre, own)
+
+
+def kamera_attend_selected_workspace_bytes(pool_k: torch.Tensor, q: torch.Tensor, page_size: int, n_select: int,
+                                           max_len: int) -> int:
+    """As ``kamera_attend_shared_workspace_bytes`` for ``kamera_attend_selected`` with
+    n_select pages a sequence and KV head."""
+    kv, query, own = _paged_structs(pool_k, q, page_size, max_len)
+    return _bytes_on(q, load_library().kamera_attend_selected_workspace_bytes, kv, query, own,
+                     C.c_int32(_int32(n_select, "n_select")))
+
+
+def kamera_select_pages_workspace_bytes(q: torch.Tensor, summary: torch.Tensor, page_size: int, max_len: int,
+                                        n_select: int, n_first: int = 1, n_last: int = 1) -> int:
+    """As ``kamera_attend_shared_workspace_bytes`` for ``kamera_select_pages``."""
+    if q.dim() != 3 or summary.dim() != 4 or q.shape[2] != summary.shape[3]:
+        raise ValueError("q must be [S, H_q, d] and summary [n_pages, H, 2, d]")
+    P = _int32(page_size, "page_size")
+    if P < 1:
+        raise ValueError("page_size must be positive")
+    x = _PageSelect(None, None, None, summary.shape[0], q.shape[0], q.shape[1], summary.shape[1], q.shape[2], P,
+                    _int32(n_select, "n_select"), _int32(n_first, "n_first"), _int32(n_last, "n_last"))
+    return _bytes_on(q, load_library().kamera_select_pages_workspace_bytes, x, _page_bounds(P, max_len))

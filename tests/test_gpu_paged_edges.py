@@ -249,3 +249,30 @@ def test_one_head_of_any_head_stride():
     torch.cuda.synchronize()
     assert torch.equal(pk, pk2) and torch.equal(pv, pv2)
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_workspaces_of_the_size_that_is_given():
+    """A workspace of exactly the bytes that Python names is enough, one less is refused."""
+    H, G, d, P, lens = 2, 7, 128, 16, [700, 33]
+    pool = Pool(98, 120, P, H, d)
+    pre, own = pool.table([600]), pool.table(lens)
+    pool.poison()
+    q = normal(pool.g, 2, H * G, d)
+    summary, select = boxes(pool.g, 120, H, d), i32([[list(range(43))] * H] * 2)
+    calls = [
+        (K.kamera_attend_shared_workspace_bytes(pool.k, q, P, 1, 2, 600, 700),
+         lambda **w: K.kamera_attend_shared(pool.k, pool.v, q, P, i32([0, 2]), pre, i32([600]), own, i32(lens), 2, 600, 700,
+                                            **w)[0]),
+        (K.kamera_select_pages_workspace_bytes(q, summary, P, 700, 9),
+         lambda **w: K.kamera_select_pages(q, summary, P, own, i32(lens), 700, 9, **w)),
+        (K.kamera_attend_selected_workspace_bytes(pool.k, q, P, 43, 700),
+         lambda **w: K.kamera_attend_selected(pool.k, pool.v, q, P, own, i32(lens), select, 700, **w)[0]),
+    ]
+    assert [n > 0 for n, _ in calls] == [True, True, False]     # the last one's splits join in a cluster
+    for n, call in calls:
+        room = torch.empty(n, dtype=torch.uint8, device=DEV)
+        assert torch.equal(call(), call(workspace=room))
+        if n:
+            with pytest.raises(K.KameraError):
+                call(workspace=room[:n - 1])
+    torch.cuda.synchronize()

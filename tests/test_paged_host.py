@@ -138,3 +138,29 @@ def test_binding_looks_at_no_stride_that_is_not_taken(monkeypatch):
     with pytest.raises(ValueError, match="share"):
         K.kamera_attend_shared(pk, torch.zeros(64, 1, 72, dtype=bf)[:, :, :64], q, 16, None, None, None, i32(0, 2),
                                i32(0), 0, 0, 20)
+
+
+def test_workspace_sizes_from_python():
+    """The sizes the C entry points give for the same call, from the call's tensors."""
+    lib, z = K.load_library(), lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    pool, q, summary = z(640, 2, 64), z(3, 8, 64), z(40, 2, 2, 64)
+    kv, query = K._PagedKV(None, None, 640, 128, 2, 64, 16, 0), K._PagedQuery(None, None, None, 3, 8, 0.5, 0)
+    own = lambda n: K._PageTable(None, None, -(-n // 16), n)
+    for groups, most, prefix, n in ((2, 2, 600, 50), (0, 0, 0, 50), (0, 0, 0, 100000), (1, 3, 30000, 0), (3, 1, 0, 17)):
+        pre = K._PrefixGroups(None, None, None, groups, -(-prefix // 16), prefix, most)
+        want = lib.kamera_attend_shared_workspace_bytes(C.byref(kv), C.byref(query), C.byref(pre), C.byref(own(n)))
+        assert K.kamera_attend_shared_workspace_bytes(pool, q, 16, groups, most, prefix, n) == want
+        assert (want > 0) == (prefix > 0 or n > 10000)
+    for k, n in ((4, 600), (2000, 100000)):
+        want = lib.kamera_attend_selected_workspace_bytes(C.byref(kv), C.byref(query), C.byref(own(n)), k)
+        assert K.kamera_attend_selected_workspace_bytes(pool, q, 16, k, n) == want and (want > 0) == (k > 1000)
+    assert K.kamera_select_pages_workspace_bytes(q, summary, 16, 601, 5) == 3 * 2 * 38 * 8
+    assert K.kamera_select_pages_workspace_bytes(q, summary, 16, 601, 5, 3, 3) == 0      # more forced than taken
+    assert K.kamera_attend_shared_workspace_bytes(pool, q, 24, 1, 3, 100, 50) == 0       # a page size it refuses
+    for call in (lambda: K.kamera_attend_shared_workspace_bytes(pool, q[:, :, :32], 16, 1, 3, 100, 50),
+                 lambda: K.kamera_attend_shared_workspace_bytes(pool, q, 0, 1, 3, 100, 50),
+                 lambda: K.kamera_attend_shared_workspace_bytes(pool, q, 16, 1, 3, 2 ** 31, 50),
+                 lambda: K.kamera_attend_selected_workspace_bytes(pool[0], q, 16, 4, 50),
+                 lambda: K.kamera_select_pages_workspace_bytes(q, summary[0], 16, 50, 4)):
+        with pytest.raises(ValueError):
+            call()
