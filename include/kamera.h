@@ -640,7 +640,9 @@ int kamera_attend_reused_static(const KameraAttnKV* kv, const KameraAttnQuery* q
  * Pages: page g of page_size P is slots g*P .. g*P + P-1 (whole pages only:
  * floor(num_slots / P) of them).  A page table row lists a sequence's pages in
  * order, int32; token t sits in slot pages[t / P] * P + t % P.  Entries past
- * ceil(len / P) are never read.  A page outside the pool: its tokens are left
+ * ceil(len / P) may hold anything and change nothing, but the kernels read some of
+ * them before they know the length: the whole [rows][max_pages] array is readable
+ * memory.  A page outside the pool: its tokens are left
  * out (as if masked) and KAMERA_DEVERR_SLOT raised.
  */
 
