@@ -834,7 +834,8 @@ def kamera_append_kv(pool_k: torch.Tensor, pool_v: torch.Tensor, k: torch.Tensor
     packed heads, any token stride (views of a fused projection); q: None or
     bf16 ``[T, H_q, d]``, any token and head strides; q_out: like q (allocated
     when None; may be q itself); positions, slots: int64 ``[T]``, slot -1 a
-    padding row.  Multi-axis RoPE: positions None, ``rope.axis_delta`` int64
+    padding row, which nothing is written for: its row of an allocated ``q_out`` is
+    uninitialised memory.  Multi-axis RoPE: positions None, ``rope.axis_delta`` int64
     ``[T, n_axes]``.  Returns ``q_out`` (None without q)."""
     return (_FAST or _fast()).append_kv(pool_k, pool_v, k, v, rope, positions, slots, layer, q, q_out, err, stream)
 
