@@ -20,8 +20,9 @@
 // thread).  A CTA owns TT tokens; a thread keeps its unit (pass, head, place)
 // and walks the tokens, so the unit is decoded once and the tokens' loads
 // overlap.  10368 tokens of 28 + 4 heads of 128 (191 MB): 30.6 us, 6.2 TB/s; 16381
-// latent rows with 16 rope queries (105 MB): 17 us, 6.2 TB/s; a step of 64 tokens
-// 2.4 us, its launch and two dependent loads.
+// latent rows with 16 rope queries (105 MB): 21.3 us, 4.9 TB/s, out of HBM (17 us with
+// the pool in L2); a step of 64 tokens 2.4 us in a graph, its launch and two dependent
+// loads.
 #include <cstdint>
 #include <cstring>
 
@@ -299,11 +300,15 @@ cudaError_t launch_append(AppendParams& p, const RopeParams& r, bool inplace, cu
         p.axis[f] = r.axis[f];
     }
     // One token a CTA while that leaves SMs idle or barely filled (a decode step is
-    // latency); four once the SMs have two CTAs each, so that the set-up (slots,
-    // angles) is shared and 64 bytes a thread are in flight: 10368 tokens of 28 + 4
-    // heads of 128 take 30.6 us with four and 34.0 with two (before the registers were
-    // held down 47.7 with one, 34.9 with two, 33.8 with four, 42.3 with eight).
-    if (p.n_tokens >= 152 * 8)
+    // latency); four from eight tokens an SM on, so that the set-up (slots, angles) is
+    // shared and 64 bytes a thread are in flight.  28 + 4 heads of 128: 5.5 us either way
+    // for 912 and 1216 tokens, 6.1 with four and 8.2 with one for 1824, 29.1 and 38.4 for
+    // 9728.  Narrow rows fill an SM later and lose nothing by four before: one 64-wide head
+    // 5.0 and 4.8 us (launches) for 1824, 7.6 and 10.5 for 9728; latent rows of 576 without
+    // queries 5.1 and 4.7, 6.7 and 11.3.  (10368 tokens of the first: 30.6 with four, 34.0
+    // with two; before the registers were held down 47.7 with one, 34.9 with two, 33.8
+    // with four, 42.3 with eight.)
+    if (p.n_tokens >= 8 * device_sms())
         return launch_append_t<4>(p, inplace, stream);
     return launch_append_t<1>(p, inplace, stream);
 }
