@@ -8,9 +8,10 @@ import torch
 
 import position_invariant_kv_chunk_gb300 as K
 from tests import paged_ref as R
-from tests.test_gpu_paged import DEV, Pool, boxes, i32, near, normal, select_ref
+from tests.test_gpu_paged import DEV, Pool, boxes, i32, near, normal, rows_ref, select_ref
 
 pytestmark = pytest.mark.gpu
+SLOT, DESCRIPTOR, TIMEOUT = 1, 4, 32
 
 
 # ------------------------------------------------------------------- append --
@@ -168,7 +169,7 @@ INF, NAN = float("inf"), float("nan")
 
 @pytest.mark.parametrize("H,G,d,P,prefix,lens", [
     (2, 7, 128, 16, 700, [50, 333, 0]),        # prefix and own pages, one side of the prefix kernel
-    (32, 2, 128, 16, 1300, [50, 33]),          # tiles in turn on the two sides
+    (32, 2, 128, 16, 1300, [50, 33]),
     (3, 16, 64, 32, 2000, [5, 70, 1, 40] * 6),  # two tiles of rows
     (1, 3, 64, 16, 0, [700, 1, 33]),           # own pages, joined in a cluster
     (2, 9, 128, 16, 0, [20, 4000]),            # in a cluster of several CTAs
@@ -276,3 +277,207 @@ def test_workspaces_of_the_size_that_is_given():
             with pytest.raises(K.KameraError):
                 call(workspace=room[:n - 1])
     torch.cuda.synchronize()
+
+
+# --------------------------------------- prefixes whose tiles go to the sides in turn
+class InTurn:
+    """Enough (group, KV head) pairs that every prefix stays in one piece, of 128 rows at
+    most and eight tiles at least: the prefix kernel's two sides take its tiles in turn."""
+
+    def __init__(self, seed, H, G, d, P, groups, prefix, lens, std=1.0):
+        self.P, self.G, self.prefix, self.lens = P, G, prefix, lens
+        n = sum(groups)
+        need = sum(-(-x // P) for x in prefix + lens) + 3
+        self.pool = Pool(seed, need, P, H, d, std=std)
+        self.pre, self.own = self.pool.table(prefix), self.pool.table(lens)
+        self.pool.poison()
+        self.q = normal(self.pool.g, n, H * G, d)
+        self.starts = np.concatenate([[0], np.cumsum(groups)])
+        self.args = (i32(self.starts.tolist()), self.pre, i32(prefix), self.own, i32(lens), max(groups), max(prefix),
+                     max(lens))
+        rows = n * H * G
+        align = lambda x: -(-x // 256) * 256
+        # two states a row of the one split: one of each side
+        assert K.kamera_attend_shared_workspace_bytes(self.pool.k, self.q, P, len(groups), max(groups), max(prefix),
+                                                      0) == align(rows * 2 * d * 4) + align(rows * 2 * 8)
+
+    def slots(self, g, n=None):
+        return R.slots_of(self.pre[g].tolist(), self.P, self.prefix[g] if n is None else n, self.pool.n_pages)
+
+    def lists(self):
+        out = []
+        for s, n in enumerate(self.lens):
+            g = int(np.searchsorted(self.starts, s, side="right")) - 1
+            out.append(np.concatenate([self.slots(g), R.slots_of(self.own[s].tolist(), self.P, n, self.pool.n_pages)]))
+        return out
+
+    def call(self, err=None, **kw):
+        return K.kamera_attend_shared(self.pool.k, self.pool.v, self.q, self.P, *self.args, err=err, **kw)
+
+
+@pytest.mark.parametrize("d,P,G", [(128, 16, 2), (64, 48, 3), (128, 128, 1)])
+def test_in_turn_reports_bad_pages(d, P, G):
+    """Pages outside the pool in tiles of the first side, of the second, in the first and the
+    last tile of a prefix, a whole tile of them, and everywhere."""
+    c = InTurn(101, 32, G, d, P, [2, 1, 1, 1], [2049, 1920, 1300, 1153], [50, 0, 33, 7, 64])
+    page = lambda token: token // P
+    for g, token, bad in ((0, 128 * 3 + 20, -1), (0, 128 * 6 + 100, 2 ** 31 - 1), (0, 2048, -7), (1, 5, -1),
+                          (1, 128 * 14 + 1, c.pool.n_pages)):
+        c.pre[g, page(token)] = bad
+    c.pre[2, page(128 * 5):page(128 * 6 + 127) + 1] = -1      # all of a tile of each side
+    c.pre[3, :] = -2
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = c.call(err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == SLOT
+    near(out, lse, rows_ref(c.q, c.pool, c.lists(), d ** -0.5), (d, P, G))
+
+
+@pytest.mark.parametrize("scale,std", [(-0.09, 1.0), (0.0, 1.0), (0.4, 2.0), (-0.3, 2.0)])
+def test_in_turn_of_other_scales(scale, std):
+    c = InTurn(102, 32, 2, 128, 16, [1, 2, 1, 1], [1100, 1301, 2176, 128], [20, 0, 33, 5, 40], std)
+    out, lse = c.call(scale=scale)
+    torch.cuda.synchronize()
+    near(out, lse, rows_ref(c.q, c.pool, c.lists(), scale), (scale, std))
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_in_turn_of_growing_scores(order):
+    """Scores that climb along the prefix (or fall): each side rescales its running output
+    again and again, or finds weights that underflow."""
+    c = InTurn(103, 32, 2, 128, 32, [1, 1, 2, 1], [1500, 1150, 1281, 1409], [20, 33, 0, 5, 16])
+    for g in range(4):
+        n = c.prefix[g]
+        at = torch.from_numpy(c.slots(g)).to(DEV)
+        ramp = torch.linspace(0, 8, n, device=DEV)
+        ramp = ramp if order > 0 else ramp.flip(0)
+        q = c.q[int(c.starts[g])].float().view(32, 2, 128).sum(1)
+        c.pool.k[at] = (c.pool.k[at].float() + ramp[:, None, None] * 0.5 * q).to(torch.bfloat16)
+    out, lse = c.call()
+    torch.cuda.synchronize()
+    near(out, lse, rows_ref(c.q, c.pool, c.lists(), 128 ** -0.5), order)
+
+
+def test_in_turn_of_infinite_and_nan_scores():
+    """Tiles of one side, of the other and of both whose scores are -infinity throughout,
+    and a NaN key."""
+    c = InTurn(104, 32, 1, 64, 16, [1, 1, 1, 1], [1200, 1290, 1153, 1025], [20, 33, 0, 5])
+    c.q.copy_(c.q.abs() + 0.5)
+    gone = []
+    for g, tiles in ((0, [0, 2, 4]), (1, [1, 3, 5, 9]), (2, [0, 1, 6, 7])):
+        t = np.concatenate([np.arange(128 * k, min(128 * k + 128, c.prefix[g])) for k in tiles])
+        c.pool.k[torch.from_numpy(c.slots(g)[t]).to(DEV)] = -3e38
+        gone.append(t)
+    c.pool.k[int(c.slots(3)[700]), 5, 3] = NAN
+    out, lse = c.call()
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(out[3, 5]).all()) and bool(torch.isnan(lse[3, 5]))
+    lists = c.lists()
+    for g, t in enumerate(gone):
+        lists[g] = np.delete(lists[g], t)
+    near(out[:3], lse[:3], rows_ref(c.q[:3], c.pool, lists[:3], 64 ** -0.5), "-inf")
+    rest = [h for h in range(32) if h != 5]
+    refs = rows_ref(c.q[3:], c.pool, lists[3:], 64 ** -0.5)
+    near(out[3:][:, rest], lse[3:][:, rest], [refs[h] for h in rest], "beside a NaN")
+
+
+def test_in_turn_infinite_values():
+    c = InTurn(107, 32, 2, 64, 16, [1, 2, 1, 1], [1200, 1290, 1153, 1025], [20, 33, 0, 5, 1])
+    for g in range(4):
+        at = c.slots(g)
+        for j in range(7):
+            c.pool.v[int(at[(j * 181 + 37 * g) % c.prefix[g]]), (5 * j + g) % 32, (9 * j) % 64] = INF if j % 2 else -INF
+        c.pool.v[int(at[-1]), 3, 63], c.pool.v[int(at[130]), 4, 1], c.pool.v[int(at[300]), 4, 1] = INF, INF, -INF
+    out, lse = c.call()
+    torch.cuda.synchronize()
+    near_with_infinities(out, lse, c.q, c.pool, [[x] * 32 for x in c.lists()], 64 ** -0.5, "in turn")
+
+
+def test_in_turn_reports_malformed_groups():
+    c = InTurn(105, 32, 2, 64, 16, [1, 1, 1, 1], [1200, 1290, 1153, 1025], [20, 33, 0, 5])
+    good, _ = c.call()
+    for starts, served in (([0, 1, 2, 2, 3], [0, 1]), ([0, 1, 9, 3, 4], [0, 3]), ([0, 1, -7, 3, 4], [0, 3])):
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out, _ = K.kamera_attend_shared(c.pool.k, c.pool.v, c.q, 16, i32(starts), *c.args[1:], err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == DESCRIPTOR, starts
+        for s in served:
+            assert torch.equal(out[s], good[s]), starts
+
+
+def test_in_turn_wait_runs_out_then_recovers(monkeypatch):
+    """No tile is loaded and every wait gives up after 1 ms: the call returns with
+    TIMEOUT, and the next one is right."""
+    c = InTurn(106, 32, 2, 128, 16, [1, 1, 1, 1], [1200, 1290, 1153, 1025], [20, 33, 0, 5])
+    good, _ = c.call()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    monkeypatch.setenv("KAMERA_WAIT_LIMIT_NS", "1000000")
+    monkeypatch.setenv("KAMERA_TEST_WITHHOLD_LOADS", "1")
+    c.call(err)
+    torch.cuda.synchronize()
+    assert int(err.item()) & TIMEOUT
+    monkeypatch.delenv("KAMERA_WAIT_LIMIT_NS")
+    monkeypatch.delenv("KAMERA_TEST_WITHHOLD_LOADS")
+    err.zero_()
+    out, _ = c.call(err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(out, good)
+
+
+# ----------------------------------------------------------------- together --
+def test_chunks_relocated_into_the_pages_of_a_table():
+    """Chunks reinstated straight into the slots of a shared prefix's page table (the second
+    begins inside a page), rows appended behind them, attention over both and over
+    selected pages, with no row moved in between."""
+    import workloads as W
+    from tests import harness as Hn
+    spec = W.scaled(W.qwen_recall(), L=1, lens=(130, 75))
+    wl = W.make(spec, DEV)
+    H, d, P, G, n, pages = spec.H, spec.d, spec.page, 7, 3, 60
+    g = torch.Generator(device=DEV).manual_seed(111)
+    order = torch.randperm(pages, generator=g, device=DEV).tolist()
+    prefix = sum(spec.lens)
+    pre = [order.pop() for _ in range(-(-prefix // P))]
+    own = [[order.pop(), order.pop()] for _ in range(n)]
+    wl.pool_k, wl.pool_v = normal(g, 1, pages * P, H, d), normal(g, 1, pages * P, H, d)
+    at = torch.from_numpy(R.slots_of(pre, P, prefix, pages)).to(DEV)
+    for c, part in zip(wl.chunks, at.split(list(spec.lens))):
+        c.slots = part.to(c.slots.dtype).contiguous()
+    before = Hn.snapshot(wl)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    Hn.run_gpu(wl, err=err)
+    Hn.check_parity(wl, before, "into pages")
+    rope, steps = K.Rope(spec.base, d), P + 3
+    for t in range(steps):
+        k, v, q = normal(g, n, H, d), normal(g, n, H, d), normal(g, n, H * G, d)
+        slot = torch.tensor([own[s][t // P] * P + t % P for s in range(n)], device=DEV)
+        turned = K.kamera_append_kv(wl.pool_k, wl.pool_v, k, v, rope, torch.full((n,), prefix + t, device=DEV), slot, q=q,
+                                    err=err)
+    kk, vv = wl.pool_k[0], wl.pool_v[0]
+    lens = i32([steps] * n)
+    out, lse = K.kamera_attend_shared(kk, vv, turned, P, i32([0, n]), i32([pre]), i32([prefix]), i32(own), lens, n, prefix,
+                                      steps, err=err)
+    # the prefix's whole pages and the own ones as one table, and three of them selected
+    whole = prefix // P
+    table, m = i32([pre[:whole] + own[s] for s in range(n)]), whole * P + steps
+    summary = torch.zeros(pages, H, 2, d, dtype=torch.bfloat16, device=DEV)
+    ids = i32(pre[:whole] + [p for o in own for p in o[:1]])
+    K.kamera_summarize_pages(kk, P, ids, torch.full_like(ids, P), summary, err=err)
+    sel = K.kamera_select_pages(turned, summary, P, table, i32([m] * n), m, 5, err=err)
+    part, part_lse = K.kamera_attend_selected(kk, vv, turned, P, table, i32([m] * n), sel, m, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    view = Pool.__new__(Pool)
+    view.k, view.v, view.H = kk, vv, H
+    lists = [np.concatenate([at.cpu().numpy(), R.slots_of(own[s], P, steps, pages)]) for s in range(n)]
+    near(out, lse, rows_ref(turned, view, lists, d ** -0.5), "dense")
+    chosen = select_ref(turned, summary, table, [m] * n, P, 5, 1, 1)
+    assert np.array_equal(sel.cpu().numpy(), chosen)
+    qh, refs = R.f64(turned), []
+    for s in range(n):
+        slots = R.slots_of(table[s].tolist(), P, m, pages)
+        for h in range(H):
+            idx = torch.from_numpy(np.concatenate([slots[j * P:j * P + P] for j in chosen[s, h]])).to(DEV)
+            o, l, a, x = R.attention(qh[s, h * G:h * G + G], R.f64(kk[idx])[:, h], R.f64(vv[idx])[:, h], d ** -0.5)
+            refs += [(o[i], l[i], a[i], x[i], len(idx)) for i in range(G)]
+    near(part, part_lse, refs, "selected")
