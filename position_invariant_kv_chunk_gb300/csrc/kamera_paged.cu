@@ -17,9 +17,9 @@
 //   - Softmax weights are not bf16 values: they enter as hi + lo pairs (about 16
 //     significant bits, both parts positive), which costs MMAs the tensor pipe has spare.
 //   - Two buffers a warp and three CTAs an SM: with three buffers and two CTAs 32
-//     sequences of 2048 selected tokens take 48.5 us with the selection, so 40.1.
-//     Their 134 MB take 20 us of HBM; the kernel's 25 add the start (three dependent
-//     loads) and the join.
+//     sequences of 2048 selected tokens took 48.5 us with the selection, where this
+//     took 40.1 (38 since the selection got shorter).  Their 134 MB take 20 us of HBM;
+//     the kernel's 25 add the start (three dependent loads) and the join.
 //   - Few rows: the tokens of a (sequence, KV head) are split over CTAs.  Without a
 //     shared prefix up to eight of them form a cluster and join their states in
 //     shared memory; else each leaves a partial state in the workspace, and the

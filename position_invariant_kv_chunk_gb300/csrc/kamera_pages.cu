@@ -1091,7 +1091,9 @@ cudaError_t launch_select(SelectParams& p, cudaStream_t stream)
     // set at every launch: the attribute belongs to the current device's context
     // few pages: few threads, whose barriers are cheaper (32 rows x 4 of 512 pages and
     // one of 2048, with the attention: 40.1 and 14.2 us, with 1024 threads 42.0 and 15.2;
-    // with 128 the latter took 2.6 us more)
+    // with 128 the latter took 2.6 us more).  Past 8192 pages a thread holds 48 scores,
+    // some of them spilled: one context of 8192 pages 20.7 us with the attention over 128
+    // pages, of 8193 26.1, of 16384 31.5, of 49152 57.1; eight contexts 46.5, 52.2, 71.1 and 152.8
     auto launch = [&](auto kernel, int threads) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return e != cudaSuccess ? e : launch_after(kernel, dim3((unsigned)units), threads, smem, stream, true, p);
