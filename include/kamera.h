@@ -80,7 +80,7 @@ extern "C" {
 
 struct CUstream_st; /* cudaStream_t == struct CUstream_st* */
 
-#define KAMERA_ABI_VERSION 10
+#define KAMERA_ABI_VERSION 11
 
 /* Limits of this library. */
 #define KAMERA_MAX_RANK 128          /* largest patch rank m */
@@ -105,6 +105,7 @@ enum {
                                       misaligned factor or slot map: chunk skipped */
     KAMERA_DEVERR_LEN = 8,         /* len > max_len: chunk skipped */
     KAMERA_DEVERR_RANK = 16,       /* rank > max_rank: chunk skipped */
+    KAMERA_DEVERR_VALUE = 64,      /* a NaN among the rows to be packed: stored as 0 */
     KAMERA_DEVERR_TIMEOUT = 32     /* an internal pipeline wait gave up: results incomplete
                                       (every wait of the tensor-core kernels is bounded by
                                       1 s; the environment variable KAMERA_WAIT_LIMIT_NS,
@@ -861,6 +862,199 @@ int kamera_attend_selected(const KameraPagedKV* kv, const KameraPagedQuery* quer
 
 size_t kamera_attend_selected_workspace_bytes(const KameraPagedKV* kv, const KameraPagedQuery* query,
                                               const KameraPageTable* table, int32_t n_select);
+
+/*
+ * ---- Latent attention over the paged MLA pool --------------------------------
+ *
+ * kamera_mla_append_kv and kamera_mla_relocate_patch write latent rows (c_KV |
+ * k_rope) into the pool; the entry points below read them there, in both forms:
+ * a decode step takes the queries through the key up-projection and attends over the
+ * latent rows themselves (absorbed), a prefill expands the rows into every head's
+ * keys and values first.  The pages name both forms' inputs only (section 2, MLA).
+ */
+
+/* One layer of the paged MLA pool: bf16 [num_slots][kv_lora_rank + rope_dim], slots
+ * slot_stride elements apart (16-byte aligned, slot_stride a multiple of 8),
+ * page_size tokens to a page (a multiple of 16). */
+typedef struct KameraPagedMlaKV {
+    const void* kv;
+    int64_t num_slots;
+    int64_t slot_stride;
+    int32_t kv_lora_rank;
+    int32_t rope_dim;
+    int32_t page_size;
+    int32_t reserved;   /* 0 */
+} KameraPagedMlaKV;
+
+/*
+ * MLA decode attention over the pool (absorbed form): for every sequence s and query
+ * head h, over the sequence's tokens j (row_j = c_j | kr_j),
+ *     out_h = softmax_j(scale (q_h . row_j)) c_j,   lse_h = log sum_j exp(scale (q_h . row_j))
+ * q_h the absorbed latent query (kv_lora_rank wide), then its rope part.  Every row
+ * is read once for up to 64 query heads (128 heads: twice, at the same time, the
+ * second time from the L2 cache).  fp32 accumulation of bf16 products; the softmax
+ * weights enter the second product as bf16 hi + lo pairs (up to 32 heads) or rounded
+ * to bf16 (more heads: at most 2^-8 of each weight, where the lo parts would cost a
+ * third of the matrix rate), one bf16 rounding of the output.  A sequence without tokens
+ * gets zeros and lse = -infinity.  Rows past a sequence's length, and pages that no
+ * table names, are not used whatever they hold.
+ *   query   q bf16 [n_seqs][num_q_heads][kv_lora_rank + rope_dim] (RoPE already
+ *           applied), out bf16 [n_seqs][num_q_heads][kv_lora_rank] (written), lse fp32
+ *           [n_seqs][num_q_heads] (written) or NULL; q and out 16-byte aligned
+ *   table   as for kamera_attend_shared's own tokens
+ *   d_workspace  at least kamera_mla_attend_paged_workspace_bytes(...) bytes, rules as
+ *           for kamera_attend_shared
+ * Supported: kv_lora_rank 512, rope_dim 64, num_q_heads 1..128, page_size a multiple
+ * of 16, num_slots <= 2^31 - 1, n_seqs <= 65535.  Device errors: SLOT (a page outside
+ * the pool: its tokens are left out), LEN (the sequence read as empty), TIMEOUT.
+ */
+int kamera_mla_attend_paged(const KameraPagedMlaKV* kv, const KameraPagedQuery* query, const KameraPageTable* table,
+                            void* d_workspace, size_t workspace_bytes, int32_t* d_err, struct CUstream_st* stream);
+
+size_t kamera_mla_attend_paged_workspace_bytes(const KameraPagedMlaKV* kv, const KameraPagedQuery* query,
+                                               const KameraPageTable* table);
+
+/*
+ * Expansion of latent rows: for every token t < n_tokens, whose row lies in pool slot
+ * slots[t], and every head h,
+ *     kv[t][h] = bf16( W_h c_t ),   k_rope[t] = kr_t  (bit copy)
+ * with W_h the head's head_width x kv_lora_rank weights (its keys' no-position part
+ * first, then its values).  fp32 accumulation of bf16 products.
+ *   kv      the pool layer (page_size is not used and may be 0)
+ *   weight  bf16 [num_heads][head_width][kv_lora_rank], packed, 16-byte aligned
+ *   slots   device int64 [n_tokens]; -1: a padding row, whose outputs are zeros; any
+ *           other slot outside the pool: zeros too, and KAMERA_DEVERR_SLOT
+ *   kv_out  bf16 [n_tokens][num_heads][head_width], k_rope_out bf16 [n_tokens][rope_dim]
+ *           (written, packed, 16-byte aligned)
+ * Supported: kv_lora_rank 512, rope_dim 64, head_width 256, num_heads 1..128.
+ */
+typedef struct KameraMlaExpand {
+    const void* weight;
+    const int64_t* slots;
+    void* kv_out;
+    void* k_rope_out;
+    int32_t n_tokens;
+    int32_t num_heads;
+    int32_t head_width;
+    int32_t reserved;   /* 0 */
+} KameraMlaExpand;
+
+int kamera_mla_expand(const KameraPagedMlaKV* kv, const KameraMlaExpand* x, int32_t* d_err, struct CUstream_st* stream);
+
+/*
+ * Prefill attention over expanded rows: sequence s has query tokens q_start[s] ..
+ * q_start[s+1]-1 (nq of them) and rows kv_start[s] .. kv_start[s+1]-1 (nk); with a
+ * causal mask query i sees rows j <= i + nk - nq (the last query sees every row),
+ * else every row.  Per head, with k_j = (kv[j][h][0..nope) | k_rope[j]) and v_j =
+ * kv[j][h][nope..),
+ *     out = softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
+ * fp32 accumulation of bf16 products, softmax weights rounded to bf16 (2^-8 of each
+ * at the most), one bf16 rounding of the output.  A query that sees no row gets zeros
+ * and lse = -infinity.  Rows of q, out and lse that no sequence has stay as they are.
+ *   q       bf16 [n_q][num_heads][nope_dim + rope_dim] (RoPE already applied), element
+ *           (t, h, i) at q[t*q_stride + h*q_head_stride + i]
+ *   kv      bf16 [n_kv][num_heads][nope_dim + v_dim], heads packed, rows kv_stride apart
+ *   k_rope  bf16 [n_kv][rope_dim], rows k_rope_stride apart
+ *   out     bf16 [n_q][num_heads][v_dim] packed (written), lse fp32 [n_q][num_heads]
+ *           (written) or NULL
+ *   q_start, kv_start  device int32 [n_seqs + 1], non-decreasing, within [0, n_q] and
+ *           [0, n_kv]; at most max_q queries a sequence.  A malformed entry, or more
+ *           queries: KAMERA_DEVERR_DESCRIPTOR / _LEN, the sequence skipped (its rows
+ *           stay as they are)
+ * Pointers 16-byte aligned, strides in elements, multiples of 8 (a stride that no
+ * element takes is not looked at).  Supported: nope_dim 128, rope_dim 64, v_dim 128,
+ * num_heads 1..128, n_kv <= 2^30.  Device error TIMEOUT as for kamera_attend_shared.
+ */
+typedef struct KameraMlaPrefill {
+    const void* q;
+    const void* kv;
+    const void* k_rope;
+    void* out;
+    float* lse;
+    const int32_t* q_start;
+    const int32_t* kv_start;
+    int64_t q_stride, q_head_stride, kv_stride, k_rope_stride;
+    int32_t n_q, n_kv, n_seqs, num_heads;
+    int32_t nope_dim, rope_dim, v_dim, max_q;
+    int32_t causal;
+    float scale;
+} KameraMlaPrefill;
+
+int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct CUstream_st* stream);
+
+/*
+ * ---- Pages in 4 bits ----------------------------------------------------------
+ *
+ * A second pool that holds cold pages in 4 bits a number, 3.6 times smaller than bf16:
+ * 16 numbers share a scale s in 8 bits (e4m3: 3 bits behind the leading one, 2^-9 ..
+ * 448) and each is one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (e2m1) times s times the pool's
+ * unit.  s is the largest magnitude / (6 unit), rounded to nearest even, and a number
+ * goes to the nearest of the levels, an even code (0, 1, 2, 4) where two are as near.
+ * Groups lie along the axis that attention sums over: a key's channels 16 g .. 16 g +
+ * 15 of one token, a value channel's tokens 16 i .. 16 i + 15 of a page.  Every value
+ * stored is exact in bf16.  An infinity becomes the largest value; 4 bits hold no NaN:
+ * one is stored as 0 and KAMERA_DEVERR_VALUE raised.
+ *   data    [num_pages][num_kv_heads][page_size (d + d / 8)] bytes, 16-byte aligned: for
+ *           each 16 tokens of a page and head 18 d bytes, written by kamera_pack_pages
+ *   k_unit, v_unit  powers of two (2^-64 .. 2^64): 1 holds magnitudes up to 2688, in
+ *           steps down to 2^-10; the values of one pool share them, in every call
+ */
+typedef struct KameraPackedPool {
+    void* data;
+    int64_t num_pages;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t reserved;   /* 0 */
+    float k_unit;
+    float v_unit;
+} KameraPackedPool;
+
+/*
+ * Packing and unpacking pages: for i < n the first tokens[i] tokens (0..page_size) of
+ * bf16 page kv_pages[i] of one layer of the pool to, or from, packed page
+ * packed_pages[i].  Packing: tokens past the count in its last 16 count as 0, later
+ * ones are left as they are.  Unpacking writes the counted tokens' rows alone, each
+ * value rounded to nothing (exact) unless it lies outside bf16's range.  A bf16 page
+ * holds the same number of tokens as a packed one; slot = page*page_size + offset.
+ * Device errors, the entry skipped: SLOT (a page outside its pool), LEN (tokens outside
+ * 0..page_size); VALUE as above.  Destination pages are distinct within a call.
+ * Supported: head_dim 64 or 128, page_size a multiple of 16.
+ */
+int kamera_pack_pages(const KameraGqaPool* pool, int32_t layer, const KameraPackedPool* packed, const int32_t* d_kv_pages,
+                      const int32_t* d_packed_pages, const int32_t* d_tokens, int32_t n, int32_t* d_err,
+                      struct CUstream_st* stream);
+
+int kamera_unpack_pages(const KameraGqaPool* pool, int32_t layer, const KameraPackedPool* packed,
+                        const int32_t* d_kv_pages, const int32_t* d_packed_pages, const int32_t* d_tokens, int32_t n,
+                        int32_t* d_err, struct CUstream_st* stream);
+
+/*
+ * Decode attention over packed pages and, in the same softmax, a tail of bf16 pages
+ * (the tokens since a sequence's last page was packed):
+ *     out = softmax(scale q [K_packed | K_tail]^T) [V_packed | V_tail]
+ * K and V the values the packed pages stand for.  The packed part: fp16 products (the
+ * stored values, and the queries scaled by a power of two a row, are exact in fp16 to
+ * 2^-27 of the row's largest) with fp32 accumulation, softmax weights rounded to fp16
+ * (2^-11).  The tail as kamera_attend_shared.  One bf16 rounding of the output; a
+ * sequence with no token gets zeros and lse = -infinity.
+ *   query   as for kamera_attend_shared
+ *   table   packed pages and lengths
+ *   tail_kv, tail  both NULL, or the bf16 pool of the tails (its own page_size) and
+ *           their page tables and lengths
+ *   d_workspace  at least kamera_attend_packed_workspace_bytes(...) bytes, rules as for
+ *           kamera_attend_shared
+ * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..16, page_size a
+ * multiple of 16, n_seqs * num_kv_heads <= 65535.  Device errors: SLOT, LEN, TIMEOUT as
+ * for kamera_attend_shared.
+ */
+int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery* query, const KameraPageTable* table,
+                         const KameraPagedKV* tail_kv, const KameraPageTable* tail, void* d_workspace,
+                         size_t workspace_bytes, int32_t* d_err, struct CUstream_st* stream);
+
+size_t kamera_attend_packed_workspace_bytes(const KameraPackedPool* packed, const KameraPagedQuery* query,
+                                            const KameraPageTable* table, const KameraPagedKV* tail_kv,
+                                            const KameraPageTable* tail);
 
 /* KAMERA_ABI_VERSION of the loaded library. */
 int kamera_abi_version(void);

@@ -31,6 +31,9 @@ __all__ = [
     "kamera_append_kv", "kamera_mla_append_kv", "kamera_attend_shared", "kamera_summarize_pages",
     "kamera_select_pages", "kamera_attend_selected", "kamera_attend_shared_workspace_bytes",
     "kamera_select_pages_workspace_bytes", "kamera_attend_selected_workspace_bytes",
+    "kamera_mla_attend_paged", "kamera_mla_expand", "kamera_mla_prefill_attend", "kamera_pack_pages",
+    "kamera_unpack_pages", "kamera_attend_packed", "kamera_mla_attend_paged_workspace_bytes",
+    "kamera_attend_packed_workspace_bytes",
     "kamera_validate_chunks", "kamera_status_string", "kamera_abi_version",
     "ROTATE_HALF", "INTERLEAVED", "DEVERR",
 ]
@@ -46,6 +49,7 @@ DEVERR = {
     8: "len > max_len",
     16: "rank > max_rank",
     32: "pipeline wait timed out",
+    64: "a NaN among the rows to be packed",
 }
 
 
@@ -254,7 +258,7 @@ def kamera_status_string(status: int) -> str:
     return load_library().kamera_status_string(int(status)).decode()
 
 
-ABI_VERSION = 10   # the KAMERA_ABI_VERSION these bindings marshal for
+ABI_VERSION = 11   # the KAMERA_ABI_VERSION these bindings marshal for
 
 
 def kamera_abi_version() -> int:
@@ -916,6 +920,108 @@ def kamera_attend_selected(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.
     rest as for ``kamera_attend_shared``.  Returns ``(out, lse)``."""
     return (_FAST or _fast()).attend_selected(pool_k, pool_v, q, page_size, pages, lens, selected, max_len, scale, out,
                                               lse, err, stream, workspace)
+
+
+# ------------------------------------------ latent attention over the pool --
+def kamera_mla_attend_paged(pool: torch.Tensor, kv_lora: int, q: torch.Tensor, page_size: int, pages: torch.Tensor,
+                            lens: torch.Tensor, max_len: int, scale: Optional[float] = None,
+                            out: Optional[torch.Tensor] = None, lse=None, err: Optional[torch.Tensor] = None, stream=None,
+                            workspace: Optional[torch.Tensor] = None):
+    """MLA decode attention (absorbed form) of one query token per sequence over the
+    latent rows in the paged pool (``kamera_mla_attend_paged`` in kamera.h).
+
+    pool: bf16 ``[S_slots, kv_lora + rope_dim]`` (one layer, any row stride); q: bf16
+    ``[S, H_q, kv_lora + rope_dim]`` contiguous (latent query, then rope query); pages
+    int32 ``[S, width]``, lens int32 ``[S]``; scale: default 1/sqrt(kv_lora + rope_dim);
+    lse: None (allocated), False (not computed) or fp32 ``[S, H_q]``; workspace: None
+    (allocated for the call) or a tensor of at least
+    ``kamera_mla_attend_paged_workspace_bytes`` bytes.  Returns ``(out, lse)``, out bf16
+    ``[S, H_q, kv_lora]``."""
+    return (_FAST or _fast()).mla_attend_paged(pool, kv_lora, q, page_size, pages, lens, max_len, scale, out, lse, err,
+                                               stream, workspace)
+
+
+def kamera_mla_expand(pool: torch.Tensor, kv_lora: int, weight: torch.Tensor, slots: torch.Tensor,
+                      kv: Optional[torch.Tensor] = None, k_rope: Optional[torch.Tensor] = None,
+                      err: Optional[torch.Tensor] = None, stream=None):
+    """Latent rows of the pool expanded into every head's keys (no-position part) and
+    values, and their rope parts gathered (``kamera_mla_expand`` in kamera.h): what a
+    prefill attends over.
+
+    pool: bf16 ``[S_slots, kv_lora + rope_dim]`` (one layer); weight: bf16 ``[H,
+    nope + v, kv_lora]`` contiguous; slots: int64 ``[T]``, the rows' pool slots (-1: a
+    padding row, zeros).  Returns ``(kv, k_rope)``: bf16 ``[T, H, nope + v]`` and
+    ``[T, rope_dim]`` (allocated unless given)."""
+    return (_FAST or _fast()).mla_expand(pool, kv_lora, weight, slots, kv, k_rope, err, stream)
+
+
+def kamera_mla_prefill_attend(q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor, q_start: torch.Tensor,
+                              kv_start: torch.Tensor, max_q: int, max_kv: Optional[int] = None, causal: bool = True,
+                              scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse=None,
+                              err: Optional[torch.Tensor] = None, stream=None):
+    """Prefill attention over expanded rows (``kamera_mla_prefill_attend`` in kamera.h):
+    the queries of sequence s are rows ``q_start[s]`` .. ``q_start[s + 1]`` of q, its
+    keys and values rows ``kv_start[s]`` .. of kv and k_rope; with ``causal`` the last
+    query sees every row, each earlier one a row less.
+
+    q: bf16 ``[T, H, nope + rope]``, any token and head strides; kv: bf16 ``[R, H,
+    nope + v]`` with packed heads, any row stride; k_rope: bf16 ``[R, rope]``, any row
+    stride; q_start, kv_start: int32 ``[n + 1]``; max_q: bound of the sequences' queries
+    (max_kv, of their rows, is not needed and accepted for symmetry); scale: default
+    1/sqrt(nope + rope); lse: None (allocated), False (not computed) or fp32 ``[T, H]``.
+    Returns ``(out, lse)``, out bf16 ``[T, H, v]``; rows of allocated outputs that no
+    sequence has are uninitialised."""
+    return (_FAST or _fast()).mla_prefill_attend(q, kv, k_rope, q_start, kv_start, max_q, causal, scale, out, lse, err,
+                                                 stream)
+
+
+# ------------------------------------------------------------ pages in 4 bits --
+def kamera_pack_pages(pool_k: torch.Tensor, pool_v: torch.Tensor, page_size: int, src_pages: torch.Tensor,
+                      page_tokens: torch.Tensor, packed: torch.Tensor, dst_pages: torch.Tensor, k_unit: float = 1.0,
+                      v_unit: float = 1.0, err: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Pages of the bf16 pool into the 4-bit pool (``kamera_pack_pages`` in kamera.h):
+    the first ``page_tokens[i]`` tokens of page ``src_pages[i]`` into ``dst_pages[i]``.
+
+    pool_*: bf16 ``[S_slots, H, d]`` (one layer); packed: uint8 ``[n_pages, H, page_size
+    * (d + d // 8)]`` contiguous; the others int32 ``[n]``; k_unit, v_unit: powers of
+    two, the same in every call on this pool.  Returns ``packed``."""
+    (_FAST or _fast()).pack_pages(pool_k, pool_v, page_size, src_pages, page_tokens, packed, dst_pages, k_unit, v_unit, err,
+                                  stream)
+    return packed
+
+
+def kamera_unpack_pages(packed: torch.Tensor, page_size: int, src_pages: torch.Tensor, page_tokens: torch.Tensor,
+                        pool_k: torch.Tensor, pool_v: torch.Tensor, dst_pages: torch.Tensor, k_unit: float = 1.0,
+                        v_unit: float = 1.0, err: Optional[torch.Tensor] = None, stream=None):
+    """Pages of the 4-bit pool back into the bf16 pool, the values they stand for
+    (``kamera_unpack_pages`` in kamera.h): the first ``page_tokens[i]`` tokens of packed
+    page ``src_pages[i]`` into page ``dst_pages[i]``.  Arguments as for
+    ``kamera_pack_pages``.  Returns ``(pool_k, pool_v)``."""
+    (_FAST or _fast()).unpack_pages(pool_k, pool_v, page_size, dst_pages, page_tokens, packed, src_pages, k_unit, v_unit,
+                                    err, stream)
+    return pool_k, pool_v
+
+
+def kamera_attend_packed(packed: torch.Tensor, q: torch.Tensor, page_size: int, pages: Optional[torch.Tensor],
+                         lens: Optional[torch.Tensor], max_len: int, pool_k: Optional[torch.Tensor] = None,
+                         pool_v: Optional[torch.Tensor] = None, tail_pages: Optional[torch.Tensor] = None,
+                         tail_lens: Optional[torch.Tensor] = None, max_tail: int = 0,
+                         tail_page_size: Optional[int] = None, k_unit: float = 1.0, v_unit: float = 1.0,
+                         scale: Optional[float] = None, out: Optional[torch.Tensor] = None, lse=None,
+                         err: Optional[torch.Tensor] = None, stream=None, workspace: Optional[torch.Tensor] = None):
+    """Decode attention over 4-bit pages and, in the same softmax, a tail of bf16 pages
+    (``kamera_attend_packed`` in kamera.h): the tokens since a sequence's last page was
+    packed.
+
+    packed: uint8 ``[n_pages, H, page_size * (d + d // 8)]``; q: bf16 ``[S, H_q, d]``
+    contiguous; pages int32 ``[S, width]``, lens int32 ``[S]``, of the packed part;
+    pool_*: bf16 ``[S_slots, H, d]`` (one layer) with tail_pages, tail_lens and max_tail
+    for the tail (all None: no tail; tail_page_size: default page_size); k_unit, v_unit:
+    as the pages were packed; scale: default 1/sqrt(d); lse and workspace as for
+    ``kamera_attend_shared``.  Returns ``(out, lse)``."""
+    return (_FAST or _fast()).attend_packed(packed, q, page_size, pages, lens, max_len, pool_k, pool_v, tail_pages,
+                                            tail_lens, max_tail, tail_page_size, k_unit, v_unit, scale, out, lse, err,
+                                            stream, workspace)
 
 
 def _int32(x, name: str) -> int:

@@ -19,6 +19,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
@@ -565,15 +566,21 @@ struct QueryArg {
     PyObject *out_o, *lse_o;
     at::Tensor made_out, made_lse;
 
-    QueryArg(const at::Tensor& q, PyObject* scale, PyObject* out_obj, PyObject* lse_obj) : out_o(out_obj), lse_o(lse_obj)
+    std::vector<int64_t> shape;   // of out: q's, or another width
+
+    QueryArg(const at::Tensor& q, PyObject* scale, PyObject* out_obj, PyObject* lse_obj, int64_t width = -1)
+        : out_o(out_obj), lse_o(lse_obj), shape(q.sizes().vec())
     {
+        if (width >= 0)
+            shape.back() = width;
         std::memset(&c, 0, sizeof(c));
         out = optional(out_obj, "out");
         want_lse = lse_obj != Py_False;
         if (want_lse)
             lse = optional(lse_obj, "lse");
-        if (out && (out->sizes() != q.sizes() || out->scalar_type() != at::kBFloat16 || !out->is_contiguous()))
-            value_error("out must be a contiguous bf16 tensor shaped like q");
+        if (out && (out->sizes() != at::IntArrayRef(shape) || out->scalar_type() != at::kBFloat16 || !out->is_contiguous()))
+            value_error(width >= 0 ? "out must be a contiguous bf16 tensor of shape " + shape_text(shape)
+                                   : std::string("out must be a contiguous bf16 tensor shaped like q"));
         if (lse && (lse->sizes() != q.sizes().slice(0, 2) || lse->scalar_type() != at::kFloat || !lse->is_contiguous()))
             value_error("lse must be a contiguous fp32 [S, H_q] tensor");
         c.q = q.data_ptr();
@@ -590,7 +597,7 @@ struct QueryArg {
     void allocate(Place& on, const at::Tensor& q)
     {
         if (!out) {
-            made_out = on.empty(q.sizes(), at::kBFloat16);
+            made_out = on.empty(shape, at::kBFloat16);
             out = &made_out;
         }
         if (want_lse && !lse) {
@@ -788,12 +795,326 @@ PyObject* select_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     });
 }
 
+// -------------------------------------------------------- latent attention --
+// One layer of the paged MLA pool; the row splits after kv_lora columns.
+KameraPagedMlaKV paged_mla(const at::Tensor& p, PyObject* kv_lora, PyObject* page_size)
+{
+    bf16(p, "pool");
+    if (p.dim() != 2 || (p.size(1) > 1 && p.stride(1) != 1))
+        value_error("pool must be [S, kv_lora + rope_dim] (one layer) with packed rows");
+    KameraPagedMlaKV kv;
+    std::memset(&kv, 0, sizeof(kv));
+    kv.kv = p.data_ptr();
+    kv.num_slots = p.size(0);
+    kv.slot_stride = p.size(0) > 1 ? p.stride(0) : p.size(1);
+    kv.kv_lora_rank = int32(kv_lora, "kv_lora");
+    kv.rope_dim = size32(p.size(1) - kv.kv_lora_rank, "pool");
+    kv.page_size = page_size ? int32(page_size, "page_size") : 0;
+    return kv;
+}
+
+// mla_attend_paged(pool, kv_lora, q, page_size, pages, lens, max_len, scale, out, lse, err, stream, workspace)
+PyObject* mla_attend_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    return guarded([&]() -> PyObject* {
+        count(n_args, 13);
+        const at::Tensor &p = tensor(a[0], "pool"), &q = tensor(a[2], "q");
+        KameraPagedMlaKV kv = paged_mla(p, a[1], a[3]);
+        check_q(q, p.size(1));
+        const at::Tensor *pages = optional(a[4], "pages"), *lens = optional(a[5], "lens"), *err = optional(a[10], "err"),
+                         *ws = optional(a[12], "workspace");
+        if (!pages || !lens)
+            value_error("pages and lens are needed");
+        KameraPageTable t = page_table(pages, lens, q.size(0), integer(a[6], "max_len"));
+        QueryArg qq(q, a[7], a[8], a[9], kv.kv_lora_rank < 0 ? 0 : kv.kv_lora_rank);
+        Place on("kamera_mla_attend_paged", q);
+        on.check(q, "q");
+        on.check(p, "pool");
+        on.check(pages, "pages");
+        on.check(lens, "lens");
+        on.check(qq.out, "out");
+        on.check(qq.lse, "lse");
+        on.check(err, "err");
+        on.check(ws, "workspace");
+        int32_t* e = error_word(err);
+        on.enter(a[11]);
+        qq.allocate(on, q);
+        Scratch s(on, ws, ws ? 0 : kamera_mla_attend_paged_workspace_bytes(&kv, &qq.c, &t));
+        status(kamera_mla_attend_paged(&kv, &qq.c, &t, s.p, s.bytes, e, on.stream()), "kamera_mla_attend_paged");
+        return qq.result();
+    });
+}
+
+// mla_expand(pool, kv_lora, weight, slots, kv, k_rope, err, stream)
+PyObject* mla_expand(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    return guarded([&]() -> PyObject* {
+        count(n_args, 8);
+        const at::Tensor &p = tensor(a[0], "pool"), &w = tensor(a[2], "weight"), &slots = tensor(a[3], "slots");
+        KameraPagedMlaKV pool = paged_mla(p, a[1], nullptr);
+        bf16(w, "weight");
+        if (w.dim() != 3 || w.size(2) != pool.kv_lora_rank || !w.is_contiguous())
+            value_error("weight must be a contiguous [H, head_width, kv_lora] tensor");
+        const int64_t T = slots.numel();
+        exact(slots, "slots", at::kLong, {T});
+        const at::Tensor *kv = optional(a[4], "kv"), *kr = optional(a[5], "k_rope"), *err = optional(a[6], "err");
+        const std::vector<int64_t> wide{T, w.size(0), w.size(1)}, narrow{T, p.size(1) - w.size(2)};
+        if (kv)
+            exact(*kv, "kv", at::kBFloat16, wide);
+        if (kr)
+            exact(*kr, "k_rope", at::kBFloat16, narrow);
+        Place on("kamera_mla_expand", p);
+        on.check(p, "pool");
+        on.check(w, "weight");
+        on.check(slots, "slots");
+        on.check(kv, "kv");
+        on.check(kr, "k_rope");
+        on.check(err, "err");
+        int32_t* e = error_word(err);
+        on.enter(a[7]);
+        at::Tensor made_kv, made_kr;
+        if (!kv) {
+            made_kv = on.empty(wide, at::kBFloat16);
+            kv = &made_kv;
+        }
+        if (!kr) {
+            made_kr = on.empty(narrow, at::kBFloat16);
+            kr = &made_kr;
+        }
+        KameraMlaExpand x;
+        std::memset(&x, 0, sizeof(x));
+        x.weight = w.data_ptr();
+        x.slots = slots.data_ptr<int64_t>();
+        x.kv_out = kv->data_ptr();
+        x.k_rope_out = kr->data_ptr();
+        x.n_tokens = size32(T, "slots");
+        x.num_heads = size32(w.size(0), "weight");
+        x.head_width = size32(w.size(1), "weight");
+        status(kamera_mla_expand(&pool, &x, e, on.stream()), "kamera_mla_expand");
+        Ref o(made_kv.defined() ? THPVariable_Wrap(made_kv) : Py_NewRef(a[4]));
+        Ref r(made_kr.defined() ? THPVariable_Wrap(made_kr) : Py_NewRef(a[5]));
+        if (!o.get() || !r.get())
+            throw Raised{};
+        return PyTuple_Pack(2, o.get(), r.get());
+    });
+}
+
+// mla_prefill_attend(q, kv, k_rope, q_start, kv_start, max_q, causal, scale, out, lse, err, stream)
+PyObject* mla_prefill_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    return guarded([&]() -> PyObject* {
+        count(n_args, 12);
+        const at::Tensor &q = tensor(a[0], "q"), &kv = tensor(a[1], "kv"), &kr = tensor(a[2], "k_rope"),
+                         &qs = tensor(a[3], "q_start"), &ks = tensor(a[4], "kv_start");
+        bf16(q, "q");
+        bf16(kv, "kv");
+        bf16(kr, "k_rope");
+        if (q.dim() != 3 || (q.size(2) > 1 && q.stride(2) != 1))
+            value_error("q must be [T, H, nope + rope] with packed rows");
+        if (kv.dim() != 3 || kv.size(1) != q.size(1) || !packed(kv))
+            value_error("kv must be [R, H, nope + v] with packed heads, the heads of q");
+        if (kr.dim() != 2 || kr.size(0) != kv.size(0) || kr.size(1) > q.size(2) || (kr.size(1) > 1 && kr.stride(1) != 1))
+            value_error("k_rope must be [R, rope] with packed rows, the rows of kv");
+        const int64_t n = qs.numel() - 1, nope = q.size(2) - kr.size(1), v = kv.size(2) - nope;
+        if (n < 0 || v < 0)
+            value_error(n < 0 ? "q_start must hold n + 1 values" : "kv is narrower than the keys' no-position part");
+        exact(qs, "q_start", at::kInt, {n + 1});
+        exact(ks, "kv_start", at::kInt, {n + 1});
+        const at::Tensor *out = optional(a[8], "out"), *lse = nullptr, *err = optional(a[10], "err");
+        const bool want_lse = a[9] != Py_False;
+        if (want_lse)
+            lse = optional(a[9], "lse");
+        const std::vector<int64_t> shape{q.size(0), q.size(1), v}, rows{q.size(0), q.size(1)};
+        if (out)
+            exact(*out, "out", at::kBFloat16, shape);
+        if (lse)
+            exact(*lse, "lse", at::kFloat, rows);
+        KameraMlaPrefill x;
+        std::memset(&x, 0, sizeof(x));
+        x.max_q = int32(a[5], "max_q");
+        const int causal = PyObject_IsTrue(a[6]);
+        if (causal < 0)
+            throw Raised{};
+        x.causal = causal;
+        if (a[7] == Py_None) {
+            x.scale = (float)(1.0 / std::sqrt((double)q.size(2)));
+        } else {
+            x.scale = (float)PyFloat_AsDouble(a[7]);
+            if (PyErr_Occurred())
+                throw Raised{};
+        }
+        Place on("kamera_mla_prefill_attend", q);
+        on.check(q, "q");
+        on.check(kv, "kv");
+        on.check(kr, "k_rope");
+        on.check(qs, "q_start");
+        on.check(ks, "kv_start");
+        on.check(out, "out");
+        on.check(lse, "lse");
+        on.check(err, "err");
+        int32_t* e = error_word(err);
+        on.enter(a[11]);
+        at::Tensor made_out, made_lse;
+        if (!out) {
+            made_out = on.empty(shape, at::kBFloat16);
+            out = &made_out;
+        }
+        if (want_lse && !lse) {
+            made_lse = on.empty(rows, at::kFloat);
+            lse = &made_lse;
+        }
+        x.q = q.data_ptr();
+        x.kv = kv.data_ptr();
+        x.k_rope = kr.data_ptr();
+        x.out = out->data_ptr();
+        x.lse = lse ? lse->data_ptr<float>() : nullptr;
+        x.q_start = qs.data_ptr<int32_t>();
+        x.kv_start = ks.data_ptr<int32_t>();
+        x.q_stride = step(q, 0);
+        x.q_head_stride = step(q, 1);
+        x.kv_stride = step(kv, 0);
+        x.k_rope_stride = step(kr, 0);
+        x.n_q = size32(q.size(0), "q");
+        x.n_kv = size32(kv.size(0), "kv");
+        x.n_seqs = size32(n, "q_start");
+        x.num_heads = size32(q.size(1), "q");
+        x.nope_dim = size32(nope, "q");
+        x.rope_dim = size32(kr.size(1), "k_rope");
+        x.v_dim = size32(v, "kv");
+        status(kamera_mla_prefill_attend(&x, e, on.stream()), "kamera_mla_prefill_attend");
+        Ref o(made_out.defined() ? THPVariable_Wrap(made_out) : Py_NewRef(a[8]));
+        Ref l(made_lse.defined() ? THPVariable_Wrap(made_lse) : Py_NewRef(lse ? a[9] : Py_None));
+        if (!o.get() || !l.get())
+            throw Raised{};
+        return PyTuple_Pack(2, o.get(), l.get());
+    });
+}
+
+// ------------------------------------------------------------ pages in 4 bits --
+KameraPackedPool packed_pool(const at::Tensor& t, int64_t d, PyObject* page_size, PyObject* k_unit, PyObject* v_unit)
+{
+    KameraPackedPool p;
+    std::memset(&p, 0, sizeof(p));
+    p.page_size = int32(page_size, "page_size");
+    p.head_dim = size32(d, "head_dim");
+    if (t.scalar_type() != at::kByte || t.dim() != 3 || !t.is_contiguous() || p.page_size < 1 ||
+        t.size(2) != (int64_t)p.page_size * (d + d / 8))
+        value_error("packed must be a contiguous uint8 [n_pages, H, page_size * (d + d / 8)] tensor");
+    p.data = t.data_ptr();
+    p.num_pages = t.size(0);
+    p.num_kv_heads = size32(t.size(1), "packed");
+    p.k_unit = (float)PyFloat_AsDouble(k_unit);
+    p.v_unit = (float)PyFloat_AsDouble(v_unit);
+    if (PyErr_Occurred())
+        throw Raised{};
+    return p;
+}
+
+// pages(pool_k, pool_v, page_size, kv_pages, tokens, packed, packed_pages, k_unit, v_unit, err, stream): what packing and
+// unpacking share
+PyObject* convert_pages(PyObject* const* a, Py_ssize_t n_args, bool pack)
+{
+    return guarded([&]() -> PyObject* {
+        count(n_args, 11);
+        const char* where = pack ? "kamera_pack_pages" : "kamera_unpack_pages";
+        const at::Tensor &pk = tensor(a[0], "pool_k"), &pv = tensor(a[1], "pool_v"), &kp = tensor(a[3], "kv_pages"),
+                         &tokens = tensor(a[4], "page_tokens"), &packed = tensor(a[5], "packed"),
+                         &pp = tensor(a[6], "packed_pages");
+        const at::Tensor* err = optional(a[9], "err");
+        const KameraPagedKV kv = paged_kv(pk, &pv, a[2]);
+        const KameraPackedPool pool = packed_pool(packed, kv.head_dim, a[2], a[7], a[8]);
+        const int64_t n = kp.numel();
+        exact(kp, "the bf16 pages", at::kInt, {n});
+        exact(pp, "the packed pages", at::kInt, {n});
+        exact(tokens, "page_tokens", at::kInt, {n});
+        Place on(where, pk);
+        on.check(pk, "pool_k");
+        on.check(pv, "pool_v");
+        on.check(kp, "the bf16 pages");
+        on.check(pp, "the packed pages");
+        on.check(tokens, "page_tokens");
+        on.check(packed, "packed");
+        on.check(err, "err");
+        KameraGqaPool g;
+        std::memset(&g, 0, sizeof(g));
+        g.num_layers = 1;
+        g.num_kv_heads = kv.num_kv_heads;
+        g.head_dim = kv.head_dim;
+        g.k = pk.data_ptr();
+        g.v = pv.data_ptr();
+        g.num_slots = kv.num_slots;
+        g.slot_stride = kv.num_slots > 1 ? kv.slot_stride : (int64_t)kv.num_kv_heads * kv.head_dim;
+        int32_t* e = error_word(err);
+        on.enter(a[10]);
+        status((pack ? kamera_pack_pages : kamera_unpack_pages)(&g, 0, &pool, kp.data_ptr<int32_t>(), pp.data_ptr<int32_t>(),
+                                                                tokens.data_ptr<int32_t>(), size32(n, "the pages"), e,
+                                                                on.stream()),
+               where);
+        return Py_NewRef(Py_None);
+    });
+}
+PyObject* pack_pages(PyObject*, PyObject* const* a, Py_ssize_t n) { return convert_pages(a, n, true); }
+PyObject* unpack_pages(PyObject*, PyObject* const* a, Py_ssize_t n) { return convert_pages(a, n, false); }
+
+// attend_packed(packed, q, page_size, pages, lens, max_len, pool_k, pool_v, tail_pages, tail_lens, max_tail, tail_page_size,
+//               k_unit, v_unit, scale, out, lse, err, stream, workspace)
+PyObject* attend_packed(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    return guarded([&]() -> PyObject* {
+        count(n_args, 20);
+        const at::Tensor &packed = tensor(a[0], "packed"), &q = tensor(a[1], "q");
+        if (q.dim() != 3)
+            value_error("q must be a contiguous [S, H_q, d] tensor");
+        const KameraPackedPool pool = packed_pool(packed, q.size(2), a[2], a[12], a[13]);
+        check_q(q, pool.head_dim);
+        const at::Tensor *pages = optional(a[3], "pages"), *lens = optional(a[4], "lens"), *pk = optional(a[6], "pool_k"),
+                         *pv = optional(a[7], "pool_v"), *tp = optional(a[8], "tail_pages"),
+                         *tl = optional(a[9], "tail_lens"), *err = optional(a[17], "err"), *ws = optional(a[19], "workspace");
+        KameraPageTable t = page_table(pages, lens, q.size(0), integer(a[5], "max_len"));
+        KameraPagedKV kv;
+        KameraPageTable tail;
+        const bool some = pk || pv || tp || tl;
+        if (some) {
+            if (!pk || !pv || !tp || !tl)
+                value_error("pool_k, pool_v, tail_pages and tail_lens go together");
+            kv = paged_kv(*pk, pv, a[11] == Py_None ? a[2] : a[11]);
+            if (kv.num_kv_heads != pool.num_kv_heads || kv.head_dim != pool.head_dim)
+                value_error("pool_k must have the packed pool's heads and width");
+            tail = page_table(tp, tl, q.size(0), integer(a[10], "max_tail"));
+        }
+        QueryArg qq(q, a[14], a[15], a[16]);
+        Place on("kamera_attend_packed", q);
+        on.check(q, "q");
+        on.check(packed, "packed");
+        on.check(pages, "pages");
+        on.check(lens, "lens");
+        on.check(pk, "pool_k");
+        on.check(pv, "pool_v");
+        on.check(tp, "tail_pages");
+        on.check(tl, "tail_lens");
+        on.check(qq.out, "out");
+        on.check(qq.lse, "lse");
+        on.check(err, "err");
+        on.check(ws, "workspace");
+        int32_t* e = error_word(err);
+        on.enter(a[18]);
+        qq.allocate(on, q);
+        const KameraPagedKV* k = some ? &kv : nullptr;
+        const KameraPageTable* tt = some ? &tail : nullptr;
+        Scratch s(on, ws, ws ? 0 : kamera_attend_packed_workspace_bytes(&pool, &qq.c, &t, k, tt));
+        status(kamera_attend_packed(&pool, &qq.c, &t, k, tt, s.p, s.bytes, e, on.stream()), "kamera_attend_packed");
+        return qq.result();
+    });
+}
+
 // A version check for the loader.
 PyObject* abi_version(PyObject*, PyObject*) { return PyLong_FromLong(kamera_abi_version()); }
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(append_kv),       FAST(mla_append_kv), FAST(attend_shared),
                          FAST(attend_selected), FAST(summarize_pages), FAST(select_pages),
+                         FAST(mla_attend_paged), FAST(mla_expand), FAST(mla_prefill_attend), FAST(pack_pages),
+                         FAST(unpack_pages), FAST(attend_packed),
                          {"abi_version", abi_version, METH_NOARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kamera_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

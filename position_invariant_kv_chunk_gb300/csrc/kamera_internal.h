@@ -120,6 +120,12 @@ bool make_rows_map(void* map, const void* base, int64_t rows, int64_t width, int
 bool make_groups_map(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int blocks,
                      int groups);
 
+// 3-D tensor map of rows of heads with strides of their own (columns, head, row):
+// boxes of box_cols columns x one head x box_rows rows, 128-byte swizzle, rows past
+// the end read as zero.
+bool make_heads_map(void* map, const void* base, int64_t rows, int heads, int width, int64_t row_stride,
+                    int64_t head_stride, int box_cols, int box_rows);
+
 // Tensor-core path (tcgen05 MMA for the rank-m patch; relocation with rank > 0).
 bool umma_supported(const RowsParams& p, int family);
 size_t umma_smem_bytes(const RowsParams& p);

@@ -1,0 +1,930 @@
+// kamera_mla_paged.cu -- MLA decode attention over the paged pool (absorbed form), on
+// the tensor cores.
+//
+// All query heads share one latent row a token, so a step reads 1152 bytes a token for
+// 2 H (576 + 512) flops: 30 flops a byte with 16 heads, 242 with 128.  Warp-level MMAs
+// (about 256 multiplies a cycle and SM) cannot do the first at the speed of HBM; the
+// 5th-generation ones can if the heads are their N:
+//   S^T [64 tokens x N]   = rows [64 x 576] q^T        (A: rows as they lie, K-major)
+//   O^T [512 dims x N]   += c^T [512 x 64] P^T         (A: the same rows, MN-major)
+// Heads as the M of an MMA would leave 112 of 128 rows empty with 16 heads and would
+// take all of TMEM for O (128 x 512 floats); as N they cost what they need, and O^T takes
+// 4 N columns.  Both products read the one copy of the rows in shared memory: a tile
+// of 64 tokens is four units of 128 columns, [8 groups of 8 rows][2 blocks of 64
+// columns][8][128 bytes] as a TMA box lands them, and a K-major operand of the first
+// product is an MN-major one of the second with other strides.
+//   N = 16, 32 (up to as many heads)   weights as bf16 hi + lo pairs, the lo parts N
+//                more columns of the same MMAs, which are bound by A's 4 KB an
+//                instruction: free
+//   N = 64       weights rounded to bf16; 65 to 128 heads are two CTAs that walk the
+//                same rows at the same time, so that the second reads them from L2
+// Work: one CTA an SM; the batch's tiles, all sequences behind one another, are cut into
+// as many equal ranges as there are SMs, whatever the lengths.  A sequence that lies in
+// one range is finished there; the pieces of one that is cut leave partial states, two a
+// range at most (its first sequence and its last), and a second launch joins them.
+//   warps 0-3  softmax: warp w has tokens 16 w .. 16 w + 15 of a tile (an M = 64
+//              accumulator sits in 16 lanes of each warp's quarter of TMEM), so a score
+//              fragment is that of a warp-level MMA; the maxima of the four warps meet
+//              only when one grew by more than 2^8 (a reduced barrier says so)
+//   warp 4     producer: TMA boxes of as many rows as lie together in a page
+//   warp 5     MMA
+// The scores of tile t + 1 are issued before the weights of tile t are waited for, so
+// the tensor pipe works through the softmax.  Every wait is bounded in time.
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "kamera_common.cuh"
+#include "kamera_hostcheck.h"
+#include "kamera_internal.h"
+#include "kamera_paged.h"
+#include "kamera_ptx.cuh"
+#include "kamera_tc.cuh"
+#include "kamera_warpmma.cuh"
+
+namespace kamera {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kMpTok = 64;              // tokens of a tile
+constexpr int kMpUnits = 4;             // units of 128 value columns
+constexpr int kMpDim = 512, kMpRow = 576;
+constexpr int kMpThreads = 192;
+constexpr int kMpProd = 4, kMpMma = 5;
+constexpr uint32_t kMpUnit = 16384;     // 64 rows x 128 columns
+constexpr uint32_t kMpRope = 8192;      // 64 rows x 64 columns
+constexpr uint32_t kMpAtom = 1024;
+constexpr int kMpMasks = 8;
+constexpr float kMpLazy = 8.0f;
+constexpr float kMpLog2e = 1.4426950408889634f, kMpLn2 = 0.6931471805599453f;
+
+template <int N>
+struct MpLayout {
+    static constexpr bool kPair = N <= 32;           // weights as hi + lo
+    static constexpr int NW = kPair ? 2 * N : N;     // columns of the second product
+    static constexpr int NU = N == 16 ? 11 : N == 32 ? 9 : 8;   // units in the ring: two tiles at least, the one whose
+                                                                // scores are issued and the one still to be weighed
+    static constexpr int NR = N == 32 ? 3 : 2;                  // rope blocks in theirs
+    static constexpr int NP = N == 64 ? 1 : 2;                  // buffers of weights
+    static constexpr uint32_t kQ = 0;                           // [9 blocks][N rows][128 bytes]
+    static constexpr uint32_t kQBlock = N * 128;
+    static constexpr uint32_t kP = kQ + 9 * kQBlock;            // [2][NW rows][128 bytes]
+    static constexpr uint32_t kPTile = NW * 128;
+    static constexpr uint32_t kRing = kP + NP * kPTile;
+    static constexpr uint32_t kRopes = kRing + NU * kMpUnit;
+    static constexpr uint32_t kBar = kRopes + NR * kMpRope;
+    static constexpr uint32_t kBytes = kBar + 512 + 5 * N * 4 + 1024;   // + alignment slack
+    static constexpr uint32_t kTmS = 0, kTmO = 2 * N;           // TMEM columns
+    static constexpr uint32_t kTmCols = kTmO + 4 * NW <= 256 ? 256 : 512;
+    static_assert(kTmO + 4 * NW <= kTmCols, "TMEM columns");
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(NU >= 2 * kMpUnits && NR >= 2, "the scores of a tile are issued before the one before is weighed");
+    static_assert(kP % 1024 == 0 && kRing % 1024 == 0, "swizzle atoms");
+};
+
+struct MpParams {
+    __nv_bfloat16* out;            // [n_seqs][Hq][512]
+    float* lse;                    // or null
+    const int32_t* pages;          // [n_seqs][max_pages]
+    const int32_t* lens;
+    float* o;                      // [2 ranges][Hq][512] partial outputs
+    float2* ml;                    // [2 ranges][Hq]
+    int4* span;                    // [n_seqs]: first and last range, first slot
+    int64_t num_pages;
+    int32_t n_seqs, Hq, P, max_pages, max_len;
+    int32_t blocks, ranges;        // head blocks of N; ranges of tiles
+    int32_t box_rows;
+    int32_t min_tiles;             // of a range
+    float scale;
+    int32_t* err;
+    uint64_t wait_ns;
+    int32_t withhold;
+};
+
+struct MpLaunch {
+    MpParams p;
+    CUtensorMap map_c, map_r, map_q;
+};
+
+struct MpBars {
+    uint64_t full[11], empty[11], rfull[3], rempty[3];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], pv_done, drained;
+    uint32_t mask[kMpMasks];
+    int64_t total;
+    int64_t first_at;          // global tile at which the range's first sequence starts
+    int32_t first_seq;
+    uint32_t tmem;
+    int32_t abort;
+};
+static_assert(sizeof(MpBars) <= 512, "barrier block");
+
+__device__ __forceinline__ int mp_len(const MpParams& p, int s)
+{
+    const int len = p.lens[s];
+    return len >= 0 && len <= p.max_len ? len : 0;
+}
+// Tiles of a sequence; an empty one has one, which writes its zeros.
+__device__ __forceinline__ int mp_tiles(int len) { return len > 0 ? (len - 1) / kMpTok + 1 : 1; }
+
+// The ranges in use and where range r starts, of T tiles.
+__device__ __forceinline__ int64_t mp_ranges(const MpParams& p, int64_t T)
+{
+    return min((int64_t)p.ranges, (T + p.min_tiles - 1) / p.min_tiles);
+}
+__device__ __forceinline__ int64_t mp_start(int64_t r, int64_t T, int64_t R) { return r * T / R; }
+__device__ __forceinline__ int64_t mp_range_of(int64_t tile, int64_t T, int64_t R) { return ((tile + 1) * R - 1) / T; }
+
+// A range's tiles, walked alike by every role.
+struct MpWalk {
+    int64_t left;        // tiles of the range from this one on
+    int s, len, n, t;    // sequence, its tokens and tiles, the tile
+    bool fresh;          // the first tile of a segment
+    __device__ __forceinline__ void start(const MpParams& p, const MpBars& b, int64_t lo, int64_t hi)
+    {
+        left = hi - lo;
+        s = b.first_seq;
+        len = mp_len(p, s);
+        n = mp_tiles(len);
+        t = (int)(lo - b.first_at);
+        fresh = true;
+    }
+    __device__ __forceinline__ bool last() const { return t + 1 == n || left == 1; }
+    __device__ __forceinline__ void next(const MpParams& p)
+    {
+        --left;
+        fresh = false;
+        if (++t == n && left > 0) {
+            ++s;
+            len = mp_len(p, s);
+            n = mp_tiles(len);
+            t = 0;
+            fresh = true;
+        }
+    }
+};
+
+// Total tiles and the sequence in which the range starts, by one warp.
+__device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
+{
+    int64_t sum = 0;
+    for (int s = lane; s < p.n_seqs; s += 32)
+        sum += mp_tiles(mp_len(p, s));
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    const int64_t T = sum, lo = mp_start(r, T, mp_ranges(p, T));
+    int64_t at = 0;
+    if (lane == 0) {
+        b.total = T;
+        b.first_seq = 0;
+        b.first_at = 0;
+    }
+    __syncwarp();
+    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+        const int s = s0 + lane, mine = s < p.n_seqs ? mp_tiles(mp_len(p, s)) : 0;
+        int64_t x = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+            if (lane >= d)
+                x += y;
+        }
+        const int64_t before = at + x - mine;
+        if (mine > 0 && before <= lo && lo < before + mine) {
+            b.first_seq = s;
+            b.first_at = before;
+        }
+        at += __shfl_sync(0xFFFFFFFFu, x, 31);
+        if (at > lo)
+            break;
+    }
+}
+
+// ---------------------------------------------------------------- producer --
+template <int N>
+__device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int lane, int block, int64_t lo, int64_t hi)
+{
+    using Y = MpLayout<N>;
+    const MpParams& p = L.p;
+    MpWalk w;
+    w.start(p, b, lo, hi);
+    auto page_of = [&](const MpWalk& v) {   // of the tile's 16-token piece `lane`
+        const int tok = v.t * kMpTok + 16 * lane;
+        return lane < kMpTok / 16 && tok < v.len ? p.pages[(int64_t)v.s * p.max_pages + tok / p.P] : -1;
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        bool got = true;
+        if (lane == 0)
+            got = wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+        return __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+    };
+    const int R = p.box_rows, boxes = kMpTok / R;
+    uint32_t unit = 0, rope = 0, tile = 0, seg = 0;
+    bool ok = true;
+    int next = page_of(w);
+    while (w.left > 0 && ok) {
+        if (w.fresh) {
+            if (seg > 0 && !(ok = wait(&b.q_empty, seg - 1)))
+                break;
+            if (lane == 0 && !p.withhold) {
+                ptx::mbar_arrive_expect_tx(ptx::smem_addr(&b.q_full), 9 * Y::kQBlock);
+                for (int i = 0; i < 9; ++i)
+                    ptx::tma_load_2d(sbase + Y::kQ + i * Y::kQBlock, &L.map_q, 64 * i, w.s * p.Hq + block * N,
+                                     ptx::smem_addr(&b.q_full));
+            }
+            ++seg;
+        }
+        const int page = next, tok0 = w.t * kMpTok, ntok = min(kMpTok, w.len - tok0);
+        const bool in = lane < kMpTok / 16 && 16 * lane < ntok, good = in && page >= 0 && page < p.num_pages;
+        if (in && !good && block == 0)
+            raise_err(p.err, KAMERA_DEVERR_SLOT);
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
+        w.next(p);
+        if (w.left > 0)
+            next = page_of(w);
+        // box l: rows l R .. l R + R - 1, whose page piece l R / 16 looked up
+        const int off = lane * R, from = __shfl_sync(0xFFFFFFFFu, page, (off / 16) & 31);
+        const bool mine = lane < boxes && off < ntok && ((mask >> (off / 16)) & 1u);
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+        const int group = (int)(((int64_t)from * p.P + (tok0 + off) % p.P) >> 3);
+        if (lane == 0)
+            b.mask[tile % kMpMasks] = mask;
+        auto load = [&](uint32_t dst, uint64_t* bar, const CUtensorMap* map, int col, uint32_t row_group) {
+            const uint32_t full = ptx::smem_addr(bar);
+            if (lane == 0 && !p.withhold) {
+                if (n > 0)
+                    ptx::mbar_arrive_expect_tx(full, (uint32_t)n * (uint32_t)(R / 8) * row_group);
+                else
+                    ptx::mbar_arrive(full);
+            }
+            __syncwarp();
+            if (mine && !p.withhold)
+                ptx::tma_load_4d(dst + (uint32_t)(off / 8) * row_group, map, 0, 0, col, group, full);
+        };
+        for (int u = 0; u < kMpUnits && ok; ++u, ++unit) {
+            const uint32_t at = unit % Y::NU, lap = unit / Y::NU;
+            if (lap > 0 && !(ok = wait(&b.empty[at], lap - 1)))
+                break;
+            load(sbase + Y::kRing + at * kMpUnit, &b.full[at], &L.map_c, 2 * u, 2 * kMpAtom);
+        }
+        if (!ok)
+            break;
+        const uint32_t at = rope % Y::NR, lap = rope / Y::NR;
+        if (lap > 0 && !(ok = wait(&b.rempty[at], lap - 1)))
+            break;
+        load(sbase + Y::kRopes + at * kMpRope, &b.rfull[at], &L.map_r, kMpDim / 64, kMpAtom);
+        ++rope;
+        ++tile;
+    }
+    // Without a timeout the MMA lane has waited for every fill.  After one, the copies
+    // this warp started land before the CTA leaves.
+    if (lane == 0 && !p.withhold && *static_cast<volatile int32_t*>(&b.abort)) {
+        if (seg > 0)
+            pf_drain_wait(ptx::smem_addr(&b.q_full), (seg - 1) & 1u, p.wait_ns);
+        for (uint32_t k = unit > (uint32_t)Y::NU ? unit - Y::NU : 0u; k < unit; ++k)
+            pf_drain_wait(ptx::smem_addr(&b.full[k % Y::NU]), (k / Y::NU) & 1u, p.wait_ns);
+        for (uint32_t k = rope > (uint32_t)Y::NR ? rope - Y::NR : 0u; k < rope; ++k)
+            pf_drain_wait(ptx::smem_addr(&b.rfull[k % Y::NR]), (k / Y::NR) & 1u, p.wait_ns);
+    }
+    __syncwarp();
+}
+
+// --------------------------------------------------------------------- MMA --
+__device__ __forceinline__ bool mp_elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+template <int N>
+__device__ void mp_mma(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t tm, int64_t lo, int64_t hi)
+{
+    using Y = MpLayout<N>;
+    const MpParams& p = L.p;
+    constexpr uint32_t idS = ptx::idesc_bf16_f32(kMpTok, N);
+    constexpr uint32_t idO = ptx::idesc_bf16_f32(128, Y::NW) | (1u << 15);       // A: MN-major
+    constexpr uint32_t hiU = (2 * kMpAtom >> 4) | (1u << 14) | (2u << 29);       // units: groups of 8 rows 2 KB apart
+    constexpr uint32_t hi1 = (kMpAtom >> 4) | (1u << 14) | (2u << 29);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+    };
+    auto desc = [](uint32_t lo_word, uint32_t hi_word) { return ((uint64_t)hi_word << 32) | lo_word; };
+    const uint32_t q_lo = ((sbase + Y::kQ) >> 4) | (1u << 16), p_lo = ((sbase + Y::kP) >> 4) | (1u << 16);
+    const uint32_t u_lo = (sbase + Y::kRing) >> 4, r_lo = ((sbase + Y::kRopes) >> 4) | (1u << 16);
+    uint32_t seg = 0;
+    // scores of tile t; its rope block is free after them
+    auto scores = [&](uint32_t t, const MpWalk& w) -> bool {
+        if (w.fresh && !wait(&b.q_full, seg))
+            return false;
+        const uint32_t d = tm + Y::kTmS + (t & 1u) * N;
+#pragma unroll 1
+        for (uint32_t u = 0; u < kMpUnits; ++u) {
+            const uint32_t k = kMpUnits * t + u, at = k % Y::NU;
+            if (!wait(&b.full[at], k / Y::NU))
+                return false;
+            ptx::tc_fence_after();
+            const uint32_t a = (u_lo + at * (kMpUnit >> 4)) | (1u << 16), q = q_lo + 2 * u * (Y::kQBlock >> 4);
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    ptx::umma_bf16(d, desc(a + blk * (kMpAtom >> 4) + 2 * ks, hiU),
+                                   desc(q + blk * (Y::kQBlock >> 4) + 2 * ks, hi1), idS, u + blk + ks > 0 ? 1u : 0u);
+        }
+        const uint32_t at = t % Y::NR;
+        if (!wait(&b.rfull[at], t / Y::NR))
+            return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+            ptx::umma_bf16(d, desc(r_lo + at * (kMpRope >> 4) + 2 * ks, hi1),
+                           desc(q_lo + 8 * (Y::kQBlock >> 4) + 2 * ks, hi1), idS, 1u);
+        ptx::umma_commit(ptx::smem_addr(&b.rempty[at]));
+        ptx::umma_commit(ptx::smem_addr(&b.s_full[t & 1u]));
+        if (w.last()) {
+            ptx::umma_commit(ptx::smem_addr(&b.q_empty));
+            ++seg;
+        }
+        return true;
+    };
+    auto weigh = [&](uint32_t t, bool fresh) -> bool {
+        if (!wait(&b.p_full[t & 1u], t >> 1))
+            return false;
+        ptx::tc_fence_after();
+        const uint32_t pb = p_lo + t % Y::NP * (Y::kPTile >> 4);
+#pragma unroll 1
+        for (uint32_t u = 0; u < kMpUnits; ++u) {
+            const uint32_t at = (kMpUnits * t + u) % Y::NU;
+            const uint32_t a = (u_lo + at * (kMpUnit >> 4)) | ((kMpAtom >> 4) << 16);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                ptx::umma_bf16(tm + Y::kTmO + u * Y::NW, desc(a + ks * (4 * kMpAtom >> 4), hiU), desc(pb + 2 * ks, hi1),
+                               idO, fresh && ks == 0 ? 0u : 1u);
+            ptx::umma_commit(ptx::smem_addr(&b.empty[at]));
+        }
+        ptx::umma_commit(ptx::smem_addr(&b.pv_done));
+        return true;
+    };
+    MpWalk w;
+    w.start(p, b, lo, hi);
+    uint32_t t = 0;
+    bool ok = w.left <= 0 || scores(0, w);
+    while (w.left > 0 && ok) {
+        const bool fresh = w.fresh;
+        w.next(p);
+        ok = (w.left <= 0 || scores(t + 1, w)) && weigh(t, fresh);
+        ++t;
+    }
+    // every MMA issued here completes before TMEM is freed
+    ptx::umma_commit(ptx::smem_addr(&b.drained));
+    pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
+}
+
+// ----------------------------------------------------------------- softmax --
+// A warp's 16 tokens x N heads: register 4 j + 2 r + c is token lane / 4 + 8 r, head
+// 8 j + 2 (lane % 4) + c.
+template <int N>
+__device__ __forceinline__ void mp_ld_scores(uint32_t ta, uint32_t (&r)[N / 2])
+{
+    if constexpr (N == 16) {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(ta)
+                     : "memory");
+    } else if constexpr (N == 32) {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+                     "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                       "=r"(r[15])
+                     : "r"(ta)
+                     : "memory");
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                       "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                       "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                       "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                     : "r"(ta)
+                     : "memory");
+    }
+}
+
+// Four 8 x 8 blocks of bf16 pairs, each stored transposed: row i of block k at the
+// address of lane 8 k + i.
+__device__ __forceinline__ void stsm_x4_t(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y),
+                 "r"(z), "r"(w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mp_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The four softmax warps meet; whether any thread said yes.
+__device__ __forceinline__ bool mp_any(bool x)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(x ? 1u : 0u)
+                 : "memory");
+    return r != 0;
+}
+
+template <int N>
+__device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* ex, uint32_t tm, int warp, int lane,
+                           int block, int range, int64_t lo, int64_t hi)
+{
+    using Y = MpLayout<N>;
+    constexpr int J = N / 8;
+    const MpParams& p = L.p;
+    const int gq = lane >> 2, t4 = lane & 3;
+    const uint32_t lanes = tm + ((uint32_t)warp << 21);
+    const float sl2 = p.scale * kMpLog2e;
+    const int heads = min(N, p.Hq - block * N);
+    const int64_t T = b.total, R = mp_ranges(p, T);
+    float* wmax = ex;              // [4 warps][N]: the warps' maxima; their sums
+    float* fac = ex + 4 * N;       // [N]: factors of the running output
+    float m[J][2], l[J][2];        // heads 8 j + 2 t4, + 1: the agreed maximum (log2 units), this thread's sum
+    // where this lane's row of a stored block goes: block k = (j, half of the tokens) in pairs of j
+    const uint32_t st_row = lane & 7, st_half = (lane >> 3) & 1, st_j = lane >> 4;
+    const uint32_t st = sbase + Y::kP + st_j * kMpAtom + sw128(st_row, 2 * warp + st_half);
+    MpWalk w;
+    w.start(p, b, lo, hi);
+    int64_t at = lo;               // the tile's place among all
+    bool ok = true;
+    for (uint32_t t = 0; w.left > 0; ++t, ++at) {
+        if (w.fresh) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.f;
+        }
+        const int ntok = min(kMpTok, w.len - w.t * kMpTok);
+        ok = ok && wmma16::tile_wait(ptx::smem_addr(&b.s_full[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        uint32_t s[N / 2];
+        bool grew = false;
+        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[t % kMpMasks]);
+        float x[J][4];
+        if (ok) {
+            ptx::tc_fence_after();
+            mp_ld_scores<N>(lanes + Y::kTmS + (t & 1u) * N, s);
+            const bool here = (mask >> warp) & 1u;
+            const bool in0 = here && 16 * warp + gq < ntok, in1 = here && 16 * warp + gq + 8 < ntok;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    x[j][c] = in0 ? __uint_as_float(s[4 * j + c]) * sl2 : -INFINITY;
+                    x[j][2 + c] = in1 ? __uint_as_float(s[4 * j + 2 + c]) * sl2 : -INFINITY;
+                    grew |= fmaxf(x[j][c], x[j][2 + c]) > m[j][c] + kMpLazy;
+                }
+            }
+        }
+        if (mp_any(grew || !ok)) {   // rare but for a segment's first tile
+            if (mp_any(!ok))
+                break;               // all four warps
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = fmaxf(x[j][c], x[j][2 + c]);
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+                    if (gq == 0)
+                        wmax[warp * N + 8 * j + 2 * t4 + c] = v;
+                }
+            mp_sync();
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int h = 8 * j + 2 * t4 + c;
+                    float v = m[j][c];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v = fmaxf(v, wmax[k * N + h]);
+                    const float f = v == -INFINITY ? 1.f : pf_ex2(m[j][c] - v);
+                    l[j][c] *= f;
+                    m[j][c] = v;
+                    if (warp == 0 && gq == 0)
+                        fac[h] = f;
+                }
+            if (!w.fresh) {          // the running output, once the products before are in it
+                ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                ptx::tc_fence_after();
+                mp_sync();
+#pragma unroll 1
+                for (int c = 0; c < 4 * Y::NW / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(lanes + Y::kTmO + 32 * c, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[(32 * (c % (N / 16 > 1 ? N / 32 : 1)) + i) % N]);
+                    tmem_st32(lanes + Y::kTmO + 32 * c, o);
+                }
+                tmem_wait_st();
+            }
+            mp_sync();               // the exchange's arrays are free again
+        }
+        // weights, transposed into the operand rows (heads) of the second product
+        const uint32_t dst = st + t % Y::NP * Y::kPTile;
+        if (Y::NP == 1 && t > 0) {   // (two buffers: the scores of this tile were issued after that product)
+            ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+#pragma unroll
+        for (int j = 0; j < J; j += 2) {
+            uint32_t h[4], lo4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {   // block k: heads of j + k / 2, tokens of half k & 1
+                const int jj = j + (k >> 1), r = k & 1;
+                const float m0 = m[jj][0] == -INFINITY ? 0.f : m[jj][0], m1 = m[jj][1] == -INFINITY ? 0.f : m[jj][1];
+                const float a = pf_ex2(x[jj][2 * r] - m0), c = pf_ex2(x[jj][2 * r + 1] - m1);
+                l[jj][0] += a;
+                l[jj][1] += c;
+                if constexpr (Y::kPair) {
+                    h[k] = weight_hi(a, c);
+                    lo4[k] = pack_bf16x2(fmaf(bf16lo(h[k]), kLessHi, a), fmaf(bf16hi(h[k]), kLessHi, c));
+                } else {
+                    h[k] = pack_bf16x2(a, c);
+                }
+            }
+            stsm_x4_t(dst + j * kMpAtom, h[0], h[1], h[2], h[3]);
+            if constexpr (Y::kPair)
+                stsm_x4_t(dst + (J + j) * kMpAtom, lo4[0], lo4[1], lo4[2], lo4[3]);
+        }
+        if (ntok < kMpTok || mask != 0xFu) {   // value rows without a token: zero, so that zero weights add nothing
+            for (int e = threadIdx.x; e < kMpTok * 64; e += 128) {
+                const int r = e >> 6, piece = e & 63, u = piece >> 4, blk = (piece >> 3) & 1;
+                if (r >= ntok || !((mask >> (r >> 4)) & 1u))
+                    ptx::st_shared_zero16(sbase + Y::kRing + (kMpUnits * t + u) % Y::NU * kMpUnit +
+                                          (uint32_t)(r >> 3) * 2 * kMpAtom + blk * kMpAtom + sw128(r & 7, piece & 7));
+            }
+        }
+        ptx::fence_proxy_async();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(ptx::smem_addr(&b.p_full[t & 1u]));
+        if (!w.last()) {
+            w.next(p);
+            continue;
+        }
+        // ---- the segment's end: its state
+        const int s_seq = w.s;
+        const int64_t a0 = at - w.t, r0 = mp_range_of(a0, T, R), r1 = mp_range_of(a0 + w.n - 1, T, R);
+        const int first_slot = (int)(2 * r0 + (mp_start(r0, T, R) == a0 ? 0 : 1));
+        const bool whole = r0 == r1;
+        const int slot = range == r0 ? first_slot : 2 * range;
+        if (range == r0 && block == 0 && threadIdx.x == 0)
+            p.span[s_seq] = make_int4((int)r0, (int)r1, first_slot, 0);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], 4);
+                l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], 8);
+                l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], 16);
+                if (gq == 0)
+                    wmax[warp * N + 8 * j + 2 * t4 + c] = l[j][c];
+            }
+        mp_sync();
+        const int64_t row0 = (int64_t)s_seq * p.Hq + block * N, part0 = (int64_t)slot * p.Hq + block * N;
+        if (warp == 0 && gq == 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int h = 8 * j + 2 * t4 + c;
+                    const float sum = (wmax[h] + wmax[N + h]) + (wmax[2 * N + h] + wmax[3 * N + h]);
+                    fac[h] = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
+                    if (h < heads) {
+                        if (!whole)
+                            p.ml[part0 + h] = make_float2(m[j][c], sum);
+                        else if (p.lse)
+                            p.lse[row0 + h] = sum > 0.f ? (m[j][c] + log2f(sum)) * kMpLn2 : (sum == sum ? -INFINITY : sum);
+                    }
+                }
+        }
+        ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), t & 1u, &b.abort, p.err, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        ptx::tc_fence_after();
+        mp_sync();
+#pragma unroll 1
+        for (int u = 0; u < kMpUnits; ++u) {
+            const int dim = 128 * u + 32 * warp + lane;
+#pragma unroll 1
+            for (int h0 = 0; h0 < heads; h0 += 16) {
+                uint32_t o[32];   // 16 heads: their hi columns, and the lo ones
+                if constexpr (N == 16) {
+                    tmem_ld32(lanes + Y::kTmO + u * Y::NW, o);
+                } else {
+                    uint32_t a[8], c[8], d[8], e[8];
+                    const uint32_t from = lanes + Y::kTmO + u * Y::NW + h0;
+                    ptx::tmem_ld8x2_issue(from, from + 8, a, c);
+                    ptx::tmem_wait8x2(a, c);
+                    if constexpr (Y::kPair) {
+                        ptx::tmem_ld8x2_issue(from + N, from + N + 8, d, e);
+                        ptx::tmem_wait8x2(d, e);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[i] = a[i], o[8 + i] = c[i];
+                        o[16 + i] = Y::kPair ? d[i] : 0u, o[24 + i] = Y::kPair ? e[i] : 0u;
+                    }
+                }
+                if (!ok)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (h0 + i >= heads)
+                        break;
+                    float v = __uint_as_float(o[i]);
+                    if constexpr (Y::kPair)
+                        v += __uint_as_float(o[16 + i]);
+                    if (whole)
+                        p.out[(row0 + h0 + i) * kMpDim + dim] = __float2bfloat16_rn(v * fac[h0 + i]);
+                    else
+                        p.o[(part0 + h0 + i) * kMpDim + dim] = v;
+                }
+            }
+        }
+        ptx::tc_fence_before();
+        mp_sync();   // the exchange's arrays, and TMEM, are free for the next segment
+        w.next(p);
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(kMpThreads, 1) mla_paged_kernel(const __grid_constant__ MpLaunch L)
+{
+    using Y = MpLayout<N>;
+    const MpParams& p = L.p;
+    extern __shared__ __align__(16) unsigned char raw[];
+    const uint32_t addr = ptx::smem_addr(raw), pad = (1024u - (addr & 1023u)) & 1023u, sbase = addr + pad;
+    MpBars& b = *reinterpret_cast<MpBars*>(raw + pad + Y::kBar);
+    float* ex = reinterpret_cast<float*>(raw + pad + Y::kBar + 512);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int block = blockIdx.x % p.blocks, range = blockIdx.x / p.blocks;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Y::NU; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&b.full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.empty[i]), 1);
+        }
+        for (int i = 0; i < Y::NR; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&b.rfull[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.rempty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&b.s_full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.p_full[i]), 4);
+        }
+        ptx::mbar_init(ptx::smem_addr(&b.q_full), 1);
+        ptx::mbar_init(ptx::smem_addr(&b.q_empty), 1);
+        ptx::mbar_init(ptx::smem_addr(&b.pv_done), 1);
+        ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
+        b.abort = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == kMpProd && lane == 0) {
+        ptx::prefetch_tmap(&L.map_c);
+        ptx::prefetch_tmap(&L.map_r);
+        ptx::prefetch_tmap(&L.map_q);
+    }
+    if (warp == kMpMma) {
+        ptx::tmem_alloc(ptx::smem_addr(&b.tmem), Y::kTmCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::grid_wait();
+    if (warp == 0)
+        mp_locate(p, b, range, lane);
+    if (blockIdx.x == 0 && warp > 0)
+        for (int s = threadIdx.x - 32; s < p.n_seqs; s += kMpThreads - 32)
+            if (p.lens[s] < 0 || p.lens[s] > p.max_len)
+                raise_err(p.err, KAMERA_DEVERR_LEN);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::grid_launch_next();   // (this CTA has its TMEM: none that starts early can take it)
+    const uint32_t tm = b.tmem;
+    const int64_t T = b.total, R = mp_ranges(p, T);
+    if (range < R) {   // (else: fewer tiles than ranges)
+        const int64_t lo = mp_start(range, T, R), hi = mp_start(range + 1, T, R);
+        if (warp < 4)
+            mp_softmax<N>(L, b, sbase, ex, tm, warp, lane, block, range, lo, hi);
+        else if (warp == kMpProd)
+            mp_producer<N>(L, b, sbase, lane, block, lo, hi);
+        else if (mp_elect())
+            mp_mma<N>(L, b, sbase, tm, lo, hi);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kMpMma) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tm, Y::kTmCols);
+    }
+}
+
+// ------------------------------------------------------------------- merge --
+// The rows whose sequence was cut: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
+// over the partial states of its ranges.  A CTA a row, a thread four columns.
+__global__ void __launch_bounds__(128) mla_merge_kernel(const MpParams p)
+{
+    const int s = blockIdx.x / p.Hq, h = blockIdx.x - s * p.Hq;
+    ptx::grid_wait();
+    ptx::grid_launch_next();
+    const int4 sp = p.span[s];
+    // finished where it was read; or, after a timeout, never written
+    if (sp.x == sp.y || sp.x < 0 || sp.y < sp.x || sp.y >= p.ranges || (sp.z >> 1) != sp.x)
+        return;
+    const int n = sp.y - sp.x + 1;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? sp.z : 2 * (sp.x + i)) * p.Hq + h; };
+    float m = -INFINITY;
+    for (int i = 0; i < n; ++i)
+        m = fmaxf(m, p.ml[slot(i)].x);
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int U = 4;
+    for (int i0 = 0; i0 < n; i0 += U) {
+        float4 v[U];
+        float2 ml[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t at = slot(min(i0 + k, n - 1));
+            ml[k] = p.ml[at];
+            v[k] = *reinterpret_cast<const float4*>(p.o + at * kMpDim + 4 * threadIdx.x);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i0 + k >= n || ml[k].y == 0.f)   // no weight: nothing to add (and no maximum to scale by)
+                continue;
+            const float f = pf_ex2(ml[k].x - m);
+            l = fmaf(ml[k].y, f, l);
+            acc.x = fmaf(v[k].x, f, acc.x);
+            acc.y = fmaf(v[k].y, f, acc.y);
+            acc.z = fmaf(v[k].z, f, acc.z);
+            acc.w = fmaf(v[k].w, f, acc.w);
+        }
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    const int64_t row = blockIdx.x;
+    *reinterpret_cast<uint2*>(p.out + row * kMpDim + 4 * threadIdx.x) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (threadIdx.x == 0 && p.lse)
+        p.lse[row] = l > 0.f ? (m + log2f(l)) * kMpLn2 : (l == l ? -INFINITY : l);
+}
+
+// -------------------------------------------------------------------- host --
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int mp_heads(int Hq) { return Hq <= 16 ? 16 : Hq <= 32 ? 32 : 64; }
+
+struct MpNeed {
+    size_t o, ml, span;
+    size_t bytes() const { return o + ml + span; }
+};
+MpNeed mp_need(const MpParams& p)
+{
+    const size_t rows = (size_t)2 * p.ranges * p.Hq;
+    return {up256(rows * kMpDim * 4), up256(rows * 8), up256((size_t)p.n_seqs * 16)};
+}
+
+int mp_plan(const KameraPagedMlaKV* kv, const KameraPagedQuery* q, const KameraPageTable* t, MpParams* p)
+{
+    if (!kv || !q || !t || kv->reserved != 0 || q->reserved != 0 || kv->kv_lora_rank < 1 || kv->rope_dim < 0 ||
+        kv->page_size < 1 || kv->num_slots < 0 || q->n_seqs < 0 || q->num_q_heads < 1 || !(q->scale == q->scale) ||
+        t->max_len < 0 || t->max_pages < 0)
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    if (kv->kv_lora_rank != kMpDim || kv->rope_dim != kMpRow - kMpDim || q->num_q_heads > 128 || kv->page_size % 16 ||
+        kv->num_slots > 0x7FFFFFFF || q->n_seqs > 65535 || t->max_len > 0x7FFFFF00)
+        return KAMERA_ERR_UNSUPPORTED;
+    if ((int64_t)t->max_pages * kv->page_size < t->max_len)
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    std::memset(p, 0, sizeof(*p));
+    p->n_seqs = q->n_seqs;
+    p->Hq = q->num_q_heads;
+    p->P = kv->page_size;
+    p->num_pages = kv->num_slots / kv->page_size;
+    p->max_pages = t->max_pages;
+    p->max_len = t->max_len;
+    p->scale = q->scale;
+    if (q->n_seqs == 0)
+        return KAMERA_OK;
+    const int N = mp_heads(p->Hq);
+    p->blocks = (p->Hq + N - 1) / N;
+    const int64_t most = (int64_t)p->n_seqs * std::max<int64_t>(1, ((int64_t)p->max_len + kMpTok - 1) / kMpTok);
+    p->ranges = (int32_t)std::min<int64_t>(std::max(1, device_sms() / p->blocks), most);
+    p->min_tiles = 1;
+    return KAMERA_OK;
+}
+
+template <int N>
+cudaError_t mp_launch(const MpLaunch& L, cudaStream_t stream)
+{
+    using Y = MpLayout<N>;
+    // set at every launch: the attribute belongs to the current device's context
+    const cudaError_t e =
+        cudaFuncSetAttribute(mla_paged_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::kBytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_after(mla_paged_kernel<N>, dim3((unsigned)(L.p.ranges * L.p.blocks)), kMpThreads, Y::kBytes, stream,
+                        true, L);
+}
+
+}  // namespace
+
+}  // namespace kamera
+
+using namespace kamera;
+
+extern "C" {
+
+size_t kamera_mla_attend_paged_workspace_bytes(const KameraPagedMlaKV* kv, const KameraPagedQuery* query,
+                                               const KameraPageTable* table)
+{
+    MpParams p;
+    return mp_plan(kv, query, table, &p) == KAMERA_OK && p.n_seqs > 0 ? mp_need(p).bytes() : 0;
+}
+
+int kamera_mla_attend_paged(const KameraPagedMlaKV* kv, const KameraPagedQuery* query, const KameraPageTable* table,
+                            void* d_workspace, size_t workspace_bytes, int32_t* d_err, struct CUstream_st* stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    MpLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    MpParams& p = L.p;
+    const int rc = mp_plan(kv, query, table, &p);
+    if (rc || p.n_seqs == 0)
+        return rc;
+    if (!query->q || !query->out || !table->lens || (!table->pages && table->max_len > 0) || !d_workspace)
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    int e;
+    if ((e = check_strided(kv->kv, 1, 0, kv->num_slots, kv->slot_stride, kMpRow, false)))
+        return e;
+    if (!aligned16(query->q) || !aligned16(query->out) || !aligned16(d_workspace) ||
+        ((reinterpret_cast<uintptr_t>(query->lse) | reinterpret_cast<uintptr_t>(table->pages) |
+          reinterpret_cast<uintptr_t>(table->lens)) & 3))
+        return KAMERA_ERR_MISALIGNED;
+    const MpNeed need = mp_need(p);
+    if (workspace_bytes < need.bytes())
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    using Span = std::pair<uintptr_t, uintptr_t>;
+    auto bytes = [](const void* a, int64_t n) -> Span {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(a);
+        return {lo, a ? lo + (uintptr_t)n : lo};
+    };
+    const int64_t rows = (int64_t)p.n_seqs * p.Hq;
+    const Span in[] = {span(kv->kv, 1, 0, kv->num_slots, kv->slot_stride, kMpRow), bytes(query->q, rows * kMpRow * 2),
+                       bytes(table->pages, (int64_t)p.n_seqs * p.max_pages * 4), bytes(table->lens, (int64_t)p.n_seqs * 4)};
+    const Span outs[] = {bytes(query->out, rows * kMpDim * 2), bytes(query->lse, rows * 4),
+                         bytes(d_workspace, (int64_t)need.bytes())};
+    for (int i = 0; i < 3; ++i) {
+        for (const Span& a : in)
+            if (overlap(a, outs[i]))
+                return KAMERA_ERR_INVALID_ARGUMENT;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j]))
+                return KAMERA_ERR_INVALID_ARGUMENT;
+    }
+    p.out = static_cast<__nv_bfloat16*>(query->out);
+    p.lse = query->lse;
+    p.pages = table->pages;
+    p.lens = table->lens;
+    unsigned char* ws = static_cast<unsigned char*>(d_workspace);
+    p.o = reinterpret_cast<float*>(ws);
+    p.ml = reinterpret_cast<float2*>(ws + need.o);
+    p.span = reinterpret_cast<int4*>(ws + need.o + need.ml);
+    p.err = d_err;
+    p.wait_ns = wait_limit_ns();
+    p.withhold = test_withhold_loads() ? 1 : 0;
+    p.box_rows = 16;
+    while (p.box_rows < kMpTok && p.P % (2 * p.box_rows) == 0)
+        p.box_rows *= 2;
+    const int N = mp_heads(p.Hq);
+    const int64_t map_rows = std::max<int64_t>(kv->num_slots, 8);   // a pool without a whole page has none to read
+    if (!make_groups_map(&L.map_c, kv->kv, map_rows, kMpRow, kv->slot_stride, 2, p.box_rows / 8) ||
+        !make_groups_map(&L.map_r, kv->kv, map_rows, kMpRow, kv->slot_stride, 1, p.box_rows / 8) ||
+        !make_rows_map(&L.map_q, query->q, rows, kMpRow, kMpRow, 64, N))
+        return KAMERA_ERR_CUDA;
+    const cudaError_t ce = N == 16 ? mp_launch<16>(L, stream) : N == 32 ? mp_launch<32>(L, stream) : mp_launch<64>(L, stream);
+    if (ce != cudaSuccess)
+        return KAMERA_ERR_CUDA;
+    if (p.ranges > 1 &&
+        launch_after(mla_merge_kernel, dim3((unsigned)rows), 128, 0, stream, true, p) != cudaSuccess)
+        return KAMERA_ERR_CUDA;
+    return KAMERA_OK;
+}
+
+}  // extern "C"

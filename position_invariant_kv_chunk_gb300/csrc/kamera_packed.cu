@@ -1,0 +1,1023 @@
+// kamera_packed.cu -- decode attention over pages in 4 bits (kamera_pack.cu has their
+// layout), joined with a tail of bf16 pages.
+//
+// A packed token costs 9 d / 8 bytes a KV head (144 for d = 128) where bf16 costs 4 d,
+// for the same 4 d G flops: warp-level MMAs, which just keep up with bf16 pages, would
+// bound it.  So the products run on the 5th-generation tensor cores, and what the
+// threads do is decode: one conversion (two e2m1 codes to fp16) and one multiplication
+// (the scale) for two numbers, straight into TMEM as the A operands:
+//   S^T [128 tokens x N]    = K [128 x d] q^T      thread = token: its row of K
+//   O^T [d channels x N]   += V^T [d x 128] P^T    thread = channel: its 128 tokens
+// with the query heads of a KV head (8 or 16) as N.  Everything is exact in fp16: e2m1
+// times e4m3 has 6 significant bits, and the queries enter as q 2^(10 - e), e the
+// exponent of the row's largest (a bf16 number keeps its 8 bits down to 2^-24 of it).
+// The weights are rounded to fp16 (2^-11), as 2^7 times the usual ones, so that small
+// ones stay normal down to 2^-21.
+//   warps 0-3   keys, then softmax (warp w: tokens 32 w .. 32 w + 31), output
+//   warps 4-7   values
+//   warp 8      producer: one bulk copy for 16 tokens of a head, a ring of tiles
+//   warp 9      MMA; it owns TMEM (256 columns, so that two CTAs share an SM: one
+//               decodes while the other waits for its products)
+// Work: the batch's tiles of 128 tokens, all (sequence, KV head) behind one another, in
+// equal ranges, one a CTA; each leaves a partial state for every (sequence, KV head)
+// that it touches, and a last launch joins them with the tail's.
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "kamera_common.cuh"
+#include "kamera_hostcheck.h"
+#include "kamera_internal.h"
+#include "kamera_packed.h"
+#include "kamera_paged.h"
+#include "kamera_ptx.cuh"
+#include "kamera_tc.cuh"
+#include "kamera_warpmma.cuh"
+
+namespace kamera {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kP4Tok = 128, kP4Pieces = kP4Tok / 16;
+constexpr int kP4Threads = 320, kP4Prod = 8, kP4Mma = 9;
+constexpr uint32_t kP4TmK = 0, kP4TmV = 64, kP4TmS = 128, kP4TmO = 144, kP4TmCols = 256;
+constexpr float kP4Lazy = 8.0f;
+constexpr float kP4Up = 7.0f;             // weights are 2^7 times the usual ones: at most 2^15 with the lazy growth
+constexpr float kP4Log2e = 1.4426950408889634f, kP4Ln2 = 0.6931471805599453f;
+
+template <int D, int N>
+struct P4Layout {
+    static constexpr uint32_t kTile = kP4Pieces * kPackedPiece<D>;
+    static constexpr int NS = D == 128 ? 5 : 8;               // tiles in the ring
+    static constexpr uint32_t kQ = 0;                         // [d / 64 blocks][N rows][128 bytes]
+    static constexpr uint32_t kP = kQ + (D / 64) * N * 128;   // [2 blocks of 64 tokens][N rows][128 bytes]
+    static constexpr uint32_t kRing = kP + 2 * N * 128;
+    static constexpr uint32_t kBar = kRing + NS * kTile;
+    static constexpr uint32_t kBytes = kBar + 512 + 6 * N * 4 + 1024;   // + alignment slack
+    static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
+    static_assert(kRing % 128 == 0 && kTile % 128 == 0, "copies");
+};
+
+struct P4Params {
+    const __nv_bfloat16* q;
+    __nv_bfloat16* out;
+    float* lse;                    // or null
+    const unsigned char* data;     // packed pages
+    const int32_t* pages;
+    const int32_t* lens;
+    float* o;                      // [2 ranges][G][d]: partial outputs
+    float2* ml;                    // [2 ranges][G]
+    int4* span;                    // [n_seqs * H]: first and last range, first slot
+    int64_t num_pages;
+    int32_t n_seqs, H, G, P, max_pages, max_len, ranges;
+    float scale, k_unit, v_unit;
+    // the tail's partial states: [rows][tail_slots]
+    const float* tail_o;
+    const float2* tail_ml;
+    const int32_t* tail_lens;
+    int32_t max_tail, tail_split, tail_slots;   // 16-token pieces of a split; splits (0: no tail)
+    int32_t first;                 // the call's first kernel
+    int32_t* err;
+    uint64_t wait_ns;
+    int32_t withhold;
+};
+
+struct P4Bars {
+    uint64_t full[8], empty[8], k_full, v_full, s_full, p_full, pv_done, drained;
+    uint32_t mask[8];              // of a stage's tile: 16-token pieces that are there
+    int64_t total, first_at;
+    int32_t first_seq;
+    uint32_t tmem;
+    int32_t abort;
+};
+static_assert(sizeof(P4Bars) <= 512, "barrier block");
+
+__device__ __forceinline__ int p4_len(const P4Params& p, int s)
+{
+    const int len = p.lens[s];
+    return len >= 0 && len <= p.max_len ? len : 0;
+}
+__device__ __forceinline__ int p4_tiles(int len) { return (len + kP4Tok - 1) / kP4Tok; }
+__device__ __forceinline__ int64_t p4_start(int64_t r, int64_t T, int64_t R) { return r * T / R; }
+__device__ __forceinline__ int64_t p4_range_of(int64_t tile, int64_t T, int64_t R) { return ((tile + 1) * R - 1) / T; }
+
+// A range's tiles, walked alike by every role: sequence, KV head, tile.
+struct P4Walk {
+    int64_t left;
+    int s, h, len, n, t;
+    bool fresh;
+    __device__ __forceinline__ void start(const P4Params& p, const P4Bars& b, int64_t lo, int64_t hi)
+    {
+        left = hi - lo;
+        s = b.first_seq;
+        len = p4_len(p, s);
+        n = p4_tiles(len);
+        const int64_t at = lo - b.first_at;
+        h = n > 0 ? (int)(at / n) : 0;
+        t = n > 0 ? (int)(at % n) : 0;
+        fresh = true;
+    }
+    __device__ __forceinline__ bool last() const { return t + 1 == n || left == 1; }
+    __device__ __forceinline__ void next(const P4Params& p)
+    {
+        --left;
+        fresh = false;
+        if (++t == n && left > 0) {
+            t = 0;
+            fresh = true;
+            if (++h == p.H) {
+                h = 0;
+                do {               // (a tile is left, so a sequence has one)
+                    ++s;
+                    len = p4_len(p, s);
+                } while (len == 0);
+                n = p4_tiles(len);
+            }
+        }
+    }
+};
+
+// Total tiles and the sequence in which the range starts, by one warp.
+__device__ void p4_locate(const P4Params& p, P4Bars& b, int r, int lane)
+{
+    int64_t sum = 0;
+    for (int s = lane; s < p.n_seqs; s += 32)
+        sum += p4_tiles(p4_len(p, s));
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    const int64_t T = sum * p.H;
+    if (lane == 0) {
+        b.total = T;
+        b.first_seq = 0;
+        b.first_at = 0;
+    }
+    __syncwarp();
+    if (T == 0)
+        return;
+    const int64_t lo = p4_start(r, T, min((int64_t)p.ranges, T));
+    int64_t at = 0;
+    for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
+        const int s = s0 + lane;
+        const int64_t mine = s < p.n_seqs ? (int64_t)p4_tiles(p4_len(p, s)) * p.H : 0;
+        int64_t x = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+            if (lane >= d)
+                x += y;
+        }
+        const int64_t before = at + x - mine;
+        if (mine > 0 && before <= lo && lo < before + mine) {
+            b.first_seq = s;
+            b.first_at = before;
+        }
+        at += __shfl_sync(0xFFFFFFFFu, x, 31);
+        if (at > lo)
+            break;
+    }
+}
+
+// ---------------------------------------------------------------- producer --
+template <int D, int N>
+__device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int lane, int64_t lo, int64_t hi)
+{
+    using Y = P4Layout<D, N>;
+    const int ppp = p.P / 16;      // pieces of a page
+    P4Walk w;
+    w.start(p, b, lo, hi);
+    auto page_of = [&](const P4Walk& v) {
+        const int piece = v.t * kP4Pieces + lane;
+        return lane < kP4Pieces && 16 * (int64_t)piece < v.len ? p.pages[(int64_t)v.s * p.max_pages + piece / ppp] : -1;
+    };
+    int next = page_of(w);
+    uint32_t k = 0;
+    bool ok = true;
+    for (; w.left > 0; ++k) {
+        const uint32_t at = k % Y::NS, lap = k / Y::NS;
+        const int page = next, piece = w.t * kP4Pieces + lane;
+        const bool in = lane < kP4Pieces && 16 * (int64_t)piece < w.len, good = in && page >= 0 && page < p.num_pages;
+        if (in && !good && w.h == 0)
+            raise_err(p.err, KAMERA_DEVERR_SLOT);
+        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
+        const unsigned char* src =
+            p.data + (((int64_t)page * p.H + w.h) * ppp + piece % ppp) * (int64_t)kPackedPiece<D>;
+        w.next(p);
+        if (w.left > 0)
+            next = page_of(w);
+        if (lap > 0) {
+            bool got = true;
+            if (lane == 0)
+                got = wmma16::tile_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns);
+            ok = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+            if (!ok)
+                break;
+        }
+        const uint32_t full = ptx::smem_addr(&b.full[at]);
+        if (lane == 0) {
+            b.mask[at] = mask;
+            if (!p.withhold) {
+                if (mask)
+                    ptx::mbar_arrive_expect_tx(full, __popc(mask) * (uint32_t)kPackedPiece<D>);
+                else
+                    ptx::mbar_arrive(full);
+            }
+        }
+        __syncwarp();
+        if (good && !p.withhold)
+            ptx::bulk_g2s(sbase + Y::kRing + at * Y::kTile + lane * kPackedPiece<D>, src, kPackedPiece<D>, full);
+    }
+    // The copies this warp started land before the CTA leaves (without a timeout every
+    // one has been waited for).
+    if (lane == 0 && !p.withhold && *static_cast<volatile int32_t*>(&b.abort))
+        for (uint32_t i = k > (uint32_t)Y::NS ? k - Y::NS : 0u; i < k; ++i)
+            pf_drain_wait(ptx::smem_addr(&b.full[i % Y::NS]), (i / Y::NS) & 1u, p.wait_ns);
+    __syncwarp();
+}
+
+// --------------------------------------------------------------------- MMA --
+__device__ __forceinline__ bool p4_elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+template <int D, int N>
+__device__ void p4_mma(const P4Params& p, P4Bars& b, uint32_t sbase, uint32_t tm, int64_t lo, int64_t hi)
+{
+    using Y = P4Layout<D, N>;
+    constexpr uint32_t id = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);   // fp16 x fp16 -> fp32, M 128
+    const uint32_t q_lo = ((sbase + Y::kQ) >> 4) | (1u << 16), p_lo = ((sbase + Y::kP) >> 4) | (1u << 16);
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+    };
+    P4Walk w;
+    w.start(p, b, lo, hi);
+    for (uint32_t t = 0; w.left > 0; ++t) {
+        const bool fresh = w.fresh;
+        if (!wait(&b.k_full, t))
+            break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t bq = q_lo + (ks >> 2) * (N * 128 >> 4) + 2 * (ks & 3);
+            if (ks == 0)
+                mma_ts<false>(tm + kP4TmS, tm + kP4TmK, bq, id);
+            else
+                mma_ts<true>(tm + kP4TmS, tm + kP4TmK + 8 * ks, bq, id);
+        }
+        ptx::umma_commit(ptx::smem_addr(&b.s_full));
+        if (!wait(&b.v_full, t) || !wait(&b.p_full, t))
+            break;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < kP4Tok / 16; ++ks) {
+            const uint32_t bp = p_lo + (ks >> 2) * (N * 128 >> 4) + 2 * (ks & 3);
+            if (ks == 0 && fresh)
+                mma_ts<false>(tm + kP4TmO, tm + kP4TmV, bp, id);
+            else
+                mma_ts<true>(tm + kP4TmO, tm + kP4TmV + 8 * ks, bp, id);
+        }
+        ptx::umma_commit(ptx::smem_addr(&b.pv_done));
+        w.next(p);
+    }
+    // every MMA issued here completes before TMEM is freed
+    ptx::umma_commit(ptx::smem_addr(&b.drained));
+    pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
+}
+
+// ------------------------------------------------------------------ values --
+__device__ __forceinline__ void decode_word(uint32_t codes, uint32_t scale2, uint32_t* out)
+{
+    out[0] = mul_f16x2(e2m1_pair<0>(codes), scale2);
+    out[1] = mul_f16x2(e2m1_pair<1>(codes), scale2);
+    out[2] = mul_f16x2(e2m1_pair<2>(codes), scale2);
+    out[3] = mul_f16x2(e2m1_pair<3>(codes), scale2);
+}
+
+// Thread = channel c: the tile's 128 tokens into the columns of its TMEM lane.
+template <int D, int N>
+__device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* ring, uint32_t tm, int warp, int lane,
+                          int64_t lo, int64_t hi)
+{
+    using Y = P4Layout<D, N>;
+    const int c = 32 * warp + lane;
+    const uint32_t tV = tm + ((uint32_t)warp << 21) + kP4TmV;
+    P4Walk w;
+    w.start(p, b, lo, hi);
+    bool ok = true;
+    for (uint32_t t = 0; w.left > 0; ++t, w.next(p)) {
+        const uint32_t at = t % Y::NS;
+        ok = wmma16::tile_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
+        if (!__all_sync(0xFFFFFFFFu, ok))
+            return;
+        const unsigned char* tile = ring + at * Y::kTile;
+        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[at]);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // four pieces, 32 columns
+            uint32_t v[32];
+            if (c < D) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int piece = 4 * half + i;
+                    const unsigned char* rec = tile + piece * kPackedPiece<D>;
+                    const uint2 codes = *reinterpret_cast<const uint2*>(rec + kPackedV<D> + 8 * c);
+                    // a piece that is not there: zero, so that zero weights add nothing
+                    const uint32_t s = (mask >> piece) & 1u ? rec[kPackedVS<D> + c] * 0x00800080u : 0u;
+                    decode_word(codes.x, s, v + 8 * i);
+                    decode_word(codes.y, s, v + 8 * i + 4);
+                }
+            }
+            if (half == 0 && t > 0) {   // the product before has read the last tile's values
+                ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                if (!__all_sync(0xFFFFFFFFu, ok))
+                    return;
+                ptx::tc_fence_after();
+            }
+            if (32 * warp < D)
+                tmem_st32(tV + 32 * half, v);
+        }
+        ptx::mbar_arrive(ptx::smem_addr(&b.empty[at]));
+        tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_addr(&b.v_full));
+    }
+}
+
+// -------------------------------------------------------- keys and softmax --
+__device__ __forceinline__ void p4_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The four warps meet; whether any thread said yes.
+__device__ __forceinline__ bool p4_any(bool x)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(x ? 1u : 0u)
+                 : "memory");
+    return r != 0;
+}
+
+// 16 lanes of a warp's quarter, N columns: register 4 j + 2 r + c is lane l / 4 + 8 r,
+// column 8 j + 2 (l % 4) + c.  Issue only.
+template <int N>
+__device__ __forceinline__ void p4_ld_scores(uint32_t ta, uint32_t* r)
+{
+    if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(ta)
+                     : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(ta)
+                     : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void p4_ld_out(uint32_t ta, uint32_t (&r)[N])
+{
+    if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                     "tcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(ta)
+                     : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
+                     "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                       "=r"(r[15])
+                     : "r"(ta)
+                     : "memory");
+}
+template <int N>
+__device__ __forceinline__ void p4_st_out(uint32_t ta, const uint32_t (&r)[N])
+{
+    if constexpr (N == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta), "r"(r[0]),
+                     "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    else
+        tmem_st16(ta, r);
+}
+
+__device__ __forceinline__ void p4_stsm_x4_t(uint32_t a, const uint32_t (&x)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x[0]), "r"(x[1]),
+                 "r"(x[2]), "r"(x[3])
+                 : "memory");
+}
+
+// The query heads of (sequence, KV head) as the B operand: fp16, each row times a power
+// of two that takes its largest entry to [2^10, 2^11); what a score is to be multiplied
+// with (log2 units) into fs.  Rows past the heads are zero.
+template <int D, int N>
+__device__ __forceinline__ void p4_stage_q(const P4Params& p, uint32_t sbase, float* fs, int s, int h, int warp, int lane)
+{
+    using Y = P4Layout<D, N>;
+    constexpr int V = D / 32;      // channels of a lane
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const int r = 4 * i + warp;
+        float x[V];
+        float amax = 0.f;
+        const __nv_bfloat16* src = p.q + (((int64_t)s * p.H + h) * p.G + r) * D + V * lane;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            x[j] = r < p.G ? __bfloat162float(src[j]) : 0.f;
+            amax = fmaxf(amax, fabsf(x[j]));
+        }
+#pragma unroll
+        for (int d = 16; d >= 1; d /= 2)
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+        // exponent of the largest entry; not below -100 (a row that small has few bits left), not above 127
+        const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100), ec = min(e, 127);
+        const float up = __uint_as_float((uint32_t)(127 + 10 - ec) << 23);   // 2^(10 - e), e in -100 .. 127
+        if (lane == 0)   // K is held at 2^-8 of its value
+            fs[r] = p.scale * kP4Log2e * p.k_unit * (__uint_as_float((uint32_t)(127 + ec) << 23) * 0.25f);
+        const int ch = V * lane;
+        const uint32_t dst = sbase + Y::kQ + (ch >> 6) * (N * 128) + (r >> 3) * 1024 + sw128(r & 7, (ch & 63) >> 3) +
+                             (ch & 7) * 2;
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const __half2 y = __floats2half2_rn(x[j] * up, x[j + 1] * up);
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + 2 * j), "r"(*reinterpret_cast<const uint32_t*>(&y)) : "memory");
+        }
+    }
+}
+
+template <int D, int N>
+__device__ void p4_softmax(const P4Params& p, P4Bars& b, const unsigned char* ring, uint32_t sbase, float* ex, uint32_t tm,
+                           int warp, int lane, int range, int64_t lo, int64_t hi)
+{
+    using Y = P4Layout<D, N>;
+    constexpr int J = N / 8;
+    const int gq = lane >> 2, t4 = lane & 3, tok = 32 * warp + lane;
+    const uint32_t lanes = tm + ((uint32_t)warp << 21);
+    const int64_t T = b.total, R = min((int64_t)p.ranges, T);
+    float* wmax = ex;              // [4 warps][N]
+    float* fac = ex + 4 * N;       // [N]
+    float* fs = ex + 5 * N;        // [N]: scores' factors
+    float m[J][2], l[J][2], f2[J][2];
+    const uint32_t st = sbase + Y::kP + (warp >> 1) * (N * 128) + sw128(lane & 7, 4 * (warp & 1) + (lane >> 3));
+    P4Walk w;
+    w.start(p, b, lo, hi);
+    int64_t at_tile = lo;
+    bool ok = true;
+    for (uint32_t t = 0; w.left > 0; ++t, ++at_tile) {
+        if (w.fresh) {
+            p4_stage_q<D, N>(p, sbase, fs, w.s, w.h, warp, lane);   // the products before have been waited for
+            p4_sync();
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    m[j][c] = -INFINITY;
+                    l[j][c] = 0.f;
+                    f2[j][c] = fs[8 * j + 2 * t4 + c];
+                }
+        }
+        const uint32_t at = t % Y::NS;
+        ok = ok && wmma16::tile_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[at]);
+        if (ok) {   // this token's keys (the scores before have been read: their product is done with TMEM)
+            const unsigned char* rec = ring + at * Y::kTile + (tok >> 4) * kPackedPiece<D>;
+            uint32_t sc[D / 64];
+            const unsigned char* ss = rec + kPackedKS<D> + (tok & 15) * (D / 16);
+            if constexpr (D == 128) {
+                const uint2 x = *reinterpret_cast<const uint2*>(ss);
+                sc[0] = x.x, sc[1] = x.y;
+            } else {
+                sc[0] = *reinterpret_cast<const uint32_t*>(ss);
+            }
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half) {   // 64 channels, 32 columns
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(rec + (2 * half + j) * 256 + (tok & 15) * 16);
+                    const uint32_t s0 = ((sc[half] >> (16 * j)) & 0xFFu) * 0x00800080u;
+                    const uint32_t s1 = ((sc[half] >> (16 * j + 8)) & 0xFFu) * 0x00800080u;
+                    decode_word(x.x, s0, v + 16 * j);
+                    decode_word(x.y, s0, v + 16 * j + 4);
+                    decode_word(x.z, s1, v + 16 * j + 8);
+                    decode_word(x.w, s1, v + 16 * j + 12);
+                }
+                tmem_st32(lanes + kP4TmK + 32 * half, v);
+            }
+            ptx::mbar_arrive(ptx::smem_addr(&b.empty[at]));
+            tmem_wait_st();
+            ptx::fence_proxy_async();   // the queries
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ptx::smem_addr(&b.k_full));
+            ok = wmma16::tile_wait(ptx::smem_addr(&b.s_full), t & 1u, &b.abort, p.err, p.wait_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+        const int ntok = min(kP4Tok, w.len - w.t * kP4Tok);
+        bool grew = false;
+        float x[2][J][4];   // half of the warp's tokens; [j][2 r + c]
+        if (ok) {
+            ptx::tc_fence_after();
+            uint32_t s[2][4 * J];
+            p4_ld_scores<N>(lanes + kP4TmS, s[0]);
+            p4_ld_scores<N>(lanes + kP4TmS + (16u << 16), s[1]);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 4 * J; ++j)
+                    asm volatile("" : "+r"(s[i][j]));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool here = (mask >> (2 * warp + i)) & 1u;
+                const int t0 = 32 * warp + 16 * i + gq;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const bool in = here && t0 + 8 * r < ntok;
+#pragma unroll
+                    for (int j = 0; j < J; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            x[i][j][2 * r + c] = in ? __uint_as_float(s[i][4 * j + 2 * r + c]) * f2[j][c] : -INFINITY;
+                            grew |= x[i][j][2 * r + c] > m[j][c] + kP4Lazy;
+                        }
+                }
+            }
+        }
+        if (p4_any(grew || !ok)) {   // rare but for a segment's first tile
+            if (p4_any(!ok))
+                return;              // all four warps
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = fmaxf(fmaxf(x[0][j][c], x[0][j][2 + c]), fmaxf(x[1][j][c], x[1][j][2 + c]));
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+                    if (gq == 0)
+                        wmax[warp * N + 8 * j + 2 * t4 + c] = v;
+                }
+            p4_sync();
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int h = 8 * j + 2 * t4 + c;
+                    float v = m[j][c];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v = fmaxf(v, wmax[k * N + h]);
+                    const float f = v == -INFINITY ? 1.f : pf_ex2(m[j][c] - v);
+                    l[j][c] *= f;
+                    m[j][c] = v;
+                    if (warp == 0 && gq == 0)
+                        fac[h] = f;
+                }
+            if (!w.fresh) {          // the running output, once the products before are in it
+                ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                ptx::tc_fence_after();
+                p4_sync();
+                uint32_t o[N];
+                p4_ld_out<N>(lanes + kP4TmO, o);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[i]);
+                p4_st_out<N>(lanes + kP4TmO, o);
+                tmem_wait_st();
+            }
+            p4_sync();               // the exchange's arrays are free again
+        }
+        // weights, transposed into the operand rows (heads) of the second product
+        uint32_t pk[J][4];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const float m0 = m[j][0] == -INFINITY ? 0.f : m[j][0] - kP4Up, m1 = m[j][1] == -INFINITY ? 0.f : m[j][1] - kP4Up;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float a = pf_ex2(x[k >> 1][j][2 * (k & 1)] - m0), c = pf_ex2(x[k >> 1][j][2 * (k & 1) + 1] - m1);
+                l[j][0] += a;
+                l[j][1] += c;
+                const __half2 y = __floats2half2_rn(a, c);
+                pk[j][k] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+        }
+        if (t > 0) {                 // the product before has read the last weights
+            ok = ok && wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            p4_stsm_x4_t(st + j * 1024, pk[j]);
+        ptx::fence_proxy_async();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(ptx::smem_addr(&b.p_full));
+        if (!w.last()) {
+            w.next(p);
+            continue;
+        }
+        // ---- the segment's end: its partial state
+        const int64_t a0 = at_tile - w.t, r0 = p4_range_of(a0, T, R), r1 = p4_range_of(a0 + w.n - 1, T, R);
+        const int first_slot = (int)(2 * r0 + (p4_start(r0, T, R) == a0 ? 0 : 1));
+        const int unit = w.s * p.H + w.h;
+        // a unit inside one range leaves its state at the unit's own place
+        const int64_t part = r0 == r1 ? 2 * (int64_t)p.ranges + unit : range == r0 ? first_slot : 2 * range;
+        if (range == r0 && threadIdx.x == 0)
+            p.span[unit] = make_int4((int)r0, (int)r1, first_slot, 0);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], 4);
+                l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], 8);
+                l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], 16);
+                if (gq == 0)
+                    wmax[warp * N + 8 * j + 2 * t4 + c] = l[j][c];
+            }
+        p4_sync();
+        if (warp == 0 && gq == 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int h = 8 * j + 2 * t4 + c;
+                    if (h < p.G)
+                        p.ml[part * p.G + h] = make_float2(m[j][c] - kP4Up, (wmax[h] + wmax[N + h]) +
+                                                                                (wmax[2 * N + h] + wmax[3 * N + h]));
+                }
+        }
+        ok = ok && wmma16::tile_wait(ptx::smem_addr(&b.pv_done), t & 1u, &b.abort, p.err, p.wait_ns);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        ptx::tc_fence_after();
+        uint32_t o[N];
+        p4_ld_out<N>(lanes + kP4TmO, o);
+        const float up = p.v_unit * 256.f;   // V is held at 2^-8 of its value
+        if (ok && tok < D) {
+#pragma unroll
+            for (int h = 0; h < N; ++h)
+                if (h < p.G)
+                    p.o[(part * p.G + h) * D + tok] = __uint_as_float(o[h]) * up;
+        }
+        ptx::tc_fence_before();
+        p4_sync();   // the exchange's arrays are free for the next segment
+        w.next(p);
+    }
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
+{
+    using Y = P4Layout<D, N>;
+    extern __shared__ __align__(16) unsigned char raw[];
+    const uint32_t addr = ptx::smem_addr(raw), pad = (1024u - (addr & 1023u)) & 1023u, sbase = addr + pad;
+    P4Bars& b = *reinterpret_cast<P4Bars*>(raw + pad + Y::kBar);
+    float* ex = reinterpret_cast<float*>(raw + pad + Y::kBar + 512);
+    const unsigned char* ring = raw + pad + Y::kRing;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, range = blockIdx.x;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Y::NS; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&b.full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.empty[i]), 256);
+        }
+        ptx::mbar_init(ptx::smem_addr(&b.k_full), 128);
+        ptx::mbar_init(ptx::smem_addr(&b.v_full), 128);
+        ptx::mbar_init(ptx::smem_addr(&b.s_full), 1);
+        ptx::mbar_init(ptx::smem_addr(&b.p_full), 4);
+        ptx::mbar_init(ptx::smem_addr(&b.pv_done), 1);
+        ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
+        b.abort = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == kP4Mma) {
+        ptx::tmem_alloc(ptx::smem_addr(&b.tmem), kP4TmCols);
+        ptx::tmem_relinquish();
+    }
+    if (p.first)   // behind the tail's kernel the call's inputs are there already
+        ptx::grid_wait();
+    if (warp == 0)
+        p4_locate(p, b, range, lane);
+    if (blockIdx.x == 0 && warp > 0)
+        for (int s = threadIdx.x - 32; s < p.n_seqs; s += kP4Threads - 32)
+            if (p.lens[s] < 0 || p.lens[s] > p.max_len)
+                raise_err(p.err, KAMERA_DEVERR_LEN);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::grid_launch_next();   // (this CTA has its TMEM: none that starts early can take it)
+    const uint32_t tm = b.tmem;
+    const int64_t T = b.total, R = min((int64_t)p.ranges, T);
+    if (range < R) {   // (else: fewer tiles than ranges)
+        const int64_t lo = p4_start(range, T, R), hi = p4_start(range + 1, T, R);
+        if (warp < 4)
+            p4_softmax<D, N>(p, b, ring, sbase, ex, tm, warp, lane, range, lo, hi);
+        else if (warp < 8)
+            p4_values<D, N>(p, b, ring, tm, warp - 4, lane, lo, hi);
+        else if (warp == kP4Prod)
+            p4_producer<D, N>(p, b, sbase, lane, lo, hi);
+        else if (p4_elect())
+            p4_mma<D, N>(p, b, sbase, tm, lo, hi);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kP4Mma) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tm, kP4TmCols);
+    }
+    // The merge that follows waits for this grid alone, which ends after the tail's.
+    if (!p.first && blockIdx.x == gridDim.x - 1)
+        ptx::grid_wait();
+}
+
+// ------------------------------------------------------------------- merge --
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a row's packed and tail
+// states.  A warp a row; the lanes work out the weights of 32 states at a time.
+constexpr int kP4MergeWarps = 4;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const P4Params p)
+{
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kP4MergeWarps + (threadIdx.x >> 5), rows = (int64_t)p.n_seqs * p.H * p.G;
+    const int unit = (int)(min(row, rows - 1) / p.G), g = (int)(min(row, rows - 1) - (int64_t)unit * p.G), s = unit / p.H;
+    int n_tail = 0;
+    if (p.tail_slots > 0) {
+        const int len = p.tail_lens[s];
+        n_tail = len > 0 && len <= p.max_tail ? ((len + 15) / 16 + p.tail_split - 1) / p.tail_split : 0;
+    }
+    const bool some = p.max_len > 0 && p4_len(p, s) > 0;
+    ptx::grid_wait();
+    ptx::grid_launch_next();
+    if (row >= rows)
+        return;
+    int n_packed = 0;
+    int4 sp = make_int4(0, 0, 0, 0);
+    if (some) {
+        sp = p.span[unit];
+        // (after a timeout it may never have been written)
+        if (sp.x >= 0 && sp.y >= sp.x && sp.y < p.ranges && (sp.z >> 1) == sp.x)
+            n_packed = sp.y - sp.x + 1;
+    }
+    auto packed_at = [&](int i) {
+        const int64_t slot = sp.x == sp.y ? 2 * (int64_t)p.ranges + unit : i == 0 ? sp.z : 2 * (sp.x + i);
+        return slot * p.G + g;
+    };
+    const int n = n_packed + n_tail;
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32)
+        m = fmaxf(m, i < n_packed ? p.ml[packed_at(i)].x : p.tail_ml[row * p.tail_slots + i - n_packed].x);
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    float l = 0.f, acc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        acc[v] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        float f = 0.f;
+        const float* src = p.o;
+        if (i < n) {
+            const bool pk = i < n_packed;
+            const int64_t at = pk ? packed_at(i) : row * p.tail_slots + i - n_packed;
+            const float2 y = pk ? p.ml[at] : p.tail_ml[at];
+            src = (pk ? p.o : p.tail_o) + at * D;
+            if (y.y != 0.f) {   // a state without weight adds nothing (and has no maximum to scale by)
+                f = pf_ex2(y.x - m);
+                l = fmaf(y.y, f, l);
+            }
+        }
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, f != 0.f || f != f);
+#pragma unroll 4
+        for (int k = 0; k < min(32, n - i0); ++k) {
+            const float x = __shfl_sync(0xFFFFFFFFu, f, k);
+            const float* o = reinterpret_cast<const float*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(src), k)) + V * lane;
+            if (!((live >> k) & 1u))
+                continue;
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(o);
+                acc[0] = fmaf(y.x, x, acc[0]), acc[1] = fmaf(y.y, x, acc[1]);
+                acc[2] = fmaf(y.z, x, acc[2]), acc[3] = fmaf(y.w, x, acc[3]);
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(o);
+                acc[0] = fmaf(y.x, x, acc[0]), acc[1] = fmaf(y.y, x, acc[1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2)
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(p.out + row * D + 4 * lane) =
+            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t*>(p.out + row * D + 2 * lane) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0 && p.lse)
+        p.lse[row] = l > 0.f ? (m + log2f(l)) * kP4Ln2 : (l == l ? -INFINITY : l);
+}
+
+// -------------------------------------------------------------------- host --
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct P4Plan {
+    P4Params p;
+    PagedParams tail;
+    bool has_tail;
+    size_t o, ml, span, tail_o, tail_ml;
+    size_t bytes() const { return o + ml + span + tail_o + tail_ml; }
+};
+
+int p4_plan(const KameraPackedPool* pk, const KameraPagedQuery* q, const KameraPageTable* t, const KameraPagedKV* kv,
+            const KameraPageTable* tail, P4Plan* x)
+{
+    const int rc = check_packed(pk);
+    if (rc == KAMERA_ERR_INVALID_ARGUMENT)
+        return rc;
+    if (!q || !t || q->reserved != 0 || q->n_seqs < 0 || q->num_q_heads < 1 || q->num_q_heads % pk->num_kv_heads ||
+        !(q->scale == q->scale) || t->max_len < 0 || t->max_pages < 0 || (kv == nullptr) != (tail == nullptr))
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    if (kv && (kv->num_kv_heads != pk->num_kv_heads || kv->head_dim != pk->head_dim))
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    const int G = q->num_q_heads / pk->num_kv_heads;
+    if (rc || G > 16 || (int64_t)q->n_seqs * pk->num_kv_heads > 65535 ||
+        (int64_t)q->n_seqs * q->num_q_heads > 0x3FFFFFF || t->max_len > 0x7FFFFF00)
+        return KAMERA_ERR_UNSUPPORTED;
+    if ((int64_t)t->max_pages * pk->page_size < t->max_len)
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    std::memset(x, 0, sizeof(*x));
+    P4Params& p = x->p;
+    p.n_seqs = q->n_seqs;
+    p.H = pk->num_kv_heads;
+    p.G = G;
+    p.P = pk->page_size;
+    p.num_pages = pk->num_pages;
+    p.max_pages = t->max_pages;
+    p.max_len = t->max_len;
+    p.scale = q->scale;
+    p.k_unit = pk->k_unit;
+    p.v_unit = pk->v_unit;
+    if (kv) {
+        const int e = plan_own_pages(kv, q, tail, &x->tail);
+        if (e)
+            return e;
+        x->has_tail = q->n_seqs > 0 && x->tail.own_slots > 0;
+    }
+    if (q->n_seqs == 0)
+        return KAMERA_OK;
+    const int64_t units = (int64_t)p.n_seqs * p.H, rows = units * G;
+    const int64_t most = units * (((int64_t)p.max_len + kP4Tok - 1) / kP4Tok);
+    p.ranges = (int32_t)std::min<int64_t>(2ll * device_sms(), most);
+    if (p.ranges > 0) {
+        const size_t slots = (size_t)(2 * p.ranges + units) * G;
+        x->o = up256(slots * pk->head_dim * 4);
+        x->ml = up256(slots * 8);
+        x->span = up256((size_t)units * 16);
+    }
+    if (x->has_tail) {
+        p.tail_split = x->tail.own_split;
+        p.tail_slots = x->tail.own_slots;
+        p.max_tail = tail->max_len;
+        x->tail_o = up256((size_t)rows * p.tail_slots * pk->head_dim * 4);
+        x->tail_ml = up256((size_t)rows * p.tail_slots * 8);
+    }
+    return KAMERA_OK;
+}
+
+template <int D, int N>
+cudaError_t p4_launch(const P4Params& p, cudaStream_t stream)
+{
+    using Y = P4Layout<D, N>;
+    // set at every launch: the attribute belongs to the current device's context
+    const cudaError_t e = cudaFuncSetAttribute(packed_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::kBytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_after(packed_kernel<D, N>, dim3((unsigned)p.ranges), kP4Threads, Y::kBytes, stream, true, p);
+}
+
+}  // namespace
+
+}  // namespace kamera
+
+using namespace kamera;
+
+extern "C" {
+
+size_t kamera_attend_packed_workspace_bytes(const KameraPackedPool* packed, const KameraPagedQuery* query,
+                                            const KameraPageTable* table, const KameraPagedKV* tail_kv,
+                                            const KameraPageTable* tail)
+{
+    P4Plan x;
+    return p4_plan(packed, query, table, tail_kv, tail, &x) == KAMERA_OK && x.p.n_seqs > 0 ? x.bytes() : 0;
+}
+
+int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery* query, const KameraPageTable* table,
+                         const KameraPagedKV* tail_kv, const KameraPageTable* tail, void* d_workspace,
+                         size_t workspace_bytes, int32_t* d_err, struct CUstream_st* stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    P4Plan x;
+    const int rc = p4_plan(packed, query, table, tail_kv, tail, &x);
+    if (rc || x.p.n_seqs == 0)
+        return rc;
+    P4Params& p = x.p;
+    const int d = packed->head_dim;
+    const int64_t rows = (int64_t)p.n_seqs * p.H * p.G, W = (int64_t)p.H * d;
+    if (!query->q || !query->out || (p.ranges > 0 && (!packed->data || !table->pages || !table->lens)) ||
+        (x.has_tail && (!tail->pages || !tail->lens)) || (x.bytes() > 0 && !d_workspace))
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    int e;
+    if (x.has_tail && ((e = check_strided(tail_kv->k, 1, 0, tail_kv->num_slots, tail_kv->slot_stride, W, false)) ||
+                       (e = check_strided(tail_kv->v, 1, 0, tail_kv->num_slots, tail_kv->slot_stride, W, false))))
+        return e;
+    const uintptr_t ints = (p.ranges > 0 ? reinterpret_cast<uintptr_t>(table->pages) | reinterpret_cast<uintptr_t>(table->lens) : 0) |
+                           (x.has_tail ? reinterpret_cast<uintptr_t>(tail->pages) | reinterpret_cast<uintptr_t>(tail->lens) : 0);
+    if (!aligned16(query->q) || !aligned16(query->out) || !aligned16(packed->data) || !aligned16(d_workspace) ||
+        ((reinterpret_cast<uintptr_t>(query->lse) | ints) & 3))
+        return KAMERA_ERR_MISALIGNED;
+    if (workspace_bytes < x.bytes())
+        return KAMERA_ERR_INVALID_ARGUMENT;
+    using Span = std::pair<uintptr_t, uintptr_t>;
+    auto bytes = [](const void* a, int64_t n) -> Span {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(a);
+        return {lo, a && n > 0 ? lo + (uintptr_t)n : lo};
+    };
+    const Span in[] = {bytes(query->q, rows * d * 2),
+                       bytes(packed->data, p.ranges > 0 ? packed_bytes(packed) : 0),
+                       bytes(table->pages, p.ranges > 0 ? (int64_t)p.n_seqs * p.max_pages * 4 : 0),
+                       bytes(table->lens, p.ranges > 0 ? (int64_t)p.n_seqs * 4 : 0),
+                       x.has_tail ? span(tail_kv->k, 1, 0, tail_kv->num_slots, tail_kv->slot_stride, W) : Span{0, 0},
+                       x.has_tail ? span(tail_kv->v, 1, 0, tail_kv->num_slots, tail_kv->slot_stride, W) : Span{0, 0},
+                       x.has_tail ? bytes(tail->pages, (int64_t)p.n_seqs * tail->max_pages * 4) : Span{0, 0},
+                       x.has_tail ? bytes(tail->lens, (int64_t)p.n_seqs * 4) : Span{0, 0}};
+    const Span outs[] = {bytes(query->out, rows * d * 2), bytes(query->lse, rows * 4),
+                         bytes(d_workspace, (int64_t)x.bytes())};
+    for (int i = 0; i < 3; ++i) {
+        for (const Span& a : in)
+            if (overlap(a, outs[i]))
+                return KAMERA_ERR_INVALID_ARGUMENT;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j]))
+                return KAMERA_ERR_INVALID_ARGUMENT;
+    }
+    p.q = static_cast<const __nv_bfloat16*>(query->q);
+    p.out = static_cast<__nv_bfloat16*>(query->out);
+    p.lse = query->lse;
+    p.data = static_cast<const unsigned char*>(packed->data);
+    p.pages = table->pages;
+    p.lens = table->lens;
+    if (p.ranges == 0)
+        p.max_len = 0;   // nothing to read: no length is looked at
+    unsigned char* ws = static_cast<unsigned char*>(d_workspace);
+    p.o = reinterpret_cast<float*>(ws);
+    p.ml = reinterpret_cast<float2*>(ws + x.o);
+    p.span = reinterpret_cast<int4*>(ws + x.o + x.ml);
+    p.err = d_err;
+    p.wait_ns = wait_limit_ns();
+    p.withhold = test_withhold_loads() ? 1 : 0;
+    p.first = x.has_tail ? 0 : 1;
+    // The tail's kernel first: short, and the packed one's CTAs start beside it.
+    if (x.has_tail) {
+        PagedParams& t = x.tail;
+        t.q = p.q;
+        t.out = p.out;
+        t.pages = tail->pages;
+        t.lens = tail->lens;
+        t.o = reinterpret_cast<float*>(ws + x.o + x.ml + x.span);
+        t.ml = reinterpret_cast<float2*>(ws + x.o + x.ml + x.span + x.tail_o);
+        t.err = d_err;
+        t.wait_ns = p.wait_ns;
+        t.withhold = p.withhold;
+        p.tail_o = t.o;
+        p.tail_ml = t.ml;
+        p.tail_lens = tail->lens;
+        if (launch_own_pages(t, tail_kv, stream) != cudaSuccess)
+            return KAMERA_ERR_CUDA;
+    }
+    cudaError_t ce = cudaSuccess;
+    if (p.ranges > 0) {
+        const bool few = p.G <= 8;
+        if (d == 128)
+            ce = few ? p4_launch<128, 8>(p, stream) : p4_launch<128, 16>(p, stream);
+        else
+            ce = few ? p4_launch<64, 8>(p, stream) : p4_launch<64, 16>(p, stream);
+        if (ce != cudaSuccess)
+            return KAMERA_ERR_CUDA;
+    }
+    const dim3 grid((unsigned)((rows + kP4MergeWarps - 1) / kP4MergeWarps));
+    ce = d == 128 ? launch_after(packed_merge_kernel<128>, grid, 32 * kP4MergeWarps, 0, stream, true, p)
+                  : launch_after(packed_merge_kernel<64>, grid, 32 * kP4MergeWarps, 0, stream, true, p);
+    return ce == cudaSuccess ? KAMERA_OK : KAMERA_ERR_CUDA;
+}
+
+}  // extern "C"

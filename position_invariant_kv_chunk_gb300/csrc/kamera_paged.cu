@@ -905,6 +905,25 @@ int attend(PagedParams& p, const KameraPagedKV* kv, const KameraPagedQuery* q, c
 
 }  // namespace
 
+int plan_own_pages(const KameraPagedKV* kv, const KameraPagedQuery* q, const KameraPageTable* own, PagedParams* p)
+{
+    return plan(kv, q, nullptr, own, false, 0, p);
+}
+
+cudaError_t launch_own_pages(const PagedParams& p, const KameraPagedKV* kv, cudaStream_t stream)
+{
+    const int64_t W = (int64_t)p.H * p.d, map_rows = kv->num_slots > 0 ? kv->num_slots : 1;
+    PagedLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    L.p = p;
+    if (!make_rows_map(&L.map_k, kv->k, map_rows, W, kv->slot_stride, 64, kPgTok) ||
+        !make_rows_map(&L.map_v, kv->v, map_rows, W, kv->slot_stride, 64, kPgTok))
+        return cudaErrorInvalidValue;
+    if (p.d == 128)
+        return p.G <= 8 ? launch_own<128, 1>(L, stream) : launch_own<128, 2>(L, stream);
+    return p.G <= 8 ? launch_own<64, 1>(L, stream) : launch_own<64, 2>(L, stream);
+}
+
 }  // namespace kamera
 
 using namespace kamera;

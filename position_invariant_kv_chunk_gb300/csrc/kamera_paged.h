@@ -96,4 +96,11 @@ __device__ __forceinline__ uint32_t weight_hi(float a, float b)
 
 cudaError_t launch_prefix(const PagedLaunch& L, cudaStream_t stream);
 
+// The own tokens' part alone, for a caller that joins their partial states with others:
+// the argument checks and the plan (a KAMERA_* status; 0 splits: nothing to read), and
+// the launch, with p's pointers filled in and its states in p.o, p.ml (row r's split i
+// at r * own_slots + i, written where it has tokens).
+int plan_own_pages(const KameraPagedKV* kv, const KameraPagedQuery* q, const KameraPageTable* own, PagedParams* p);
+cudaError_t launch_own_pages(const PagedParams& p, const KameraPagedKV* kv, cudaStream_t stream);
+
 }  // namespace kamera

@@ -1049,6 +1049,21 @@ bool make_rows_map(void* map, const void* base, int64_t rows, int64_t width, int
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_heads_map(void* map, const void* base, int64_t rows, int heads, int width, int64_t row_stride,
+                    int64_t head_stride, int box_cols, int box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn || rows < 1 || heads < 1 || width < 1)
+        return false;
+    cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2u, (cuuint64_t)row_stride * 2u};
+    cuuint32_t box[3] = {(cuuint32_t)box_cols, 1u, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 4-D tensor map of the same array as groups of eight rows: (64 columns, row in
 // its group, column block, group), 128-byte swizzle, boxes of `blocks` column
 // blocks of `groups` groups.  A box lands as [group][block][8 rows][128 bytes],
