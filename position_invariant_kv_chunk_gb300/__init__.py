@@ -165,6 +165,29 @@ class _PageSelect(C.Structure):
                 ("n_last", C.c_int32)]
 
 
+class _PagedMlaKV(C.Structure):
+    _fields_ = [("kv", C.c_void_p), ("num_slots", C.c_int64), ("slot_stride", C.c_int64), ("kv_lora_rank", C.c_int32),
+                ("rope_dim", C.c_int32), ("page_size", C.c_int32), ("reserved", C.c_int32)]
+
+
+class _MlaExpand(C.Structure):
+    _fields_ = [("weight", C.c_void_p), ("slots", C.c_void_p), ("kv_out", C.c_void_p), ("k_rope_out", C.c_void_p),
+                ("n_tokens", C.c_int32), ("num_heads", C.c_int32), ("head_width", C.c_int32), ("reserved", C.c_int32)]
+
+
+class _MlaPrefill(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("kv", C.c_void_p), ("k_rope", C.c_void_p), ("out", C.c_void_p), ("lse", C.c_void_p),
+                ("q_start", C.c_void_p), ("kv_start", C.c_void_p), ("q_stride", C.c_int64), ("q_head_stride", C.c_int64),
+                ("kv_stride", C.c_int64), ("k_rope_stride", C.c_int64), ("n_q", C.c_int32), ("n_kv", C.c_int32),
+                ("n_seqs", C.c_int32), ("num_heads", C.c_int32), ("nope_dim", C.c_int32), ("rope_dim", C.c_int32),
+                ("v_dim", C.c_int32), ("max_q", C.c_int32), ("causal", C.c_int32), ("scale", C.c_float)]
+
+
+class _PackedPool(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("num_pages", C.c_int64), ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page_size", C.c_int32), ("reserved", C.c_int32), ("k_unit", C.c_float), ("v_unit", C.c_float)]
+
+
 assert C.sizeof(_Chunk) == 64
 
 _LIB: Optional[C.CDLL] = None
@@ -239,6 +262,25 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = True) -> C
                                            C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]
     lib.kamera_attend_selected_workspace_bytes.restype = C.c_size_t
     lib.kamera_attend_selected_workspace_bytes.argtypes = [P(_PagedKV), P(_PagedQuery), P(_PageTable), C.c_int32]
+    lib.kamera_mla_attend_paged.restype = C.c_int
+    lib.kamera_mla_attend_paged.argtypes = [P(_PagedMlaKV), P(_PagedQuery), P(_PageTable), C.c_void_p, C.c_size_t,
+                                            C.c_void_p, C.c_void_p]
+    lib.kamera_mla_attend_paged_workspace_bytes.restype = C.c_size_t
+    lib.kamera_mla_attend_paged_workspace_bytes.argtypes = [P(_PagedMlaKV), P(_PagedQuery), P(_PageTable)]
+    lib.kamera_mla_expand.restype = C.c_int
+    lib.kamera_mla_expand.argtypes = [P(_PagedMlaKV), P(_MlaExpand), C.c_void_p, C.c_void_p]
+    lib.kamera_mla_prefill_attend.restype = C.c_int
+    lib.kamera_mla_prefill_attend.argtypes = [P(_MlaPrefill), C.c_void_p, C.c_void_p]
+    for f in (lib.kamera_pack_pages, lib.kamera_unpack_pages):
+        f.restype = C.c_int
+        f.argtypes = [P(_GqaPool), C.c_int32, P(_PackedPool), C.c_void_p, C.c_void_p, C.c_void_p, C.c_int32, C.c_void_p,
+                      C.c_void_p]
+    lib.kamera_attend_packed.restype = C.c_int
+    lib.kamera_attend_packed.argtypes = [P(_PackedPool), P(_PagedQuery), P(_PageTable), P(_PagedKV), P(_PageTable),
+                                         C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]
+    lib.kamera_attend_packed_workspace_bytes.restype = C.c_size_t
+    lib.kamera_attend_packed_workspace_bytes.argtypes = [P(_PackedPool), P(_PagedQuery), P(_PageTable), P(_PagedKV),
+                                                         P(_PageTable)]
     lib.kamera_validate_chunks.restype = C.c_int
     lib.kamera_validate_chunks.argtypes = [P(_Chunk), C.c_int32, C.c_int64, C.c_int64, C.c_int32,
                                            C.c_int32, P(C.c_int32), P(C.c_int32)]
@@ -1088,3 +1130,36 @@ def kamera_select_pages_workspace_bytes(q: torch.Tensor, summary: torch.Tensor, 
     x = _PageSelect(None, None, None, summary.shape[0], q.shape[0], q.shape[1], summary.shape[1], q.shape[2], P,
                     _int32(n_select, "n_select"), _int32(n_first, "n_first"), _int32(n_last, "n_last"))
     return _bytes_on(q, load_library().kamera_select_pages_workspace_bytes, x, _page_bounds(P, max_len))
+
+
+def kamera_mla_attend_paged_workspace_bytes(pool: torch.Tensor, kv_lora: int, q: torch.Tensor, page_size: int,
+                                            max_len: int) -> int:
+    """As ``kamera_attend_shared_workspace_bytes`` for ``kamera_mla_attend_paged``."""
+    if pool.dim() != 2 or q.dim() != 3 or q.shape[2] != pool.shape[1]:
+        raise ValueError("pool must be [S_slots, kv_lora + rope_dim] and q [S, H_q, kv_lora + rope_dim]")
+    P = _int32(page_size, "page_size")
+    if P < 1:
+        raise ValueError("page_size must be positive")
+    lora = _int32(kv_lora, "kv_lora")
+    kv = _PagedMlaKV(None, pool.shape[0], pool.stride(0), lora, pool.shape[1] - lora, P, 0)
+    query = _PagedQuery(None, None, None, q.shape[0], q.shape[1], 1.0, 0)
+    return _bytes_on(q, load_library().kamera_mla_attend_paged_workspace_bytes, kv, query, _page_bounds(P, max_len))
+
+
+def kamera_attend_packed_workspace_bytes(packed: torch.Tensor, q: torch.Tensor, page_size: int, max_len: int,
+                                         max_tail: int = 0, tail_page_size: Optional[int] = None) -> int:
+    """As ``kamera_attend_shared_workspace_bytes`` for ``kamera_attend_packed`` (max_tail 0:
+    no tail)."""
+    if packed.dim() != 3 or q.dim() != 3:
+        raise ValueError("packed must be [n_pages, H, page_size * (d + d // 8)] and q [S, H_q, d]")
+    P = _int32(page_size, "page_size")
+    T = P if tail_page_size is None else _int32(tail_page_size, "tail_page_size")
+    if P < 1 or T < 1:
+        raise ValueError("page_size must be positive")
+    H, d = packed.shape[1], q.shape[2]
+    pool = _PackedPool(None, packed.shape[0], H, d, P, 0, 1.0, 1.0)
+    query = _PagedQuery(None, None, None, q.shape[0], q.shape[1], 1.0, 0)
+    tail = _page_bounds(T, max_tail)
+    kv = _PagedKV(None, None, 0, H * d, H, d, T, 0)
+    return _bytes_on(q, load_library().kamera_attend_packed_workspace_bytes, pool, query, _page_bounds(P, max_len), kv,
+                     tail)
