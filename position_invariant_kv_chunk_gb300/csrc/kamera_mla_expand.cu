@@ -106,7 +106,7 @@ __device__ void ex_producer(const ExLaunch& L, ExBars& b, uint32_t sbase)
     for (ExWalk w(p); w.more() && ok; w.next())
         for (int c = 0; c < kExChunks; ++c, ++k) {
             const uint32_t at = k % kExStages, lap = k / kExStages, full = ptx::smem_addr(&b.full[at]);
-            if (lap > 0 && !wmma16::tile_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns)) {
+            if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns)) {
                 ok = false;
                 break;
             }
@@ -126,7 +126,7 @@ __device__ void ex_mma(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm
     constexpr uint32_t id = ptx::idesc_bf16_f32(kExTok, kExN);
     const uint32_t a_lo = (sbase >> 4) | (1u << 16), r_lo = ((sbase + kExRing) >> 4) | (1u << 16);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
     uint32_t k = 0, n = 0, tiles = 0;
     bool ok = true, fresh = true;
@@ -173,7 +173,7 @@ __device__ void ex_gather(const ExLaunch& L, ExBars& b, uint32_t sbase, int warp
     for (ExWalk w(p); w.more(); w.next()) {
         if (fresh) {
             if (tiles > 0)
-                ok = wmma16::tile_wait(ptx::smem_addr(&b.a_empty), (tiles - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.a_empty), (tiles - 1) & 1u, &b.abort, p.err, p.wait_ns);
             if (!__all_sync(0xFFFFFFFFu, ok))
                 return;
             const int t0 = w.tile * kExTok + 32 * warp;
@@ -227,7 +227,7 @@ __device__ void ex_epilogue(const ExLaunch& L, ExBars& b, uint32_t tm, int warp,
     const uint32_t lanes = tm + ((uint32_t)warp << 21);
     uint32_t n = 0;
     for (ExWalk w(p); w.more(); w.next(), ++n) {
-        const bool ok = wmma16::tile_wait(ptx::smem_addr(&b.acc_full[n & 1u]), (n >> 1) & 1u, &b.abort, p.err, p.wait_ns);
+        const bool ok = wmma16::cycle_wait(ptx::smem_addr(&b.acc_full[n & 1u]), (n >> 1) & 1u, &b.abort, p.err, p.wait_ns);
         if (!__all_sync(0xFFFFFFFFu, ok))
             return;
         ptx::tc_fence_after();

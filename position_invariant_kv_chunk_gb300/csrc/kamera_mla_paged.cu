@@ -4,32 +4,33 @@
 // All query heads share one latent row a token, so a step reads 1152 bytes a token for
 // 2 H (576 + 512) flops: 30 flops a byte with 16 heads, 242 with 128.  Warp-level MMAs
 // (about 256 multiplies a cycle and SM) cannot do the first at the speed of HBM; the
-// 5th-generation ones can if the heads are their N:
-//   S^T [64 tokens x N]   = rows [64 x 576] q^T        (A: rows as they lie, K-major)
-//   O^T [512 dims x N]   += c^T [512 x 64] P^T         (A: the same rows, MN-major)
-// Heads as the M of an MMA would leave 112 of 128 rows empty with 16 heads and would
-// take all of TMEM for O (128 x 512 floats); as N they cost what they need, and O^T takes
-// 4 N columns.  Both products read the one copy of the rows in shared memory: a tile
-// of 64 tokens is four units of 128 columns, [8 groups of 8 rows][2 blocks of 64
-// columns][8][128 bytes] as a TMA box lands them, and a K-major operand of the first
-// product is an MN-major one of the second with other strides.
-//   N = 16, 32 (up to as many heads)   weights as bf16 hi + lo pairs, the lo parts N
-//                more columns of the same MMAs, which are bound by A's 4 KB an
-//                instruction: free
+// 5th-generation ones can if few heads do not cost what 128 would:
+//   S^T [64 tokens x N]    = rows [64 x 576] q^T      (A: the rows as they lie, K-major; the heads are N)
+//   O [64 x 512 columns]  += P [64 x 64 tokens] c     (B: the same rows, MN-major; the heads are M)
+// The queries stay N x 1152 bytes of shared memory (as the M of an MMA 64 rows of them
+// would take 72 KB), and both products read the one copy of the rows: a tile of 64
+// tokens is four units of 128 columns, [8 groups of 8 rows][2 blocks of 64
+// columns][8][128 bytes] as a TMA box lands them.  A tile's MMAs take 36 x 26 (N = 16)
+// or 34 (N = 64) and 16 x 66 cycles.  An M = 64 accumulator sits in 16 lanes of each warp's quarter of TMEM: columns 0-255 of O in
+// the lower 16, 256-511 in the upper 16.
+//   N = 16, 32 (up to as many heads)   weights as bf16 hi + lo pairs, the lo parts eight
+//                more rows behind eight heads: free, as M is 64 anyway
 //   N = 64       weights rounded to bf16; 65 to 128 heads are two CTAs that walk the
 //                same rows at the same time, so that the second reads them from L2
 // Work: one CTA an SM; the batch's tiles, all sequences behind one another, are cut into
 // as many equal ranges as there are SMs, whatever the lengths.  A sequence that lies in
 // one range is finished there; the pieces of one that is cut leave partial states, two a
 // range at most (its first sequence and its last), and a second launch joins them.
-//   warps 0-3  softmax: warp w has tokens 16 w .. 16 w + 15 of a tile (an M = 64
-//              accumulator sits in 16 lanes of each warp's quarter of TMEM), so a score
-//              fragment is that of a warp-level MMA; the maxima of the four warps meet
-//              only when one grew by more than 2^8 (a reduced barrier says so)
-//   warp 4     producer: TMA boxes of as many rows as lie together in a page
-//   warp 5     MMA
-// The scores of tile t + 1 are issued before the weights of tile t are waited for, so
-// the tensor pipe works through the softmax.  Every wait is bounded in time.
+//   four warps  softmax (N = 64: eight, four for each half of the heads): warp w has
+//              tokens 16 w .. 16 w + 15 of a tile (an M = 64 accumulator sits in 16
+//              lanes of each warp's quarter of TMEM), so a score fragment is that of a
+//              warp-level MMA; the maxima of the four warps meet only when one grew by
+//              more than 2^8 (a reduced barrier says so)
+//   one warp   producer: TMA boxes of as many rows as lie together in a page
+//   two warps  MMA, the scores' and the products': what a lane issues next waits behind
+//              its MMAs, barriers too, and with one lane for both (300 cycles for every
+//              barrier between MMAs) neither kept the tensor pipe busy
+// Every wait is bounded in time.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -51,8 +52,6 @@ using namespace tc;
 constexpr int kMpTok = 64;              // tokens of a tile
 constexpr int kMpUnits = 4;             // units of 128 value columns
 constexpr int kMpDim = 512, kMpRow = 576;
-constexpr int kMpThreads = 192;
-constexpr int kMpProd = 4, kMpMma = 5;
 constexpr uint32_t kMpUnit = 16384;     // 64 rows x 128 columns
 constexpr uint32_t kMpRope = 8192;      // 64 rows x 64 columns
 constexpr uint32_t kMpAtom = 1024;
@@ -63,24 +62,27 @@ constexpr float kMpLog2e = 1.4426950408889634f, kMpLn2 = 0.6931471805599453f;
 template <int N>
 struct MpLayout {
     static constexpr bool kPair = N <= 32;           // weights as hi + lo
-    static constexpr int NW = kPair ? 2 * N : N;     // columns of the second product
+    static constexpr int NW = kPair ? 2 * N : N;     // rows of the second product: heads, or eight hi, eight lo, ...
+    static constexpr int HG = kPair ? N : 32;        // heads of a softmax warpgroup
+    static constexpr int kProd = 4 * (N / HG), kScores = kProd + 1, kProducts = kProd + 2;   // warps
+    static constexpr int kThreads = 32 * (kProducts + 1);
     static constexpr int NU = N == 16 ? 11 : N == 32 ? 9 : 8;   // units in the ring: two tiles at least, the one whose
                                                                 // scores are issued and the one still to be weighed
     static constexpr int NR = N == 32 ? 3 : 2;                  // rope blocks in theirs
     static constexpr int NP = N == 64 ? 1 : 2;                  // buffers of weights
     static constexpr uint32_t kQ = 0;                           // [9 blocks][N rows][128 bytes]
     static constexpr uint32_t kQBlock = N * 128;
-    static constexpr uint32_t kP = kQ + 9 * kQBlock;            // [2][NW rows][128 bytes]
+    static constexpr uint32_t kP = kQ + 9 * kQBlock;            // [NP][NW rows][128 bytes]
     static constexpr uint32_t kPTile = NW * 128;
     static constexpr uint32_t kRing = kP + NP * kPTile;
     static constexpr uint32_t kRopes = kRing + NU * kMpUnit;
     static constexpr uint32_t kBar = kRopes + NR * kMpRope;
     static constexpr uint32_t kBytes = kBar + 512 + 5 * N * 4 + 1024;   // + alignment slack
     static constexpr uint32_t kTmS = 0, kTmO = 2 * N;           // TMEM columns
-    static constexpr uint32_t kTmCols = kTmO + 4 * NW <= 256 ? 256 : 512;
-    static_assert(kTmO + 4 * NW <= kTmCols, "TMEM columns");
+    static constexpr uint32_t kTmCols = 512;
+    static_assert(kTmO + kMpDim / 2 <= kTmCols, "TMEM columns");
     static_assert(kBytes <= 227 * 1024, "shared memory");
-    static_assert(NU >= 2 * kMpUnits && NR >= 2, "the scores of a tile are issued before the one before is weighed");
+    static_assert(NU >= 2 * kMpUnits && NR >= 2, "a tile's scores while the one before is weighed");
     static_assert(kP % 1024 == 0 && kRing % 1024 == 0, "swizzle atoms");
 };
 
@@ -111,7 +113,7 @@ struct MpLaunch {
 struct MpBars {
     uint64_t full[11], empty[11], rfull[3], rempty[3];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], pv_done, drained;
+    uint64_t s_full[2], p_full[2], pv_done[2], drained[2];
     uint32_t mask[kMpMasks];
     int64_t total;
     int64_t first_at;          // global tile at which the range's first sequence starts
@@ -218,7 +220,7 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         bool got = true;
         if (lane == 0)
-            got = wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+            got = wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
         return __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
     };
     const int R = p.box_rows, boxes = kMpTok / R;
@@ -300,88 +302,147 @@ __device__ __forceinline__ bool mp_elect()
     return r != 0;
 }
 
+// MMAs whose A (mma_ds) or B (mma_sd) is a unit, groups of eight rows 2 KB apart; the
+// other operand has them 1 KB apart.  The accumulate flag and the descriptors' high
+// words are constants: with them in registers an issue took 58 cycles, where the tensor
+// pipe needs 26 to 66.
+constexpr uint32_t kMpHiU = (2 * kMpAtom >> 4) | (1u << 14) | (2u << 29);
+
+template <bool ACC, uint32_t HA, uint32_t HB>
+__device__ __forceinline__ void mp_issue(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
+{
+    if constexpr (ACC)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 1, 1;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(pf_desc<HA>(a_lo)), "l"(pf_desc<HB>(b_lo)), "r"(idesc)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 1, 1;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(pf_desc<HA>(a_lo)), "l"(pf_desc<HB>(b_lo)), "r"(idesc)
+                     : "memory");
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ds(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
+{
+    mp_issue<ACC, kMpHiU, kDescHi>(d, a_lo, b_lo, idesc);
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_sd(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
+{
+    mp_issue<ACC, kDescHi, kMpHiU>(d, a_lo, b_lo, idesc);
+}
+
+// The scores' lane: tile by tile as the rows come.
 template <int N>
-__device__ void mp_mma(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t tm, int64_t lo, int64_t hi)
+__device__ void mp_scores(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t tm, int64_t lo, int64_t hi)
 {
     using Y = MpLayout<N>;
     const MpParams& p = L.p;
     constexpr uint32_t idS = ptx::idesc_bf16_f32(kMpTok, N);
-    constexpr uint32_t idO = ptx::idesc_bf16_f32(128, Y::NW) | (1u << 15);       // A: MN-major
-    constexpr uint32_t hiU = (2 * kMpAtom >> 4) | (1u << 14) | (2u << 29);       // units: groups of 8 rows 2 KB apart
-    constexpr uint32_t hi1 = (kMpAtom >> 4) | (1u << 14) | (2u << 29);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
-    auto desc = [](uint32_t lo_word, uint32_t hi_word) { return ((uint64_t)hi_word << 32) | lo_word; };
-    const uint32_t q_lo = ((sbase + Y::kQ) >> 4) | (1u << 16), p_lo = ((sbase + Y::kP) >> 4) | (1u << 16);
-    const uint32_t u_lo = (sbase + Y::kRing) >> 4, r_lo = ((sbase + Y::kRopes) >> 4) | (1u << 16);
-    uint32_t seg = 0;
-    // scores of tile t; its rope block is free after them
-    auto scores = [&](uint32_t t, const MpWalk& w) -> bool {
+    const uint32_t q_lo = ((sbase + Y::kQ) >> 4) | (1u << 16), u_lo = ((sbase + Y::kRing) >> 4) | (1u << 16);
+    const uint32_t r_lo = ((sbase + Y::kRopes) >> 4) | (1u << 16);
+    MpWalk w;
+    w.start(p, b, lo, hi);
+    uint32_t seg = 0, at = 0, lap = 0;   // place in the ring
+    for (uint32_t t = 0; w.left > 0; ++t, w.next(p)) {
         if (w.fresh && !wait(&b.q_full, seg))
-            return false;
+            break;
+        if (t >= 2 && !wait(&b.p_full[t & 1u], (t >> 1) - 1))   // the scores that stood there have been read
+            break;
         const uint32_t d = tm + Y::kTmS + (t & 1u) * N;
-#pragma unroll 1
+        bool ok = true;
+#pragma unroll
         for (uint32_t u = 0; u < kMpUnits; ++u) {
-            const uint32_t k = kMpUnits * t + u, at = k % Y::NU;
-            if (!wait(&b.full[at], k / Y::NU))
-                return false;
+            if (!(ok = ok && wait(&b.full[at], lap)))
+                break;
             ptx::tc_fence_after();
-            const uint32_t a = (u_lo + at * (kMpUnit >> 4)) | (1u << 16), q = q_lo + 2 * u * (Y::kQBlock >> 4);
+            const uint32_t a = u_lo + at * (kMpUnit >> 4), q = q_lo + 2 * u * (Y::kQBlock >> 4);
+            if (u == 0)
+                mma_ds<false>(d, a, q, idS);
+            else
+                mma_ds<true>(d, a, q, idS);
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    ptx::umma_bf16(d, desc(a + blk * (kMpAtom >> 4) + 2 * ks, hiU),
-                                   desc(q + blk * (Y::kQBlock >> 4) + 2 * ks, hi1), idS, u + blk + ks > 0 ? 1u : 0u);
+            for (int i = 1; i < 8; ++i)   // two blocks of 64 columns
+                mma_ds<true>(d, a + (i >> 2) * (kMpAtom >> 4) + 2 * (i & 3),
+                             q + (i >> 2) * (Y::kQBlock >> 4) + 2 * (i & 3), idS);
+            if (++at == (uint32_t)Y::NU) {
+                at = 0;
+                ++lap;
+            }
         }
-        const uint32_t at = t % Y::NR;
-        if (!wait(&b.rfull[at], t / Y::NR))
-            return false;
+        const uint32_t ra = t % Y::NR;
+        if (!ok || !wait(&b.rfull[ra], t / Y::NR))
+            break;
         ptx::tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-            ptx::umma_bf16(d, desc(r_lo + at * (kMpRope >> 4) + 2 * ks, hi1),
-                           desc(q_lo + 8 * (Y::kQBlock >> 4) + 2 * ks, hi1), idS, 1u);
-        ptx::umma_commit(ptx::smem_addr(&b.rempty[at]));
+            mma_ss<true>(d, r_lo + ra * (kMpRope >> 4) + 2 * ks, q_lo + 8 * (Y::kQBlock >> 4) + 2 * ks, idS);
+        ptx::umma_commit(ptx::smem_addr(&b.rempty[ra]));
         ptx::umma_commit(ptx::smem_addr(&b.s_full[t & 1u]));
         if (w.last()) {
             ptx::umma_commit(ptx::smem_addr(&b.q_empty));
             ++seg;
         }
-        return true;
-    };
-    auto weigh = [&](uint32_t t, bool fresh) -> bool {
-        if (!wait(&b.p_full[t & 1u], t >> 1))
-            return false;
-        ptx::tc_fence_after();
-        const uint32_t pb = p_lo + t % Y::NP * (Y::kPTile >> 4);
-#pragma unroll 1
-        for (uint32_t u = 0; u < kMpUnits; ++u) {
-            const uint32_t at = (kMpUnits * t + u) % Y::NU;
-            const uint32_t a = (u_lo + at * (kMpUnit >> 4)) | ((kMpAtom >> 4) << 16);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                ptx::umma_bf16(tm + Y::kTmO + u * Y::NW, desc(a + ks * (4 * kMpAtom >> 4), hiU), desc(pb + 2 * ks, hi1),
-                               idO, fresh && ks == 0 ? 0u : 1u);
-            ptx::umma_commit(ptx::smem_addr(&b.empty[at]));
-        }
-        ptx::umma_commit(ptx::smem_addr(&b.pv_done));
-        return true;
-    };
-    MpWalk w;
-    w.start(p, b, lo, hi);
-    uint32_t t = 0;
-    bool ok = w.left <= 0 || scores(0, w);
-    while (w.left > 0 && ok) {
-        const bool fresh = w.fresh;
-        w.next(p);
-        ok = (w.left <= 0 || scores(t + 1, w)) && weigh(t, fresh);
-        ++t;
     }
     // every MMA issued here completes before TMEM is freed
-    ptx::umma_commit(ptx::smem_addr(&b.drained));
-    pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
+    ptx::umma_commit(ptx::smem_addr(&b.drained[0]));
+    pf_drain_wait(ptx::smem_addr(&b.drained[0]), 0u, p.wait_ns);
+}
+
+// The products' lane: tile by tile as the weights come; a tile's units are free behind it.
+template <int N>
+__device__ void mp_products(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t tm, int64_t lo, int64_t hi)
+{
+    using Y = MpLayout<N>;
+    const MpParams& p = L.p;
+    constexpr uint32_t idO = ptx::idesc_bf16_f32(64, 128) | (1u << 16);   // B: MN-major
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+    };
+    const uint32_t p_lo = ((sbase + Y::kP) >> 4) | (1u << 16);
+    const uint32_t u_lo = ((sbase + Y::kRing) >> 4) | ((kMpAtom >> 4) << 16);
+    MpWalk w;
+    w.start(p, b, lo, hi);
+    uint32_t at = 0, lap = 0;
+    for (uint32_t t = 0; w.left > 0; ++t, w.next(p)) {
+        uint32_t x = at, xl = lap;
+        bool ok = true;
+        for (uint32_t u = 0; u < kMpUnits && ok; ++u) {   // there long since: the weights come behind their scores
+            ok = wait(&b.full[x], xl);
+            if (++x == (uint32_t)Y::NU) {
+                x = 0;
+                ++xl;
+            }
+        }
+        if (!ok || !wait(&b.p_full[t & 1u], t >> 1))
+            break;
+        ptx::tc_fence_after();
+        const uint32_t pb = p_lo + t % Y::NP * (Y::kPTile >> 4);
+#pragma unroll
+        for (uint32_t u = 0; u < kMpUnits; ++u) {
+            const uint32_t v = u_lo + at * (kMpUnit >> 4);
+            const uint32_t d = tm + Y::kTmO + (u & 1u) * 128 + ((u >> 1) << 20);   // columns 256 on: 16 lanes further
+            if (w.fresh)
+                mma_sd<false>(d, pb, v, idO);
+            else
+                mma_sd<true>(d, pb, v, idO);
+#pragma unroll
+            for (int ks = 1; ks < 4; ++ks)
+                mma_sd<true>(d, pb + 2 * ks, v + ks * (4 * kMpAtom >> 4), idO);
+            ptx::umma_commit(ptx::smem_addr(&b.empty[at]));
+            if (++at == (uint32_t)Y::NU) {
+                at = 0;
+                ++lap;
+            }
+        }
+        ptx::umma_commit(ptx::smem_addr(&b.pv_done[t & 1u]));
+    }
+    ptx::umma_commit(ptx::smem_addr(&b.drained[1]));
+    pf_drain_wait(ptx::smem_addr(&b.drained[1]), 0u, p.wait_ns);
 }
 
 // ----------------------------------------------------------------- softmax --
@@ -396,23 +457,12 @@ __device__ __forceinline__ void mp_ld_scores(uint32_t ta, uint32_t (&r)[N / 2])
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(ta)
                      : "memory");
-    } else if constexpr (N == 32) {
+    } else {
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, "
                      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
                        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
                        "=r"(r[15])
-                     : "r"(ta)
-                     : "memory");
-    } else {
-        asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                     "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-                     "tcgen05.wait::ld.sync.aligned;"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-                       "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-                       "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-                       "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                      : "r"(ta)
                      : "memory");
     }
@@ -427,37 +477,48 @@ __device__ __forceinline__ void stsm_x4_t(uint32_t a, uint32_t x, uint32_t y, ui
                  : "memory");
 }
 
-__device__ __forceinline__ void mp_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-// The four softmax warps meet; whether any thread said yes.
+// The four warps of softmax group GRP meet.
+template <int GRP>
+__device__ __forceinline__ void mp_sync()
+{
+    asm volatile("bar.sync %0, 128;" ::"n"(1 + 2 * GRP) : "memory");
+}
+// The same; whether any thread said yes.
+template <int GRP>
 __device__ __forceinline__ bool mp_any(bool x)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 2, 128, p;\n\t"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\t"
                  "selp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"(x ? 1u : 0u)
+                 : "r"(x ? 1u : 0u), "n"(2 + 2 * GRP)
                  : "memory");
     return r != 0;
 }
 
-template <int N>
+// Softmax group GRP: heads GRP HG .. of the block.
+template <int N, int GRP>
 __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* ex, uint32_t tm, int warp, int lane,
                            int block, int range, int64_t lo, int64_t hi)
 {
     using Y = MpLayout<N>;
-    constexpr int J = N / 8;
+    constexpr int HG = Y::HG, J = HG / 8, G0 = GRP * HG;
     const MpParams& p = L.p;
     const int gq = lane >> 2, t4 = lane & 3;
     const uint32_t lanes = tm + ((uint32_t)warp << 21);
     const float sl2 = p.scale * kMpLog2e;
-    const int heads = min(N, p.Hq - block * N);
+    const int head0 = block * N + G0, heads = min(HG, p.Hq - head0);   // (none at all for a last group: 0 or less)
     const int64_t T = b.total, R = mp_ranges(p, T);
-    float* wmax = ex;              // [4 warps][N]: the warps' maxima; their sums
-    float* fac = ex + 4 * N;       // [N]: factors of the running output
+    float* wmax = ex + 5 * G0;     // [4 warps][HG]: the warps' maxima; their sums
+    float* fac = wmax + 4 * HG;    // [HG]: factors of the running output
+    // the output's rows of this group: whether this warp's lanes hold some, and the lane's head
+    constexpr int Q0 = Y::kPair ? 0 : G0 / 16, Q1 = Q0 + (Y::kPair ? 2 : 1) * HG / 16;
+    const bool out_warp = warp >= Q0 && warp < Q1;
+    const int out_head = out_warp ? (Y::kPair ? 8 * warp + (lane & 7) : 16 * (warp - Q0) + (lane & 15)) : 0;
     float m[J][2], l[J][2];        // heads 8 j + 2 t4, + 1: the agreed maximum (log2 units), this thread's sum
     // where this lane's row of a stored block goes: block k = (j, half of the tokens) in pairs of j
     const uint32_t st_row = lane & 7, st_half = (lane >> 3) & 1, st_j = lane >> 4;
-    const uint32_t st = sbase + Y::kP + st_j * kMpAtom + sw128(st_row, 2 * warp + st_half);
+    const uint32_t st = sbase + Y::kP + (G0 / 8 + st_j) * (Y::kPair ? 2 : 1) * kMpAtom + sw128(st_row, 2 * warp + st_half);
     MpWalk w;
     w.start(p, b, lo, hi);
     int64_t at = lo;               // the tile's place among all
@@ -469,15 +530,15 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                 m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.f;
         }
         const int ntok = min(kMpTok, w.len - w.t * kMpTok);
-        ok = ok && wmma16::tile_wait(ptx::smem_addr(&b.s_full[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_ns);
+        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        uint32_t s[N / 2];
+        uint32_t s[HG / 2];
         bool grew = false;
         const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[t % kMpMasks]);
         float x[J][4];
         if (ok) {
             ptx::tc_fence_after();
-            mp_ld_scores<N>(lanes + Y::kTmS + (t & 1u) * N, s);
+            mp_ld_scores<HG>(lanes + Y::kTmS + (t & 1u) * N + G0, s);
             const bool here = (mask >> warp) & 1u;
             const bool in0 = here && 16 * warp + gq < ntok, in1 = here && 16 * warp + gq + 8 < ntok;
 #pragma unroll
@@ -490,8 +551,8 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                 }
             }
         }
-        if (mp_any(grew || !ok)) {   // rare but for a segment's first tile
-            if (mp_any(!ok))
+        if (mp_any<GRP>(grew || !ok)) {   // rare but for a segment's first tile
+            if (mp_any<GRP>(!ok))
                 break;               // all four warps
 #pragma unroll
             for (int j = 0; j < J; ++j)
@@ -502,9 +563,9 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                     v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
                     if (gq == 0)
-                        wmax[warp * N + 8 * j + 2 * t4 + c] = v;
+                        wmax[warp * HG + 8 * j + 2 * t4 + c] = v;
                 }
-            mp_sync();
+            mp_sync<GRP>();
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -513,7 +574,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                     float v = m[j][c];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        v = fmaxf(v, wmax[k * N + h]);
+                        v = fmaxf(v, wmax[k * HG + h]);
                     const float f = v == -INFINITY ? 1.f : pf_ex2(m[j][c] - v);
                     l[j][c] *= f;
                     m[j][c] = v;
@@ -521,27 +582,31 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                         fac[h] = f;
                 }
             if (!w.fresh) {          // the running output, once the products before are in it
-                ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 ptx::tc_fence_after();
-                mp_sync();
+                mp_sync<GRP>();
+                if (out_warp) {
+                    const float f = fac[out_head];
 #pragma unroll 1
-                for (int c = 0; c < 4 * Y::NW / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(lanes + Y::kTmO + 32 * c, o);
+                    for (int c = 0; c < kMpDim / 2 / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(lanes + Y::kTmO + 32 * c, o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[(32 * (c % (N / 16 > 1 ? N / 32 : 1)) + i) % N]);
-                    tmem_st32(lanes + Y::kTmO + 32 * c, o);
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(lanes + Y::kTmO + 32 * c, o);
+                    }
+                    tmem_wait_st();
                 }
-                tmem_wait_st();
             }
-            mp_sync();               // the exchange's arrays are free again
+            mp_sync<GRP>();               // the exchange's arrays are free again
         }
         // weights, transposed into the operand rows (heads) of the second product
         const uint32_t dst = st + t % Y::NP * Y::kPTile;
-        if (Y::NP == 1 && t > 0) {   // (two buffers: the scores of this tile were issued after that product)
-            ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+        if (t >= Y::NP) {            // the product that read the buffer's last weights
+            const uint32_t k = t - Y::NP;
+            ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[k & 1u]), (k >> 1) & 1u, &b.abort, p.err, p.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
         }
 #pragma unroll
@@ -561,12 +626,12 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                     h[k] = pack_bf16x2(a, c);
                 }
             }
-            stsm_x4_t(dst + j * kMpAtom, h[0], h[1], h[2], h[3]);
+            stsm_x4_t(dst + j * (Y::kPair ? 2 : 1) * kMpAtom, h[0], h[1], h[2], h[3]);
             if constexpr (Y::kPair)
-                stsm_x4_t(dst + (J + j) * kMpAtom, lo4[0], lo4[1], lo4[2], lo4[3]);
+                stsm_x4_t(dst + (2 * j + 1) * kMpAtom, lo4[0], lo4[1], lo4[2], lo4[3]);
         }
         if (ntok < kMpTok || mask != 0xFu) {   // value rows without a token: zero, so that zero weights add nothing
-            for (int e = threadIdx.x; e < kMpTok * 64; e += 128) {
+            for (int e = threadIdx.x; e < kMpTok * 64; e += 4 * 32 * (N / HG)) {
                 const int r = e >> 6, piece = e & 63, u = piece >> 4, blk = (piece >> 3) & 1;
                 if (r >= ntok || !((mask >> (r >> 4)) & 1u))
                     ptx::st_shared_zero16(sbase + Y::kRing + (kMpUnits * t + u) % Y::NU * kMpUnit +
@@ -588,7 +653,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
         const int first_slot = (int)(2 * r0 + (mp_start(r0, T, R) == a0 ? 0 : 1));
         const bool whole = r0 == r1;
         const int slot = range == r0 ? first_slot : 2 * range;
-        if (range == r0 && block == 0 && threadIdx.x == 0)
+        if (range == r0 && block == 0 && GRP == 0 && warp == 0 && lane == 0)
             p.span[s_seq] = make_int4((int)r0, (int)r1, first_slot, 0);
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -598,17 +663,17 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                 l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], 8);
                 l[j][c] += __shfl_xor_sync(0xFFFFFFFFu, l[j][c], 16);
                 if (gq == 0)
-                    wmax[warp * N + 8 * j + 2 * t4 + c] = l[j][c];
+                    wmax[warp * HG + 8 * j + 2 * t4 + c] = l[j][c];
             }
-        mp_sync();
-        const int64_t row0 = (int64_t)s_seq * p.Hq + block * N, part0 = (int64_t)slot * p.Hq + block * N;
+        mp_sync<GRP>();
+        const int64_t row0 = (int64_t)s_seq * p.Hq + head0, part0 = (int64_t)slot * p.Hq + head0;
         if (warp == 0 && gq == 0) {
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int h = 8 * j + 2 * t4 + c;
-                    const float sum = (wmax[h] + wmax[N + h]) + (wmax[2 * N + h] + wmax[3 * N + h]);
+                    const float sum = (wmax[h] + wmax[HG + h]) + (wmax[2 * HG + h] + wmax[3 * HG + h]);
                     fac[h] = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
                     if (h < heads) {
                         if (!whole)
@@ -618,57 +683,55 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                     }
                 }
         }
-        ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), t & 1u, &b.abort, p.err, p.wait_ns);
+        ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
-        mp_sync();
+        mp_sync<GRP>();
+        if (out_warp) {
+            const bool mine = ok && out_head < heads;
+            const float inv = fac[out_head];
+            const int dim0 = (lane >> 4) * (kMpDim / 2);
 #pragma unroll 1
-        for (int u = 0; u < kMpUnits; ++u) {
-            const int dim = 128 * u + 32 * warp + lane;
-#pragma unroll 1
-            for (int h0 = 0; h0 < heads; h0 += 16) {
-                uint32_t o[32];   // 16 heads: their hi columns, and the lo ones
-                if constexpr (N == 16) {
-                    tmem_ld32(lanes + Y::kTmO + u * Y::NW, o);
-                } else {
-                    uint32_t a[8], c[8], d[8], e[8];
-                    const uint32_t from = lanes + Y::kTmO + u * Y::NW + h0;
-                    ptx::tmem_ld8x2_issue(from, from + 8, a, c);
-                    ptx::tmem_wait8x2(a, c);
-                    if constexpr (Y::kPair) {
-                        ptx::tmem_ld8x2_issue(from + N, from + N + 8, d, e);
-                        ptx::tmem_wait8x2(d, e);
-                    }
+            for (int c = 0; c < kMpDim / 2 / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(lanes + Y::kTmO + 32 * c, o);
+                if constexpr (Y::kPair) {   // a lane with hi sums and one with lo sums: each writes half of the columns
+                    const bool lo_row = lane & 8;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        o[i] = a[i], o[8 + i] = c[i];
-                        o[16 + i] = Y::kPair ? d[i] : 0u, o[24 + i] = Y::kPair ? e[i] : 0u;
+                    for (int i = 0; i < 16; ++i) {
+                        const float give = __uint_as_float(lo_row ? o[i] : o[16 + i]);
+                        const float keep = __uint_as_float(lo_row ? o[16 + i] : o[i]);
+                        o[i] = __float_as_uint(keep + __shfl_xor_sync(0xFFFFFFFFu, give, 8));
                     }
                 }
-                if (!ok)
-                    continue;
+                constexpr int C = Y::kPair ? 16 : 32;
+                const int dim = dim0 + 32 * c + (Y::kPair ? (lane & 8) * 2 : 0);
+                if (mine && whole) {
+                    __nv_bfloat16* dst = p.out + (row0 + out_head) * kMpDim + dim;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (h0 + i >= heads)
-                        break;
-                    float v = __uint_as_float(o[i]);
-                    if constexpr (Y::kPair)
-                        v += __uint_as_float(o[16 + i]);
-                    if (whole)
-                        p.out[(row0 + h0 + i) * kMpDim + dim] = __float2bfloat16_rn(v * fac[h0 + i]);
-                    else
-                        p.o[(part0 + h0 + i) * kMpDim + dim] = v;
+                    for (int i = 0; i < C; i += 8)
+                        *reinterpret_cast<uint4*>(dst + i) =
+                            make_uint4(pack_bf16x2(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv),
+                                       pack_bf16x2(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv),
+                                       pack_bf16x2(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv),
+                                       pack_bf16x2(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv));
+                } else if (mine) {
+                    float* dst = p.o + (part0 + out_head) * kMpDim + dim;
+#pragma unroll
+                    for (int i = 0; i < C; i += 4)
+                        *reinterpret_cast<uint4*>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
+                __syncwarp();
             }
         }
         ptx::tc_fence_before();
-        mp_sync();   // the exchange's arrays, and TMEM, are free for the next segment
+        mp_sync<GRP>();   // the exchange's arrays, and TMEM, are free for the next segment
         w.next(p);
     }
 }
 
 template <int N>
-__global__ void __launch_bounds__(kMpThreads, 1) mla_paged_kernel(const __grid_constant__ MpLaunch L)
+__global__ void __launch_bounds__(MpLayout<N>::kThreads, 1) mla_paged_kernel(const __grid_constant__ MpLaunch L)
 {
     using Y = MpLayout<N>;
     const MpParams& p = L.p;
@@ -689,21 +752,21 @@ __global__ void __launch_bounds__(kMpThreads, 1) mla_paged_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_addr(&b.s_full[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&b.p_full[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&b.p_full[i]), Y::kProd);   // softmax warps
+            ptx::mbar_init(ptx::smem_addr(&b.pv_done[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.drained[i]), 1);
         }
         ptx::mbar_init(ptx::smem_addr(&b.q_full), 1);
         ptx::mbar_init(ptx::smem_addr(&b.q_empty), 1);
-        ptx::mbar_init(ptx::smem_addr(&b.pv_done), 1);
-        ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
         ptx::fence_barrier_init();
     }
-    if (warp == kMpProd && lane == 0) {
+    if (warp == Y::kProd && lane == 0) {
         ptx::prefetch_tmap(&L.map_c);
         ptx::prefetch_tmap(&L.map_r);
         ptx::prefetch_tmap(&L.map_q);
     }
-    if (warp == kMpMma) {
+    if (warp == Y::kScores) {
         ptx::tmem_alloc(ptx::smem_addr(&b.tmem), Y::kTmCols);
         ptx::tmem_relinquish();
     }
@@ -711,7 +774,7 @@ __global__ void __launch_bounds__(kMpThreads, 1) mla_paged_kernel(const __grid_c
     if (warp == 0)
         mp_locate(p, b, range, lane);
     if (blockIdx.x == 0 && warp > 0)
-        for (int s = threadIdx.x - 32; s < p.n_seqs; s += kMpThreads - 32)
+        for (int s = threadIdx.x - 32; s < p.n_seqs; s += Y::kThreads - 32)
             if (p.lens[s] < 0 || p.lens[s] > p.max_len)
                 raise_err(p.err, KAMERA_DEVERR_LEN);
     ptx::tc_fence_before();
@@ -723,15 +786,20 @@ __global__ void __launch_bounds__(kMpThreads, 1) mla_paged_kernel(const __grid_c
     if (range < R) {   // (else: fewer tiles than ranges)
         const int64_t lo = mp_start(range, T, R), hi = mp_start(range + 1, T, R);
         if (warp < 4)
-            mp_softmax<N>(L, b, sbase, ex, tm, warp, lane, block, range, lo, hi);
-        else if (warp == kMpProd)
+            mp_softmax<N, 0>(L, b, sbase, ex, tm, warp, lane, block, range, lo, hi);
+        else if (warp < Y::kProd)
+            mp_softmax<N, N / Y::HG - 1>(L, b, sbase, ex, tm, warp - 4, lane, block, range, lo, hi);
+        else if (warp == Y::kProd)
             mp_producer<N>(L, b, sbase, lane, block, lo, hi);
-        else if (mp_elect())
-            mp_mma<N>(L, b, sbase, tm, lo, hi);
+        else if (warp == Y::kScores) {
+            if (mp_elect())
+                mp_scores<N>(L, b, sbase, tm, lo, hi);
+        } else if (mp_elect())
+            mp_products<N>(L, b, sbase, tm, lo, hi);
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == kMpMma) {
+    if (warp == Y::kScores) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tm, Y::kTmCols);
     }
@@ -739,10 +807,18 @@ __global__ void __launch_bounds__(kMpThreads, 1) mla_paged_kernel(const __grid_c
 
 // ------------------------------------------------------------------- merge --
 // The rows whose sequence was cut: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
-// over the partial states of its ranges.  A CTA a row, a thread four columns.
-__global__ void __launch_bounds__(128) mla_merge_kernel(const MpParams p)
+// over the partial states of its ranges.  A CTA a row, a thread four columns of every
+// GR-th state, whose outputs it asks for eight at a time before their weights are known;
+// the GR sums join in order.  GR = 4 where a sequence may have many states: all latency
+// (one thread for all states of four columns: 9 us more where one sequence is cut 64
+// times); 1 where the rows are many and have two or three (four groups: 30 us more for
+// 6144 rows).
+template <int GR>
+__global__ void __launch_bounds__(128 * GR) mla_merge_kernel(const MpParams p)
 {
+    __shared__ float4 part[GR > 1 ? GR - 1 : 1][128];
     const int s = blockIdx.x / p.Hq, h = blockIdx.x - s * p.Hq;
+    const int lane = threadIdx.x & 31, group = threadIdx.x >> 7, col = threadIdx.x & 127;
     ptx::grid_wait();
     ptx::grid_launch_next();
     const int4 sp = p.span[s];
@@ -751,36 +827,69 @@ __global__ void __launch_bounds__(128) mla_merge_kernel(const MpParams p)
         return;
     const int n = sp.y - sp.x + 1;
     auto slot = [&](int i) { return (int64_t)(i == 0 ? sp.z : 2 * (sp.x + i)) * p.Hq + h; };
+    constexpr int U = 8;
+    float4 v[U];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + GR * k + group;
+            if (i < n)
+                v[k] = *reinterpret_cast<const float4*>(p.o + slot(i) * kMpDim + 4 * col);
+        }
+    };
+    load(0);
     float m = -INFINITY;
-    for (int i = 0; i < n; ++i)
+    for (int i = lane; i < n; i += 32)
         m = fmaxf(m, p.ml[slot(i)].x);
+#pragma unroll
+    for (int d = 16; d >= 1; d /= 2)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int U = 4;
-    for (int i0 = 0; i0 < n; i0 += U) {
-        float4 v[U];
-        float2 ml[U];
+    for (int i0 = 0; i0 < n; i0 += U * GR) {
+        if (i0 > 0)
+            load(i0);
+        float f = 0.f;   // a state without weight adds nothing (and has no maximum to scale by)
+        bool some = false;
+        if (lane < U * GR && i0 + lane < n) {
+            const float2 y = p.ml[slot(i0 + lane)];
+            some = y.y != 0.f;
+            if (some) {
+                f = pf_ex2(y.x - m);
+                l = fmaf(y.y, f, l);
+            }
+        }
+        const uint32_t live = __ballot_sync(0xFFFFFFFFu, some);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int64_t at = slot(min(i0 + k, n - 1));
-            ml[k] = p.ml[at];
-            v[k] = *reinterpret_cast<const float4*>(p.o + at * kMpDim + 4 * threadIdx.x);
+            const int j = GR * k + group;
+            const float x = __shfl_sync(0xFFFFFFFFu, f, j);
+            if ((live >> j) & 1u) {
+                acc.x = fmaf(v[k].x, x, acc.x);
+                acc.y = fmaf(v[k].y, x, acc.y);
+                acc.z = fmaf(v[k].z, x, acc.z);
+                acc.w = fmaf(v[k].w, x, acc.w);
+            }
         }
+    }
+    if constexpr (GR > 1) {
+        if (group > 0)
+            part[group - 1][col] = acc;
+        __syncthreads();
+        if (group > 0)
+            return;
+    }
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i0 + k >= n || ml[k].y == 0.f)   // no weight: nothing to add (and no maximum to scale by)
-                continue;
-            const float f = pf_ex2(ml[k].x - m);
-            l = fmaf(ml[k].y, f, l);
-            acc.x = fmaf(v[k].x, f, acc.x);
-            acc.y = fmaf(v[k].y, f, acc.y);
-            acc.z = fmaf(v[k].z, f, acc.z);
-            acc.w = fmaf(v[k].w, f, acc.w);
-        }
+    for (int d = 16; d >= 1; d /= 2)
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+#pragma unroll
+    for (int g = 0; g < GR - 1; ++g) {
+        const float4 y = part[g][col];
+        acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
     }
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
     const int64_t row = blockIdx.x;
-    *reinterpret_cast<uint2*>(p.out + row * kMpDim + 4 * threadIdx.x) =
+    *reinterpret_cast<uint2*>(p.out + row * kMpDim + 4 * col) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     if (threadIdx.x == 0 && p.lse)
         p.lse[row] = l > 0.f ? (m + log2f(l)) * kMpLn2 : (l == l ? -INFINITY : l);
@@ -839,7 +948,7 @@ cudaError_t mp_launch(const MpLaunch& L, cudaStream_t stream)
         cudaFuncSetAttribute(mla_paged_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Y::kBytes);
     if (e != cudaSuccess)
         return e;
-    return launch_after(mla_paged_kernel<N>, dim3((unsigned)(L.p.ranges * L.p.blocks)), kMpThreads, Y::kBytes, stream,
+    return launch_after(mla_paged_kernel<N>, dim3((unsigned)(L.p.ranges * L.p.blocks)), Y::kThreads, Y::kBytes, stream,
                         true, L);
 }
 
@@ -921,9 +1030,14 @@ int kamera_mla_attend_paged(const KameraPagedMlaKV* kv, const KameraPagedQuery* 
     const cudaError_t ce = N == 16 ? mp_launch<16>(L, stream) : N == 32 ? mp_launch<32>(L, stream) : mp_launch<64>(L, stream);
     if (ce != cudaSuccess)
         return KAMERA_ERR_CUDA;
-    if (p.ranges > 1 &&
-        launch_after(mla_merge_kernel, dim3((unsigned)rows), 128, 0, stream, true, p) != cudaSuccess)
-        return KAMERA_ERR_CUDA;
+    if (p.ranges > 1) {
+        // states of a row on average: a range ends in each but the last
+        const bool many = p.ranges >= 8ll * p.n_seqs;
+        const dim3 grid((unsigned)rows);
+        if ((many ? launch_after(mla_merge_kernel<4>, grid, 512, 0, stream, true, p)
+                  : launch_after(mla_merge_kernel<1>, grid, 128, 0, stream, true, p)) != cudaSuccess)
+            return KAMERA_ERR_CUDA;
+    }
     return KAMERA_OK;
 }
 

@@ -146,7 +146,7 @@ __device__ void pr_producer(const PrLaunch& L, const PrWork& w, PrBars& b, uint3
     for (int t = 0; t < n && ok; ++t)
         for (int u = 0; u < kPrTile; ++u, ++k) {
             const uint32_t at = k % kPrUnits, lap = k / kPrUnits, full = ptx::smem_addr(&b.full[at]);
-            if (lap > 0 && !wmma16::tile_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns)) {
+            if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns)) {
                 ok = false;
                 break;
             }
@@ -185,7 +185,7 @@ __device__ void pr_mma(const PrLaunch& L, const PrWork& w, PrBars& b, uint32_t s
     constexpr uint32_t idV = ptx::idesc_bf16_f32(kPrRows, 64) | (1u << 16);   // value rows: MN-major
     const uint32_t q_lo = ((sbase + kPrQ) >> 4) | (1u << 16), r_lo = (sbase + kPrRing) >> 4;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
     // scores of side a's tile t; the tile's keys are free after its last side
     auto scores = [&](auto side, int t) -> bool {
@@ -297,7 +297,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int t = 0; t < nt; ++t) {
-        if (!wmma16::tile_wait(ptx::smem_addr(&b.s_full[a]), (uint32_t)t & 1u, &b.abort, p.err, p.wait_ns))
+        if (!wmma16::cycle_wait(ptx::smem_addr(&b.s_full[a]), (uint32_t)t & 1u, &b.abort, p.err, p.wait_ns))
             ok = false;
         if (!__all_sync(0xFFFFFFFFu, ok)) {
             ok = false;
@@ -351,7 +351,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
             const float f = m_new == -INFINITY ? 1.f : pf_ex2(m_run - m_new);
             l_run *= f;
             m_run = m_new;
-            if (!wmma16::tile_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(t - 1) & 1u, &b.abort, p.err, p.wait_ns))
+            if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(t - 1) & 1u, &b.abort, p.err, p.wait_ns))
                 ok = false;
             ok = __all_sync(0xFFFFFFFFu, ok);
             ptx::tc_fence_after();
@@ -369,7 +369,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
             const uint32_t k = (uint32_t)(kPrTile * t + 3);
             bool in = true;
             for (int u = 0; u < 2; ++u)
-                in = in && wmma16::tile_wait(ptx::smem_addr(&b.full[(k + u) % kPrUnits]), ((k + u) / kPrUnits) & 1u, &b.abort,
+                in = in && wmma16::cycle_wait(ptx::smem_addr(&b.full[(k + u) % kPrUnits]), ((k + u) / kPrUnits) & 1u, &b.abort,
                                              p.err, p.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok && in);
             for (int i = r; i < (base + kPrTok - w.nk) * 16; i += kPrRows) {
@@ -413,7 +413,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
         }
     }
     if (nt > 0 && ok) {
-        if (!wmma16::tile_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(nt - 1) & 1u, &b.abort, p.err, p.wait_ns))
+        if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(nt - 1) & 1u, &b.abort, p.err, p.wait_ns))
             ok = false;
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();

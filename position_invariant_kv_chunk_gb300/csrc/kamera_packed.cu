@@ -210,7 +210,7 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
         if (lap > 0) {
             bool got = true;
             if (lane == 0)
-                got = wmma16::tile_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns);
+                got = wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns);
             ok = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
             if (!ok)
                 break;
@@ -252,7 +252,7 @@ __device__ void p4_mma(const P4Params& p, P4Bars& b, uint32_t sbase, uint32_t tm
     constexpr uint32_t id = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);   // fp16 x fp16 -> fp32, M 128
     const uint32_t q_lo = ((sbase + Y::kQ) >> 4) | (1u << 16), p_lo = ((sbase + Y::kP) >> 4) | (1u << 16);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::tile_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
     P4Walk w;
     w.start(p, b, lo, hi);
@@ -311,7 +311,7 @@ __device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* rin
     bool ok = true;
     for (uint32_t t = 0; w.left > 0; ++t, w.next(p)) {
         const uint32_t at = t % Y::NS;
-        ok = wmma16::tile_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
+        ok = wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
         if (!__all_sync(0xFFFFFFFFu, ok))
             return;
         const unsigned char* tile = ring + at * Y::kTile;
@@ -332,7 +332,7 @@ __device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* rin
                 }
             }
             if (half == 0 && t > 0) {   // the product before has read the last tile's values
-                ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
                 if (!__all_sync(0xFFFFFFFFu, ok))
                     return;
                 ptx::tc_fence_after();
@@ -484,7 +484,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, const unsigned char* ri
                 }
         }
         const uint32_t at = t % Y::NS;
-        ok = ok && wmma16::tile_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
+        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[at]);
         if (ok) {   // this token's keys (the scores before have been read: their product is done with TMEM)
@@ -517,7 +517,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, const unsigned char* ri
             ptx::fence_proxy_async();   // the queries
             ptx::tc_fence_before();
             ptx::mbar_arrive(ptx::smem_addr(&b.k_full));
-            ok = wmma16::tile_wait(ptx::smem_addr(&b.s_full), t & 1u, &b.abort, p.err, p.wait_ns);
+            ok = wmma16::cycle_wait(ptx::smem_addr(&b.s_full), t & 1u, &b.abort, p.err, p.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
         }
         const int ntok = min(kP4Tok, w.len - w.t * kP4Tok);
@@ -582,7 +582,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, const unsigned char* ri
                         fac[h] = f;
                 }
             if (!w.fresh) {          // the running output, once the products before are in it
-                ok = wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 ptx::tc_fence_after();
                 p4_sync();
@@ -611,7 +611,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, const unsigned char* ri
             }
         }
         if (t > 0) {                 // the product before has read the last weights
-            ok = ok && wmma16::tile_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+            ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
         }
 #pragma unroll
@@ -656,7 +656,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, const unsigned char* ri
                                                                                 (wmax[2 * N + h] + wmax[3 * N + h]));
                 }
         }
-        ok = ok && wmma16::tile_wait(ptx::smem_addr(&b.pv_done), t & 1u, &b.abort, p.err, p.wait_ns);
+        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done), t & 1u, &b.abort, p.err, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
         uint32_t o[N];
