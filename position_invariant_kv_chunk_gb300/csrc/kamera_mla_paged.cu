@@ -211,22 +211,48 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
 {
     using Y = MpLayout<N>;
     const MpParams& p = L.p;
-    MpWalk w;
+    // Lane l is at 16-token piece l % 4 of tile l / 4 of eight tiles, and of the eight
+    // after them: pages are looked up, and rows worked out, for 32 pieces at once and
+    // eight tiles ahead (under load a look-up takes 2000 cycles).
+    constexpr int kPieces = kMpTok / 16, kAhead = 32 / kPieces;
+    const int R = p.box_rows, off = 16 * (lane % kPieces);   // a box of R rows is issued by its first piece's lane
+    MpWalk w, mine;
     w.start(p, b, lo, hi);
-    auto page_of = [&](const MpWalk& v) {   // of the tile's 16-token piece `lane`
-        const int tok = v.t * kMpTok + 16 * lane;
-        return lane < kMpTok / 16 && tok < v.len ? p.pages[(int64_t)v.s * p.max_pages + tok / p.P] : -1;
+    mine = w;
+    auto advance = [&](int n) {
+        if (mine.left > n && mine.t + n < mine.n) {
+            mine.left -= n;
+            mine.t += n;
+        } else {
+            for (int i = 0; i < n && mine.left > 0; ++i)
+                mine.next(p);
+        }
     };
+    auto look_up = [&](int& page, int& row) {   // page -1: no piece; row: its first one in the page
+        page = -1;
+        row = 0;
+        const int tok = mine.t * kMpTok + off;
+        if (mine.left <= 0 || tok >= mine.len)
+            return;
+        const int slot = tok / p.P;
+        row = tok - slot * p.P;
+        page = p.pages[(int64_t)mine.s * p.max_pages + slot];
+        page = page < 0 ? -2 : page;
+    };
+    advance(lane / kPieces);
+    int page, row, page_next, row_next, group = 0;
+    look_up(page, row);
+    advance(kAhead);
+    look_up(page_next, row_next);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         bool got = true;
         if (lane == 0)
             got = wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
         return __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
     };
-    const int R = p.box_rows, boxes = kMpTok / R;
-    uint32_t unit = 0, rope = 0, tile = 0, seg = 0;
-    bool ok = true;
-    int next = page_of(w);
+    uint32_t unit = 0, rope = 0, tile = 0, seg = 0, there = 0;
+    uint32_t at = 0, lap = 0;      // place in the ring
+    bool ok = true, good = false;
     while (w.left > 0 && ok) {
         if (w.fresh) {
             if (seg > 0 && !(ok = wait(&b.q_empty, seg - 1)))
@@ -239,19 +265,23 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
             }
             ++seg;
         }
-        const int page = next, tok0 = w.t * kMpTok, ntok = min(kMpTok, w.len - tok0);
-        const bool in = lane < kMpTok / 16 && 16 * lane < ntok, good = in && page >= 0 && page < p.num_pages;
-        if (in && !good && block == 0)
-            raise_err(p.err, KAMERA_DEVERR_SLOT);
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
+        if (tile % kAhead == 0) {
+            if (tile > 0) {
+                page = page_next;
+                row = row_next;
+                advance(kAhead);
+                look_up(page_next, row_next);
+            }
+            good = page >= 0 && page < p.num_pages;
+            if (page != -1 && !good && block == 0)
+                raise_err(p.err, KAMERA_DEVERR_SLOT);
+            group = (int)(((int64_t)page * p.P + row) >> 3);
+            there = __ballot_sync(0xFFFFFFFFu, good);
+        }
+        const uint32_t mask = (there >> (kPieces * (tile % kAhead))) & 0xFu;
+        const bool box = lane / kPieces == (int)(tile % kAhead) && good && off % R == 0;
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, box));
         w.next(p);
-        if (w.left > 0)
-            next = page_of(w);
-        // box l: rows l R .. l R + R - 1, whose page piece l R / 16 looked up
-        const int off = lane * R, from = __shfl_sync(0xFFFFFFFFu, page, (off / 16) & 31);
-        const bool mine = lane < boxes && off < ntok && ((mask >> (off / 16)) & 1u);
-        const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine));
-        const int group = (int)(((int64_t)from * p.P + (tok0 + off) % p.P) >> 3);
         if (lane == 0)
             b.mask[tile % kMpMasks] = mask;
         auto load = [&](uint32_t dst, uint64_t* bar, const CUtensorMap* map, int col, uint32_t row_group) {
@@ -263,21 +293,24 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
                     ptx::mbar_arrive(full);
             }
             __syncwarp();
-            if (mine && !p.withhold)
+            if (box && !p.withhold)
                 ptx::tma_load_4d(dst + (uint32_t)(off / 8) * row_group, map, 0, 0, col, group, full);
         };
         for (int u = 0; u < kMpUnits && ok; ++u, ++unit) {
-            const uint32_t at = unit % Y::NU, lap = unit / Y::NU;
             if (lap > 0 && !(ok = wait(&b.empty[at], lap - 1)))
                 break;
             load(sbase + Y::kRing + at * kMpUnit, &b.full[at], &L.map_c, 2 * u, 2 * kMpAtom);
+            if (++at == (uint32_t)Y::NU) {
+                at = 0;
+                ++lap;
+            }
         }
         if (!ok)
             break;
-        const uint32_t at = rope % Y::NR, lap = rope / Y::NR;
-        if (lap > 0 && !(ok = wait(&b.rempty[at], lap - 1)))
+        const uint32_t ra = rope % Y::NR, rl = rope / Y::NR;
+        if (rl > 0 && !(ok = wait(&b.rempty[ra], rl - 1)))
             break;
-        load(sbase + Y::kRopes + at * kMpRope, &b.rfull[at], &L.map_r, kMpDim / 64, kMpAtom);
+        load(sbase + Y::kRopes + ra * kMpRope, &b.rfull[ra], &L.map_r, kMpDim / 64, kMpAtom);
         ++rope;
         ++tile;
     }

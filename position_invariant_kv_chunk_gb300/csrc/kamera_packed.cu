@@ -13,10 +13,11 @@
 // exponent of the row's largest (a bf16 number keeps its 8 bits down to 2^-24 of it).
 // The weights are rounded to fp16 (2^-11), as 2^7 times the usual ones, so that small
 // ones stay normal down to 2^-21.
-//   warps 0-3   keys, then softmax (warp w: tokens 32 w .. 32 w + 31), output
-//   warps 4-7   values
-//   warp 8      producer: one bulk copy for 16 tokens of a head, a ring of tiles
-//   warp 9      MMA; it owns TMEM (256 columns, so that two CTAs share an SM: one
+//   warps 0-3   softmax (warp w: tokens 32 w .. 32 w + 31) and output
+//   warps 4-7   keys, two tiles of them in TMEM
+//   warps 8-11  values
+//   warp 12     producer: one bulk copy for 16 tokens of a head, a ring of tiles
+//   warp 13     MMA; it owns TMEM (256 columns, so that two CTAs share an SM: one
 //               decodes while the other waits for its products)
 // Work: the batch's tiles of 128 tokens, all (sequence, KV head) behind one another, in
 // equal ranges, one a CTA; each leaves a partial state for every (sequence, KV head)
@@ -41,8 +42,10 @@ namespace {
 using namespace tc;
 
 constexpr int kP4Tok = 128, kP4Pieces = kP4Tok / 16;
-constexpr int kP4Threads = 320, kP4Prod = 8, kP4Mma = 9;
-constexpr uint32_t kP4TmK = 0, kP4TmV = 64, kP4TmS = 128, kP4TmO = 144, kP4TmCols = 256;
+constexpr int kP4Threads = 448, kP4Keys = 4, kP4Values = 8, kP4Prod = 12, kP4Mma = 13;   // first warps of the roles
+constexpr int kP4Masks = 16;              // tiles whose masks are kept: the ring's and those behind it
+// TMEM columns: two tiles' keys, a tile's values, two tiles' scores, the output
+constexpr uint32_t kP4TmK = 0, kP4TmV = 128, kP4TmS = 192, kP4TmO = 224, kP4TmCols = 256;
 constexpr float kP4Lazy = 8.0f;
 constexpr float kP4Up = 7.0f;             // weights are 2^7 times the usual ones: at most 2^15 with the lazy growth
 constexpr float kP4Log2e = 1.4426950408889634f, kP4Ln2 = 0.6931471805599453f;
@@ -51,11 +54,12 @@ template <int D, int N>
 struct P4Layout {
     static constexpr uint32_t kTile = kP4Pieces * kPackedPiece<D>;
     static constexpr int NS = D == 128 ? 5 : 8;               // tiles in the ring
-    static constexpr uint32_t kQ = 0;                         // [d / 64 blocks][N rows][128 bytes]
-    static constexpr uint32_t kP = kQ + (D / 64) * N * 128;   // [2 blocks of 64 tokens][N rows][128 bytes]
+    static constexpr uint32_t kQ = 0;                         // [2 segments][d / 64 blocks][N rows][128 bytes]
+    static constexpr uint32_t kQSeg = (D / 64) * N * 128;
+    static constexpr uint32_t kP = kQ + 2 * kQSeg;            // [2 blocks of 64 tokens][N rows][128 bytes]
     static constexpr uint32_t kRing = kP + 2 * N * 128;
     static constexpr uint32_t kBar = kRing + NS * kTile;
-    static constexpr uint32_t kBytes = kBar + 512 + 6 * N * 4 + 1024;   // + alignment slack
+    static constexpr uint32_t kBytes = kBar + 512 + 7 * N * 4 + 1024;   // + alignment slack
     static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
     static_assert(kRing % 128 == 0 && kTile % 128 == 0, "copies");
 };
@@ -85,8 +89,8 @@ struct P4Params {
 };
 
 struct P4Bars {
-    uint64_t full[8], empty[8], k_full, v_full, s_full, p_full, pv_done, drained;
-    uint32_t mask[8];              // of a stage's tile: 16-token pieces that are there
+    uint64_t full[8], empty[8], q_full[2], k_full[2], v_full, s_full[2], p_full, pv_done, drained;
+    uint32_t mask[kP4Masks];       // tile t (mod kP4Masks): 16-token pieces that are there
     int64_t total, first_at;
     int32_t first_seq;
     uint32_t tmem;
@@ -120,6 +124,18 @@ struct P4Walk {
         fresh = true;
     }
     __device__ __forceinline__ bool last() const { return t + 1 == n || left == 1; }
+    // to the next segment's first tile (left 0: there is none)
+    __device__ __forceinline__ void skip(const P4Params& p)
+    {
+        const int rest = n - 1 - t;
+        if (left <= rest + 1) {
+            left = 0;
+            return;
+        }
+        left -= rest;
+        t = n - 1;
+        next(p);
+    }
     __device__ __forceinline__ void next(const P4Params& p)
     {
         --left;
@@ -186,38 +202,71 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
 {
     using Y = P4Layout<D, N>;
     const int ppp = p.P / 16;      // pieces of a page
-    P4Walk w;
-    w.start(p, b, lo, hi);
-    auto page_of = [&](const P4Walk& v) {
-        const int piece = v.t * kP4Pieces + lane;
-        return lane < kP4Pieces && 16 * (int64_t)piece < v.len ? p.pages[(int64_t)v.s * p.max_pages + piece / ppp] : -1;
+    // Lane l is at piece l % 8 of tile l / 8 of four tiles, and of the four after them:
+    // pages are looked up, and addresses worked out, for 32 pieces at once and four tiles
+    // ahead.  (Under load a look-up takes 2000 cycles, and a tile's divisions and
+    // look-ups as it came 1900: more than its decoding.)
+    constexpr int kAhead = 32 / kP4Pieces;
+    P4Walk mine;
+    mine.start(p, b, lo, hi);
+    auto advance = [&](int n) {
+        if (mine.left > n && mine.t + n < mine.n) {
+            mine.left -= n;
+            mine.t += n;
+        } else {
+            for (int i = 0; i < n && mine.left > 0; ++i)
+                mine.next(p);
+        }
     };
-    int next = page_of(w);
-    uint32_t k = 0;
-    bool ok = true;
-    for (; w.left > 0; ++k) {
-        const uint32_t at = k % Y::NS, lap = k / Y::NS;
-        const int page = next, piece = w.t * kP4Pieces + lane;
-        const bool in = lane < kP4Pieces && 16 * (int64_t)piece < w.len, good = in && page >= 0 && page < p.num_pages;
-        if (in && !good && w.h == 0)
-            raise_err(p.err, KAMERA_DEVERR_SLOT);
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, good);
-        const unsigned char* src =
-            p.data + (((int64_t)page * p.H + w.h) * ppp + piece % ppp) * (int64_t)kPackedPiece<D>;
-        w.next(p);
-        if (w.left > 0)
-            next = page_of(w);
+    auto look_up = [&](int& page, int64_t& at) {   // page -1: no piece; at: its place in pieces, beside the page's
+        page = -1;
+        at = 0;
+        const int piece = mine.t * kP4Pieces + lane % kP4Pieces;
+        if (mine.left <= 0 || 16 * (int64_t)piece >= mine.len)
+            return;
+        const int slot = piece / ppp;
+        at = ((int64_t)mine.h * ppp + (piece - slot * ppp)) * 2 + (mine.h == 0 ? 1 : 0);
+        page = p.pages[(int64_t)mine.s * p.max_pages + slot];
+        page = page < 0 ? -2 : page;
+    };
+    advance(lane / kP4Pieces);
+    int page, page_next;
+    int64_t place, place_next;
+    look_up(page, place);
+    advance(kAhead);
+    look_up(page_next, place_next);
+    const int64_t page_bytes = (int64_t)p.H * ppp * kPackedPiece<D>;
+    const unsigned char* src = nullptr;
+    bool good = false;
+    uint32_t there = 0;            // the four tiles' pieces that are there
+    const uint32_t n = (uint32_t)(hi - lo);
+    uint32_t k = 0, at = 0, lap = 0;
+    for (; k < n; ++k) {
+        if (k % kAhead == 0) {
+            if (k > 0) {
+                page = page_next;
+                place = place_next;
+                advance(kAhead);
+                look_up(page_next, place_next);
+            }
+            good = page >= 0 && page < p.num_pages;
+            if (page != -1 && !good && (place & 1))   // (once, with the first head)
+                raise_err(p.err, KAMERA_DEVERR_SLOT);
+            src = p.data + page * page_bytes + (place >> 1) * kPackedPiece<D>;
+            there = __ballot_sync(0xFFFFFFFFu, good);
+        }
+        const int mine_now = (int)(k % kAhead);
+        const uint32_t mask = (there >> (kP4Pieces * mine_now)) & 0xFFu;
         if (lap > 0) {
             bool got = true;
             if (lane == 0)
                 got = wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns);
-            ok = __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
-            if (!ok)
+            if (!__shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0))
                 break;
         }
         const uint32_t full = ptx::smem_addr(&b.full[at]);
         if (lane == 0) {
-            b.mask[at] = mask;
+            b.mask[k % kP4Masks] = mask;
             if (!p.withhold) {
                 if (mask)
                     ptx::mbar_arrive_expect_tx(full, __popc(mask) * (uint32_t)kPackedPiece<D>);
@@ -226,8 +275,12 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
             }
         }
         __syncwarp();
-        if (good && !p.withhold)
-            ptx::bulk_g2s(sbase + Y::kRing + at * Y::kTile + lane * kPackedPiece<D>, src, kPackedPiece<D>, full);
+        if (lane / kP4Pieces == mine_now && good && !p.withhold)
+            ptx::bulk_g2s(sbase + Y::kRing + at * Y::kTile + (lane % kP4Pieces) * kPackedPiece<D>, src, kPackedPiece<D>, full);
+        if (++at == (uint32_t)Y::NS) {
+            at = 0;
+            ++lap;
+        }
     }
     // The copies this warp started land before the CTA leaves (without a timeout every
     // one has been waited for).
@@ -254,35 +307,38 @@ __device__ void p4_mma(const P4Params& p, P4Bars& b, uint32_t sbase, uint32_t tm
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
+    uint32_t seg = 0;
+    auto scores = [&](uint32_t t, const P4Walk& v) -> bool {   // of tile t, whose keys are there
+        if ((v.fresh && !wait(&b.q_full[seg & 1u], seg >> 1)) || !wait(&b.k_full[t & 1u], t >> 1))
+            return false;
+        ptx::tc_fence_after();
+        const uint32_t d = tm + kP4TmS + (t & 1u) * 16, k = tm + kP4TmK + (t & 1u) * 64;
+        const uint32_t q = q_lo + (seg & 1u) * (Y::kQSeg >> 4);
+        mma_ts<false>(d, k, q, id);
+#pragma unroll
+        for (int ks = 1; ks < D / 16; ++ks)
+            mma_ts<true>(d, k + 8 * ks, q + (ks >> 2) * (N * 128 >> 4) + 2 * (ks & 3), id);
+        ptx::umma_commit(ptx::smem_addr(&b.s_full[t & 1u]));
+        seg += v.last() ? 1u : 0u;
+        return true;
+    };
     P4Walk w;
     w.start(p, b, lo, hi);
-    for (uint32_t t = 0; w.left > 0; ++t) {
+    bool ok = w.left <= 0 || scores(0, w);
+    for (uint32_t t = 0; ok && w.left > 0; ++t) {
         const bool fresh = w.fresh;
-        if (!wait(&b.k_full, t))
-            break;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t bq = q_lo + (ks >> 2) * (N * 128 >> 4) + 2 * (ks & 3);
-            if (ks == 0)
-                mma_ts<false>(tm + kP4TmS, tm + kP4TmK, bq, id);
-            else
-                mma_ts<true>(tm + kP4TmS, tm + kP4TmK + 8 * ks, bq, id);
-        }
-        ptx::umma_commit(ptx::smem_addr(&b.s_full));
-        if (!wait(&b.v_full, t) || !wait(&b.p_full, t))
-            break;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < kP4Tok / 16; ++ks) {
-            const uint32_t bp = p_lo + (ks >> 2) * (N * 128 >> 4) + 2 * (ks & 3);
-            if (ks == 0 && fresh)
-                mma_ts<false>(tm + kP4TmO, tm + kP4TmV, bp, id);
-            else
-                mma_ts<true>(tm + kP4TmO, tm + kP4TmV + 8 * ks, bp, id);
-        }
-        ptx::umma_commit(ptx::smem_addr(&b.pv_done));
         w.next(p);
+        if (!(ok = w.left <= 0 || scores(t + 1, w)) || !(ok = wait(&b.v_full, t) && wait(&b.p_full, t)))
+            break;
+        ptx::tc_fence_after();
+        if (fresh)
+            mma_ts<false>(tm + kP4TmO, tm + kP4TmV, p_lo, id);
+        else
+            mma_ts<true>(tm + kP4TmO, tm + kP4TmV, p_lo, id);
+#pragma unroll
+        for (int ks = 1; ks < kP4Tok / 16; ++ks)
+            mma_ts<true>(tm + kP4TmO, tm + kP4TmV + 8 * ks, p_lo + (ks >> 2) * (N * 128 >> 4) + 2 * (ks & 3), id);
+        ptx::umma_commit(ptx::smem_addr(&b.pv_done));
     }
     // every MMA issued here completes before TMEM is freed
     ptx::umma_commit(ptx::smem_addr(&b.drained));
@@ -300,22 +356,19 @@ __device__ __forceinline__ void decode_word(uint32_t codes, uint32_t scale2, uin
 
 // Thread = channel c: the tile's 128 tokens into the columns of its TMEM lane.
 template <int D, int N>
-__device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* ring, uint32_t tm, int warp, int lane,
-                          int64_t lo, int64_t hi)
+__device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* ring, uint32_t tm, int warp, int lane, int64_t n)
 {
     using Y = P4Layout<D, N>;
     const int c = 32 * warp + lane;
     const uint32_t tV = tm + ((uint32_t)warp << 21) + kP4TmV;
-    P4Walk w;
-    w.start(p, b, lo, hi);
     bool ok = true;
-    for (uint32_t t = 0; w.left > 0; ++t, w.next(p)) {
+    for (uint32_t t = 0; t < n; ++t) {
         const uint32_t at = t % Y::NS;
         ok = wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
         if (!__all_sync(0xFFFFFFFFu, ok))
             return;
         const unsigned char* tile = ring + at * Y::kTile;
-        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[at]);
+        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[t % kP4Masks]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {   // four pieces, 32 columns
             uint32_t v[32];
@@ -325,8 +378,9 @@ __device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* rin
                     const int piece = 4 * half + i;
                     const unsigned char* rec = tile + piece * kPackedPiece<D>;
                     const uint2 codes = *reinterpret_cast<const uint2*>(rec + kPackedV<D> + 8 * c);
-                    // a piece that is not there: zero, so that zero weights add nothing
-                    const uint32_t s = (mask >> piece) & 1u ? rec[kPackedVS<D> + c] * 0x00800080u : 0u;
+                    uint32_t s = rec[kPackedVS<D> + c] * 0x00800080u;
+                    if (mask != 0xFFu && !((mask >> piece) & 1u))
+                        s = 0u;   // a piece that is not there: zero, so that zero weights add nothing
                     decode_word(codes.x, s, v + 8 * i);
                     decode_word(codes.y, s, v + 8 * i + 4);
                 }
@@ -347,7 +401,7 @@ __device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* rin
     }
 }
 
-// -------------------------------------------------------- keys and softmax --
+// -------------------------------------------------------- keys, softmax --
 __device__ __forceinline__ void p4_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 // The four warps meet; whether any thread said yes.
 __device__ __forceinline__ bool p4_any(bool x)
@@ -418,9 +472,8 @@ __device__ __forceinline__ void p4_stsm_x4_t(uint32_t a, const uint32_t (&x)[4])
 // of two that takes its largest entry to [2^10, 2^11); what a score is to be multiplied
 // with (log2 units) into fs.  Rows past the heads are zero.
 template <int D, int N>
-__device__ __forceinline__ void p4_stage_q(const P4Params& p, uint32_t sbase, float* fs, int s, int h, int warp, int lane)
+__device__ __forceinline__ void p4_stage_q(const P4Params& p, uint32_t q_smem, float* fs, int s, int h, int warp, int lane)
 {
-    using Y = P4Layout<D, N>;
     constexpr int V = D / 32;      // channels of a lane
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
@@ -442,7 +495,7 @@ __device__ __forceinline__ void p4_stage_q(const P4Params& p, uint32_t sbase, fl
         if (lane == 0)   // K is held at 2^-8 of its value
             fs[r] = p.scale * kP4Log2e * p.k_unit * (__uint_as_float((uint32_t)(127 + ec) << 23) * 0.25f);
         const int ch = V * lane;
-        const uint32_t dst = sbase + Y::kQ + (ch >> 6) * (N * 128) + (r >> 3) * 1024 + sw128(r & 7, (ch & 63) >> 3) +
+        const uint32_t dst = q_smem + (ch >> 6) * (N * 128) + (r >> 3) * 1024 + sw128(r & 7, (ch & 63) >> 3) +
                              (ch & 7) * 2;
 #pragma unroll
         for (int j = 0; j < V; j += 2) {
@@ -452,9 +505,55 @@ __device__ __forceinline__ void p4_stage_q(const P4Params& p, uint32_t sbase, fl
     }
 }
 
+// Thread = token of the tile: its keys into the columns of its TMEM lane.
 template <int D, int N>
-__device__ void p4_softmax(const P4Params& p, P4Bars& b, const unsigned char* ring, uint32_t sbase, float* ex, uint32_t tm,
-                           int warp, int lane, int range, int64_t lo, int64_t hi)
+__device__ void p4_keys(const P4Params& p, P4Bars& b, const unsigned char* ring, uint32_t tm, int warp, int lane, int64_t n)
+{
+    using Y = P4Layout<D, N>;
+    const int tok = 32 * warp + lane;
+    const uint32_t tK = tm + ((uint32_t)warp << 21) + kP4TmK;
+    for (uint32_t t = 0; t < n; ++t) {
+        const uint32_t at = t % Y::NS;
+        bool ok = wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
+        if (t >= 2)   // the keys of two tiles before have been scored
+            ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), ((t >> 1) - 1) & 1u, &b.abort, p.err, p.wait_ns);
+        if (!__all_sync(0xFFFFFFFFu, ok))
+            return;
+        ptx::tc_fence_after();
+        const unsigned char* rec = ring + at * Y::kTile + (tok >> 4) * kPackedPiece<D>;
+        uint32_t sc[D / 64];
+        const unsigned char* ss = rec + kPackedKS<D> + (tok & 15) * (D / 16);
+        if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(ss);
+            sc[0] = x.x, sc[1] = x.y;
+        } else {
+            sc[0] = *reinterpret_cast<const uint32_t*>(ss);
+        }
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {   // 64 channels, 32 columns
+            uint32_t x[32];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint4 c = *reinterpret_cast<const uint4*>(rec + (2 * half + j) * 256 + (tok & 15) * 16);
+                const uint32_t s0 = ((sc[half] >> (16 * j)) & 0xFFu) * 0x00800080u;
+                const uint32_t s1 = ((sc[half] >> (16 * j + 8)) & 0xFFu) * 0x00800080u;
+                decode_word(c.x, s0, x + 16 * j);
+                decode_word(c.y, s0, x + 16 * j + 4);
+                decode_word(c.z, s1, x + 16 * j + 8);
+                decode_word(c.w, s1, x + 16 * j + 12);
+            }
+            tmem_st32(tK + (t & 1u) * 64 + 32 * half, x);
+        }
+        ptx::mbar_arrive(ptx::smem_addr(&b.empty[at]));
+        tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(ptx::smem_addr(&b.k_full[t & 1u]));
+    }
+}
+
+template <int D, int N>
+__device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* ex, uint32_t tm, int warp, int lane,
+                           int range, int64_t lo, int64_t hi)
 {
     using Y = P4Layout<D, N>;
     constexpr int J = N / 8;
@@ -463,71 +562,52 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, const unsigned char* ri
     const int64_t T = b.total, R = min((int64_t)p.ranges, T);
     float* wmax = ex;              // [4 warps][N]
     float* fac = ex + 4 * N;       // [N]
-    float* fs = ex + 5 * N;        // [N]: scores' factors
+    float* fs = ex + 5 * N;        // [2 segments][N]: scores' factors
     float m[J][2], l[J][2], f2[J][2];
     const uint32_t st = sbase + Y::kP + (warp >> 1) * (N * 128) + sw128(lane & 7, 4 * (warp & 1) + (lane >> 3));
+    bool ok = true;
+    uint32_t seg = 0;              // segments whose queries are staged
+    // Segment i's queries, staged as segment i - 1 starts: what stood there, of segment
+    // i - 2, has been scored.
+    auto stage = [&](const P4Walk& v) {
+        p4_stage_q<D, N>(p, sbase + Y::kQ + (seg & 1u) * Y::kQSeg, fs + (seg & 1u) * N, v.s, v.h, warp, lane);
+        ptx::fence_proxy_async();
+        ptx::mbar_arrive(ptx::smem_addr(&b.q_full[seg & 1u]));
+        ++seg;
+    };
     P4Walk w;
     w.start(p, b, lo, hi);
+    if (w.left > 0)
+        stage(w);
+    p4_sync();
     int64_t at_tile = lo;
-    bool ok = true;
     for (uint32_t t = 0; w.left > 0; ++t, ++at_tile) {
         if (w.fresh) {
-            p4_stage_q<D, N>(p, sbase, fs, w.s, w.h, warp, lane);   // the products before have been waited for
-            p4_sync();
+            const float* from = fs + ((seg - 1) & 1u) * N;   // (a barrier lies behind their staging)
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     m[j][c] = -INFINITY;
                     l[j][c] = 0.f;
-                    f2[j][c] = fs[8 * j + 2 * t4 + c];
+                    f2[j][c] = from[8 * j + 2 * t4 + c];
                 }
+            P4Walk next = w;
+            next.skip(p);
+            if (next.left > 0)
+                stage(next);
         }
-        const uint32_t at = t % Y::NS;
-        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_ns);
+        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[at]);
-        if (ok) {   // this token's keys (the scores before have been read: their product is done with TMEM)
-            const unsigned char* rec = ring + at * Y::kTile + (tok >> 4) * kPackedPiece<D>;
-            uint32_t sc[D / 64];
-            const unsigned char* ss = rec + kPackedKS<D> + (tok & 15) * (D / 16);
-            if constexpr (D == 128) {
-                const uint2 x = *reinterpret_cast<const uint2*>(ss);
-                sc[0] = x.x, sc[1] = x.y;
-            } else {
-                sc[0] = *reinterpret_cast<const uint32_t*>(ss);
-            }
-#pragma unroll
-            for (int half = 0; half < D / 64; ++half) {   // 64 channels, 32 columns
-                uint32_t v[32];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(rec + (2 * half + j) * 256 + (tok & 15) * 16);
-                    const uint32_t s0 = ((sc[half] >> (16 * j)) & 0xFFu) * 0x00800080u;
-                    const uint32_t s1 = ((sc[half] >> (16 * j + 8)) & 0xFFu) * 0x00800080u;
-                    decode_word(x.x, s0, v + 16 * j);
-                    decode_word(x.y, s0, v + 16 * j + 4);
-                    decode_word(x.z, s1, v + 16 * j + 8);
-                    decode_word(x.w, s1, v + 16 * j + 12);
-                }
-                tmem_st32(lanes + kP4TmK + 32 * half, v);
-            }
-            ptx::mbar_arrive(ptx::smem_addr(&b.empty[at]));
-            tmem_wait_st();
-            ptx::fence_proxy_async();   // the queries
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(ptx::smem_addr(&b.k_full));
-            ok = wmma16::cycle_wait(ptx::smem_addr(&b.s_full), t & 1u, &b.abort, p.err, p.wait_ns);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-        }
+        const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[t % kP4Masks]);
         const int ntok = min(kP4Tok, w.len - w.t * kP4Tok);
         bool grew = false;
         float x[2][J][4];   // half of the warp's tokens; [j][2 r + c]
         if (ok) {
             ptx::tc_fence_after();
             uint32_t s[2][4 * J];
-            p4_ld_scores<N>(lanes + kP4TmS, s[0]);
-            p4_ld_scores<N>(lanes + kP4TmS + (16u << 16), s[1]);
+            p4_ld_scores<N>(lanes + kP4TmS + (t & 1u) * 16, s[0]);
+            p4_ld_scores<N>(lanes + kP4TmS + (t & 1u) * 16 + (16u << 16), s[1]);
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -689,9 +769,12 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
             ptx::mbar_init(ptx::smem_addr(&b.full[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&b.empty[i]), 256);
         }
-        ptx::mbar_init(ptx::smem_addr(&b.k_full), 128);
         ptx::mbar_init(ptx::smem_addr(&b.v_full), 128);
-        ptx::mbar_init(ptx::smem_addr(&b.s_full), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&b.q_full[i]), 128);
+            ptx::mbar_init(ptx::smem_addr(&b.k_full[i]), 128);
+            ptx::mbar_init(ptx::smem_addr(&b.s_full[i]), 1);
+        }
         ptx::mbar_init(ptx::smem_addr(&b.p_full), 4);
         ptx::mbar_init(ptx::smem_addr(&b.pv_done), 1);
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
@@ -718,10 +801,12 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
     const int64_t T = b.total, R = min((int64_t)p.ranges, T);
     if (range < R) {   // (else: fewer tiles than ranges)
         const int64_t lo = p4_start(range, T, R), hi = p4_start(range + 1, T, R);
-        if (warp < 4)
-            p4_softmax<D, N>(p, b, ring, sbase, ex, tm, warp, lane, range, lo, hi);
-        else if (warp < 8)
-            p4_values<D, N>(p, b, ring, tm, warp - 4, lane, lo, hi);
+        if (warp < kP4Keys)
+            p4_softmax<D, N>(p, b, sbase, ex, tm, warp, lane, range, lo, hi);
+        else if (warp < kP4Values)
+            p4_keys<D, N>(p, b, ring, tm, warp - kP4Keys, lane, hi - lo);
+        else if (warp < kP4Prod)
+            p4_values<D, N>(p, b, ring, tm, warp - kP4Values, lane, hi - lo);
         else if (warp == kP4Prod)
             p4_producer<D, N>(p, b, sbase, lane, lo, hi);
         else if (p4_elect())
@@ -740,16 +825,20 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
 
 // ------------------------------------------------------------------- merge --
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a row's packed and tail
-// states.  A warp a row; the lanes work out the weights of 32 states at a time.
+// states.  All latency: a CTA a row, warp w takes every fourth state; a warp's outputs
+// are asked for eight at a time before their weights are known, and the lanes work out
+// the weights of 32 states at once; the four warps' sums join in order.
 constexpr int kP4MergeWarps = 4;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const P4Params p)
 {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * kP4MergeWarps + (threadIdx.x >> 5), rows = (int64_t)p.n_seqs * p.H * p.G;
-    const int unit = (int)(min(row, rows - 1) / p.G), g = (int)(min(row, rows - 1) - (int64_t)unit * p.G), s = unit / p.H;
+    constexpr int V = D / 32, PW = 32 / kP4MergeWarps;
+    __shared__ float part[kP4MergeWarps][D];
+    __shared__ float sum;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x, unit = row / p.G, g = row - unit * p.G, s = unit / p.H;
+    // what the call was given, while the kernels before may still run
     int n_tail = 0;
     if (p.tail_slots > 0) {
         const int len = p.tail_lens[s];
@@ -758,8 +847,6 @@ __global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const 
     const bool some = p.max_len > 0 && p4_len(p, s) > 0;
     ptx::grid_wait();
     ptx::grid_launch_next();
-    if (row >= rows)
-        return;
     int n_packed = 0;
     int4 sp = make_int4(0, 0, 0, 0);
     if (some) {
@@ -768,14 +855,33 @@ __global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const 
         if (sp.x >= 0 && sp.y >= sp.x && sp.y < p.ranges && (sp.z >> 1) == sp.x)
             n_packed = sp.y - sp.x + 1;
     }
-    auto packed_at = [&](int i) {
-        const int64_t slot = sp.x == sp.y ? 2 * (int64_t)p.ranges + unit : i == 0 ? sp.z : 2 * (sp.x + i);
-        return slot * p.G + g;
-    };
     const int n = n_packed + n_tail;
+    auto at = [&](int i) -> int64_t {
+        if (i >= n_packed)
+            return (int64_t)row * p.tail_slots + i - n_packed;
+        return (sp.x == sp.y ? 2 * (int64_t)p.ranges + unit : i == 0 ? sp.z : 2 * (sp.x + i)) * p.G + g;
+    };
+    float x[PW][V];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < PW; ++k) {
+            const int i = i0 + kP4MergeWarps * k + warp;
+            if (i >= n)
+                continue;
+            const float* src = (i < n_packed ? p.o : p.tail_o) + at(i) * D + V * lane;
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(src);
+                x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(src);
+                x[k][0] = y.x, x[k][1] = y.y;
+            }
+        }
+    };
+    load(0);
     float m = -INFINITY;
     for (int i = lane; i < n; i += 32)
-        m = fmaxf(m, i < n_packed ? p.ml[packed_at(i)].x : p.tail_ml[row * p.tail_slots + i - n_packed].x);
+        m = fmaxf(m, (i < n_packed ? p.ml : p.tail_ml)[at(i)].x);
 #pragma unroll
     for (int d = 16; d >= 1; d /= 2)
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
@@ -784,46 +890,52 @@ __global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const 
     for (int v = 0; v < V; ++v)
         acc[v] = 0.f;
     for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        float f = 0.f;
-        const float* src = p.o;
-        if (i < n) {
-            const bool pk = i < n_packed;
-            const int64_t at = pk ? packed_at(i) : row * p.tail_slots + i - n_packed;
-            const float2 y = pk ? p.ml[at] : p.tail_ml[at];
-            src = (pk ? p.o : p.tail_o) + at * D;
-            if (y.y != 0.f) {   // a state without weight adds nothing (and has no maximum to scale by)
+        if (i0 > 0)
+            load(i0);
+        float f = 0.f;   // a state without weight adds nothing (and has no maximum to scale by)
+        bool live = false;
+        if (i0 + lane < n) {
+            const float2 y = (i0 + lane < n_packed ? p.ml : p.tail_ml)[at(i0 + lane)];
+            live = y.y != 0.f;
+            if (live) {
                 f = pf_ex2(y.x - m);
                 l = fmaf(y.y, f, l);
             }
         }
-        const uint32_t live = __ballot_sync(0xFFFFFFFFu, f != 0.f || f != f);
-#pragma unroll 4
-        for (int k = 0; k < min(32, n - i0); ++k) {
-            const float x = __shfl_sync(0xFFFFFFFFu, f, k);
-            const float* o = reinterpret_cast<const float*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(src), k)) + V * lane;
-            if (!((live >> k) & 1u))
-                continue;
-            if constexpr (V == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(o);
-                acc[0] = fmaf(y.x, x, acc[0]), acc[1] = fmaf(y.y, x, acc[1]);
-                acc[2] = fmaf(y.z, x, acc[2]), acc[3] = fmaf(y.w, x, acc[3]);
-            } else {
-                const float2 y = *reinterpret_cast<const float2*>(o);
-                acc[0] = fmaf(y.x, x, acc[0]), acc[1] = fmaf(y.y, x, acc[1]);
-            }
+        const uint32_t any = __ballot_sync(0xFFFFFFFFu, live);
+#pragma unroll
+        for (int k = 0; k < PW; ++k) {
+            const int j = kP4MergeWarps * k + warp;
+            const float y = __shfl_sync(0xFFFFFFFFu, f, j);
+            if ((any >> j) & 1u)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    acc[v] = fmaf(x[k][v], y, acc[v]);
         }
     }
+    if (warp == 0) {
 #pragma unroll
-    for (int d = 16; d >= 1; d /= 2)
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        for (int d = 16; d >= 1; d /= 2)
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        if (lane == 0)
+            sum = l;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        part[warp][V * lane + v] = acc[v];
+    __syncthreads();
+    l = sum;
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    if constexpr (V == 4)
-        *reinterpret_cast<uint2*>(p.out + row * D + 4 * lane) =
-            make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t*>(p.out + row * D + 2 * lane) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && p.lse)
+    for (int i = 2 * threadIdx.x; i < D; i += 64 * kP4MergeWarps) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int w = 0; w < kP4MergeWarps; ++w) {
+            a += part[w][i];
+            b += part[w][i + 1];
+        }
+        *reinterpret_cast<uint32_t*>(p.out + (int64_t)row * D + i) = pack_bf16x2(a * inv, b * inv);
+    }
+    if (threadIdx.x == 0 && p.lse)
         p.lse[row] = l > 0.f ? (m + log2f(l)) * kP4Ln2 : (l == l ? -INFINITY : l);
 }
 
@@ -1014,7 +1126,7 @@ int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery*
         if (ce != cudaSuccess)
             return KAMERA_ERR_CUDA;
     }
-    const dim3 grid((unsigned)((rows + kP4MergeWarps - 1) / kP4MergeWarps));
+    const dim3 grid((unsigned)rows);
     ce = d == 128 ? launch_after(packed_merge_kernel<128>, grid, 32 * kP4MergeWarps, 0, stream, true, p)
                   : launch_after(packed_merge_kernel<64>, grid, 32 * kP4MergeWarps, 0, stream, true, p);
     return ce == cudaSuccess ? KAMERA_OK : KAMERA_ERR_CUDA;
