@@ -168,12 +168,15 @@ struct MpWalk {
     }
 };
 
-// Total tiles and the sequence in which the range starts, by one warp.
+// Total tiles and the sequence in which the range starts, by one warp: one look at the
+// lengths of up to 32 sequences, two at those of more.
 __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
 {
-    int64_t sum = 0;
-    for (int s = lane; s < p.n_seqs; s += 32)
-        sum += mp_tiles(mp_len(p, s));
+    auto tiles = [&](int s) { return s < p.n_seqs ? (int64_t)mp_tiles(mp_len(p, s)) : 0; };
+    const int64_t first = tiles(lane);
+    int64_t sum = first;
+    for (int s = lane + 32; s < p.n_seqs; s += 32)
+        sum += tiles(s);
 #pragma unroll
     for (int d = 16; d >= 1; d /= 2)
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
@@ -186,7 +189,7 @@ __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
     }
     __syncwarp();
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-        const int s = s0 + lane, mine = s < p.n_seqs ? mp_tiles(mp_len(p, s)) : 0;
+        const int64_t mine = s0 == 0 ? first : tiles(s0 + lane);
         int64_t x = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -196,7 +199,7 @@ __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
         }
         const int64_t before = at + x - mine;
         if (mine > 0 && before <= lo && lo < before + mine) {
-            b.first_seq = s;
+            b.first_seq = s0 + lane;
             b.first_at = before;
         }
         at += __shfl_sync(0xFFFFFFFFu, x, 31);

@@ -15,8 +15,10 @@
 // kernels take, would be 40% more MMAs here, where they are the bound.
 //   warps 0-3, 4-7  softmax of side A, B: thread = query = TMEM lane; running maximum
 //                   with lazy rescaling (only when it grows by more than 2^8)
-//   warp 8          producer: 128B-swizzled TMA boxes of 64 columns x 128 rows into a
-//                   ring of eight 16 KB units (a tile is three of keys, two of values)
+//   warp 8          producer: 128B-swizzled TMA boxes of 64 columns into a ring of eight
+//                   16 KB units: a tile is three of keys (64 columns x 128 rows) and two
+//                   of values (128 columns x 64 rows, so that an MMA takes N = 128 from
+//                   one unit: 67 cycles, where two of N = 64 take 100)
 //   warp 10         MMA; it owns TMEM (warps 9, 11 idle: registers are moved between
 //                   whole warpgroups)
 // Blocks of queries with the most rows to see start first.  Every wait is bounded.
@@ -69,7 +71,7 @@ struct PrParams {
 
 struct PrLaunch {
     PrParams p;
-    CUtensorMap map_q, map_kv, map_r;
+    CUtensorMap map_q, map_k, map_v, map_r;
 };
 
 struct PrBars {
@@ -153,10 +155,15 @@ __device__ void pr_producer(const PrLaunch& L, const PrWork& w, PrBars& b, uint3
             ptx::mbar_arrive_expect_tx(full, kPrUnit);
             const uint32_t dst = sbase + kPrRing + at * kPrUnit;
             const int row = w.k0 + t * kPrTok;
-            if (u == 2)
+            const int col = w.h * (kPrNope + kPrV);
+            if (u < 2) {
+                ptx::tma_load_2d(dst, &L.map_k, col + 64 * u, row, full);
+            } else if (u == 2) {
                 ptx::tma_load_2d(dst, &L.map_r, 0, row, full);
-            else   // key columns 0, 64, value columns 128, 192 of the head
-                ptx::tma_load_2d(dst, &L.map_kv, w.h * (kPrNope + kPrV) + 64 * (u > 2 ? u - 1 : u), row, full);
+            } else {
+                ptx::tma_load_2d(dst, &L.map_v, col + kPrNope, row + 64 * (u - 3), full);
+                ptx::tma_load_2d(dst + kPrUnit / 2, &L.map_v, col + kPrNope + 64, row + 64 * (u - 3), full);
+            }
         }
     // Without a timeout the MMA lane has waited for every fill.  After one, the copies
     // started here land before the CTA leaves.
@@ -182,7 +189,7 @@ __device__ void pr_mma(const PrLaunch& L, const PrWork& w, PrBars& b, uint32_t s
 {
     const PrParams& p = L.p;
     constexpr uint32_t idS = ptx::idesc_bf16_f32(kPrRows, kPrTok);
-    constexpr uint32_t idV = ptx::idesc_bf16_f32(kPrRows, 64) | (1u << 16);   // value rows: MN-major
+    constexpr uint32_t idV = ptx::idesc_bf16_f32(kPrRows, kPrV) | (1u << 16);   // value rows: MN-major
     const uint32_t q_lo = ((sbase + kPrQ) >> 4) | (1u << 16), r_lo = (sbase + kPrRing) >> 4;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
@@ -218,23 +225,19 @@ __device__ void pr_mma(const PrLaunch& L, const PrWork& w, PrBars& b, uint32_t s
         const uint32_t k = (uint32_t)(kPrTile * t + 3), at0 = k % kPrUnits, at1 = (k + 1) % kPrUnits;
         if (!wait(&b.full[at0], k / kPrUnits) || !wait(&b.full[at1], (k + 1) / kPrUnits))
             return false;
-        const uint32_t v0 = (r_lo + at0 * (kPrUnit >> 4)) | (1u << 16), v1 = (r_lo + at1 * (kPrUnit >> 4)) | (1u << 16);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {   // the first 64 tokens while the others' weights are computed
             if (!wait(&b.p_full[a][half], t))
                 return false;
             ptx::tc_fence_after();
+            // 64 columns are 8 KB from the next 64, 16 tokens 2 KB from the next 16
+            const uint32_t v = (r_lo + (half ? at1 : at0) * (kPrUnit >> 4)) | ((kPrUnit / 2 >> 4) << 16);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int ks = 4 * half + i;
-                if (ks == 0 && t == 0) {
-                    mma_ts<false>(dO, aP, v0, idV);
-                    mma_ts<false>(dO + 64, aP, v1, idV);
-                } else {
-                    mma_ts<true>(dO, aP + 8 * ks, v0 + 128 * ks, idV);
-                    mma_ts<true>(dO + 64, aP + 8 * ks, v1 + 128 * ks, idV);
-                }
-            }
+            for (int i = 0; i < 4; ++i)
+                if (half == 0 && i == 0 && t == 0)
+                    mma_ts<false>(dO, aP, v, idV);
+                else
+                    mma_ts<true>(dO, aP + 8 * (4 * half + i), v + 128 * i, idV);
         }
         ptx::umma_commit(ptx::smem_addr(&b.pv_done[a]));
         if (a == 1 || t >= w.tiles_b) {
@@ -373,9 +376,9 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
                                              p.err, p.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok && in);
             for (int i = r; i < (base + kPrTok - w.nk) * 16; i += kPrRows) {
-                const int row = w.nk - base + (i >> 4), u = (i >> 3) & 1;
-                ptx::st_shared_zero16(sbase + kPrRing + (k + u) % kPrUnits * kPrUnit + (uint32_t)(row >> 3) * 1024u +
-                                      sw128(row & 7, i & 7));
+                const int row = w.nk - base + (i >> 4), in_unit = row & 63;
+                ptx::st_shared_zero16(sbase + kPrRing + (k + (row >> 6)) % kPrUnits * kPrUnit + ((i >> 3) & 1) * (kPrUnit / 2) +
+                                      (uint32_t)(in_unit >> 3) * 1024u + sw128(in_unit & 7, i & 7));
             }
             ptx::fence_proxy_async();   // (the product waits for every thread's weights, which follow)
         }
@@ -571,7 +574,7 @@ int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct 
     const void* kr = x->n_kv > 0 ? x->k_rope : x->q;
     const int64_t rows = std::max(x->n_kv, 1);
     if (!make_heads_map(&L.map_q, x->q, x->n_q, H, kPrQk, qt, qh, 64, kPrRows) ||
-        !make_rows_map(&L.map_kv, kv, rows, kvw, kt, 64, kPrTok) ||
+        !make_rows_map(&L.map_k, kv, rows, kvw, kt, 64, kPrTok) || !make_rows_map(&L.map_v, kv, rows, kvw, kt, 64, 64) ||
         !make_rows_map(&L.map_r, kr, rows, kPrQk - kPrNope, rt, 64, kPrTok))
         return KAMERA_ERR_CUDA;
     // set at every launch: the attribute belongs to the current device's context

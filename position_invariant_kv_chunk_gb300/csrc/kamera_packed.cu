@@ -155,16 +155,19 @@ struct P4Walk {
     }
 };
 
-// Total tiles and the sequence in which the range starts, by one warp.
+// Total tiles and the sequence in which the range starts, by one warp: one look at the
+// lengths of up to 32 sequences, two at those of more.
 __device__ void p4_locate(const P4Params& p, P4Bars& b, int r, int lane)
 {
-    int64_t sum = 0;
-    for (int s = lane; s < p.n_seqs; s += 32)
-        sum += p4_tiles(p4_len(p, s));
+    auto tiles = [&](int s) { return s < p.n_seqs ? (int64_t)p4_tiles(p4_len(p, s)) * p.H : 0; };
+    const int64_t first = tiles(lane);
+    int64_t sum = first;
+    for (int s = lane + 32; s < p.n_seqs; s += 32)
+        sum += tiles(s);
 #pragma unroll
     for (int d = 16; d >= 1; d /= 2)
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    const int64_t T = sum * p.H;
+    const int64_t T = sum;
     if (lane == 0) {
         b.total = T;
         b.first_seq = 0;
@@ -176,8 +179,7 @@ __device__ void p4_locate(const P4Params& p, P4Bars& b, int r, int lane)
     const int64_t lo = p4_start(r, T, min((int64_t)p.ranges, T));
     int64_t at = 0;
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-        const int s = s0 + lane;
-        const int64_t mine = s < p.n_seqs ? (int64_t)p4_tiles(p4_len(p, s)) * p.H : 0;
+        const int64_t mine = s0 == 0 ? first : tiles(s0 + lane);
         int64_t x = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -187,7 +189,7 @@ __device__ void p4_locate(const P4Params& p, P4Bars& b, int r, int lane)
         }
         const int64_t before = at + x - mine;
         if (mine > 0 && before <= lo && lo < before + mine) {
-            b.first_seq = s;
+            b.first_seq = s0 + lane;
             b.first_at = before;
         }
         at += __shfl_sync(0xFFFFFFFFu, x, 31);
@@ -825,16 +827,16 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
 
 // ------------------------------------------------------------------- merge --
 // out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over a row's packed and tail
-// states.  All latency: a CTA a row, warp w takes every fourth state; a warp's outputs
+// states.  All latency: a CTA a row, warp w takes every NW-th state; a warp's outputs
 // are asked for eight at a time before their weights are known, and the lanes work out
-// the weights of 32 states at once; the four warps' sums join in order.
-constexpr int kP4MergeWarps = 4;
-
-template <int D>
-__global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const P4Params p)
+// the weights of 32 states at once; the warps' sums join in order.  16 warps where a row
+// may have many states (77 of 28 rows: 6 us less than with four), four where the rows
+// are many.
+template <int D, int NW>
+__global__ void __launch_bounds__(32 * NW) packed_merge_kernel(const P4Params p)
 {
-    constexpr int V = D / 32, PW = 32 / kP4MergeWarps;
-    __shared__ float part[kP4MergeWarps][D];
+    constexpr int V = D / 32, PW = 8, SW = NW / 4;   // a round: eight states a warp, SW a lane
+    __shared__ float part[NW][D];
     __shared__ float sum;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x, unit = row / p.G, g = row - unit * p.G, s = unit / p.H;
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const 
     auto load = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < PW; ++k) {
-            const int i = i0 + kP4MergeWarps * k + warp;
+            const int i = i0 + NW * k + warp;
             if (i >= n)
                 continue;
             const float* src = (i < n_packed ? p.o : p.tail_o) + at(i) * D + V * lane;
@@ -889,25 +891,32 @@ __global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const 
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
+    for (int i0 = 0; i0 < n; i0 += PW * NW) {
         if (i0 > 0)
             load(i0);
-        float f = 0.f;   // a state without weight adds nothing (and has no maximum to scale by)
-        bool live = false;
-        if (i0 + lane < n) {
-            const float2 y = (i0 + lane < n_packed ? p.ml : p.tail_ml)[at(i0 + lane)];
-            live = y.y != 0.f;
-            if (live) {
-                f = pf_ex2(y.x - m);
-                l = fmaf(y.y, f, l);
+        float f[SW];   // lane's states i0 + 32 c + lane; one without weight adds nothing (and has no maximum to scale by)
+        uint32_t any[SW];
+#pragma unroll
+        for (int c = 0; c < SW; ++c) {
+            const int i = i0 + 32 * c + lane;
+            f[c] = 0.f;
+            bool live = false;
+            if (i < n) {
+                const float2 y = (i < n_packed ? p.ml : p.tail_ml)[at(i)];
+                live = y.y != 0.f;
+                if (live) {
+                    f[c] = pf_ex2(y.x - m);
+                    l = fmaf(y.y, f[c], l);
+                }
             }
+            any[c] = __ballot_sync(0xFFFFFFFFu, live);
         }
-        const uint32_t any = __ballot_sync(0xFFFFFFFFu, live);
 #pragma unroll
         for (int k = 0; k < PW; ++k) {
-            const int j = kP4MergeWarps * k + warp;
-            const float y = __shfl_sync(0xFFFFFFFFu, f, j);
-            if ((any >> j) & 1u)
+            const int j = NW * k + warp;   // of the round's states
+            const int c = (NW * k) / 32;
+            const float y = __shfl_sync(0xFFFFFFFFu, f[c], j & 31);
+            if ((any[c] >> (j & 31)) & 1u)
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     acc[v] = fmaf(x[k][v], y, acc[v]);
@@ -926,10 +935,10 @@ __global__ void __launch_bounds__(32 * kP4MergeWarps) packed_merge_kernel(const 
     __syncthreads();
     l = sum;
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    for (int i = 2 * threadIdx.x; i < D; i += 64 * kP4MergeWarps) {
+    for (int i = 2 * threadIdx.x; i < D; i += 64 * NW) {
         float a = 0.f, b = 0.f;
 #pragma unroll
-        for (int w = 0; w < kP4MergeWarps; ++w) {
+        for (int w = 0; w < NW; ++w) {
             a += part[w][i];
             b += part[w][i + 1];
         }
@@ -1127,8 +1136,13 @@ int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery*
             return KAMERA_ERR_CUDA;
     }
     const dim3 grid((unsigned)rows);
-    ce = d == 128 ? launch_after(packed_merge_kernel<128>, grid, 32 * kP4MergeWarps, 0, stream, true, p)
-                  : launch_after(packed_merge_kernel<64>, grid, 32 * kP4MergeWarps, 0, stream, true, p);
+    const bool many = p.ranges >= 8ll * p.n_seqs * p.H;   // states of a row on average: a range ends in each but the last
+    if (d == 128)
+        ce = many ? launch_after(packed_merge_kernel<128, 16>, grid, 512, 0, stream, true, p)
+                  : launch_after(packed_merge_kernel<128, 4>, grid, 128, 0, stream, true, p);
+    else
+        ce = many ? launch_after(packed_merge_kernel<64, 16>, grid, 512, 0, stream, true, p)
+                  : launch_after(packed_merge_kernel<64, 4>, grid, 128, 0, stream, true, p);
     return ce == cudaSuccess ? KAMERA_OK : KAMERA_ERR_CUDA;
 }
 
