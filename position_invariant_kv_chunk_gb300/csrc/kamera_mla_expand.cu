@@ -4,15 +4,18 @@
 // A matrix product, [tokens x 512] [512 x heads 256], whose left rows lie at pool slots.
 // 2 x 512 flops a value written (2 bytes): bound by the tensor cores from some hundred
 // tokens on.  A CTA holds the latent parts of 128 tokens in shared memory (128 KB,
-// gathered once) and runs heads past them: a head's weights come in eight 32 KB chunks
-// of 64 columns through a ring of three, and its 128 x 256 sums stand in one of two TMEM
-// halves while the epilogue empties the other.
-//   warps 0-3  epilogue: thread = token = TMEM lane, 32-byte stores (whole sectors)
+// gathered once) and runs heads past them: a head's weights come in sixteen 16 KB chunks
+// of 32 columns through a ring of five, and its 128 x 256 sums stand in one of two TMEM
+// halves while the epilogue empties the other, 64 columns at a time through shared memory
+// and a TMA store (rows stored from the registers, 32 bytes a lane, took 6000 cycles a
+// head, half more than its MMAs).
+//   warps 0-3  epilogue: thread = token = TMEM lane
 //   warp 4     producer of the weights (TMA)
 //   warp 5     MMA (M 128, N 256); it owns TMEM
 //   warps 6-9  gather of the tokens' rows: 16-byte async copies, a warp a row, and
 //              k_rope's copy
-// Work: (128 tokens, head) items, tokens outermost, cut into equal ranges, one a CTA.
+// Work: (2 x 128 tokens, head) items, tokens outermost, cut into equal ranges, one a
+// cluster.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -32,13 +35,15 @@ namespace {
 using namespace tc;
 
 constexpr int kExTok = 128, kExK = 512, kExRope = 64, kExN = 256;
-constexpr int kExChunks = kExK / 64;
-constexpr int kExStages = 3;
+constexpr int kExChunks = kExK / 32;
+constexpr int kExStages = 5;
 constexpr int kExThreads = 320, kExProd = 4, kExMma = 5, kExGather = 6;
 constexpr uint32_t kExBlock = kExTok * 128;           // 64 columns of the tokens: 16 KB
-constexpr uint32_t kExStage = kExN * 128;             // 64 columns of a head's weights: 32 KB
-constexpr uint32_t kExRing = kExChunks * kExBlock;
-constexpr uint32_t kExBar = kExRing + kExStages * kExStage;
+constexpr uint32_t kExStage = kExN * 64;              // 32 columns of a head's weights: 16 KB
+constexpr uint32_t kExRing = kExK / 64 * kExBlock;
+constexpr uint32_t kExOut = kExRing + kExStages * kExStage;   // 64 columns of the output: 16 KB
+constexpr uint32_t kExBar = kExOut + kExTok * 128;
+constexpr uint32_t kExHi64 = (512u >> 4) | (1u << 14) | (4u << 29);   // descriptors of the weights: 64-byte swizzle
 constexpr uint32_t kExBytes = kExBar + 256 + 1024;
 static_assert(kExBytes <= 227 * 1024, "shared memory");
 
@@ -48,7 +53,7 @@ struct ExParams {
     __nv_bfloat16* kv;
     __nv_bfloat16* rope;
     int64_t num_slots, slot_stride, items;
-    int32_t T, H, wide;
+    int32_t T, H;
     int32_t* err;
     uint64_t wait_ns;
     int32_t withhold;
@@ -56,7 +61,7 @@ struct ExParams {
 
 struct ExLaunch {
     ExParams p;
-    CUtensorMap map_w;
+    CUtensorMap map_w, map_o;
 };
 
 struct ExBars {
@@ -66,16 +71,19 @@ struct ExBars {
 };
 static_assert(sizeof(ExBars) <= 256, "barrier block");
 
-// A CTA's items [lo, hi), walked alike by every role: tile of tokens, head.
+// A cluster's items [lo, hi), walked alike by every role of both CTAs: tile of tokens
+// (each its own of the pair), head.
 struct ExWalk {
     int64_t i, hi;
     int tile, head, H;
     __device__ __forceinline__ ExWalk(const ExParams& p) : H(p.H)
     {
-        i = blockIdx.x * p.items / gridDim.x;
-        hi = (blockIdx.x + 1) * p.items / gridDim.x;
-        tile = (int)(i / H);
-        head = (int)(i - (int64_t)tile * H);
+        const int64_t c = blockIdx.x >> 1, n = gridDim.x >> 1;
+        i = c * p.items / n;
+        hi = (c + 1) * p.items / n;
+        const int pair = (int)(i / H);
+        tile = 2 * pair + (int)(blockIdx.x & 1);
+        head = (int)(i - (int64_t)pair * H);
     }
     __device__ __forceinline__ bool more() const { return i < hi; }
     __device__ __forceinline__ bool last_of_tile() const { return head + 1 == H || i + 1 == hi; }
@@ -84,10 +92,32 @@ struct ExWalk {
         ++i;
         if (++head == H) {
             head = 0;
-            ++tile;
+            tile += 2;
         }
     }
 };
+
+__device__ __forceinline__ void ex_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A box into the same place of both CTAs' shared memory, counted on both CTAs' barriers.
+__device__ __forceinline__ void ex_load_both(uint32_t dst, const void* tmap, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
+                 "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+                 "l"(tmap), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
+                 : "memory");
+}
+
+// Arrives on both CTAs' barrier once every MMA this thread issued so far has completed.
+__device__ __forceinline__ void ex_commit_both(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
 
 __device__ __forceinline__ bool ex_elect()
 {
@@ -110,8 +140,11 @@ __device__ void ex_producer(const ExLaunch& L, ExBars& b, uint32_t sbase)
                 ok = false;
                 break;
             }
+            // this CTA's half of the chunk's rows for both, the other's half from the other
             ptx::mbar_arrive_expect_tx(full, kExStage);
-            ptx::tma_load_2d(sbase + kExRing + at * kExStage, &L.map_w, 64 * c, w.head * kExN, full);
+            const int half = blockIdx.x & 1;
+            ex_load_both(sbase + kExRing + at * kExStage + half * (kExStage / 2), &L.map_w, 32 * c,
+                         w.head * kExN + half * (kExN / 2), full);
         }
     // Without a timeout the MMA lane has waited for every fill.  After one, the copies
     // started here land before the CTA leaves.
@@ -142,11 +175,13 @@ __device__ void ex_mma(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm
             if (!(ok = wait(&b.full[at], k / kExStages)))
                 break;
             ptx::tc_fence_after();
-            const uint32_t a = a_lo + c * (kExBlock >> 4), w_lo = r_lo + at * (kExStage >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                ptx::umma_bf16(d, pf_desc(a + 2 * ks), pf_desc(w_lo + 2 * ks), id, c + ks > 0 ? 1u : 0u);
-            ptx::umma_commit(ptx::smem_addr(&b.empty[at]));
+            const uint32_t a = a_lo + (c >> 1) * (kExBlock >> 4) + 4 * (c & 1), w_lo = r_lo + at * (kExStage >> 4);
+            if (c == 0)
+                mma_ss2<false, kDescHi, kExHi64>(d, a, w_lo, id);
+            else
+                mma_ss2<true, kDescHi, kExHi64>(d, a, w_lo, id);
+            mma_ss2<true, kDescHi, kExHi64>(d, a + 2, w_lo + 2, id);
+            ex_commit_both(ptx::smem_addr(&b.empty[at]));
         }
         if (!ok)
             break;
@@ -183,7 +218,7 @@ __device__ void ex_gather(const ExLaunch& L, ExBars& b, uint32_t sbase, int warp
                     raise_err(p.err, KAMERA_DEVERR_SLOT);
                 mine = -1;
             }
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < 32; ++i) {
                 const int64_t slot = __shfl_sync(0xFFFFFFFFu, mine, i);
                 const int r = 32 * warp + i;
@@ -198,72 +233,92 @@ __device__ void ex_gather(const ExLaunch& L, ExBars& b, uint32_t sbase, int warp
                         ptx::st_shared_zero16(dst);
                 }
             }
-            if (w.head == 0) {
-#pragma unroll 2
-                for (int i = 0; i < 32; i += 4) {   // four rows of eight pieces
-                    const int r = i + (lane >> 3), t = t0 + r;
-                    const int64_t slot = __shfl_sync(0xFFFFFFFFu, mine, r);
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            ptx::cp_async_commit();
+            uint4 v[8];   // k_rope: four rows of eight pieces at a time
+            const bool rope = w.head == 0;
+            if (rope) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t slot = __shfl_sync(0xFFFFFFFFu, mine, 4 * i + (lane >> 3));
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
                     if (slot >= 0)
-                        v = *reinterpret_cast<const uint4*>(p.pool + slot * p.slot_stride + kExK + 8 * (lane & 7));
-                    if (t < p.T)
-                        *reinterpret_cast<uint4*>(p.rope + (int64_t)t * kExRope + 8 * (lane & 7)) = v;
+                        v[i] = *reinterpret_cast<const uint4*>(p.pool + slot * p.slot_stride + kExK + 8 * (lane & 7));
                 }
             }
-            ptx::cp_async_commit();
             ptx::cp_async_wait<0>();
             ptx::fence_proxy_async();
             if (!p.withhold)
                 ptx::mbar_arrive(ptx::smem_addr(&b.a_full));
+            if (rope) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int t = t0 + 4 * i + (lane >> 3);
+                    if (t < p.T)
+                        *reinterpret_cast<uint4*>(p.rope + (int64_t)t * kExRope + 8 * (lane & 7)) = v[i];
+                }
+            }
             ++tiles;
         }
         fresh = w.last_of_tile();
     }
 }
 
-__device__ void ex_epilogue(const ExLaunch& L, ExBars& b, uint32_t tm, int warp, int lane)
+__device__ void ex_epilogue(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm, int warp, int lane)
 {
     const ExParams& p = L.p;
     const uint32_t lanes = tm + ((uint32_t)warp << 21);
-    uint32_t n = 0;
-    for (ExWalk w(p); w.more(); w.next(), ++n) {
-        const bool ok = wmma16::cycle_wait(ptx::smem_addr(&b.acc_full[n & 1u]), (n >> 1) & 1u, &b.abort, p.err, p.wait_ns);
-        if (!__all_sync(0xFFFFFFFFu, ok))
-            return;
+    const int r = 32 * warp + lane;
+    const uint32_t row = sbase + kExOut + (uint32_t)(r >> 3) * 1024u;
+    uint32_t n = 0, ok_word;
+    bool ok = true;
+    for (ExWalk w(p); w.more() && ok; w.next(), ++n) {
+        ok = wmma16::cycle_wait(ptx::smem_addr(&b.acc_full[n & 1u]), (n >> 1) & 1u, &b.abort, p.err, p.wait_ns);
         ptx::tc_fence_after();
-        const int t = w.tile * kExTok + 32 * warp + lane;
-        __nv_bfloat16* dst = p.kv + ((int64_t)t * p.H + w.head) * kExN;
-#pragma unroll 2
-        for (int c = 0; c < kExN / 32; ++c) {
-            uint32_t o[32], x[16];
-            tmem_ld32(lanes + (n & 1u) * kExN + 32 * c, o);
+        const bool some = w.tile * kExTok < p.T;
+#pragma unroll 1
+        for (int c = 0; c < kExN / 64; ++c) {
+            uint32_t o[32], q[32];
+            tmem_ld32_issue(lanes + (n & 1u) * kExN + 64 * c, o);
+            tmem_ld32(lanes + (n & 1u) * kExN + 64 * c + 32, q);   // waits for both
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                x[j] = pack_bf16x2(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
-            if (t >= p.T)
-                continue;
-            if (p.wide) {
+            for (int j = 0; j < 32; ++j)
+                asm volatile("" : "+r"(o[j]));
+            if (r == 0)
+                ptx::bulk_wait_read_all();   // the store before has read the buffer
+            asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 32 * c + 16 * i),
-                                 "r"(x[8 * i]), "r"(x[8 * i + 1]), "r"(x[8 * i + 2]), "r"(x[8 * i + 3]), "r"(x[8 * i + 4]),
-                                 "r"(x[8 * i + 5]), "r"(x[8 * i + 6]), "r"(x[8 * i + 7])
-                                 : "memory");
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4*>(dst + 32 * c + 8 * i) =
-                        make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t* x = j < 4 ? o + 8 * j : q + 8 * (j - 4);
+                ptx::sts128(row + sw128(r & 7, j), pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                            pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                            pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                            pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
+            }
+            ptx::fence_proxy_async();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (r == 0 && some && ok) {      // rows past the last token are not written
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&L.map_o),
+                             "r"(w.head * kExN + 64 * c), "r"(w.tile * kExTok), "r"(sbase + kExOut)
+                             : "memory");
+                ptx::bulk_commit();
             }
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(ptx::smem_addr(&b.acc_empty[n & 1u]));
+        // a thread whose wait ran out leaves with the others
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 2, 128, p;\n\t"
+                     "selp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(ok_word)
+                     : "r"(ok ? 1u : 0u)
+                     : "memory");
+        ok = ok_word != 0;
     }
+    if (r == 0)
+        ptx::bulk_wait_all();
 }
 
 __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_constant__ ExLaunch L)
 {
-    const ExParams& p = L.p;
     extern __shared__ __align__(16) unsigned char raw[];
     const uint32_t at = ptx::smem_addr(raw), pad = (1024u - (at & 1023u)) & 1023u, sbase = at + pad;
     ExBars& b = *reinterpret_cast<ExBars*>(raw + pad + kExBar);
@@ -271,7 +326,7 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < kExStages; ++i) {
             ptx::mbar_init(ptx::smem_addr(&b.full[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&b.empty[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.empty[i]), 2);   // both CTAs' MMAs
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_addr(&b.acc_full[i]), 1);
@@ -290,13 +345,13 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
-    __syncthreads();
+    ex_cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tm = b.tmem;
     ptx::grid_wait();
     ptx::grid_launch_next();
     if (warp < 4)
-        ex_epilogue(L, b, tm, warp, lane);
+        ex_epilogue(L, b, sbase, tm, warp, lane);
     else if (warp == kExProd) {
         if (ex_elect())
             ex_producer(L, b, sbase);
@@ -306,7 +361,8 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
     } else
         ex_gather(L, b, sbase, warp - kExGather, lane);
     ptx::tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    ex_cluster_sync();   // neither CTA leaves while the other may write to it
     if (warp == kExMma) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tm, 512);
@@ -364,19 +420,32 @@ int kamera_mla_expand(const KameraPagedMlaKV* kv, const KameraMlaExpand* x, int3
     p.slot_stride = kv->slot_stride;
     p.T = x->n_tokens;
     p.H = x->num_heads;
-    p.items = (T + kExTok - 1) / kExTok * H;
-    p.wide = (reinterpret_cast<uintptr_t>(x->kv_out) & 31) == 0;
+    p.items = (T + 2 * kExTok - 1) / (2 * kExTok) * H;
     p.err = d_err;
     p.wait_ns = wait_limit_ns();
     p.withhold = test_withhold_loads() ? 1 : 0;
-    if (!make_rows_map(&L.map_w, x->weight, H * kExN, kExK, kExK, 64, kExN))
+    if (!make_rows_map64(&L.map_w, x->weight, H * kExN, kExK, kExK, kExN / 2) ||
+        !make_rows_map(&L.map_o, x->kv_out, T, H * kExN, H * kExN, 64, kExTok))
         return KAMERA_ERR_CUDA;
-    const int64_t ctas = std::min<int64_t>(device_sms(), p.items);
     // set at every launch: the attribute belongs to the current device's context
-    if (cudaFuncSetAttribute(mla_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kExBytes) !=
-            cudaSuccess ||
-        launch_after(mla_expand_kernel, dim3((unsigned)ctas), kExThreads, kExBytes, reinterpret_cast<cudaStream_t>(stream),
-                     true, L) != cudaSuccess)
+    if (cudaFuncSetAttribute(mla_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kExBytes) != cudaSuccess)
+        return KAMERA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    const int fit = cluster_fit(reinterpret_cast<const void*>(mla_expand_kernel), kExThreads, (int)kExBytes, 2);
+    cfg.gridDim = dim3(2u * (unsigned)std::min<int64_t>(fit > 0 ? fit : std::max(1, device_sms() / 2), p.items));
+    cfg.blockDim = dim3(kExThreads);
+    cfg.dynamicSmemBytes = kExBytes;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, mla_expand_kernel, L) != cudaSuccess)
         return KAMERA_ERR_CUDA;
     return KAMERA_OK;
 }

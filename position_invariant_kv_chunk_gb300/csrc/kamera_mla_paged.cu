@@ -344,29 +344,15 @@ __device__ __forceinline__ bool mp_elect()
 // pipe needs 26 to 66.
 constexpr uint32_t kMpHiU = (2 * kMpAtom >> 4) | (1u << 14) | (2u << 29);
 
-template <bool ACC, uint32_t HA, uint32_t HB>
-__device__ __forceinline__ void mp_issue(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
-{
-    if constexpr (ACC)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 1, 1;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                     "l"(pf_desc<HA>(a_lo)), "l"(pf_desc<HB>(b_lo)), "r"(idesc)
-                     : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 1, 1;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                     "l"(pf_desc<HA>(a_lo)), "l"(pf_desc<HB>(b_lo)), "r"(idesc)
-                     : "memory");
-}
 template <bool ACC>
 __device__ __forceinline__ void mma_ds(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
 {
-    mp_issue<ACC, kMpHiU, kDescHi>(d, a_lo, b_lo, idesc);
+    mma_ss2<ACC, kMpHiU, kDescHi>(d, a_lo, b_lo, idesc);
 }
 template <bool ACC>
 __device__ __forceinline__ void mma_sd(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
 {
-    mp_issue<ACC, kDescHi, kMpHiU>(d, a_lo, b_lo, idesc);
+    mma_ss2<ACC, kDescHi, kMpHiU>(d, a_lo, b_lo, idesc);
 }
 
 // The scores' lane: tile by tile as the rows come.

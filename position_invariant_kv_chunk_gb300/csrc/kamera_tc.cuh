@@ -145,6 +145,22 @@ __device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t 
                      : "memory");
 }
 
+// The same with a descriptor high word for each operand.
+template <bool ACC, uint32_t HA, uint32_t HB>
+__device__ __forceinline__ void mma_ss2(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
+{
+    if constexpr (ACC)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 1, 1;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "l"(pf_desc<HA>(a_lo)), "l"(pf_desc<HB>(b_lo)), "r"(idesc)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 1, 1;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                     "l"(pf_desc<HA>(a_lo)), "l"(pf_desc<HB>(b_lo)), "r"(idesc)
+                     : "memory");
+}
+
 // 2^x (the MUFU approximation: relative error near 2^-22, subnormal results
 // flushed to zero).
 __device__ __forceinline__ float pf_ex2(float x)
