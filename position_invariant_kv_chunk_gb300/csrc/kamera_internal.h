@@ -108,11 +108,10 @@ inline int device_sms()
 
 // 2-D tensor map (a CUtensorMap, 64-byte aligned, at `map`) over a bf16 array
 // of `rows` rows of `width` elements, row_stride elements apart: boxes of
-// box_cols x box_rows, 128-byte swizzle (64-byte: boxes of 32 columns), rows past the
-// end read as zero.  False if the driver has no encoder or refuses the shape.
+// box_cols x box_rows, 128-byte swizzle, rows past the end read as zero.
+// False if the driver has no encoder or refuses the shape.
 bool make_rows_map(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int box_cols,
                    int box_rows);
-bool make_rows_map64(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int box_rows);
 
 // The same array in groups of eight rows (64 columns, row in its group, column
 // block of 64, group): one box holds `blocks` column blocks of `groups` groups,

@@ -3,16 +3,23 @@
 //
 // A matrix product, [tokens x 512] [512 x heads 256], whose left rows lie at pool slots.
 // 2 x 512 flops a value written (2 bytes): bound by the tensor cores from some hundred
-// tokens on.  A CTA holds the latent parts of 128 tokens in shared memory (128 KB,
-// gathered once) and runs heads past them: a head's weights come in sixteen 16 KB chunks
-// of 32 columns through a ring of five, and its 128 x 256 sums stand in one of two TMEM
-// halves while the epilogue empties the other, 64 columns at a time through shared memory
-// and a TMA store (rows stored from the registers, 32 bytes a lane, took 6000 cycles a
-// head, half more than its MMAs).
-//   warps 0-3  epilogue: thread = token = TMEM lane
-//   warp 4     producer of the weights (TMA)
-//   warp 5     MMA (M 128, N 256); it owns TMEM
-//   warps 6-9  gather of the tokens' rows: 16-byte async copies, a warp a row, and
+// tokens on.  Two CTAs form a pair (cta_group::2) of 256 tokens: each holds the latent
+// parts of its 128 in shared memory (128 KB, gathered once), and the pair runs heads past
+// them, one MMA (M 256, N 256) taking each CTA's tokens and half of the head's weights
+// from either CTA's shared memory.  So an SM loads half of the weights -- they come in
+// eight chunks of 64 columns, 16 KB to a CTA, through a ring of four -- and reads 8 KB of
+// shared memory an MMA.  (A CTA alone: 70 us for 16381 tokens of 16 heads, its ring of
+// 96 KB too short for L2's latency; with the weights by multicast to both, 65.)  A head's
+// 128 x 256 sums stand in one of two TMEM halves while two epilogue groups empty the other,
+// each 64 columns at a time through shared memory and a TMA store (one group took 6200
+// cycles a head, rows stored from the registers 6000, its MMAs 4200).  16381 tokens of 16
+// heads take 60 us (1150 TFLOP/s, floor 35): a head now takes 6100 cycles, in which an SM
+// reads 128 KB of weights from L2 and writes 64 KB.
+//   warps 0-3, 4-7  epilogue of a head's first and last 128 columns: thread = token = TMEM lane
+//   warp 8     producer of the CTA's half of the weights (TMA, counted on the first CTA's
+//              barriers)
+//   warp 9     MMA (the first CTA's for both); it owns TMEM
+//   warps 10-13  gather of the tokens' rows: 16-byte async copies, a warp a row, and
 //              k_rope's copy
 // Work: (2 x 128 tokens, head) items, tokens outermost, cut into equal ranges, one a
 // cluster.
@@ -35,15 +42,14 @@ namespace {
 using namespace tc;
 
 constexpr int kExTok = 128, kExK = 512, kExRope = 64, kExN = 256;
-constexpr int kExChunks = kExK / 32;
-constexpr int kExStages = 5;
-constexpr int kExThreads = 320, kExProd = 4, kExMma = 5, kExGather = 6;
+constexpr int kExChunks = kExK / 64;
+constexpr int kExStages = 4;
+constexpr int kExThreads = 448, kExProd = 8, kExMma = 9, kExGather = 10;
 constexpr uint32_t kExBlock = kExTok * 128;           // 64 columns of the tokens: 16 KB
-constexpr uint32_t kExStage = kExN * 64;              // 32 columns of a head's weights: 16 KB
+constexpr uint32_t kExStage = kExN / 2 * 128;         // 64 columns of half of a head's weights: 16 KB
 constexpr uint32_t kExRing = kExK / 64 * kExBlock;
-constexpr uint32_t kExOut = kExRing + kExStages * kExStage;   // 64 columns of the output: 16 KB
-constexpr uint32_t kExBar = kExOut + kExTok * 128;
-constexpr uint32_t kExHi64 = (512u >> 4) | (1u << 14) | (4u << 29);   // descriptors of the weights: 64-byte swizzle
+constexpr uint32_t kExOut = kExRing + kExStages * kExStage;   // two groups' 64 columns of the output: 16 KB each
+constexpr uint32_t kExBar = kExOut + 2 * kExTok * 128;
 constexpr uint32_t kExBytes = kExBar + 256 + 1024;
 static_assert(kExBytes <= 227 * 1024, "shared memory");
 
@@ -65,7 +71,7 @@ struct ExLaunch {
 };
 
 struct ExBars {
-    uint64_t full[kExStages], empty[kExStages], acc_full[2], acc_empty[2], a_full, a_empty, drained;
+    uint64_t full[kExStages], empty[kExStages], acc_full[2], acc_empty[2], a_full, a_empty[kExChunks], drained;
     uint32_t tmem;
     int32_t abort;
 };
@@ -102,19 +108,48 @@ __device__ __forceinline__ void ex_cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A box into the same place of both CTAs' shared memory, counted on both CTAs' barriers.
-__device__ __forceinline__ void ex_load_both(uint32_t dst, const void* tmap, int x, int y, uint32_t bar)
+// A shared-memory address of this CTA as the pair's first CTA has it.
+__device__ __forceinline__ uint32_t ex_first(uint32_t addr)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-                 "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-                 "l"(tmap), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void ex_arrive_first(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(ex_first(bar)) : "memory");
+}
+
+// A box into this CTA's shared memory, counted on a barrier of the pair's first CTA.
+__device__ __forceinline__ void ex_load(uint32_t dst, const void* tmap, int x, int y, uint32_t first_bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(tmap), "r"(x), "r"(y), "r"(first_bar)
                  : "memory");
 }
 
-// Arrives on both CTAs' barrier once every MMA this thread issued so far has completed.
-__device__ __forceinline__ void ex_commit_both(uint32_t bar)
+// D (+)= A B^T over the pair: M 256 (each CTA its 128 rows and accumulator), N 256 (half
+// of B's rows in each CTA).
+template <bool ACC>
+__device__ __forceinline__ void ex_mma2(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+    if constexpr (ACC)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 1, 1;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(pf_desc(a_lo)), "l"(pf_desc(b_lo)), "r"(idesc)
+                     : "memory");
+    else
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, 1, 1;\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                     "l"(pf_desc(a_lo)), "l"(pf_desc(b_lo)), "r"(idesc)
+                     : "memory");
+}
+
+// Arrives on both CTAs' barrier once every MMA this thread issued so far has completed.
+__device__ __forceinline__ void ex_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
                  "h"((uint16_t)3)
                  : "memory");
 }
@@ -131,6 +166,7 @@ __device__ void ex_producer(const ExLaunch& L, ExBars& b, uint32_t sbase)
     const ExParams& p = L.p;
     if (p.withhold)
         return;
+    const int half = blockIdx.x & 1;
     uint32_t k = 0;
     bool ok = true;
     for (ExWalk w(p); w.more() && ok; w.next())
@@ -140,23 +176,26 @@ __device__ void ex_producer(const ExLaunch& L, ExBars& b, uint32_t sbase)
                 ok = false;
                 break;
             }
-            // this CTA's half of the chunk's rows for both, the other's half from the other
-            ptx::mbar_arrive_expect_tx(full, kExStage);
-            const int half = blockIdx.x & 1;
-            ex_load_both(sbase + kExRing + at * kExStage + half * (kExStage / 2), &L.map_w, 32 * c,
-                         w.head * kExN + half * (kExN / 2), full);
+            if (half == 0)
+                ptx::mbar_arrive_expect_tx(full, 2 * kExStage);
+            ex_load(sbase + kExRing + at * kExStage, &L.map_w, 64 * c, w.head * kExN + half * (kExN / 2), ex_first(full));
         }
     // Without a timeout the MMA lane has waited for every fill.  After one, the copies
-    // started here land before the CTA leaves.
-    if (*static_cast<volatile int32_t*>(&b.abort))
-        for (uint32_t i = k > (uint32_t)kExStages ? k - kExStages : 0u; i < k; ++i)
+    // started here land before the CTAs leave: the first CTA waits for both halves of what
+    // it can, the other for as long.
+    if (*static_cast<volatile int32_t*>(&b.abort)) {
+        const int64_t t0 = clock64();
+        for (uint32_t i = k > (uint32_t)kExStages ? k - kExStages : 0u; i < k && half == 0; ++i)
             pf_drain_wait(ptx::smem_addr(&b.full[i % kExStages]), (i / kExStages) & 1u, p.wait_ns);
+        while (half == 1 && (uint64_t)(clock64() - t0) < 100000u)   // 50 us: no load takes that long
+            ;
+    }
 }
 
 __device__ void ex_mma(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm)
 {
     const ExParams& p = L.p;
-    constexpr uint32_t id = ptx::idesc_bf16_f32(kExTok, kExN);
+    constexpr uint32_t id = ptx::idesc_bf16_f32(2 * kExTok, kExN);
     const uint32_t a_lo = (sbase >> 4) | (1u << 16), r_lo = ((sbase + kExRing) >> 4) | (1u << 16);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
@@ -164,6 +203,7 @@ __device__ void ex_mma(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm
     uint32_t k = 0, n = 0, tiles = 0;
     bool ok = true, fresh = true;
     for (ExWalk w(p); w.more() && ok; ++n) {
+        const bool last = w.last_of_tile();
         if (fresh && !(ok = wait(&b.a_full, tiles)))
             break;
         if (n >= 2 && !(ok = wait(&b.acc_empty[n & 1u], (n >> 1) - 1)))
@@ -175,80 +215,98 @@ __device__ void ex_mma(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm
             if (!(ok = wait(&b.full[at], k / kExStages)))
                 break;
             ptx::tc_fence_after();
-            const uint32_t a = a_lo + (c >> 1) * (kExBlock >> 4) + 4 * (c & 1), w_lo = r_lo + at * (kExStage >> 4);
+            const uint32_t x = a_lo + c * (kExBlock >> 4), w_lo = r_lo + at * (kExStage >> 4);
             if (c == 0)
-                mma_ss2<false, kDescHi, kExHi64>(d, a, w_lo, id);
+                ex_mma2<false>(d, x, w_lo, id);
             else
-                mma_ss2<true, kDescHi, kExHi64>(d, a, w_lo, id);
-            mma_ss2<true, kDescHi, kExHi64>(d, a + 2, w_lo + 2, id);
-            ex_commit_both(ptx::smem_addr(&b.empty[at]));
+                ex_mma2<true>(d, x, w_lo, id);
+#pragma unroll
+            for (int ks = 1; ks < 4; ++ks)
+                ex_mma2<true>(d, x + 2 * ks, w_lo + 2 * ks, id);
+            ex_commit(ptx::smem_addr(&b.empty[at]));
+            if (last)
+                ex_commit(ptx::smem_addr(&b.a_empty[c]));
         }
         if (!ok)
             break;
-        ptx::umma_commit(ptx::smem_addr(&b.acc_full[n & 1u]));
-        fresh = w.last_of_tile();
-        if (fresh) {
-            ptx::umma_commit(ptx::smem_addr(&b.a_empty));
-            ++tiles;
-        }
+        ex_commit(ptx::smem_addr(&b.acc_full[n & 1u]));
+        fresh = last;
+        tiles += last ? 1u : 0u;
         w.next();
     }
     // every MMA issued here completes before TMEM is freed
-    ptx::umma_commit(ptx::smem_addr(&b.drained));
+    ex_commit(ptx::smem_addr(&b.drained));
     pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
 }
 
 // The tokens' rows into shared memory (K-major, 128B-swizzled blocks of 64 columns),
-// zero where there is none; k_rope's rows by the CTA that has the tile's first head.
+// zero where there is none, a block as soon as the tile before has no MMA left that reads
+// it; k_rope's rows by the CTA that has the tile's first head.  The rows of the pair's
+// next tile are asked into L2 meanwhile.
 __device__ void ex_gather(const ExLaunch& L, ExBars& b, uint32_t sbase, int warp, int lane)
 {
     const ExParams& p = L.p;
     uint32_t tiles = 0;
     bool fresh = true, ok = true;
+    auto piece = [&](int r, int c, int64_t slot) {   // 16-byte piece c of row r's latent part
+        const uint32_t dst = sbase + (uint32_t)(c >> 3) * kExBlock + (uint32_t)(r >> 3) * 1024u + sw128(r & 7, c & 7);
+        if (slot >= 0)
+            ptx::cp_async16(dst, p.pool + slot * p.slot_stride + 8 * c);
+        else
+            ptx::st_shared_zero16(dst);
+    };
+    auto slot_of = [&](int t) -> int64_t { return t < p.T ? p.slots[t] : -1; };
+    int64_t mine = -1;
     for (ExWalk w(p); w.more(); w.next()) {
         if (fresh) {
-            if (tiles > 0)
-                ok = wmma16::cycle_wait(ptx::smem_addr(&b.a_empty), (tiles - 1) & 1u, &b.abort, p.err, p.wait_ns);
-            if (!__all_sync(0xFFFFFFFFu, ok))
-                return;
             const int t0 = w.tile * kExTok + 32 * warp;
-            int64_t mine = t0 + lane < p.T ? p.slots[t0 + lane] : -1;   // lane l: row l of the warp's 32
+            if (tiles == 0)
+                mine = slot_of(t0 + lane);   // lane l: row l of the warp's 32
             if (mine < 0 || mine >= p.num_slots) {
                 if (mine != -1 && w.head == 0)
                     raise_err(p.err, KAMERA_DEVERR_SLOT);
                 mine = -1;
             }
-#pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
-                const int64_t slot = __shfl_sync(0xFFFFFFFFu, mine, i);
-                const int r = 32 * warp + i;
-                const __nv_bfloat16* src = p.pool + slot * p.slot_stride;
+            int64_t slot[8];   // the rows of this lane's pieces of a block: 4 i + lane / 8
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int c = 32 * x + lane;   // 16-byte piece of the latent part
-                    const uint32_t dst = sbase + (uint32_t)(c >> 3) * kExBlock + (uint32_t)(r >> 3) * 1024u + sw128(r & 7, c & 7);
-                    if (slot >= 0)
-                        ptx::cp_async16(dst, src + 8 * c);
-                    else
-                        ptx::st_shared_zero16(dst);
+            for (int i = 0; i < 8; ++i)
+                slot[i] = __shfl_sync(0xFFFFFFFFu, mine, 4 * i + (lane >> 3));
+            if (tiles == 0) {   // nothing to wait for: row after row (block after block, 1296 tokens 18.4 us, not 16.7)
+#pragma unroll 8
+                for (int i = 0; i < 32; ++i) {
+                    const int64_t s = __shfl_sync(0xFFFFFFFFu, mine, i);
+                    piece(32 * warp + i, lane, s);
+                    piece(32 * warp + i, 32 + lane, s);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kExChunks; ++c) {
+                    ok = wmma16::cycle_wait(ptx::smem_addr(&b.a_empty[c]), (tiles - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ptx::cp_async_commit();
+                        ptx::cp_async_wait<0>();
+                        return;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        piece(32 * warp + 4 * i + (lane >> 3), 8 * c + (lane & 7), slot[i]);
                 }
             }
             ptx::cp_async_commit();
-            uint4 v[8];   // k_rope: four rows of eight pieces at a time
+            uint4 v[8];   // k_rope
             const bool rope = w.head == 0;
             if (rope) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int64_t slot = __shfl_sync(0xFFFFFFFFu, mine, 4 * i + (lane >> 3));
                     v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (slot >= 0)
-                        v[i] = *reinterpret_cast<const uint4*>(p.pool + slot * p.slot_stride + kExK + 8 * (lane & 7));
+                    if (slot[i] >= 0)
+                        v[i] = *reinterpret_cast<const uint4*>(p.pool + slot[i] * p.slot_stride + kExK + 8 * (lane & 7));
                 }
             }
             ptx::cp_async_wait<0>();
             ptx::fence_proxy_async();
             if (!p.withhold)
-                ptx::mbar_arrive(ptx::smem_addr(&b.a_full));
+                ex_arrive_first(ptx::smem_addr(&b.a_full));
             if (rope) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -258,17 +316,27 @@ __device__ void ex_gather(const ExLaunch& L, ExBars& b, uint32_t sbase, int warp
                 }
             }
             ++tiles;
+            if (w.hi - w.i > w.H - w.head) {   // the pair has a tile after this one
+                mine = slot_of(t0 + 2 * kExTok + lane);
+                if (mine >= 0 && mine < p.num_slots) {
+                    const char* row = reinterpret_cast<const char*>(p.pool + mine * p.slot_stride);
+#pragma unroll
+                    for (int i = 0; i < (kExK + kExRope) * 2 / 128; ++i)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 128 * i));
+                }
+            }
         }
         fresh = w.last_of_tile();
     }
 }
 
+template <int GRP>
 __device__ void ex_epilogue(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm, int warp, int lane)
 {
     const ExParams& p = L.p;
     const uint32_t lanes = tm + ((uint32_t)warp << 21);
     const int r = 32 * warp + lane;
-    const uint32_t row = sbase + kExOut + (uint32_t)(r >> 3) * 1024u;
+    const uint32_t out = sbase + kExOut + GRP * kExTok * 128, row = out + (uint32_t)(r >> 3) * 1024u;
     uint32_t n = 0, ok_word;
     bool ok = true;
     for (ExWalk w(p); w.more() && ok; w.next(), ++n) {
@@ -276,7 +344,7 @@ __device__ void ex_epilogue(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32
         ptx::tc_fence_after();
         const bool some = w.tile * kExTok < p.T;
 #pragma unroll 1
-        for (int c = 0; c < kExN / 64; ++c) {
+        for (int c = GRP * (kExN / 128); c < (GRP + 1) * (kExN / 128); ++c) {
             uint32_t o[32], q[32];
             tmem_ld32_issue(lanes + (n & 1u) * kExN + 64 * c, o);
             tmem_ld32(lanes + (n & 1u) * kExN + 64 * c + 32, q);   // waits for both
@@ -285,7 +353,7 @@ __device__ void ex_epilogue(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32
                 asm volatile("" : "+r"(o[j]));
             if (r == 0)
                 ptx::bulk_wait_read_all();   // the store before has read the buffer
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync %0, 128;" ::"n"(1 + 2 * GRP) : "memory");
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const uint32_t* x = j < 4 ? o + 8 * j : q + 8 * (j - 4);
@@ -295,21 +363,21 @@ __device__ void ex_epilogue(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32
                             pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
             }
             ptx::fence_proxy_async();
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            asm volatile("bar.sync %0, 128;" ::"n"(1 + 2 * GRP) : "memory");
             if (r == 0 && some && ok) {      // rows past the last token are not written
                 asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(&L.map_o),
-                             "r"(w.head * kExN + 64 * c), "r"(w.tile * kExTok), "r"(sbase + kExOut)
+                             "r"(w.head * kExN + 64 * c), "r"(w.tile * kExTok), "r"(out)
                              : "memory");
                 ptx::bulk_commit();
             }
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(ptx::smem_addr(&b.acc_empty[n & 1u]));
+        ex_arrive_first(ptx::smem_addr(&b.acc_empty[n & 1u]));
         // a thread whose wait ran out leaves with the others
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 2, 128, p;\n\t"
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, 128, p;\n\t"
                      "selp.u32 %0, 1, 0, q;\n\t}"
                      : "=r"(ok_word)
-                     : "r"(ok ? 1u : 0u)
+                     : "r"(ok ? 1u : 0u), "n"(2 + 2 * GRP)
                      : "memory");
         ok = ok_word != 0;
     }
@@ -326,14 +394,15 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < kExStages; ++i) {
             ptx::mbar_init(ptx::smem_addr(&b.full[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&b.empty[i]), 2);   // both CTAs' MMAs
+            ptx::mbar_init(ptx::smem_addr(&b.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_addr(&b.acc_full[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&b.acc_empty[i]), 128);
+            ptx::mbar_init(ptx::smem_addr(&b.acc_empty[i]), 512);   // both CTAs' epilogues
         }
-        ptx::mbar_init(ptx::smem_addr(&b.a_full), 128);
-        ptx::mbar_init(ptx::smem_addr(&b.a_empty), 1);
+        ptx::mbar_init(ptx::smem_addr(&b.a_full), 256);
+        for (int i = 0; i < kExChunks; ++i)
+            ptx::mbar_init(ptx::smem_addr(&b.a_empty[i]), 1);
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
         ptx::fence_barrier_init();
@@ -341,8 +410,9 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
     if (warp == kExProd && lane == 0)
         ptx::prefetch_tmap(&L.map_w);
     if (warp == kExMma) {
-        ptx::tmem_alloc(ptx::smem_addr(&b.tmem), 512);
-        ptx::tmem_relinquish();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_addr(&b.tmem)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     ptx::tc_fence_before();
     ex_cluster_sync();
@@ -351,12 +421,14 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
     ptx::grid_wait();
     ptx::grid_launch_next();
     if (warp < 4)
-        ex_epilogue(L, b, sbase, tm, warp, lane);
+        ex_epilogue<0>(L, b, sbase, tm, warp, lane);
+    else if (warp < kExProd)
+        ex_epilogue<1>(L, b, sbase, tm, warp - 4, lane);
     else if (warp == kExProd) {
         if (ex_elect())
             ex_producer(L, b, sbase);
     } else if (warp == kExMma) {
-        if (ex_elect())
+        if ((blockIdx.x & 1) == 0 && ex_elect())
             ex_mma(L, b, sbase, tm);
     } else
         ex_gather(L, b, sbase, warp - kExGather, lane);
@@ -365,7 +437,7 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
     ex_cluster_sync();   // neither CTA leaves while the other may write to it
     if (warp == kExMma) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tm, 512);
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
     }
 }
 
@@ -424,7 +496,7 @@ int kamera_mla_expand(const KameraPagedMlaKV* kv, const KameraMlaExpand* x, int3
     p.err = d_err;
     p.wait_ns = wait_limit_ns();
     p.withhold = test_withhold_loads() ? 1 : 0;
-    if (!make_rows_map64(&L.map_w, x->weight, H * kExN, kExK, kExK, kExN / 2) ||
+    if (!make_rows_map(&L.map_w, x->weight, H * kExN, kExK, kExK, 64, kExN / 2) ||
         !make_rows_map(&L.map_o, x->kv_out, T, H * kExN, H * kExN, 64, kExTok))
         return KAMERA_ERR_CUDA;
     // set at every launch: the attribute belongs to the current device's context

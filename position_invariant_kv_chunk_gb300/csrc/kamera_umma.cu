@@ -1034,8 +1034,8 @@ cudaError_t launch_kernel(const UmmaParams& core, const KameraChunk* h_chunks, i
 
 }  // namespace
 
-static bool rows_map(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int box_cols,
-                     int box_rows, CUtensorMapSwizzle swizzle)
+bool make_rows_map(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int box_cols,
+                   int box_rows)
 {
     auto fn = encode_fn();
     if (!fn || rows < 1 || width < 1)
@@ -1045,19 +1045,8 @@ static bool rows_map(void* map, const void* base, int64_t rows, int64_t width, i
     cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1u, 1u};
     return fn(static_cast<CUtensorMap*>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_rows_map(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int box_cols,
-                   int box_rows)
-{
-    return rows_map(map, base, rows, width, row_stride, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
-bool make_rows_map64(void* map, const void* base, int64_t rows, int64_t width, int64_t row_stride, int box_rows)
-{
-    return rows_map(map, base, rows, width, row_stride, 32, box_rows, CU_TENSOR_MAP_SWIZZLE_64B);
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool make_heads_map(void* map, const void* base, int64_t rows, int heads, int width, int64_t row_stride,
