@@ -115,9 +115,8 @@ struct MpBars {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], pv_done[2], drained[2];
     uint32_t mask[kMpMasks];
-    int64_t total;
-    int64_t first_at;          // global tile at which the range's first sequence starts
-    int32_t first_seq;
+    int64_t total, lo, hi;     // the batch's tiles and the range's
+    int32_t first_seq, first_len, first_n, first_t;   // where the range starts
     uint32_t tmem;
     int32_t abort;
 };
@@ -134,23 +133,23 @@ __device__ __forceinline__ int mp_tiles(int len) { return len > 0 ? (len - 1) / 
 // The ranges in use and where range r starts, of T tiles.
 __device__ __forceinline__ int64_t mp_ranges(const MpParams& p, int64_t T)
 {
-    return min((int64_t)p.ranges, (T + p.min_tiles - 1) / p.min_tiles);
+    return min((int64_t)p.ranges, wmma16::quotient(T + p.min_tiles - 1, p.min_tiles));
 }
-__device__ __forceinline__ int64_t mp_start(int64_t r, int64_t T, int64_t R) { return r * T / R; }
-__device__ __forceinline__ int64_t mp_range_of(int64_t tile, int64_t T, int64_t R) { return ((tile + 1) * R - 1) / T; }
+__device__ __forceinline__ int64_t mp_start(int64_t r, int64_t T, int64_t R) { return wmma16::quotient(r * T, R); }
+__device__ __forceinline__ int64_t mp_range_of(int64_t tile, int64_t T, int64_t R) { return wmma16::quotient((tile + 1) * R - 1, T); }
 
 // A range's tiles, walked alike by every role.
 struct MpWalk {
     int64_t left;        // tiles of the range from this one on
     int s, len, n, t;    // sequence, its tokens and tiles, the tile
     bool fresh;          // the first tile of a segment
-    __device__ __forceinline__ void start(const MpParams& p, const MpBars& b, int64_t lo, int64_t hi)
+    __device__ __forceinline__ void start(const MpBars& b)
     {
-        left = hi - lo;
+        left = b.hi - b.lo;
         s = b.first_seq;
-        len = mp_len(p, s);
-        n = mp_tiles(len);
-        t = (int)(lo - b.first_at);
+        len = b.first_len;
+        n = b.first_n;
+        t = b.first_t;
         fresh = true;
     }
     __device__ __forceinline__ bool last() const { return t + 1 == n || left == 1; }
@@ -168,28 +167,28 @@ struct MpWalk {
     }
 };
 
-// Total tiles and the sequence in which the range starts, by one warp: one look at the
-// lengths of up to 32 sequences, two at those of more.
+// Total tiles and where the range starts, by one warp: one look at the lengths of up to
+// 32 sequences, two at those of more.
 __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
 {
-    auto tiles = [&](int s) { return s < p.n_seqs ? (int64_t)mp_tiles(mp_len(p, s)) : 0; };
-    const int64_t first = tiles(lane);
-    int64_t sum = first;
+    auto length = [&](int s) { return s < p.n_seqs ? mp_len(p, s) : 0; };
+    const int first = length(lane);
+    int64_t sum = lane < p.n_seqs ? mp_tiles(first) : 0;
     for (int s = lane + 32; s < p.n_seqs; s += 32)
-        sum += tiles(s);
+        sum += mp_tiles(length(s));
 #pragma unroll
     for (int d = 16; d >= 1; d /= 2)
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    const int64_t T = sum, lo = mp_start(r, T, mp_ranges(p, T));
+    const int64_t T = sum, R = mp_ranges(p, T);
     int64_t at = 0;
-    if (lane == 0) {
+    if (lane == 0)
         b.total = T;
-        b.first_seq = 0;
-        b.first_at = 0;
-    }
-    __syncwarp();
+    if (r >= R)   // fewer tiles than ranges
+        return;
+    const int64_t lo = mp_start(r, T, R);
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-        const int64_t mine = s0 == 0 ? first : tiles(s0 + lane);
+        const int len = s0 == 0 ? first : length(s0 + lane);
+        const int64_t mine = s0 + lane < p.n_seqs ? mp_tiles(len) : 0;
         int64_t x = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -200,7 +199,11 @@ __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
         const int64_t before = at + x - mine;
         if (mine > 0 && before <= lo && lo < before + mine) {
             b.first_seq = s0 + lane;
-            b.first_at = before;
+            b.first_len = len;
+            b.first_n = (int)mine;
+            b.first_t = (int)(lo - before);
+            b.lo = lo;
+            b.hi = mp_start(r + 1, T, R);
         }
         at += __shfl_sync(0xFFFFFFFFu, x, 31);
         if (at > lo)
@@ -210,7 +213,7 @@ __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
 
 // ---------------------------------------------------------------- producer --
 template <int N>
-__device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int lane, int block, int64_t lo, int64_t hi)
+__device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int lane, int block)
 {
     using Y = MpLayout<N>;
     const MpParams& p = L.p;
@@ -220,7 +223,7 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
     constexpr int kPieces = kMpTok / 16, kAhead = 32 / kPieces;
     const int R = p.box_rows, off = 16 * (lane % kPieces);   // a box of R rows is issued by its first piece's lane
     MpWalk w, mine;
-    w.start(p, b, lo, hi);
+    w.start(b);
     mine = w;
     auto advance = [&](int n) {
         if (mine.left > n && mine.t + n < mine.n) {
@@ -243,10 +246,8 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
         page = page < 0 ? -2 : page;
     };
     advance(lane / kPieces);
-    int page, row, page_next, row_next, group = 0;
+    int page, row, page_next = -1, row_next = 0, group = 0;
     look_up(page, row);
-    advance(kAhead);
-    look_up(page_next, row_next);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         bool got = true;
         if (lane == 0)
@@ -272,8 +273,6 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
             if (tile > 0) {
                 page = page_next;
                 row = row_next;
-                advance(kAhead);
-                look_up(page_next, row_next);
             }
             good = page >= 0 && page < p.num_pages;
             if (page != -1 && !good && block == 0)
@@ -315,6 +314,10 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
             break;
         load(sbase + Y::kRopes + ra * kMpRope, &b.rfull[ra], &L.map_r, kMpDim / 64, kMpAtom);
         ++rope;
+        if (tile % kAhead == 0) {  // the eight tiles after these
+            advance(kAhead);
+            look_up(page_next, row_next);
+        }
         ++tile;
     }
     // Without a timeout the MMA lane has waited for every fill.  After one, the copies
@@ -357,7 +360,7 @@ __device__ __forceinline__ void mma_sd(uint32_t d, uint32_t a_lo, uint32_t b_lo,
 
 // The scores' lane: tile by tile as the rows come.
 template <int N>
-__device__ void mp_scores(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t tm, int64_t lo, int64_t hi)
+__device__ void mp_scores(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t tm)
 {
     using Y = MpLayout<N>;
     const MpParams& p = L.p;
@@ -368,7 +371,7 @@ __device__ void mp_scores(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t
     const uint32_t q_lo = ((sbase + Y::kQ) >> 4) | (1u << 16), u_lo = ((sbase + Y::kRing) >> 4) | (1u << 16);
     const uint32_t r_lo = ((sbase + Y::kRopes) >> 4) | (1u << 16);
     MpWalk w;
-    w.start(p, b, lo, hi);
+    w.start(b);
     uint32_t seg = 0, at = 0, lap = 0;   // place in the ring
     for (uint32_t t = 0; w.left > 0; ++t, w.next(p)) {
         if (w.fresh && !wait(&b.q_full, seg))
@@ -417,7 +420,7 @@ __device__ void mp_scores(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t
 
 // The products' lane: tile by tile as the weights come; a tile's units are free behind it.
 template <int N>
-__device__ void mp_products(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t tm, int64_t lo, int64_t hi)
+__device__ void mp_products(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t tm)
 {
     using Y = MpLayout<N>;
     const MpParams& p = L.p;
@@ -428,7 +431,7 @@ __device__ void mp_products(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32
     const uint32_t p_lo = ((sbase + Y::kP) >> 4) | (1u << 16);
     const uint32_t u_lo = ((sbase + Y::kRing) >> 4) | ((kMpAtom >> 4) << 16);
     MpWalk w;
-    w.start(p, b, lo, hi);
+    w.start(b);
     uint32_t at = 0, lap = 0;
     for (uint32_t t = 0; w.left > 0; ++t, w.next(p)) {
         uint32_t x = at, xl = lap;
@@ -542,7 +545,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
     const uint32_t st_row = lane & 7, st_half = (lane >> 3) & 1, st_j = lane >> 4;
     const uint32_t st = sbase + Y::kP + (G0 / 8 + st_j) * (Y::kPair ? 2 : 1) * kMpAtom + sw128(st_row, 2 * warp + st_half);
     MpWalk w;
-    w.start(p, b, lo, hi);
+    w.start(b);
     int64_t at = lo;               // the tile's place among all
     bool ok = true;
     for (uint32_t t = 0; w.left > 0; ++t, ++at) {
@@ -806,18 +809,18 @@ __global__ void __launch_bounds__(MpLayout<N>::kThreads, 1) mla_paged_kernel(con
     const uint32_t tm = b.tmem;
     const int64_t T = b.total, R = mp_ranges(p, T);
     if (range < R) {   // (else: fewer tiles than ranges)
-        const int64_t lo = mp_start(range, T, R), hi = mp_start(range + 1, T, R);
+        const int64_t lo = b.lo, hi = b.hi;
         if (warp < 4)
             mp_softmax<N, 0>(L, b, sbase, ex, tm, warp, lane, block, range, lo, hi);
         else if (warp < Y::kProd)
             mp_softmax<N, N / Y::HG - 1>(L, b, sbase, ex, tm, warp - 4, lane, block, range, lo, hi);
         else if (warp == Y::kProd)
-            mp_producer<N>(L, b, sbase, lane, block, lo, hi);
+            mp_producer<N>(L, b, sbase, lane, block);
         else if (warp == Y::kScores) {
             if (mp_elect())
-                mp_scores<N>(L, b, sbase, tm, lo, hi);
+                mp_scores<N>(L, b, sbase, tm);
         } else if (mp_elect())
-            mp_products<N>(L, b, sbase, tm, lo, hi);
+            mp_products<N>(L, b, sbase, tm);
     }
     ptx::tc_fence_before();
     __syncthreads();

@@ -56,8 +56,9 @@ struct P4Layout {
     static constexpr int NS = D == 128 ? 5 : 8;               // tiles in the ring
     static constexpr uint32_t kQ = 0;                         // [2 segments][d / 64 blocks][N rows][128 bytes]
     static constexpr uint32_t kQSeg = (D / 64) * N * 128;
-    static constexpr uint32_t kP = kQ + 2 * kQSeg;            // [2 blocks of 64 tokens][N rows][128 bytes]
-    static constexpr uint32_t kRing = kP + 2 * N * 128;
+    static constexpr uint32_t kP = kQ + 2 * kQSeg;            // [2 tiles][2 blocks of 64 tokens][N rows][128 bytes]
+    static constexpr uint32_t kPTile = 2 * N * 128;
+    static constexpr uint32_t kRing = kP + 2 * kPTile;
     static constexpr uint32_t kBar = kRing + NS * kTile;
     static constexpr uint32_t kBytes = kBar + 512 + 7 * N * 4 + 1024;   // + alignment slack
     static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -89,10 +90,10 @@ struct P4Params {
 };
 
 struct P4Bars {
-    uint64_t full[8], empty[8], q_full[2], k_full[2], v_full, s_full[2], p_full, pv_done, drained;
+    uint64_t full[8], empty[8], q_full[2], k_full[2], v_full, s_full[2], p_full[2], pv_done[2], drained;
     uint32_t mask[kP4Masks];       // tile t (mod kP4Masks): 16-token pieces that are there
-    int64_t total, first_at;
-    int32_t first_seq;
+    int64_t total, lo, hi;         // the batch's tiles and the range's
+    int32_t first_seq, first_len, first_n, first_h, first_t;   // where the range starts
     uint32_t tmem;
     int32_t abort;
 };
@@ -104,23 +105,22 @@ __device__ __forceinline__ int p4_len(const P4Params& p, int s)
     return len >= 0 && len <= p.max_len ? len : 0;
 }
 __device__ __forceinline__ int p4_tiles(int len) { return (len + kP4Tok - 1) / kP4Tok; }
-__device__ __forceinline__ int64_t p4_start(int64_t r, int64_t T, int64_t R) { return r * T / R; }
-__device__ __forceinline__ int64_t p4_range_of(int64_t tile, int64_t T, int64_t R) { return ((tile + 1) * R - 1) / T; }
+__device__ __forceinline__ int64_t p4_start(int64_t r, int64_t T, int64_t R) { return wmma16::quotient(r * T, R); }
+__device__ __forceinline__ int64_t p4_range_of(int64_t tile, int64_t T, int64_t R) { return wmma16::quotient((tile + 1) * R - 1, T); }
 
 // A range's tiles, walked alike by every role: sequence, KV head, tile.
 struct P4Walk {
     int64_t left;
     int s, h, len, n, t;
     bool fresh;
-    __device__ __forceinline__ void start(const P4Params& p, const P4Bars& b, int64_t lo, int64_t hi)
+    __device__ __forceinline__ void start(const P4Bars& b)
     {
-        left = hi - lo;
+        left = b.hi - b.lo;
         s = b.first_seq;
-        len = p4_len(p, s);
-        n = p4_tiles(len);
-        const int64_t at = lo - b.first_at;
-        h = n > 0 ? (int)(at / n) : 0;
-        t = n > 0 ? (int)(at % n) : 0;
+        len = b.first_len;
+        n = b.first_n;
+        h = b.first_h;
+        t = b.first_t;
         fresh = true;
     }
     __device__ __forceinline__ bool last() const { return t + 1 == n || left == 1; }
@@ -155,31 +155,29 @@ struct P4Walk {
     }
 };
 
-// Total tiles and the sequence in which the range starts, by one warp: one look at the
-// lengths of up to 32 sequences, two at those of more.
+// Total tiles and where the range starts, by one warp: one look at the lengths of up to
+// 32 sequences, two at those of more.
 __device__ void p4_locate(const P4Params& p, P4Bars& b, int r, int lane)
 {
-    auto tiles = [&](int s) { return s < p.n_seqs ? (int64_t)p4_tiles(p4_len(p, s)) * p.H : 0; };
-    const int64_t first = tiles(lane);
-    int64_t sum = first;
+    auto length = [&](int s) { return s < p.n_seqs ? p4_len(p, s) : 0; };
+    const int first = length(lane);
+    int64_t sum = (int64_t)p4_tiles(first) * p.H;
     for (int s = lane + 32; s < p.n_seqs; s += 32)
-        sum += tiles(s);
+        sum += (int64_t)p4_tiles(length(s)) * p.H;
 #pragma unroll
     for (int d = 16; d >= 1; d /= 2)
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
     const int64_t T = sum;
-    if (lane == 0) {
+    if (lane == 0)
         b.total = T;
-        b.first_seq = 0;
-        b.first_at = 0;
-    }
-    __syncwarp();
-    if (T == 0)
+    const int64_t R = min((int64_t)p.ranges, T);
+    if (r >= R)   // fewer tiles than ranges
         return;
-    const int64_t lo = p4_start(r, T, min((int64_t)p.ranges, T));
+    const int64_t lo = p4_start(r, T, R);
     int64_t at = 0;
     for (int s0 = 0; s0 < p.n_seqs; s0 += 32) {
-        const int64_t mine = s0 == 0 ? first : tiles(s0 + lane);
+        const int len = s0 == 0 ? first : length(s0 + lane), n = p4_tiles(len);
+        const int64_t mine = (int64_t)n * p.H;
         int64_t x = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
@@ -189,13 +187,26 @@ __device__ void p4_locate(const P4Params& p, P4Bars& b, int r, int lane)
         }
         const int64_t before = at + x - mine;
         if (mine > 0 && before <= lo && lo < before + mine) {
+            const int h = (int)wmma16::quotient(lo - before, n);
             b.first_seq = s0 + lane;
-            b.first_at = before;
+            b.first_len = len;
+            b.first_n = n;
+            b.first_h = h;
+            b.first_t = (int)(lo - before - (int64_t)h * n);
+            b.lo = lo;
+            b.hi = p4_start(r + 1, T, R);
         }
         at += __shfl_sync(0xFFFFFFFFu, x, 31);
         if (at > lo)
             break;
     }
+}
+
+__device__ __forceinline__ bool p4_elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 // ---------------------------------------------------------------- producer --
@@ -210,7 +221,7 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
     // look-ups as it came 1900: more than its decoding.)
     constexpr int kAhead = 32 / kP4Pieces;
     P4Walk mine;
-    mine.start(p, b, lo, hi);
+    mine.start(b);
     auto advance = [&](int n) {
         if (mine.left > n && mine.t + n < mine.n) {
             mine.left -= n;
@@ -232,11 +243,9 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
         page = page < 0 ? -2 : page;
     };
     advance(lane / kP4Pieces);
-    int page, page_next;
-    int64_t place, place_next;
+    int page, page_next = -1;
+    int64_t place, place_next = 0;
     look_up(page, place);
-    advance(kAhead);
-    look_up(page_next, place_next);
     const int64_t page_bytes = (int64_t)p.H * ppp * kPackedPiece<D>;
     const unsigned char* src = nullptr;
     bool good = false;
@@ -248,8 +257,6 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
             if (k > 0) {
                 page = page_next;
                 place = place_next;
-                advance(kAhead);
-                look_up(page_next, place_next);
             }
             good = page >= 0 && page < p.num_pages;
             if (page != -1 && !good && (place & 1))   // (once, with the first head)
@@ -277,8 +284,24 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
             }
         }
         __syncwarp();
-        if (lane / kP4Pieces == mine_now && good && !p.withhold)
+        if (mask == 0xFFu && !p.withhold) {   // by one thread, its addresses at hand: eight lanes, each by itself, take 1400 cycles
+            const unsigned char* from[kP4Pieces];
+#pragma unroll
+            for (int i = 0; i < kP4Pieces; ++i)
+                from[i] = reinterpret_cast<const unsigned char*>(
+                    __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), kP4Pieces * mine_now + i));
+            if (p4_elect()) {
+#pragma unroll
+                for (int i = 0; i < kP4Pieces; ++i)
+                    ptx::bulk_g2s(sbase + Y::kRing + at * Y::kTile + i * kPackedPiece<D>, from[i], kPackedPiece<D>, full);
+            }
+            __syncwarp();
+        } else if (lane / kP4Pieces == mine_now && good && !p.withhold)
             ptx::bulk_g2s(sbase + Y::kRing + at * Y::kTile + (lane % kP4Pieces) * kPackedPiece<D>, src, kPackedPiece<D>, full);
+        if (k % kAhead == 0) {     // the four tiles after these
+            advance(kAhead);
+            look_up(page_next, place_next);
+        }
         if (++at == (uint32_t)Y::NS) {
             at = 0;
             ++lap;
@@ -293,15 +316,8 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
 }
 
 // --------------------------------------------------------------------- MMA --
-__device__ __forceinline__ bool p4_elect()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 template <int D, int N>
-__device__ void p4_mma(const P4Params& p, P4Bars& b, uint32_t sbase, uint32_t tm, int64_t lo, int64_t hi)
+__device__ void p4_mma(const P4Params& p, P4Bars& b, uint32_t sbase, uint32_t tm)
 {
     using Y = P4Layout<D, N>;
     constexpr uint32_t id = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);   // fp16 x fp16 -> fp32, M 128
@@ -325,22 +341,23 @@ __device__ void p4_mma(const P4Params& p, P4Bars& b, uint32_t sbase, uint32_t tm
         return true;
     };
     P4Walk w;
-    w.start(p, b, lo, hi);
+    w.start(b);
     bool ok = w.left <= 0 || scores(0, w);
     for (uint32_t t = 0; ok && w.left > 0; ++t) {
         const bool fresh = w.fresh;
         w.next(p);
-        if (!(ok = w.left <= 0 || scores(t + 1, w)) || !(ok = wait(&b.v_full, t) && wait(&b.p_full, t)))
+        if (!(ok = w.left <= 0 || scores(t + 1, w)) || !(ok = wait(&b.v_full, t) && wait(&b.p_full[t & 1u], t >> 1)))
             break;
         ptx::tc_fence_after();
+        const uint32_t pt = p_lo + (t & 1u) * (Y::kPTile >> 4);
         if (fresh)
-            mma_ts<false>(tm + kP4TmO, tm + kP4TmV, p_lo, id);
+            mma_ts<false>(tm + kP4TmO, tm + kP4TmV, pt, id);
         else
-            mma_ts<true>(tm + kP4TmO, tm + kP4TmV, p_lo, id);
+            mma_ts<true>(tm + kP4TmO, tm + kP4TmV, pt, id);
 #pragma unroll
         for (int ks = 1; ks < kP4Tok / 16; ++ks)
-            mma_ts<true>(tm + kP4TmO, tm + kP4TmV + 8 * ks, p_lo + (ks >> 2) * (N * 128 >> 4) + 2 * (ks & 3), id);
-        ptx::umma_commit(ptx::smem_addr(&b.pv_done));
+            mma_ts<true>(tm + kP4TmO, tm + kP4TmV + 8 * ks, pt + (ks >> 2) * (N * 128 >> 4) + 2 * (ks & 3), id);
+        ptx::umma_commit(ptx::smem_addr(&b.pv_done[t & 1u]));
     }
     // every MMA issued here completes before TMEM is freed
     ptx::umma_commit(ptx::smem_addr(&b.drained));
@@ -388,7 +405,7 @@ __device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* rin
                 }
             }
             if (half == 0 && t > 0) {   // the product before has read the last tile's values
-                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.wait_ns);
                 if (!__all_sync(0xFFFFFFFFu, ok))
                     return;
                 ptx::tc_fence_after();
@@ -578,7 +595,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* 
         ++seg;
     };
     P4Walk w;
-    w.start(p, b, lo, hi);
+    w.start(b);
     if (w.left > 0)
         stage(w);
     p4_sync();
@@ -664,7 +681,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* 
                         fac[h] = f;
                 }
             if (!w.fresh) {          // the running output, once the products before are in it
-                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 ptx::tc_fence_after();
                 p4_sync();
@@ -692,18 +709,18 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* 
                 pk[j][k] = *reinterpret_cast<const uint32_t*>(&y);
             }
         }
-        if (t > 0) {                 // the product before has read the last weights
-            ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done), (t - 1) & 1u, &b.abort, p.err, p.wait_ns);
+        if (t > 1) {                 // the weights of two tiles before have been read
+            ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), ((t >> 1) - 1) & 1u, &b.abort, p.err, p.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
         }
 #pragma unroll
         for (int j = 0; j < J; ++j)
-            p4_stsm_x4_t(st + j * 1024, pk[j]);
+            p4_stsm_x4_t(st + (t & 1u) * Y::kPTile + j * 1024, pk[j]);
         ptx::fence_proxy_async();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0)
-            ptx::mbar_arrive(ptx::smem_addr(&b.p_full));
+            ptx::mbar_arrive(ptx::smem_addr(&b.p_full[t & 1u]));
         if (!w.last()) {
             w.next(p);
             continue;
@@ -738,7 +755,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* 
                                                                                 (wmax[2 * N + h] + wmax[3 * N + h]));
                 }
         }
-        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done), t & 1u, &b.abort, p.err, p.wait_ns);
+        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
         uint32_t o[N];
@@ -776,9 +793,9 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
             ptx::mbar_init(ptx::smem_addr(&b.q_full[i]), 128);
             ptx::mbar_init(ptx::smem_addr(&b.k_full[i]), 128);
             ptx::mbar_init(ptx::smem_addr(&b.s_full[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&b.p_full[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&b.pv_done[i]), 1);
         }
-        ptx::mbar_init(ptx::smem_addr(&b.p_full), 4);
-        ptx::mbar_init(ptx::smem_addr(&b.pv_done), 1);
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
         ptx::fence_barrier_init();
@@ -802,7 +819,7 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
     const uint32_t tm = b.tmem;
     const int64_t T = b.total, R = min((int64_t)p.ranges, T);
     if (range < R) {   // (else: fewer tiles than ranges)
-        const int64_t lo = p4_start(range, T, R), hi = p4_start(range + 1, T, R);
+        const int64_t lo = b.lo, hi = b.hi;
         if (warp < kP4Keys)
             p4_softmax<D, N>(p, b, sbase, ex, tm, warp, lane, range, lo, hi);
         else if (warp < kP4Values)
@@ -812,7 +829,7 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
         else if (warp == kP4Prod)
             p4_producer<D, N>(p, b, sbase, lane, lo, hi);
         else if (p4_elect())
-            p4_mma<D, N>(p, b, sbase, tm, lo, hi);
+            p4_mma<D, N>(p, b, sbase, tm);
     }
     ptx::tc_fence_before();
     __syncthreads();

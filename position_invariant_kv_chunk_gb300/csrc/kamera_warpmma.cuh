@@ -108,5 +108,14 @@ __device__ __forceinline__ bool cycle_wait(uint32_t bar, uint32_t parity, volati
     }
 }
 
+// a / b of numbers that are not negative: in 32 bits where both fit (in 64 it takes some
+// hundred cycles, which a short kernel's start feels).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    if (((a | b) >> 32) == 0)
+        return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 }  // namespace wmma16
 }  // namespace kamera
