@@ -10,7 +10,9 @@
 // it) and their own softmax warpgroup; the MMA lane alternates between them:
 //   S [128 x 128]  = Q [128 x 192] K^T      (both from shared memory)
 //   O [128 x 128] += P V                    (P from TMEM, over S's columns, bf16)
-// Both sides see the same rows, so a row is read once for 256 queries.  The weights are
+// Both sides see the same rows, so a row is read once for 256 queries; or, where there
+// are too few queries to fill the GPU that way, the sides have the same 128 queries and
+// every second tile of rows each (SPLIT), and join their states at the end.  The weights are
 // rounded to bf16 (2^-8 of each at the most): a hi + lo pair, as the library's decode
 // kernels take, would be 40% more MMAs here, where they are the bound.
 //   warps 0-3, 4-7  softmax of side A, B: thread = query = TMEM lane; running maximum
@@ -45,13 +47,17 @@ constexpr int kPrRows = 128, kPrTok = 128;
 constexpr int kPrQk = 192, kPrNope = 128, kPrV = 128;
 constexpr int kPrThreads = 384;
 constexpr int kPrProd = 8, kPrMma = 10;
-constexpr int kPrUnits = 8;             // ring
 constexpr int kPrTile = 5;              // units of a tile: three of keys, two of values
 constexpr uint32_t kPrUnit = 16384;     // 128 rows x 128 bytes
 constexpr float kPrLazy = 8.0f;
-constexpr uint32_t kPrQ = 0;            // [2 sides][3 blocks of 64 columns][128 rows][128 bytes]
-constexpr uint32_t kPrRing = 6 * kPrUnit;
-constexpr uint32_t kPrBar = kPrRing + kPrUnits * kPrUnit;
+// Queries ([1 or 2 sides][3 blocks of 64 columns][128 rows][128 bytes]) and the ring share
+// 14 units: one block of queries leaves the ring eleven, two leave it eight.
+template <bool SPLIT>
+struct PrLayout {
+    static constexpr int kQUnits = SPLIT ? 3 : 6, kUnits = 14 - kQUnits;
+    static constexpr int kQueries = SPLIT ? kPrRows : 2 * kPrRows;   // of a CTA
+};
+constexpr uint32_t kPrBar = 14 * kPrUnit;
 constexpr uint32_t kPrBytes = kPrBar + 512 + 1024;
 constexpr uint32_t kPrTmS = 0, kPrTmO = 2 * kPrTok;
 static_assert(kPrBytes <= 227 * 1024, "shared memory");
@@ -61,7 +67,7 @@ struct PrParams {
     float* lse;                    // or null
     const int32_t* q_start;
     const int32_t* kv_start;
-    int32_t n_q, n_kv, n_seqs, H, max_q, blocks;   // blocks: of 256 queries of a sequence
+    int32_t n_q, n_kv, n_seqs, H, max_q, blocks;   // blocks: of a CTA's queries, of a sequence
     int32_t causal, wide;          // wide: out is 32-byte aligned
     float scale;
     int32_t* err;
@@ -75,7 +81,7 @@ struct PrLaunch {
 };
 
 struct PrBars {
-    uint64_t full[kPrUnits], empty[kPrUnits];
+    uint64_t full[11], empty[11];
     uint64_t q_full, s_full[2], p_full[2][2], pv_done[2], drained;   // p_full: tokens 0-63, 64-127 of the tile
     uint32_t tmem;
     int32_t abort;
@@ -83,6 +89,7 @@ struct PrBars {
 static_assert(sizeof(PrBars) <= 512, "barrier block");
 
 // What a CTA does, worked out alike by every role.
+template <bool SPLIT>
 struct PrWork {
     int h, q0, k0;           // head, the block's first query and the sequence's first row (of all)
     int rows;                // queries of the block
@@ -90,10 +97,15 @@ struct PrWork {
     int tiles_a, tiles_b;
     __device__ __forceinline__ int tiles(int a) const { return a ? tiles_b : tiles_a; }
     __device__ __forceinline__ int most() const { return max(tiles_a, tiles_b); }
+    __device__ __forceinline__ int all() const { return SPLIT ? tiles_a + tiles_b : most(); }
+    // side a's i-th tile; its first query (of the CTA's)
+    __device__ __forceinline__ static int tile(int a, int i) { return SPLIT ? 2 * i + a : i; }
+    __device__ __forceinline__ static int query0(int a) { return SPLIT ? 0 : a * kPrRows; }
     __device__ __forceinline__ int side_rows(int a) const { return min(kPrRows, rows - a * kPrRows); }
 };
 
-__device__ __forceinline__ int pr_tiles(const PrParams& p, const PrWork& w, int a)
+template <bool SPLIT>
+__device__ __forceinline__ int pr_tiles(const PrParams& p, const PrWork<SPLIT>& w, int a)
 {
     const int r = w.side_rows(a);
     if (r <= 0)
@@ -103,8 +115,10 @@ __device__ __forceinline__ int pr_tiles(const PrParams& p, const PrWork& w, int 
 }
 
 // False: nothing to do (no queries, or a malformed sequence).
-__device__ __forceinline__ bool pr_work(const PrParams& p, PrWork& w)
+template <bool SPLIT>
+__device__ __forceinline__ bool pr_work(const PrParams& p, PrWork<SPLIT>& w)
 {
+    constexpr int kQueries = PrLayout<SPLIT>::kQueries;
     int id = blockIdx.x;
     w.h = id % p.H;
     id /= p.H;
@@ -120,29 +134,33 @@ __device__ __forceinline__ bool pr_work(const PrParams& p, PrWork& w)
             raise_err(p.err, bits);
         return false;
     }
-    const int nq = b - a, first = 2 * kPrRows * blk;
-    w.rows = min(2 * kPrRows, nq - first);
+    const int nq = b - a, first = kQueries * blk;
+    w.rows = min(kQueries, nq - first);
     if (w.rows <= 0)
         return false;
     w.q0 = a + first;
     w.k0 = c;
     w.nk = d - c;
     w.shift = w.nk - nq + first;
-    w.tiles_a = pr_tiles(p, w, 0);
-    w.tiles_b = pr_tiles(p, w, 1);
+    const int n = pr_tiles(p, w, 0);
+    w.tiles_a = SPLIT ? (n + 1) / 2 : n;
+    w.tiles_b = SPLIT ? n / 2 : pr_tiles(p, w, 1);
     return true;
 }
 
-__device__ void pr_producer(const PrLaunch& L, const PrWork& w, PrBars& b, uint32_t sbase)
+template <bool SPLIT>
+__device__ void pr_producer(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b, uint32_t sbase)
 {
     const PrParams& p = L.p;
     const uint32_t q_full = ptx::smem_addr(&b.q_full);
-    const int sides = w.rows > kPrRows ? 2 : 1, n = w.most();
+    constexpr int kPrUnits = PrLayout<SPLIT>::kUnits;
+    constexpr uint32_t kPrRing = PrLayout<SPLIT>::kQUnits * kPrUnit;
+    const int sides = w.rows > kPrRows ? 2 : 1, n = w.all();
     if (p.withhold)
         return;
     ptx::mbar_arrive_expect_tx(q_full, (uint32_t)sides * 3 * kPrUnit);
     for (int i = 0; i < 3 * sides; ++i)
-        ptx::tma_load_3d(sbase + kPrQ + i * kPrUnit, &L.map_q, 64 * (i % 3), w.h, w.q0 + kPrRows * (i / 3), q_full);
+        ptx::tma_load_3d(sbase + i * kPrUnit, &L.map_q, 64 * (i % 3), w.h, w.q0 + kPrRows * (i / 3), q_full);
     uint32_t k = 0;
     bool ok = true;
     for (int t = 0; t < n && ok; ++t)
@@ -190,27 +208,29 @@ __device__ __forceinline__ bool pr_elect()
 // and its weights 200 (the first half of the weights starts the product early).  TMEM
 // addresses are offsets: the CTA holds all 512 columns, so its allocation starts at
 // address 0.
-__device__ void pr_mma(const PrLaunch& L, const PrWork& w, PrBars& b, uint32_t sbase)
+template <bool SPLIT>
+__device__ void pr_mma(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b, uint32_t sbase)
 {
     const PrParams& p = L.p;
     constexpr uint32_t idS = ptx::idesc_bf16_f32(kPrRows, kPrTok);
     constexpr uint32_t idV = ptx::idesc_bf16_f32(kPrRows, kPrV) | (1u << 16);   // value rows: MN-major
-    const uint32_t q_lo = ((sbase + kPrQ) >> 4) | (1u << 16), r_lo = (sbase + kPrRing) >> 4;
+    constexpr int kPrUnits = PrLayout<SPLIT>::kUnits;
+    const uint32_t q_lo = (sbase >> 4) | (1u << 16), r_lo = (sbase + PrLayout<SPLIT>::kQUnits * kPrUnit) >> 4;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
-    // scores of side a's tile t; the tile's keys are free after its last side
+    // scores of side a's t-th tile; its keys are free after the last side that sees it
     auto scores = [&](auto side, int t) -> bool {
         constexpr int a = decltype(side)::value;
         constexpr uint32_t dS = kPrTmS + a * kPrTok;
-        const bool free = a == 1 || t >= w.tiles_b;
+        const bool free = SPLIT || a == 1 || t >= w.tiles_b;
 #pragma unroll
         for (int u = 0; u < 3; ++u) {
-            const uint32_t k = (uint32_t)(kPrTile * t + u), at = k % kPrUnits;
+            const uint32_t k = (uint32_t)(kPrTile * w.tile(a, t) + u), at = k % kPrUnits;
             if (!wait(&b.full[at], k / kPrUnits))
                 return false;
             ptx::tc_fence_after();
-            const uint32_t aq = q_lo + (3 * a + u) * (kPrUnit >> 4), bk = (r_lo + at * (kPrUnit >> 4)) | (1u << 16);
+            const uint32_t aq = q_lo + ((SPLIT ? 0 : 3 * a) + u) * (kPrUnit >> 4), bk = (r_lo + at * (kPrUnit >> 4)) | (1u << 16);
             if (u == 0)
                 mma_ss<false>(dS, aq, bk, idS);
             else
@@ -227,7 +247,7 @@ __device__ void pr_mma(const PrLaunch& L, const PrWork& w, PrBars& b, uint32_t s
     auto weigh = [&](auto side, int t) -> bool {
         constexpr int a = decltype(side)::value;
         constexpr uint32_t dO = kPrTmO + a * kPrV, aP = kPrTmS + a * kPrTok;
-        const uint32_t k = (uint32_t)(kPrTile * t + 3), at0 = k % kPrUnits, at1 = (k + 1) % kPrUnits;
+        const uint32_t k = (uint32_t)(kPrTile * w.tile(a, t) + 3), at0 = k % kPrUnits, at1 = (k + 1) % kPrUnits;
         if (!wait(&b.full[at0], k / kPrUnits) || !wait(&b.full[at1], (k + 1) / kPrUnits))
             return false;
 #pragma unroll
@@ -245,7 +265,7 @@ __device__ void pr_mma(const PrLaunch& L, const PrWork& w, PrBars& b, uint32_t s
                     mma_ts<true>(dO, aP + 8 * (4 * half + i), v + 128 * i, idV);
         }
         ptx::umma_commit(ptx::smem_addr(&b.pv_done[a]));
-        if (a == 1 || t >= w.tiles_b) {
+        if (SPLIT || a == 1 || t >= w.tiles_b) {
             ptx::umma_commit(ptx::smem_addr(&b.empty[at0]));
             ptx::umma_commit(ptx::smem_addr(&b.empty[at1]));
         }
@@ -289,11 +309,26 @@ __device__ __forceinline__ void pr_store(__nv_bfloat16* dst, const uint32_t (&w)
     }
 }
 
+// A barrier of both sides: whether all of their threads said yes.
+__device__ __forceinline__ bool pr_all(bool ok)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 256, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(ok ? 1u : 0u)
+                 : "memory");
+    return r != 0;
+}
+
 // Side a's softmax, thread r = query r of the side = TMEM lane r.
-__device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32_t sbase, uint32_t tm, int a, int r)
+template <bool SPLIT>
+__device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b, uint32_t sbase, uint32_t tm, int a, int r)
 {
     const PrParams& p = L.p;
-    const int nt = w.tiles(a), query = a * kPrRows + r;
+    constexpr int kPrUnits = PrLayout<SPLIT>::kUnits;
+    constexpr uint32_t kPrRing = PrLayout<SPLIT>::kQUnits * kPrUnit;
+    const int nt = w.tiles(a), query = w.query0(a) + r;
     const bool valid = query < w.rows;
     const uint32_t lanes = tm + ((uint32_t)(r & ~31) << 16);
     const uint32_t tS = lanes + kPrTmS + a * kPrTok, tO = lanes + kPrTmO + a * kPrV;
@@ -301,7 +336,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
     // masked score stays infinite under it (a score of 2^100 still rounds to 0)
     const float sl2 = p.scale == 0.f ? 1.17549435e-38f : p.scale * 1.4426950408889634f;
     const int limit = p.causal ? min(w.nk, query + w.shift + 1) : w.nk;   // rows that the query sees
-    const int least = p.causal ? min(w.nk, a * kPrRows + w.shift + 1) : w.nk;   // ... that the side's first one sees
+    const int least = p.causal ? min(w.nk, w.query0(a) + w.shift + 1) : w.nk;   // ... that the side's first one sees
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int t = 0; t < nt; ++t) {
@@ -317,7 +352,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
         for (int c = 0; c < 4; ++c)
             tmem_ld32_issue(tS + 32 * c, s[c]);
         tmem_ld_wait128(s);
-        const int base = t * kPrTok;
+        const int base = w.tile(a, t) * kPrTok;
         if (base + kPrTok > least) {
             const int mine = limit - base;   // columns of the tile that this query sees
 #pragma unroll
@@ -374,7 +409,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
             }
         }
         if (base + kPrTok > w.nk) {   // value rows past the sequence: zero, so that zero weights add nothing
-            const uint32_t k = (uint32_t)(kPrTile * t + 3);
+            const uint32_t k = (uint32_t)(kPrTile * w.tile(a, t) + 3);
             bool in = true;
             for (int u = 0; u < 2; ++u)
                 in = in && wmma16::cycle_wait(ptx::smem_addr(&b.full[(k + u) % kPrUnits]), ((k + u) / kPrUnits) & 1u, &b.abort,
@@ -426,6 +461,56 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
     }
+    if constexpr (SPLIT) {
+        // The sides have seen every second tile each: they exchange their state and half
+        // of their output's columns through the ring, which nobody reads any more, and
+        // either finishes the other half, 2^(m_a - m) O_a + 2^(m_b - m) O_b.
+        if (!pr_all(ok))
+            return;              // both sides
+        auto theirs = [&](int side, int c) { return sbase + kPrRing + (uint32_t)((side * 66 + c) * kPrRows + r) * 4; };
+        auto put = [&](uint32_t at, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory"); };
+        auto get = [&](uint32_t at) {
+            float v;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+            return v;
+        };
+        put(theirs(a ^ 1, 64), __float_as_uint(m_run));
+        put(theirs(a ^ 1, 65), __float_as_uint(l_run));
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            uint32_t o[32];
+            if (nt > 0)
+                tmem_ld32(tO + 64 * (a ^ 1) + 32 * c, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                put(theirs(a ^ 1, 32 * c + j), nt > 0 ? o[j] : 0u);
+        }
+        pr_all(true);
+        const float m_other = get(theirs(a, 64)), l_other = get(theirs(a, 65)), m = fmaxf(m_run, m_other);
+        const float f = m_run == -INFINITY ? 0.f : pf_ex2(m_run - m), f_other = m_other == -INFINITY ? 0.f : pf_ex2(m_other - m);
+        const float l = l_run * f + l_other * f_other;
+        const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+        const int64_t row = (int64_t)(w.q0 + query) * p.H + w.h;
+        if (valid && p.lse && a == 0)
+            p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : (l == l ? -INFINITY : l);
+        const float g = f * inv, g_other = f_other * inv;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+            uint32_t o[32], x[16];
+            if (nt > 0)
+                tmem_ld32(tO + 64 * a + 32 * c, o);
+            float y[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                y[j] = fmaf(get(theirs(a, 32 * c + j)), g_other, nt > 0 ? __uint_as_float(o[j]) * g : 0.f);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                x[j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+            if (valid)
+                pr_store(p.out + row * kPrV + 64 * a + 32 * c, x, p.wide != 0);
+        }
+        return;
+    }
     if (!ok)
         return;
     const float inv = l_run > 0.f ? 1.f / l_run : (l_run == l_run ? 0.f : l_run);
@@ -445,6 +530,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork& w, PrBars& b, uint32
     }
 }
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid_constant__ PrLaunch L)
 {
     const PrParams& p = L.p;
@@ -453,7 +539,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid
     PrBars& b = *reinterpret_cast<PrBars*>(raw + pad + kPrBar);
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kPrUnits; ++i) {
+        for (int i = 0; i < PrLayout<SPLIT>::kUnits; ++i) {
             ptx::mbar_init(ptx::smem_addr(&b.full[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&b.empty[i]), 1);
         }
@@ -469,7 +555,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid
         ptx::fence_barrier_init();
     }
     ptx::grid_wait();
-    PrWork w;
+    PrWork<SPLIT> w;
     if (!pr_work(p, w))   // (the CTA)
         return;
     if (warp == kPrMma) {
@@ -519,8 +605,15 @@ int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct 
     if (x->nope_dim != kPrNope || x->rope_dim != kPrQk - kPrNope || x->v_dim != kPrV || x->num_heads > 128 ||
         x->n_kv > (1 << 30) || x->n_q > (1 << 30))
         return KAMERA_ERR_UNSUPPORTED;
-    const int64_t blocks = ((int64_t)x->max_q + 2 * kPrRows - 1) / (2 * kPrRows);
-    const int64_t ctas = blocks * x->n_seqs * x->num_heads;
+    auto blocks_of = [&](int rows) { return ((int64_t)x->max_q + rows - 1) / rows; };
+    const int64_t pairs = (int64_t)x->n_seqs * x->num_heads;
+    // One block of queries a CTA, its tiles split between the sides, while that makes no
+    // more than two CTAs an SM: then blocks of 256 would leave SMs idle or half of a CTA's
+    // sides (16 heads; 777 queries behind 1296 rows, 112 such CTAs: 21 us against 35; 2000
+    // behind 4000, 256: 78 against 87; 2432, 304: 29 against 37).  With more, rows are
+    // better read once for 256 queries (4 x 1200, 640: 39 against 30).
+    const bool split = blocks_of(kPrRows) * pairs <= 2 * (int64_t)device_sms();
+    const int64_t blocks = blocks_of(split ? kPrRows : 2 * kPrRows), ctas = blocks * pairs;
     if (ctas > 0x7FFFFFFF)
         return KAMERA_ERR_UNSUPPORTED;
     if (x->n_seqs == 0 || x->n_q == 0 || blocks == 0)
@@ -582,11 +675,13 @@ int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct 
         !make_rows_map(&L.map_k, kv, rows, kvw, kt, 64, kPrTok) || !make_rows_map(&L.map_v, kv, rows, kvw, kt, 64, 64) ||
         !make_rows_map(&L.map_r, kr, rows, kPrQk - kPrNope, rt, 64, kPrTok))
         return KAMERA_ERR_CUDA;
-    // set at every launch: the attribute belongs to the current device's context
-    if (cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrBytes) !=
-            cudaSuccess ||
-        launch_after(mla_prefill_kernel, dim3((unsigned)ctas), kPrThreads, kPrBytes, reinterpret_cast<cudaStream_t>(stream),
-                     true, L) != cudaSuccess)
+    auto launch = [&](auto kernel) {
+        // set at every launch: the attribute belongs to the current device's context
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPrBytes) == cudaSuccess &&
+               launch_after(kernel, dim3((unsigned)ctas), kPrThreads, kPrBytes, reinterpret_cast<cudaStream_t>(stream), true,
+                            L) == cudaSuccess;
+    };
+    if (!(split ? launch(mla_prefill_kernel<true>) : launch(mla_prefill_kernel<false>)))
         return KAMERA_ERR_CUDA;
     return KAMERA_OK;
 }

@@ -299,6 +299,19 @@ def test_prefill_matches_definition(H, nq, nk, causal):
     L.near(out, lse, refs, 192, 2.0 ** -8, (H, nq, nk, causal))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_of_many_blocks_matches_definition(causal):
+    """More blocks of queries than two an SM: two blocks share the rows that a CTA reads."""
+    g = gen(77)
+    H, nq, nk = 18, [300, 1, 0, 257, 40, 3], [300, 131, 7, 400, 40, 260]
+    qs, ks = starts(nq), starts(nk)
+    q, kv, kr = normal(g, qs[-1], H, 192), normal(g, ks[-1], H, 256), normal(g, ks[-1], 64)
+    out, lse = K.kamera_mla_prefill_attend(q, kv, kr, i32(qs), i32(ks), max(nq), causal=causal)
+    torch.cuda.synchronize()
+    refs, _ = prefill_refs(q, kv, kr, qs, ks, 192 ** -0.5, causal)
+    L.near(out, lse, refs, 192, 2.0 ** -8, causal)
+
+
 @pytest.mark.parametrize("scale", [-0.07, 0.0, 2.0])
 def test_prefill_of_views_gaps_and_scales(scale):
     """Queries inside a wider projection, heads apart, rows with gaps of NaN between the
