@@ -3,11 +3,12 @@
 // 16 numbers share a scale s (e4m3) and are each a level of e2m1 (0, 0.5, 1, 1.5, 2,
 // 3, 4, 6) times s.  s = rn(max |x| / (6 unit)); a number's code is rn(x / (s unit)).
 // Both roundings are decided exactly:
-//   - a bf16 maximum over 6 lies at least 2^-11 of itself from a tie of e4m3 or on it,
-//     where the fp32 quotient is exact;
+//   - a bf16 maximum over 6 lies at least 2^-11 of itself from a tie of e4m3 or on it, so
+//     the product with fp32's 1/6 (2^-23 off at most) is rounded to 14 bits first, which
+//     puts ties (five bits) back where they belong;
 //   - x / s (8 bits over 4) lies on a tie of e2m1 or at least 2^-10 from it, so the
-//     product with the rounded reciprocal (2^-22 off at most) is rounded to a multiple
-//     of 2^-13 first, which puts ties back where they belong.
+//     product with the reciprocal (2^-22 off at most) is likewise rounded to a multiple
+//     of 2^-13 first.
 // What attention reads (kamera_packed.cu) sets the layout: 16 tokens of a head are one
 // run of 18 d bytes,
 //   keys     [d / 32][16 tokens][16 bytes]   32 channels of a token in 16 bytes
@@ -16,7 +17,9 @@
 // so that a thread per token (keys) or per channel (values) reads its numbers in whole
 // vectors without bank conflicts.
 // A warp takes 16 tokens of a head: 8 d values, all its loads in flight at once.
-// Bound by memory: 65536 tokens of four heads of 128 (172 MB either way).
+// Bound by memory: 65536 tokens of four heads of 128, 172 MB either way, take 30 us to
+// pack and 25.5 to unpack (5.7 and 6.7 TB/s).  Packing has most of its instructions in the
+// rounding: divisions in it, instead of products rounded once more, cost 5 us.
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -28,6 +31,7 @@
 #include "kamera_internal.h"
 #include "kamera_packed.h"
 #include "kamera_ptx.cuh"
+#include "kamera_warpmma.cuh"
 
 namespace kamera {
 
@@ -62,9 +66,9 @@ __device__ __forceinline__ bool pack_item(const PackParams& p, PackItem& it)
     const int64_t item = (int64_t)blockIdx.x * kPkWarps + (threadIdx.x >> 5);
     if (item >= p.items)
         return false;
-    const int64_t at = item / p.H;
+    const int64_t at = wmma16::quotient(item, p.H);
     it.h = (int)(item - at * p.H);
-    const int64_t e = at / p.pieces;
+    const int64_t e = wmma16::quotient(at, p.pieces);
     const int piece = (int)(at - e * p.pieces);
     const int64_t a = p.kv_pages[e], b = p.packed_pages[e];
     const int n = p.tokens[e];
@@ -98,12 +102,15 @@ __device__ __forceinline__ uint32_t drop_nan(uint32_t w)
 __device__ __forceinline__ uint32_t group_scale(uint32_t amax, float unit, float& factor)
 {
     // (an infinity saturates to 448; the unit is a power of two)
-    const float want = __fdiv_rn(__uint_as_float(amax << 16) * (1.f / unit), 6.f);
+    const float sixth = __uint_as_float(amax << 16) * (1.f / unit) * (1.f / 6.f);
+    const float want = __uint_as_float((__float_as_uint(sixth) + 0x200u) & ~0x3FFu);
     uint16_t two;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(want));
     const uint32_t byte = two & 0xFFu;
     const float s = e4m3_to_float(byte);
-    factor = byte ? 1.f / s * (1.f / unit) : 0.f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));   // (2^-23 off at most; s is 2^-9 to 448)
+    factor = byte ? inv * (1.f / unit) : 0.f;
     return byte;
 }
 
@@ -112,7 +119,13 @@ __device__ __forceinline__ uint32_t codes2(float a, float b, float factor)
 {
     constexpr float kRound = 1536.f;   // the sum's last place is 2^-13
     uint16_t r;
-    const float x = fmaf(a, factor, kRound) - kRound, y = fmaf(b, factor, kRound) - kRound;
+    const uint64_t f2 = ptx::f2_make(__float_as_uint(factor), __float_as_uint(factor));
+    const uint64_t up = ptx::f2_make(__float_as_uint(kRound), __float_as_uint(kRound));
+    const uint64_t down = ptx::f2_make(__float_as_uint(-kRound), __float_as_uint(-kRound));
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;"
+        : "=f"(x), "=f"(y)
+        : "l"(ptx::f2_add(ptx::f2_fma(ptx::f2_make(__float_as_uint(a), __float_as_uint(b)), f2, up), down)));
     asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u16.u8 %0, t;\n\t}" : "=h"(r) : "f"(y), "f"(x));
     return r;
 }

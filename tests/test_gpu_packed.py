@@ -99,6 +99,25 @@ def test_packing_borders():
     assert np.array_equal(R.f64(bk), pk) and np.array_equal(R.f64(bv), pv)
 
 
+def test_packing_scale_of_every_maximum():
+    """Every finite bf16 magnitude as a group's largest number, half of it and less beside."""
+    P, H, d = 16, 1, 128
+    x = torch.zeros(0x8000, 16, device=DEV)
+    x[:0x7F80, 0] = torch.arange(0x7F80, device=DEV, dtype=torch.int32).to(torch.int16).view(BF).float()
+    x[:, 1:] = x[:, :1] * (1 - 2 * (torch.arange(15, device=DEV) % 2)) * torch.linspace(0.01, 0.5, 15, device=DEV)
+    x = x.to(BF)
+    n = len(x) * 16 // (P * d)
+    k = x.view(n * P, H, d).contiguous()
+    v = x.view(n, d, 16).transpose(1, 2).reshape(n * P, H, d).contiguous()
+    packed, bk, bv = packed_like(n, H, P, d), torch.empty_like(k), torch.empty_like(v)
+    ids, full = whole(n, P)
+    for units in ((1.0, 1.0), (2.0 ** -40, 2.0 ** 30)):
+        K.kamera_pack_pages(k, v, P, ids, full, packed, ids, *units)
+        K.kamera_unpack_pages(packed, P, ids, full, bk, bv, ids, *units)
+        pk, pv = pack_ref(k, v, P, n, *units)
+        assert np.array_equal(R.f64(bk), pk) and np.array_equal(R.f64(bv), pv), units
+
+
 def test_packing_extremes():
     """Zeros, numbers too small for a scale, saturation, infinities, NaN."""
     P, H, d = 16, 2, 64
