@@ -212,6 +212,14 @@ __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
 }
 
 // ---------------------------------------------------------------- producer --
+// --------------------------------------------------------------------- MMA --
+__device__ __forceinline__ bool mp_elect()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 template <int N>
 __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int lane, int block)
 {
@@ -248,81 +256,88 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
     advance(lane / kPieces);
     int page, row, page_next = -1, row_next = 0, group = 0;
     look_up(page, row);
+    const uint32_t starts = R == 16 ? 0xFu : R == 32 ? 0x5u : 0x1u;   // the pieces at which a box of R rows starts
+    // The lane that waits and issues has these to itself.
+    uint32_t unit = 0, rope = 0, seg = 0, at = 0, lap = 0, ra = 0, rl = 0;   // issued so far; places in the rings
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        bool got = true;
-        if (lane == 0)
-            got = wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
-        return __shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0) != 0;
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
-    uint32_t unit = 0, rope = 0, tile = 0, seg = 0, there = 0;
-    uint32_t at = 0, lap = 0;      // place in the ring
-    bool ok = true, good = false;
+    uint32_t tile = 0, there = 0;
+    bool ok = true;
     while (w.left > 0 && ok) {
-        if (w.fresh) {
-            if (seg > 0 && !(ok = wait(&b.q_empty, seg - 1)))
-                break;
-            if (lane == 0 && !p.withhold) {
-                ptx::mbar_arrive_expect_tx(ptx::smem_addr(&b.q_full), 9 * Y::kQBlock);
-                for (int i = 0; i < 9; ++i)
-                    ptx::tma_load_2d(sbase + Y::kQ + i * Y::kQBlock, &L.map_q, 64 * i, w.s * p.Hq + block * N,
-                                     ptx::smem_addr(&b.q_full));
-            }
-            ++seg;
-        }
         if (tile % kAhead == 0) {
             if (tile > 0) {
                 page = page_next;
                 row = row_next;
             }
-            good = page >= 0 && page < p.num_pages;
+            const bool good = page >= 0 && page < p.num_pages;
             if (page != -1 && !good && block == 0)
                 raise_err(p.err, KAMERA_DEVERR_SLOT);
             group = (int)(((int64_t)page * p.P + row) >> 3);
             there = __ballot_sync(0xFFFFFFFFu, good);
         }
-        const uint32_t mask = (there >> (kPieces * (tile % kAhead))) & 0xFu;
-        const bool box = lane / kPieces == (int)(tile % kAhead) && good && off % R == 0;
-        const int n = __popc(__ballot_sync(0xFFFFFFFFu, box));
-        w.next(p);
-        if (lane == 0)
-            b.mask[tile % kMpMasks] = mask;
-        auto load = [&](uint32_t dst, uint64_t* bar, const CUtensorMap* map, int col, uint32_t row_group) {
-            const uint32_t full = ptx::smem_addr(bar);
-            if (lane == 0 && !p.withhold) {
+        const uint32_t mask = (there >> (kPieces * (tile % kAhead))) & 0xFu, boxes = mask & starts;
+        const int n = __popc(boxes);
+        int groups[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            groups[i] = __shfl_sync(0xFFFFFFFFu, group, kPieces * (int)(tile % kAhead) + i);
+        // One lane for all of a tile: a step that the warp takes together, or that lanes
+        // take each by itself, costs this warp 150 cycles and more, and 580 a unit made it
+        // what the whole CTA waited for.
+        if (mp_elect()) {
+            auto load = [&](uint32_t dst, uint32_t full, const CUtensorMap* map, int col, uint32_t row_group) {
+                if (p.withhold)
+                    return;
                 if (n > 0)
-                    ptx::mbar_arrive_expect_tx(full, (uint32_t)n * (uint32_t)(R / 8) * row_group);
+                    ptx::mbar_arrive_expect_tx(full, (uint32_t)(n * (R >> 3)) * row_group);
                 else
                     ptx::mbar_arrive(full);
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    if ((boxes >> i) & 1u)
+                        ptx::tma_load_4d(dst + 2 * i * row_group, map, 0, 0, col, groups[i], full);
+            };
+            if (w.fresh && (seg == 0 || (ok = wait(&b.q_empty, seg - 1)))) {
+                if (!p.withhold) {
+                    ptx::mbar_arrive_expect_tx(ptx::smem_addr(&b.q_full), 9 * Y::kQBlock);
+                    for (int i = 0; i < 9; ++i)
+                        ptx::tma_load_2d(sbase + Y::kQ + i * Y::kQBlock, &L.map_q, 64 * i, w.s * p.Hq + block * N,
+                                         ptx::smem_addr(&b.q_full));
+                }
+                ++seg;
             }
-            __syncwarp();
-            if (box && !p.withhold)
-                ptx::tma_load_4d(dst + (uint32_t)(off / 8) * row_group, map, 0, 0, col, group, full);
-        };
-        for (int u = 0; u < kMpUnits && ok; ++u, ++unit) {
-            if (lap > 0 && !(ok = wait(&b.empty[at], lap - 1)))
-                break;
-            load(sbase + Y::kRing + at * kMpUnit, &b.full[at], &L.map_c, 2 * u, 2 * kMpAtom);
-            if (++at == (uint32_t)Y::NU) {
-                at = 0;
-                ++lap;
+            b.mask[tile % kMpMasks] = mask;
+            for (int u = 0; u < kMpUnits && ok; ++u) {
+                if (lap > 0 && !(ok = wait(&b.empty[at], lap - 1)))
+                    break;
+                load(sbase + Y::kRing + at * kMpUnit, ptx::smem_addr(&b.full[at]), &L.map_c, 2 * u, 2 * kMpAtom);
+                ++unit;
+                if (++at == (uint32_t)Y::NU) {
+                    at = 0;
+                    ++lap;
+                }
+            }
+            if (ok && (rl == 0 || (ok = wait(&b.rempty[ra], rl - 1)))) {
+                load(sbase + Y::kRopes + ra * kMpRope, ptx::smem_addr(&b.rfull[ra]), &L.map_r, kMpDim / 64, kMpAtom);
+                ++rope;
+                if (++ra == (uint32_t)Y::NR) {
+                    ra = 0;
+                    ++rl;
+                }
             }
         }
-        if (!ok)
-            break;
-        const uint32_t ra = rope % Y::NR, rl = rope / Y::NR;
-        if (rl > 0 && !(ok = wait(&b.rempty[ra], rl - 1)))
-            break;
-        load(sbase + Y::kRopes + ra * kMpRope, &b.rfull[ra], &L.map_r, kMpDim / 64, kMpAtom);
-        ++rope;
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (tile % kAhead == 0) {  // the eight tiles after these
             advance(kAhead);
             look_up(page_next, row_next);
         }
+        w.next(p);
         ++tile;
     }
-    // Without a timeout the MMA lane has waited for every fill.  After one, the copies
-    // this warp started land before the CTA leaves.
-    if (lane == 0 && !p.withhold && *static_cast<volatile int32_t*>(&b.abort)) {
+    // Without a timeout the MMA lanes have waited for every fill.  After one, the copies
+    // started here land before the CTA leaves.
+    if (mp_elect() && !p.withhold && *static_cast<volatile int32_t*>(&b.abort)) {
         if (seg > 0)
             pf_drain_wait(ptx::smem_addr(&b.q_full), (seg - 1) & 1u, p.wait_ns);
         for (uint32_t k = unit > (uint32_t)Y::NU ? unit - Y::NU : 0u; k < unit; ++k)
@@ -331,14 +346,6 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
             pf_drain_wait(ptx::smem_addr(&b.rfull[k % Y::NR]), (k / Y::NR) & 1u, p.wait_ns);
     }
     __syncwarp();
-}
-
-// --------------------------------------------------------------------- MMA --
-__device__ __forceinline__ bool mp_elect()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
 }
 
 // MMAs whose A (mma_ds) or B (mma_sd) is a unit, groups of eight rows 2 KB apart; the
