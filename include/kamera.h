@@ -950,7 +950,8 @@ int kamera_mla_expand(const KameraPagedMlaKV* kv, const KameraMlaExpand* x, int3
  *     out = softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
  * fp32 accumulation of bf16 products, softmax weights rounded to bf16 (2^-8 of each
  * at the most), one bf16 rounding of the output.  A query that sees no row gets zeros
- * and lse = -infinity.  Rows of q, out and lse that no sequence has stay as they are.
+ * and lse = -infinity.  A row reaches the queries that see it alone, whatever it holds.
+ * Rows of q, out and lse that no sequence has stay as they are.
  *   q       bf16 [n_q][num_heads][nope_dim + rope_dim] (RoPE already applied), element
  *           (t, h, i) at q[t*q_stride + h*q_head_stride + i]
  *   kv      bf16 [n_kv][num_heads][nope_dim + v_dim], heads packed, rows kv_stride apart

@@ -58,7 +58,9 @@ struct PrLayout {
     static constexpr int kQueries = SPLIT ? kPrRows : 2 * kPrRows;   // of a CTA
 };
 constexpr uint32_t kPrBar = 14 * kPrUnit;
-constexpr uint32_t kPrBytes = kPrBar + 512 + 1024;
+constexpr uint32_t kPrOdd = kPrBar + 512;   // [NaN, +inf, -inf][128 value columns]: the first masked row that holds one
+constexpr uint32_t kPrBytes = kPrOdd + 3 * kPrV * 4 + 1024;
+static_assert(3 * kPrV == kPrThreads, "a thread an entry");
 constexpr uint32_t kPrTmS = 0, kPrTmO = 2 * kPrTok;
 static_assert(kPrBytes <= 227 * 1024, "shared memory");
 
@@ -84,7 +86,7 @@ struct PrBars {
     uint64_t full[11], empty[11];
     uint64_t q_full, s_full[2], p_full[2][2], pv_done[2], drained;   // p_full: tokens 0-63, 64-127 of the tile
     uint32_t tmem;
-    int32_t abort;
+    int32_t abort, odd;      // odd: some masked value is not finite
 };
 static_assert(sizeof(PrBars) <= 512, "barrier block");
 
@@ -321,9 +323,64 @@ __device__ __forceinline__ bool pr_all(bool ok)
     return r != 0;
 }
 
+// A masked weight is zero, and zero times a value that is not finite is not zero.  So a
+// value row that some query of a side does not see is looked through, a value that is not
+// finite becomes 0, and its row is noted for its column; what queries that do see it get
+// is added at the end (out of line, both: the code that never runs costs a short prompt's
+// call 2 us in line).
+__device__ __noinline__ void pr_clean(uint32_t at, int in_unit, int row, int32_t* first, int32_t* odd)
+{
+#pragma unroll 1
+    for (int c = 0; c < kPrV; ++c) {
+        const uint32_t a = at + (c >> 6) * (kPrUnit / 2) + sw128(in_unit & 7, (c & 63) >> 3) + (c & 7) * 2;
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a) : "memory");
+        if ((x & 0x7F80) != 0x7F80)
+            continue;
+        atomicMin(first + ((x & 0x7F) ? 0 : (x >> 15) ? 2 : 1) * kPrV + c, row);
+        *static_cast<volatile int32_t*>(odd) = 1;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)0) : "memory");
+    }
+}
+
+// Thread r: row r of the tile; `unit` holds it, `in_unit` is its place there.
+__device__ __forceinline__ void pr_clean_row(uint32_t unit, int in_unit, int row, int32_t* first, int32_t* odd)
+{
+    const uint32_t at = unit + (uint32_t)(in_unit >> 3) * 1024u;
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        uint32_t x[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(at + (i >> 3) * (kPrUnit / 2) + sw128(in_unit & 7, i & 7))
+                     : "memory");
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            most = __vmaxu2(most, x[j] & 0x7FFF7FFFu);
+    }
+    if (max(most & 0xFFFFu, most >> 16) >= 0x7F80u)
+        pr_clean(at, in_unit, row, first, odd);
+}
+
+// A query that sees the rows below `limit`: what is noted for columns c0 .. c1 - 1, added
+// to its output.
+__device__ __noinline__ void pr_add_odd(const int32_t* first, __nv_bfloat16* out, int c0, int c1, int limit)
+{
+    for (int c = c0; c < c1; ++c) {
+        const volatile int32_t* f = first + c;
+        float x = f[0] < limit ? __uint_as_float(0x7FC00000u) : 0.f;
+        x += f[kPrV] < limit ? INFINITY : 0.f;
+        x -= f[2 * kPrV] < limit ? INFINITY : 0.f;
+        if (x != 0.f)
+            out[c] = __float2bfloat16(__bfloat162float(out[c]) + x);
+    }
+}
+
 // Side a's softmax, thread r = query r of the side = TMEM lane r.
 template <bool SPLIT>
-__device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b, uint32_t sbase, uint32_t tm, int a, int r)
+__device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b, uint32_t sbase, uint32_t tm, int a, int r,
+                           int32_t* first)
 {
     const PrParams& p = L.p;
     constexpr int kPrUnits = PrLayout<SPLIT>::kUnits;
@@ -340,6 +397,25 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int t = 0; t < nt; ++t) {
+        const int base = w.tile(a, t) * kPrTok;
+        if (base + kPrTok > least) {   // value rows that not every query of the side sees; while the scores come
+            const uint32_t k = (uint32_t)(kPrTile * w.tile(a, t) + 3);
+            auto unit = [&](int row) { return sbase + kPrRing + (k + (row >> 6)) % kPrUnits * kPrUnit; };
+            bool in = true;
+            for (int u = 0; u < 2; ++u)
+                in = in && wmma16::cycle_wait(ptx::smem_addr(&b.full[(k + u) % kPrUnits]), ((k + u) / kPrUnits) & 1u, &b.abort,
+                                             p.err, p.wait_ns);
+            ok = __all_sync(0xFFFFFFFFu, ok && in);
+            if (base + r >= least && base + r < w.nk)
+                pr_clean_row(unit(r), r & 63, base + r, first, &b.odd);
+            // past the sequence: zero, so that zero weights add nothing
+            for (int i = r; i < (base + kPrTok - w.nk) * 16; i += kPrRows) {
+                const int row = w.nk - base + (i >> 4), in_unit = row & 63;
+                ptx::st_shared_zero16(unit(row) + ((i >> 3) & 1) * (kPrUnit / 2) + (uint32_t)(in_unit >> 3) * 1024u +
+                                      sw128(in_unit & 7, i & 7));
+            }
+            ptx::fence_proxy_async();   // (the product waits for every thread's weights, which follow)
+        }
         if (!wmma16::cycle_wait(ptx::smem_addr(&b.s_full[a]), (uint32_t)t & 1u, &b.abort, p.err, p.wait_ns))
             ok = false;
         if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -352,7 +428,6 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
         for (int c = 0; c < 4; ++c)
             tmem_ld32_issue(tS + 32 * c, s[c]);
         tmem_ld_wait128(s);
-        const int base = w.tile(a, t) * kPrTok;
         if (base + kPrTok > least) {
             const int mine = limit - base;   // columns of the tile that this query sees
 #pragma unroll
@@ -407,20 +482,6 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
                     o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                 tmem_st32(tO + 32 * c, o);
             }
-        }
-        if (base + kPrTok > w.nk) {   // value rows past the sequence: zero, so that zero weights add nothing
-            const uint32_t k = (uint32_t)(kPrTile * w.tile(a, t) + 3);
-            bool in = true;
-            for (int u = 0; u < 2; ++u)
-                in = in && wmma16::cycle_wait(ptx::smem_addr(&b.full[(k + u) % kPrUnits]), ((k + u) / kPrUnits) & 1u, &b.abort,
-                                             p.err, p.wait_ns);
-            ok = __all_sync(0xFFFFFFFFu, ok && in);
-            for (int i = r; i < (base + kPrTok - w.nk) * 16; i += kPrRows) {
-                const int row = w.nk - base + (i >> 4), in_unit = row & 63;
-                ptx::st_shared_zero16(sbase + kPrRing + (k + (row >> 6)) % kPrUnits * kPrUnit + ((i >> 3) & 1) * (kPrUnit / 2) +
-                                      (uint32_t)(in_unit >> 3) * 1024u + sw128(in_unit & 7, i & 7));
-            }
-            ptx::fence_proxy_async();   // (the product waits for every thread's weights, which follow)
         }
         // weights 2^(sl2 s - m), bf16, over the scores' columns
         const float ref = m_run == -INFINITY ? 0.f : m_run;
@@ -509,6 +570,8 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
             if (valid)
                 pr_store(p.out + row * kPrV + 64 * a + 32 * c, x, p.wide != 0);
         }
+        if (valid && *static_cast<volatile int32_t*>(&b.odd))
+            pr_add_odd(first, p.out + row * kPrV, 64 * a, 64 * a + 64, limit);
         return;
     }
     if (!ok)
@@ -528,6 +591,8 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
         if (valid)
             pr_store(p.out + row * kPrV + 32 * c, x, p.wide != 0);
     }
+    if (valid && *static_cast<volatile int32_t*>(&b.odd))
+        pr_add_odd(first, p.out + row * kPrV, 0, kPrV, limit);
 }
 
 template <bool SPLIT>
@@ -552,8 +617,11 @@ __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid
         ptx::mbar_init(ptx::smem_addr(&b.q_full), 1);
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
+        b.odd = 0;
         ptx::fence_barrier_init();
     }
+    int32_t* first = reinterpret_cast<int32_t*>(raw + pad + kPrOdd);
+    first[threadIdx.x] = 0x7FFFFFFF;
     ptx::grid_wait();
     PrWork<SPLIT> w;
     if (!pr_work(p, w))   // (the CTA)
@@ -571,7 +639,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid
     // (256 x 208 + 128 x 56 of the launch's 384 x 168).
     if (warp < 8) {
         ptx::setmaxnreg_inc<208>();
-        pr_softmax(L, w, b, sbase, tm, warp >> 2, threadIdx.x & (kPrRows - 1));
+        pr_softmax(L, w, b, sbase, tm, warp >> 2, threadIdx.x & (kPrRows - 1), first);
     } else {
         ptx::setmaxnreg_dec<56>();
         if (w.most() > 0) {

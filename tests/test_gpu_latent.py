@@ -352,6 +352,40 @@ def test_prefill_neighbours_of_nan_are_untouched():
     assert bool(torch.isnan(out[100:200]).all())
 
 
+@pytest.mark.parametrize("seqs,H", [(1, 2), (4, 40)])
+def test_prefill_masked_values_that_are_not_finite(seqs, H):
+    """A value that is not finite reaches the queries that see its row, in its column, and
+    no other; so does a key (every column)."""
+    g = gen(31)
+    nq, nk = 270, 500                                          # query i sees rows up to i + 230
+    qs, ks = starts([nq] * seqs), starts([nk] * seqs)
+    q, kv, kr = normal(g, qs[-1], H, 192), normal(g, ks[-1], H, 256), normal(g, ks[-1], 64)
+    args = (i32(qs), i32(ks), nq)
+    ref, rl = K.kamera_mla_prefill_attend(q, kv, kr, *args)
+    first = {}                                                 # (head, column) -> first row with one
+    bad = kv.clone()
+    for row, h, c, x in [(499, 0, 3, "nan"), (300, 0, 77, "inf"), (384, 0, 77, "inf"), (231, 1, 127, "-inf"),
+                         (250, 1, 127, "inf"), (260, 1, 64, "nan"), (400, 0, 0, "-inf")]:
+        bad[row, h, 128 + c] = float(x)
+        first.setdefault((h, c), []).append((row, float(x)))
+    out, lse = K.kamera_mla_prefill_attend(q, bad, kr, *args)
+    torch.cuda.synchronize()
+    assert torch.equal(lse, rl)
+    want = ref.clone()
+    for (h, c), rows in first.items():
+        for row, x in rows:
+            want[max(row - 230, 0):nq, h, c] += x              # (inf - inf: NaN)
+    same = (out == want) | (out.isnan() & want.isnan())
+    assert bool(same.all()), same.logical_not().nonzero()[:5]
+    bad = kv.clone()
+    bad[350, 1, 5] = float("nan")
+    out, lse = K.kamera_mla_prefill_attend(q, bad, kr, *args)
+    torch.cuda.synchronize()
+    assert bool(out[120:nq, 1].isnan().all()) and bool(lse[120:nq, 1].isnan().all())
+    out[120:nq, 1], lse[120:nq, 1] = ref[120:nq, 1], rl[120:nq, 1]
+    assert torch.equal(out, ref) and torch.equal(lse, rl)
+
+
 def test_prefill_reports_malformed_sequences():
     g = gen(11)
     q, kv, kr = normal(g, 60, 2, 192), normal(g, 80, 2, 256), normal(g, 80, 64)
