@@ -220,6 +220,14 @@ __device__ __forceinline__ bool mp_elect()
     return r != 0;
 }
 
+// The rows that a load of the same place would bring, into L2.
+__device__ __forceinline__ void mp_prefetch(const CUtensorMap* map, int col, int group)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %1, %2, %3}];" ::"l"(map), "r"(0), "r"(col),
+                 "r"(group)
+                 : "memory");
+}
+
 template <int N>
 __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int lane, int block)
 {
@@ -229,6 +237,7 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
     // after them: pages are looked up, and rows worked out, for 32 pieces at once and
     // eight tiles ahead (under load a look-up takes 2000 cycles).
     constexpr int kPieces = kMpTok / 16, kAhead = 32 / kPieces;
+    constexpr bool kPrefetch = N == 64;
     const int R = p.box_rows, off = 16 * (lane % kPieces);   // a box of R rows is issued by its first piece's lane
     MpWalk w, mine;
     w.start(b);
@@ -262,7 +271,8 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
     };
-    uint32_t tile = 0, there = 0;
+    uint32_t tile = 0, there = 0, there_next = 0;   // (the _next ones: once two tiles on are of the eight after)
+    int group_next = 0;
     bool ok = true;
     while (w.left > 0 && ok) {
         if (tile % kAhead == 0) {
@@ -282,6 +292,22 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
             groups[i] = __shfl_sync(0xFFFFFFFFu, group, kPieces * (int)(tile % kAhead) + i);
+        // The rows of two tiles on are asked into L2 where the ring is short, by each head
+        // block its share of the units: 150 -> 146 us for 128 heads (16 heads, whose ring
+        // is longer: 93.4 -> 94.4, so not there).
+        uint32_t far_boxes = 0;
+        int far[kPieces] = {};
+        if constexpr (kPrefetch) {
+            const int to = (int)(tile % kAhead) + 2;
+            if (to == kAhead) {
+                group_next = (int)(((int64_t)page_next * p.P + row_next) >> 3);
+                there_next = __ballot_sync(0xFFFFFFFFu, page_next >= 0 && page_next < p.num_pages);
+            }
+            far_boxes = ((to < kAhead ? there : there_next) >> (kPieces * (to % kAhead))) & starts;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                far[i] = __shfl_sync(0xFFFFFFFFu, to < kAhead ? group : group_next, kPieces * (to % kAhead) + i);
+        }
         // One lane for all of a tile: a step that the warp takes together, or that lanes
         // take each by itself, costs this warp 150 cycles and more, and 580 a unit made it
         // what the whole CTA waited for.
@@ -326,6 +352,17 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
                     ++rl;
                 }
             }
+            if (kPrefetch && ok && !p.withhold)
+#pragma unroll 1
+                for (int i = 0; i < kPieces; ++i)
+                    if ((far_boxes >> i) & 1u) {
+                        const int g = i == 0 ? far[0] : i == 1 ? far[1] : i == 2 ? far[2] : far[3];
+#pragma unroll 1
+                        for (int u = block; u < kMpUnits; u += p.blocks)
+                            mp_prefetch(&L.map_c, 2 * u, g);
+                        if (block == 0)
+                            mp_prefetch(&L.map_r, kMpDim / 64, g);
+                    }
         }
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (tile % kAhead == 0) {  // the eight tiles after these
@@ -509,32 +546,30 @@ __device__ __forceinline__ void stsm_x4_t(uint32_t a, uint32_t x, uint32_t y, ui
                  : "memory");
 }
 
-// The four warps of softmax group GRP meet.
-template <int GRP>
-__device__ __forceinline__ void mp_sync()
-{
-    asm volatile("bar.sync %0, 128;" ::"n"(1 + 2 * GRP) : "memory");
-}
+// The four warps of a softmax group meet.
+__device__ __forceinline__ void mp_sync(int grp) { asm volatile("bar.sync %0, 128;" ::"r"(1 + 2 * grp) : "memory"); }
 // The same; whether any thread said yes.
-template <int GRP>
-__device__ __forceinline__ bool mp_any(bool x)
+__device__ __forceinline__ bool mp_any(int grp, bool x)
 {
     uint32_t r;
     asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 128, p;\n\t"
                  "selp.u32 %0, 1, 0, q;\n\t}"
                  : "=r"(r)
-                 : "r"(x ? 1u : 0u), "n"(2 + 2 * GRP)
+                 : "r"(x ? 1u : 0u), "r"(2 + 2 * grp)
                  : "memory");
     return r != 0;
 }
 
-// Softmax group GRP: heads GRP HG .. of the block.
-template <int N, int GRP>
-__device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* ex, uint32_t tm, int warp, int lane,
+// Softmax group grp: heads grp HG .. of the block.  One code for all groups: with two
+// copies of it the roles' loops do not fit the instruction cache together (128 heads: 173
+// us instead of 150, a quarter of the stalls for want of instructions).
+template <int N>
+__device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* ex, uint32_t tm, int grp, int warp, int lane,
                            int block, int range, int64_t lo, int64_t hi)
 {
     using Y = MpLayout<N>;
-    constexpr int HG = Y::HG, J = HG / 8, G0 = GRP * HG;
+    constexpr int HG = Y::HG, J = HG / 8;
+    const int G0 = grp * HG;
     const MpParams& p = L.p;
     const int gq = lane >> 2, t4 = lane & 3;
     const uint32_t lanes = tm + ((uint32_t)warp << 21);
@@ -544,7 +579,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
     float* wmax = ex + 5 * G0;     // [4 warps][HG]: the warps' maxima; their sums
     float* fac = wmax + 4 * HG;    // [HG]: factors of the running output
     // the output's rows of this group: whether this warp's lanes hold some, and the lane's head
-    constexpr int Q0 = Y::kPair ? 0 : G0 / 16, Q1 = Q0 + (Y::kPair ? 2 : 1) * HG / 16;
+    const int Q0 = Y::kPair ? 0 : G0 / 16, Q1 = Q0 + (Y::kPair ? 2 : 1) * HG / 16;
     const bool out_warp = warp >= Q0 && warp < Q1;
     const int out_head = out_warp ? (Y::kPair ? 8 * warp + (lane & 7) : 16 * (warp - Q0) + (lane & 15)) : 0;
     float m[J][2], l[J][2];        // heads 8 j + 2 t4, + 1: the agreed maximum (log2 units), this thread's sum
@@ -583,8 +618,8 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                 }
             }
         }
-        if (mp_any<GRP>(grew || !ok)) {   // rare but for a segment's first tile
-            if (mp_any<GRP>(!ok))
+        if (mp_any(grp, grew || !ok)) {   // rare but for a segment's first tile
+            if (mp_any(grp, !ok))
                 break;               // all four warps
 #pragma unroll
             for (int j = 0; j < J; ++j)
@@ -597,7 +632,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                     if (gq == 0)
                         wmax[warp * HG + 8 * j + 2 * t4 + c] = v;
                 }
-            mp_sync<GRP>();
+            mp_sync(grp);
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -617,7 +652,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                 ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.wait_ns);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 ptx::tc_fence_after();
-                mp_sync<GRP>();
+                mp_sync(grp);
                 if (out_warp) {
                     const float f = fac[out_head];
 #pragma unroll 1
@@ -632,7 +667,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                     tmem_wait_st();
                 }
             }
-            mp_sync<GRP>();               // the exchange's arrays are free again
+            mp_sync(grp);               // the exchange's arrays are free again
         }
         // weights, transposed into the operand rows (heads) of the second product
         const uint32_t dst = st + t % Y::NP * Y::kPTile;
@@ -685,7 +720,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
         const int first_slot = (int)(2 * r0 + (mp_start(r0, T, R) == a0 ? 0 : 1));
         const bool whole = r0 == r1;
         const int slot = range == r0 ? first_slot : 2 * range;
-        if (range == r0 && block == 0 && GRP == 0 && warp == 0 && lane == 0)
+        if (range == r0 && block == 0 && grp == 0 && warp == 0 && lane == 0)
             p.span[s_seq] = make_int4((int)r0, (int)r1, first_slot, 0);
 #pragma unroll
         for (int j = 0; j < J; ++j)
@@ -697,7 +732,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                 if (gq == 0)
                     wmax[warp * HG + 8 * j + 2 * t4 + c] = l[j][c];
             }
-        mp_sync<GRP>();
+        mp_sync(grp);
         const int64_t row0 = (int64_t)s_seq * p.Hq + head0, part0 = (int64_t)slot * p.Hq + head0;
         if (warp == 0 && gq == 0) {
 #pragma unroll
@@ -718,7 +753,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
         ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_ns);
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
-        mp_sync<GRP>();
+        mp_sync(grp);
         if (out_warp) {
             const bool mine = ok && out_head < heads;
             const float inv = fac[out_head];
@@ -757,7 +792,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
             }
         }
         ptx::tc_fence_before();
-        mp_sync<GRP>();   // the exchange's arrays, and TMEM, are free for the next segment
+        mp_sync(grp);   // the exchange's arrays, and TMEM, are free for the next segment
         w.next(p);
     }
 }
@@ -817,10 +852,8 @@ __global__ void __launch_bounds__(MpLayout<N>::kThreads, 1) mla_paged_kernel(con
     const int64_t T = b.total, R = mp_ranges(p, T);
     if (range < R) {   // (else: fewer tiles than ranges)
         const int64_t lo = b.lo, hi = b.hi;
-        if (warp < 4)
-            mp_softmax<N, 0>(L, b, sbase, ex, tm, warp, lane, block, range, lo, hi);
-        else if (warp < Y::kProd)
-            mp_softmax<N, N / Y::HG - 1>(L, b, sbase, ex, tm, warp - 4, lane, block, range, lo, hi);
+        if (warp < Y::kProd)
+            mp_softmax<N>(L, b, sbase, ex, tm, Y::kProd > 4 ? warp >> 2 : 0, warp & 3, lane, block, range, lo, hi);
         else if (warp == Y::kProd)
             mp_producer<N>(L, b, sbase, lane, block);
         else if (warp == Y::kScores) {
