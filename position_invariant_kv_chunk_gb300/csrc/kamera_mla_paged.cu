@@ -11,8 +11,8 @@
 // would take 72 KB), and both products read the one copy of the rows: a tile of 64
 // tokens is four units of 128 columns, [8 groups of 8 rows][2 blocks of 64
 // columns][8][128 bytes] as a TMA box lands them.  A tile's MMAs take 36 x 26 (N = 16)
-// or 34 (N = 64) and 16 x 66 cycles.  An M = 64 accumulator sits in 16 lanes of each warp's quarter of TMEM: columns 0-255 of O in
-// the lower 16, 256-511 in the upper 16.
+// or 34 (N = 64) and 16 x 66 cycles.  An M = 64 accumulator sits in 16 lanes of each
+// warp's quarter of TMEM: columns 0-255 of O in the lower 16, 256-511 in the upper 16.
 //   N = 16, 32 (up to as many heads)   weights as bf16 hi + lo pairs, the lo parts eight
 //                more rows behind eight heads: free, as M is 64 anyway
 //   N = 64       weights rounded to bf16; 65 to 128 heads are two CTAs that walk the
@@ -30,6 +30,11 @@
 //   two warps  MMA, the scores' and the products': what a lane issues next waits behind
 //              its MMAs, barriers too, and with one lane for both (300 cycles for every
 //              barrier between MMAs) neither kept the tensor pipe busy
+// Measured: 32 contexts of up to 16384 tokens with 16 heads in 93 us (5.5 TB/s of the
+// rows; HBM, 81% of a copy's rate), 48 of up to 8192 with 128 heads in 146 (646 TFLOP/s).
+// There the ring holds two tiles, beside 72 KB of queries, and a tile stays from its load
+// (1700 cycles) over its scores and their softmax to its product: the tensor pipe works
+// 62% of the time.  One context of 4096 tokens takes 16.4: one tile a CTA and the join.
 // Every wait is bounded in time.
 #include <algorithm>
 #include <cstdint>

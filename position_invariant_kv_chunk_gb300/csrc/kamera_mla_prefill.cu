@@ -18,12 +18,14 @@
 //   warps 0-3, 4-7  softmax of side A, B: thread = query = TMEM lane; running maximum
 //                   with lazy rescaling (only when it grows by more than 2^8)
 //   warp 8          producer: 128B-swizzled TMA boxes of 64 columns into a ring of eight
-//                   16 KB units: a tile is three of keys (64 columns x 128 rows) and two
+//                   (SPLIT: eleven) 16 KB units: a tile is three of keys (64 columns x 128 rows) and two
 //                   of values (128 columns x 64 rows, so that an MMA takes N = 128 from
 //                   one unit: 67 cycles, where two of N = 64 take 100)
 //   warp 10         MMA; it owns TMEM (warps 9, 11 idle: registers are moved between
 //                   whole warpgroups)
 // Blocks of queries with the most rows to see start first.  Every wait is bounded.
+// Measured: 4 prompts of up to 4096 tokens, 16 heads, in 192 us (1386 TFLOP/s), 777
+// queries behind 1296 rows in 23.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
@@ -205,7 +207,7 @@ __device__ __forceinline__ bool pr_elect()
 
 // The MMA lane.  What it does next waits behind the dispatch of its MMAs, looks at
 // barriers too, which leaves the tensor pipe idle for about 500 of 3350 cycles a pair of
-// tiles (2680 of MMAs).  Tried for 4 x 4096 tokens, 195 us: a lane a side 230 (both sides
+// tiles (2680 of MMAs).  Tried for 4 x 4096 tokens, at 195 us: a lane a side 230 (both sides
 // then weigh at the same time), with turns 214; one barrier for a tile's keys, its values
 // and its weights 200 (the first half of the weights starts the product early).  TMEM
 // addresses are offsets: the CTA holds all 512 columns, so its allocation starts at

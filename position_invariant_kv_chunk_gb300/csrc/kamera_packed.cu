@@ -22,6 +22,12 @@
 // Work: the batch's tiles of 128 tokens, all (sequence, KV head) behind one another, in
 // equal ranges, one a CTA; each leaves a partial state for every (sequence, KV head)
 // that it touches, and a last launch joins them with the tail's.
+// Measured: 32 contexts of up to 32768 tokens, 4 KV heads of 128 with 7 query heads, in
+// 109 us (4.7 TB/s), 32 KV heads with one each 60: a tile takes an SM 865 cycles where
+// HBM alone would need 785 (the issue slots are 70% full), but CTAs with equal work end
+// up to 20% apart.  One context of 32768: 18.6, start, three tiles and the join.  Steps
+// of two tiles for the softmax (8 query heads) were slower, 114: a step's products then
+// wait for the keys of two more tiles.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
