@@ -31,10 +31,10 @@
 //              its MMAs, barriers too, and with one lane for both (300 cycles for every
 //              barrier between MMAs) neither kept the tensor pipe busy
 // Measured: 32 contexts of up to 16384 tokens with 16 heads in 93 us (5.5 TB/s of the
-// rows; HBM, 81% of a copy's rate), 48 of up to 8192 with 128 heads in 146 (646 TFLOP/s).
+// rows; HBM, 81% of a copy's rate), 48 of up to 8192 with 128 heads in 144 (652 TFLOP/s).
 // There the ring holds two tiles, beside 72 KB of queries, and a tile stays from its load
 // (1700 cycles) over its scores and their softmax to its product: the tensor pipe works
-// 62% of the time.  One context of 4096 tokens takes 16.4: one tile a CTA and the join.
+// 62% of the time.  One context of 4096 tokens takes 14.6: one tile a CTA and the join.
 // Every wait is bounded in time.
 #include <algorithm>
 #include <cstdint>
@@ -763,10 +763,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
             const bool mine = ok && out_head < heads;
             const float inv = fac[out_head];
             const int dim0 = (lane >> 4) * (kMpDim / 2);
-#pragma unroll 1
-            for (int c = 0; c < kMpDim / 2 / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(lanes + Y::kTmO + 32 * c, o);
+            auto put = [&](int c, uint32_t (&o)[32]) {   // 32 of the columns
                 if constexpr (Y::kPair) {   // a lane with hi sums and one with lo sums: each writes half of the columns
                     const bool lo_row = lane & 8;
 #pragma unroll
@@ -794,6 +791,17 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                         *reinterpret_cast<uint4*>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
                 __syncwarp();
+            };
+#pragma unroll 1
+            for (int c = 0; c < kMpDim / 2 / 32; c += 2) {   // (one at a time takes 3400 cycles in all)
+                uint32_t o[2][32];
+                tmem_ld32_issue(lanes + Y::kTmO + 32 * c, o[0]);
+                tmem_ld32(lanes + Y::kTmO + 32 * c + 32, o[1]);   // waits for both
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    asm volatile("" : "+r"(o[0][i]));
+                put(c, o[0]);
+                put(c + 1, o[1]);
             }
         }
         ptx::tc_fence_before();
@@ -877,18 +885,22 @@ __global__ void __launch_bounds__(MpLayout<N>::kThreads, 1) mla_paged_kernel(con
 
 // ------------------------------------------------------------------- merge --
 // The rows whose sequence was cut: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i
-// over the partial states of its ranges.  A CTA a row, a thread four columns of every
+// over the partial states of its ranges.  CQ CTAs a row, a thread four columns of every
 // GR-th state, whose outputs it asks for eight at a time before their weights are known;
-// the GR sums join in order.  GR = 4 where a sequence may have many states: all latency
-// (one thread for all states of four columns: 9 us more where one sequence is cut 64
-// times); 1 where the rows are many and have two or three (four groups: 30 us more for
-// 6144 rows).
-template <int GR>
-__global__ void __launch_bounds__(128 * GR) mla_merge_kernel(const MpParams p)
+// the GR sums join in order.  Where a sequence may have many states it is all latency: a
+// warp a state and a quarter of the columns, 16 of them (for one sequence cut 64 times 2 us
+// less than four groups of whole rows, which took 9 less than one); where the rows are
+// many and have two or three states, a thread for all of them (four groups: 30 us more
+// for 6144 rows).
+template <int GR, int CQ>
+__global__ void __launch_bounds__(128 / CQ * GR) mla_merge_kernel(const MpParams p)
 {
-    __shared__ float4 part[GR > 1 ? GR - 1 : 1][128];
-    const int s = blockIdx.x / p.Hq, h = blockIdx.x - s * p.Hq;
-    const int lane = threadIdx.x & 31, group = threadIdx.x >> 7, col = threadIdx.x & 127;
+    constexpr int TG = 128 / CQ;   // threads of a group
+    __shared__ float4 part[GR > 1 ? GR - 1 : 1][TG];
+    const int64_t row = blockIdx.x / CQ;
+    const int s = (int)(row / p.Hq), h = (int)(row - (int64_t)s * p.Hq);
+    const int lane = threadIdx.x & 31, group = threadIdx.x / TG, mine = threadIdx.x % TG;
+    const int col = (int)(blockIdx.x % CQ) * TG + mine;
     ptx::grid_wait();
     ptx::grid_launch_next();
     const int4 sp = p.span[s];
@@ -897,7 +909,7 @@ __global__ void __launch_bounds__(128 * GR) mla_merge_kernel(const MpParams p)
         return;
     const int n = sp.y - sp.x + 1;
     auto slot = [&](int i) { return (int64_t)(i == 0 ? sp.z : 2 * (sp.x + i)) * p.Hq + h; };
-    constexpr int U = 8;
+    constexpr int U = 8, SW = U * GR > 32 ? U * GR / 32 : 1;   // a round: eight states a group, SW a lane
     float4 v[U];
     auto load = [&](int i0) {
 #pragma unroll
@@ -919,22 +931,28 @@ __global__ void __launch_bounds__(128 * GR) mla_merge_kernel(const MpParams p)
     for (int i0 = 0; i0 < n; i0 += U * GR) {
         if (i0 > 0)
             load(i0);
-        float f = 0.f;   // a state without weight adds nothing (and has no maximum to scale by)
-        bool some = false;
-        if (lane < U * GR && i0 + lane < n) {
-            const float2 y = p.ml[slot(i0 + lane)];
-            some = y.y != 0.f;
-            if (some) {
-                f = pf_ex2(y.x - m);
-                l = fmaf(y.y, f, l);
+        float f[SW];   // a state without weight adds nothing (and has no maximum to scale by)
+        uint32_t live[SW];
+#pragma unroll
+        for (int c = 0; c < SW; ++c) {
+            const int j = 32 * c + lane;
+            f[c] = 0.f;
+            bool some = false;
+            if (j < U * GR && i0 + j < n) {
+                const float2 y = p.ml[slot(i0 + j)];
+                some = y.y != 0.f;
+                if (some) {
+                    f[c] = pf_ex2(y.x - m);
+                    l = fmaf(y.y, f[c], l);
+                }
             }
+            live[c] = __ballot_sync(0xFFFFFFFFu, some);
         }
-        const uint32_t live = __ballot_sync(0xFFFFFFFFu, some);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int j = GR * k + group;
-            const float x = __shfl_sync(0xFFFFFFFFu, f, j);
-            if ((live >> j) & 1u) {
+            const int j = GR * k + group, c = GR * k / 32;   // (a round's state j: lane j % 32 has its weight)
+            const float x = __shfl_sync(0xFFFFFFFFu, f[c], j & 31);
+            if ((live[c] >> (j & 31)) & 1u) {
                 acc.x = fmaf(v[k].x, x, acc.x);
                 acc.y = fmaf(v[k].y, x, acc.y);
                 acc.z = fmaf(v[k].z, x, acc.z);
@@ -944,7 +962,7 @@ __global__ void __launch_bounds__(128 * GR) mla_merge_kernel(const MpParams p)
     }
     if constexpr (GR > 1) {
         if (group > 0)
-            part[group - 1][col] = acc;
+            part[group - 1][mine] = acc;
         __syncthreads();
         if (group > 0)
             return;
@@ -954,14 +972,13 @@ __global__ void __launch_bounds__(128 * GR) mla_merge_kernel(const MpParams p)
         l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
 #pragma unroll
     for (int g = 0; g < GR - 1; ++g) {
-        const float4 y = part[g][col];
+        const float4 y = part[g][mine];
         acc.x += y.x, acc.y += y.y, acc.z += y.z, acc.w += y.w;
     }
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-    const int64_t row = blockIdx.x;
     *reinterpret_cast<uint2*>(p.out + row * kMpDim + 4 * col) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (threadIdx.x == 0 && p.lse)
+    if (col == 0 && p.lse)
         p.lse[row] = l > 0.f ? (m + log2f(l)) * kMpLn2 : (l == l ? -INFINITY : l);
 }
 
@@ -1103,9 +1120,8 @@ int kamera_mla_attend_paged(const KameraPagedMlaKV* kv, const KameraPagedQuery* 
     if (p.ranges > 1) {
         // states of a row on average: a range ends in each but the last
         const bool many = p.ranges >= 8ll * p.n_seqs;
-        const dim3 grid((unsigned)rows);
-        if ((many ? launch_after(mla_merge_kernel<4>, grid, 512, 0, stream, true, p)
-                  : launch_after(mla_merge_kernel<1>, grid, 128, 0, stream, true, p)) != cudaSuccess)
+        if ((many ? launch_after(mla_merge_kernel<16, 4>, dim3(4 * (unsigned)rows), 512, 0, stream, true, p)
+                  : launch_after(mla_merge_kernel<1, 1>, dim3((unsigned)rows), 128, 0, stream, true, p)) != cudaSuccess)
             return KAMERA_ERR_CUDA;
     }
     return KAMERA_OK;
