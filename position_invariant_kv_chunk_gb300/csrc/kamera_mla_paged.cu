@@ -178,6 +178,32 @@ __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
 {
     auto length = [&](int s) { return s < p.n_seqs ? mp_len(p, s) : 0; };
     const int first = length(lane);
+    if (p.n_seqs <= 32) {   // one scan in 32 bits, as a sequence has at most 2^25 tiles (one context: 12.3 -> 12.0 us)
+        const uint32_t n = lane < p.n_seqs ? (uint32_t)mp_tiles(first) : 0u;
+        uint32_t x = n;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+            if (lane >= d)
+                x += y;
+        }
+        const uint32_t T = __shfl_sync(0xFFFFFFFFu, x, 31);
+        const int64_t R = mp_ranges(p, T);
+        if (lane == 0)
+            b.total = T;
+        if (r >= R)
+            return;
+        const uint32_t lo = (uint32_t)mp_start(r, T, R), before = x - n;
+        if (before <= lo && lo < x) {
+            b.first_seq = lane;
+            b.first_len = first;
+            b.first_n = (int)n;
+            b.first_t = (int)(lo - before);
+            b.lo = lo;
+            b.hi = mp_start(r + 1, T, R);
+        }
+        return;
+    }
     int64_t sum = lane < p.n_seqs ? mp_tiles(first) : 0;
     for (int s = lane + 32; s < p.n_seqs; s += 32)
         sum += mp_tiles(length(s));
