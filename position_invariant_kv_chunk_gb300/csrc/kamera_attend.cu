@@ -48,6 +48,7 @@
 #include "kamera_common.cuh"
 #include "kamera_internal.h"
 #include "kamera_ptx.cuh"
+#include "kamera_tc.cuh"
 #include "kamera_warpmma.cuh"
 
 namespace kamera {
@@ -383,7 +384,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
                 const uint32_t ub = ut0 + (SM::UB ? b : 0) * kUBuf, uvb = uv0 + (SM::UB ? b : 0) * kUBuf;
                 const bool active = r0 < ntok;
                 if (active) {
-                    tile_wait(ptx::smem_addr(&s.full[warp][b]), (ph >> b) & 1u, &s.abort, p.err, P.wait_ns);
+                    // (after a timeout still waited for: no copy outlives the CTA)
+                    if (!tile_wait(ptx::smem_addr(&s.full[warp][b]), (ph >> b) & 1u, &s.abort, p.err, P.wait_ns))
+                        tc::pf_drain_wait(ptx::smem_addr(&s.full[warp][b]), (ph >> b) & 1u);
                     ph ^= 1u << b;
                     // ---- this warp's rows of the buffer: U rows of ranks that are not whole
                     // 16-byte vectors, U columns past the rank, value rows past the chunk

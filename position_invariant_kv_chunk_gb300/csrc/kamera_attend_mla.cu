@@ -48,6 +48,7 @@
 #include "kamera_common.cuh"
 #include "kamera_internal.h"
 #include "kamera_ptx.cuh"
+#include "kamera_tc.cuh"
 #include "kamera_warpmma.cuh"
 
 namespace kamera {
@@ -364,7 +365,9 @@ __global__ void __launch_bounds__(kMlThreads, 1) mla_attend_kernel(const __grid_
 
         for (int tl = t_lo; tl < t_hi; ++tl) {
             const int b = (tl - t_lo) & 1, ntok = min(kMlT, len - tl * kMlT);
-            tile_wait(ptx::smem_addr(&s.full[b]), (ph >> b) & 1u, &s.abort, p.err, P.wait_ns);
+            // (after a timeout still waited for: no copy outlives the CTA)
+            if (!tile_wait(ptx::smem_addr(&s.full[b]), (ph >> b) & 1u, &s.abort, p.err, P.wait_ns))
+                tc::pf_drain_wait(ptx::smem_addr(&s.full[b]), (ph >> b) & 1u);
             ph ^= 1u << b;
             ptx::cp_async_wait<0>();   // this thread's copies of tile tl (the only group in flight)
             const uint32_t kb = kt0 + b * kBuf, uxb = ux0 + b * kUBuf;

@@ -186,7 +186,7 @@ __device__ void ex_producer(const ExLaunch& L, ExBars& b, uint32_t sbase)
     if (*static_cast<volatile int32_t*>(&b.abort)) {
         const int64_t t0 = clock64();
         for (uint32_t i = k > (uint32_t)kExStages ? k - kExStages : 0u; i < k && half == 0; ++i)
-            pf_drain_wait(ptx::smem_addr(&b.full[i % kExStages]), (i / kExStages) & 1u, p.wait_ns);
+            pf_drain_wait(ptx::smem_addr(&b.full[i % kExStages]), (i / kExStages) & 1u);
         while (half == 1 && (uint64_t)(clock64() - t0) < 100000u)   // 50 us: no load takes that long
             ;
     }
@@ -236,7 +236,7 @@ __device__ void ex_mma(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm
     }
     // every MMA issued here completes before TMEM is freed
     ex_commit(ptx::smem_addr(&b.drained));
-    pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
+    pf_drain_wait(ptx::smem_addr(&b.drained), 0u);
 }
 
 // The tokens' rows into shared memory (K-major, 128B-swizzled blocks of 64 columns),

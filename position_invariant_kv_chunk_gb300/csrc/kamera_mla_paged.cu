@@ -121,6 +121,7 @@ struct MpBars {
     uint32_t mask[kMpMasks];
     int64_t total, lo, hi;     // the batch's tiles and the range's
     int32_t first_seq, first_len, first_n, first_t;   // where the range starts
+    uint32_t units, ropes, segs;   // fills whose loads were issued
     uint32_t tmem;
     int32_t abort;
 };
@@ -408,17 +409,23 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
         w.next(p);
         ++tile;
     }
-    // Without a timeout the MMA lanes have waited for every fill.  After one, the copies
-    // started here land before the CTA leaves.
-    if (mp_elect() && !p.withhold && *static_cast<volatile int32_t*>(&b.abort)) {
-        if (seg > 0)
-            pf_drain_wait(ptx::smem_addr(&b.q_full), (seg - 1) & 1u, p.wait_ns);
-        for (uint32_t k = unit > (uint32_t)Y::NU ? unit - Y::NU : 0u; k < unit; ++k)
-            pf_drain_wait(ptx::smem_addr(&b.full[k % Y::NU]), (k / Y::NU) & 1u, p.wait_ns);
-        for (uint32_t k = rope > (uint32_t)Y::NR ? rope - Y::NR : 0u; k < rope; ++k)
-            pf_drain_wait(ptx::smem_addr(&b.rfull[k % Y::NR]), (k / Y::NR) & 1u, p.wait_ns);
+    if (mp_elect() && !p.withhold) {
+        b.units = unit;
+        b.ropes = rope;
+        b.segs = seg;
     }
     __syncwarp();
+}
+
+// After a timeout, once every role has left its loop: the copies that the CTA started land
+// before it leaves.  (Without one the MMA lanes have waited for every fill.)
+template <int N>
+__device__ __forceinline__ void mp_drain(const MpBars& b)
+{
+    using Y = MpLayout<N>;
+    pf_drain_ring(&b.q_full, b.segs, 1);
+    pf_drain_ring(b.full, b.units, Y::NU);
+    pf_drain_ring(b.rfull, b.ropes, Y::NR);
 }
 
 // MMAs whose A (mma_ds) or B (mma_sd) is a unit, groups of eight rows 2 KB apart; the
@@ -495,7 +502,7 @@ __device__ void mp_scores(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t
     }
     // every MMA issued here completes before TMEM is freed
     ptx::umma_commit(ptx::smem_addr(&b.drained[0]));
-    pf_drain_wait(ptx::smem_addr(&b.drained[0]), 0u, p.wait_ns);
+    pf_drain_wait(ptx::smem_addr(&b.drained[0]), 0u);
 }
 
 // The products' lane: tile by tile as the weights come; a tile's units are free behind it.
@@ -547,7 +554,7 @@ __device__ void mp_products(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32
         ptx::umma_commit(ptx::smem_addr(&b.pv_done[t & 1u]));
     }
     ptx::umma_commit(ptx::smem_addr(&b.drained[1]));
-    pf_drain_wait(ptx::smem_addr(&b.drained[1]), 0u, p.wait_ns);
+    pf_drain_wait(ptx::smem_addr(&b.drained[1]), 0u);
 }
 
 // ----------------------------------------------------------------- softmax --
@@ -870,6 +877,7 @@ __global__ void __launch_bounds__(MpLayout<N>::kThreads, 1) mla_paged_kernel(con
         ptx::mbar_init(ptx::smem_addr(&b.q_full), 1);
         ptx::mbar_init(ptx::smem_addr(&b.q_empty), 1);
         b.abort = 0;
+        b.units = b.ropes = b.segs = 0;
         ptx::fence_barrier_init();
     }
     if (warp == Y::kProd && lane == 0) {
@@ -912,6 +920,8 @@ __global__ void __launch_bounds__(MpLayout<N>::kThreads, 1) mla_paged_kernel(con
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tm, Y::kTmCols);
     }
+    if (threadIdx.x == 32 * Y::kProd && b.abort)
+        mp_drain<N>(b);
 }
 
 // ------------------------------------------------------------------- merge --

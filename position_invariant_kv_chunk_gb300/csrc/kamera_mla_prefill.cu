@@ -87,6 +87,7 @@ struct PrLaunch {
 struct PrBars {
     uint64_t full[11], empty[11];
     uint64_t q_full, s_full[2], p_full[2][2], pv_done[2], drained;   // p_full: tokens 0-63, 64-127 of the tile
+    uint32_t units, queries;   // fills whose loads were issued: of the ring, of the queries (0 or 1)
     uint32_t tmem;
     int32_t abort, odd;      // odd: some masked value is not finite
 };
@@ -187,13 +188,17 @@ __device__ void pr_producer(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b
                 ptx::tma_load_2d(dst + kPrUnit / 2, &L.map_v, col + kPrNope + 64, row + 64 * (u - 3), full);
             }
         }
-    // Without a timeout the MMA lane has waited for every fill.  After one, the copies
-    // started here land before the CTA leaves.
-    if (*static_cast<volatile int32_t*>(&b.abort)) {
-        pf_drain_wait(q_full, 0u, p.wait_ns);
-        for (uint32_t i = k > (uint32_t)kPrUnits ? k - kPrUnits : 0u; i < k; ++i)
-            pf_drain_wait(ptx::smem_addr(&b.full[i % kPrUnits]), (i / kPrUnits) & 1u, p.wait_ns);
-    }
+    b.queries = 1;
+    b.units = k;
+}
+
+// After a timeout, once every role has left its loop: the copies that the CTA started land
+// before it leaves.  (Without one the MMA lane has waited for every fill.)
+template <bool SPLIT>
+__device__ __forceinline__ void pr_drain(const PrBars& b)
+{
+    pf_drain_ring(&b.q_full, b.queries, 1);
+    pf_drain_ring(b.full, b.units, PrLayout<SPLIT>::kUnits);
 }
 
 // One lane of the (converged) warp; the compiler knows that a branch on it holds a
@@ -286,7 +291,7 @@ __device__ void pr_mma(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b, uin
     }
     // every MMA issued here completes before TMEM is freed
     ptx::umma_commit(ptx::smem_addr(&b.drained));
-    pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
+    pf_drain_wait(ptx::smem_addr(&b.drained), 0u);
 }
 
 __device__ __forceinline__ float pr_max3(float a, uint32_t b, uint32_t c)
@@ -620,6 +625,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
         b.odd = 0;
+        b.units = b.queries = 0;
         ptx::fence_barrier_init();
     }
     int32_t* first = reinterpret_cast<int32_t*>(raw + pad + kPrOdd);
@@ -657,6 +663,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tm, 512);
     }
+    if (threadIdx.x == 32 * kPrProd && b.abort)
+        pr_drain<SPLIT>(b);
 }
 
 }  // namespace

@@ -100,6 +100,7 @@ struct P4Bars {
     uint32_t mask[kP4Masks];       // tile t (mod kP4Masks): 16-token pieces that are there
     int64_t total, lo, hi;         // the batch's tiles and the range's
     int32_t first_seq, first_len, first_n, first_h, first_t;   // where the range starts
+    uint32_t tiles;                // whose loads were issued
     uint32_t tmem;
     int32_t abort;
 };
@@ -355,11 +356,8 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
             ++lap;
         }
     }
-    // The copies this warp started land before the CTA leaves (without a timeout every
-    // one has been waited for).
-    if (lane == 0 && !p.withhold && *static_cast<volatile int32_t*>(&b.abort))
-        for (uint32_t i = k > (uint32_t)Y::NS ? k - Y::NS : 0u; i < k; ++i)
-            pf_drain_wait(ptx::smem_addr(&b.full[i % Y::NS]), (i / Y::NS) & 1u, p.wait_ns);
+    if (lane == 0 && !p.withhold)
+        b.tiles = k;
     __syncwarp();
 }
 
@@ -409,7 +407,7 @@ __device__ void p4_mma(const P4Params& p, P4Bars& b, uint32_t sbase, uint32_t tm
     }
     // every MMA issued here completes before TMEM is freed
     ptx::umma_commit(ptx::smem_addr(&b.drained));
-    pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
+    pf_drain_wait(ptx::smem_addr(&b.drained), 0u);
 }
 
 // ------------------------------------------------------------------ values --
@@ -846,6 +844,7 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
         }
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
+        b.tiles = 0;
         ptx::fence_barrier_init();
     }
     if (warp == kP4Mma) {
@@ -885,6 +884,10 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tm, kP4TmCols);
     }
+    // After a timeout the copies that the CTA started land before it leaves.  (Without one
+    // every fill has been waited for.)
+    if (threadIdx.x == 32 * kP4Prod && b.abort)
+        pf_drain_ring(b.full, b.tiles, Y::NS);
     // The merge that follows waits for this grid alone, which ends after the tail's.
     if (!p.first && blockIdx.x == gridDim.x - 1)
         ptx::grid_wait();

@@ -34,6 +34,7 @@
 #include "kamera_internal.h"
 #include "kamera_paged.h"
 #include "kamera_ptx.cuh"
+#include "kamera_tc.cuh"
 #include "kamera_warpmma.cuh"
 
 namespace kamera {
@@ -355,12 +356,8 @@ __global__ void __launch_bounds__(kPgThreads) paged_kernel(const __grid_constant
     }
     if (!ok) {   // a wait ran out: the copies in flight land before the CTA leaves
         for (int b = 0; b < NS; ++b)
-            if ((flying >> b) & 1u) {
-                const uint64_t t0 = ptx::globaltimer();
-                while (!ptx::mbar_try_wait(bar + 8 * b, (parity >> b) & 1u))
-                    if (ptx::globaltimer() - t0 > p.wait_ns)
-                        break;
-            }
+            if ((flying >> b) & 1u)
+                tc::pf_drain_wait(bar + 8 * b, (parity >> b) & 1u);
     }
     // ---- the warps' states through shared memory
 #pragma unroll

@@ -288,9 +288,8 @@ __device__ void pf_producer(const PrefillLaunch& P, uint32_t sbase, PfBars& b, i
         ptx::mbar_arrive(ptx::smem_addr(&b.full[(n - 1) % L::NS]));
     }
     // the copies this warp started land before the CTA leaves
-    if (lane == 0)
-        for (uint32_t k = n > (uint32_t)L::NS ? n - L::NS : 0u; k < n; ++k)
-            pf_drain_wait(ptx::smem_addr(&b.full[k % L::NS]), (k / L::NS) & 1u, P.wait_ns);
+    if (lane == 0 && !P.withhold)
+        pf_drain_ring(b.full, n, L::NS);
     __syncwarp();
 }
 
@@ -462,7 +461,7 @@ __device__ void pf_mma(const PrefillLaunch& P, uint32_t sbase, PfBars& b, uint32
     }
     // every MMA issued here completes before TMEM is freed
     ptx::umma_commit(ptx::smem_addr(&b.drained));
-    pf_drain_wait(ptx::smem_addr(&b.drained), 0u, P.wait_ns);
+    pf_drain_wait(ptx::smem_addr(&b.drained), 0u);
 }
 
 // An m-wide V factor block [d][m] (`src`) into a [d][64] bf16 tile of

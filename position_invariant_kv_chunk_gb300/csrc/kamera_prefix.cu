@@ -105,6 +105,7 @@ struct PxBars {
     uint32_t mask[kPxMasks];   // tile t (mod kPxMasks): 16-token pieces with tokens that count
     uint32_t tmem;
     int32_t abort;
+    int32_t issued[2], tiles;  // tiles of keys and of values whose loads were issued; of the split
 };
 static_assert(sizeof(PxBars) <= 512, "barrier block");
 
@@ -237,14 +238,34 @@ __device__ void px_producer(const PagedLaunch& L, const PxWork& w, PxBars& b, ui
             ptx::tma_load_4d(dst + (uint32_t)(off / 8) * Y::kGroup, VALUES ? &L.map_v : &L.map_k, 0, 0, w.h * Y::NB,
                              (from * p.P + (tok0 + off) % p.P) >> 3, full);
     }
-    // Without a timeout the MMA lane has waited for every fill.  After one, the
-    // copies this warp started land before the CTA leaves.
-    if (lane == 0 && !p.withhold && *static_cast<volatile int32_t*>(&b.abort))
-        for (int k = max(0, t - kPxBuf); k < t; ++k) {
-            const uint32_t at = VALUES ? px_v_at(two, k, w.tiles) : px_k_at(two, k);
-            pf_drain_wait(ptx::smem_addr(&b.full[at % kPxBuf]), (at / kPxBuf) & 1u, p.wait_ns);
-        }
+    if (lane == 0) {
+        b.issued[VALUES] = t;
+        if (!VALUES)
+            b.tiles = w.tiles;
+    }
     __syncwarp();
+}
+
+// After a timeout, once every role has left its loop: the copies that the CTA started land
+// before it leaves.  (Without one the MMA lane has waited for every fill.)  A fill was
+// issued behind the use of the one kPxBuf places before, so older ones have landed.
+__device__ __forceinline__ void px_drain(const PagedParams& p, const PxBars& b)
+{
+    const bool two = p.two_tile != 0;
+    const int nk = b.issued[0], nv = b.issued[1];
+    uint32_t end = 0;   // behind the last place that was filled
+    if (nk > 0)
+        end = px_k_at(two, nk - 1) + 1;
+    if (nv > 0)
+        end = max(end, px_v_at(two, nv - 1, b.tiles) + 1);
+    auto landed = [&](uint32_t at) {
+        if (at + kPxBuf >= end)
+            pf_drain_wait(ptx::smem_addr(&b.full[at % kPxBuf]), (at / kPxBuf) & 1u);
+    };
+    for (int k = max(0, nk - kPxBuf); k < nk; ++k)
+        landed(px_k_at(two, k));
+    for (int k = max(0, nv - kPxBuf); k < nv; ++k)
+        landed(px_v_at(two, k, b.tiles));
 }
 
 // One lane of the (converged) warp: the compiler knows that a branch on it holds
@@ -331,7 +352,7 @@ __device__ void px_mma(const PagedLaunch& L, const PxWork& w, PxBars& b, uint32_
     }
     // every MMA issued here completes before TMEM is freed
     ptx::umma_commit(ptx::smem_addr(&b.drained));
-    pf_drain_wait(ptx::smem_addr(&b.drained), 0u, p.wait_ns);
+    pf_drain_wait(ptx::smem_addr(&b.drained), 0u);
 }
 
 __device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c)
@@ -594,6 +615,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         ptx::mbar_init(ptx::smem_addr(&b.q_full), (p.two_tile ? 2 : 1) * kPxRows);
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
+        b.issued[0] = b.issued[1] = 0;
         ptx::fence_barrier_init();
     }
     if (warp == kPxProdK && lane == 0) {
@@ -636,6 +658,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tm, Y::kTmCols);
     }
+    if (threadIdx.x == 32 * kPxProdK && b.abort && !p.withhold)
+        px_drain(p, b);
 }
 
 template <int D>
