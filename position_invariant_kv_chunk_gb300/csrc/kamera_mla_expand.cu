@@ -72,6 +72,8 @@ struct ExLaunch {
 
 struct ExBars {
     uint64_t full[kExStages], empty[kExStages], acc_full[2], acc_empty[2], a_full, a_empty[kExChunks], drained;
+    uint32_t issued;       // fills whose loads this CTA issued
+    uint32_t gave_up[2];   // either CTA of the pair: 0, or 1 + its fills where a wait ran out
     uint32_t tmem;
     int32_t abort;
 };
@@ -108,13 +110,14 @@ __device__ __forceinline__ void ex_cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// A shared-memory address of this CTA as the pair's first CTA has it.
-__device__ __forceinline__ uint32_t ex_first(uint32_t addr)
+// A shared-memory address of this CTA as a CTA of the pair has it.
+__device__ __forceinline__ uint32_t ex_at(uint32_t addr, uint32_t rank)
 {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+__device__ __forceinline__ uint32_t ex_first(uint32_t addr) { return ex_at(addr, 0); }
 __device__ __forceinline__ void ex_arrive_first(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(ex_first(bar)) : "memory");
@@ -161,35 +164,55 @@ __device__ __forceinline__ bool ex_elect()
     return r != 0;
 }
 
+// This CTA's half of fill k, of a head's weights.
+__device__ __forceinline__ void ex_fill(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t k, int head)
+{
+    const int half = blockIdx.x & 1, c = (int)(k % kExChunks);
+    const uint32_t at = k % kExStages, full = ptx::smem_addr(&b.full[at]);
+    if (half == 0)
+        ptx::mbar_arrive_expect_tx(full, 2 * kExStage);
+    ex_load(sbase + kExRing + at * kExStage, &L.map_w, 64 * c, head * kExN + half * (kExN / 2), ex_first(full));
+}
+
 __device__ void ex_producer(const ExLaunch& L, ExBars& b, uint32_t sbase)
 {
     const ExParams& p = L.p;
     if (p.withhold)
         return;
-    const int half = blockIdx.x & 1;
     uint32_t k = 0;
     bool ok = true;
     for (ExWalk w(p); w.more() && ok; w.next())
         for (int c = 0; c < kExChunks; ++c, ++k) {
-            const uint32_t at = k % kExStages, lap = k / kExStages, full = ptx::smem_addr(&b.full[at]);
+            const uint32_t at = k % kExStages, lap = k / kExStages;
             if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns)) {
                 ok = false;
                 break;
             }
-            if (half == 0)
-                ptx::mbar_arrive_expect_tx(full, 2 * kExStage);
-            ex_load(sbase + kExRing + at * kExStage, &L.map_w, 64 * c, w.head * kExN + half * (kExN / 2), ex_first(full));
+            ex_fill(L, b, sbase, k, w.head);
         }
-    // Without a timeout the MMA lane has waited for every fill.  After one, the copies
-    // started here land before the CTAs leave: the first CTA waits for both halves of what
-    // it can, the other for as long.
-    if (*static_cast<volatile int32_t*>(&b.abort)) {
-        const int64_t t0 = clock64();
-        for (uint32_t i = k > (uint32_t)kExStages ? k - kExStages : 0u; i < k && half == 0; ++i)
-            pf_drain_wait(ptx::smem_addr(&b.full[i % kExStages]), (i / kExStages) & 1u);
-        while (half == 1 && (uint64_t)(clock64() - t0) < 100000u)   // 50 us: no load takes that long
-            ;
-    }
+    b.issued = k;
+}
+
+// After a timeout, once every role of both CTAs has left its loop and either knows the
+// other's fills: the copies that the pair started land before its CTAs leave.  (Without one
+// the MMA lane has waited for every fill.)  A fill counts both halves, so the CTA that is
+// behind issues its own of those that the other issued -- no more than the ring holds: the
+// other had waited for the use of what stood there before -- and the first CTA, whose
+// barriers count them, waits.
+__device__ __forceinline__ void ex_drain(const ExLaunch& L, ExBars& b, uint32_t sbase)
+{
+    const ExWalk w(L.p);
+    const uint32_t all = (uint32_t)(w.hi - w.i) * kExChunks;
+    auto fills = [&](int r) {
+        const uint32_t x = *static_cast<volatile uint32_t*>(&b.gave_up[r]);
+        return x ? x - 1 : all;   // one whose waits were all met has issued every fill
+    };
+    const int half = blockIdx.x & 1;
+    const uint32_t most = max(fills(0), fills(1));
+    for (uint32_t k = fills(half); k < most; ++k)
+        ex_fill(L, b, sbase, k, (int)((w.head + k / kExChunks) % w.H));
+    if (half == 0)
+        pf_drain_ring(b.full, most, kExStages);
 }
 
 __device__ void ex_mma(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm)
@@ -405,6 +428,7 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
             ptx::mbar_init(ptx::smem_addr(&b.a_empty[i]), 1);
         ptx::mbar_init(ptx::smem_addr(&b.drained), 1);
         b.abort = 0;
+        b.issued = b.gave_up[0] = b.gave_up[1] = 0;
         ptx::fence_barrier_init();
     }
     if (warp == kExProd && lane == 0)
@@ -433,11 +457,27 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
     } else
         ex_gather(L, b, sbase, warp - kExGather, lane);
     ptx::tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 32 * kExMma && (blockIdx.x & 1))   // the first CTA's MMA lane has waited for its own
+        pf_drain_wait(ptx::smem_addr(&b.drained), 0u);
+    if (threadIdx.x == 0 && b.abort)
+        for (uint32_t r = 0; r < 2; ++r)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ex_at(ptx::smem_addr(&b.gave_up[blockIdx.x & 1]), r)),
+                         "r"(b.issued + 1)
+                         : "memory");
     __syncwarp();
     ex_cluster_sync();   // neither CTA leaves while the other may write to it
+    const volatile uint32_t* gave_up = b.gave_up;
+    const bool late = (gave_up[0] | gave_up[1]) != 0 && !L.p.withhold;
     if (warp == kExMma) {
         ptx::tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(512) : "memory");
+    }
+    if (late) {   // (both CTAs alike)
+        if (threadIdx.x == 32 * kExProd)
+            ex_drain(L, b, sbase);
+        __syncwarp();
+        ex_cluster_sync();
     }
 }
 

@@ -45,6 +45,15 @@ def test_latent_decode(Hq, monkeypatch):
                                                                               err=err))
 
 
+@pytest.mark.parametrize("tokens,H", [(100, 1), (1300, 16), (20000, 3)])
+def test_expansion(tokens, H, monkeypatch):
+    """Two CTAs share a barrier for their halves of the weights: either may give up first."""
+    g = gen(tokens)
+    pool, weight = normal(g, 700, T.W), normal(g, H, 256, LORA, std=0.05)
+    slots = torch.randint(0, 700, (tokens,), generator=g, device="cuda")
+    gives_up_then_recovers(monkeypatch, lambda err: K.kamera_mla_expand(pool, LORA, weight, slots, err=err), 20)
+
+
 @pytest.mark.parametrize("seqs,H", [(1, 2), (4, 40)])
 def test_latent_prefill(seqs, H, monkeypatch):
     g = gen(12)
