@@ -105,18 +105,23 @@ enum {
                                       misaligned factor or slot map: chunk skipped */
     KAMERA_DEVERR_LEN = 8,         /* len > max_len: chunk skipped */
     KAMERA_DEVERR_RANK = 16,       /* rank > max_rank: chunk skipped */
-    KAMERA_DEVERR_VALUE = 64,      /* a NaN among the rows to be packed: stored as 0 */
-    KAMERA_DEVERR_TIMEOUT = 32     /* an internal pipeline wait gave up: results incomplete
+    KAMERA_DEVERR_TIMEOUT = 32,    /* an internal pipeline wait gave up: results incomplete
                                       (every wait of the tensor-core kernels is bounded by
-                                      1 s; the environment variable KAMERA_WAIT_LIMIT_NS,
-                                      read at each call, overrides the bound.  Test hooks:
+                                      1 s; those of the latent and packed kernels count
+                                      SM cycles, so 1 s at the highest clock and as much
+                                      longer as a lower one is slower.  The environment
+                                      variable KAMERA_WAIT_LIMIT_NS, read at each call,
+                                      overrides the bound.  Test hooks:
                                       KAMERA_TEST_WITHHOLD_LOADS=1 makes the producers of
-                                      the relocation and prefill attention kernels issue
-                                      no tile loads, and for patch
+                                      the relocation, prefill attention, paged attention,
+                                      latent and packed decode kernels issue no tile
+                                      loads, and for patch
                                       formation a bound of 0 gives up at its first wait;
                                       the kernels then give up early, drain their own
-                                      copies and MMAs, free their tensor memory and
-                                      return with this bit set) */
+                                      copies and MMAs (for up to 1 s, whatever the
+                                      bound), free their tensor memory and return with
+                                      this bit set) */
+    KAMERA_DEVERR_VALUE = 64       /* a NaN among the rows to be packed: stored as 0 */
 };
 
 /* RoPE pairings. */

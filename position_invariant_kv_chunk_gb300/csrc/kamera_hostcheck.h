@@ -43,6 +43,11 @@ inline int check_strided(const void* base, int64_t L, int64_t ls, int64_t rows, 
     return KAMERA_OK;
 }
 
+// SM cycles that last at least `ns` at any clock up to 2125 MHz (2070 is this chip's
+// highest; at half of it they last twice as long), and 1000 for a bound of nothing.  A
+// bound that they would pass 64 bits for is none.
+constexpr uint64_t wait_cycles(uint64_t ns) { return ns < (1ull << 62) ? 2 * ns + ns / 8 + 1000 : ~0ull; }
+
 // theta / (2 pi) modulo 1, in units of 2^-64 (theta finite): the quotient as a
 // double-double, whose integer part drops out of a phase.  The fraction is taken
 // of |theta|, where it is exact (x - floor(x) is not for x in (-1, 0)), and negated

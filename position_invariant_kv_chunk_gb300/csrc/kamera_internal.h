@@ -18,13 +18,15 @@ struct RowsParams;
 // Bound, in ns, of the pipeline waits of the tensor-core kernels: 1 s, or the
 // value of the environment variable KAMERA_WAIT_LIMIT_NS when it is set (a
 // test hook: a short bound makes the kernels give up early and report
-// KAMERA_DEVERR_TIMEOUT).  Read on the host at each launch.
+// KAMERA_DEVERR_TIMEOUT; they drain their own copies and MMAs all the same, for up to
+// 1 s).  Read on the host at each launch.
 uint64_t wait_limit_ns();
 
 // Test hook: KAMERA_TEST_WITHHOLD_LOADS=1 in the environment makes the
-// producers of the relocation and prefill attention kernels issue no loads,
-// so their first pipeline waits run out after the bound above (read on the
-// host at each launch).
+// producers of the relocation, prefill attention, paged attention, latent
+// (decode, expansion, prefill) and packed decode kernels issue no loads, so
+// their first pipeline waits run out after the bound above (read on the host
+// at each launch).
 bool test_withhold_loads();
 
 // CUDA-core streaming path (any rank within the shared-memory budget).

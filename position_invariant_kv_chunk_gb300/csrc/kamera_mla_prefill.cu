@@ -75,7 +75,7 @@ struct PrParams {
     int32_t causal, wide;          // wide: out is 32-byte aligned
     float scale;
     int32_t* err;
-    uint64_t wait_ns;
+    uint64_t wait_cycles;
     int32_t withhold;
 };
 
@@ -171,7 +171,7 @@ __device__ void pr_producer(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b
     for (int t = 0; t < n && ok; ++t)
         for (int u = 0; u < kPrTile; ++u, ++k) {
             const uint32_t at = k % kPrUnits, lap = k / kPrUnits, full = ptx::smem_addr(&b.full[at]);
-            if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_ns)) {
+            if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_cycles)) {
                 ok = false;
                 break;
             }
@@ -226,7 +226,7 @@ __device__ void pr_mma(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b, uin
     constexpr int kPrUnits = PrLayout<SPLIT>::kUnits;
     const uint32_t q_lo = (sbase >> 4) | (1u << 16), r_lo = (sbase + PrLayout<SPLIT>::kQUnits * kPrUnit) >> 4;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_ns);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_cycles);
     };
     // scores of side a's t-th tile; its keys are free after the last side that sees it
     auto scores = [&](auto side, int t) -> bool {
@@ -411,7 +411,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
             bool in = true;
             for (int u = 0; u < 2; ++u)
                 in = in && wmma16::cycle_wait(ptx::smem_addr(&b.full[(k + u) % kPrUnits]), ((k + u) / kPrUnits) & 1u, &b.abort,
-                                             p.err, p.wait_ns);
+                                             p.err, p.wait_cycles);
             ok = __all_sync(0xFFFFFFFFu, ok && in);
             if (base + r >= least && base + r < w.nk)
                 pr_clean_row(unit(r), r & 63, base + r, first, &b.odd);
@@ -423,7 +423,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
             }
             ptx::fence_proxy_async();   // (the product waits for every thread's weights, which follow)
         }
-        if (!wmma16::cycle_wait(ptx::smem_addr(&b.s_full[a]), (uint32_t)t & 1u, &b.abort, p.err, p.wait_ns))
+        if (!wmma16::cycle_wait(ptx::smem_addr(&b.s_full[a]), (uint32_t)t & 1u, &b.abort, p.err, p.wait_cycles))
             ok = false;
         if (!__all_sync(0xFFFFFFFFu, ok)) {
             ok = false;
@@ -476,7 +476,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
             const float f = m_new == -INFINITY ? 1.f : pf_ex2(m_run - m_new);
             l_run *= f;
             m_run = m_new;
-            if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(t - 1) & 1u, &b.abort, p.err, p.wait_ns))
+            if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(t - 1) & 1u, &b.abort, p.err, p.wait_cycles))
                 ok = false;
             ok = __all_sync(0xFFFFFFFFu, ok);
             ptx::tc_fence_after();
@@ -524,7 +524,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
         }
     }
     if (nt > 0 && ok) {
-        if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(nt - 1) & 1u, &b.abort, p.err, p.wait_ns))
+        if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(nt - 1) & 1u, &b.abort, p.err, p.wait_cycles))
             ok = false;
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
@@ -743,7 +743,7 @@ int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct 
     p.wide = (reinterpret_cast<uintptr_t>(x->out) & 31) == 0;
     p.scale = x->scale;
     p.err = d_err;
-    p.wait_ns = wait_limit_ns();
+    p.wait_cycles = wait_cycles(wait_limit_ns());
     p.withhold = test_withhold_loads() ? 1 : 0;
     // (without a row no tile is read: the maps take the queries' memory)
     const void* kv = x->n_kv > 0 ? x->kv : x->q;

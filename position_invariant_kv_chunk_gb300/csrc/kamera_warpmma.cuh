@@ -86,11 +86,10 @@ __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-// The same, timed by the SM's clock: reading the global timer takes a microsecond or
-// more, which a wait that outlasts one try pays every time.  Two cycles a nanosecond
-// (and some for a bound of nothing) are at least the bound at any clock this chip has.
+// The same, timed by the SM's clock (`cycles` of it: wait_cycles()): reading the global
+// timer takes a microsecond or more, which a wait that outlasts one try pays every time.
 __device__ __forceinline__ bool cycle_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort, int32_t* err,
-                                           uint64_t limit)
+                                           uint64_t cycles)
 {
     if (ptx::mbar_try_wait(bar, parity))
         return true;
@@ -100,7 +99,7 @@ __device__ __forceinline__ bool cycle_wait(uint32_t bar, uint32_t parity, volati
             return true;
         if (*abort)
             return false;
-        if ((uint64_t)(clock64() - t0) > 2 * limit + 1000) {
+        if ((uint64_t)(clock64() - t0) > cycles) {
             *abort = 1;
             raise_err(err, KAMERA_DEVERR_TIMEOUT);
             return false;

@@ -84,3 +84,28 @@ def test_reused_chunks(monkeypatch):
     gives_up_then_recovers(monkeypatch, lambda err: [A.run_attend(a, err=err)])
     a = W.make_mla_attend(M.CASES["dsv2_ragged"], "cuda")
     gives_up_then_recovers(monkeypatch, lambda err: [M.run_mla(a, err=err)])
+
+
+@pytest.mark.parametrize("bound", [2 ** 63, 2 ** 63 + 7, 2 ** 64 - 1])
+def test_bounds_past_63_bits_are_long(bound, monkeypatch):
+    lens = [3000, 65]
+    pool = T.Pool(8, 300, 16)
+    table = pool.table(lens)
+    q = normal(pool.g, 2, 16, T.W)
+    g = gen(3)
+    weight, slots = normal(g, 2, 256, LORA, std=0.05), torch.arange(1000, device="cuda")
+    c = P4.Cache(26, [900, 400], [20, 130], 2, 128, 16)
+    qd = normal(c.g, 2, 14, 128)
+    err = i32([0])
+
+    def calls():
+        out = [*K.kamera_mla_attend_paged(pool.kv, LORA, q, 16, table, i32(lens), 3000, err=err),
+               *K.kamera_mla_expand(pool.kv, LORA, weight, slots, err=err), *K.kamera_attend_packed(*c.args(qd), err=err)]
+        kv, kr = out[2:4]
+        out += K.kamera_mla_prefill_attend(normal(gen(1), 300, 2, 192), kv, kr, i32([0, 300]), i32([0, 1000]), 300, err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return out
+    good = calls()
+    monkeypatch.setenv("KAMERA_WAIT_LIMIT_NS", str(bound))
+    assert all(torch.equal(a, b) for a, b in zip(good, calls()))
