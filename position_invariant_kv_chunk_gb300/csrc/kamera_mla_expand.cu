@@ -56,7 +56,6 @@ static_assert(kExBytes <= 227 * 1024, "shared memory");
 struct ExParams {
     const __nv_bfloat16* pool;
     const int64_t* slots;
-    __nv_bfloat16* kv;
     __nv_bfloat16* rope;
     int64_t num_slots, slot_stride, items;
     int32_t T, H;
@@ -526,7 +525,6 @@ int kamera_mla_expand(const KameraPagedMlaKV* kv, const KameraMlaExpand* x, int3
     ExParams& p = L.p;
     p.pool = static_cast<const __nv_bfloat16*>(kv->kv);
     p.slots = x->slots;
-    p.kv = static_cast<__nv_bfloat16*>(x->kv_out);
     p.rope = static_cast<__nv_bfloat16*>(x->k_rope_out);
     p.num_slots = kv->num_slots;
     p.slot_stride = kv->slot_stride;
