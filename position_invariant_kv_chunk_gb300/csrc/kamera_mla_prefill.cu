@@ -683,7 +683,8 @@ int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct 
     if (x->nope_dim != kPrNope || x->rope_dim != kPrQk - kPrNope || x->v_dim != kPrV || x->num_heads > 128 ||
         x->n_kv > (1 << 30) || x->n_q > (1 << 30))
         return KAMERA_ERR_UNSUPPORTED;
-    auto blocks_of = [&](int rows) { return ((int64_t)x->max_q + rows - 1) / rows; };
+    // (a bound of no queries still has a block a sequence, which reports those that have some)
+    auto blocks_of = [&](int rows) { return std::max<int64_t>(1, ((int64_t)x->max_q + rows - 1) / rows); };
     const int64_t pairs = (int64_t)x->n_seqs * x->num_heads;
     // One block of queries a CTA, its tiles split between the sides, while that makes no
     // more than two CTAs an SM: then blocks of 256 would leave SMs idle or half of a CTA's
@@ -694,7 +695,7 @@ int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct 
     const int64_t blocks = blocks_of(split ? kPrRows : 2 * kPrRows), ctas = blocks * pairs;
     if (ctas > 0x7FFFFFFF)
         return KAMERA_ERR_UNSUPPORTED;
-    if (x->n_seqs == 0 || x->n_q == 0 || blocks == 0)
+    if (x->n_seqs == 0 || x->n_q == 0 || (x->max_q == 0 && !d_err))   // nothing to write, or to report
         return KAMERA_OK;
     if (!x->q || !x->out || !x->q_start || !x->kv_start || (x->n_kv > 0 && (!x->kv || !x->k_rope)))
         return KAMERA_ERR_INVALID_ARGUMENT;
