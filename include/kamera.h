@@ -906,7 +906,8 @@ typedef struct KameraPagedMlaKV {
  *   query   q bf16 [n_seqs][num_q_heads][kv_lora_rank + rope_dim] (RoPE already
  *           applied), out bf16 [n_seqs][num_q_heads][kv_lora_rank] (written), lse fp32
  *           [n_seqs][num_q_heads] (written) or NULL; q and out 16-byte aligned
- *   table   as for kamera_attend_shared's own tokens
+ *   table   as for kamera_attend_shared's own tokens (but lens is read, and needed, where
+ *           max_len is 0 too)
  *   d_workspace  at least kamera_mla_attend_paged_workspace_bytes(...) bytes, rules as
  *           for kamera_attend_shared
  * Supported: kv_lora_rank 512, rope_dim 64, num_q_heads 1..128, page_size a multiple
@@ -1045,9 +1046,10 @@ int kamera_unpack_pages(const KameraGqaPool* pool, int32_t layer, const KameraPa
  * (2^-11).  The tail as kamera_attend_shared.  One bf16 rounding of the output; a
  * sequence with no token gets zeros and lse = -infinity.
  *   query   as for kamera_attend_shared
- *   table   packed pages and lengths
+ *   table   packed pages and lengths (max_len 0: none; pages is not read, lens is NULL
+ *           or looked at, and a length other than 0 reported)
  *   tail_kv, tail  both NULL, or the bf16 pool of the tails (its own page_size) and
- *           their page tables and lengths
+ *           their page tables and lengths (max_len 0 as for table)
  *   d_workspace  at least kamera_attend_packed_workspace_bytes(...) bytes, rules as for
  *           kamera_attend_shared
  * Supported: head_dim 64 or 128, num_q_heads / num_kv_heads in 1..16, page_size a

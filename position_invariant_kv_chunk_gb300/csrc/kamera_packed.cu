@@ -77,7 +77,7 @@ struct P4Params {
     float* lse;                    // or null
     const unsigned char* data;     // packed pages
     const int32_t* pages;
-    const int32_t* lens;
+    const int32_t* lens;           // null: max_len is 0
     float* o;                      // [2 ranges][G][d]: partial outputs
     float2* ml;                    // [2 ranges][G]
     int4* span;                    // [n_seqs * H]: first and last range, first slot
@@ -87,7 +87,7 @@ struct P4Params {
     // the tail's partial states: [rows][tail_slots]
     const float* tail_o;
     const float2* tail_ml;
-    const int32_t* tail_lens;
+    const int32_t* tail_lens;      // or null
     int32_t max_tail, tail_split, tail_slots;   // 16-token pieces of a split; splits (0: no tail)
     int32_t first;                 // the call's first kernel
     int32_t* err;
@@ -917,6 +917,9 @@ __global__ void __launch_bounds__(32 * NW) packed_merge_kernel(const P4Params p)
     const bool some = p.max_len > 0 && p4_len(p, s) > 0;
     ptx::grid_wait();
     ptx::grid_launch_next();
+    if (threadIdx.x == 0 && g == 0 && unit == s * p.H &&   // a bound of no tokens: no other kernel looks at the lengths
+        ((p.max_len == 0 && p.lens && p.lens[s] != 0) || (p.tail_slots == 0 && p.tail_lens && p.tail_lens[s] != 0)))
+        raise_err(p.err, KAMERA_DEVERR_LEN);
     int n_packed = 0;
     int4 sp = make_int4(0, 0, 0, 0);
     if (some) {
@@ -1129,8 +1132,9 @@ int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery*
     if (x.has_tail && ((e = check_strided(tail_kv->k, 1, 0, tail_kv->num_slots, tail_kv->slot_stride, W, false)) ||
                        (e = check_strided(tail_kv->v, 1, 0, tail_kv->num_slots, tail_kv->slot_stride, W, false))))
         return e;
-    const uintptr_t ints = (p.ranges > 0 ? reinterpret_cast<uintptr_t>(table->pages) | reinterpret_cast<uintptr_t>(table->lens) : 0) |
-                           (x.has_tail ? reinterpret_cast<uintptr_t>(tail->pages) | reinterpret_cast<uintptr_t>(tail->lens) : 0);
+    const int32_t* tail_lens = tail ? tail->lens : nullptr;
+    const uintptr_t ints = (p.ranges > 0 ? reinterpret_cast<uintptr_t>(table->pages) : 0) | reinterpret_cast<uintptr_t>(table->lens) |
+                           (x.has_tail ? reinterpret_cast<uintptr_t>(tail->pages) : 0) | reinterpret_cast<uintptr_t>(tail_lens);
     if (!aligned16(query->q) || !aligned16(query->out) || !aligned16(packed->data) || !aligned16(d_workspace) ||
         ((reinterpret_cast<uintptr_t>(query->lse) | ints) & 3))
         return KAMERA_ERR_MISALIGNED;
@@ -1144,11 +1148,11 @@ int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery*
     const Span in[] = {bytes(query->q, rows * d * 2),
                        bytes(packed->data, p.ranges > 0 ? packed_bytes(packed) : 0),
                        bytes(table->pages, p.ranges > 0 ? (int64_t)p.n_seqs * p.max_pages * 4 : 0),
-                       bytes(table->lens, p.ranges > 0 ? (int64_t)p.n_seqs * 4 : 0),
+                       bytes(table->lens, (int64_t)p.n_seqs * 4),
                        x.has_tail ? span(tail_kv->k, 1, 0, tail_kv->num_slots, tail_kv->slot_stride, W) : Span{0, 0},
                        x.has_tail ? span(tail_kv->v, 1, 0, tail_kv->num_slots, tail_kv->slot_stride, W) : Span{0, 0},
                        x.has_tail ? bytes(tail->pages, (int64_t)p.n_seqs * tail->max_pages * 4) : Span{0, 0},
-                       x.has_tail ? bytes(tail->lens, (int64_t)p.n_seqs * 4) : Span{0, 0}};
+                       bytes(tail_lens, (int64_t)p.n_seqs * 4)};
     const Span outs[] = {bytes(query->out, rows * d * 2), bytes(query->lse, rows * 4),
                          bytes(d_workspace, (int64_t)x.bytes())};
     for (int i = 0; i < 3; ++i) {
@@ -1165,8 +1169,7 @@ int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery*
     p.data = static_cast<const unsigned char*>(packed->data);
     p.pages = table->pages;
     p.lens = table->lens;
-    if (p.ranges == 0)
-        p.max_len = 0;   // nothing to read: no length is looked at
+    p.tail_lens = tail_lens;
     unsigned char* ws = static_cast<unsigned char*>(d_workspace);
     p.o = reinterpret_cast<float*>(ws);
     p.ml = reinterpret_cast<float2*>(ws + x.o);
@@ -1189,7 +1192,6 @@ int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery*
         t.withhold = p.withhold;
         p.tail_o = t.o;
         p.tail_ml = t.ml;
-        p.tail_lens = tail->lens;
         if (launch_own_pages(t, tail_kv, stream) != cudaSuccess)
             return KAMERA_ERR_CUDA;
     }
