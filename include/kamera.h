@@ -905,7 +905,9 @@ typedef struct KameraPagedMlaKV {
  * table names, are not used whatever they hold.
  *   query   q bf16 [n_seqs][num_q_heads][kv_lora_rank + rope_dim] (RoPE already
  *           applied), out bf16 [n_seqs][num_q_heads][kv_lora_rank] (written), lse fp32
- *           [n_seqs][num_q_heads] (written) or NULL; q and out 16-byte aligned
+ *           [n_seqs][num_q_heads] (written) or NULL; q and out 16-byte aligned; scale is
+ *           the model's, 1 / sqrt(nope_dim + rope_dim) of its heads' keys before their
+ *           no-position part is absorbed, as in kamera_mla_prefill_attend
  *   table   as for kamera_attend_shared's own tokens (but lens is read, and needed, where
  *           max_len is 0 too)
  *   d_workspace  at least kamera_mla_attend_paged_workspace_bytes(...) bytes, rules as

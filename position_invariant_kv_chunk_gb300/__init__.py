@@ -814,8 +814,9 @@ def kamera_mla_attend_reused(store: torch.Tensor, kv_lora: int, q: torch.Tensor,
     store: bf16 ``[N, kv_lora + rope_dim]`` (one layer, any row stride);
     q: bf16 ``[S, H_q, kv_lora + rope_dim]`` contiguous (latent query, then
     rope query); seq_start: device int32 ``[S + 1]``; rope: rot_offset
-    relative to k_rope; scale: default 1/sqrt(kv_lora + rope_dim); workspace:
-    as for ``kamera_attend_reused``.  Returns ``out`` (bf16 ``[S, H_q, kv_lora]``)."""
+    relative to k_rope; scale: default 1/sqrt(kv_lora + rope_dim), the rows' own width (a
+    model's is 1/sqrt(nope_dim + rope_dim), of its heads' keys before the absorption);
+    workspace: as for ``kamera_attend_reused``.  Returns ``out`` (bf16 ``[S, H_q, kv_lora]``)."""
     _on_device("kamera_mla_attend_reused", store=store, q=q, chunks=chunks, seq_start=seq_start, out=out, err=err)
     for t, nm in ((store, "store"), (q, "q")):
         _bf16(t, nm)
@@ -968,17 +969,29 @@ def kamera_attend_selected(pool_k: torch.Tensor, pool_v: torch.Tensor, q: torch.
 def kamera_mla_attend_paged(pool: torch.Tensor, kv_lora: int, q: torch.Tensor, page_size: int, pages: torch.Tensor,
                             lens: torch.Tensor, max_len: int, scale: Optional[float] = None,
                             out: Optional[torch.Tensor] = None, lse=None, err: Optional[torch.Tensor] = None, stream=None,
-                            workspace: Optional[torch.Tensor] = None):
+                            workspace: Optional[torch.Tensor] = None, nope_dim: Optional[int] = None):
     """MLA decode attention (absorbed form) of one query token per sequence over the
     latent rows in the paged pool (``kamera_mla_attend_paged`` in kamera.h).
 
     pool: bf16 ``[S_slots, kv_lora + rope_dim]`` (one layer, any row stride); q: bf16
     ``[S, H_q, kv_lora + rope_dim]`` contiguous (latent query, then rope query); pages
-    int32 ``[S, width]``, lens int32 ``[S]``; scale: default 1/sqrt(kv_lora + rope_dim);
-    lse: None (allocated), False (not computed) or fp32 ``[S, H_q]``; workspace: None
-    (allocated for the call) or a tensor of at least
+    int32 ``[S, width]``, lens int32 ``[S]``; lse: None (allocated), False (not computed)
+    or fp32 ``[S, H_q]``; workspace: None (allocated for the call) or a tensor of at least
     ``kamera_mla_attend_paged_workspace_bytes`` bytes.  Returns ``(out, lse)``, out bf16
-    ``[S, H_q, kv_lora]``."""
+    ``[S, H_q, kv_lora]``.
+
+    scale, nope_dim: a model's softmax is scaled for its heads' keys, nope_dim + rope_dim
+    wide before their no-position part is absorbed, which the latent rows do not show.
+    Give ``nope_dim`` (128: the default scale of ``kamera_mla_prefill_attend`` over the
+    expanded rows, 192 ** -0.5), or the scale itself.  With neither it is 1/sqrt(kv_lora +
+    rope_dim), the rows' own width."""
+    if nope_dim is not None:
+        if scale is not None:
+            raise ValueError("scale and nope_dim: give one of them")
+        width = operator.index(nope_dim) + pool.shape[-1] - kv_lora
+        if nope_dim < 0 or width < 1:
+            raise ValueError("nope_dim must not be negative, and the heads' keys at least one wide")
+        scale = width ** -0.5
     return (_FAST or _fast()).mla_attend_paged(pool, kv_lora, q, page_size, pages, lens, max_len, scale, out, lse, err,
                                                stream, workspace)
 

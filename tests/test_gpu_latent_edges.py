@@ -57,3 +57,19 @@ def test_packed_attention_with_a_bound_of_no_tokens(H, G, d):
     assert bits == LEN
     (want, wl), bits = call(None, None, 0, **tail)
     assert bits == 0 and torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("Hq,nope", [(16, 128), (40, 128), (4, 0)])
+def test_decode_scaled_for_the_heads_before_the_absorption(Hq, nope):
+    """nope_dim gives the scale of the expanded heads' keys, the one that prefill takes."""
+    lens = [200, 0, 65]
+    pool = T.Pool(Hq, 30, 16)
+    table = pool.table(lens)
+    q = normal(pool.g, 3, Hq, T.W)
+    args = (pool.kv, T.LORA, q, 16, table, i32(lens), 200)
+    scale = float(np.float32((nope + 64) ** -0.5))
+    out, lse = K.kamera_mla_attend_paged(*args, nope_dim=nope)
+    same, sl = K.kamera_mla_attend_paged(*args, scale=(nope + 64) ** -0.5)
+    torch.cuda.synchronize()
+    assert torch.equal(out, same) and torch.equal(lse, sl)
+    L.near(out, lse, T.decode_refs(q, pool, table, lens, scale), T.W, T.weight_error(Hq), (Hq, nope))
