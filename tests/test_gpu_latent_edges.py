@@ -5,6 +5,7 @@ import torch
 
 import position_invariant_kv_chunk_gb300 as K
 from tests import latent_ref as L
+from tests import paged_ref as R
 from tests import test_gpu_latent as T
 from tests import test_gpu_packed as P4
 from tests.test_gpu_latent import DESCRIPTOR, DEV, LEN, gen, i32, normal
@@ -73,3 +74,98 @@ def test_decode_scaled_for_the_heads_before_the_absorption(Hq, nope):
     torch.cuda.synchronize()
     assert torch.equal(out, same) and torch.equal(lse, sl)
     L.near(out, lse, T.decode_refs(q, pool, table, lens, scale), T.W, T.weight_error(Hq), (Hq, nope))
+
+
+@pytest.mark.parametrize("tokens,H", [(1, 128), (300, 128), (2000, 100), (700, 40)])
+def test_expansion_of_many_heads(tokens, H):
+    g = gen(tokens + H)
+    pool, weight = normal(g, tokens + 9, T.W), normal(g, H, 256, T.LORA, std=0.05)
+    slots = torch.randperm(tokens + 9, generator=g, device=DEV)[:tokens]
+    err = i32([0])
+    kv, kr = K.kamera_mla_expand(pool, T.LORA, weight, slots, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(kr, pool[slots][:, T.LORA:])
+    T.expand_near(kv, pool, weight, slots.cpu().numpy())
+
+
+@pytest.mark.parametrize("Hq", [16, 128])
+def test_latent_rows_past_32_bits(Hq):
+    """Rows whose place in the pool, in elements and in bytes, passes 32 bits."""
+    P, W, lens = 16, T.W, [90, 200]
+    n = 2 ** 32 // (P * W) + 40                                     # pages; 8.6 GB
+    g = gen(Hq)
+    pool = torch.empty(n * P, W, dtype=BF, device=DEV)
+    pages = [n - 1 - i for i in range(10)] + [2 ** 31 // (P * W) + i for i in range(10)]
+    rows = torch.tensor([p * P + t for p in pages for t in range(P)], device=DEV)
+    pool[rows] = normal(g, len(rows), W)
+    table = [pages[0::3] + [-1] * 6, pages[1::3] + pages[2::3]]
+    table = i32([row[:13] for row in table])
+    q, weight = normal(g, 2, Hq, W), normal(g, 3, 256, T.LORA, std=0.05)
+    err = i32([0])
+    out, lse = K.kamera_mla_attend_paged(pool, T.LORA, q, P, table, i32(lens), 200, err=err)
+    kv, kr = K.kamera_mla_expand(pool, T.LORA, weight, rows, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    refs = []
+    for s, m in enumerate(lens):
+        at = torch.tensor([int(table[s, t // P]) * P + t % P for t in range(m)], device=DEV)
+        refs += L.latent_rows(R.f64(q)[s], R.f64(pool[at]), T.LORA, W ** -0.5)
+    L.near(out, lse, refs, W, T.weight_error(Hq), Hq)
+    here = pool[rows]
+    assert torch.equal(kr, here[:, T.LORA:])
+    T.expand_near(kv, here, weight, np.arange(len(rows)))
+
+
+def test_packed_pages_past_32_bits():
+    """Pages of either pool behind 2^31 elements and 2^32 bytes, both ways and read by attention."""
+    P, H, d, G = 16, 4, 128, 7
+    n, m = 2 ** 32 // (P * H * P * 9) + 30, 2 ** 31 // (P * H * d) + 30     # packed pages (4.3 GB), bf16 pages (4.3 GB a pool)
+    g = gen(8)
+    packed = torch.empty(n, H, P * (d + d // 8), dtype=torch.uint8, device=DEV)
+    k, v = torch.empty(m * P, H, d, dtype=BF, device=DEV), torch.empty(m * P, H, d, dtype=BF, device=DEV)
+    src, dst, back = [m - 1 - i for i in range(8)], [n - 1 - 2 * i for i in range(8)], [m - 20 - i for i in range(8)]
+    rows = lambda pages: torch.tensor([p * P + t for p in pages for t in range(P)], device=DEV)
+    k[rows(src)], v[rows(src)] = normal(g, 8 * P, H, d), normal(g, 8 * P, H, d)
+    err = i32([0])
+    K.kamera_pack_pages(k, v, P, i32(src), i32([P] * 8), packed, i32(dst), err=err)
+    K.kamera_unpack_pages(packed, P, i32(dst), i32([P] * 8), k, v, i32(back), err=err)
+    q = normal(g, 1, H * G, d)
+    out, lse = K.kamera_attend_packed(packed, q, P, i32([dst]), i32([120]), 120, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    pk, pv = P4.pack_ref(k[rows(src)], v[rows(src)], P, 8)
+    assert np.array_equal(R.f64(k[rows(back)]), pk) and np.array_equal(R.f64(v[rows(back)]), pv)
+    refs = []
+    for h in range(H):
+        o, l, mag, x = R.attention(R.f64(q)[0, h * G:h * G + G], pk[:120, h], pv[:120, h], d ** -0.5)
+        refs += [(o[j], l[j], mag[j], x[j], 120, np.abs(pv[:120, h]).sum(0)) for j in range(G)]
+    L.near(out, lse, refs, d, P4.HALF, "packed", P4.LEAST)
+
+
+def test_expanded_rows_and_outputs_past_32_bits():
+    """Expanded rows, queries and outputs behind 2^31 elements."""
+    H, n = 128, 2 ** 31 // (128 * 256) + 500
+    g = gen(11)
+    pool, weight = normal(g, 400, T.W), normal(g, H, 256, T.LORA, std=0.05)
+    slots = torch.arange(n, device=DEV) % 400
+    err = i32([0])
+    kv, kr = K.kamera_mla_expand(pool, T.LORA, weight, slots, err=err)
+    one, _ = K.kamera_mla_expand(pool, T.LORA, weight, slots[:400], err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for a in (0, n // 2, n - 400):
+        assert torch.equal(kv[a:a + 400], one[slots[a:a + 400]]) and torch.equal(kr[a:a + 400], pool[slots[a:a + 400]][:, T.LORA:])
+    nq, nk = 2 ** 31 // (H * 128) + 300, 150
+    q = torch.empty(nq, H, 192, dtype=BF, device=DEV)
+    for a in range(0, nq, 20000):
+        q[a:a + 20000] = normal(g, min(20000, nq - a), H, 192)
+    start = [0, 7, nq]
+    out, lse = K.kamera_mla_prefill_attend(q, kv, kr, i32(start), i32([n - 2 * nk, n - nk, n]), nq, causal=False, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    for h in (0, H - 1):
+        for s, some in ((0, [0, 6]), (1, [7, nq // 2, nq - 130, nq - 1])):
+            rows = slice(n - (2 - s) * nk, n - (1 - s) * nk)
+            k = np.concatenate([R.f64(kv[rows, h, :128]), R.f64(kr[rows])], axis=1)
+            refs = L.prefill_rows(R.f64(q[some, h]), k, R.f64(kv[rows, h, 128:]), 192 ** -0.5, False)
+            L.near(out[some, h], lse[some, h], refs, 192, 2.0 ** -8, (h, s))
