@@ -13,13 +13,13 @@
 // them.  A captured graph therefore owns its workspace.
 #include <Python.h>
 
+#include <array>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <optional>
 #include <stdexcept>
 #include <string>
-#include <vector>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
@@ -565,14 +565,11 @@ struct QueryArg {
     bool want_lse;
     PyObject *out_o, *lse_o;
     at::Tensor made_out, made_lse;
-
-    std::vector<int64_t> shape;   // of out: q's, or another width
+    std::array<int64_t, 3> shape;   // of out: q's, or another width
 
     QueryArg(const at::Tensor& q, PyObject* scale, PyObject* out_obj, PyObject* lse_obj, int64_t width = -1)
-        : out_o(out_obj), lse_o(lse_obj), shape(q.sizes().vec())
+        : out_o(out_obj), lse_o(lse_obj), shape{q.size(0), q.size(1), width >= 0 ? width : q.size(2)}
     {
-        if (width >= 0)
-            shape.back() = width;
         std::memset(&c, 0, sizeof(c));
         out = optional(out_obj, "out");
         want_lse = lse_obj != Py_False;
@@ -858,7 +855,8 @@ PyObject* mla_expand(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         const int64_t T = slots.numel();
         exact(slots, "slots", at::kLong, {T});
         const at::Tensor *kv = optional(a[4], "kv"), *kr = optional(a[5], "k_rope"), *err = optional(a[6], "err");
-        const std::vector<int64_t> wide{T, w.size(0), w.size(1)}, narrow{T, p.size(1) - w.size(2)};
+        const std::array<int64_t, 3> wide{T, w.size(0), w.size(1)};
+        const std::array<int64_t, 2> narrow{T, p.size(1) - w.size(2)};
         if (kv)
             exact(*kv, "kv", at::kBFloat16, wide);
         if (kr)
@@ -924,7 +922,8 @@ PyObject* mla_prefill_attend(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         const bool want_lse = a[9] != Py_False;
         if (want_lse)
             lse = optional(a[9], "lse");
-        const std::vector<int64_t> shape{q.size(0), q.size(1), v}, rows{q.size(0), q.size(1)};
+        const std::array<int64_t, 3> shape{q.size(0), q.size(1), v};
+        const std::array<int64_t, 2> rows{q.size(0), q.size(1)};
         if (out)
             exact(*out, "out", at::kBFloat16, shape);
         if (lse)
