@@ -396,9 +396,9 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
     const bool valid = query < w.rows;
     const uint32_t lanes = tm + ((uint32_t)(r & ~31) << 16);
     const uint32_t tS = lanes + kPrTmS + a * kPrTok, tO = lanes + kPrTmO + a * kPrV;
-    // scores in log2 units; a scale of zero becomes the smallest normal float, so that a
-    // masked score stays infinite under it (a score of 2^100 still rounds to 0)
-    const float sl2 = p.scale == 0.f ? 1.17549435e-38f : p.scale * 1.4426950408889634f;
+    // scores in log2 units; a scale of zero becomes the smallest float, 2^-149, so that a
+    // masked score stays infinite under it (the largest finite one becomes 2^-21)
+    const float sl2 = p.scale == 0.f ? 1.40129846e-45f : p.scale * 1.4426950408889634f;
     const int limit = p.causal ? min(w.nk, query + w.shift + 1) : w.nk;   // rows that the query sees
     const int least = p.causal ? min(w.nk, w.query0(a) + w.shift + 1) : w.nk;   // ... that the side's first one sees
     float m_run = -INFINITY, l_run = 0.f;

@@ -169,3 +169,18 @@ def test_expanded_rows_and_outputs_past_32_bits():
             k = np.concatenate([R.f64(kv[rows, h, :128]), R.f64(kr[rows])], axis=1)
             refs = L.prefill_rows(R.f64(q[some, h]), k, R.f64(kv[rows, h, 128:]), 192 ** -0.5, False)
             L.near(out[some, h], lse[some, h], refs, 192, 2.0 ** -8, (h, s))
+
+
+@pytest.mark.parametrize("seqs,H,scale", [(1, 2, 0.0), (1, 2, -0.0), (4, 40, 0.0), (1, 2, 2.0 ** -149)])
+def test_prefill_of_large_scores_without_a_scale(seqs, H, scale):
+    """A scale of zero weighs every row that is seen alike, scores of up to 2^125 too."""
+    g = gen(13)
+    nq, nk = 150, 300
+    qs, ks = T.starts([nq] * seqs), T.starts([nk] * seqs)
+    q, kv, kr = normal(g, qs[-1], H, 192), normal(g, ks[-1], H, 256), normal(g, ks[-1], 64)
+    q[:, :, 1:], q[:, :, 0] = 0, 2.0 ** 62
+    kv[:, :, 0] = torch.linspace(-8, 8, ks[-1], device=DEV)[:, None].to(BF) * 2.0 ** 60
+    out, lse = K.kamera_mla_prefill_attend(q, kv, kr, i32(qs), i32(ks), nq, scale=scale)
+    torch.cuda.synchronize()
+    refs, seen = T.prefill_refs(q[:nq], kv[:nk], kr[:nk], [0, nq], [0, nk], 0.0, True)
+    L.near(out[:nq], lse[:nq], refs, 192, 2.0 ** -8, (seqs, H, scale))
