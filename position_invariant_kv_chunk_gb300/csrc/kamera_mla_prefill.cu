@@ -720,7 +720,7 @@ int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct 
     };
     const Span in[] = {bytes(x->q, ((x->n_q - 1) * qt + (H - 1) * qh + kPrQk) * 2),
                        span(x->kv, 1, 0, x->n_kv, kt, kvw), span(x->k_rope, 1, 0, x->n_kv, rt, kPrQk - kPrNope),
-                       bytes(x->q_start, (int64_t)(x->n_seqs + 1) * 4), bytes(x->kv_start, (int64_t)(x->n_seqs + 1) * 4)};
+                       bytes(x->q_start, ((int64_t)x->n_seqs + 1) * 4), bytes(x->kv_start, ((int64_t)x->n_seqs + 1) * 4)};
     const Span os = bytes(x->out, (int64_t)x->n_q * H * kPrV * 2), ls = bytes(x->lse, (int64_t)x->n_q * H * 4);
     for (const Span& a : in)
         if (overlap(a, os) || overlap(a, ls))
