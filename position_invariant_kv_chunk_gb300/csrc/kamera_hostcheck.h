@@ -45,8 +45,10 @@ inline int check_strided(const void* base, int64_t L, int64_t ls, int64_t rows, 
 
 // SM cycles that last at least `ns` at any clock up to 2125 MHz (2070 is this chip's
 // highest; at half of it they last twice as long), and 1000 for a bound of nothing.  A
-// bound that they would pass 64 bits for is none.
-constexpr uint64_t wait_cycles(uint64_t ns) { return ns < (1ull << 62) ? 2 * ns + ns / 8 + 1000 : ~0ull; }
+// kernel gets half of them: with the sum taken on the host the prefill kernel's registers
+// fall out worse (4 x 4096 tokens 208 -> 213 us).
+constexpr uint64_t half_wait(uint64_t ns) { return ns < (1ull << 62) ? ns + ns / 16 : (1ull << 62) + (1ull << 58); }
+constexpr uint64_t wait_cycles(uint64_t half) { return 2 * half + 1000; }
 
 // theta / (2 pi) modulo 1, in units of 2^-64 (theta finite): the quotient as a
 // double-double, whose integer part drops out of a phase.  The fraction is taken

@@ -60,7 +60,7 @@ struct ExParams {
     int64_t num_slots, slot_stride, items;
     int32_t T, H;
     int32_t* err;
-    uint64_t wait_cycles;
+    uint64_t half_wait;
     int32_t withhold;
 };
 
@@ -183,7 +183,7 @@ __device__ void ex_producer(const ExLaunch& L, ExBars& b, uint32_t sbase)
     for (ExWalk w(p); w.more() && ok; w.next())
         for (int c = 0; c < kExChunks; ++c, ++k) {
             const uint32_t at = k % kExStages, lap = k / kExStages;
-            if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_cycles)) {
+            if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.half_wait)) {
                 ok = false;
                 break;
             }
@@ -220,7 +220,7 @@ __device__ void ex_mma(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t tm
     constexpr uint32_t id = ptx::idesc_bf16_f32(2 * kExTok, kExN);
     const uint32_t a_lo = (sbase >> 4) | (1u << 16), r_lo = ((sbase + kExRing) >> 4) | (1u << 16);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_cycles);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.half_wait);
     };
     uint32_t k = 0, n = 0, tiles = 0;
     bool ok = true, fresh = true;
@@ -303,7 +303,7 @@ __device__ void ex_gather(const ExLaunch& L, ExBars& b, uint32_t sbase, int warp
             } else {
 #pragma unroll
                 for (int c = 0; c < kExChunks; ++c) {
-                    ok = wmma16::cycle_wait(ptx::smem_addr(&b.a_empty[c]), (tiles - 1) & 1u, &b.abort, p.err, p.wait_cycles);
+                    ok = wmma16::cycle_wait(ptx::smem_addr(&b.a_empty[c]), (tiles - 1) & 1u, &b.abort, p.err, p.half_wait);
                     if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ptx::cp_async_commit();
                         ptx::cp_async_wait<0>();
@@ -362,7 +362,7 @@ __device__ void ex_epilogue(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32
     uint32_t n = 0, ok_word;
     bool ok = true;
     for (ExWalk w(p); w.more() && ok; w.next(), ++n) {
-        ok = wmma16::cycle_wait(ptx::smem_addr(&b.acc_full[n & 1u]), (n >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+        ok = wmma16::cycle_wait(ptx::smem_addr(&b.acc_full[n & 1u]), (n >> 1) & 1u, &b.abort, p.err, p.half_wait);
         ptx::tc_fence_after();
         const bool some = w.tile * kExTok < p.T;
 #pragma unroll 1
@@ -532,7 +532,7 @@ int kamera_mla_expand(const KameraPagedMlaKV* kv, const KameraMlaExpand* x, int3
     p.H = x->num_heads;
     p.items = (T + 2 * kExTok - 1) / (2 * kExTok) * H;
     p.err = d_err;
-    p.wait_cycles = wait_cycles(wait_limit_ns());
+    p.half_wait = half_wait(wait_limit_ns());
     p.withhold = test_withhold_loads() ? 1 : 0;
     if (!make_rows_map(&L.map_w, x->weight, H * kExN, kExK, kExK, 64, kExN / 2) ||
         !make_rows_map(&L.map_o, x->kv_out, T, H * kExN, H * kExN, 64, kExTok))

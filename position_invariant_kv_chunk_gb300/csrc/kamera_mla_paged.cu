@@ -105,7 +105,7 @@ struct MpParams {
     int32_t box_rows;
     float scale;
     int32_t* err;
-    uint64_t wait_cycles;
+    uint64_t half_wait;
     int32_t withhold;
 };
 
@@ -306,7 +306,7 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
     // The lane that waits and issues has these to itself.
     uint32_t unit = 0, rope = 0, seg = 0, at = 0, lap = 0, ra = 0, rl = 0;   // issued so far; places in the rings
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_cycles);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.half_wait);
     };
     uint32_t tile = 0, there = 0, there_next = 0;   // (the _next ones: once two tiles on are of the eight after)
     int group_next = 0;
@@ -453,7 +453,7 @@ __device__ void mp_scores(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32_t
     const MpParams& p = L.p;
     constexpr uint32_t idS = ptx::idesc_bf16_f32(kMpTok, N);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_cycles);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.half_wait);
     };
     const uint32_t q_lo = ((sbase + Y::kQ) >> 4) | (1u << 16), u_lo = ((sbase + Y::kRing) >> 4) | (1u << 16);
     const uint32_t r_lo = ((sbase + Y::kRopes) >> 4) | (1u << 16);
@@ -513,7 +513,7 @@ __device__ void mp_products(const MpLaunch& L, MpBars& b, uint32_t sbase, uint32
     const MpParams& p = L.p;
     constexpr uint32_t idO = ptx::idesc_bf16_f32(64, 128) | (1u << 16);   // B: MN-major
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_cycles);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.half_wait);
     };
     const uint32_t p_lo = ((sbase + Y::kP) >> 4) | (1u << 16);
     const uint32_t u_lo = ((sbase + Y::kRing) >> 4) | ((kMpAtom >> 4) << 16);
@@ -640,7 +640,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                 m[j][0] = m[j][1] = -INFINITY, l[j][0] = l[j][1] = 0.f;
         }
         const int ntok = min(kMpTok, w.len - w.t * kMpTok);
-        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.half_wait);
         ok = __all_sync(0xFFFFFFFFu, ok);
         uint32_t s[HG / 2];
         bool grew = false;
@@ -692,7 +692,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                         fac[h] = f;
                 }
             if (!w.fresh) {          // the running output, once the products before are in it
-                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.half_wait);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 ptx::tc_fence_after();
                 mp_sync(grp);
@@ -716,7 +716,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
         const uint32_t dst = st + t % Y::NP * Y::kPTile;
         if (t >= Y::NP) {            // the product that read the buffer's last weights
             const uint32_t k = t - Y::NP;
-            ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[k & 1u]), (k >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+            ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[k & 1u]), (k >> 1) & 1u, &b.abort, p.err, p.half_wait);
             ok = __all_sync(0xFFFFFFFFu, ok);
         }
 #pragma unroll
@@ -793,7 +793,7 @@ __device__ void mp_softmax(const MpLaunch& L, MpBars& b, uint32_t sbase, float* 
                     }
                 }
         }
-        ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+        ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.half_wait);
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
         mp_sync(grp);
@@ -1143,7 +1143,7 @@ int kamera_mla_attend_paged(const KameraPagedMlaKV* kv, const KameraPagedQuery* 
     p.ml = reinterpret_cast<float2*>(ws + need.o);
     p.span = reinterpret_cast<int4*>(ws + need.o + need.ml);
     p.err = d_err;
-    p.wait_cycles = wait_cycles(wait_limit_ns());
+    p.half_wait = half_wait(wait_limit_ns());
     p.withhold = test_withhold_loads() ? 1 : 0;
     p.box_rows = 16;
     while (p.box_rows < kMpTok && p.P % (2 * p.box_rows) == 0)

@@ -75,7 +75,7 @@ struct PrParams {
     int32_t causal, wide;          // wide: out is 32-byte aligned
     float scale;
     int32_t* err;
-    uint64_t wait_cycles;
+    uint64_t half_wait;
     int32_t withhold;
 };
 
@@ -171,7 +171,7 @@ __device__ void pr_producer(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b
     for (int t = 0; t < n && ok; ++t)
         for (int u = 0; u < kPrTile; ++u, ++k) {
             const uint32_t at = k % kPrUnits, lap = k / kPrUnits, full = ptx::smem_addr(&b.full[at]);
-            if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_cycles)) {
+            if (lap > 0 && !wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.half_wait)) {
                 ok = false;
                 break;
             }
@@ -193,9 +193,10 @@ __device__ void pr_producer(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b
 }
 
 // After a timeout, once every role has left its loop: the copies that the CTA started land
-// before it leaves.  (Without one the MMA lane has waited for every fill.)
+// before it leaves.  (Without one the MMA lane has waited for every fill.  Out of line, and
+// called with a softmax warp's registers: in line it costs a short prompt's call 0.2 us.)
 template <bool SPLIT>
-__device__ __forceinline__ void pr_drain(const PrBars& b)
+__device__ __noinline__ void pr_drain(const PrBars& b)
 {
     pf_drain_ring(&b.q_full, b.queries, 1);
     pf_drain_ring(b.full, b.units, PrLayout<SPLIT>::kUnits);
@@ -226,7 +227,7 @@ __device__ void pr_mma(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b, uin
     constexpr int kPrUnits = PrLayout<SPLIT>::kUnits;
     const uint32_t q_lo = (sbase >> 4) | (1u << 16), r_lo = (sbase + PrLayout<SPLIT>::kQUnits * kPrUnit) >> 4;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_cycles);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.half_wait);
     };
     // scores of side a's t-th tile; its keys are free after the last side that sees it
     auto scores = [&](auto side, int t) -> bool {
@@ -411,7 +412,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
             bool in = true;
             for (int u = 0; u < 2; ++u)
                 in = in && wmma16::cycle_wait(ptx::smem_addr(&b.full[(k + u) % kPrUnits]), ((k + u) / kPrUnits) & 1u, &b.abort,
-                                             p.err, p.wait_cycles);
+                                             p.err, p.half_wait);
             ok = __all_sync(0xFFFFFFFFu, ok && in);
             if (base + r >= least && base + r < w.nk)
                 pr_clean_row(unit(r), r & 63, base + r, first, &b.odd);
@@ -423,7 +424,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
             }
             ptx::fence_proxy_async();   // (the product waits for every thread's weights, which follow)
         }
-        if (!wmma16::cycle_wait(ptx::smem_addr(&b.s_full[a]), (uint32_t)t & 1u, &b.abort, p.err, p.wait_cycles))
+        if (!wmma16::cycle_wait(ptx::smem_addr(&b.s_full[a]), (uint32_t)t & 1u, &b.abort, p.err, p.half_wait))
             ok = false;
         if (!__all_sync(0xFFFFFFFFu, ok)) {
             ok = false;
@@ -476,7 +477,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
             const float f = m_new == -INFINITY ? 1.f : pf_ex2(m_run - m_new);
             l_run *= f;
             m_run = m_new;
-            if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(t - 1) & 1u, &b.abort, p.err, p.wait_cycles))
+            if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(t - 1) & 1u, &b.abort, p.err, p.half_wait))
                 ok = false;
             ok = __all_sync(0xFFFFFFFFu, ok);
             ptx::tc_fence_after();
@@ -524,7 +525,7 @@ __device__ void pr_softmax(const PrLaunch& L, const PrWork<SPLIT>& w, PrBars& b,
         }
     }
     if (nt > 0 && ok) {
-        if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(nt - 1) & 1u, &b.abort, p.err, p.wait_cycles))
+        if (!wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[a]), (uint32_t)(nt - 1) & 1u, &b.abort, p.err, p.half_wait))
             ok = false;
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tm, 512);
     }
-    if (threadIdx.x == 32 * kPrProd && b.abort)
+    if (threadIdx.x == 0 && b.abort)
         pr_drain<SPLIT>(b);
 }
 
@@ -744,7 +745,7 @@ int kamera_mla_prefill_attend(const KameraMlaPrefill* x, int32_t* d_err, struct 
     p.wide = (reinterpret_cast<uintptr_t>(x->out) & 31) == 0;
     p.scale = x->scale;
     p.err = d_err;
-    p.wait_cycles = wait_cycles(wait_limit_ns());
+    p.half_wait = half_wait(wait_limit_ns());
     p.withhold = test_withhold_loads() ? 1 : 0;
     // (without a row no tile is read: the maps take the queries' memory)
     const void* kv = x->n_kv > 0 ? x->kv : x->q;

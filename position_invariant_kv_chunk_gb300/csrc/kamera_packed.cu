@@ -91,7 +91,7 @@ struct P4Params {
     int32_t max_tail, tail_split, tail_slots;   // 16-token pieces of a split; splits (0: no tail)
     int32_t first;                 // the call's first kernel
     int32_t* err;
-    uint64_t wait_cycles;
+    uint64_t half_wait;
     int32_t withhold;
 };
 
@@ -318,7 +318,7 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
         if (lap > 0) {
             bool got = true;
             if (lane == 0)
-                got = wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.wait_cycles);
+                got = wmma16::cycle_wait(ptx::smem_addr(&b.empty[at]), (lap & 1u) ^ 1u, &b.abort, p.err, p.half_wait);
             if (!__shfl_sync(0xFFFFFFFFu, got ? 1 : 0, 0))
                 break;
         }
@@ -369,7 +369,7 @@ __device__ void p4_mma(const P4Params& p, P4Bars& b, uint32_t sbase, uint32_t tm
     constexpr uint32_t id = (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24);   // fp16 x fp16 -> fp32, M 128
     const uint32_t q_lo = ((sbase + Y::kQ) >> 4) | (1u << 16), p_lo = ((sbase + Y::kP) >> 4) | (1u << 16);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.wait_cycles);
+        return wmma16::cycle_wait(ptx::smem_addr(bar), parity & 1u, &b.abort, p.err, p.half_wait);
     };
     uint32_t seg = 0;
     auto scores = [&](uint32_t t, const P4Walk& v) -> bool {   // of tile t, whose keys are there
@@ -429,7 +429,7 @@ __device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* rin
     bool ok = true;
     for (uint32_t t = 0; t < n; ++t) {
         const uint32_t at = t % Y::NS;
-        ok = wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_cycles);
+        ok = wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.half_wait);
         if (!__all_sync(0xFFFFFFFFu, ok))
             return;
         const unsigned char* tile = ring + at * Y::kTile;
@@ -451,7 +451,7 @@ __device__ void p4_values(const P4Params& p, P4Bars& b, const unsigned char* rin
                 }
             }
             if (half == 0 && t > 0) {   // the product before has read the last tile's values
-                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.half_wait);
                 if (!__all_sync(0xFFFFFFFFu, ok))
                     return;
                 ptx::tc_fence_after();
@@ -579,9 +579,9 @@ __device__ void p4_keys(const P4Params& p, P4Bars& b, const unsigned char* ring,
     const uint32_t tK = tm + ((uint32_t)warp << 21) + kP4TmK;
     for (uint32_t t = 0; t < n; ++t) {
         const uint32_t at = t % Y::NS;
-        bool ok = wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.wait_cycles);
+        bool ok = wmma16::cycle_wait(ptx::smem_addr(&b.full[at]), (t / Y::NS) & 1u, &b.abort, p.err, p.half_wait);
         if (t >= 2)   // the keys of two tiles before have been scored
-            ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), ((t >> 1) - 1) & 1u, &b.abort, p.err, p.wait_cycles);
+            ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), ((t >> 1) - 1) & 1u, &b.abort, p.err, p.half_wait);
         if (!__all_sync(0xFFFFFFFFu, ok))
             return;
         ptx::tc_fence_after();
@@ -662,7 +662,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* 
             if (next.left > 0)
                 stage(next);
         }
-        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.s_full[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.half_wait);
         ok = __all_sync(0xFFFFFFFFu, ok);
         const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&b.mask[t % kP4Masks]);
         const int ntok = min(kP4Tok, w.len - w.t * kP4Tok);
@@ -727,7 +727,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* 
                         fac[h] = f;
                 }
             if (!w.fresh) {          // the running output, once the products before are in it
-                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+                ok = wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[(t - 1) & 1u]), ((t - 1) >> 1) & 1u, &b.abort, p.err, p.half_wait);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 ptx::tc_fence_after();
                 p4_sync();
@@ -756,7 +756,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* 
             }
         }
         if (t > 1) {                 // the weights of two tiles before have been read
-            ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), ((t >> 1) - 1) & 1u, &b.abort, p.err, p.wait_cycles);
+            ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), ((t >> 1) - 1) & 1u, &b.abort, p.err, p.half_wait);
             ok = __all_sync(0xFFFFFFFFu, ok);
         }
 #pragma unroll
@@ -801,7 +801,7 @@ __device__ void p4_softmax(const P4Params& p, P4Bars& b, uint32_t sbase, float* 
                                                                                 (wmax[2 * N + h] + wmax[3 * N + h]));
                 }
         }
-        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.wait_cycles);
+        ok = ok && wmma16::cycle_wait(ptx::smem_addr(&b.pv_done[t & 1u]), (t >> 1) & 1u, &b.abort, p.err, p.half_wait);
         ok = __all_sync(0xFFFFFFFFu, ok);
         ptx::tc_fence_after();
         uint32_t o[N];
@@ -1175,7 +1175,7 @@ int kamera_attend_packed(const KameraPackedPool* packed, const KameraPagedQuery*
     p.ml = reinterpret_cast<float2*>(ws + x.o);
     p.span = reinterpret_cast<int4*>(ws + x.o + x.ml);
     p.err = d_err;
-    p.wait_cycles = wait_cycles(wait_limit_ns());
+    p.half_wait = half_wait(wait_limit_ns());
     p.withhold = test_withhold_loads() ? 1 : 0;
     p.first = x.has_tail ? 0 : 1;
     // The tail's kernel first: short, and the packed one's CTAs start beside it.

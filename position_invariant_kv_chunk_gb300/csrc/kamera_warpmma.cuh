@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 
 #include "kamera_common.cuh"
+#include "kamera_hostcheck.h"
 #include "kamera_ptx.cuh"
 
 namespace kamera {
@@ -86,10 +87,10 @@ __device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
-// The same, timed by the SM's clock (`cycles` of it: wait_cycles()): reading the global
+// The same, timed by the SM's clock (bound: half_wait()): reading the global
 // timer takes a microsecond or more, which a wait that outlasts one try pays every time.
 __device__ __forceinline__ bool cycle_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort, int32_t* err,
-                                           uint64_t cycles)
+                                           uint64_t half)
 {
     if (ptx::mbar_try_wait(bar, parity))
         return true;
@@ -99,7 +100,7 @@ __device__ __forceinline__ bool cycle_wait(uint32_t bar, uint32_t parity, volati
             return true;
         if (*abort)
             return false;
-        if ((uint64_t)(clock64() - t0) > cycles) {
+        if ((uint64_t)(clock64() - t0) > wait_cycles(half)) {
             *abort = 1;
             raise_err(err, KAMERA_DEVERR_TIMEOUT);
             return false;
