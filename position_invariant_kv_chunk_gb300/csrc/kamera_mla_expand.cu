@@ -156,13 +156,6 @@ __device__ __forceinline__ void ex_commit(uint32_t bar)
                  : "memory");
 }
 
-__device__ __forceinline__ bool ex_elect()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // This CTA's half of fill k, of a head's weights.
 __device__ __forceinline__ void ex_fill(const ExLaunch& L, ExBars& b, uint32_t sbase, uint32_t k, int head)
 {
@@ -448,10 +441,10 @@ __global__ void __launch_bounds__(kExThreads, 1) mla_expand_kernel(const __grid_
     else if (warp < kExProd)
         ex_epilogue<1>(L, b, sbase, tm, warp - 4, lane);
     else if (warp == kExProd) {
-        if (ex_elect())
+        if (elect_one())
             ex_producer(L, b, sbase);
     } else if (warp == kExMma) {
-        if ((blockIdx.x & 1) == 0 && ex_elect())
+        if ((blockIdx.x & 1) == 0 && elect_one())
             ex_mma(L, b, sbase, tm);
     } else
         ex_gather(L, b, sbase, warp - kExGather, lane);

@@ -249,14 +249,6 @@ __device__ void mp_locate(const MpParams& p, MpBars& b, int r, int lane)
 }
 
 // ---------------------------------------------------------------- producer --
-// --------------------------------------------------------------------- MMA --
-__device__ __forceinline__ bool mp_elect()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // The rows that a load of the same place would bring, into L2.
 __device__ __forceinline__ void mp_prefetch(const CUtensorMap* map, int col, int group)
 {
@@ -348,7 +340,7 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
         // One lane for all of a tile: a step that the warp takes together, or that lanes
         // take each by itself, costs this warp 150 cycles and more, and 580 a unit made it
         // what the whole CTA waited for.
-        if (mp_elect()) {
+        if (elect_one()) {
             auto load = [&](uint32_t dst, uint32_t full, const CUtensorMap* map, int col, uint32_t row_group) {
                 if (p.withhold)
                     return;
@@ -409,7 +401,7 @@ __device__ void mp_producer(const MpLaunch& L, MpBars& b, uint32_t sbase, int la
         w.next(p);
         ++tile;
     }
-    if (mp_elect() && !p.withhold) {
+    if (elect_one() && !p.withhold) {
         b.units = unit;
         b.ropes = rope;
         b.segs = seg;
@@ -428,6 +420,7 @@ __device__ __forceinline__ void mp_drain(const MpBars& b)
     pf_drain_ring(b.rfull, b.ropes, Y::NR);
 }
 
+// --------------------------------------------------------------------- MMA --
 // MMAs whose A (mma_ds) or B (mma_sd) is a unit, groups of eight rows 2 KB apart; the
 // other operand has them 1 KB apart.  The accumulate flag and the descriptors' high
 // words are constants: with them in registers an issue took 58 cycles, where the tensor
@@ -909,9 +902,9 @@ __global__ void __launch_bounds__(MpLayout<N>::kThreads, 1) mla_paged_kernel(con
         else if (warp == Y::kProd)
             mp_producer<N>(L, b, sbase, lane, block);
         else if (warp == Y::kScores) {
-            if (mp_elect())
+            if (elect_one())
                 mp_scores<N>(L, b, sbase, tm);
-        } else if (mp_elect())
+        } else if (elect_one())
             mp_products<N>(L, b, sbase, tm);
     }
     ptx::tc_fence_before();

@@ -202,15 +202,6 @@ __device__ __noinline__ void pr_drain(const PrBars& b)
     pf_drain_ring(b.full, b.units, PrLayout<SPLIT>::kUnits);
 }
 
-// One lane of the (converged) warp; the compiler knows that a branch on it holds a
-// single thread.
-__device__ __forceinline__ bool pr_elect()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // The MMA lane.  What it does next waits behind the dispatch of its MMAs, looks at
 // barriers too, which leaves the tensor pipe idle for about 500 of 3350 cycles a pair of
 // tiles (2680 of MMAs).  Tried for 4 x 4096 tokens, at 195 us: a lane a side 230 (both sides
@@ -652,9 +643,9 @@ __global__ void __launch_bounds__(kPrThreads, 1) mla_prefill_kernel(const __grid
     } else {
         ptx::setmaxnreg_dec<56>();
         if (w.most() > 0) {
-            if (warp == kPrProd && pr_elect())
+            if (warp == kPrProd && elect_one())
                 pr_producer(L, w, b, sbase);
-            else if (warp == kPrMma && pr_elect())
+            else if (warp == kPrMma && elect_one())
                 pr_mma(L, w, b, sbase);
         }
     }

@@ -251,13 +251,6 @@ __device__ void p4_locate(const P4Params& p, P4Bars& b, int r, int lane)
     }
 }
 
-__device__ __forceinline__ bool p4_elect()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // ---------------------------------------------------------------- producer --
 template <int D, int N>
 __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int lane, int64_t lo, int64_t hi)
@@ -339,7 +332,7 @@ __device__ void p4_producer(const P4Params& p, P4Bars& b, uint32_t sbase, int la
             for (int i = 0; i < kP4Pieces; ++i)
                 from[i] = reinterpret_cast<const unsigned char*>(
                     __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(src), kP4Pieces * mine_now + i));
-            if (p4_elect()) {
+            if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < kP4Pieces; ++i)
                     ptx::bulk_g2s(sbase + Y::kRing + at * Y::kTile + i * kPackedPiece<D>, from[i], kPackedPiece<D>, full);
@@ -875,7 +868,7 @@ __global__ void __launch_bounds__(kP4Threads, 2) packed_kernel(const P4Params p)
             p4_values<D, N>(p, b, ring, tm, warp - kP4Values, lane, hi - lo);
         else if (warp == kP4Prod)
             p4_producer<D, N>(p, b, sbase, lane, lo, hi);
-        else if (p4_elect())
+        else if (elect_one())
             p4_mma<D, N>(p, b, sbase, tm);
     }
     ptx::tc_fence_before();

@@ -268,16 +268,6 @@ __device__ __forceinline__ void px_drain(const PagedParams& p, const PxBars& b)
         landed(px_v_at(two, k, b.tiles));
 }
 
-// One lane of the (converged) warp: the compiler knows that a branch on it holds
-// a single thread, and hands the MMA its operands without a loop over the lanes
-// that might differ (which cost 35 of 100 cycles an MMA in a branch on lane 0).
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 // The MMA lane.  TMEM addresses are offsets: the CTA holds all 512 columns, so
 // its allocation starts at address 0.
 template <int D>

@@ -85,6 +85,16 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // and MMA layout): piece c ^ (r & 7).
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
+// One lane of the (converged) warp: the compiler knows that a branch on it holds a single
+// thread, and hands an MMA its operands without a loop over the lanes that might differ
+// (which cost 35 of 100 cycles an MMA in a branch on lane 0).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // Waits for a phase whatever the abort flag says: the drain of copies and MMAs that a CTA
 // started, before it leaves.  Up to 1 s, whatever bound the call's other waits have: one
 // that is shorter than a load would let the CTA go with copies on their way into shared
