@@ -184,3 +184,113 @@ def test_prefill_of_large_scores_without_a_scale(seqs, H, scale):
     torch.cuda.synchronize()
     refs, seen = T.prefill_refs(q[:nq], kv[:nk], kr[:nk], [0, nq], [0, nk], 0.0, True)
     L.near(out[:nq], lse[:nq], refs, 192, 2.0 ** -8, (seqs, H, scale))
+
+
+@pytest.mark.parametrize("Hq", [16, 40, 128])
+def test_decode_beside_nan(Hq):
+    """A query head that is NaN leaves the other heads, a sequence whose rows are NaN the
+    sequences beside it in a CTA's share."""
+    lens = [70, 300, 5, 40, 1000]
+    pool = T.Pool(Hq, 100, 16)
+    table = pool.table(lens)
+    q = normal(pool.g, 5, Hq, T.W)
+    args = (pool.kv, T.LORA, q, 16, table, i32(lens), 1000)
+    refs = T.decode_refs(q, pool, table, lens, T.W ** -0.5)
+    good, gl = K.kamera_mla_attend_paged(*args)
+    rows = torch.from_numpy(R.slots_of(table[1].tolist(), 16, 300, 100)).to(DEV)
+    kept = pool.kv[rows].clone()
+    pool.kv[rows] = float("nan")
+    out, lse = K.kamera_mla_attend_paged(*args)
+    torch.cuda.synchronize()
+    rest = [0, 2, 3, 4]
+    assert torch.equal(out[rest], good[rest]) and torch.equal(lse[rest], gl[rest])
+    assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
+    pool.kv[rows] = kept
+    q[:, 3], q[0, Hq - 1, 7] = float("nan"), float("inf")
+    out, lse = K.kamera_mla_attend_paged(*args)
+    torch.cuda.synchronize()
+    bad = torch.zeros(5, Hq, dtype=torch.bool, device=DEV)
+    bad[:, 3] = bad[0, Hq - 1] = True
+    assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
+    fine = (~bad).flatten().nonzero()[:, 0].tolist()
+    L.near(out.flatten(0, 1)[fine], lse.flatten()[fine], [refs[i] for i in fine], T.W, T.weight_error(Hq), Hq)
+
+
+def test_packed_attention_beside_nan():
+    c = P4.Cache(51, [300, 40, 1000], [9, 20, 3], 2, 128, 16)
+    q = normal(c.g, 3, 14, 128)
+    args = c.args(q)
+    refs = c.refs(q, 128 ** -0.5)
+    good, gl = K.kamera_attend_packed(*args)
+    c.tk[torch.from_numpy(c.tail_slots[1][:1]).to(DEV)] = float("nan")
+    out, lse = K.kamera_attend_packed(*args)
+    torch.cuda.synchronize()
+    assert torch.equal(out[[0, 2]], good[[0, 2]]) and torch.equal(lse[[0, 2]], gl[[0, 2]]) and bool(out[1].isnan().all())
+    q[:, 3] = float("nan")
+    out, lse = K.kamera_attend_packed(*args)
+    torch.cuda.synchronize()
+    assert bool(out[:, 3].isnan().all()) and bool(lse[:, 3].isnan().all())
+    fine = [i for i in range(3 * 14) if i % 14 != 3 and i // 14 != 1]
+    L.near(out.flatten(0, 1)[fine], lse.flatten()[fine], [refs[i] for i in fine], 128, P4.HALF, "heads", P4.LEAST)
+
+
+def test_prefill_of_heads_outermost_and_expansion_in_a_graph():
+    """Queries whose heads lie further apart than their tokens; the expansion captured with
+    the prefill that reads it, replayed on other inputs."""
+    g = gen(61)
+    H, nq, nk = 3, 200, 333
+    pool, weight = normal(g, 500, T.W), normal(g, H, 256, T.LORA, std=0.05)
+    slots = torch.randperm(500, generator=g, device=DEV)[:nk].contiguous()
+    q = normal(g, H, nq, 192).transpose(0, 1)
+    starts = i32([0, nq]), i32([0, nk])
+
+    def call():
+        kv, kr = K.kamera_mla_expand(pool, T.LORA, weight, slots)
+        return kv, kr, *K.kamera_mla_prefill_attend(q, kv, kr, *starts, nq)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv, kr, out, lse = call()
+    for _ in range(2):
+        pool.copy_(normal(g, 500, T.W))
+        q.copy_(normal(g, nq, H, 192))
+        slots.copy_(torch.randperm(500, generator=g, device=DEV)[:nk])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((kv, kr, out, lse), want))
+        T.expand_near(kv, pool, weight, slots.cpu().numpy())
+        refs, _ = T.prefill_refs(q, kv, kr, [0, nq], [0, nk], 192 ** -0.5, True)
+        L.near(out, lse, refs, 192, 2.0 ** -8, "graph")
+
+
+def test_packing_one_page_to_two_places():
+    P, H, d = 32, 2, 64
+    g = gen(71)
+    k, v = normal(g, 4 * P, H, d), normal(g, 4 * P, H, d)
+    packed = P4.packed_like(5, H, P, d)
+    K.kamera_pack_pages(k, v, P, i32([2, 2, 0, 2]), i32([P, P, P, 20]), packed, i32([4, 0, 1, 3]))
+    torch.cuda.synchronize()
+    assert torch.equal(packed[4], packed[0]) and not bool(packed[2].any())
+    piece = 18 * d
+    assert torch.equal(packed[3, :, :piece], packed[0, :, :piece])
+
+
+def test_workspace_of_a_larger_call_again():
+    """One workspace for calls one behind another: nothing of the larger one's states is read."""
+    lens = [900, 20, 3000, 64, 0, 700]
+    pool = T.Pool(81, 400, 16)
+    table = pool.table(lens)
+    pool.poison()
+    q = normal(pool.g, 6, 16, T.W)
+    ws = torch.empty(K.kamera_mla_attend_paged_workspace_bytes(pool.kv, T.LORA, q, 16, 3000), dtype=torch.uint8, device=DEV)
+    calls = [(list(range(6)), 3000), ([5, 1], 700), ([2], 3000), ([4, 3], 64), ([0, 1, 4], 900)]
+    alone = [K.kamera_mla_attend_paged(pool.kv, T.LORA, q[s], 16, table[s].contiguous(), i32([lens[i] for i in s]), m)
+             for s, m in calls]
+    again = [K.kamera_mla_attend_paged(pool.kv, T.LORA, q[s], 16, table[s].contiguous(), i32([lens[i] for i in s]), m,
+                                       workspace=ws) for s, m in calls]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, again):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
