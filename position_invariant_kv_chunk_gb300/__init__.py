@@ -1071,8 +1071,9 @@ def kamera_attend_packed(packed: torch.Tensor, q: torch.Tensor, page_size: int, 
     packed: uint8 ``[n_pages, H, page_size * (d + d // 8)]``; q: bf16 ``[S, H_q, d]``
     contiguous; pages int32 ``[S, width]``, lens int32 ``[S]``, of the packed part;
     pool_*: bf16 ``[S_slots, H, d]`` (one layer) with tail_pages, tail_lens and max_tail
-    for the tail (all None: no tail; tail_page_size: default page_size); k_unit, v_unit:
-    as the pages were packed; scale: default 1/sqrt(d); lse and workspace as for
+    for the tail (all None: no tail; tail_page_size: default page_size); a length behind a
+    bound of 0 (max_tail's default) raises LEN and counts as 0; k_unit, v_unit: as the pages
+    were packed; scale: default 1/sqrt(d); lse and workspace as for
     ``kamera_attend_shared``.  Returns ``(out, lse)``."""
     return (_FAST or _fast()).attend_packed(packed, q, page_size, pages, lens, max_len, pool_k, pool_v, tail_pages,
                                             tail_lens, max_tail, tail_page_size, k_unit, v_unit, scale, out, lse, err,

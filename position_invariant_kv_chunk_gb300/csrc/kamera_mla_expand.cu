@@ -13,8 +13,8 @@
 // 128 x 256 sums stand in one of two TMEM halves while two epilogue groups empty the other,
 // each 64 columns at a time through shared memory and a TMA store (one group took 6200
 // cycles a head, rows stored from the registers 6000, its MMAs 4200).  16381 tokens of 16
-// heads take 60 us (1150 TFLOP/s, floor 35): a head now takes 6100 cycles, in which an SM
-// reads 128 KB of weights from L2 and writes 64 KB.
+// heads take 58 us on data in turn (1180 TFLOP/s, floor 35): a head now takes 6100 cycles,
+// in which an SM reads 128 KB of weights from L2 and writes 64 KB.
 //   warps 0-3, 4-7  epilogue of a head's first and last 128 columns: thread = token = TMEM lane
 //   warp 8     producer of the CTA's half of the weights (TMA, counted on the first CTA's
 //              barriers)

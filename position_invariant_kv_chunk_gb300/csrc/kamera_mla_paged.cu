@@ -30,11 +30,12 @@
 //   two warps  MMA, the scores' and the products': what a lane issues next waits behind
 //              its MMAs, barriers too, and with one lane for both (300 cycles for every
 //              barrier between MMAs) neither kept the tensor pipe busy
-// Measured: 32 contexts of up to 16384 tokens with 16 heads in 93 us (5.5 TB/s of the
-// rows; HBM, 81% of a copy's rate), 48 of up to 8192 with 128 heads in 144 (652 TFLOP/s).
-// There the ring holds two tiles, beside 72 KB of queries, and a tile stays from its load
-// (1700 cycles) over its scores and their softmax to its product: the tensor pipe works
-// 62% of the time.  One context of 4096 tokens takes 14.6: one tile a CTA and the join.
+// Measured, calls back to back on data in turn: 32 contexts of up to 16384 tokens with 16
+// heads in 90 us (5.7 TB/s of the rows; HBM, 84% of a copy's rate), 48 of up to 8192 with
+// 128 heads in 140 (674 TFLOP/s).  There the ring holds two tiles, beside 72 KB of queries,
+// and a tile stays from its load (1700 cycles) over its scores and their softmax to its
+// product: the tensor pipe works 62% of the time, in M = 64 MMAs that run at half rate.
+// One context of 4096 tokens takes 11.9: one tile a CTA and the join.
 // Every wait is bounded in time.
 #include <algorithm>
 #include <cstdint>
@@ -138,7 +139,8 @@ __device__ __forceinline__ int mp_tiles(int len) { return len > 0 ? (len - 1) / 
 // The ranges in use, of T tiles.  Where one sequence gives each a few tiles, as few as
 // leave the longest as it is: fewer states to join (12000 tokens 21.0 -> 16.8 us, 40000
 // 26.6 -> 24.5); ranges that hold the end of one sequence and the start of another are
-// better short (four of 8000 tokens 16.8, 18.9 with fewer).
+// better short (four of 8000 tokens 16.8, 18.9 with fewer).  A batch of more rows has all
+// ranges, one that is a single sequence and empty rows too.
 __device__ __forceinline__ int64_t mp_ranges(const MpParams& p, int64_t T)
 {
     if (p.n_seqs > 1 || T <= p.ranges || T > 8ll * p.ranges)

@@ -24,8 +24,9 @@
 //   warp 10         MMA; it owns TMEM (warps 9, 11 idle: registers are moved between
 //                   whole warpgroups)
 // Blocks of queries with the most rows to see start first.  Every wait is bounded.
-// Measured: 4 prompts of up to 4096 tokens, 16 heads, in 192 us (1386 TFLOP/s), 777
-// queries behind 1296 rows in 23.
+// Measured, calls back to back on data in turn: 4 prompts of up to 4096 tokens, 16 heads,
+// in 209 us (1275 TFLOP/s; over one prompt's rows again and again, which L2 holds in part,
+// 189), 777 queries behind 1296 rows in 22.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>

@@ -22,12 +22,12 @@
 // Work: the batch's tiles of 128 tokens, all (sequence, KV head) behind one another, in
 // equal ranges, one a CTA; each leaves a partial state for every (sequence, KV head)
 // that it touches, and a last launch joins them with the tail's.
-// Measured: 32 contexts of up to 32768 tokens, 4 KV heads of 128 with 7 query heads, in
-// 109 us (4.7 TB/s), 32 KV heads with one each 60: a tile takes an SM 865 cycles where
-// HBM alone would need 785 (the issue slots are 70% full), but CTAs with equal work end
-// up to 20% apart.  One context of 32768 takes 15.1 a call: start, four tiles, the join.  Steps
-// of two tiles for the softmax (8 query heads) were slower, 114: a step's products then
-// wait for the keys of two more tiles.
+// Measured, calls back to back on data in turn: 32 contexts of up to 32768 tokens, 4 KV
+// heads of 128 with 7 query heads, in 105 us (4.9 TB/s), 32 KV heads with one each 56: a
+// tile takes an SM 865 cycles where HBM alone would need 785 (the issue slots are 70%
+// full), but CTAs with equal work end up to 20% apart.  One context of 32768 takes 14.9:
+// start, four tiles, the join.  Steps of two tiles for the softmax (8 query heads) took 5%
+// more: a step's products then wait for the keys of two more tiles.
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
