@@ -384,9 +384,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attend_kernel(const __grid_cons
                 const uint32_t ub = ut0 + (SM::UB ? b : 0) * kUBuf, uvb = uv0 + (SM::UB ? b : 0) * kUBuf;
                 const bool active = r0 < ntok;
                 if (active) {
-                    // (after a timeout still waited for: no copy outlives the CTA)
-                    if (!tile_wait(ptx::smem_addr(&s.full[warp][b]), (ph >> b) & 1u, &s.abort, p.err, P.wait_ns))
-                        tc::pf_drain_wait(ptx::smem_addr(&s.full[warp][b]), (ph >> b) & 1u);
+                    // (after a timeout still waited for, as no copy may outlive the CTA, until one does not land)
+                    if (!tile_wait(ptx::smem_addr(&s.full[warp][b]), (ph >> b) & 1u, &s.abort, p.err, P.wait_ns) &&
+                        *static_cast<volatile int32_t*>(&s.abort) != 2 &&
+                        !tc::pf_drain_wait(ptx::smem_addr(&s.full[warp][b]), (ph >> b) & 1u))
+                        s.abort = 2;
                     ph ^= 1u << b;
                     // ---- this warp's rows of the buffer: U rows of ranks that are not whole
                     // 16-byte vectors, U columns past the rank, value rows past the chunk

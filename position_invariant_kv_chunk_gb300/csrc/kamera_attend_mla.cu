@@ -365,9 +365,11 @@ __global__ void __launch_bounds__(kMlThreads, 1) mla_attend_kernel(const __grid_
 
         for (int tl = t_lo; tl < t_hi; ++tl) {
             const int b = (tl - t_lo) & 1, ntok = min(kMlT, len - tl * kMlT);
-            // (after a timeout still waited for: no copy outlives the CTA)
-            if (!tile_wait(ptx::smem_addr(&s.full[b]), (ph >> b) & 1u, &s.abort, p.err, P.wait_ns))
-                tc::pf_drain_wait(ptx::smem_addr(&s.full[b]), (ph >> b) & 1u);
+            // (after a timeout still waited for, as no copy may outlive the CTA, until one does not land)
+            if (!tile_wait(ptx::smem_addr(&s.full[b]), (ph >> b) & 1u, &s.abort, p.err, P.wait_ns) &&
+                *static_cast<volatile int32_t*>(&s.abort) != 2 &&
+                !tc::pf_drain_wait(ptx::smem_addr(&s.full[b]), (ph >> b) & 1u))
+                s.abort = 2;
             ph ^= 1u << b;
             ptx::cp_async_wait<0>();   // this thread's copies of tile tl (the only group in flight)
             const uint32_t kb = kt0 + b * kBuf, uxb = ux0 + b * kUBuf;

@@ -98,20 +98,22 @@ __device__ __forceinline__ bool elect_one()
 // Waits for a phase whatever the abort flag says: the drain of copies and MMAs that a CTA
 // started, before it leaves.  Up to 1 s, whatever bound the call's other waits have: one
 // that is shorter than a load would let the CTA go with copies on their way into shared
-// memory that its successor owns.
-__device__ __forceinline__ void pf_drain_wait(uint32_t bar, uint32_t parity)
+// memory that its successor owns.  False: given up.
+__device__ __forceinline__ bool pf_drain_wait(uint32_t bar, uint32_t parity)
 {
     const uint64_t t0 = ptx::globaltimer();
     while (!ptx::mbar_try_wait(bar, parity))
         if (ptx::globaltimer() - t0 > 1000000000ull)
-            return;
+            return false;
+    return true;
 }
 
 // The last `ring` of `n` fills of a ring of barriers (fill k: barrier k % ring), waited for.
 __device__ __forceinline__ void pf_drain_ring(const uint64_t* bars, uint32_t n, uint32_t ring)
 {
     for (uint32_t k = n > ring ? n - ring : 0u; k < n; ++k)
-        pf_drain_wait(ptx::smem_addr(&bars[k % ring]), (k / ring) & 1u);
+        if (!pf_drain_wait(ptx::smem_addr(&bars[k % ring]), (k / ring) & 1u))
+            return;
 }
 
 // Shared-memory matrix descriptors as (low word, high word): the low word holds
